@@ -53,7 +53,7 @@ typedef enum {
     TA_ERR_CUDA = 5              /* the CUDA runtime reported an error */
 } ta_status;
 
-typedef enum { TA_F32 = 0, TA_F16 = 1, TA_BF16 = 2, TA_U32 = 3, TA_I32 = 4 } ta_dtype;
+typedef enum { TA_F32 = 0, TA_F16 = 1, TA_BF16 = 2, TA_U32 = 3, TA_I32 = 4, TA_I64 = 5 } ta_dtype;
 
 /*
  * Kernel family of a call (ta_tree_options.kernel, ta_quant_params.kernel).
@@ -360,6 +360,197 @@ ta_status quant_sdpa_fwd_tree(const ta_quant_params *p, uint32_t q_l, const ta_b
                               const ta_buf *k_biases, const ta_buf *v_packed, const ta_buf *v_scales,
                               const ta_buf *v_biases, const ta_buf *sinks, const ta_buf *mask_bool,
                               const ta_buf *tmp, const ta_buf *out, void *stream);
+
+/* --------------------------------------------------------------- serving */
+
+/*
+ * Batched serving around the verify step: many requests, each with its own
+ * length, on one paged K/V cache.  The order of a step is paged_plan_build
+ * (pages, tables and slots from the requests' lengths), paged_kv_append (the
+ * new tokens' K/V rows into their pages, per layer) and paged_attn_fwd (the new
+ * tokens' attention over the pages, per layer); prompt_attn_fwd is the attention
+ * of whole prompts before anything of them is cached.  The pages of the
+ * sources have no counterpart of these calls.
+ *
+ * Common to them:
+ *   - Rows are packed: the new tokens of request b are rows cu[b] .. cu[b+1]-1
+ *     of q, out, k_new, ... (cu: [batch + 1] i32, non-decreasing, cu[0] >= 0).
+ *     Rows behind the last request are left as they were.
+ *   - Lengths, tables and slots are device data, read by the kernels: no call
+ *     waits for them, so a captured graph may be replayed with other lengths.
+ *   - A cache is [n_pages, n_kv_heads, page_size, head_dim] f16 or bf16 with
+ *     any page, head and token strides (elements, multiples of 8, the last
+ *     axis contiguous), so a [n_pages, page_size, n_kv_heads, head_dim] cache is
+ *     the same cache with other strides.  page_size: 16, 32, 64, 128 or 256.
+ *   - Device data that contradicts itself (a length beyond its table row, a
+ *     page outside the cache, offsets that run backwards) never makes a kernel
+ *     read or write outside its buffers; it sets bits of the call's status
+ *     word, which the kernels only OR into: a caller that wants to check zeroes
+ *     the word before the call and reads it after.  The outputs of the rows
+ *     concerned are then not valid.
+ */
+
+/*
+ * Planning of one step.
+ *   batch       requests B, 1 .. 16384
+ *   page_size   tokens per page: 16, 32, 64, 128 or 256
+ *   max_pages   cells per block-table row
+ *   capacity    cells of the free stack
+ *   max_tokens  rows of slot_map and positions
+ */
+typedef struct {
+    uint32_t batch;
+    uint32_t page_size;
+    uint32_t max_pages;
+    uint32_t capacity;
+    uint32_t max_tokens;
+    uint32_t reserved; /* must be 0 */
+} ta_plan_params;
+
+/*
+ * Block tables, slot map and row offsets of a step, built on the device from
+ * request lengths.  For request b: keep[b] tokens stay cached (0 for a new or
+ * a finished request; fewer than before when drafts were rejected),
+ * fresh[b] tokens join, held[b] pages are in its table row now.  It needs
+ * need[b] = ceil((keep[b] + fresh[b]) / page_size) pages:
+ *   - cells need[b] .. held[b]-1 are given back: pushed on the free stack
+ *     (stack[n_free], stack[n_free + 1], ...) in row, then cell order;
+ *   - then cells held[b] .. need[b]-1 are filled from the top of the stack
+ *     downwards, in row, then cell order.
+ * Cells past need[b] and stack cells past the new count keep their old values,
+ * which mean nothing.
+ *   keep, fresh, held   [B] i32
+ *   table               [B, max_pages] i32, updated in place
+ *   stack               [capacity] i32, updated in place; n_free [1] i32 cells in use
+ *   held_out [B] i32, n_free_out [1] i32   the counts after the step; they may be
+ *                       the memory of held and n_free (no other buffers may overlap)
+ *   cu        [B + 1] i32   exclusive prefix sum of fresh
+ *   kv_lens   [B] i32       keep + fresh
+ *   slot_map  [max_tokens] i64   cache slot (page * page_size + token in page) of each
+ *                           new token in packed order; -1 behind the last
+ *   positions [max_tokens] i32   position of each new token in its request; -1 behind
+ *   status    [1] i32       ORed: 1 too few free pages, 2 a negative length or a row
+ *                           that needs more than max_pages cells, 4 more than
+ *                           max_tokens new tokens, 8 the stack cannot take the pages
+ *                           given back (or n_free is out of range)
+ * With any status bit nothing moves: table and stack stay, held_out and
+ * n_free_out repeat their inputs, cu and kv_lens are 0, slot_map and positions -1.
+ */
+ta_status paged_plan_build(const ta_plan_params *p, const ta_buf *keep, const ta_buf *fresh, const ta_buf *held,
+                           const ta_buf *table, const ta_buf *stack, const ta_buf *n_free, const ta_buf *held_out,
+                           const ta_buf *n_free_out, const ta_buf *cu, const ta_buf *kv_lens,
+                           const ta_buf *slot_map, const ta_buf *positions, const ta_buf *status, void *stream);
+
+/*
+ * Writing new K/V rows to their pages.
+ *   tokens       rows T of k_new, v_new and slot_map (0: nothing is launched)
+ *   k_token_stride, k_head_stride, v_token_stride, v_head_stride   of the new rows
+ *   page_stride, head_stride, token_stride   of both caches
+ * Strides in elements, multiples of 8; 0 = the contiguous layout's.
+ */
+typedef struct {
+    uint32_t tokens;
+    uint32_t n_kv_heads;
+    uint32_t head_dim;   /* 64, 128 or 256 */
+    uint32_t page_size;
+    uint32_t n_pages;
+    uint32_t reserved;   /* must be 0 */
+    uint64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+    uint64_t page_stride, head_stride, token_stride;
+} ta_append_params;
+
+/*
+ * Row t of k_new, v_new ([tokens, n_kv_heads, head_dim]) to cache slot
+ * slot_map[t] ([tokens] i64).  Slots outside [0, n_pages * page_size), such as
+ * the -1 of paged_plan_build, store nothing.  No two rows may name the same
+ * slot.  k_new, v_new, k_cache, v_cache: one type, f16 or bf16, 16-byte aligned.
+ */
+ta_status paged_kv_append(const ta_append_params *p, const ta_buf *k_new, const ta_buf *v_new,
+                          const ta_buf *k_cache, const ta_buf *v_cache, const ta_buf *slot_map, void *stream);
+
+/*
+ * Attention of each request's new tokens over its pages.
+ *   batch, n_heads, n_kv_heads (n_heads % n_kv_heads == 0, at most 128 query
+ *   heads per KV head), head_dim 64, 128 or 256
+ *   tokens       rows T of q and out (0: nothing is launched)
+ *   max_q_len    no request has more new tokens than this (it also chooses the
+ *                kernel; rows past it are left as they were and set a status bit)
+ *   window       0, or the number of last positions a token sees, itself included
+ *   page_size, n_pages, max_pages (cells per block-table row)
+ *   kernel       ta_kernel
+ *   scale        logit = (q . k) * scale
+ *   strides in elements, multiples of 8; 0 = contiguous
+ */
+typedef struct {
+    uint32_t batch;
+    uint32_t n_heads;
+    uint32_t n_kv_heads;
+    uint32_t head_dim;
+    uint32_t tokens;
+    uint32_t max_q_len;
+    uint32_t window;
+    uint32_t page_size;
+    uint32_t n_pages;
+    uint32_t max_pages;
+    uint32_t kernel;
+    float scale;
+    uint64_t q_token_stride, q_head_stride, out_token_stride, out_head_stride;
+    uint64_t page_stride, head_stride, token_stride;   /* both caches */
+} ta_paged_params;
+
+/* Bytes the `tmp` buffer of paged_attn_fwd must hold; SIZE_MAX on invalid parameters. */
+size_t paged_attn_workspace_bytes(const ta_paged_params *p);
+
+/*
+ * For token i of request b, at position pos = kv_lens[b] - q_len + i (q_len =
+ * cu[b+1] - cu[b]), and each head: softmax over the visible keys j of
+ * scale * q . k_j, applied to v_j.  Visible without parents: j <= pos, and with
+ * a window j > pos - window.  With parents (draft trees, the rule of
+ * tree_mask_build per request: parents[cu[b] + i] is the parent's index inside
+ * the request's chunk; a chain ends at a value outside [0, current node)):
+ * the prefix j < kv_lens[b] - q_len, the node's ancestors and itself.
+ * A row that sees no key gives zeros.  K and V at positions a row does not see
+ * do not touch its result, whatever they hold.  A V value that is infinite or
+ * NaN makes the rows that see it NaN or infinite in its column.
+ *   q, out      [tokens, n_heads, head_dim], the cache's type
+ *   k_cache, v_cache   as above
+ *   table       [batch, max_pages] i32; cells past a request's last page are not read
+ *   cu [batch + 1] i32, kv_lens [batch] i32
+ *   parents     [tokens] i32 or absent; with parents window must be 0, and
+ *               max_q_len > 256 is TA_ERR_UNSUPPORTED
+ *   tmp         >= paged_attn_workspace_bytes(p), f32, 16-byte aligned.  Its first
+ *               32-bit word is the status word: 1 a bounded wait gave up, 2 a page
+ *               outside the cache, 4 a length or offset out of range.
+ */
+ta_status paged_attn_fwd(const ta_paged_params *p, const ta_buf *q, const ta_buf *k_cache, const ta_buf *v_cache,
+                         const ta_buf *table, const ta_buf *cu, const ta_buf *kv_lens, const ta_buf *parents,
+                         const ta_buf *tmp, const ta_buf *out, void *stream);
+
+/* As ta_paged_params, for whole prompts: K and V are packed rows like q. */
+typedef struct {
+    uint32_t batch;
+    uint32_t n_heads;
+    uint32_t n_kv_heads;
+    uint32_t head_dim;
+    uint32_t tokens;
+    uint32_t window;
+    uint32_t kernel;
+    float scale;
+    uint64_t q_token_stride, q_head_stride, out_token_stride, out_head_stride;
+    uint64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+} ta_prompt_params;
+
+/* Bytes the `tmp` buffer of prompt_attn_fwd must hold; SIZE_MAX on invalid parameters. */
+size_t prompt_attn_workspace_bytes(const ta_prompt_params *p);
+
+/*
+ * Causal attention over packed prompts: row i of request b sees rows
+ * max(0, i - window + 1) .. i of the same request (window 0: 0 .. i).
+ *   q, out [tokens, n_heads, head_dim]; k, v [tokens, n_kv_heads, head_dim]; one
+ *   type, f16 or bf16, 16-byte aligned; cu [batch + 1] i32; tmp as above.
+ */
+ta_status prompt_attn_fwd(const ta_prompt_params *p, const ta_buf *q, const ta_buf *k, const ta_buf *v,
+                          const ta_buf *cu, const ta_buf *tmp, const ta_buf *out, void *stream);
 
 /* ----------------------------------------------------------------- misc */
 

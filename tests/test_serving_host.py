@@ -1,0 +1,210 @@
+"""Refusals of the serving entry points: every bad argument is reported before
+any launch (no GPU needed)."""
+import ctypes
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def ta():
+    import tree_masked_speculative_gb300 as m
+    return m
+
+
+BIG = 1 << 44
+
+
+def _b(ta, code, nbytes=BIG, ptr=0x10000, reserved=0):
+    return ta.Buf(ptr, nbytes, code, reserved)
+
+
+def _call(ta, fn, p, bufs):
+    before = ta.ta_launch_count()
+    st = fn(ctypes.byref(p) if p is not None else None, *[ctypes.byref(b) if b is not None else None for b in bufs], None)
+    assert ta.ta_launch_count() == before
+    return st, ta.ta_last_error()
+
+
+def test_struct_sizes(ta):
+    assert ctypes.sizeof(ta.PlanParams) == 24
+    assert ctypes.sizeof(ta.AppendParams) == 24 + 7 * 8
+    assert ctypes.sizeof(ta.PagedParams) == 48 + 7 * 8
+    assert ctypes.sizeof(ta.PromptParams) == 32 + 8 * 8
+
+
+PLAN = dict(batch=4, page_size=16, max_pages=8, capacity=64, max_tokens=100)
+PLAN_BUFS = ["keep", "fresh", "held", "table", "stack", "n_free", "held_out", "n_free_out", "cu", "kv_lens",
+             "slot_map", "positions", "status"]
+
+
+@pytest.mark.parametrize("kw,buf,change,want,frag", [
+    (dict(batch=0), None, None, 1, "batch"),
+    (dict(batch=16385), None, None, 4, "batch"),
+    (dict(page_size=24), None, None, 1, "page_size"),
+    (dict(page_size=8), None, None, 1, "page_size"),
+    (dict(max_pages=0), None, None, 1, "max_pages"),
+    (dict(max_pages=1 << 30), None, None, 4, "index range"),
+    (dict(reserved=1), None, None, 1, "reserved"),
+    ({}, "table", dict(nbytes=4 * 8 * 4 - 1), 2, "table"),
+    ({}, "cu", dict(nbytes=16), 2, "cu"),
+    ({}, "slot_map", dict(nbytes=799), 2, "slot_map"),
+    ({}, "slot_map", dict(ptr=0x10004), 1, "aligned"),
+    ({}, "slot_map", dict(code="TA_I32"), 1, "slot_map dtype"),
+    ({}, "keep", dict(code="TA_I64"), 1, "keep dtype"),
+    ({}, "status", None, 1, "status"),
+    ({}, "positions", dict(reserved=3), 1, "reserved"),
+])
+def test_plan_rejections(ta, kw, buf, change, want, frag):
+    p = ta.PlanParams(**{**PLAN, **kw})
+    bufs = {n: _b(ta, ta.TA_I64 if n == "slot_map" else ta.TA_I32) for n in PLAN_BUFS}
+    if buf is not None:
+        if change is None:
+            bufs[buf] = None
+        else:
+            c = dict(change)
+            code = getattr(ta, c.pop("code")) if "code" in c else bufs[buf].dtype
+            bufs[buf] = _b(ta, code, **c)
+    st, msg = _call(ta, ta.lib.paged_plan_build, p, bufs.values())
+    assert st == want and frag in msg, msg
+
+
+def test_null_params(ta):
+    for fn, n in ((ta.lib.paged_plan_build, 13), (ta.lib.paged_kv_append, 5), (ta.lib.paged_attn_fwd, 9),
+                  (ta.lib.prompt_attn_fwd, 6)):
+        st, msg = _call(ta, fn, None, [None] * n)
+        assert st == 1 and "NULL" in msg
+    assert ta.lib.paged_attn_workspace_bytes(None) == 2 ** 64 - 1
+    assert ta.lib.prompt_attn_workspace_bytes(None) == 2 ** 64 - 1
+
+
+APPEND = dict(tokens=10, n_kv_heads=2, head_dim=128, page_size=16, n_pages=5)
+
+
+@pytest.mark.parametrize("kw,buf,change,want,frag", [
+    (dict(n_kv_heads=0), None, None, 1, "n_kv_heads"),
+    (dict(n_pages=0), None, None, 1, "n_pages"),
+    (dict(head_dim=96), None, None, 1, "head_dim"),
+    (dict(page_size=48), None, None, 1, "page_size"),
+    (dict(k_token_stride=260), None, None, 1, "k_token_stride"),
+    (dict(page_stride=1 << 38), None, None, 4, "page_stride"),
+    (dict(n_pages=2 ** 31 - 1, page_stride=2 ** 37), None, None, 3, "overflow"),
+    ({}, 0, dict(code="TA_F32"), 1, "k_new dtype"),
+    ({}, 1, dict(code="TA_BF16"), 1, "v_new dtype"),
+    ({}, 2, dict(code="TA_BF16"), 1, "k_cache dtype"),
+    ({}, 2, dict(ptr=0x10008), 1, "aligned"),
+    ({}, 0, dict(nbytes=10 * 256 * 2 - 1), 2, "k_new"),
+    ({}, 3, dict(nbytes=5 * 16 * 256 * 2 - 1), 2, "v_cache"),
+    ({}, 4, dict(code="TA_I32"), 1, "slot_map dtype"),
+    ({}, 4, dict(nbytes=79), 2, "slot_map"),
+    ({}, 4, None, 1, "slot_map"),
+])
+def test_append_rejections(ta, kw, buf, change, want, frag):
+    p = ta.AppendParams(**{**APPEND, **kw})
+    bufs = [_b(ta, ta.TA_F16) for _ in range(4)] + [_b(ta, ta.TA_I64)]
+    if buf is not None:
+        c = dict(change or {})
+        bufs[buf] = None if change is None else _b(ta, getattr(ta, c.pop("code")) if "code" in c else bufs[buf].dtype, **c)
+    st, msg = _call(ta, ta.lib.paged_kv_append, p, bufs)
+    assert st == want and frag in msg, msg
+
+
+def test_nothing_to_do_launches_nothing(ta):
+    none = [None] * 9
+    assert _call(ta, ta.lib.paged_kv_append, ta.AppendParams(**{**APPEND, "tokens": 0}), none[:5])[0] == 0
+    assert _call(ta, ta.lib.paged_attn_fwd, ta.PagedParams(**{**PAGED, "tokens": 0}), none)[0] == 0
+    assert _call(ta, ta.lib.prompt_attn_fwd, ta.PromptParams(**{**PROMPT, "tokens": 0}), none[:6])[0] == 0
+
+
+PAGED = dict(batch=3, n_heads=8, n_kv_heads=2, head_dim=128, tokens=12, max_q_len=4, page_size=16, n_pages=9,
+             max_pages=4, scale=0.1)
+PAGED_BUFS = ["q", "k_cache", "v_cache", "table", "cu", "kv_lens", "parents", "tmp", "out"]
+
+
+@pytest.mark.parametrize("kw,buf,change,want,frag", [
+    (dict(batch=0), None, None, 1, "batch"),
+    (dict(batch=65536), None, None, 4, "index range"),
+    (dict(n_heads=9), None, None, 1, "divisible"),
+    (dict(n_heads=258), None, None, 4, "128 query heads"),
+    (dict(head_dim=512), None, None, 1, "head_dim"),
+    (dict(head_dim=80), None, None, 1, "head_dim"),
+    (dict(max_q_len=0), None, None, 1, "max_q_len"),
+    (dict(page_size=0), None, None, 1, "page_size"),
+    (dict(page_size=512), None, None, 1, "page_size"),
+    (dict(n_pages=0), None, None, 1, "n_pages"),
+    (dict(max_pages=0), None, None, 1, "max_pages"),
+    (dict(max_pages=1 << 27), None, None, 4, "index range"),
+    (dict(window=1 << 31), None, None, 4, "index range"),
+    (dict(tokens=2 ** 30), None, None, 4, "index range"),
+    (dict(kernel=4), None, None, 1, "kernel"),
+    (dict(scale=float("nan")), None, None, 1, "scale"),
+    (dict(scale=float("inf")), None, None, 1, "scale"),
+    (dict(window=5), None, None, 1, "window must be 0 with parents"),
+    (dict(max_q_len=257), None, None, 4, "max_q_len <= 256"),
+    (dict(q_head_stride=132), None, None, 1, "q_head_stride"),
+    (dict(token_stride=4), None, None, 1, "token_stride"),
+    (dict(head_stride=1 << 40), None, None, 4, "head_stride"),
+    ({}, "q", dict(code="TA_F32"), 1, "q dtype"),
+    ({}, "q", dict(nbytes=12 * 1024 * 2 - 1), 2, "q"),
+    ({}, "q", dict(ptr=0x10002), 1, "aligned"),
+    ({}, "k_cache", dict(code="TA_BF16"), 1, "k_cache dtype"),
+    ({}, "v_cache", dict(nbytes=9 * 16 * 256 * 2 - 2), 2, "v_cache"),
+    ({}, "table", dict(nbytes=47), 2, "table"),
+    ({}, "table", dict(code="TA_I64"), 1, "table dtype"),
+    ({}, "cu", dict(nbytes=12), 2, "cu"),
+    ({}, "kv_lens", None, 1, "kv_lens"),
+    ({}, "parents", dict(nbytes=44), 2, "parents"),
+    ({}, "parents", dict(code="TA_I64"), 1, "parents dtype"),
+    ({}, "tmp", dict(nbytes=8), 2, "tmp"),
+    ({}, "tmp", dict(code="TA_F16"), 1, "tmp dtype"),
+    ({}, "out", dict(code="TA_F32"), 1, "out dtype"),
+    ({}, "out", None, 1, "out"),
+    ({}, "out", dict(reserved=1), 1, "reserved"),
+])
+def test_paged_rejections(ta, kw, buf, change, want, frag):
+    p = ta.PagedParams(**{**PAGED, **kw})
+    codes = dict(table=ta.TA_I32, cu=ta.TA_I32, kv_lens=ta.TA_I32, parents=ta.TA_I32, tmp=ta.TA_F32)
+    bufs = {n: _b(ta, codes.get(n, ta.TA_F16)) for n in PAGED_BUFS}
+    if buf is not None:
+        c = dict(change or {})
+        bufs[buf] = None if change is None else _b(ta, getattr(ta, c.pop("code")) if "code" in c else bufs[buf].dtype, **c)
+    st, msg = _call(ta, ta.lib.paged_attn_fwd, p, bufs.values())
+    assert st == want and frag in msg, msg
+
+
+PROMPT = dict(batch=3, n_heads=8, n_kv_heads=2, head_dim=128, tokens=12, scale=0.1)
+PROMPT_BUFS = ["q", "k", "v", "cu", "tmp", "out"]
+
+
+@pytest.mark.parametrize("kw,buf,change,want,frag", [
+    (dict(n_kv_heads=0), None, None, 1, "n_kv_heads"),
+    (dict(n_heads=7), None, None, 1, "divisible"),
+    (dict(head_dim=32), None, None, 1, "head_dim"),
+    (dict(window=2 ** 32 - 1), None, None, 4, "index range"),
+    (dict(kernel=9), None, None, 1, "kernel"),
+    (dict(v_token_stride=12), None, None, 1, "v_token_stride"),
+    (dict(k_head_stride=1 << 39), None, None, 4, "k_head_stride"),
+    ({}, "k", dict(code="TA_BF16"), 1, "k dtype"),
+    ({}, "v", dict(nbytes=12 * 256 * 2 - 1), 2, "v"),
+    ({}, "v", dict(ptr=0x10001), 1, "aligned"),
+    ({}, "cu", dict(code="TA_F32"), 1, "cu dtype"),
+    ({}, "tmp", None, 1, "tmp"),
+    ({}, "out", dict(nbytes=0), 2, "out"),
+])
+def test_prompt_rejections(ta, kw, buf, change, want, frag):
+    p = ta.PromptParams(**{**PROMPT, **kw})
+    codes = dict(cu=ta.TA_I32, tmp=ta.TA_F32)
+    bufs = {n: _b(ta, codes.get(n, ta.TA_F16)) for n in PROMPT_BUFS}
+    if buf is not None:
+        c = dict(change or {})
+        bufs[buf] = None if change is None else _b(ta, getattr(ta, c.pop("code")) if "code" in c else bufs[buf].dtype, **c)
+    st, msg = _call(ta, ta.lib.prompt_attn_fwd, p, bufs.values())
+    assert st == want and frag in msg, msg
+
+
+def test_python_refuses_host_tensors(ta):
+    x = torch.zeros(4, 2, 64, dtype=torch.float16)
+    with pytest.raises(ValueError, match="CUDA"):
+        ta.prompt_attention(x, x, x, torch.tensor([0, 4], dtype=torch.int32), scale=1.0)
+    with pytest.raises(ValueError, match="CUDA"):
+        ta.paged_append(x, x, x[None], x[None], torch.zeros(4, dtype=torch.int64))

@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -25,10 +25,13 @@ __all__ = [
     "quant_sdpa_kernel_family", "KERNEL_WARP_MMA",
     "ta_test_quant_sdpa_fwd_wait_limit", "quant_sdpa_fwd_tree", "tree_attention", "quant_sdpa", "tree_params", "quant_params",
     "tree_mask_build", "TreeOptions", "KERNEL_AUTO", "KERNEL_CUDA_CORES", "KERNEL_TENSOR_CORES",
+    "PlanParams", "AppendParams", "PagedParams", "PromptParams", "PagedStep", "paged_plan", "paged_append",
+    "paged_attention", "paged_attention_workspace", "paged_attn_workspace_bytes", "prompt_attention",
+    "prompt_attention_workspace", "prompt_attn_workspace_bytes",
 ]
 
 TA_OK = 0
-TA_F32, TA_F16, TA_BF16, TA_U32, TA_I32 = 0, 1, 2, 3, 4
+TA_F32, TA_F16, TA_BF16, TA_U32, TA_I32, TA_I64 = 0, 1, 2, 3, 4, 5
 KERNEL_AUTO, KERNEL_CUDA_CORES, KERNEL_TENSOR_CORES, KERNEL_WARP_MMA = 0, 1, 2, 3
 MASK_DENSE, MASK_CAUSAL, MASK_PARENTS = 0, 1, 2
 STATUS_NAMES = {0: "TA_OK", 1: "TA_ERR_INVALID_ARGUMENT", 2: "TA_ERR_BUFFER_TOO_SMALL",
@@ -64,6 +67,35 @@ class QuantParams(ctypes.Structure):
 class TreeOptions(ctypes.Structure):
     _fields_ = [("kernel", ctypes.c_int32), ("mask_kind", ctypes.c_int32), ("window_start", ctypes.c_uint32),
                 ("reserved", ctypes.c_int32)]
+
+
+class PlanParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_uint32) for n in ("batch", "page_size", "max_pages", "capacity", "max_tokens",
+                                               "reserved")]
+
+
+class AppendParams(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_uint32) for n in ("tokens", "n_kv_heads", "head_dim", "page_size", "n_pages",
+                                                "reserved")] +
+                [(n, ctypes.c_uint64) for n in ("k_token_stride", "k_head_stride", "v_token_stride", "v_head_stride",
+                                                "page_stride", "head_stride", "token_stride")])
+
+
+class PagedParams(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_uint32) for n in ("batch", "n_heads", "n_kv_heads", "head_dim", "tokens", "max_q_len",
+                                                "window", "page_size", "n_pages", "max_pages", "kernel")] +
+                [("scale", ctypes.c_float)] +
+                [(n, ctypes.c_uint64) for n in ("q_token_stride", "q_head_stride", "out_token_stride",
+                                                "out_head_stride", "page_stride", "head_stride", "token_stride")])
+
+
+class PromptParams(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_uint32) for n in ("batch", "n_heads", "n_kv_heads", "head_dim", "tokens", "window",
+                                                "kernel")] +
+                [("scale", ctypes.c_float)] +
+                [(n, ctypes.c_uint64) for n in ("q_token_stride", "q_head_stride", "out_token_stride",
+                                                "out_head_stride", "k_token_stride", "k_head_stride",
+                                                "v_token_stride", "v_head_stride")])
 
 
 def library_path() -> str:
@@ -120,6 +152,18 @@ def _load() -> ctypes.CDLL:
     L.quant_sdpa_kernel_family.restype = ctypes.c_int
     L.tree_mask_build.argtypes = [PT, B, B, P]
     L.tree_mask_build.restype = ctypes.c_int
+    L.paged_plan_build.argtypes = [ctypes.POINTER(PlanParams)] + [B] * 13 + [P]
+    L.paged_plan_build.restype = ctypes.c_int
+    L.paged_kv_append.argtypes = [ctypes.POINTER(AppendParams)] + [B] * 5 + [P]
+    L.paged_kv_append.restype = ctypes.c_int
+    L.paged_attn_workspace_bytes.argtypes = [ctypes.POINTER(PagedParams)]
+    L.paged_attn_workspace_bytes.restype = ctypes.c_size_t
+    L.paged_attn_fwd.argtypes = [ctypes.POINTER(PagedParams)] + [B] * 9 + [P]
+    L.paged_attn_fwd.restype = ctypes.c_int
+    L.prompt_attn_workspace_bytes.argtypes = [ctypes.POINTER(PromptParams)]
+    L.prompt_attn_workspace_bytes.restype = ctypes.c_size_t
+    L.prompt_attn_fwd.argtypes = [ctypes.POINTER(PromptParams)] + [B] * 6 + [P]
+    L.prompt_attn_fwd.restype = ctypes.c_int
     return L
 
 
@@ -356,3 +400,284 @@ def quant_sdpa(inputs: dict, *, batch: int, n_q_heads: int, n_kv_heads: int, dim
 def tree_mask_build(p: TreeParams, parents: torch.Tensor, mask: torch.Tensor, stream=None):
     """Dense tree mask [q_l, mask_stride] f32 from parents [q_l] int32, on the device."""
     _check(lib.tree_mask_build(ctypes.byref(p), buf(parents, TA_I32), buf(mask), _stream(stream)))
+
+
+# ------------------------------------------------------------------ serving
+# Batched requests on a paged K/V cache.  A step plans its pages and slots
+# (paged_plan), writes the new K/V rows of each layer (paged_append) and
+# attends them (paged_attention); prompt_attention serves whole prompts whose
+# K/V are at hand.  Every length is device data: nothing here waits for the GPU.
+
+class PagedStep(NamedTuple):
+    """What paged_plan writes: pages held and free after the step, row offsets
+    [B + 1], key counts [B], and per new token (-1 behind the last) its cache
+    slot (int64) and its position; `status` collects error bits."""
+    held: torch.Tensor
+    n_free: torch.Tensor
+    cu_q: torch.Tensor
+    kv_lens: torch.Tensor
+    slot_map: torch.Tensor
+    positions: torch.Tensor
+    status: torch.Tensor
+
+
+_SERVE_CODE = {torch.float32: TA_F32, torch.float16: TA_F16, torch.bfloat16: TA_BF16, torch.int32: TA_I32,
+               torch.int64: TA_I64}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _cuda_index(t: torch.Tensor) -> int:
+    if not t.is_cuda:
+        raise ValueError("tensors must be on a CUDA device, got %s" % t.device)
+    return t.get_device()
+
+
+def _current(dev: int) -> ctypes.c_void_p:
+    return ctypes.c_void_p(_raw_stream(dev) if _raw_stream is not None
+                           else torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _as_stream(stream) -> torch.cuda.Stream:
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+
+
+def _flat(t: Optional[torch.Tensor], dev: int) -> Optional[Buf]:
+    """A contiguous tensor on device `dev` as a ta_buf."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.get_device() != dev:
+        raise ValueError("all tensors must be on cuda:%d, got %s" % (dev, t.device))
+    if not t.is_contiguous():
+        raise ValueError("tensor must be contiguous")
+    code = _SERVE_CODE.get(t.dtype)
+    if code is None:
+        raise ValueError("unsupported dtype %s" % t.dtype)
+    return Buf(t.data_ptr(), t.numel() * t.element_size(), code, 0)
+
+
+def _strided(t: torch.Tensor, dev: int, ndim: int, what: str):
+    """A tensor with any outer strides as a ta_buf and its outer strides (0 for
+    an axis of one entry, whose stride means nothing)."""
+    if t.dim() != ndim:
+        raise ValueError("%s must have %d dimensions, got %d" % (what, ndim, t.dim()))
+    if not t.is_cuda or t.get_device() != dev:
+        raise ValueError("all tensors must be on cuda:%d, got %s" % (dev, t.device))
+    code = _SERVE_CODE.get(t.dtype)
+    if code is None:
+        raise ValueError("unsupported dtype %s" % t.dtype)
+    es = t.element_size()
+    if t.is_contiguous():
+        return Buf(t.data_ptr(), t.numel() * es, code, 0), (0,) * (ndim - 1)
+    shape, stride = t.shape, t.stride()
+    if stride[-1] != 1 and shape[-1] > 1:
+        raise ValueError("%s: the last dimension must be contiguous" % what)
+    extent, outer = shape[-1], []
+    for n, s in zip(shape[:-1], stride[:-1]):
+        if n > 1 and s == 0:
+            raise ValueError("%s: a broadcast dimension is not supported" % what)
+        outer.append(s if n > 1 else 0)
+        extent += (n - 1) * s
+    return Buf(t.data_ptr(), extent * es if t.numel() else 0, code, 0), outer
+
+
+def _contiguous_default(strides, shape):
+    """The strides with 0 (an axis of one entry) replaced by a size that is
+    always allowed: C reads 0 as the contiguous layout's stride."""
+    full, step = [], shape[-1]
+    for n in reversed(shape[1:-1]):
+        full.append(step)
+        step *= n
+    full.append(step)
+    full.reverse()
+    return [s or f for s, f in zip(strides, full)]
+
+
+def _ref(b: Optional[Buf]):
+    return None if b is None else ctypes.byref(b)
+
+
+def paged_plan(keep_lens: torch.Tensor, new_lens: torch.Tensor, held: torch.Tensor, block_table: torch.Tensor,
+               free_pages: torch.Tensor, n_free: torch.Tensor, *, page_size: int, max_tokens: int,
+               out=None, stream=None) -> PagedStep:
+    """Plan a step: request b keeps keep_lens[b] cached tokens and gets
+    new_lens[b] new ones (int32 [B]).  Pages it no longer needs go back to the
+    stack free_pages[:n_free], pages it needs are taken from its top; block_table
+    [B, max_pages] and free_pages are updated in place.  `out`: the seven tensors
+    of a PagedStep to write into (its held and n_free may be the inputs)."""
+    if stream is not None:
+        with torch.cuda.stream(_as_stream(stream)):
+            return paged_plan(keep_lens, new_lens, held, block_table, free_pages, n_free, page_size=page_size,
+                              max_tokens=max_tokens, out=out)
+    dev = _cuda_index(block_table)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return paged_plan(keep_lens, new_lens, held, block_table, free_pages, n_free, page_size=page_size,
+                              max_tokens=max_tokens, out=out)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [batch, max_pages]")
+    batch, width = block_table.shape
+    if out is None:
+        def new(n, dtype=torch.int32):
+            return torch.empty(n, dtype=dtype, device=block_table.device)
+        out = (new(batch), new(1), new(batch + 1), new(batch), new(max_tokens, torch.int64), new(max_tokens),
+               torch.zeros(1, dtype=torch.int32, device=block_table.device))
+    step = PagedStep(*out)
+    p = PlanParams(batch, page_size, width, free_pages.numel(), max_tokens, 0)
+    bufs = [_flat(t, dev) for t in (keep_lens, new_lens, held, block_table, free_pages, n_free) + tuple(step)]
+    _check(lib.paged_plan_build(ctypes.byref(p), *[ctypes.byref(b) for b in bufs], _current(dev)))
+    return step
+
+
+def _cache_pair(k_cache, v_cache, dev):
+    kb, ks = _strided(k_cache, dev, 4, "k_cache")
+    vb, vs = _strided(v_cache, dev, 4, "v_cache")
+    if k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache must have one shape")
+    if any(ks) or any(vs):
+        ks, vs = _contiguous_default(ks, k_cache.shape), _contiguous_default(vs, v_cache.shape)
+        if ks != vs:
+            raise ValueError("k_cache and v_cache must have the same strides")
+    return kb, vb, ks
+
+
+def paged_append(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                 slot_map: torch.Tensor, stream=None) -> None:
+    """Write the rows k_new, v_new [T, Hk, D] to the slots slot_map [T] (int64) of
+    the caches [n_pages, Hk, page_size, D]; slots outside the cache (-1) are
+    skipped.  No two rows may have the same slot."""
+    if stream is not None:
+        with torch.cuda.stream(_as_stream(stream)):
+            return paged_append(k_new, v_new, k_cache, v_cache, slot_map)
+    dev = _cuda_index(k_cache)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return paged_append(k_new, v_new, k_cache, v_cache, slot_map)
+    kn, (kt, kh) = _strided(k_new, dev, 3, "k_new")
+    vn, (vt, vh) = _strided(v_new, dev, 3, "v_new")
+    kb, vb, cs = _cache_pair(k_cache, v_cache, dev)
+    n_pages, hk, ps, d = k_cache.shape
+    t = k_new.shape[0]
+    if k_new.shape != v_new.shape or k_new.shape[1] != hk or k_new.shape[2] != d:
+        raise ValueError("k_new and v_new must be [T, %d, %d]" % (hk, d))
+    if slot_map.dim() != 1 or slot_map.shape[0] < t:
+        raise ValueError("slot_map must be [T]")
+    p = AppendParams(t, hk, d, ps, n_pages, 0, kt, kh, vt, vh, cs[0], cs[1], cs[2])
+    _check(lib.paged_kv_append(ctypes.byref(p), ctypes.byref(kn), ctypes.byref(vn), ctypes.byref(kb),
+                               ctypes.byref(vb), _ref(_flat(slot_map, dev)), _current(dev)))
+
+
+def paged_attn_workspace_bytes(p: PagedParams) -> int:
+    return int(lib.paged_attn_workspace_bytes(ctypes.byref(p)))
+
+
+def prompt_attn_workspace_bytes(p: PromptParams) -> int:
+    return int(lib.prompt_attn_workspace_bytes(ctypes.byref(p)))
+
+
+def _workspace(nbytes: int, device) -> torch.Tensor:
+    if nbytes >= 2 ** 63:
+        raise TreeAttentionError(1, ta_last_error())
+    ws = torch.empty((nbytes + 3) // 4, dtype=torch.float32, device=device)
+    ws[:1].zero_()                                   # the status word
+    return ws
+
+
+def paged_attention_workspace(q: torch.Tensor, k_cache: torch.Tensor, block_table: torch.Tensor, *,
+                              max_q_len: int, kernel: int = KERNEL_AUTO) -> torch.Tensor:
+    """A tmp buffer for paged_attention calls of these shapes (its first 32-bit
+    word, zero here, is the status word; calls that overlap must not share it)."""
+    n_pages, hk, ps, d = k_cache.shape
+    p = PagedParams(block_table.shape[0], q.shape[1], hk, d, q.shape[0], max_q_len, 0, ps, n_pages,
+                    block_table.shape[1], kernel, 1.0)
+    with torch.cuda.device(_cuda_index(q)):
+        return _workspace(paged_attn_workspace_bytes(p), q.device)
+
+
+def prompt_attention_workspace(q: torch.Tensor, k: torch.Tensor, cu_seqlens: torch.Tensor, *,
+                               kernel: int = KERNEL_AUTO) -> torch.Tensor:
+    """A tmp buffer for prompt_attention calls of these shapes."""
+    p = PromptParams(cu_seqlens.numel() - 1, q.shape[1], k.shape[1], q.shape[2], q.shape[0], 0, kernel, 1.0)
+    with torch.cuda.device(_cuda_index(q)):
+        return _workspace(prompt_attn_workspace_bytes(p), q.device)
+
+
+def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                    cu_q: torch.Tensor, kv_lens: torch.Tensor, *, scale: float, max_q_len: int, window: int = 0,
+                    parents: Optional[torch.Tensor] = None, tmp: Optional[torch.Tensor] = None,
+                    out: Optional[torch.Tensor] = None, kernel: int = KERNEL_AUTO, stream=None) -> torch.Tensor:
+    """Attention of each request's new tokens over its pages.  q [T, H, D] holds
+    the requests' new tokens one behind the other (cu_q [B + 1]); the caches are
+    [n_pages, Hk, page_size, D] (any strides) and already hold the new tokens'
+    K/V; kv_lens [B] counts all keys.  Token i of q_len sees the keys up to its own
+    position kv_len - q_len + i (the last `window` of them), or, with `parents`
+    (int32 [T], each request's draft tree by index inside its chunk), the prefix,
+    its ancestors and itself.  Returns out [T, H, D] in q's type; rows behind the
+    last request are not written."""
+    if stream is not None:
+        with torch.cuda.stream(_as_stream(stream)):
+            return paged_attention(q, k_cache, v_cache, block_table, cu_q, kv_lens, scale=scale,
+                                   max_q_len=max_q_len, window=window, parents=parents, tmp=tmp, out=out,
+                                   kernel=kernel)
+    dev = _cuda_index(q)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return paged_attention(q, k_cache, v_cache, block_table, cu_q, kv_lens, scale=scale,
+                                   max_q_len=max_q_len, window=window, parents=parents, tmp=tmp, out=out,
+                                   kernel=kernel)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    qb, (qt, qh) = _strided(q, dev, 3, "q")
+    ob, (ot, oh) = _strided(out, dev, 3, "out")
+    kb, vb, cs = _cache_pair(k_cache, v_cache, dev)
+    t, h, d = q.shape
+    n_pages, hk, ps, dk = k_cache.shape
+    if d != dk:
+        raise ValueError("q and the caches must have one head dimension")
+    if block_table.dim() != 2 or cu_q.numel() != block_table.shape[0] + 1 or kv_lens.numel() != block_table.shape[0]:
+        raise ValueError("block_table must be [batch, max_pages], cu_q [batch + 1] and kv_lens [batch]")
+    p = PagedParams(block_table.shape[0], h, hk, d, t, max_q_len, window, ps, n_pages, block_table.shape[1], kernel,
+                    scale, qt, qh, ot, oh, cs[0], cs[1], cs[2])
+    if tmp is None:
+        tmp = _workspace(paged_attn_workspace_bytes(p), q.device)
+    _check(lib.paged_attn_fwd(ctypes.byref(p), ctypes.byref(qb), ctypes.byref(kb), ctypes.byref(vb),
+                              ctypes.byref(_flat(block_table, dev)), ctypes.byref(_flat(cu_q, dev)),
+                              ctypes.byref(_flat(kv_lens, dev)), _ref(_flat(parents, dev)),
+                              ctypes.byref(_flat(tmp, dev)), ctypes.byref(ob), _current(dev)))
+    return out
+
+
+def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, *, scale: float,
+                     window: int = 0, tmp: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                     kernel: int = KERNEL_AUTO, stream=None) -> torch.Tensor:
+    """Causal attention over whole prompts packed one behind the other: q [T, H, D],
+    k and v [T, Hk, D] (any token and head strides, as slices of one projection),
+    cu_seqlens [B + 1] int32 on the device.  Row i of a prompt sees its rows up to
+    i (the last `window` of them).  Returns out [T, H, D] in q's type; rows behind
+    the last prompt are not written."""
+    if stream is not None:
+        with torch.cuda.stream(_as_stream(stream)):
+            return prompt_attention(q, k, v, cu_seqlens, scale=scale, window=window, tmp=tmp, out=out, kernel=kernel)
+    dev = _cuda_index(q)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return prompt_attention(q, k, v, cu_seqlens, scale=scale, window=window, tmp=tmp, out=out, kernel=kernel)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    qb, (qt, qh) = _strided(q, dev, 3, "q")
+    ob, (ot, oh) = _strided(out, dev, 3, "out")
+    kb, (kt, kh) = _strided(k, dev, 3, "k")
+    vb, (vt, vh) = _strided(v, dev, 3, "v")
+    t, h, d = q.shape
+    if k.shape != v.shape or k.shape[0] != t or k.shape[2] != d:
+        raise ValueError("k and v must be [%d, Hk, %d]" % (t, d))
+    p = PromptParams(cu_seqlens.numel() - 1, h, k.shape[1], d, t, window, kernel, scale, qt, qh, ot, oh, kt, kh, vt, vh)
+    if tmp is None:
+        tmp = _workspace(prompt_attn_workspace_bytes(p), q.device)
+    _check(lib.prompt_attn_fwd(ctypes.byref(p), ctypes.byref(qb), ctypes.byref(kb), ctypes.byref(vb),
+                               ctypes.byref(_flat(cu_seqlens, dev)), ctypes.byref(_flat(tmp, dev)),
+                               ctypes.byref(ob), _current(dev)))
+    return out

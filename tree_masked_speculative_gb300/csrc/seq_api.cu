@@ -1,0 +1,402 @@
+// C ABI of the batched serving operators: argument checks (all before any
+// launch, overflow-checked), workspace sizes and kernel choice.
+#include <climits>
+#include <cmath>
+
+#include "seq_internal.cuh"
+#include "tree_attn.h"
+
+#define TA_EXPORT extern "C" __attribute__((visibility("default")))
+
+namespace ta {
+namespace {
+
+#define SEQ_FAIL(st, ...)            \
+    do {                             \
+        set_last_error(__VA_ARGS__); \
+        return st;                   \
+    } while (0)
+#define SEQ_TRY(x)                   \
+    do {                             \
+        const ta_status _s = (x);    \
+        if (_s != TA_OK) return _s;  \
+    } while (0)
+
+constexpr ta_buf kNone = {nullptr, 0, TA_F32, 0};
+bool is_absent(const ta_buf *b) { return b == nullptr || (b->ptr == nullptr && b->bytes == 0); }
+const ta_buf &of(const ta_buf *b) { return b ? *b : kNone; }
+
+const char *type_name(int t) {
+    static const char *const names[] = {"F32", "F16", "BF16", "U32", "I32", "I64"};
+    return t >= 0 && t <= TA_I64 ? names[t] : "unknown";
+}
+
+ta_status check(const char *op, const char *name, const ta_buf &b, int type, uint64_t need, size_t align) {
+    if (b.reserved != 0) SEQ_FAIL(TA_ERR_INVALID_ARGUMENT, "%s: %s: reserved field must be 0", op, name);
+    if (b.ptr == nullptr) SEQ_FAIL(TA_ERR_INVALID_ARGUMENT, "%s: %s: NULL pointer", op, name);
+    if (b.dtype != type)
+        SEQ_FAIL(TA_ERR_INVALID_ARGUMENT, "%s: %s dtype must be %s, got %s", op, name, type_name(type), type_name(b.dtype));
+    if (reinterpret_cast<uintptr_t>(b.ptr) % align != 0)
+        SEQ_FAIL(TA_ERR_INVALID_ARGUMENT, "%s: %s: pointer must be %zu-byte aligned", op, name, align);
+    if (b.bytes < need)
+        SEQ_FAIL(TA_ERR_BUFFER_TOO_SMALL, "%s: %s buffer too small: have %llu bytes, need >= %llu", op, name,
+                 static_cast<unsigned long long>(b.bytes), static_cast<unsigned long long>(need));
+    return TA_OK;
+}
+
+ta_status check_16bit(const char *op, const char *name, const ta_buf &b) {
+    if (b.dtype != TA_F16 && b.dtype != TA_BF16)
+        SEQ_FAIL(TA_ERR_INVALID_ARGUMENT, "%s: %s dtype must be F16 or BF16, got %s", op, name, type_name(b.dtype));
+    return TA_OK;
+}
+
+bool page_size_ok(uint32_t ps) { return ps == 16 || ps == 32 || ps == 64 || ps == 128 || ps == 256; }
+int log2_of(uint32_t ps) { return __builtin_ctz(ps); }
+
+// Bytes of a strided 16-bit array: sum of (n_i - 1) * stride_i, plus the last
+// axis's head_dim elements.  false on overflow.
+struct Axis {
+    uint64_t n, stride;
+};
+template <int N>
+bool extent(const Axis (&ax)[N], uint64_t dim, uint64_t *bytes) {
+    uint64_t e = dim;
+    for (const Axis &x : ax) {
+        uint64_t t;
+        if (__builtin_mul_overflow(x.n - 1, x.stride, &t) || __builtin_add_overflow(e, t, &e)) return false;
+    }
+    return !__builtin_mul_overflow(e, uint64_t(2), bytes) && *bytes <= static_cast<uint64_t>(LLONG_MAX);
+}
+
+ta_status check_stride(const char *op, const char *name, uint64_t s) {
+    if (s % 8 != 0) SEQ_FAIL(TA_ERR_INVALID_ARGUMENT, "%s: %s must be a multiple of 8 elements", op, name);
+    // the range a tensor-map stride holds (2^40 bytes), and signed 64-bit offsets in the kernels
+    if (s >= (uint64_t(1) << 38)) SEQ_FAIL(TA_ERR_UNSUPPORTED, "%s: %s exceeds 2^38 elements", op, name);
+    return TA_OK;
+}
+
+ta_status check_heads(const char *op, uint32_t batch, uint32_t h, uint32_t hk, uint32_t d, uint32_t tokens, uint32_t kernel,
+                      float scale) {
+    if (batch == 0 || h == 0 || hk == 0) SEQ_FAIL(TA_ERR_INVALID_ARGUMENT, "%s: batch, n_heads and n_kv_heads must be > 0", op);
+    if (h % hk != 0) SEQ_FAIL(TA_ERR_INVALID_ARGUMENT, "%s: n_heads (%u) must be divisible by n_kv_heads (%u)", op, h, hk);
+    if (d != 64 && d != 128 && d != 256) SEQ_FAIL(TA_ERR_INVALID_ARGUMENT, "%s: head_dim must be 64, 128 or 256, got %u", op, d);
+    if (h / hk > 128) SEQ_FAIL(TA_ERR_UNSUPPORTED, "%s: more than 128 query heads per KV head", op);
+    if (batch > 65535 || hk > 65535 || static_cast<uint64_t>(tokens) * h > static_cast<uint64_t>(INT_MAX))
+        SEQ_FAIL(TA_ERR_UNSUPPORTED, "%s: sizes exceed the kernels' index range", op);
+    if (kernel > TA_KERNEL_WARP_MMA) SEQ_FAIL(TA_ERR_INVALID_ARGUMENT, "%s: kernel must be 0 (auto), 1, 2 or 3, got %u", op, kernel);
+    if (!std::isfinite(scale)) SEQ_FAIL(TA_ERR_INVALID_ARGUMENT, "%s: scale is not finite", op);
+    return TA_OK;
+}
+
+// Contiguous strides where the caller gave 0.
+void row_strides(uint64_t h, uint64_t d, uint64_t *token, uint64_t *head) {
+    if (*head == 0) *head = d;
+    if (*token == 0) *token = h * d;
+}
+void cache_strides(uint64_t hk, uint64_t ps, uint64_t d, uint64_t *page, uint64_t *head, uint64_t *token) {
+    if (*token == 0) *token = d;
+    if (*head == 0) *head = ps * d;
+    if (*page == 0) *page = hk * ps * d;
+}
+
+constexpr uint64_t kStatusBytes = 256;
+
+ta_status check_paged(const ta_paged_params *p) {
+    if (p == nullptr) SEQ_FAIL(TA_ERR_INVALID_ARGUMENT, "paged_attn: params is NULL");
+    SEQ_TRY(check_heads("paged_attn", p->batch, p->n_heads, p->n_kv_heads, p->head_dim, p->tokens, p->kernel, p->scale));
+    if (p->max_q_len == 0) SEQ_FAIL(TA_ERR_INVALID_ARGUMENT, "paged_attn: max_q_len must be > 0");
+    if (!page_size_ok(p->page_size))
+        SEQ_FAIL(TA_ERR_INVALID_ARGUMENT, "paged_attn: page_size must be 16, 32, 64, 128 or 256, got %u", p->page_size);
+    if (p->n_pages == 0 || p->max_pages == 0)
+        SEQ_FAIL(TA_ERR_INVALID_ARGUMENT, "paged_attn: n_pages and max_pages must be > 0");
+    if (p->window > static_cast<uint32_t>(INT_MAX) || p->max_q_len > static_cast<uint32_t>(INT_MAX) ||
+        p->n_pages > static_cast<uint32_t>(INT_MAX) ||
+        static_cast<uint64_t>(p->max_pages) * p->page_size > static_cast<uint64_t>(INT_MAX) / 2)
+        SEQ_FAIL(TA_ERR_UNSUPPORTED, "paged_attn: sizes exceed the kernels' index range");
+    return TA_OK;
+}
+
+ta_status check_prompt(const ta_prompt_params *p) {
+    if (p == nullptr) SEQ_FAIL(TA_ERR_INVALID_ARGUMENT, "prompt_attn: params is NULL");
+    SEQ_TRY(check_heads("prompt_attn", p->batch, p->n_heads, p->n_kv_heads, p->head_dim, p->tokens, p->kernel, p->scale));
+    if (p->window > static_cast<uint32_t>(INT_MAX))
+        SEQ_FAIL(TA_ERR_UNSUPPORTED, "prompt_attn: sizes exceed the kernels' index range");
+    return TA_OK;
+}
+
+// Workspace: the status word's 256 bytes.
+uint64_t seq_workspace(uint32_t, uint32_t, uint32_t, uint32_t) { return kStatusBytes; }
+
+ta_status run_seq(const char *op, const SeqArgs &a, cudaStream_t s) {
+    const cudaError_t e = launch_seq_fma(a, s);
+    if (e != cudaSuccess) SEQ_FAIL(TA_ERR_CUDA, "%s: launch: %s", op, cudaGetErrorString(e));
+    return TA_OK;
+}
+
+}  // namespace
+}  // namespace ta
+
+using namespace ta;
+
+TA_EXPORT ta_status paged_plan_build(const ta_plan_params *p, const ta_buf *keep, const ta_buf *fresh, const ta_buf *held,
+                                     const ta_buf *table, const ta_buf *stack, const ta_buf *n_free,
+                                     const ta_buf *held_out, const ta_buf *n_free_out, const ta_buf *cu,
+                                     const ta_buf *kv_lens, const ta_buf *slot_map, const ta_buf *positions,
+                                     const ta_buf *status, void *stream) {
+    const char *op = "paged_plan";
+    if (p == nullptr) SEQ_FAIL(TA_ERR_INVALID_ARGUMENT, "paged_plan: params is NULL");
+    if (p->reserved != 0) SEQ_FAIL(TA_ERR_INVALID_ARGUMENT, "paged_plan: reserved must be 0");
+    if (p->batch == 0) SEQ_FAIL(TA_ERR_INVALID_ARGUMENT, "paged_plan: batch must be > 0");
+    if (!page_size_ok(p->page_size))
+        SEQ_FAIL(TA_ERR_INVALID_ARGUMENT, "paged_plan: page_size must be 16, 32, 64, 128 or 256, got %u", p->page_size);
+    if (p->max_pages == 0) SEQ_FAIL(TA_ERR_INVALID_ARGUMENT, "paged_plan: max_pages must be > 0");
+    if (p->batch > static_cast<uint32_t>(kPlanMaxBatch))
+        SEQ_FAIL(TA_ERR_UNSUPPORTED, "paged_plan: batch > %d is not implemented", kPlanMaxBatch);
+    if (static_cast<uint64_t>(p->max_pages) * p->page_size > static_cast<uint64_t>(INT_MAX) ||
+        static_cast<uint64_t>(p->batch) * p->max_pages > static_cast<uint64_t>(INT_MAX) / 2 ||
+        p->capacity > static_cast<uint32_t>(INT_MAX) / 2 || p->max_tokens > static_cast<uint32_t>(INT_MAX) / 2)
+        SEQ_FAIL(TA_ERR_UNSUPPORTED, "paged_plan: sizes exceed the kernel's index range");
+    const uint64_t b4 = static_cast<uint64_t>(p->batch) * 4;
+    SEQ_TRY(check(op, "keep", of(keep), TA_I32, b4, 4));
+    SEQ_TRY(check(op, "fresh", of(fresh), TA_I32, b4, 4));
+    SEQ_TRY(check(op, "held", of(held), TA_I32, b4, 4));
+    SEQ_TRY(check(op, "table", of(table), TA_I32, b4 * p->max_pages, 4));
+    if (p->capacity > 0) SEQ_TRY(check(op, "stack", of(stack), TA_I32, static_cast<uint64_t>(p->capacity) * 4, 4));
+    SEQ_TRY(check(op, "n_free", of(n_free), TA_I32, 4, 4));
+    SEQ_TRY(check(op, "held_out", of(held_out), TA_I32, b4, 4));
+    SEQ_TRY(check(op, "n_free_out", of(n_free_out), TA_I32, 4, 4));
+    SEQ_TRY(check(op, "cu", of(cu), TA_I32, b4 + 4, 4));
+    SEQ_TRY(check(op, "kv_lens", of(kv_lens), TA_I32, b4, 4));
+    if (p->max_tokens > 0) {
+        SEQ_TRY(check(op, "slot_map", of(slot_map), TA_I64, static_cast<uint64_t>(p->max_tokens) * 8, 8));
+        SEQ_TRY(check(op, "positions", of(positions), TA_I32, static_cast<uint64_t>(p->max_tokens) * 4, 4));
+    }
+    SEQ_TRY(check(op, "status", of(status), TA_I32, 4, 4));
+    PlanArgs a;
+    a.keep = static_cast<const int32_t *>(keep->ptr);
+    a.fresh = static_cast<const int32_t *>(fresh->ptr);
+    a.held = static_cast<const int32_t *>(held->ptr);
+    a.table = static_cast<int32_t *>(table->ptr);
+    a.stack = static_cast<int32_t *>(of(stack).ptr);
+    a.n_free = static_cast<const int32_t *>(n_free->ptr);
+    a.held_out = static_cast<int32_t *>(held_out->ptr);
+    a.n_free_out = static_cast<int32_t *>(n_free_out->ptr);
+    a.cu = static_cast<int32_t *>(cu->ptr);
+    a.lens = static_cast<int32_t *>(kv_lens->ptr);
+    a.slot = static_cast<int64_t *>(of(slot_map).ptr);
+    a.pos = static_cast<int32_t *>(of(positions).ptr);
+    a.status = static_cast<int32_t *>(status->ptr);
+    a.B = static_cast<int>(p->batch);
+    a.max_pages = static_cast<int>(p->max_pages);
+    a.capacity = static_cast<int>(p->capacity);
+    a.max_tokens = static_cast<int>(p->max_tokens);
+    a.page_shift = log2_of(p->page_size);
+    const cudaError_t e = launch_paged_plan(a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) SEQ_FAIL(TA_ERR_CUDA, "paged_plan: launch: %s", cudaGetErrorString(e));
+    return TA_OK;
+}
+
+TA_EXPORT ta_status paged_kv_append(const ta_append_params *pp, const ta_buf *k_new, const ta_buf *v_new,
+                                    const ta_buf *k_cache, const ta_buf *v_cache, const ta_buf *slot_map, void *stream) {
+    const char *op = "paged_append";
+    if (pp == nullptr) SEQ_FAIL(TA_ERR_INVALID_ARGUMENT, "paged_append: params is NULL");
+    ta_append_params p = *pp;
+    if (p.reserved != 0) SEQ_FAIL(TA_ERR_INVALID_ARGUMENT, "paged_append: reserved must be 0");
+    if (p.n_kv_heads == 0 || p.n_pages == 0) SEQ_FAIL(TA_ERR_INVALID_ARGUMENT, "paged_append: n_kv_heads and n_pages must be > 0");
+    if (p.head_dim != 64 && p.head_dim != 128 && p.head_dim != 256)
+        SEQ_FAIL(TA_ERR_INVALID_ARGUMENT, "paged_append: head_dim must be 64, 128 or 256, got %u", p.head_dim);
+    if (!page_size_ok(p.page_size))
+        SEQ_FAIL(TA_ERR_INVALID_ARGUMENT, "paged_append: page_size must be 16, 32, 64, 128 or 256, got %u", p.page_size);
+    if (p.n_kv_heads > 65535 || p.tokens > static_cast<uint32_t>(INT_MAX) || p.n_pages > static_cast<uint32_t>(INT_MAX))
+        SEQ_FAIL(TA_ERR_UNSUPPORTED, "paged_append: sizes exceed the kernel's index range");
+    row_strides(p.n_kv_heads, p.head_dim, &p.k_token_stride, &p.k_head_stride);
+    row_strides(p.n_kv_heads, p.head_dim, &p.v_token_stride, &p.v_head_stride);
+    cache_strides(p.n_kv_heads, p.page_size, p.head_dim, &p.page_stride, &p.head_stride, &p.token_stride);
+    SEQ_TRY(check_stride(op, "k_token_stride", p.k_token_stride));
+    SEQ_TRY(check_stride(op, "k_head_stride", p.k_head_stride));
+    SEQ_TRY(check_stride(op, "v_token_stride", p.v_token_stride));
+    SEQ_TRY(check_stride(op, "v_head_stride", p.v_head_stride));
+    SEQ_TRY(check_stride(op, "page_stride", p.page_stride));
+    SEQ_TRY(check_stride(op, "head_stride", p.head_stride));
+    SEQ_TRY(check_stride(op, "token_stride", p.token_stride));
+    if (p.tokens == 0) return TA_OK;
+    SEQ_TRY(check_16bit(op, "k_new", of(k_new)));
+    const int type = k_new->dtype;
+    uint64_t nk, nv, nc;
+    const Axis kax[2] = {{p.tokens, p.k_token_stride}, {p.n_kv_heads, p.k_head_stride}};
+    const Axis vax[2] = {{p.tokens, p.v_token_stride}, {p.n_kv_heads, p.v_head_stride}};
+    const Axis cax[3] = {{p.n_pages, p.page_stride}, {p.n_kv_heads, p.head_stride}, {p.page_size, p.token_stride}};
+    if (!extent(kax, p.head_dim, &nk) || !extent(vax, p.head_dim, &nv) || !extent(cax, p.head_dim, &nc))
+        SEQ_FAIL(TA_ERR_OVERFLOW, "paged_append: sizes overflow");
+    SEQ_TRY(check(op, "k_new", *k_new, type, nk, 16));
+    SEQ_TRY(check(op, "v_new", of(v_new), type, nv, 16));
+    SEQ_TRY(check(op, "k_cache", of(k_cache), type, nc, 16));
+    SEQ_TRY(check(op, "v_cache", of(v_cache), type, nc, 16));
+    SEQ_TRY(check(op, "slot_map", of(slot_map), TA_I64, static_cast<uint64_t>(p.tokens) * 8, 8));
+    AppendArgs a;
+    a.k_new = k_new->ptr;
+    a.v_new = v_new->ptr;
+    a.k = k_cache->ptr;
+    a.v = v_cache->ptr;
+    a.slot = static_cast<const int64_t *>(slot_map->ptr);
+    a.T = static_cast<int>(p.tokens);
+    a.Hk = static_cast<int>(p.n_kv_heads);
+    a.D = static_cast<int>(p.head_dim);
+    a.page_shift = log2_of(p.page_size);
+    a.n_pages = static_cast<int>(p.n_pages);
+    // the kernel counts in 16-byte vectors
+    a.kn_st = static_cast<long long>(p.k_token_stride / 8);
+    a.kn_sh = static_cast<long long>(p.k_head_stride / 8);
+    a.vn_st = static_cast<long long>(p.v_token_stride / 8);
+    a.vn_sh = static_cast<long long>(p.v_head_stride / 8);
+    a.c_sp = static_cast<long long>(p.page_stride / 8);
+    a.c_st = static_cast<long long>(p.token_stride / 8);
+    a.c_sh = static_cast<long long>(p.head_stride / 8);
+    const cudaError_t e = launch_paged_append(a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) SEQ_FAIL(TA_ERR_CUDA, "paged_append: launch: %s", cudaGetErrorString(e));
+    return TA_OK;
+}
+
+TA_EXPORT size_t paged_attn_workspace_bytes(const ta_paged_params *p) {
+    if (check_paged(p) != TA_OK) return SIZE_MAX;
+    return seq_workspace(p->n_heads, p->n_kv_heads, p->head_dim, p->max_q_len);
+}
+
+TA_EXPORT size_t prompt_attn_workspace_bytes(const ta_prompt_params *p) {
+    if (check_prompt(p) != TA_OK) return SIZE_MAX;
+    return seq_workspace(p->n_heads, p->n_kv_heads, p->head_dim, p->tokens);
+}
+
+TA_EXPORT ta_status paged_attn_fwd(const ta_paged_params *pp, const ta_buf *q, const ta_buf *k_cache,
+                                   const ta_buf *v_cache, const ta_buf *table, const ta_buf *cu, const ta_buf *kv_lens,
+                                   const ta_buf *parents, const ta_buf *tmp, const ta_buf *out, void *stream) {
+    const char *op = "paged_attn";
+    SEQ_TRY(check_paged(pp));
+    ta_paged_params p = *pp;
+    const bool tree = !is_absent(parents);
+    if (tree && p.window != 0) SEQ_FAIL(TA_ERR_INVALID_ARGUMENT, "paged_attn: window must be 0 with parents");
+    if (tree && p.max_q_len > static_cast<uint32_t>(kMaxTreeBitsNodes))
+        SEQ_FAIL(TA_ERR_UNSUPPORTED, "paged_attn: parents take max_q_len <= %d (got %u)", kMaxTreeBitsNodes, p.max_q_len);
+    row_strides(p.n_heads, p.head_dim, &p.q_token_stride, &p.q_head_stride);
+    row_strides(p.n_heads, p.head_dim, &p.out_token_stride, &p.out_head_stride);
+    cache_strides(p.n_kv_heads, p.page_size, p.head_dim, &p.page_stride, &p.head_stride, &p.token_stride);
+    SEQ_TRY(check_stride(op, "q_token_stride", p.q_token_stride));
+    SEQ_TRY(check_stride(op, "q_head_stride", p.q_head_stride));
+    SEQ_TRY(check_stride(op, "out_token_stride", p.out_token_stride));
+    SEQ_TRY(check_stride(op, "out_head_stride", p.out_head_stride));
+    SEQ_TRY(check_stride(op, "page_stride", p.page_stride));
+    SEQ_TRY(check_stride(op, "head_stride", p.head_stride));
+    SEQ_TRY(check_stride(op, "token_stride", p.token_stride));
+    if (p.tokens == 0) return TA_OK;
+    SEQ_TRY(check_16bit(op, "q", of(q)));
+    const int type = q->dtype;
+    uint64_t nq, no, nc;
+    const Axis qax[2] = {{p.tokens, p.q_token_stride}, {p.n_heads, p.q_head_stride}};
+    const Axis oax[2] = {{p.tokens, p.out_token_stride}, {p.n_heads, p.out_head_stride}};
+    const Axis cax[3] = {{p.n_pages, p.page_stride}, {p.n_kv_heads, p.head_stride}, {p.page_size, p.token_stride}};
+    if (!extent(qax, p.head_dim, &nq) || !extent(oax, p.head_dim, &no) || !extent(cax, p.head_dim, &nc))
+        SEQ_FAIL(TA_ERR_OVERFLOW, "paged_attn: sizes overflow");
+    const uint64_t ws = seq_workspace(p.n_heads, p.n_kv_heads, p.head_dim, p.max_q_len);
+    SEQ_TRY(check(op, "q", *q, type, nq, 16));
+    SEQ_TRY(check(op, "k_cache", of(k_cache), type, nc, 16));
+    SEQ_TRY(check(op, "v_cache", of(v_cache), type, nc, 16));
+    SEQ_TRY(check(op, "table", of(table), TA_I32, static_cast<uint64_t>(p.batch) * p.max_pages * 4, 4));
+    SEQ_TRY(check(op, "cu", of(cu), TA_I32, (static_cast<uint64_t>(p.batch) + 1) * 4, 4));
+    SEQ_TRY(check(op, "kv_lens", of(kv_lens), TA_I32, static_cast<uint64_t>(p.batch) * 4, 4));
+    if (tree) SEQ_TRY(check(op, "parents", *parents, TA_I32, static_cast<uint64_t>(p.tokens) * 4, 4));
+    SEQ_TRY(check(op, "tmp", of(tmp), TA_F32, ws, 16));
+    SEQ_TRY(check(op, "out", of(out), type, no, 16));
+    SeqArgs a = {};
+    a.q = q->ptr;
+    a.k = k_cache->ptr;
+    a.v = v_cache->ptr;
+    a.out = out->ptr;
+    a.cu = static_cast<const int32_t *>(cu->ptr);
+    a.kv_lens = static_cast<const int32_t *>(kv_lens->ptr);
+    a.table = static_cast<const int32_t *>(table->ptr);
+    a.parents = tree ? static_cast<const int32_t *>(parents->ptr) : nullptr;
+    a.status = static_cast<int32_t *>(tmp->ptr);
+    a.B = static_cast<int>(p.batch);
+    a.H = static_cast<int>(p.n_heads);
+    a.Hk = static_cast<int>(p.n_kv_heads);
+    a.g = a.H / a.Hk;
+    a.D = static_cast<int>(p.head_dim);
+    a.T = static_cast<int>(p.tokens);
+    a.max_q = static_cast<int>(p.max_q_len);
+    a.window = static_cast<int>(p.window);
+    a.page_shift = log2_of(p.page_size);
+    a.n_pages = static_cast<int>(p.n_pages);
+    a.max_pages = static_cast<int>(p.max_pages);
+    a.bf16 = type == TA_BF16;
+    a.q_st = static_cast<long long>(p.q_token_stride);
+    a.q_sh = static_cast<long long>(p.q_head_stride);
+    a.o_st = static_cast<long long>(p.out_token_stride);
+    a.o_sh = static_cast<long long>(p.out_head_stride);
+    a.k_sp = static_cast<long long>(p.page_stride);
+    a.k_st = a.v_st = static_cast<long long>(p.token_stride);
+    a.k_sh = a.v_sh = static_cast<long long>(p.head_stride);
+    a.scale = p.scale;
+    return run_seq(op, a, static_cast<cudaStream_t>(stream));
+}
+
+TA_EXPORT ta_status prompt_attn_fwd(const ta_prompt_params *pp, const ta_buf *q, const ta_buf *k, const ta_buf *v,
+                                    const ta_buf *cu, const ta_buf *tmp, const ta_buf *out, void *stream) {
+    const char *op = "prompt_attn";
+    SEQ_TRY(check_prompt(pp));
+    ta_prompt_params p = *pp;
+    row_strides(p.n_heads, p.head_dim, &p.q_token_stride, &p.q_head_stride);
+    row_strides(p.n_heads, p.head_dim, &p.out_token_stride, &p.out_head_stride);
+    row_strides(p.n_kv_heads, p.head_dim, &p.k_token_stride, &p.k_head_stride);
+    row_strides(p.n_kv_heads, p.head_dim, &p.v_token_stride, &p.v_head_stride);
+    SEQ_TRY(check_stride(op, "q_token_stride", p.q_token_stride));
+    SEQ_TRY(check_stride(op, "q_head_stride", p.q_head_stride));
+    SEQ_TRY(check_stride(op, "out_token_stride", p.out_token_stride));
+    SEQ_TRY(check_stride(op, "out_head_stride", p.out_head_stride));
+    SEQ_TRY(check_stride(op, "k_token_stride", p.k_token_stride));
+    SEQ_TRY(check_stride(op, "k_head_stride", p.k_head_stride));
+    SEQ_TRY(check_stride(op, "v_token_stride", p.v_token_stride));
+    SEQ_TRY(check_stride(op, "v_head_stride", p.v_head_stride));
+    if (p.tokens == 0) return TA_OK;
+    SEQ_TRY(check_16bit(op, "q", of(q)));
+    const int type = q->dtype;
+    uint64_t nq, no, nk, nv;
+    const Axis qax[2] = {{p.tokens, p.q_token_stride}, {p.n_heads, p.q_head_stride}};
+    const Axis oax[2] = {{p.tokens, p.out_token_stride}, {p.n_heads, p.out_head_stride}};
+    const Axis kax[2] = {{p.tokens, p.k_token_stride}, {p.n_kv_heads, p.k_head_stride}};
+    const Axis vax[2] = {{p.tokens, p.v_token_stride}, {p.n_kv_heads, p.v_head_stride}};
+    if (!extent(qax, p.head_dim, &nq) || !extent(oax, p.head_dim, &no) || !extent(kax, p.head_dim, &nk) ||
+        !extent(vax, p.head_dim, &nv))
+        SEQ_FAIL(TA_ERR_OVERFLOW, "prompt_attn: sizes overflow");
+    const uint64_t ws = seq_workspace(p.n_heads, p.n_kv_heads, p.head_dim, p.tokens);
+    SEQ_TRY(check(op, "q", *q, type, nq, 16));
+    SEQ_TRY(check(op, "k", of(k), type, nk, 16));
+    SEQ_TRY(check(op, "v", of(v), type, nv, 16));
+    SEQ_TRY(check(op, "cu", of(cu), TA_I32, (static_cast<uint64_t>(p.batch) + 1) * 4, 4));
+    SEQ_TRY(check(op, "tmp", of(tmp), TA_F32, ws, 16));
+    SEQ_TRY(check(op, "out", of(out), type, no, 16));
+    SeqArgs a = {};
+    a.q = q->ptr;
+    a.k = k->ptr;
+    a.v = v->ptr;
+    a.out = out->ptr;
+    a.cu = static_cast<const int32_t *>(cu->ptr);
+    a.status = static_cast<int32_t *>(tmp->ptr);
+    a.B = static_cast<int>(p.batch);
+    a.H = static_cast<int>(p.n_heads);
+    a.Hk = static_cast<int>(p.n_kv_heads);
+    a.g = a.H / a.Hk;
+    a.D = static_cast<int>(p.head_dim);
+    a.T = a.max_q = static_cast<int>(p.tokens);
+    a.window = static_cast<int>(p.window);
+    a.bf16 = type == TA_BF16;
+    a.q_st = static_cast<long long>(p.q_token_stride);
+    a.q_sh = static_cast<long long>(p.q_head_stride);
+    a.o_st = static_cast<long long>(p.out_token_stride);
+    a.o_sh = static_cast<long long>(p.out_head_stride);
+    a.k_st = static_cast<long long>(p.k_token_stride);
+    a.k_sh = static_cast<long long>(p.k_head_stride);
+    a.v_st = static_cast<long long>(p.v_token_stride);
+    a.v_sh = static_cast<long long>(p.v_head_stride);
+    a.scale = p.scale;
+    return run_seq(op, a, static_cast<cudaStream_t>(stream));
+}
