@@ -124,11 +124,47 @@ ta_status check_prompt(const ta_prompt_params *p) {
     return TA_OK;
 }
 
-// Workspace: the status word's 256 bytes.
-uint64_t seq_workspace(uint32_t, uint32_t, uint32_t, uint32_t) { return kStatusBytes; }
+// Workspace of a call; 0 when no device is visible to size the grid for.
+uint64_t seq_workspace(uint32_t d, uint32_t kernel) {
+    if (kernel == TA_KERNEL_CUDA_CORES) return kStatusBytes;
+    const int sms = device_sm_count();
+    return sms > 0 ? seq_tc_workspace(static_cast<int>(d), sms) : 0;
+}
 
-ta_status run_seq(const char *op, const SeqArgs &a, cudaStream_t s) {
-    const cudaError_t e = launch_seq_fma(a, s);
+// Tensor map of K or V: {D, page_size, Hk, n_pages} (paged) or {D, T, Hk}.
+bool kv_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap *m, const SeqArgs &a, const void *ptr, long long st,
+            long long sh) {
+    const cuuint64_t ps = cuuint64_t(1) << a.page_shift;
+    const cuuint32_t tk = static_cast<cuuint32_t>(seq_tc_tile_keys(a.D));
+    cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.D), ps, static_cast<cuuint64_t>(a.Hk), static_cast<cuuint64_t>(a.n_pages)};
+    const cuuint64_t str[3] = {static_cast<cuuint64_t>(st) * 2, static_cast<cuuint64_t>(sh) * 2, static_cast<cuuint64_t>(a.k_sp) * 2};
+    cuuint32_t box[4] = {64, static_cast<cuuint32_t>(ps < tk ? ps : tk), 1, 1};
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    int rank = 4;
+    if (a.kv_lens == nullptr) {
+        dims[1] = static_cast<cuuint64_t>(a.T);
+        box[1] = tk;
+        rank = 3;
+    }
+    return encode(m, a.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
+                  const_cast<void *>(ptr), dims, str, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+ta_status run_seq(const char *op, const SeqArgs &a, uint32_t kernel, void *ws, cudaStream_t s) {
+    cudaError_t e;
+    if (kernel == TA_KERNEL_CUDA_CORES) {
+        e = launch_seq_fma(a, s);
+    } else {
+        SeqTcPlan pl;
+        pl.G = device_sm_count();
+        pl.ws = ws;
+        const auto encode = tensor_map_encoder();
+        if (encode == nullptr) SEQ_FAIL(TA_ERR_CUDA, "%s: cuTensorMapEncodeTiled is not available", op);
+        if (!kv_map(encode, &pl.k, a, a.k, a.k_st, a.k_sh) || !kv_map(encode, &pl.v, a, a.v, a.v_st, a.v_sh))
+            SEQ_FAIL(TA_ERR_CUDA, "%s: TMA descriptor encoding failed", op);
+        e = a.D == 64 ? launch_seq_tc64(a, pl, s) : a.D == 128 ? launch_seq_tc128(a, pl, s) : launch_seq_tc256(a, pl, s);
+    }
     if (e != cudaSuccess) SEQ_FAIL(TA_ERR_CUDA, "%s: launch: %s", op, cudaGetErrorString(e));
     return TA_OK;
 }
@@ -259,12 +295,16 @@ TA_EXPORT ta_status paged_kv_append(const ta_append_params *pp, const ta_buf *k_
 
 TA_EXPORT size_t paged_attn_workspace_bytes(const ta_paged_params *p) {
     if (check_paged(p) != TA_OK) return SIZE_MAX;
-    return seq_workspace(p->n_heads, p->n_kv_heads, p->head_dim, p->max_q_len);
+    const uint64_t ws = seq_workspace(p->head_dim, p->kernel);
+    if (ws == 0) set_last_error("paged_attn: no CUDA device to size the workspace for");
+    return ws ? ws : SIZE_MAX;
 }
 
 TA_EXPORT size_t prompt_attn_workspace_bytes(const ta_prompt_params *p) {
     if (check_prompt(p) != TA_OK) return SIZE_MAX;
-    return seq_workspace(p->n_heads, p->n_kv_heads, p->head_dim, p->tokens);
+    const uint64_t ws = seq_workspace(p->head_dim, p->kernel);
+    if (ws == 0) set_last_error("prompt_attn: no CUDA device to size the workspace for");
+    return ws ? ws : SIZE_MAX;
 }
 
 TA_EXPORT ta_status paged_attn_fwd(const ta_paged_params *pp, const ta_buf *q, const ta_buf *k_cache,
@@ -296,7 +336,7 @@ TA_EXPORT ta_status paged_attn_fwd(const ta_paged_params *pp, const ta_buf *q, c
     const Axis cax[3] = {{p.n_pages, p.page_stride}, {p.n_kv_heads, p.head_stride}, {p.page_size, p.token_stride}};
     if (!extent(qax, p.head_dim, &nq) || !extent(oax, p.head_dim, &no) || !extent(cax, p.head_dim, &nc))
         SEQ_FAIL(TA_ERR_OVERFLOW, "paged_attn: sizes overflow");
-    const uint64_t ws = seq_workspace(p.n_heads, p.n_kv_heads, p.head_dim, p.max_q_len);
+    const uint64_t ws = seq_workspace(p.head_dim, p.kernel);
     SEQ_TRY(check(op, "q", *q, type, nq, 16));
     SEQ_TRY(check(op, "k_cache", of(k_cache), type, nc, 16));
     SEQ_TRY(check(op, "v_cache", of(v_cache), type, nc, 16));
@@ -304,7 +344,7 @@ TA_EXPORT ta_status paged_attn_fwd(const ta_paged_params *pp, const ta_buf *q, c
     SEQ_TRY(check(op, "cu", of(cu), TA_I32, (static_cast<uint64_t>(p.batch) + 1) * 4, 4));
     SEQ_TRY(check(op, "kv_lens", of(kv_lens), TA_I32, static_cast<uint64_t>(p.batch) * 4, 4));
     if (tree) SEQ_TRY(check(op, "parents", *parents, TA_I32, static_cast<uint64_t>(p.tokens) * 4, 4));
-    SEQ_TRY(check(op, "tmp", of(tmp), TA_F32, ws, 16));
+    SEQ_TRY(check(op, "tmp", of(tmp), TA_F32, ws ? ws : kStatusBytes, 16));
     SEQ_TRY(check(op, "out", of(out), type, no, 16));
     SeqArgs a = {};
     a.q = q->ptr;
@@ -336,7 +376,8 @@ TA_EXPORT ta_status paged_attn_fwd(const ta_paged_params *pp, const ta_buf *q, c
     a.k_st = a.v_st = static_cast<long long>(p.token_stride);
     a.k_sh = a.v_sh = static_cast<long long>(p.head_stride);
     a.scale = p.scale;
-    return run_seq(op, a, static_cast<cudaStream_t>(stream));
+    if (ws == 0) SEQ_FAIL(TA_ERR_CUDA, "%s: no CUDA device", op);
+    return run_seq(op, a, p.kernel, tmp->ptr, static_cast<cudaStream_t>(stream));
 }
 
 TA_EXPORT ta_status prompt_attn_fwd(const ta_prompt_params *pp, const ta_buf *q, const ta_buf *k, const ta_buf *v,
@@ -367,12 +408,12 @@ TA_EXPORT ta_status prompt_attn_fwd(const ta_prompt_params *pp, const ta_buf *q,
     if (!extent(qax, p.head_dim, &nq) || !extent(oax, p.head_dim, &no) || !extent(kax, p.head_dim, &nk) ||
         !extent(vax, p.head_dim, &nv))
         SEQ_FAIL(TA_ERR_OVERFLOW, "prompt_attn: sizes overflow");
-    const uint64_t ws = seq_workspace(p.n_heads, p.n_kv_heads, p.head_dim, p.tokens);
+    const uint64_t ws = seq_workspace(p.head_dim, p.kernel);
     SEQ_TRY(check(op, "q", *q, type, nq, 16));
     SEQ_TRY(check(op, "k", of(k), type, nk, 16));
     SEQ_TRY(check(op, "v", of(v), type, nv, 16));
     SEQ_TRY(check(op, "cu", of(cu), TA_I32, (static_cast<uint64_t>(p.batch) + 1) * 4, 4));
-    SEQ_TRY(check(op, "tmp", of(tmp), TA_F32, ws, 16));
+    SEQ_TRY(check(op, "tmp", of(tmp), TA_F32, ws ? ws : kStatusBytes, 16));
     SEQ_TRY(check(op, "out", of(out), type, no, 16));
     SeqArgs a = {};
     a.q = q->ptr;
@@ -398,5 +439,6 @@ TA_EXPORT ta_status prompt_attn_fwd(const ta_prompt_params *pp, const ta_buf *q,
     a.v_st = static_cast<long long>(p.v_token_stride);
     a.v_sh = static_cast<long long>(p.v_head_stride);
     a.scale = p.scale;
-    return run_seq(op, a, static_cast<cudaStream_t>(stream));
+    if (ws == 0) SEQ_FAIL(TA_ERR_CUDA, "%s: no CUDA device", op);
+    return run_seq(op, a, p.kernel, tmp->ptr, static_cast<cudaStream_t>(stream));
 }

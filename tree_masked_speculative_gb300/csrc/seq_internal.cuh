@@ -67,6 +67,25 @@ __device__ __forceinline__ SeqReq seq_request(const SeqArgs &a, int b) {
 
 cudaError_t launch_seq_fma(const SeqArgs &a, cudaStream_t s);
 
+// Tensor-core kernel: grid size, workspace and the tensor maps of K and V.
+struct SeqTcPlan {
+    int G;
+    void *ws;
+    CUtensorMap k, v;
+};
+// Keys per key tile and rows per row tile of the tensor-core kernel.
+constexpr int seq_tc_tile_keys(int d) { return d == 256 ? 64 : 128; }
+constexpr int seq_tc_rows(int d) { return d == 256 ? 128 : 256; }
+// Its workspace on a grid of G CTAs: status, records, (m, l) and O of 2 G partial
+// slots, and the marks of columns that are not finite (8 pieces a CTA).
+constexpr unsigned long long seq_tc_workspace(int d, int G) {
+    return 256ull + (G * 16ull + 255) / 256 * 256 + 2ull * G * seq_tc_rows(d) * (8ull + 4ull * d) +
+           8ull * G * seq_tc_rows(d) * (d / 8);
+}
+cudaError_t launch_seq_tc64(const SeqArgs &a, const SeqTcPlan &pl, cudaStream_t s);
+cudaError_t launch_seq_tc128(const SeqArgs &a, const SeqTcPlan &pl, cudaStream_t s);
+cudaError_t launch_seq_tc256(const SeqArgs &a, const SeqTcPlan &pl, cudaStream_t s);
+
 // ---------------------------------------------------------------- planning
 struct PlanArgs {
     const int32_t *keep, *fresh, *held;

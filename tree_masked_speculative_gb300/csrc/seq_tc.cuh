@@ -1,0 +1,748 @@
+// Attention of ragged rows on the 5th-generation tensor core (tcgen05): paged
+// K/V (PAGED) or packed prompts, f16 / bf16, head dimension 64, 128 or 256.
+//
+// Rows of a unit are (token, query head) pairs of one KV head, so grouped heads
+// share every K/V tile.  For D <= 128 a unit has 256 rows in two streams of 128
+// (S and O of both in TMEM: 2 x 128 + 2 x D columns), for D = 256 it has 128 rows
+// (S of two consecutive key tiles and O: 2 x 64 + 256 columns).  S = Q K^T is
+// taken from TMEM by one thread a row, P overwrites it there as one 16-bit term
+// (its rounding is the size of the output's own) and P V accumulates in f32.
+//
+//   warp 0      schedule and TMA producer: K and V tiles through two rings
+//   warps 1, 2  MMA issuers: D <= 128 one per stream (Q K^T and P V of it), so one
+//               stream's products run while the other's softmax does; D = 256 warp 1
+//               issues Q K^T, warp 2 P V
+//   warp 3      V guard: before a V tile that not every row sees in full is used,
+//               rows past the last key are zeroed and elements that are not finite
+//               are taken out (0 x NaN would reach rows that do not see them); the
+//               rows that do see such an element get NaN in its column at the end
+//   warps 4-7   softmax, Q loads and epilogue of stream 0 (D = 256: of the unit)
+//   warps 8-11  the same of stream 1 (D <= 128)
+// The running max moves only when a row's max exceeds it by more than 2^8
+// (P <= 256 fits f16, the sum stays in f32), so O in TMEM is rarely rescaled.
+// Every wait is bounded; a wait that gives up sets the status word, and the CTA
+// drains its copies and MMAs, frees TMEM and exits.
+#pragma once
+
+#include "seq_sched.cuh"
+#include "sm100_ptx.cuh"
+
+namespace ta {
+namespace seqtc {
+
+using namespace sm100;
+
+template <int D>
+struct Cfg {
+    static constexpr int TKS = D == 256 ? 6 : 7;
+    static constexpr int TK = 1 << TKS;                 // keys per tile
+    static constexpr int NSTR = D == 256 ? 1 : 2;       // row streams
+    static constexpr int ROWS = 128 * NSTR;
+    static constexpr int THREADS = 128 + 128 * NSTR;
+    static constexpr int SLABS = D / 64;                // 64-column slabs of a tile
+    static constexpr int SLAB = TK * 128;               // bytes of a K / V slab
+    static constexpr int QSLAB = 128 * 128;             // bytes of a Q slab
+    static constexpr int STAGE = SLABS * SLAB;
+    static constexpr int NK = D == 64 ? 4 : 2, NV = D == 64 ? 4 : 3;
+    static constexpr int OFF_Q = 0;
+    static constexpr int OFF_K = OFF_Q + NSTR * SLABS * QSLAB;
+    static constexpr int OFF_V = OFF_K + NK * STAGE;
+    static constexpr int OFF_MISC = OFF_V + NV * STAGE;
+};
+
+constexpr int kPieces = 4;
+// The guard is at most kPieces + 2 pieces ahead of an epilogue (a piece is published
+// once every reader has fetched the one kPieces before it, and an epilogue runs
+// right after the next fetch), so a ring of 8 marks is never overrun.
+constexpr int kPoison = 8;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kSlack = 8.0f;
+
+struct Misc {
+    uint64_t k_full[4], k_empty[4], v_full[4], v_ready[4], v_empty[4];
+    uint64_t q_full[2], s_full[2], p_full[2], o_done[2], o_free[2];
+    uint64_t piece_full[kPieces], piece_empty[kPieces];
+    uint64_t drain[2];
+    SeqPiece piece[kPieces];
+    SeqScratch sched;
+    uint32_t tmem_base;
+    volatile int abort_flag;
+    int poisoned[kPoison];            // piece n % kPoison: some row has a poisoned column
+    int32_t parents[kMaxTreeBitsNodes];
+};
+static_assert(sizeof(Misc) <= 2900, "barrier area");
+template <int D>
+constexpr int kSmem = Cfg<D>::OFF_MISC + 2900;
+static_assert(kSmem<64> <= 232448 && kSmem<128> <= 232448 && kSmem<256> <= 232448, "shared memory budget");
+
+struct Args {
+    SeqArgs a;
+    SeqWs ws;
+    uint32_t *poison;     // [G][kPoison][ROWS][D / 32]
+    int tpt, G;
+};
+struct Maps {
+    CUtensorMap k, v;     // paged: {D, page, Hk, pages}; packed: {D, T, Hk}; 64-column boxes, 128-byte swizzle
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Two f32 at a time.
+__device__ __forceinline__ uint64_t pack64(float x, float y) {
+    return static_cast<uint64_t>(__float_as_uint(x)) | (static_cast<uint64_t>(__float_as_uint(y)) << 32);
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+__device__ __forceinline__ float lo64(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x)); }
+__device__ __forceinline__ float hi64(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x >> 32)); }
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+    if constexpr (BF16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    } else {
+        const __half2 v = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+}
+// Does a pair of 16-bit values hold an infinity or a NaN (all exponent bits set).
+template <bool BF16>
+__device__ __forceinline__ bool odd16(uint32_t w) {
+    constexpr uint32_t e = BF16 ? 0x7f80u : 0x7c00u;
+    return (w & e) == e || ((w >> 16) & e) == e;
+}
+
+__device__ __forceinline__ bool wait_or_abort(Misc *m, uint64_t *bar, uint32_t parity, int *status) {
+    if (mbar_try_wait(bar, parity)) return true;
+    for (uint32_t i = 0; i < (1u << 21); ++i) {         // about 2 s
+        if (m->abort_flag) return false;
+        if (mbar_try_wait_sleep(bar, parity, 1000)) return true;
+    }
+    m->abort_flag = 1;
+    atomicOr(status, kSeqTimeout);
+    return false;
+}
+
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z, int w) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+
+template <int D, bool PAGED, bool BF16>
+__global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args ar, const __grid_constant__ Maps maps) {
+    using C = Cfg<D>;
+    constexpr int TK = C::TK, TKS = C::TKS, NSTR = C::NSTR, NK = C::NK, NV = C::NV, ROWS = C::ROWS;
+    extern __shared__ __align__(1024) unsigned char sm[];
+    const SeqArgs &a = ar.a;
+    if ((smem_u32(sm) & 1023u) != 0) {                  // swizzled tiles need it; the same in every CTA
+        if (threadIdx.x == 0) atomicOr(a.status, kSeqTimeout);
+        return;
+    }
+    Misc *mi = reinterpret_cast<Misc *>(sm + C::OFF_MISC);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
+    // arrivals on a piece's empty slot: issuers, guard, softmax warps
+    constexpr int kReaders = 3 + 4 * NSTR;
+    if (tid == 0) {
+        for (int i = 0; i < NK; ++i) { mbar_init(&mi->k_full[i], 1); mbar_init(&mi->k_empty[i], NSTR); }
+        for (int i = 0; i < NV; ++i) {
+            mbar_init(&mi->v_full[i], 1);
+            mbar_init(&mi->v_ready[i], 1);
+            mbar_init(&mi->v_empty[i], NSTR);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&mi->q_full[i], 4);
+            mbar_init(&mi->s_full[i], 1);
+            mbar_init(&mi->p_full[i], 4);
+            mbar_init(&mi->o_done[i], 1);
+            mbar_init(&mi->o_free[i], 4);
+            mbar_init(&mi->drain[i], 1);
+        }
+        for (int i = 0; i < kPieces; ++i) { mbar_init(&mi->piece_full[i], 1); mbar_init(&mi->piece_empty[i], kReaders); }
+        mi->abort_flag = 0;
+        for (int i = 0; i < kPoison; ++i) mi->poisoned[i] = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&mi->tmem_base, 512);
+        tmem_relinquish();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&maps.k);
+        tma_prefetch_desc(&maps.v);
+    }
+    pdl_wait();
+    const SeqRun run = seq_schedule<C::THREADS, TKS>(a, ar.tpt, cta, ar.G, &mi->sched);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_launch_dependents();
+    const uint32_t tmem = mi->tmem_base;
+    const uint32_t tm_o0 = tmem + 256;
+
+    // The next piece, in order; a reader's warp-wide copy.
+    int piece_n = 0;
+    auto fetch = [&](SeqPiece *p) -> bool {
+        const int i = piece_n % kPieces;
+        bool ok = wait_or_abort(mi, &mi->piece_full[i], static_cast<uint32_t>(piece_n / kPieces) & 1u, a.status);
+        ok = __all_sync(0xffffffffu, ok);
+        ++piece_n;
+        if (!ok) { p->valid = 0; return false; }
+        *p = mi->piece[i];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&mi->piece_empty[i]);
+        return p->valid != 0;
+    };
+    // Does some row of the piece not see all of key tile t.
+    auto is_masked = [&](const SeqPiece &p, int t) { return (t << TKS) < p.full_lo || ((t + 1) << TKS) > p.full_hi; };
+
+    if (warp == 0) {
+        // ------------------------------------------------- schedule, TMA producer
+        SeqWalk<TKS> walk;
+        walk.init(a, ar.tpt, run, &mi->sched, cta);
+        int n = 0, kn = 0, vn = 0;                      // pieces, K tiles, V tiles so far
+        bool ok = true;
+        if (lane == 0) ar.ws.rec[cta] = {0, 0, 0, 0};
+        for (;; ++n) {
+            SeqPiece p;
+            p.valid = 0;
+            const bool more = walk.next(a, ar.tpt, run, &p);
+            const int i = n % kPieces;
+            if (n >= kPieces)
+                ok = __all_sync(0xffffffffu, wait_or_abort(mi, &mi->piece_empty[i],
+                                                           static_cast<uint32_t>(n / kPieces - 1) & 1u, a.status));
+            if (!ok) break;
+            if (lane == 0) {
+                mi->piece[i] = p;
+                mbar_arrive(&mi->piece_full[i]);
+                // the unit's first piece leaves the record of how many there are
+                if (more && p.parts > 0) ar.ws.rec[cta] = {p.parts, p.q0 + p.i0, p.kh, p.rows};
+            }
+            __syncwarp();
+            if (!more) break;
+            // a tile = SLABS boxes per page (or per tile); lanes 0 .. boxes-1 issue one each
+            const int bk = PAGED ? min(TK, 1 << a.page_shift) : TK;       // keys per box
+            const int per_slab = TK / bk;
+            const int box = lane % per_slab, slab = lane / per_slab;       // per_slab: a power of two, at most 8
+            auto load = [&](const CUtensorMap *map, unsigned char *dst, uint64_t *bar, int page, int key) {
+                for (int s = slab; s < C::SLABS; s += 32 / per_slab) {
+                    unsigned char *d = dst + s * C::SLAB + box * bk * 128;
+                    if constexpr (PAGED) {
+                        tma_load_4d(d, map, bar, s * 64, key & ((1 << a.page_shift) - 1), p.kh, page);
+                    } else if (lane < C::SLABS) {
+                        tma_load_3d(d, map, bar, s * 64, p.q0 + key, p.kh);
+                    }
+                }
+            };
+            // page of this lane's box of tile t (n_pages: out of range, read as zeros)
+            auto page_of = [&](int t) -> int {
+                if constexpr (!PAGED) return 0;
+                const int key = (t << TKS) + box * bk;
+                if (key >= p.kv) return a.n_pages;
+                const int g = __ldg(a.table + static_cast<long long>(p.b) * a.max_pages + (key >> a.page_shift));
+                if (g >= 0 && g < a.n_pages) return g;
+                if (slab == 0) atomicOr(a.status, kSeqBadPage);
+                return a.n_pages;
+            };
+            int page_k = page_of(p.t0), page_v = page_k;
+            for (int t = 0; t <= p.nt && ok; ++t) {
+                // K of tile t, then V of tile t - 1: the order the issuers use them in
+                if (t < p.nt) {
+                    const int st = kn % NK;
+                    const int next = t + 1 < p.nt ? page_of(p.t0 + t + 1) : 0;
+                    ok = wait_or_abort(mi, &mi->k_empty[st], (static_cast<uint32_t>(kn / NK) & 1u) ^ 1u, a.status);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_expect_tx(&mi->k_full[st], C::STAGE);
+                    __syncwarp();
+                    load(&maps.k, sm + C::OFF_K + st * C::STAGE, &mi->k_full[st], page_k, ((p.t0 + t) << TKS) + box * bk);
+                    ++kn;
+                    if (t == 0) { page_k = next; continue; }
+                    const int cur = page_v;
+                    page_v = page_k;
+                    page_k = next;
+                    const int sv = vn % NV;
+                    ok = wait_or_abort(mi, &mi->v_empty[sv], (static_cast<uint32_t>(vn / NV) & 1u) ^ 1u, a.status);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_expect_tx(&mi->v_full[sv], C::STAGE);
+                    __syncwarp();
+                    load(&maps.v, sm + C::OFF_V + sv * C::STAGE, &mi->v_full[sv], cur, ((p.t0 + t - 1) << TKS) + box * bk);
+                    ++vn;
+                } else {
+                    const int sv = vn % NV;
+                    ok = wait_or_abort(mi, &mi->v_empty[sv], (static_cast<uint32_t>(vn / NV) & 1u) ^ 1u, a.status);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_expect_tx(&mi->v_full[sv], C::STAGE);
+                    __syncwarp();
+                    load(&maps.v, sm + C::OFF_V + sv * C::STAGE, &mi->v_full[sv], page_v, ((p.t0 + t - 1) << TKS) + box * bk);
+                    ++vn;
+                }
+            }
+            if (!ok) break;
+        }
+        // Drain: every copy issued has landed before the CTA's memory goes.
+        if (lane == 0) {
+            for (int i = max(0, kn - NK); i < kn; ++i)
+                if (!mbar_wait_sleep(&mi->k_full[i % NK], static_cast<uint32_t>(i / NK) & 1u, 1u << 21, 1000))
+                    atomicOr(a.status, kSeqTimeout);
+            for (int i = max(0, vn - NV); i < vn; ++i)
+                if (!mbar_wait_sleep(&mi->v_full[i % NV], static_cast<uint32_t>(i / NV) & 1u, 1u << 21, 1000))
+                    atomicOr(a.status, kSeqTimeout);
+        }
+    } else if (warp <= 2) {
+        // ------------------------------------------------------------ MMA issuers
+        const int w = warp - 1;
+        const uint32_t q_addr = smem_u32(sm + C::OFF_Q), k_addr = smem_u32(sm + C::OFF_K), v_addr = smem_u32(sm + C::OFF_V);
+        constexpr uint32_t id_qk = idesc_f16(128, TK, BF16 ? 1 : 0, 0, 0);
+        constexpr uint32_t id_pv = idesc_f16(128, D, BF16 ? 1 : 0, 0, 1);
+        auto qk = [&](uint32_t q, uint32_t k, uint32_t s) {
+#pragma unroll
+            for (int sl = 0; sl < C::SLABS; ++sl)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_f16_ss(s, sw128_desc(q + sl * C::QSLAB + kk * 32, 16, 1024),
+                               sw128_desc(k + sl * C::SLAB + kk * 32, 16, 1024), id_qk, (sl | kk) != 0);
+        };
+        auto pv = [&](uint32_t p, uint32_t v, uint32_t o, bool first) {
+#pragma unroll
+            for (int kk = 0; kk < TK / 16; ++kk)
+                mma_f16_ts(o, p + 8 * kk, sw128_desc(v + kk * 2048, C::SLAB, 1024), id_pv, !first || kk != 0);
+        };
+        int kn = 0, vn = 0, tn = 0, qn = 0;             // K / V tiles of the CTA; tiles and Q tiles of this stream
+        bool ok = true;
+        SeqPiece p;
+        while (ok && fetch(&p)) {
+            const bool act = NSTR == 1 || p.rows > 128 * w;
+            if (lane == 0) {
+                auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_or_abort(mi, bar, parity & 1u, a.status); };
+                if (!act) {
+                    // this piece is the other stream's alone: release the tiles with it
+                    for (int t = 0; t < p.nt && ok; ++t, ++kn, ++vn) {
+                        ok = wait(&mi->k_full[kn % NK], kn / NK);
+                        if (ok) mbar_arrive(&mi->k_empty[kn % NK]);
+                        if (ok) ok = wait(&mi->v_ready[vn % NV], vn / NV);
+                        if (ok) mbar_arrive(&mi->v_empty[vn % NV]);
+                    }
+                } else if constexpr (NSTR == 2) {
+                    const uint32_t q = q_addr + w * C::SLABS * C::QSLAB, s = tmem + 128 * w, o = tm_o0 + 128 * w;
+                    auto do_qk = [&]() {
+                        // S overwrites P: the P V before it has read it
+                        if (ok && tn > 0) ok = wait(&mi->o_done[w], tn - 1);
+                        if (ok) ok = wait(&mi->k_full[kn % NK], kn / NK);
+                        if (!ok) return;
+                        tc_fence_after();
+                        qk(q, k_addr + (kn % NK) * C::STAGE, s);
+                        mma_commit(&mi->s_full[w]);
+                        mma_commit(&mi->k_empty[kn % NK]);
+                        ++kn;
+                    };
+                    ok = wait(&mi->q_full[w], qn);
+                    if (ok) do_qk();
+                    for (int t = 0; t < p.nt && ok; ++t) {
+                        ok = wait(&mi->p_full[w], tn);
+                        // O is rewritten: the piece before has been read out
+                        if (ok && t == 0 && qn > 0) ok = wait(&mi->o_free[w], qn - 1);
+                        if (ok) ok = wait(&mi->v_ready[vn % NV], vn / NV);
+                        if (!ok) break;
+                        tc_fence_after();
+                        pv(s, v_addr + (vn % NV) * C::STAGE, o, t == 0);
+                        mma_commit(&mi->o_done[w]);
+                        mma_commit(&mi->v_empty[vn % NV]);
+                        ++vn;
+                        ++tn;
+                        if (t + 1 < p.nt) do_qk();
+                    }
+                    ++qn;
+                } else if (w == 0) {
+                    ok = wait(&mi->q_full[0], qn++);
+                    for (int t = 0; t < p.nt && ok; ++t, ++tn) {
+                        const int sb = tn & 1;
+                        if (tn >= 2) ok = wait(&mi->o_done[sb], (tn - 2) >> 1);
+                        if (ok) ok = wait(&mi->k_full[kn % NK], kn / NK);
+                        if (!ok) break;
+                        tc_fence_after();
+                        qk(q_addr, k_addr + (kn % NK) * C::STAGE, tmem + 128 * sb);
+                        mma_commit(&mi->s_full[sb]);
+                        mma_commit(&mi->k_empty[kn % NK]);
+                        ++kn;
+                    }
+                } else {
+                    for (int t = 0; t < p.nt && ok; ++t, ++tn) {
+                        const int sb = tn & 1;
+                        ok = wait(&mi->p_full[sb], tn >> 1);
+                        if (ok && t == 0 && qn > 0) ok = wait(&mi->o_free[0], qn - 1);
+                        if (ok) ok = wait(&mi->v_ready[vn % NV], vn / NV);
+                        if (!ok) break;
+                        tc_fence_after();
+                        pv(tmem + 128 * sb, v_addr + (vn % NV) * C::STAGE, tm_o0, t == 0);
+                        mma_commit(&mi->o_done[sb]);
+                        mma_commit(&mi->v_empty[vn % NV]);
+                        ++vn;
+                    }
+                    ++qn;
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+        }
+        if (lane == 0) {                                // every MMA issued has completed
+            mma_commit(&mi->drain[w]);
+            if (!mbar_wait_sleep(&mi->drain[w], 0, 1u << 21, 1000)) atomicOr(a.status, kSeqTimeout);
+        }
+        __syncwarp();
+    } else if (warp == 3) {
+        // ---------------------------------------------------------------- V guard
+        int vn = 0, n = 0;
+        bool ok = true;
+        SeqPiece p;
+        for (; ok && fetch(&p); ++n) {
+            bool marked = false;
+            uint32_t *poison = ar.poison + (static_cast<size_t>(cta) * kPoison + n % kPoison) * ROWS * (D / 32);
+            if (lane == 0) mi->poisoned[n % kPoison] = 0;
+            for (int t = 0; t < p.nt && ok; ++t, ++vn) {
+                const int st = vn % NV, k0 = (p.t0 + t) << TKS;
+                ok = __all_sync(0xffffffffu, wait_or_abort(mi, &mi->v_full[st], static_cast<uint32_t>(vn / NV) & 1u, a.status));
+                if (!ok) break;
+                if (is_masked(p, p.t0 + t)) {
+                    unsigned char *v = sm + C::OFF_V + st * C::STAGE;
+                    const int live = min(max(p.kv - k0, 0), TK);
+                    // slab rows are 128 bytes; lane l takes chunk l % 8 of rows l / 8, l / 8 + 4, ...
+                    bool found = false;
+                    for (int s = 0; s < C::SLABS; ++s)
+#pragma unroll 4
+                        for (int r = lane >> 3; r < TK; r += 4) {
+                            uint4 *x = reinterpret_cast<uint4 *>(v + s * C::SLAB + r * 128 + (lane & 7) * 16);
+                            if (r >= live) {
+                                *x = make_uint4(0, 0, 0, 0);
+                            } else {
+                                const uint4 y = *x;
+                                found |= odd16<BF16>(y.x) | odd16<BF16>(y.y) | odd16<BF16>(y.z) | odd16<BF16>(y.w);
+                            }
+                        }
+                    if (__any_sync(0xffffffffu, found)) {
+                        // rare: mark the rows that see an element that is not finite, then take it out
+                        if (!marked) {
+                            for (int i = lane; i < ROWS * (D / 32); i += 32) poison[i] = 0u;
+                            marked = true;
+                            __syncwarp();
+                        }
+                        for (int r = 0; r < live; ++r)
+                            for (int c = lane; c < D / 2; c += 32) {
+                                // column pair c of key row r, at its swizzled place
+                                const int s = c >> 5, ch = (c & 31) >> 2;
+                                uint32_t *x = reinterpret_cast<uint32_t *>(v + s * C::SLAB + r * 128 + ((ch ^ (r & 7)) << 4)) + (c & 3);
+                                constexpr uint32_t e = BF16 ? 0x7f80u : 0x7c00u;
+                                const bool l = (*x & e) == e, h = ((*x >> 16) & e) == e;
+                                if (!l && !h) continue;
+                                const uint32_t bits = (l ? 1u : 0u) << ((2 * c) & 31) | (h ? 1u : 0u) << ((2 * c + 1) & 31);
+                                for (int row = 0; row < p.rows; ++row) {
+                                    const int i = p.i0 + row / a.g;
+                                    uint32_t anc[kMaxTreeBitsNodes / 32] = {}, m[1];
+                                    if (a.parents) seq_ancestors(a.parents + p.q0, i, anc);
+                                    seq_visible<1>(a, p.prefix, p.kv, i, anc, k0 + r, m);
+                                    if (m[0] & 1u) atomicOr(poison + row * (D / 32) + (2 * c) / 32, bits);
+                                }
+                                if (l) *x &= 0xffff0000u;
+                                if (h) *x &= 0x0000ffffu;
+                            }
+                        __threadfence();
+                        __syncwarp();
+                        if (lane == 0) mi->poisoned[n % kPoison] = 1;
+                    }
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&mi->v_ready[st]);
+            }
+        }
+    } else {
+        // ------------------------------------------- softmax, Q loads, epilogue
+        const int s = (warp - 4) >> 2;                  // stream
+        const int quarter = warp & 3;
+        const int r = quarter * 32 + lane;              // row within the stream
+        const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+        const uint32_t tm_s = tmem + lane_off + (NSTR == 2 ? 128 * s : 0), tm_o = tm_o0 + lane_off + 128 * s;
+        // a negative scale turns into negated queries (exact), so that the largest
+        // product is the largest logit
+        const float scale2 = fmaxf(fabsf(a.scale) * kLog2e, FLT_MIN);   // above 0: a masked -inf stays -inf
+        const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
+        int tn = 0, vn = 0;                             // tiles of this stream, tiles of the CTA
+        bool ok = true;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            ok = __all_sync(0xffffffffu, ok && wait_or_abort(mi, bar, parity & 1u, a.status));
+        };
+        auto active = [&](const SeqPiece &p) { return NSTR == 1 || p.rows > 128 * s; };
+        // this warp's 32 rows of Q into shared memory (8 lanes a 128-byte row piece)
+        auto load_q = [&](const SeqPiece &p) {
+            unsigned char *dst = sm + C::OFF_Q + s * C::SLABS * C::QSLAB;
+#pragma unroll 2
+            for (int it = 0; it < 8; ++it) {
+                const int row = quarter * 32 + it * 4 + (lane >> 3), ch = lane & 7;
+                const int ur = 128 * s + row;
+                const bool live = ur < p.rows;
+                const int tok = ur / a.g, h = p.kh * a.g + ur - tok * a.g;
+                const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) +
+                                                                   static_cast<long long>(p.q0 + p.i0 + tok) * a.q_st + h * a.q_sh) + ch;
+#pragma unroll
+                for (int sl = 0; sl < C::SLABS; ++sl) {
+                    uint4 x = live ? __ldg(src + sl * 8) : make_uint4(0, 0, 0, 0);
+                    x.x ^= flip; x.y ^= flip; x.z ^= flip; x.w ^= flip;
+                    *reinterpret_cast<uint4 *>(dst + sl * C::QSLAB + row * 128 + ((ch ^ (row & 7)) << 4)) = x;
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&mi->q_full[s]);
+        };
+
+        SeqPiece p;
+        int n = 0;                                      // pieces of the CTA
+        bool have = fetch(&p);
+        if (have && active(p)) load_q(p);
+        for (; have && ok; ++n) {
+            const bool act = active(p);
+            float m_run = -INFINITY, l_run = 0.0f;
+            const int urow = 128 * s + r;
+            const bool live = urow < p.rows;
+            if (act) {
+                const int i = p.i0 + urow / a.g;
+                uint32_t anc[kMaxTreeBitsNodes / 32];
+                if (a.parents && live) seq_ancestors(a.parents + p.q0, i, anc);
+                for (int t = 0; t < p.nt && ok; ++t, ++tn) {
+                    const int sb = NSTR == 2 ? s : tn & 1;
+                    const uint32_t ph = NSTR == 2 ? tn : tn >> 1;
+                    const uint32_t col = tm_s + (NSTR == 2 ? 0 : 128 * sb);
+                    wait(&mi->s_full[sb], ph);
+                    if (!ok) break;
+                    tc_fence_after();
+                    uint32_t v[TK];
+#pragma unroll
+                    for (int c = 0; c < TK / 32; ++c)
+                        tmem_ld32(col + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&v[32 * c]));
+                    tmem_wait_ld();
+                    const bool masked = is_masked(p, p.t0 + t);
+                    if (masked) {
+                        uint32_t m[TK / 32];
+                        seq_visible<TK / 32>(a, p.prefix, live ? p.kv : 0, i, anc, (p.t0 + t) << TKS, m);
+#pragma unroll
+                        for (int e = 0; e < TK; ++e)
+                            if (!((m[e >> 5] >> (e & 31)) & 1u)) v[e] = 0xff800000u;
+                    }
+                    float mx[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mx[e] = __uint_as_float(v[e]);
+#pragma unroll
+                    for (int e = 4; e < TK; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(v[e]));
+                    const float rmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale2;
+                    float alpha = 1.0f;
+                    if (rmax > m_run + kSlack) {
+                        alpha = ex2(m_run - rmax);      // 0 from -inf
+                        l_run *= alpha;
+                        m_run = rmax;
+                    }
+                    if (t > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
+                        // O must be at rest: the P V of the tile before is done
+                        const int pb = NSTR == 2 ? s : (tn - 1) & 1;
+                        wait(&mi->o_done[pb], NSTR == 2 ? tn - 1 : (tn - 1) >> 1);
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(tm_o + c, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                            tmem_st32(tm_o + c, o);
+                        }
+                    }
+                    const float m_use = m_run == -INFINITY ? 0.0f : m_run;
+                    const uint64_t sc = pack64(scale2, scale2), mm = pack64(-m_use, -m_use);
+                    uint64_t sum[2] = {0, 0};
+#pragma unroll
+                    for (int c = 0; c < TK / 32; c += 2) {
+                        uint32_t pk[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const uint64_t x = fma2(pack64(__uint_as_float(v[32 * c + 2 * e]), __uint_as_float(v[32 * c + 2 * e + 1])), sc, mm);
+                            const float p0 = ex2(lo64(x)), p1 = ex2(hi64(x));
+                            sum[e & 1] = add2(sum[e & 1], pack64(p0, p1));
+                            pk[e] = pack16<BF16>(p0, p1);
+                        }
+                        tmem_st32(col + 16 * c, pk);
+                    }
+                    const uint64_t all = add2(sum[0], sum[1]);
+                    l_run += lo64(all) + hi64(all);
+                    // the guard's marks of this V tile are in before its P V can be issued
+                    if (masked) wait(&mi->v_ready[(vn + t) % NV], (vn + t) / NV);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (ok && lane == 0) mbar_arrive(&mi->p_full[sb]);
+                }
+            }
+            vn += p.nt;
+            SeqPiece nx;
+            nx.valid = 0;
+            if (ok) have = fetch(&nx);
+            if (ok && have && active(nx)) load_q(nx);
+            if (act && ok) {
+                const int pb = NSTR == 2 ? s : (tn - 1) & 1;
+                wait(&mi->o_done[pb], NSTR == 2 ? tn - 1 : (tn - 1) >> 1);
+                if (!ok) break;
+                tc_fence_after();
+                const bool odd = *static_cast<volatile int *>(&mi->poisoned[n % kPoison]) != 0;
+                const uint32_t *poison = ar.poison + ((static_cast<size_t>(cta) * kPoison + n % kPoison) * ROWS + urow) * (D / 32);
+                const float inv = l_run > 0.0f ? 1.0f / l_run : (l_run == 0.0f ? 0.0f : l_run);
+                const int tok = urow / a.g, h = p.kh * a.g + urow - tok * a.g;
+                uint16_t *out = static_cast<uint16_t *>(a.out) + static_cast<long long>(p.q0 + p.i0 + tok) * a.o_st + h * a.o_sh;
+                const size_t slot = static_cast<size_t>(p.slot < 0 ? 0 : p.slot);
+                float4 *part = reinterpret_cast<float4 *>(ar.ws.o) + slot * (D / 4) * ROWS + urow;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(tm_o + c, o);
+                    tmem_wait_ld();
+                    if (odd && live) {                 // poisoned columns of this row
+                        const uint32_t bits = __ldcg(poison + c / 32);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if ((bits >> e) & 1u) o[e] = 0x7fffffffu;
+                    }
+                    if (live && p.slot < 0) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            uint4 x;
+                            x.x = pack16<BF16>(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+                            x.y = pack16<BF16>(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+                            x.z = pack16<BF16>(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
+                            x.w = pack16<BF16>(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
+                            *reinterpret_cast<uint4 *>(out + c + e) = x;
+                        }
+                    } else if (live) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            part[static_cast<size_t>((c + e) / 4) * ROWS] =
+                                make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
+                                            __uint_as_float(o[e + 3]));
+                    }
+                    __syncwarp();
+                }
+                if (live && p.slot >= 0) ar.ws.ml[slot * ROWS + urow] = make_float2(m_run, l_run);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&mi->o_free[s]);
+            }
+            p = nx;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Merge of the pieces of the units that start in CTA blockIdx.x and are cut:
+// out = sum_p O_p 2^(m_p - m*) / sum_p l_p 2^(m_p - m*).  16 columns a block, one
+// row a thread; partials are laid out so that a warp reads whole lines.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(Cfg<D>::ROWS) seq_merge_kernel(const SeqArgs a, const SeqWs ws) {
+    constexpr int ROWS = Cfg<D>::ROWS;
+    pdl_wait();
+    const int c = blockIdx.x, r = threadIdx.x, d0 = blockIdx.y * 16;
+    const SeqRec rec = ws.rec[c];
+    if (r >= rec.rows || rec.parts == 0) return;
+    // pieces: slot 2 c + 1, then the first slots of the CTAs after it
+    auto slot = [&](int p) { return static_cast<size_t>(p == 0 ? 2 * c + 1 : 2 * (c + p)); };
+    float m = -INFINITY, l = 0.0f, o[16] = {};
+    for (int p = 0; p < rec.parts; ++p) {
+        const float2 x = ws.ml[slot(p) * ROWS + r];
+        if (x.x == -INFINITY) continue;
+        const float mn = fmaxf(m, x.x), f = ex2(m - mn), g = ex2(x.x - mn);
+        l = l * f + x.y * g;
+        const float4 *src = reinterpret_cast<const float4 *>(ws.o) + (slot(p) * (D / 4) + d0 / 4) * ROWS + r;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float4 y = src[e * ROWS];
+            o[4 * e] = o[4 * e] * f + y.x * g;
+            o[4 * e + 1] = o[4 * e + 1] * f + y.y * g;
+            o[4 * e + 2] = o[4 * e + 2] * f + y.z * g;
+            o[4 * e + 3] = o[4 * e + 3] * f + y.w * g;
+        }
+        m = mn;
+    }
+    const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+    const int tok = r / a.g, h = rec.kh * a.g + r - tok * a.g;
+    uint16_t *out = static_cast<uint16_t *>(a.out) + static_cast<long long>(rec.token + tok) * a.o_st + h * a.o_sh + d0;
+#pragma unroll
+    for (int e = 0; e < 16; e += 8) {
+        uint4 x;
+        x.x = pack16<BF16>(o[e] * inv, o[e + 1] * inv);
+        x.y = pack16<BF16>(o[e + 2] * inv, o[e + 3] * inv);
+        x.z = pack16<BF16>(o[e + 4] * inv, o[e + 5] * inv);
+        x.w = pack16<BF16>(o[e + 6] * inv, o[e + 7] * inv);
+        *reinterpret_cast<uint4 *>(out + e) = x;
+    }
+}
+
+template <int D, bool PAGED, bool BF16>
+cudaError_t launch(const Args &ar, const Maps &maps, cudaStream_t s) {
+    auto kern = seq_tc_kernel<D, PAGED, BF16>;
+    static unsigned long long done = 0;
+    cudaError_t e = set_smem_limit_once(kern, kSmem<D>, &done);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(kern, dim3(ar.G), dim3(Cfg<D>::THREADS), kSmem<D>, s, ar, maps);
+    count_launch();
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(seq_merge_kernel<D, BF16>, dim3(ar.G, D / 16), dim3(Cfg<D>::ROWS), 0, s, ar.a, ar.ws);
+    count_launch();
+    return e;
+}
+
+template <int D>
+cudaError_t launch_dim(const SeqArgs &a, const SeqTcPlan &pl, cudaStream_t s) {
+    Args ar;
+    ar.a = a;
+    ar.G = pl.G;
+    ar.tpt = Cfg<D>::ROWS / a.g;
+    char *ws = static_cast<char *>(pl.ws);
+    ar.ws.rec = reinterpret_cast<SeqRec *>(ws + 256);
+    const size_t slots = 2 * static_cast<size_t>(pl.G), rows = Cfg<D>::ROWS;
+    size_t off = 256 + (pl.G * sizeof(SeqRec) + 255) / 256 * 256;
+    ar.ws.ml = reinterpret_cast<float2 *>(ws + off);
+    off += slots * rows * sizeof(float2);
+    ar.ws.o = reinterpret_cast<float *>(ws + off);
+    off += slots * rows * D * sizeof(float);
+    ar.poison = reinterpret_cast<uint32_t *>(ws + off);
+    Maps maps;
+    maps.k = pl.k;
+    maps.v = pl.v;
+    if (a.kv_lens)
+        return a.bf16 ? launch<D, true, true>(ar, maps, s) : launch<D, true, false>(ar, maps, s);
+    return a.bf16 ? launch<D, false, true>(ar, maps, s) : launch<D, false, false>(ar, maps, s);
+}
+
+}  // namespace seqtc
+}  // namespace ta

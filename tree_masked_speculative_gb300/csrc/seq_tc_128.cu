@@ -1,0 +1,8 @@
+// Tensor-core attention of ragged rows, head dimension 128.
+#include "seq_tc.cuh"
+
+namespace ta {
+cudaError_t launch_seq_tc128(const SeqArgs &a, const SeqTcPlan &pl, cudaStream_t s) {
+    return seqtc::launch_dim<128>(a, pl, s);
+}
+}  // namespace ta
