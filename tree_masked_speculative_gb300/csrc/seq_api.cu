@@ -131,29 +131,43 @@ uint64_t seq_workspace(uint32_t d, uint32_t kernel) {
     return sms > 0 ? seq_tc_workspace(static_cast<int>(d), sms) : 0;
 }
 
+bool encode_16bit(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap *m, const SeqArgs &a, const void *ptr, int rank,
+                  const cuuint64_t *dims, const cuuint64_t *str, const cuuint32_t *box) {
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    return encode(m, a.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
+                  const_cast<void *>(ptr), dims, str, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Tensor map of Q: {D, H, T}, a unit's tokens x the g heads of a KV head at once.
+bool q_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap *m, const SeqArgs &a) {
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.D), static_cast<cuuint64_t>(a.H), static_cast<cuuint64_t>(a.T)};
+    const cuuint64_t str[2] = {static_cast<cuuint64_t>(a.q_sh) * 2, static_cast<cuuint64_t>(a.q_st) * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(a.g), static_cast<cuuint32_t>(seq_tc_rows(a.D) / a.g)};
+    return encode_16bit(encode, m, a, a.q, 3, dims, str, box);
+}
+
 // Tensor map of K or V: {D, page_size, Hk, n_pages} (paged) or {D, T, Hk}.
 bool kv_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap *m, const SeqArgs &a, const void *ptr, long long st,
             long long sh) {
     const cuuint64_t ps = cuuint64_t(1) << a.page_shift;
-    const cuuint32_t tk = static_cast<cuuint32_t>(seq_tc_tile_keys(a.D));
+    const cuuint32_t tk = kSeqTcTileKeys;
     cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.D), ps, static_cast<cuuint64_t>(a.Hk), static_cast<cuuint64_t>(a.n_pages)};
     const cuuint64_t str[3] = {static_cast<cuuint64_t>(st) * 2, static_cast<cuuint64_t>(sh) * 2, static_cast<cuuint64_t>(a.k_sp) * 2};
     cuuint32_t box[4] = {64, static_cast<cuuint32_t>(ps < tk ? ps : tk), 1, 1};
-    const cuuint32_t es[4] = {1, 1, 1, 1};
     int rank = 4;
     if (a.kv_lens == nullptr) {
         dims[1] = static_cast<cuuint64_t>(a.T);
         box[1] = tk;
         rank = 3;
     }
-    return encode(m, a.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
-                  const_cast<void *>(ptr), dims, str, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode_16bit(encode, m, a, ptr, rank, dims, str, box);
 }
 
 ta_status run_seq(const char *op, const SeqArgs &a, uint32_t kernel, void *ws, cudaStream_t s) {
     cudaError_t e;
-    if (kernel == TA_KERNEL_CUDA_CORES) {
+    // the tensor-core kernel takes the largest product for the largest logit: no negative scale
+    if (kernel == TA_KERNEL_CUDA_CORES || a.scale < 0.0f) {
         e = launch_seq_fma(a, s);
     } else {
         SeqTcPlan pl;
@@ -161,7 +175,7 @@ ta_status run_seq(const char *op, const SeqArgs &a, uint32_t kernel, void *ws, c
         pl.ws = ws;
         const auto encode = tensor_map_encoder();
         if (encode == nullptr) SEQ_FAIL(TA_ERR_CUDA, "%s: cuTensorMapEncodeTiled is not available", op);
-        if (!kv_map(encode, &pl.k, a, a.k, a.k_st, a.k_sh) || !kv_map(encode, &pl.v, a, a.v, a.v_st, a.v_sh))
+        if (!q_map(encode, &pl.q, a) || !kv_map(encode, &pl.k, a, a.k, a.k_st, a.k_sh) || !kv_map(encode, &pl.v, a, a.v, a.v_st, a.v_sh))
             SEQ_FAIL(TA_ERR_CUDA, "%s: TMA descriptor encoding failed", op);
         e = a.D == 64 ? launch_seq_tc64(a, pl, s) : a.D == 128 ? launch_seq_tc128(a, pl, s) : launch_seq_tc256(a, pl, s);
     }

@@ -71,10 +71,10 @@ cudaError_t launch_seq_fma(const SeqArgs &a, cudaStream_t s);
 struct SeqTcPlan {
     int G;
     void *ws;
-    CUtensorMap k, v;
+    CUtensorMap q, k, v;
 };
 // Keys per key tile and rows per row tile of the tensor-core kernel.
-constexpr int seq_tc_tile_keys(int d) { return d == 256 ? 64 : 128; }
+constexpr int kSeqTcTileKeys = 64;
 constexpr int seq_tc_rows(int d) { return d == 256 ? 128 : 256; }
 // Its workspace on a grid of G CTAs: status, records, (m, l) and O of 2 G partial
 // slots, and the marks of columns that are not finite (8 pieces a CTA).

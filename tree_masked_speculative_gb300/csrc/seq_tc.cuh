@@ -2,22 +2,24 @@
 // K/V (PAGED) or packed prompts, f16 / bf16, head dimension 64, 128 or 256.
 //
 // Rows of a unit are (token, query head) pairs of one KV head, so grouped heads
-// share every K/V tile.  For D <= 128 a unit has 256 rows in two streams of 128
-// (S and O of both in TMEM: 2 x 128 + 2 x D columns), for D = 256 it has 128 rows
-// (S of two consecutive key tiles and O: 2 x 64 + 256 columns).  S = Q K^T is
-// taken from TMEM by one thread a row, P overwrites it there as one 16-bit term
+// share every K/V tile.  For D <= 128 a unit has 256 rows in two streams of 128, for
+// D = 256 it has 128 rows in one.  Key tiles are 64 wide, and each stream has S in two
+// TMEM buffers, so Q K^T of the next tile runs while the softmax warps work on this
+// one: they never wait for a product (with 128-key tiles and one buffer the chain
+// Q K^T, softmax, P V of a stream took 3500 cycles, against 2048 of products of both).
+// S is taken from TMEM by one thread a row, P overwrites it there as one 16-bit term
 // (its rounding is the size of the output's own) and P V accumulates in f32.
 //
-//   warp 0      schedule and TMA producer: K and V tiles through two rings
-//   warps 1, 2  MMA issuers: D <= 128 one per stream (Q K^T and P V of it), so one
-//               stream's products run while the other's softmax does; D = 256 warp 1
-//               issues Q K^T, warp 2 P V
+//   warp 0      schedule and TMA producer: Q of a unit, K and V tiles through rings
+//   warps 1, 2  issue Q K^T and P V of stream 0; warps 4, 5 of stream 1.  Four issuing
+//               threads: the tensor core's queue is short, so it idles while a thread
+//               that has just issued its products waits on barriers and commits (two
+//               threads for both streams: 2240 cycles a tile, of them 1280 of products)
 //   warp 3      V guard: before a V tile that not every row sees in full is used,
 //               rows past the last key are zeroed and elements that are not finite
 //               are taken out (0 x NaN would reach rows that do not see them); the
 //               rows that do see such an element get NaN in its column at the end
-//   warps 4-7   softmax, Q loads and epilogue of stream 0 (D = 256: of the unit)
-//   warps 8-11  the same of stream 1 (D <= 128)
+//   4 warps per stream  softmax and epilogue, one row a thread
 // The running max moves only when a row's max exceeds it by more than 2^8
 // (P <= 256 fits f16, the sum stays in f32), so O in TMEM is rarely rescaled.
 // Every wait is bounded; a wait that gives up sets the status word, and the CTA
@@ -34,20 +36,22 @@ using namespace sm100;
 
 template <int D>
 struct Cfg {
-    static constexpr int TKS = D == 256 ? 6 : 7;
+    static constexpr int TKS = 6;
     static constexpr int TK = 1 << TKS;                 // keys per tile
     static constexpr int NSTR = D == 256 ? 1 : 2;       // row streams
     static constexpr int ROWS = 128 * NSTR;
-    static constexpr int THREADS = 128 + 128 * NSTR;
+    static constexpr int SW = 4 * NSTR;                 // first softmax warp
+    static constexpr int THREADS = 256 * NSTR;
     static constexpr int SLABS = D / 64;                // 64-column slabs of a tile
     static constexpr int SLAB = TK * 128;               // bytes of a K / V slab
-    static constexpr int QSLAB = 128 * 128;             // bytes of a Q slab
+    static constexpr int QSLAB = ROWS * 128;            // bytes of a Q slab
     static constexpr int STAGE = SLABS * SLAB;
-    static constexpr int NK = D == 64 ? 4 : 2, NV = D == 64 ? 4 : 3;
+    static constexpr int NK = D == 256 ? 2 : 4, NV = D == 256 ? 2 : 4;
     static constexpr int OFF_Q = 0;
-    static constexpr int OFF_K = OFF_Q + NSTR * SLABS * QSLAB;
+    static constexpr int OFF_K = OFF_Q + SLABS * QSLAB;
     static constexpr int OFF_V = OFF_K + NK * STAGE;
-    static constexpr int OFF_MISC = OFF_V + NV * STAGE;
+    static constexpr int OFF_OUT = OFF_V + NV * STAGE;   // 2 KB a softmax warp: 32 rows x 32 columns of the output
+    static constexpr int OFF_MISC = OFF_OUT + NSTR * 8192;
 };
 
 constexpr int kPieces = 4;
@@ -60,19 +64,19 @@ constexpr float kSlack = 8.0f;
 
 struct Misc {
     uint64_t k_full[4], k_empty[4], v_full[4], v_ready[4], v_empty[4];
-    uint64_t q_full[2], s_full[2], p_full[2], o_done[2], o_free[2];
+    uint64_t q_full, q_empty, s_full[2][2], p_full[2][2], o_done[2][2], o_free[2];   // stream, S buffer
     uint64_t piece_full[kPieces], piece_empty[kPieces];
-    uint64_t drain[2];
+    uint64_t drain[4];
     SeqPiece piece[kPieces];
     SeqScratch sched;
     uint32_t tmem_base;
     volatile int abort_flag;
     int poisoned[kPoison];            // piece n % kPoison: some row has a poisoned column
-    int32_t parents[kMaxTreeBitsNodes];
 };
-static_assert(sizeof(Misc) <= 2900, "barrier area");
+constexpr int kMiscBytes = 3000;
+static_assert(sizeof(Misc) <= kMiscBytes, "barrier area");
 template <int D>
-constexpr int kSmem = Cfg<D>::OFF_MISC + 2900;
+constexpr int kSmem = Cfg<D>::OFF_MISC + kMiscBytes;
 static_assert(kSmem<64> <= 232448 && kSmem<128> <= 232448 && kSmem<256> <= 232448, "shared memory budget");
 
 struct Args {
@@ -80,8 +84,10 @@ struct Args {
     SeqWs ws;
     uint32_t *poison;     // [G][kPoison][ROWS][D / 32]
     int tpt, G;
+    uint32_t g_inv;       // ceil(2^16 / g): row / g = row * g_inv >> 16, exact for rows < 256 and g <= 128
 };
 struct Maps {
+    CUtensorMap q;        // {D, H, T}, box {64, g, tokens of a unit}: rows (token, head) as they stand in a unit
     CUtensorMap k, v;     // paged: {D, page, Hk, pages}; packed: {D, T, Hk}; 64-column boxes, 128-byte swizzle
 };
 
@@ -89,6 +95,11 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
 }
 // Two f32 at a time.
 __device__ __forceinline__ uint64_t pack64(float x, float y) {
@@ -122,22 +133,55 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
         return *reinterpret_cast<const uint32_t *>(&v);
     }
 }
-// Does a pair of 16-bit values hold an infinity or a NaN (all exponent bits set).
+// Bits 15 and 31: does the low / high 16-bit value hold an infinity or a NaN.  One
+// added to an exponent field carries into the (cleared) sign place only from all ones.
 template <bool BF16>
-__device__ __forceinline__ bool odd16(uint32_t w) {
-    constexpr uint32_t e = BF16 ? 0x7f80u : 0x7c00u;
-    return (w & e) == e || ((w >> 16) & e) == e;
+__device__ __forceinline__ uint32_t odd16(uint32_t w) {
+    return BF16 ? (w & 0x7f807f80u) + 0x00800080u : (w & 0x7c007c00u) + 0x04000400u;
 }
 
-__device__ __forceinline__ bool wait_or_abort(Misc *m, uint64_t *bar, uint32_t parity, int *status) {
-    if (mbar_try_wait(bar, parity)) return true;
-    for (uint32_t i = 0; i < (1u << 21); ++i) {         // about 2 s
-        if (m->abort_flag) return false;
-        if (mbar_try_wait_sleep(bar, parity, 1000)) return true;
-    }
+static __device__ __noinline__ bool give_up(Misc *m, int *status) {
     m->abort_flag = 1;
     atomicOr(status, kSeqTimeout);
     return false;
+}
+__device__ __forceinline__ bool wait_or_abort(Misc *m, uint64_t *bar, uint32_t parity, int *status) {
+    if (mbar_try_wait(bar, parity)) return true;
+#pragma unroll 1
+    for (uint32_t i = 0; i < (1u << 21); ++i) {         // about 2 s
+        if (mbar_try_wait_sleep(bar, parity, 1000)) return true;
+        if (m->abort_flag) return false;
+    }
+    return give_up(m, status);
+}
+
+// Registers of this warpgroup's threads from here on (the block's sum stays what
+// it was launched with).
+template <int N>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// MMAs with descriptors as (low word with the address, constant high word).
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                       uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 q, %6, 0;\n\t"
+        "mov.b64 a, {%1, %2};\n\t"
+        "mov.b64 b, {%3, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, q;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, q;\n\t}" ::"r"(d),
+        "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc)
+        : "memory");
 }
 
 __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z, int w) {
@@ -146,6 +190,41 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, u
         " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
         : "memory");
+}
+
+// One warp: mark the rows that see an element of this V tile that is not finite
+// (bit d of a row's marks), and take the element out.
+template <int D, bool BF16>
+__device__ __noinline__ void mark_odd(const SeqArgs &a, const SeqPiece &p, int k0, int live, unsigned char *v, uint32_t *poison,
+                                      bool clear) {
+    using C = Cfg<D>;
+    const int lane = threadIdx.x & 31;
+    if (clear)
+        for (int i = lane; i < C::ROWS * (D / 32); i += 32) poison[i] = 0u;
+    __syncwarp();
+#pragma unroll 1
+    for (int r = 0; r < live; ++r)
+#pragma unroll 1
+        for (int c = lane; c < D / 2; c += 32) {
+            // column pair c of key row r, at its swizzled place
+            const int s = c >> 5, ch = (c & 31) >> 2;
+            uint32_t *x = reinterpret_cast<uint32_t *>(v + s * C::SLAB + r * 128 + ((ch ^ (r & 7)) << 4)) + (c & 3);
+            const uint32_t odd = odd16<BF16>(*x) & 0x80008000u;
+            if (odd == 0u) continue;
+            const uint32_t bits = ((odd >> 15) & 1u) << ((2 * c) & 31) | (odd >> 31) << ((2 * c + 1) & 31);
+#pragma unroll 1
+            for (int row = 0; row < p.rows; ++row) {
+                const int i = p.i0 + row / a.g;
+                uint32_t anc[kMaxTreeBitsNodes / 32] = {}, m[1];
+                if (a.parents) seq_ancestors(a.parents + p.q0, i, anc);
+                seq_visible<1>(a, p.prefix, p.kv, i, anc, k0 + r, m);
+                if (m[0] & 1u) atomicOr(poison + row * (D / 32) + (2 * c) / 32, bits);
+            }
+            if (odd & 0x8000u) *x &= 0xffff0000u;
+            if (odd >> 31) *x &= 0x0000ffffu;
+        }
+    __threadfence();
+    __syncwarp();
 }
 
 template <int D, bool PAGED, bool BF16>
@@ -161,7 +240,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
     Misc *mi = reinterpret_cast<Misc *>(sm + C::OFF_MISC);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
     // arrivals on a piece's empty slot: issuers, guard, softmax warps
-    constexpr int kReaders = 3 + 4 * NSTR;
+    constexpr int kReaders = 2 * NSTR + 1 + 4 * NSTR;
     if (tid == 0) {
         for (int i = 0; i < NK; ++i) { mbar_init(&mi->k_full[i], 1); mbar_init(&mi->k_empty[i], NSTR); }
         for (int i = 0; i < NV; ++i) {
@@ -169,13 +248,17 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
             mbar_init(&mi->v_ready[i], 1);
             mbar_init(&mi->v_empty[i], NSTR);
         }
+        mbar_init(&mi->q_full, 1);
+        mbar_init(&mi->q_empty, NSTR);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&mi->q_full[i], 4);
-            mbar_init(&mi->s_full[i], 1);
-            mbar_init(&mi->p_full[i], 4);
-            mbar_init(&mi->o_done[i], 1);
+            for (int j = 0; j < 2; ++j) {
+                mbar_init(&mi->s_full[i][j], 1);
+                mbar_init(&mi->p_full[i][j], 4);
+                mbar_init(&mi->o_done[i][j], 1);
+            }
             mbar_init(&mi->o_free[i], 4);
-            mbar_init(&mi->drain[i], 1);
+            mbar_init(&mi->drain[2 * i], 1);
+            mbar_init(&mi->drain[2 * i + 1], 1);
         }
         for (int i = 0; i < kPieces; ++i) { mbar_init(&mi->piece_full[i], 1); mbar_init(&mi->piece_empty[i], kReaders); }
         mi->abort_flag = 0;
@@ -187,6 +270,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
         tmem_relinquish();
     }
     if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&maps.q);
         tma_prefetch_desc(&maps.k);
         tma_prefetch_desc(&maps.v);
     }
@@ -215,13 +299,17 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
     // Does some row of the piece not see all of key tile t.
     auto is_masked = [&](const SeqPiece &p, int t) { return (t << TKS) < p.full_lo || ((t + 1) << TKS) > p.full_hi; };
 
+    // D <= 128: 4 x 128 registers a thread at launch = 2 x 88 + 2 x 168.
+    if (warp < C::SW) {
+    if constexpr (NSTR == 2) regs_down<88>();
     if (warp == 0) {
         // ------------------------------------------------- schedule, TMA producer
         SeqWalk<TKS> walk;
         walk.init(a, ar.tpt, run, &mi->sched, cta);
-        int n = 0, kn = 0, vn = 0;                      // pieces, K tiles, V tiles so far
+        int n = 0, kn = 0, vn = 0, qn = 0;              // pieces, K tiles, V tiles, Q tiles so far
         bool ok = true;
         if (lane == 0) ar.ws.rec[cta] = {0, 0, 0, 0};
+#pragma unroll 1
         for (;; ++n) {
             SeqPiece p;
             p.valid = 0;
@@ -263,46 +351,50 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                 if (slab == 0) atomicOr(a.status, kSeqBadPage);
                 return a.n_pages;
             };
-            int page_k = page_of(p.t0), page_v = page_k;
-            for (int t = 0; t <= p.nt && ok; ++t) {
-                // K of tile t, then V of tile t - 1: the order the issuers use them in
-                if (t < p.nt) {
-                    const int st = kn % NK;
-                    const int next = t + 1 < p.nt ? page_of(p.t0 + t + 1) : 0;
-                    ok = wait_or_abort(mi, &mi->k_empty[st], (static_cast<uint32_t>(kn / NK) & 1u) ^ 1u, a.status);
+            int page = page_of(p.t0);
+#pragma unroll 1
+            for (int t = 0; t < p.nt; ++t) {
+                const int next = t + 1 < p.nt ? page_of(p.t0 + t + 1) : 0;
+                const int key = ((p.t0 + t) << TKS) + box * bk;
+                // K and V of a tile together: V of tile t is then on its way while Q K^T of
+                // tile t - 1 still holds its K stage
+                const int sk = kn % NK;
+                ok = wait_or_abort(mi, &mi->k_empty[sk], (static_cast<uint32_t>(kn / NK) & 1u) ^ 1u, a.status);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(&mi->k_full[sk], C::STAGE);
+                __syncwarp();
+                load(&maps.k, sm + C::OFF_K + sk * C::STAGE, &mi->k_full[sk], page, key);
+                ++kn;
+                if (t == 0) {
+                    // the unit's rows of Q, once the products of the piece before have read theirs
+                    if (n > 0) ok = wait_or_abort(mi, &mi->q_empty, static_cast<uint32_t>(n - 1) & 1u, a.status);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
-                    if (lane == 0) mbar_arrive_expect_tx(&mi->k_full[st], C::STAGE);
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&mi->q_full, C::SLABS * ar.tpt * a.g * 128);
+                        for (int x = 0; x < C::SLABS; ++x)
+                            tma_load_3d(sm + C::OFF_Q + x * C::QSLAB, &maps.q, &mi->q_full, x * 64, p.kh * a.g, p.q0 + p.i0);
+                        ++qn;
+                    }
                     __syncwarp();
-                    load(&maps.k, sm + C::OFF_K + st * C::STAGE, &mi->k_full[st], page_k, ((p.t0 + t) << TKS) + box * bk);
-                    ++kn;
-                    if (t == 0) { page_k = next; continue; }
-                    const int cur = page_v;
-                    page_v = page_k;
-                    page_k = next;
-                    const int sv = vn % NV;
-                    ok = wait_or_abort(mi, &mi->v_empty[sv], (static_cast<uint32_t>(vn / NV) & 1u) ^ 1u, a.status);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    if (lane == 0) mbar_arrive_expect_tx(&mi->v_full[sv], C::STAGE);
-                    __syncwarp();
-                    load(&maps.v, sm + C::OFF_V + sv * C::STAGE, &mi->v_full[sv], cur, ((p.t0 + t - 1) << TKS) + box * bk);
-                    ++vn;
-                } else {
-                    const int sv = vn % NV;
-                    ok = wait_or_abort(mi, &mi->v_empty[sv], (static_cast<uint32_t>(vn / NV) & 1u) ^ 1u, a.status);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    if (lane == 0) mbar_arrive_expect_tx(&mi->v_full[sv], C::STAGE);
-                    __syncwarp();
-                    load(&maps.v, sm + C::OFF_V + sv * C::STAGE, &mi->v_full[sv], page_v, ((p.t0 + t - 1) << TKS) + box * bk);
-                    ++vn;
                 }
+                const int sv = vn % NV;
+                ok = wait_or_abort(mi, &mi->v_empty[sv], (static_cast<uint32_t>(vn / NV) & 1u) ^ 1u, a.status);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(&mi->v_full[sv], C::STAGE);
+                __syncwarp();
+                load(&maps.v, sm + C::OFF_V + sv * C::STAGE, &mi->v_full[sv], page, key);
+                ++vn;
+                page = next;
             }
             if (!ok) break;
         }
         // Drain: every copy issued has landed before the CTA's memory goes.
         if (lane == 0) {
+            if (qn > 0 && !mbar_wait_sleep(&mi->q_full, static_cast<uint32_t>(qn - 1) & 1u, 1u << 21, 1000))
+                atomicOr(a.status, kSeqTimeout);
             for (int i = max(0, kn - NK); i < kn; ++i)
                 if (!mbar_wait_sleep(&mi->k_full[i % NK], static_cast<uint32_t>(i / NK) & 1u, 1u << 21, 1000))
                     atomicOr(a.status, kSeqTimeout);
@@ -310,104 +402,90 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                 if (!mbar_wait_sleep(&mi->v_full[i % NV], static_cast<uint32_t>(i / NV) & 1u, 1u << 21, 1000))
                     atomicOr(a.status, kSeqTimeout);
         }
-    } else if (warp <= 2) {
+    } else if (warp == 1 || warp == 2 || warp == 4 || warp == 5) {
         // ------------------------------------------------------------ MMA issuers
-        const int w = warp - 1;
+        const int x = warp >> 2, w = warp - (x ? 4 : 1);   // stream; 0: Q K^T, 1: P V
         const uint32_t q_addr = smem_u32(sm + C::OFF_Q), k_addr = smem_u32(sm + C::OFF_K), v_addr = smem_u32(sm + C::OFF_V);
         constexpr uint32_t id_qk = idesc_f16(128, TK, BF16 ? 1 : 0, 0, 0);
         constexpr uint32_t id_pv = idesc_f16(128, D, BF16 ? 1 : 0, 0, 1);
+        constexpr uint64_t kHiQK = (uint64_t(16 >> 4) << 16) | (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+        constexpr uint64_t kHiV = (uint64_t(C::SLAB >> 4) << 16) | (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+        constexpr uint32_t qk_lo = static_cast<uint32_t>(kHiQK), qk_hi = static_cast<uint32_t>(kHiQK >> 32);
+        constexpr uint32_t v_lo = static_cast<uint32_t>(kHiV), v_hi = static_cast<uint32_t>(kHiV >> 32);
+        // shared addresses in a descriptor's 16-byte units
+        const uint32_t q16 = (q_addr >> 4) | qk_lo, k16 = (k_addr >> 4) | qk_lo, v16 = (v_addr >> 4) | v_lo;
         auto qk = [&](uint32_t q, uint32_t k, uint32_t s) {
 #pragma unroll
             for (int sl = 0; sl < C::SLABS; ++sl)
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_f16_ss(s, sw128_desc(q + sl * C::QSLAB + kk * 32, 16, 1024),
-                               sw128_desc(k + sl * C::SLAB + kk * 32, 16, 1024), id_qk, (sl | kk) != 0);
+                    mma_ss(s, q + sl * (C::QSLAB >> 4) + kk * 2, qk_hi, k + sl * (C::SLAB >> 4) + kk * 2, qk_hi, id_qk,
+                           (sl | kk) != 0);
         };
-        auto pv = [&](uint32_t p, uint32_t v, uint32_t o, bool first) {
+        auto pv = [&](uint32_t p, uint32_t v, uint32_t o, uint32_t acc) {
 #pragma unroll
-            for (int kk = 0; kk < TK / 16; ++kk)
-                mma_f16_ts(o, p + 8 * kk, sw128_desc(v + kk * 2048, C::SLAB, 1024), id_pv, !first || kk != 0);
+            for (int kk = 0; kk < TK / 16; ++kk) mma_ts(o, p + 8 * kk, v + kk * (2048 >> 4), v_hi, id_pv, kk != 0 ? 1u : acc);
         };
-        int kn = 0, vn = 0, tn = 0, qn = 0;             // K / V tiles of the CTA; tiles and Q tiles of this stream
         bool ok = true;
         SeqPiece p;
+        auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_or_abort(mi, bar, parity & 1u, a.status); };
+        // bn: tiles of the stream, in its two S buffers in turn; pn: its pieces; cn: tiles of
+        // the CTA; n: its pieces
+        int bn = 0, pn = 0, cn = 0, n = 0;
+        const uint32_t s0 = tmem + 128 * x, o = tm_o0 + 128 * x, q = q16 + x * (16384 >> 4);
+#pragma unroll 1
         while (ok && fetch(&p)) {
-            const bool act = NSTR == 1 || p.rows > 128 * w;
             if (lane == 0) {
-                auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_or_abort(mi, bar, parity & 1u, a.status); };
-                if (!act) {
-                    // this piece is the other stream's alone: release the tiles with it
-                    for (int t = 0; t < p.nt && ok; ++t, ++kn, ++vn) {
-                        ok = wait(&mi->k_full[kn % NK], kn / NK);
-                        if (ok) mbar_arrive(&mi->k_empty[kn % NK]);
-                        if (ok) ok = wait(&mi->v_ready[vn % NV], vn / NV);
-                        if (ok) mbar_arrive(&mi->v_empty[vn % NV]);
-                    }
-                } else if constexpr (NSTR == 2) {
-                    const uint32_t q = q_addr + w * C::SLABS * C::QSLAB, s = tmem + 128 * w, o = tm_o0 + 128 * w;
-                    auto do_qk = [&]() {
-                        // S overwrites P: the P V before it has read it
-                        if (ok && tn > 0) ok = wait(&mi->o_done[w], tn - 1);
-                        if (ok) ok = wait(&mi->k_full[kn % NK], kn / NK);
-                        if (!ok) return;
-                        tc_fence_after();
-                        qk(q, k_addr + (kn % NK) * C::STAGE, s);
-                        mma_commit(&mi->s_full[w]);
-                        mma_commit(&mi->k_empty[kn % NK]);
-                        ++kn;
-                    };
-                    ok = wait(&mi->q_full[w], qn);
-                    if (ok) do_qk();
-                    for (int t = 0; t < p.nt && ok; ++t) {
-                        ok = wait(&mi->p_full[w], tn);
-                        // O is rewritten: the piece before has been read out
-                        if (ok && t == 0 && qn > 0) ok = wait(&mi->o_free[w], qn - 1);
-                        if (ok) ok = wait(&mi->v_ready[vn % NV], vn / NV);
+                const bool act = NSTR == 1 || p.rows > 128 * x;
+                if (w == 0) {
+                    ok = wait(&mi->q_full, n);
+#pragma unroll 1
+                    for (int t = 0; t < p.nt && ok; ++t, ++cn) {
+                        const int st = cn % NK, sb = bn & 1;
+                        ok = wait(&mi->k_full[st], cn / NK);
+                        if (!act) {                     // the other stream's alone: release it with that one
+                            mbar_arrive(&mi->k_empty[st]);
+                            continue;
+                        }
+                        // S over P: the P V that read this buffer two tiles ago is done
+                        if (ok && bn >= 2) ok = wait(&mi->o_done[x][sb], (bn >> 1) - 1);
                         if (!ok) break;
                         tc_fence_after();
-                        pv(s, v_addr + (vn % NV) * C::STAGE, o, t == 0);
-                        mma_commit(&mi->o_done[w]);
-                        mma_commit(&mi->v_empty[vn % NV]);
-                        ++vn;
-                        ++tn;
-                        if (t + 1 < p.nt) do_qk();
+                        qk(q, k16 + st * (C::STAGE >> 4), s0 + 64 * sb);
+                        mma_commit(&mi->s_full[x][sb]);
+                        mma_commit(&mi->k_empty[st]);
+                        ++bn;
                     }
-                    ++qn;
-                } else if (w == 0) {
-                    ok = wait(&mi->q_full[0], qn++);
-                    for (int t = 0; t < p.nt && ok; ++t, ++tn) {
-                        const int sb = tn & 1;
-                        if (tn >= 2) ok = wait(&mi->o_done[sb], (tn - 2) >> 1);
-                        if (ok) ok = wait(&mi->k_full[kn % NK], kn / NK);
-                        if (!ok) break;
-                        tc_fence_after();
-                        qk(q_addr, k_addr + (kn % NK) * C::STAGE, tmem + 128 * sb);
-                        mma_commit(&mi->s_full[sb]);
-                        mma_commit(&mi->k_empty[kn % NK]);
-                        ++kn;
-                    }
+                    if (act) mma_commit(&mi->q_empty);
+                    else mbar_arrive(&mi->q_empty);
                 } else {
-                    for (int t = 0; t < p.nt && ok; ++t, ++tn) {
-                        const int sb = tn & 1;
-                        ok = wait(&mi->p_full[sb], tn >> 1);
-                        if (ok && t == 0 && qn > 0) ok = wait(&mi->o_free[0], qn - 1);
-                        if (ok) ok = wait(&mi->v_ready[vn % NV], vn / NV);
+#pragma unroll 1
+                    for (int t = 0; t < p.nt && ok; ++t, ++cn) {
+                        const int st = cn % NV, sb = bn & 1;
+                        ok = wait(&mi->v_ready[st], cn / NV);
+                        if (!act) {
+                            mbar_arrive(&mi->v_empty[st]);
+                            continue;
+                        }
+                        if (ok) ok = wait(&mi->p_full[x][sb], bn >> 1);
+                        // O is rewritten: the piece before has been read out
+                        if (ok && t == 0 && pn > 0) ok = wait(&mi->o_free[x], pn - 1);
                         if (!ok) break;
                         tc_fence_after();
-                        pv(tmem + 128 * sb, v_addr + (vn % NV) * C::STAGE, tm_o0, t == 0);
-                        mma_commit(&mi->o_done[sb]);
-                        mma_commit(&mi->v_empty[vn % NV]);
-                        ++vn;
+                        pv(s0 + 64 * sb, v16 + st * (C::STAGE >> 4), o, t != 0);
+                        mma_commit(&mi->o_done[x][sb]);
+                        mma_commit(&mi->v_empty[st]);
+                        ++bn;
                     }
-                    ++qn;
+                    if (act) ++pn;
                 }
+                ++n;
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
         }
         if (lane == 0) {                                // every MMA issued has completed
-            mma_commit(&mi->drain[w]);
-            if (!mbar_wait_sleep(&mi->drain[w], 0, 1u << 21, 1000)) atomicOr(a.status, kSeqTimeout);
+            mma_commit(&mi->drain[2 * x + w]);
+            if (!mbar_wait_sleep(&mi->drain[2 * x + w], 0, 1u << 21, 1000)) atomicOr(a.status, kSeqTimeout);
         }
         __syncwarp();
     } else if (warp == 3) {
@@ -415,10 +493,12 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
         int vn = 0, n = 0;
         bool ok = true;
         SeqPiece p;
+#pragma unroll 1
         for (; ok && fetch(&p); ++n) {
             bool marked = false;
             uint32_t *poison = ar.poison + (static_cast<size_t>(cta) * kPoison + n % kPoison) * ROWS * (D / 32);
             if (lane == 0) mi->poisoned[n % kPoison] = 0;
+#pragma unroll 1
             for (int t = 0; t < p.nt && ok; ++t, ++vn) {
                 const int st = vn % NV, k0 = (p.t0 + t) << TKS;
                 ok = __all_sync(0xffffffffu, wait_or_abort(mi, &mi->v_full[st], static_cast<uint32_t>(vn / NV) & 1u, a.status));
@@ -427,46 +507,37 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                     unsigned char *v = sm + C::OFF_V + st * C::STAGE;
                     const int live = min(max(p.kv - k0, 0), TK);
                     // slab rows are 128 bytes; lane l takes chunk l % 8 of rows l / 8, l / 8 + 4, ...
-                    bool found = false;
-                    for (int s = 0; s < C::SLABS; ++s)
-#pragma unroll 4
-                        for (int r = lane >> 3; r < TK; r += 4) {
-                            uint4 *x = reinterpret_cast<uint4 *>(v + s * C::SLAB + r * 128 + (lane & 7) * 16);
-                            if (r >= live) {
-                                *x = make_uint4(0, 0, 0, 0);
-                            } else {
-                                const uint4 y = *x;
-                                found |= odd16<BF16>(y.x) | odd16<BF16>(y.y) | odd16<BF16>(y.z) | odd16<BF16>(y.w);
-                            }
-                        }
-                    if (__any_sync(0xffffffffu, found)) {
-                        // rare: mark the rows that see an element that is not finite, then take it out
-                        if (!marked) {
-                            for (int i = lane; i < ROWS * (D / 32); i += 32) poison[i] = 0u;
-                            marked = true;
-                            __syncwarp();
-                        }
-                        for (int r = 0; r < live; ++r)
-                            for (int c = lane; c < D / 2; c += 32) {
-                                // column pair c of key row r, at its swizzled place
-                                const int s = c >> 5, ch = (c & 31) >> 2;
-                                uint32_t *x = reinterpret_cast<uint32_t *>(v + s * C::SLAB + r * 128 + ((ch ^ (r & 7)) << 4)) + (c & 3);
-                                constexpr uint32_t e = BF16 ? 0x7f80u : 0x7c00u;
-                                const bool l = (*x & e) == e, h = ((*x >> 16) & e) == e;
-                                if (!l && !h) continue;
-                                const uint32_t bits = (l ? 1u : 0u) << ((2 * c) & 31) | (h ? 1u : 0u) << ((2 * c + 1) & 31);
-                                for (int row = 0; row < p.rows; ++row) {
-                                    const int i = p.i0 + row / a.g;
-                                    uint32_t anc[kMaxTreeBitsNodes / 32] = {}, m[1];
-                                    if (a.parents) seq_ancestors(a.parents + p.q0, i, anc);
-                                    seq_visible<1>(a, p.prefix, p.kv, i, anc, k0 + r, m);
-                                    if (m[0] & 1u) atomicOr(poison + row * (D / 32) + (2 * c) / 32, bits);
+                    // Rows that every row of the unit sees need no look: left of full_lo and
+                    // right of full_hi they are scanned, past the last key zeroed.  16 vectors in
+                    // flight: the one warp's latency is the scan's time.
+                    uint32_t acc[4] = {};
+                    auto scan = [&](int r0, int r1) {              // slab-wise, r0 a multiple of 4
+                        for (int s = 0; s < C::SLABS; ++s)
+#pragma unroll 1
+                            for (int r = r0 + (lane >> 3); r < r1; r += 64) {
+                                const uint4 *x = reinterpret_cast<const uint4 *>(v + s * C::SLAB + r * 128 + (lane & 7) * 16);
+                                uint4 y[16];
+#pragma unroll
+                                for (int u = 0; u < 16; ++u) y[u] = r + 4 * u < r1 ? x[u * 32] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                                for (int u = 0; u < 16; ++u) {
+                                    acc[0] |= odd16<BF16>(y[u].x);
+                                    acc[1] |= odd16<BF16>(y[u].y);
+                                    acc[2] |= odd16<BF16>(y[u].z);
+                                    acc[3] |= odd16<BF16>(y[u].w);
                                 }
-                                if (l) *x &= 0xffff0000u;
-                                if (h) *x &= 0x0000ffffu;
                             }
-                        __threadfence();
-                        __syncwarp();
+                    };
+                    const int right = min(max(p.full_hi - k0, 0), live) & ~3, left = min(p.full_lo - k0, right);
+                    if (left > 0) scan(0, left);
+                    if (right < live) scan(right, live);
+                    for (int s = 0; s < C::SLABS; ++s)
+                        for (int r = live + (lane >> 3); r < TK; r += 4)
+                            *reinterpret_cast<uint4 *>(v + s * C::SLAB + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    const bool found = ((acc[0] | acc[1] | acc[2] | acc[3]) & 0x80008000u) != 0;
+                    if (__any_sync(0xffffffffu, found)) {
+                        mark_odd<D, BF16>(a, p, k0, live, v, poison, !marked);
+                        marked = true;
                         if (lane == 0) mi->poisoned[n % kPoison] = 1;
                     }
                     fence_proxy_async_smem();
@@ -475,161 +546,145 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                 if (lane == 0) mbar_arrive(&mi->v_ready[st]);
             }
         }
+    }
     } else {
-        // ------------------------------------------- softmax, Q loads, epilogue
-        const int s = (warp - 4) >> 2;                  // stream
+        // ---------------------------------------------------- softmax and epilogue
+        if constexpr (NSTR == 2) regs_up<168>();
+        const int s = (warp - C::SW) >> 2;
         const int quarter = warp & 3;
         const int r = quarter * 32 + lane;              // row within the stream
+        const int urow = 128 * s + r;                   // row within the unit
         const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-        const uint32_t tm_s = tmem + lane_off + (NSTR == 2 ? 128 * s : 0), tm_o = tm_o0 + lane_off + 128 * s;
-        // a negative scale turns into negated queries (exact), so that the largest
-        // product is the largest logit
-        const float scale2 = fmaxf(fabsf(a.scale) * kLog2e, FLT_MIN);   // above 0: a masked -inf stays -inf
-        const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
+        const uint32_t tm_s = tmem + lane_off + 128 * s, tm_o = tm_o0 + lane_off + 128 * s;
+        const float scale2 = fmaxf(a.scale * kLog2e, FLT_MIN);   // above 0: a masked -inf stays -inf
+        const int tok_row = static_cast<int>((static_cast<uint32_t>(urow) * ar.g_inv) >> 16);
         int tn = 0, vn = 0;                             // tiles of this stream, tiles of the CTA
         bool ok = true;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             ok = __all_sync(0xffffffffu, ok && wait_or_abort(mi, bar, parity & 1u, a.status));
         };
-        auto active = [&](const SeqPiece &p) { return NSTR == 1 || p.rows > 128 * s; };
-        // this warp's 32 rows of Q into shared memory (8 lanes a 128-byte row piece)
-        auto load_q = [&](const SeqPiece &p) {
-            unsigned char *dst = sm + C::OFF_Q + s * C::SLABS * C::QSLAB;
-#pragma unroll 2
-            for (int it = 0; it < 8; ++it) {
-                const int row = quarter * 32 + it * 4 + (lane >> 3), ch = lane & 7;
-                const int ur = 128 * s + row;
-                const bool live = ur < p.rows;
-                const int tok = ur / a.g, h = p.kh * a.g + ur - tok * a.g;
-                const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) +
-                                                                   static_cast<long long>(p.q0 + p.i0 + tok) * a.q_st + h * a.q_sh) + ch;
-#pragma unroll
-                for (int sl = 0; sl < C::SLABS; ++sl) {
-                    uint4 x = live ? __ldg(src + sl * 8) : make_uint4(0, 0, 0, 0);
-                    x.x ^= flip; x.y ^= flip; x.z ^= flip; x.w ^= flip;
-                    *reinterpret_cast<uint4 *>(dst + sl * C::QSLAB + row * 128 + ((ch ^ (row & 7)) << 4)) = x;
-                }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&mi->q_full[s]);
-        };
-
         SeqPiece p;
-        int n = 0;                                      // pieces of the CTA
-        bool have = fetch(&p);
-        if (have && active(p)) load_q(p);
-        for (; have && ok; ++n) {
-            const bool act = active(p);
+#pragma unroll 1
+        for (int n = 0; ok && fetch(&p); ++n) {         // pieces of the CTA
+            const bool act = NSTR == 1 || p.rows > 128 * s, live = urow < p.rows;
             float m_run = -INFINITY, l_run = 0.0f;
-            const int urow = 128 * s + r;
-            const bool live = urow < p.rows;
             if (act) {
-                const int i = p.i0 + urow / a.g;
+                const int i = p.i0 + tok_row;
                 uint32_t anc[kMaxTreeBitsNodes / 32];
                 if (a.parents && live) seq_ancestors(a.parents + p.q0, i, anc);
-                for (int t = 0; t < p.nt && ok; ++t, ++tn) {
-                    const int sb = NSTR == 2 ? s : tn & 1;
-                    const uint32_t ph = NSTR == 2 ? tn : tn >> 1;
-                    const uint32_t col = tm_s + (NSTR == 2 ? 0 : 128 * sb);
-                    wait(&mi->s_full[sb], ph);
+#pragma unroll 1
+                for (int t = 0; t < p.nt; ++t, ++tn) {
+                    const int sb = tn & 1;
+                    const uint32_t col = tm_s + 64 * sb;
+                    wait(&mi->s_full[s][sb], tn >> 1);
                     if (!ok) break;
                     tc_fence_after();
-                    uint32_t v[TK];
-#pragma unroll
-                    for (int c = 0; c < TK / 32; ++c)
-                        tmem_ld32(col + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&v[32 * c]));
-                    tmem_wait_ld();
                     const bool masked = is_masked(p, p.t0 + t);
-                    if (masked) {
-                        uint32_t m[TK / 32];
-                        seq_visible<TK / 32>(a, p.prefix, live ? p.kv : 0, i, anc, (p.t0 + t) << TKS, m);
-#pragma unroll
-                        for (int e = 0; e < TK; ++e)
-                            if (!((m[e >> 5] >> (e & 31)) & 1u)) v[e] = 0xff800000u;
-                    }
-                    float mx[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) mx[e] = __uint_as_float(v[e]);
-#pragma unroll
-                    for (int e = 4; e < TK; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(v[e]));
-                    const float rmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale2;
-                    float alpha = 1.0f;
-                    if (rmax > m_run + kSlack) {
-                        alpha = ex2(m_run - rmax);      // 0 from -inf
-                        l_run *= alpha;
-                        m_run = rmax;
-                    }
-                    if (t > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
-                        // O must be at rest: the P V of the tile before is done
-                        const int pb = NSTR == 2 ? s : (tn - 1) & 1;
-                        wait(&mi->o_done[pb], NSTR == 2 ? tn - 1 : (tn - 1) >> 1);
-                        if (!ok) break;
-                        tc_fence_after();
+                    // The row max is needed before the exponentials on a piece's first tile, and
+                    // on masked ones.  Else P is taken with the running max as it is and the
+                    // tile's own max beside the exponentials (other pipes); only where some
+                    // row's max rose by more than 2^8 is the tile done again.
+                    bool known = t == 0 || masked, again = false;
+                    float top = -INFINITY;
+                    uint32_t pk[TK / 2];
+                    float l_tile;
 #pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
-                            uint32_t o[32];
-                            tmem_ld32(tm_o + c, o);
-                            tmem_wait_ld();
+                    for (;;) {
+                        uint32_t v[TK];
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                            tmem_st32(tm_o + c, o);
+                        for (int c = 0; c < TK / 32; ++c)
+                            tmem_ld32(col + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&v[32 * c]));
+                        tmem_wait_ld();
+                        if (masked) {
+                            uint32_t m[TK / 32];
+                            seq_visible<TK / 32>(a, p.prefix, live ? p.kv : 0, i, anc, (p.t0 + t) << TKS, m);
+#pragma unroll
+                            for (int e = 0; e < TK; ++e)
+                                if (!((m[e >> 5] >> (e & 31)) & 1u)) v[e] = 0xff800000u;
                         }
-                    }
-                    const float m_use = m_run == -INFINITY ? 0.0f : m_run;
-                    const uint64_t sc = pack64(scale2, scale2), mm = pack64(-m_use, -m_use);
-                    uint64_t sum[2] = {0, 0};
+                        if (known) {
+                            if (!again) {
 #pragma unroll
-                    for (int c = 0; c < TK / 32; c += 2) {
-                        uint32_t pk[32];
+                                for (int e = 0; e < TK; e += 2) top = max3(top, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+                            }
+                            // O and l follow where the running max rises
+                            const float rmax = top * scale2;
+                            float alpha = 1.0f;
+                            if (rmax > m_run + kSlack) {
+                                alpha = ex2(m_run - rmax);          // 0 from -inf
+                                l_run *= alpha;
+                                m_run = rmax;
+                            }
+                            if (t > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
+                                // O must be at rest: the P V of the tile before is done
+                                wait(&mi->o_done[s][(tn - 1) & 1], (tn - 1) >> 1);
+                                tc_fence_after();
+#pragma unroll 1
+                                for (int c = 0; c < D; c += 16) {
+                                    uint32_t o[16];
+                                    tmem_ld16(tm_o + c, o);
+                                    tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const uint64_t x = fma2(pack64(__uint_as_float(v[32 * c + 2 * e]), __uint_as_float(v[32 * c + 2 * e + 1])), sc, mm);
+                                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                    tmem_st16(tm_o + c, o);
+                                }
+                            }
+                        }
+                        const float m_use = m_run == -INFINITY ? 0.0f : m_run;
+                        const uint64_t sc = pack64(scale2, scale2), mm = pack64(-m_use, -m_use);
+                        uint64_t sum[2] = {0, 0};
+                        float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                        for (int e = 0; e < TK / 2; ++e) {
+                            const float s0 = __uint_as_float(v[2 * e]), s1 = __uint_as_float(v[2 * e + 1]);
+                            const uint64_t x = fma2(pack64(s0, s1), sc, mm);
                             const float p0 = ex2(lo64(x)), p1 = ex2(hi64(x));
                             sum[e & 1] = add2(sum[e & 1], pack64(p0, p1));
                             pk[e] = pack16<BF16>(p0, p1);
+                            mx[e & 1] = max3(mx[e & 1], s0, s1);
                         }
-                        tmem_st32(col + 16 * c, pk);
+                        const uint64_t all = add2(sum[0], sum[1]);
+                        l_tile = lo64(all) + hi64(all);
+                        if (known) break;
+                        top = fmaxf(mx[0], mx[1]);
+                        if (!__any_sync(0xffffffffu, top * scale2 > m_run + kSlack)) break;
+                        known = again = true;
                     }
-                    const uint64_t all = add2(sum[0], sum[1]);
-                    l_run += lo64(all) + hi64(all);
+                    l_run += l_tile;
+                    tmem_st32(col, pk);
                     // the guard's marks of this V tile are in before its P V can be issued
                     if (masked) wait(&mi->v_ready[(vn + t) % NV], (vn + t) / NV);
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
-                    if (ok && lane == 0) mbar_arrive(&mi->p_full[sb]);
+                    if (lane == 0) mbar_arrive(&mi->p_full[s][sb]);
                 }
             }
             vn += p.nt;
-            SeqPiece nx;
-            nx.valid = 0;
-            if (ok) have = fetch(&nx);
-            if (ok && have && active(nx)) load_q(nx);
             if (act && ok) {
-                const int pb = NSTR == 2 ? s : (tn - 1) & 1;
-                wait(&mi->o_done[pb], NSTR == 2 ? tn - 1 : (tn - 1) >> 1);
+                wait(&mi->o_done[s][(tn - 1) & 1], (tn - 1) >> 1);
                 if (!ok) break;
                 tc_fence_after();
                 const bool odd = *static_cast<volatile int *>(&mi->poisoned[n % kPoison]) != 0;
                 const uint32_t *poison = ar.poison + ((static_cast<size_t>(cta) * kPoison + n % kPoison) * ROWS + urow) * (D / 32);
                 const float inv = l_run > 0.0f ? 1.0f / l_run : (l_run == 0.0f ? 0.0f : l_run);
-                const int tok = urow / a.g, h = p.kh * a.g + urow - tok * a.g;
-                uint16_t *out = static_cast<uint16_t *>(a.out) + static_cast<long long>(p.q0 + p.i0 + tok) * a.o_st + h * a.o_sh;
                 const size_t slot = static_cast<size_t>(p.slot < 0 ? 0 : p.slot);
                 float4 *part = reinterpret_cast<float4 *>(ar.ws.o) + slot * (D / 4) * ROWS + urow;
+                unsigned char *stage = sm + C::OFF_OUT + (warp - C::SW) * 2048;
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     uint32_t o[32];
                     tmem_ld32(tm_o + c, o);
                     tmem_wait_ld();
-                    if (odd && live) {                 // poisoned columns of this row
+                    if (odd && live) {                  // poisoned columns of this row
                         const uint32_t bits = __ldcg(poison + c / 32);
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
                             if ((bits >> e) & 1u) o[e] = 0x7fffffffu;
                     }
-                    if (live && p.slot < 0) {
+                    if (p.slot < 0) {
+                        // 32 columns of the warp's 32 rows through shared memory, so that a store
+                        // covers 8 rows' 64 bytes (a row a lane took 32 cycles a store)
 #pragma unroll
                         for (int e = 0; e < 32; e += 8) {
                             uint4 x;
@@ -637,7 +692,18 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                             x.y = pack16<BF16>(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
                             x.z = pack16<BF16>(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
                             x.w = pack16<BF16>(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
-                            *reinterpret_cast<uint4 *>(out + c + e) = x;
+                            *reinterpret_cast<uint4 *>(stage + lane * 64 + (((e / 8) ^ ((lane >> 1) & 3)) << 4)) = x;
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int u = 0; u < 32; u += 8) {
+                            const int row = u + (lane >> 2), ch = lane & 3, ur = 128 * s + 32 * quarter + row;
+                            const uint4 x = *reinterpret_cast<const uint4 *>(stage + row * 64 + ((ch ^ ((row >> 1) & 3)) << 4));
+                            const int tok = static_cast<int>((static_cast<uint32_t>(ur) * ar.g_inv) >> 16), h = p.kh * a.g + ur - tok * a.g;
+                            if (ur < p.rows)
+                                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) +
+                                                           static_cast<long long>(p.q0 + p.i0 + tok) * a.o_st + h * a.o_sh + c +
+                                                           ch * 8) = x;
                         }
                     } else if (live) {
 #pragma unroll
@@ -653,7 +719,6 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&mi->o_free[s]);
             }
-            p = nx;
         }
     }
     tc_fence_before();
@@ -727,6 +792,7 @@ cudaError_t launch_dim(const SeqArgs &a, const SeqTcPlan &pl, cudaStream_t s) {
     ar.a = a;
     ar.G = pl.G;
     ar.tpt = Cfg<D>::ROWS / a.g;
+    ar.g_inv = (65536u + a.g - 1) / a.g;
     char *ws = static_cast<char *>(pl.ws);
     ar.ws.rec = reinterpret_cast<SeqRec *>(ws + 256);
     const size_t slots = 2 * static_cast<size_t>(pl.G), rows = Cfg<D>::ROWS;
@@ -737,6 +803,7 @@ cudaError_t launch_dim(const SeqArgs &a, const SeqTcPlan &pl, cudaStream_t s) {
     off += slots * rows * D * sizeof(float);
     ar.poison = reinterpret_cast<uint32_t *>(ws + off);
     Maps maps;
+    maps.q = pl.q;
     maps.k = pl.k;
     maps.v = pl.v;
     if (a.kv_lens)
