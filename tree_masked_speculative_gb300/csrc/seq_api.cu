@@ -124,11 +124,33 @@ ta_status check_prompt(const ta_prompt_params *p) {
     return TA_OK;
 }
 
+// Kernel family of a call (rows: most query rows of a request per KV head, 0 for
+// prompts).  Few rows over pages go to the warp-MMA kernel unless another family is
+// asked for; the tensor-core kernel takes the largest product for the largest
+// logit, so a negative scale goes to the CUDA cores, as it does for the warp-MMA one.
+int seq_family(uint32_t d, uint32_t kernel, uint64_t rows, float scale) {
+    if (kernel == TA_KERNEL_CUDA_CORES || scale < 0.0f) return TA_KERNEL_CUDA_CORES;
+    if (kernel != TA_KERNEL_TENSOR_CORES && rows > 0 && seq_mma_takes(static_cast<int>(d), static_cast<long long>(rows)))
+        return TA_KERNEL_WARP_MMA;
+    return TA_KERNEL_TENSOR_CORES;
+}
+
 // Workspace of a call; 0 when no device is visible to size the grid for.
-uint64_t seq_workspace(uint32_t d, uint32_t kernel) {
-    if (kernel == TA_KERNEL_CUDA_CORES) return kStatusBytes;
+uint64_t seq_workspace(uint32_t d, int family, uint64_t rows) {
+    if (family == TA_KERNEL_CUDA_CORES) return kStatusBytes;
     const int sms = device_sm_count();
-    return sms > 0 ? seq_tc_workspace(static_cast<int>(d), sms) : 0;
+    if (sms <= 0) return 0;
+    return family == TA_KERNEL_WARP_MMA ? seq_mma_workspace(static_cast<int>(d), static_cast<int>(rows), sms)
+                                        : seq_tc_workspace(static_cast<int>(d), sms);
+}
+int paged_family(const ta_paged_params *p) {
+    return seq_family(p->head_dim, p->kernel, static_cast<uint64_t>(p->max_q_len) * (p->n_heads / p->n_kv_heads), p->scale);
+}
+uint64_t paged_workspace(const ta_paged_params *p) {
+    return seq_workspace(p->head_dim, paged_family(p), static_cast<uint64_t>(p->max_q_len) * (p->n_heads / p->n_kv_heads));
+}
+uint64_t prompt_workspace(const ta_prompt_params *p) {
+    return seq_workspace(p->head_dim, seq_family(p->head_dim, p->kernel, 0, p->scale), 0);
 }
 
 bool encode_16bit(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap *m, const SeqArgs &a, const void *ptr, int rank,
@@ -164,11 +186,12 @@ bool kv_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap *m, const SeqA
     return encode_16bit(encode, m, a, ptr, rank, dims, str, box);
 }
 
-ta_status run_seq(const char *op, const SeqArgs &a, uint32_t kernel, void *ws, cudaStream_t s) {
+ta_status run_seq(const char *op, const SeqArgs &a, int family, void *ws, cudaStream_t s) {
     cudaError_t e;
-    // the tensor-core kernel takes the largest product for the largest logit: no negative scale
-    if (kernel == TA_KERNEL_CUDA_CORES || a.scale < 0.0f) {
+    if (family == TA_KERNEL_CUDA_CORES) {
         e = launch_seq_fma(a, s);
+    } else if (family == TA_KERNEL_WARP_MMA) {
+        e = launch_seq_mma(a, ws, device_sm_count(), s);
     } else {
         SeqTcPlan pl;
         pl.G = device_sm_count();
@@ -309,14 +332,14 @@ TA_EXPORT ta_status paged_kv_append(const ta_append_params *pp, const ta_buf *k_
 
 TA_EXPORT size_t paged_attn_workspace_bytes(const ta_paged_params *p) {
     if (check_paged(p) != TA_OK) return SIZE_MAX;
-    const uint64_t ws = seq_workspace(p->head_dim, p->kernel);
+    const uint64_t ws = paged_workspace(p);
     if (ws == 0) set_last_error("paged_attn: no CUDA device to size the workspace for");
     return ws ? ws : SIZE_MAX;
 }
 
 TA_EXPORT size_t prompt_attn_workspace_bytes(const ta_prompt_params *p) {
     if (check_prompt(p) != TA_OK) return SIZE_MAX;
-    const uint64_t ws = seq_workspace(p->head_dim, p->kernel);
+    const uint64_t ws = prompt_workspace(p);
     if (ws == 0) set_last_error("prompt_attn: no CUDA device to size the workspace for");
     return ws ? ws : SIZE_MAX;
 }
@@ -350,7 +373,7 @@ TA_EXPORT ta_status paged_attn_fwd(const ta_paged_params *pp, const ta_buf *q, c
     const Axis cax[3] = {{p.n_pages, p.page_stride}, {p.n_kv_heads, p.head_stride}, {p.page_size, p.token_stride}};
     if (!extent(qax, p.head_dim, &nq) || !extent(oax, p.head_dim, &no) || !extent(cax, p.head_dim, &nc))
         SEQ_FAIL(TA_ERR_OVERFLOW, "paged_attn: sizes overflow");
-    const uint64_t ws = seq_workspace(p.head_dim, p.kernel);
+    const uint64_t ws = paged_workspace(&p);
     SEQ_TRY(check(op, "q", *q, type, nq, 16));
     SEQ_TRY(check(op, "k_cache", of(k_cache), type, nc, 16));
     SEQ_TRY(check(op, "v_cache", of(v_cache), type, nc, 16));
@@ -391,7 +414,7 @@ TA_EXPORT ta_status paged_attn_fwd(const ta_paged_params *pp, const ta_buf *q, c
     a.k_sh = a.v_sh = static_cast<long long>(p.head_stride);
     a.scale = p.scale;
     if (ws == 0) SEQ_FAIL(TA_ERR_CUDA, "%s: no CUDA device", op);
-    return run_seq(op, a, p.kernel, tmp->ptr, static_cast<cudaStream_t>(stream));
+    return run_seq(op, a, paged_family(&p), tmp->ptr, static_cast<cudaStream_t>(stream));
 }
 
 TA_EXPORT ta_status prompt_attn_fwd(const ta_prompt_params *pp, const ta_buf *q, const ta_buf *k, const ta_buf *v,
@@ -422,7 +445,7 @@ TA_EXPORT ta_status prompt_attn_fwd(const ta_prompt_params *pp, const ta_buf *q,
     if (!extent(qax, p.head_dim, &nq) || !extent(oax, p.head_dim, &no) || !extent(kax, p.head_dim, &nk) ||
         !extent(vax, p.head_dim, &nv))
         SEQ_FAIL(TA_ERR_OVERFLOW, "prompt_attn: sizes overflow");
-    const uint64_t ws = seq_workspace(p.head_dim, p.kernel);
+    const uint64_t ws = prompt_workspace(&p);
     SEQ_TRY(check(op, "q", *q, type, nq, 16));
     SEQ_TRY(check(op, "k", of(k), type, nk, 16));
     SEQ_TRY(check(op, "v", of(v), type, nv, 16));
@@ -454,5 +477,5 @@ TA_EXPORT ta_status prompt_attn_fwd(const ta_prompt_params *pp, const ta_buf *q,
     a.v_sh = static_cast<long long>(p.v_head_stride);
     a.scale = p.scale;
     if (ws == 0) SEQ_FAIL(TA_ERR_CUDA, "%s: no CUDA device", op);
-    return run_seq(op, a, p.kernel, tmp->ptr, static_cast<cudaStream_t>(stream));
+    return run_seq(op, a, seq_family(p.head_dim, p.kernel, 0, p.scale), tmp->ptr, static_cast<cudaStream_t>(stream));
 }
