@@ -101,7 +101,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D, RH>) seq_mma_kernel(co
     walk.init(a, a.max_q, run, &sched, cta);
     SeqPiece p;
     while (walk.next(a, a.max_q, run, &p)) {
-        if (tid == 0 && p.parts > 0) ar.rec[cta] = {p.parts, p.q0 + p.i0, p.kh, p.rows};
         // Q fragments: columns 32 j + 8 t + 4 h + {0, 1 | 2, 3} of rows g, g + 8
         uint32_t qa[RH][D / 16][2];
         int tok[RH];
@@ -302,6 +301,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D, RH>) seq_mma_kernel(co
             load_v(next, key + 16 * kWarps);
             next = after;
         }
+        if (tid == 0 && p.rest > 0) ar.rec[cta] = seq_record(run, cta, p);
         // ---- join the four warps
 #pragma unroll
         for (int x = 0; x < RH; ++x) {
@@ -375,40 +375,69 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D, RH>) seq_mma_kernel(co
 }
 
 // out = sum_p O_p 2^(m_p - m*) / sum_p l_p 2^(m_p - m*) over the pieces of the cut unit
-// that starts in CTA blockIdx.x; 8 columns of a row a thread.
+// that starts in CTA blockIdx.x.  A few units are cut into many pieces when the
+// batch is small, so a block's threads share the pieces as well as the columns
+// (one thread a column through all of 22 pieces took 14 us).
+constexpr int kMergeThreads = 256;
 template <int D, bool BF16>
-__global__ void __launch_bounds__(128) seq_mma_merge_kernel(const MmaArgs ar) {
+__global__ void __launch_bounds__(kMergeThreads) seq_mma_merge_kernel(const MmaArgs ar) {
     const SeqArgs &a = ar.a;
+    __shared__ float s_m[16], s_inv[16];
+    __shared__ float4 s_part[kMergeThreads];
     pdl_wait();
-    const int c = blockIdx.x;
+    const int c = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const SeqRec rec = ar.rec[c];
     if (rec.parts == 0) return;
     auto slot = [&](int p) { return static_cast<size_t>(p == 0 ? 2 * c + 1 : 2 * (c + p)); };
-    for (int i = threadIdx.x + blockIdx.y * 128; i < rec.rows * (D / 8); i += 128 * gridDim.y) {
-        const int row = i / (D / 8), d = (i - row * (D / 8)) * 8;
-        float m = -INFINITY, l = 0.0f, r[8] = {};
-#pragma unroll 4
-        for (int p = 0; p < rec.parts; ++p) {
+    for (int row = warp; row < rec.rows; row += kMergeThreads / 32) {
+        float m = -INFINITY, l = 0.0f;
+#pragma unroll 2
+        for (int p = lane; p < rec.parts; p += 32) {
             const float2 w = ar.ml[slot(p) * 16 + row];
-            const float *src = ar.o + (slot(p) * 16 + row) * D + d;
-            const float4 y = *reinterpret_cast<const float4 *>(src), z = *reinterpret_cast<const float4 *>(src + 4);
-            if (w.x == -INFINITY) continue;
-            const float mn = fmaxf(m, w.x), f = ex2(m - mn), h = ex2(w.x - mn);
-            l = l * f + w.y * h;
-            r[0] = r[0] * f + y.x * h; r[1] = r[1] * f + y.y * h; r[2] = r[2] * f + y.z * h; r[3] = r[3] * f + y.w * h;
-            r[4] = r[4] * f + z.x * h; r[5] = r[5] * f + z.y * h; r[6] = r[6] * f + z.z * h; r[7] = r[7] * f + z.w * h;
+            const float mn = fmaxf(m, w.x), mu = mn == -INFINITY ? 0.0f : mn;
+            l = l * ex2(m - mu) + w.y * ex2(w.x - mu);
             m = mn;
         }
-        const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-        const int tk = row / a.g;
-        uint16_t *out = static_cast<uint16_t *>(a.out) + static_cast<long long>(rec.token + tk) * a.o_st +
-                        static_cast<long long>(rec.kh * a.g + row - tk * a.g) * a.o_sh + d;
-        uint4 y;
-        y.x = pack16<BF16>(r[0] * inv, r[1] * inv);
-        y.y = pack16<BF16>(r[2] * inv, r[3] * inv);
-        y.z = pack16<BF16>(r[4] * inv, r[5] * inv);
-        y.w = pack16<BF16>(r[6] * inv, r[7] * inv);
-        *reinterpret_cast<uint4 *>(out) = y;
+        const float mr = warp_max(m), mu = mr == -INFINITY ? 0.0f : mr;
+        l = warp_sum(l * ex2(m - mu));
+        if (lane == 0) {
+            s_m[row] = mu;
+            s_inv[row] = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+        }
+    }
+    __syncthreads();
+    // items: 4 columns of a row; `share` threads take the pieces of one item in turn
+    const int items = rec.rows * (D / 4);
+    int share = 1;
+    while (2 * share * items <= kMergeThreads) share *= 2;
+    const int per = kMergeThreads / share;              // items at a time
+    for (int i0 = 0; i0 < items; i0 += per) {
+        const int k = tid / per, i = i0 + tid - k * per;
+        float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const int row = i / (D / 4), d = (i - row * (D / 4)) * 4;
+        if (i < items) {
+            const float mu = s_m[row];
+#pragma unroll 4
+            for (int p = k; p < rec.parts; p += share) {
+                const float f = ex2(ar.ml[slot(p) * 16 + row].x - mu);
+                const float4 y = *reinterpret_cast<const float4 *>(ar.o + (slot(p) * 16 + row) * D + d);
+                r.x += f * y.x; r.y += f * y.y; r.z += f * y.z; r.w += f * y.w;
+            }
+        }
+        s_part[tid] = r;
+        __syncthreads();
+        if (k == 0 && i < items) {
+            for (int j = 1; j < share; ++j) {
+                const float4 y = s_part[tid + j * per];
+                r.x += y.x; r.y += y.y; r.z += y.z; r.w += y.w;
+            }
+            const float inv = s_inv[row];
+            const int tk = row / a.g;
+            uint16_t *out = static_cast<uint16_t *>(a.out) + static_cast<long long>(rec.token + tk) * a.o_st +
+                            static_cast<long long>(rec.kh * a.g + row - tk * a.g) * a.o_sh + d;
+            *reinterpret_cast<uint2 *>(out) = make_uint2(pack16<BF16>(r.x * inv, r.y * inv), pack16<BF16>(r.z * inv, r.w * inv));
+        }
+        __syncthreads();
     }
 }
 
@@ -419,7 +448,7 @@ cudaError_t launch(const MmaArgs &ar, cudaStream_t s) {
     cudaError_t e = launch_pdl(kern, dim3(ar.G), dim3(kThreads), smem, s, ar);
     count_launch();
     if (e != cudaSuccess) return e;
-    e = launch_pdl(seq_mma_merge_kernel<D, BF16>, dim3(ar.G), dim3(128), 0, s, ar);
+    e = launch_pdl(seq_mma_merge_kernel<D, BF16>, dim3(ar.G), dim3(kMergeThreads), 0, s, ar);
     count_launch();
     return e;
 }

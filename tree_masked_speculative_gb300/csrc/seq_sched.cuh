@@ -49,26 +49,48 @@ __device__ __forceinline__ int seq_head_tiles(const SeqArgs &a, int qn, int kv, 
     return c;
 }
 
+struct SeqRec {
+    int parts;      // pieces of the cut unit that starts in this CTA (0: none)
+    int token;      // its first row of q / out
+    int kh, rows;
+};
+
+// Cut of W key tiles into G runs whose lengths differ by one at most: CTA c
+// starts at c * base + min(c, extra).
+struct SeqRun {
+    long long W, P0, P1;
+    long long base;
+    int G, extra;       // G: CTAs with work, one key tile at least for each
+    __device__ __forceinline__ long long start(int c) const { return c * base + min(c, extra); }
+    // CTA whose run holds position P
+    __device__ __forceinline__ int cta_of(long long P) const {
+        const long long big = extra * (base + 1);
+        const long long x = P < big ? P : P - big, d = P < big ? base + 1 : base;
+        const int q = W <= 0x7fffffffll ? static_cast<int>(static_cast<uint32_t>(x) / static_cast<uint32_t>(d)) : static_cast<int>(x / d);
+        return P < big ? q : extra + q;
+    }
+};
+
 struct SeqScratch {
     long long warp_tot[32];
     long long off;      // start inside the first request, in key tiles
-    int b;
+    SeqReq r;           // the first request
+    int b, per_head;    // its index; its key tiles of one KV head
 };
 
-// This CTA's run [P0, P1) of the W key tiles and where it starts (s->b, s->off,
-// valid when P0 < P1).  Block-collective.
-struct SeqRun {
-    long long W, P0, P1;
-    int G;              // CTAs with work: one key tile at least for each
-};
+// This CTA's run [P0, P1) of the W key tiles and where it starts (in *s, valid when
+// P0 < P1).  Block-collective.
 template <int NT, int TKS>
 __device__ SeqRun seq_schedule(const SeqArgs &a, int tpt, int cta, int G, SeqScratch *s) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    SeqReq r;
+    int per_head;
     auto tiles_of = [&](int b) -> long long {      // warp-collective
-        SeqReq r = {0, 0, 0, false};
+        r = {0, 0, 0, false};
         if (b < a.B) r = seq_request(a, b);
         if (r.bad && cta == 0) atomicOr(a.status, kSeqBadLength);
-        return static_cast<long long>(seq_head_tiles<TKS>(a, r.qn, r.kv, tpt)) * a.Hk;
+        per_head = seq_head_tiles<TKS>(a, r.qn, r.kv, tpt);
+        return static_cast<long long>(per_head) * a.Hk;
     };
     // inclusive sum over the block's threads; *total of all
     auto scan = [&](long long x, long long *total) -> long long {
@@ -94,22 +116,34 @@ __device__ SeqRun seq_schedule(const SeqArgs &a, int tpt, int cta, int G, SeqScr
     long long mine = tiles_of(tid), tot;
     long long inc = scan(mine, &tot);
     run.W = tot;
+#pragma unroll 1
     for (int b0 = NT; b0 < a.B; b0 += NT) {
         long long t;
         scan(tiles_of(b0 + tid), &t);
         run.W += t;
     }
     run.G = static_cast<int>(min(static_cast<long long>(G), run.W));
-    run.P0 = cta < run.G ? flat_start(cta, run.W, run.G) : run.W;
-    run.P1 = cta < run.G ? flat_start(cta + 1, run.W, run.G) : run.W;
+    if (run.W <= 0x7fffffffll) {
+        const uint32_t g = max(run.G, 1), w = static_cast<uint32_t>(run.W), q = w / g;
+        run.base = q;
+        run.extra = static_cast<int>(w - q * g);
+    } else {
+        run.base = run.W / run.G;
+        run.extra = static_cast<int>(run.W - run.base * run.G);
+    }
+    run.P0 = cta < run.G ? run.start(cta) : run.W;
+    run.P1 = cta < run.G ? run.start(cta + 1) : run.W;
     long long before = 0;
+#pragma unroll 1
     for (int b0 = 0; b0 < a.B; b0 += NT) {
-        if (b0 > 0) {
+        if (b0 > 0 || a.B > NT) {
             mine = tiles_of(b0 + tid);
             inc = scan(mine, &tot);
         }
         if (run.P0 < run.P1 && run.P0 >= before + inc - mine && run.P0 < before + inc) {
             s->b = b0 + tid;
+            s->r = r;
+            s->per_head = per_head;
             s->off = run.P0 - (before + inc - mine);
         }
         before += tot;
@@ -129,7 +163,8 @@ struct SeqPiece {
     int t0, nt;          // first key tile, key tiles
     int full_lo, full_hi;  // every row sees the keys in [full_lo, full_hi)
     int slot;            // partial slot, or -1: the whole unit
-    int parts;           // pieces of the unit, counted in its first piece (else 0)
+    long long pos;       // position of its first tile among all
+    int rest;            // key tiles of the unit after this piece, counted in a cut unit's first piece (else 0)
 };
 
 // Walks this CTA's pieces.  Warp-collective; all lanes hold the same state.
@@ -149,11 +184,16 @@ struct SeqWalk {
         cta = cta_;
         if (left <= 0) return;
         b = s->b;
-        enter(a, tpt);
-        const int per_head = seq_head_tiles<TKS>(a, (threadIdx.x & 31) == 0 ? r.qn : 0, r.kv, tpt);
-        const int c = __shfl_sync(0xffffffffu, per_head, 0);
-        const int kh = static_cast<int>(s->off / c);
-        off = static_cast<int>(s->off - static_cast<long long>(kh) * c);
+        r = s->r;
+        nqt = (r.qn + tpt - 1) / tpt;
+        const long long o = s->off;
+        const int c = s->per_head;
+        const int kh = o <= 0x7fffffffll ? static_cast<int>(static_cast<uint32_t>(o) / static_cast<uint32_t>(c)) : static_cast<int>(o / c);
+        off = static_cast<int>(o - static_cast<long long>(kh) * c);
+        if (nqt == 1) {
+            u = kh;
+            return;
+        }
         int qt = 0;
         // the row tile that holds tile `off` of this KV head, 32 row tiles a step
         for (;; qt += 32) {
@@ -180,10 +220,10 @@ struct SeqWalk {
     __device__ bool next(const SeqArgs &a, int tpt, const SeqRun &run, SeqPiece *p) {
         if (left <= 0) return false;
         int first;
-        const int qt = u % nqt, n = seq_unit_tiles<TKS>(a, r.qn, r.kv, qt, tpt, &first);
+        const int kh = nqt == 1 ? u : u / nqt, qt = u - kh * nqt, n = seq_unit_tiles<TKS>(a, r.qn, r.kv, qt, tpt, &first);
         p->valid = 1;
         p->b = b;
-        p->kh = u / nqt;
+        p->kh = kh;
         p->q0 = r.q0;
         p->i0 = qt * tpt;
         const int nt_tok = min(tpt, r.qn - p->i0);
@@ -196,7 +236,8 @@ struct SeqWalk {
         p->full_lo = a.parents || !a.window ? 0 : max(0, p->prefix + p->i0 + nt_tok - a.window);
         const bool starts = off == 0, ends = off + p->nt == n;
         p->slot = starts && ends ? -1 : starts ? 2 * cta + 1 : 2 * cta;
-        p->parts = starts && !ends ? flat_group_of(pos + n - 1, run.W, run.G) - cta + 1 : 0;
+        p->rest = starts && !ends ? n - p->nt : 0;
+        p->pos = pos;
         pos += p->nt;
         left -= p->nt;
         off = 0;
@@ -211,6 +252,11 @@ struct SeqWalk {
         return true;
     }
 };
+
+// Record of a cut unit's first piece, for the merge.
+__device__ __forceinline__ SeqRec seq_record(const SeqRun &run, int cta, const SeqPiece &p) {
+    return {run.cta_of(p.pos + p.nt + p.rest - 1) - cta + 1, p.q0 + p.i0, p.kh, p.rows};
+}
 
 // Bit e of word w: does row `i` (token of its request) of a piece see key
 // k0 + 32 w + e.  `anc`: the token's ancestor bits (trees).
@@ -256,11 +302,6 @@ __device__ __forceinline__ void seq_ancestors(const int32_t *parents, int i, uin
 
 // Workspace of the scheduled kernels: [status word, 256 B][records][(m, l) of
 // the partial slots][O of the partial slots].
-struct SeqRec {
-    int parts;      // pieces of the cut unit that starts in this CTA (0: none)
-    int token;      // its first row of q / out
-    int kh, rows;
-};
 struct SeqWs {
     SeqRec *rec;       // [G]
     float2 *ml;        // [2 G][rows]: running max in log2 units, sum

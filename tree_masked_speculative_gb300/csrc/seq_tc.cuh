@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                 mi->piece[i] = p;
                 mbar_arrive(&mi->piece_full[i]);
                 // the unit's first piece leaves the record of how many there are
-                if (more && p.parts > 0) ar.ws.rec[cta] = {p.parts, p.q0 + p.i0, p.kh, p.rows};
+                if (more && p.rest > 0) ar.ws.rec[cta] = seq_record(run, cta, p);
             }
             __syncwarp();
             if (!more) break;
@@ -741,22 +741,25 @@ __global__ void __launch_bounds__(Cfg<D>::ROWS) seq_merge_kernel(const SeqArgs a
     if (r >= rec.rows || rec.parts == 0) return;
     // pieces: slot 2 c + 1, then the first slots of the CTAs after it
     auto slot = [&](int p) { return static_cast<size_t>(p == 0 ? 2 * c + 1 : 2 * (c + p)); };
+    // the max first, then sums whose loads do not wait for one another
     float m = -INFINITY, l = 0.0f, o[16] = {};
+#pragma unroll 4
+    for (int p = 0; p < rec.parts; ++p) m = fmaxf(m, ws.ml[slot(p) * ROWS + r].x);
+    const float mu = m == -INFINITY ? 0.0f : m;
+#pragma unroll 4
     for (int p = 0; p < rec.parts; ++p) {
         const float2 x = ws.ml[slot(p) * ROWS + r];
-        if (x.x == -INFINITY) continue;
-        const float mn = fmaxf(m, x.x), f = ex2(m - mn), g = ex2(x.x - mn);
-        l = l * f + x.y * g;
+        const float g = ex2(x.x - mu);
+        l += x.y * g;
         const float4 *src = reinterpret_cast<const float4 *>(ws.o) + (slot(p) * (D / 4) + d0 / 4) * ROWS + r;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const float4 y = src[e * ROWS];
-            o[4 * e] = o[4 * e] * f + y.x * g;
-            o[4 * e + 1] = o[4 * e + 1] * f + y.y * g;
-            o[4 * e + 2] = o[4 * e + 2] * f + y.z * g;
-            o[4 * e + 3] = o[4 * e + 3] * f + y.w * g;
+            o[4 * e] += y.x * g;
+            o[4 * e + 1] += y.y * g;
+            o[4 * e + 2] += y.z * g;
+            o[4 * e + 3] += y.w * g;
         }
-        m = mn;
     }
     const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
     const int tok = r / a.g, h = rec.kh * a.g + r - tok * a.g;
