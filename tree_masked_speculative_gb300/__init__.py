@@ -10,6 +10,8 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
+import threading
 from typing import NamedTuple, Optional
 
 import torch
@@ -423,51 +425,85 @@ class PagedStep(NamedTuple):
 
 _SERVE_CODE = {torch.float32: TA_F32, torch.float16: TA_F16, torch.bfloat16: TA_BF16, torch.int32: TA_I32,
                torch.int64: TA_I64}
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_this_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_BUF = "QQii"
+_ABSENT = (0, 0, TA_F32, 0)
 
 
-def _cuda_index(t: torch.Tensor) -> int:
-    if not t.is_cuda:
-        raise ValueError("tensors must be on a CUDA device, got %s" % t.device)
-    return t.get_device()
+class _Entry:
+    """A C entry point whose params struct and ta_bufs are packed into one block of
+    memory a thread: a serving step makes these calls per layer, and building the
+    ctypes objects one by one took longer than the small kernels."""
+
+    def __init__(self, name: str, params: str, n_bufs: int):
+        self.layout = struct.Struct("=" + params + _BUF * n_bufs)
+        self.offsets = [0] + [struct.calcsize("=" + params) + 24 * i for i in range(n_bufs)]
+        self.fn = ctypes.CFUNCTYPE(ctypes.c_int, *[ctypes.c_void_p] * (n_bufs + 2))((name, lib))
+        self.local = threading.local()
+
+    def __call__(self, dev: int, *values):
+        local = self.local
+        try:
+            mem, args = local.mem, local.args
+        except AttributeError:
+            mem = local.mem = ctypes.create_string_buffer(self.layout.size)
+            base = ctypes.addressof(mem)
+            args = local.args = tuple(ctypes.c_void_p(base + o) for o in self.offsets)
+        try:
+            self.layout.pack_into(mem, 0, *values)
+        except struct.error as e:
+            raise ValueError("argument out of range: %s" % e) from None
+        status = self.fn(*args, _raw_stream(dev))
+        if status != TA_OK:
+            raise TreeAttentionError(status, lib.ta_last_error().decode())
 
 
-def _current(dev: int) -> ctypes.c_void_p:
-    return ctypes.c_void_p(_raw_stream(dev) if _raw_stream is not None
-                           else torch.cuda.current_stream(dev).cuda_stream)
+_plan_entry = _Entry("paged_plan_build", "6I", 13)
+_append_entry = _Entry("paged_kv_append", "6I7Q", 5)
+_paged_entry = _Entry("paged_attn_fwd", "11If7Q", 9)
+_prompt_entry = _Entry("prompt_attn_fwd", "7If8Q", 6)
 
 
 def _as_stream(stream) -> torch.cuda.Stream:
     return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
 
 
-def _flat(t: Optional[torch.Tensor], dev: int) -> Optional[Buf]:
-    """A contiguous tensor on device `dev` as a ta_buf."""
+def _device_of(t: torch.Tensor) -> int:
+    dev = t.get_device()
+    if dev < 0 or not t.is_cuda:
+        raise ValueError("tensors must be on a CUDA device, got %s" % t.device)
+    return dev
+
+
+def _flat(t: Optional[torch.Tensor], dev: int):
+    """A contiguous tensor on device `dev` as the fields of a ta_buf."""
     if t is None:
-        return None
-    if not t.is_cuda or t.get_device() != dev:
+        return _ABSENT
+    if t.get_device() != dev:
         raise ValueError("all tensors must be on cuda:%d, got %s" % (dev, t.device))
     if not t.is_contiguous():
         raise ValueError("tensor must be contiguous")
     code = _SERVE_CODE.get(t.dtype)
     if code is None:
         raise ValueError("unsupported dtype %s" % t.dtype)
-    return Buf(t.data_ptr(), t.numel() * t.element_size(), code, 0)
+    return t.data_ptr(), t.nbytes, code, 0
 
 
 def _strided(t: torch.Tensor, dev: int, ndim: int, what: str):
-    """A tensor with any outer strides as a ta_buf and its outer strides (0 for
-    an axis of one entry, whose stride means nothing)."""
+    """A tensor with any outer strides as the fields of a ta_buf and its outer
+    strides (0 for an axis of one entry, whose stride means nothing, and for a
+    contiguous tensor)."""
     if t.dim() != ndim:
         raise ValueError("%s must have %d dimensions, got %d" % (what, ndim, t.dim()))
-    if not t.is_cuda or t.get_device() != dev:
+    if t.is_contiguous():
+        return _flat(t, dev), (0,) * (ndim - 1)
+    if t.get_device() != dev:
         raise ValueError("all tensors must be on cuda:%d, got %s" % (dev, t.device))
     code = _SERVE_CODE.get(t.dtype)
     if code is None:
         raise ValueError("unsupported dtype %s" % t.dtype)
-    es = t.element_size()
-    if t.is_contiguous():
-        return Buf(t.data_ptr(), t.numel() * es, code, 0), (0,) * (ndim - 1)
     shape, stride = t.shape, t.stride()
     if stride[-1] != 1 and shape[-1] > 1:
         raise ValueError("%s: the last dimension must be contiguous" % what)
@@ -477,12 +513,12 @@ def _strided(t: torch.Tensor, dev: int, ndim: int, what: str):
             raise ValueError("%s: a broadcast dimension is not supported" % what)
         outer.append(s if n > 1 else 0)
         extent += (n - 1) * s
-    return Buf(t.data_ptr(), extent * es if t.numel() else 0, code, 0), outer
+    return (t.data_ptr(), extent * t.element_size() if t.numel() else 0, code, 0), outer
 
 
 def _contiguous_default(strides, shape):
-    """The strides with 0 (an axis of one entry) replaced by a size that is
-    always allowed: C reads 0 as the contiguous layout's stride."""
+    """The strides with 0 (an axis of one entry) replaced by the contiguous
+    layout's, which C reads 0 as."""
     full, step = [], shape[-1]
     for n in reversed(shape[1:-1]):
         full.append(step)
@@ -490,42 +526,6 @@ def _contiguous_default(strides, shape):
     full.append(step)
     full.reverse()
     return [s or f for s, f in zip(strides, full)]
-
-
-def _ref(b: Optional[Buf]):
-    return None if b is None else ctypes.byref(b)
-
-
-def paged_plan(keep_lens: torch.Tensor, new_lens: torch.Tensor, held: torch.Tensor, block_table: torch.Tensor,
-               free_pages: torch.Tensor, n_free: torch.Tensor, *, page_size: int, max_tokens: int,
-               out=None, stream=None) -> PagedStep:
-    """Plan a step: request b keeps keep_lens[b] cached tokens and gets
-    new_lens[b] new ones (int32 [B]).  Pages it no longer needs go back to the
-    stack free_pages[:n_free], pages it needs are taken from its top; block_table
-    [B, max_pages] and free_pages are updated in place.  `out`: the seven tensors
-    of a PagedStep to write into (its held and n_free may be the inputs)."""
-    if stream is not None:
-        with torch.cuda.stream(_as_stream(stream)):
-            return paged_plan(keep_lens, new_lens, held, block_table, free_pages, n_free, page_size=page_size,
-                              max_tokens=max_tokens, out=out)
-    dev = _cuda_index(block_table)
-    if dev != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return paged_plan(keep_lens, new_lens, held, block_table, free_pages, n_free, page_size=page_size,
-                              max_tokens=max_tokens, out=out)
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [batch, max_pages]")
-    batch, width = block_table.shape
-    if out is None:
-        def new(n, dtype=torch.int32):
-            return torch.empty(n, dtype=dtype, device=block_table.device)
-        out = (new(batch), new(1), new(batch + 1), new(batch), new(max_tokens, torch.int64), new(max_tokens),
-               torch.zeros(1, dtype=torch.int32, device=block_table.device))
-    step = PagedStep(*out)
-    p = PlanParams(batch, page_size, width, free_pages.numel(), max_tokens, 0)
-    bufs = [_flat(t, dev) for t in (keep_lens, new_lens, held, block_table, free_pages, n_free) + tuple(step)]
-    _check(lib.paged_plan_build(ctypes.byref(p), *[ctypes.byref(b) for b in bufs], _current(dev)))
-    return step
 
 
 def _cache_pair(k_cache, v_cache, dev):
@@ -540,30 +540,59 @@ def _cache_pair(k_cache, v_cache, dev):
     return kb, vb, ks
 
 
+def _elsewhere(fn, dev, stream, args, kw):
+    """The call made with `stream`, or with the tensors' device, current."""
+    with torch.cuda.stream(_as_stream(stream)) if stream is not None else torch.cuda.device(dev):
+        return fn(*args, **kw)
+
+
+def paged_plan(keep_lens: torch.Tensor, new_lens: torch.Tensor, held: torch.Tensor, block_table: torch.Tensor,
+               free_pages: torch.Tensor, n_free: torch.Tensor, *, page_size: int, max_tokens: int,
+               out=None, stream=None) -> PagedStep:
+    """Plan a step: request b keeps keep_lens[b] cached tokens and gets
+    new_lens[b] new ones (int32 [B]).  Pages it no longer needs go back to the
+    stack free_pages[:n_free], pages it needs are taken from its top; block_table
+    [B, max_pages] and free_pages are updated in place.  `out`: the seven tensors
+    of a PagedStep to write into (its held and n_free may be the inputs)."""
+    dev = _device_of(block_table)
+    if stream is not None or dev != _this_device():
+        return _elsewhere(paged_plan, dev, stream, (keep_lens, new_lens, held, block_table, free_pages, n_free),
+                          dict(page_size=page_size, max_tokens=max_tokens, out=out))
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [batch, max_pages]")
+    batch, width = block_table.shape
+    if out is None:
+        def new(n, dtype=torch.int32):
+            return torch.empty(n, dtype=dtype, device=block_table.device)
+        out = (new(batch), new(1), new(batch + 1), new(batch), new(max_tokens, torch.int64), new(max_tokens),
+               torch.zeros(1, dtype=torch.int32, device=block_table.device))
+    step = PagedStep(*out)
+    _plan_entry(dev, batch, page_size, width, free_pages.numel(), max_tokens, 0, *_flat(keep_lens, dev),
+                *_flat(new_lens, dev), *_flat(held, dev), *_flat(block_table, dev), *_flat(free_pages, dev),
+                *_flat(n_free, dev), *_flat(step.held, dev), *_flat(step.n_free, dev), *_flat(step.cu_q, dev),
+                *_flat(step.kv_lens, dev), *_flat(step.slot_map, dev), *_flat(step.positions, dev),
+                *_flat(step.status, dev))
+    return step
+
+
 def paged_append(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                  slot_map: torch.Tensor, stream=None) -> None:
     """Write the rows k_new, v_new [T, Hk, D] to the slots slot_map [T] (int64) of
     the caches [n_pages, Hk, page_size, D]; slots outside the cache (-1) are
     skipped.  No two rows may have the same slot."""
-    if stream is not None:
-        with torch.cuda.stream(_as_stream(stream)):
-            return paged_append(k_new, v_new, k_cache, v_cache, slot_map)
-    dev = _cuda_index(k_cache)
-    if dev != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return paged_append(k_new, v_new, k_cache, v_cache, slot_map)
-    kn, (kt, kh) = _strided(k_new, dev, 3, "k_new")
-    vn, (vt, vh) = _strided(v_new, dev, 3, "v_new")
+    dev = _device_of(k_cache)
+    if stream is not None or dev != _this_device():
+        return _elsewhere(paged_append, dev, stream, (k_new, v_new, k_cache, v_cache, slot_map), {})
+    kn, ks = _strided(k_new, dev, 3, "k_new")
+    vn, vs = _strided(v_new, dev, 3, "v_new")
     kb, vb, cs = _cache_pair(k_cache, v_cache, dev)
     n_pages, hk, ps, d = k_cache.shape
-    t = k_new.shape[0]
-    if k_new.shape != v_new.shape or k_new.shape[1] != hk or k_new.shape[2] != d:
+    t, hn, dn = k_new.shape
+    if k_new.shape != v_new.shape or hn != hk or dn != d:
         raise ValueError("k_new and v_new must be [T, %d, %d]" % (hk, d))
     if slot_map.dim() != 1 or slot_map.shape[0] < t:
         raise ValueError("slot_map must be [T]")
-    p = AppendParams(t, hk, d, ps, n_pages, 0, kt, kh, vt, vh, cs[0], cs[1], cs[2])
-    _check(lib.paged_kv_append(ctypes.byref(p), ctypes.byref(kn), ctypes.byref(vn), ctypes.byref(kb),
-                               ctypes.byref(vb), _ref(_flat(slot_map, dev)), _current(dev)))
+    _append_entry(dev, t, hk, d, ps, n_pages, 0, *ks, *vs, *cs, *kn, *vn, *kb, *vb, *_flat(slot_map, dev))
 
 
 def paged_attn_workspace_bytes(p: PagedParams) -> int:
@@ -583,21 +612,21 @@ def _workspace(nbytes: int, device) -> torch.Tensor:
 
 
 def paged_attention_workspace(q: torch.Tensor, k_cache: torch.Tensor, block_table: torch.Tensor, *,
-                              max_q_len: int, kernel: int = KERNEL_AUTO) -> torch.Tensor:
+                              max_q_len: int, kernel: int = KERNEL_AUTO, scale: float = 1.0) -> torch.Tensor:
     """A tmp buffer for paged_attention calls of these shapes (its first 32-bit
     word, zero here, is the status word; calls that overlap must not share it)."""
     n_pages, hk, ps, d = k_cache.shape
     p = PagedParams(block_table.shape[0], q.shape[1], hk, d, q.shape[0], max_q_len, 0, ps, n_pages,
-                    block_table.shape[1], kernel, 1.0)
-    with torch.cuda.device(_cuda_index(q)):
+                    block_table.shape[1], kernel, scale)
+    with torch.cuda.device(_device_of(q)):
         return _workspace(paged_attn_workspace_bytes(p), q.device)
 
 
 def prompt_attention_workspace(q: torch.Tensor, k: torch.Tensor, cu_seqlens: torch.Tensor, *,
-                               kernel: int = KERNEL_AUTO) -> torch.Tensor:
+                               kernel: int = KERNEL_AUTO, scale: float = 1.0) -> torch.Tensor:
     """A tmp buffer for prompt_attention calls of these shapes."""
-    p = PromptParams(cu_seqlens.numel() - 1, q.shape[1], k.shape[1], q.shape[2], q.shape[0], 0, kernel, 1.0)
-    with torch.cuda.device(_cuda_index(q)):
+    p = PromptParams(cu_seqlens.numel() - 1, q.shape[1], k.shape[1], q.shape[2], q.shape[0], 0, kernel, scale)
+    with torch.cuda.device(_device_of(q)):
         return _workspace(prompt_attn_workspace_bytes(p), q.device)
 
 
@@ -613,23 +642,17 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     (int32 [T], each request's draft tree by index inside its chunk), the prefix,
     its ancestors and itself.  Returns out [T, H, D] in q's type; rows behind the
     last request are not written."""
-    if stream is not None:
-        with torch.cuda.stream(_as_stream(stream)):
-            return paged_attention(q, k_cache, v_cache, block_table, cu_q, kv_lens, scale=scale,
-                                   max_q_len=max_q_len, window=window, parents=parents, tmp=tmp, out=out,
-                                   kernel=kernel)
-    dev = _cuda_index(q)
-    if dev != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return paged_attention(q, k_cache, v_cache, block_table, cu_q, kv_lens, scale=scale,
-                                   max_q_len=max_q_len, window=window, parents=parents, tmp=tmp, out=out,
-                                   kernel=kernel)
+    dev = _device_of(q)
+    if stream is not None or dev != _this_device():
+        return _elsewhere(paged_attention, dev, stream, (q, k_cache, v_cache, block_table, cu_q, kv_lens),
+                          dict(scale=scale, max_q_len=max_q_len, window=window, parents=parents, tmp=tmp, out=out,
+                               kernel=kernel))
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     elif out.shape != q.shape:
         raise ValueError("out must have q's shape")
-    qb, (qt, qh) = _strided(q, dev, 3, "q")
-    ob, (ot, oh) = _strided(out, dev, 3, "out")
+    qb, qs = _strided(q, dev, 3, "q")
+    ob, os_ = _strided(out, dev, 3, "out")
     kb, vb, cs = _cache_pair(k_cache, v_cache, dev)
     t, h, d = q.shape
     n_pages, hk, ps, dk = k_cache.shape
@@ -637,14 +660,13 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         raise ValueError("q and the caches must have one head dimension")
     if block_table.dim() != 2 or cu_q.numel() != block_table.shape[0] + 1 or kv_lens.numel() != block_table.shape[0]:
         raise ValueError("block_table must be [batch, max_pages], cu_q [batch + 1] and kv_lens [batch]")
-    p = PagedParams(block_table.shape[0], h, hk, d, t, max_q_len, window, ps, n_pages, block_table.shape[1], kernel,
-                    scale, qt, qh, ot, oh, cs[0], cs[1], cs[2])
+    batch, width = block_table.shape
     if tmp is None:
-        tmp = _workspace(paged_attn_workspace_bytes(p), q.device)
-    _check(lib.paged_attn_fwd(ctypes.byref(p), ctypes.byref(qb), ctypes.byref(kb), ctypes.byref(vb),
-                              ctypes.byref(_flat(block_table, dev)), ctypes.byref(_flat(cu_q, dev)),
-                              ctypes.byref(_flat(kv_lens, dev)), _ref(_flat(parents, dev)),
-                              ctypes.byref(_flat(tmp, dev)), ctypes.byref(ob), _current(dev)))
+        tmp = _workspace(paged_attn_workspace_bytes(PagedParams(batch, h, hk, d, t, max_q_len, window, ps, n_pages, width,
+                                                                kernel, scale)), q.device)
+    _paged_entry(dev, batch, h, hk, d, t, max_q_len, window, ps, n_pages, width, kernel, scale, *qs, *os_, *cs, *qb, *kb,
+                 *vb, *_flat(block_table, dev), *_flat(cu_q, dev), *_flat(kv_lens, dev), *_flat(parents, dev),
+                 *_flat(tmp, dev), *ob)
     return out
 
 
@@ -656,28 +678,24 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     cu_seqlens [B + 1] int32 on the device.  Row i of a prompt sees its rows up to
     i (the last `window` of them).  Returns out [T, H, D] in q's type; rows behind
     the last prompt are not written."""
-    if stream is not None:
-        with torch.cuda.stream(_as_stream(stream)):
-            return prompt_attention(q, k, v, cu_seqlens, scale=scale, window=window, tmp=tmp, out=out, kernel=kernel)
-    dev = _cuda_index(q)
-    if dev != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return prompt_attention(q, k, v, cu_seqlens, scale=scale, window=window, tmp=tmp, out=out, kernel=kernel)
+    dev = _device_of(q)
+    if stream is not None or dev != _this_device():
+        return _elsewhere(prompt_attention, dev, stream, (q, k, v, cu_seqlens),
+                          dict(scale=scale, window=window, tmp=tmp, out=out, kernel=kernel))
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     elif out.shape != q.shape:
         raise ValueError("out must have q's shape")
-    qb, (qt, qh) = _strided(q, dev, 3, "q")
-    ob, (ot, oh) = _strided(out, dev, 3, "out")
-    kb, (kt, kh) = _strided(k, dev, 3, "k")
-    vb, (vt, vh) = _strided(v, dev, 3, "v")
+    qb, qs = _strided(q, dev, 3, "q")
+    ob, os_ = _strided(out, dev, 3, "out")
+    kb, ks = _strided(k, dev, 3, "k")
+    vb, vs = _strided(v, dev, 3, "v")
     t, h, d = q.shape
     if k.shape != v.shape or k.shape[0] != t or k.shape[2] != d:
         raise ValueError("k and v must be [%d, Hk, %d]" % (t, d))
-    p = PromptParams(cu_seqlens.numel() - 1, h, k.shape[1], d, t, window, kernel, scale, qt, qh, ot, oh, kt, kh, vt, vh)
+    batch, hk = cu_seqlens.numel() - 1, k.shape[1]
     if tmp is None:
-        tmp = _workspace(prompt_attn_workspace_bytes(p), q.device)
-    _check(lib.prompt_attn_fwd(ctypes.byref(p), ctypes.byref(qb), ctypes.byref(kb), ctypes.byref(vb),
-                               ctypes.byref(_flat(cu_seqlens, dev)), ctypes.byref(_flat(tmp, dev)),
-                               ctypes.byref(ob), _current(dev)))
+        tmp = _workspace(prompt_attn_workspace_bytes(PromptParams(max(batch, 0), h, hk, d, t, window, kernel, scale)), q.device)
+    _prompt_entry(dev, batch, h, hk, d, t, window, kernel, scale, *qs, *os_, *ks, *vs, *qb, *kb, *vb,
+                  *_flat(cu_seqlens, dev), *_flat(tmp, dev), *ob)
     return out

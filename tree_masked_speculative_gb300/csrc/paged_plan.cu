@@ -10,11 +10,13 @@
 //   slot[t]  = table[b, pos / page_size] * page_size + pos % page_size with
 //              pos = keep[b] + t - cu[b]; -1 for t >= cu[B]
 //
-// The work is a few prefix sums over the batch and 12 bytes a token, so a
-// launch's latency bounds it, not bandwidth.  One cluster does all of it in one
-// launch: every CTA scans the whole batch (cheaper than exchanging results) and
-// takes its share of rows and tokens; cluster barriers separate the phases that
-// hand pages over through memory (pushes before pops, pops before slots).
+// The work is a few prefix sums over the batch and 12 bytes a token, so latency
+// bounds it, not bandwidth.  One cluster does the batch in one launch: every CTA scans
+// all of it (cheaper than exchanging results) and takes its share of pages, a
+// (row, cell) pair a thread; cluster barriers separate the phases that hand pages over
+// through memory (pushes before pops, pops before slots).  Few tokens get their slots
+// in the same launch; many in a second one over the whole GPU (131k tokens by the 8
+// CTAs of the cluster: 32 us in all, with one warp a row and one token a thread).
 #include "seq_internal.cuh"
 #include "sm100_ptx.cuh"
 
@@ -22,6 +24,7 @@ namespace ta {
 namespace {
 
 constexpr int kThreads = 512;
+constexpr int kTokensHere = 4096;       // up to this many tokens get their slots in the planning launch
 constexpr int kWarps = kThreads / 32;
 
 struct Sums {
@@ -102,24 +105,30 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const PlanArgs a) 
     // every CTA has read held and n_free: the outputs may be the inputs' memory
     sm100::cluster_sync();
     const int top = n_free + run.back;
-    const int warp = (tid >> 5) * nr + rank, lane = tid & 31, nw = kWarps * nr;
+    const int me = rank * kThreads + tid, all = nr * kThreads;
+    // the last row whose exclusive sum is at most k: the row of page (or token) k
+    auto row_of = [&](const int *sums, int k) {
+        int lo = 0, hi = a.B;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (sums[mid] <= k) lo = mid; else hi = mid;
+        }
+        return lo;
+    };
+    auto need_of = [&](int b) { return static_cast<int>((static_cast<long long>(a.keep[b]) + a.fresh[b] + ps - 1) >> a.page_shift); };
     if (!bad && run.back > 0) {
-        for (int b = warp; b < a.B; b += nw) {
-            const int n = s_back[b + 1] - s_back[b];
-            if (n == 0) continue;
-            const int need = static_cast<int>((static_cast<long long>(a.keep[b]) + a.fresh[b] + ps - 1) >> a.page_shift);
-            for (int j = lane; j < n; j += 32)
-                a.stack[n_free + s_back[b] + j] = a.table[static_cast<long long>(b) * a.max_pages + need + j];
+#pragma unroll 4
+        for (int k = me; k < run.back; k += all) {
+            const int b = row_of(s_back, k);
+            a.stack[n_free + k] = a.table[static_cast<long long>(b) * a.max_pages + need_of(b) + k - s_back[b]];
         }
         sm100::cluster_sync();
     }
     if (!bad) {
-        for (int b = warp; b < a.B; b += nw) {
-            const int n = s_grow[b + 1] - s_grow[b];
-            if (n == 0) continue;
-            const int need = static_cast<int>((static_cast<long long>(a.keep[b]) + a.fresh[b] + ps - 1) >> a.page_shift);
-            for (int j = lane; j < n; j += 32)
-                a.table[static_cast<long long>(b) * a.max_pages + need - n + j] = a.stack[top - 1 - s_grow[b] - j];
+#pragma unroll 4
+        for (int k = me; k < run.grow; k += all) {
+            const int b = row_of(s_grow, k);
+            a.table[static_cast<long long>(b) * a.max_pages + need_of(b) - (s_grow[b + 1] - k)] = a.stack[top - 1 - k];
         }
     }
     sm100::cluster_sync();
@@ -136,22 +145,77 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const PlanArgs a) 
         *a.n_free_out = bad ? n_free : top - run.grow;
         if (bad) atomicOr(a.status, bad);
     }
+    if (a.max_tokens > kTokensHere) return;             // the slots are the next launch's
     const int total = s_cu[a.B];
-    for (int t = rank * kThreads + tid; t < a.max_tokens; t += nr * kThreads) {
+    for (int t = me; t < a.max_tokens; t += all) {
         long long slot = -1;
         int pos = -1;
         if (t < total) {
-            int lo = 0, hi = a.B;
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (s_cu[mid] <= t) lo = mid; else hi = mid;
-            }
-            pos = a.keep[lo] + t - s_cu[lo];
-            slot = (static_cast<long long>(a.table[static_cast<long long>(lo) * a.max_pages + (pos >> a.page_shift)])
+            const int b = row_of(s_cu, t);
+            pos = a.keep[b] + t - s_cu[b];
+            slot = (static_cast<long long>(a.table[static_cast<long long>(b) * a.max_pages + (pos >> a.page_shift)])
                     << a.page_shift) + (pos & (ps - 1));
         }
         a.slot[t] = slot;
         a.pos[t] = pos;
+    }
+}
+
+// Slots and positions of 4 consecutive tokens a thread, from the row offsets and
+// tables that the first kernel has written.
+constexpr int kSlotThreads = 256, kSlotTokens = 4, kSlotRows = 2048;
+__global__ void __launch_bounds__(kSlotThreads) paged_slots_kernel(const PlanArgs a) {
+    __shared__ int s_cu[kSlotRows + 1];
+    pdl_wait();
+    const bool here = a.B <= kSlotRows;
+    if (here) {
+        for (int i = threadIdx.x; i <= a.B; i += kSlotThreads) s_cu[i] = a.cu[i];
+        __syncthreads();
+    }
+    const int *cu = here ? s_cu : a.cu;
+    const int t0 = (blockIdx.x * kSlotThreads + threadIdx.x) * kSlotTokens;
+    if (t0 >= a.max_tokens) return;
+    const int total = cu[a.B], mask = (1 << a.page_shift) - 1;
+    int lo = 0, hi = a.B;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cu[mid] <= t0) lo = mid; else hi = mid;
+    }
+    long long slot[kSlotTokens];
+    int pos[kSlotTokens];
+    int row = -1, cell = -1, page = 0, keep = 0, first = 0, end = cu[lo + 1];
+#pragma unroll
+    for (int i = 0; i < kSlotTokens; ++i) {
+        const int t = t0 + i;
+        slot[i] = -1;
+        pos[i] = -1;
+        if (t >= total) continue;
+        while (t >= end) end = cu[++lo + 1];            // ends: t < total = cu[B]
+        if (lo != row) {
+            row = lo;
+            keep = a.keep[row];
+            first = cu[row];
+            cell = -1;
+        }
+        pos[i] = keep + t - first;
+        if ((pos[i] >> a.page_shift) != cell) {
+            cell = pos[i] >> a.page_shift;
+            page = a.table[static_cast<long long>(row) * a.max_pages + cell];
+        }
+        slot[i] = (static_cast<long long>(page) << a.page_shift) + (pos[i] & mask);
+    }
+    const bool wide = t0 + kSlotTokens <= a.max_tokens && ((reinterpret_cast<uintptr_t>(a.slot) | reinterpret_cast<uintptr_t>(a.pos)) & 15) == 0;
+    if (wide) {
+        *reinterpret_cast<longlong2 *>(a.slot + t0) = make_longlong2(slot[0], slot[1]);
+        *reinterpret_cast<longlong2 *>(a.slot + t0 + 2) = make_longlong2(slot[2], slot[3]);
+        *reinterpret_cast<int4 *>(a.pos + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kSlotTokens; ++i)
+            if (t0 + i < a.max_tokens) {
+                a.slot[t0 + i] = slot[i];
+                a.pos[t0 + i] = pos[i];
+            }
     }
 }
 
@@ -165,8 +229,12 @@ cudaError_t launch_paged_plan(const PlanArgs &a, cudaStream_t s) {
         if (e != cudaSuccess) return e;
     }
     // one CTA where it holds the batch and the tokens in one sweep; else 8
-    const unsigned ctas = a.B <= kThreads && a.max_tokens <= kThreads ? 1 : 8;
-    const cudaError_t e = launch_pdl_cluster(paged_plan_kernel, dim3(ctas), dim3(kThreads), smem, s, ctas, 1u, a);
+    const unsigned ctas = a.B <= kThreads / 2 && a.max_tokens <= kThreads ? 1 : 8;
+    cudaError_t e = launch_pdl_cluster(paged_plan_kernel, dim3(ctas), dim3(kThreads), smem, s, ctas, 1u, a);
+    count_launch();
+    if (e != cudaSuccess || a.max_tokens <= kTokensHere) return e;
+    const unsigned blocks = (static_cast<unsigned>(a.max_tokens) + kSlotThreads * kSlotTokens - 1) / (kSlotThreads * kSlotTokens);
+    e = launch_pdl(paged_slots_kernel, dim3(blocks), dim3(kSlotThreads), 0, s, a);
     count_launch();
     return e;
 }
