@@ -155,7 +155,7 @@ uint64_t prompt_workspace(const ta_prompt_params *p) {
 
 bool encode_16bit(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap *m, const SeqArgs &a, const void *ptr, int rank,
                   const cuuint64_t *dims, const cuuint64_t *str, const cuuint32_t *box) {
-    const cuuint32_t es[4] = {1, 1, 1, 1};
+    const cuuint32_t es[5] = {1, 1, 1, 1, 1};
     return encode(m, a.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
                   const_cast<void *>(ptr), dims, str, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -169,21 +169,18 @@ bool q_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap *m, const SeqAr
     return encode_16bit(encode, m, a, a.q, 3, dims, str, box);
 }
 
-// Tensor map of K or V: {D, page_size, Hk, n_pages} (paged) or {D, T, Hk}.
+// Tensor map of K or V: {64, page_size, D / 64, Hk, n_pages} (paged) or {64, T, D / 64, Hk};
+// a box holds `slabs` 64-column slabs.
 bool kv_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap *m, const SeqArgs &a, const void *ptr, long long st,
-            long long sh) {
-    const cuuint64_t ps = cuuint64_t(1) << a.page_shift;
-    const cuuint32_t tk = kSeqTcTileKeys;
-    cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.D), ps, static_cast<cuuint64_t>(a.Hk), static_cast<cuuint64_t>(a.n_pages)};
-    const cuuint64_t str[3] = {static_cast<cuuint64_t>(st) * 2, static_cast<cuuint64_t>(sh) * 2, static_cast<cuuint64_t>(a.k_sp) * 2};
-    cuuint32_t box[4] = {64, static_cast<cuuint32_t>(ps < tk ? ps : tk), 1, 1};
-    int rank = 4;
-    if (a.kv_lens == nullptr) {
-        dims[1] = static_cast<cuuint64_t>(a.T);
-        box[1] = tk;
-        rank = 3;
-    }
-    return encode_16bit(encode, m, a, ptr, rank, dims, str, box);
+            long long sh, bool is_v) {
+    const bool paged = a.kv_lens != nullptr;
+    const cuuint64_t rows = paged ? cuuint64_t(1) << a.page_shift : static_cast<cuuint64_t>(a.T);
+    const cuuint64_t slabs = static_cast<cuuint64_t>(a.D) / 64;
+    const cuuint64_t dims[5] = {64, rows, slabs, static_cast<cuuint64_t>(a.Hk), static_cast<cuuint64_t>(a.n_pages)};
+    const cuuint64_t str[4] = {static_cast<cuuint64_t>(st) * 2, 128, static_cast<cuuint64_t>(sh) * 2, static_cast<cuuint64_t>(a.k_sp) * 2};
+    const cuuint32_t box_rows = paged && rows < kSeqTcTileKeys ? static_cast<cuuint32_t>(rows) : kSeqTcTileKeys;
+    const cuuint32_t box[5] = {64, box_rows, is_v || box_rows == kSeqTcTileKeys ? static_cast<cuuint32_t>(slabs) : 1, 1, 1};
+    return encode_16bit(encode, m, a, ptr, paged ? 5 : 4, dims, str, box);
 }
 
 ta_status run_seq(const char *op, const SeqArgs &a, int family, void *ws, cudaStream_t s) {
@@ -198,7 +195,8 @@ ta_status run_seq(const char *op, const SeqArgs &a, int family, void *ws, cudaSt
         pl.ws = ws;
         const auto encode = tensor_map_encoder();
         if (encode == nullptr) SEQ_FAIL(TA_ERR_CUDA, "%s: cuTensorMapEncodeTiled is not available", op);
-        if (!q_map(encode, &pl.q, a) || !kv_map(encode, &pl.k, a, a.k, a.k_st, a.k_sh) || !kv_map(encode, &pl.v, a, a.v, a.v_st, a.v_sh))
+        if (!q_map(encode, &pl.q, a) || !kv_map(encode, &pl.k, a, a.k, a.k_st, a.k_sh, false) ||
+            !kv_map(encode, &pl.v, a, a.v, a.v_st, a.v_sh, true))
             SEQ_FAIL(TA_ERR_CUDA, "%s: TMA descriptor encoding failed", op);
         e = a.D == 64 ? launch_seq_tc64(a, pl, s) : a.D == 128 ? launch_seq_tc128(a, pl, s) : launch_seq_tc256(a, pl, s);
     }

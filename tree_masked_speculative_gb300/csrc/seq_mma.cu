@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D, RH>) seq_mma_kernel(co
     extern __shared__ __align__(16) float s_o[];        // [kWarps][RR][D]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3, cta = blockIdx.x;
     pdl_wait();
-    const SeqRun run = seq_schedule<kThreads, kTks>(a, a.max_q, cta, ar.G, &sched);
+    const SeqRun run = seq_schedule<kThreads, kTks, 0>(a, a.max_q, cta, ar.G, &sched);
     pdl_launch_dependents();
     if (tid == 0) {
         ar.rec[cta] = {0, 0, 0, 0};
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D, RH>) seq_mma_kernel(co
     __syncthreads();
     const float scale2 = fmaxf(a.scale * kLog2e, FLT_MIN);   // above 0: a masked -inf stays -inf
     const uint16_t *kc = static_cast<const uint16_t *>(a.k), *vc = static_cast<const uint16_t *>(a.v);
-    SeqWalk<kTks> walk;
+    SeqWalk<kTks, 0> walk;
     walk.init(a, a.max_q, run, &sched, cta);
     SeqPiece p;
     while (walk.next(a, a.max_q, run, &p)) {

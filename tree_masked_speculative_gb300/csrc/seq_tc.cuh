@@ -3,19 +3,22 @@
 //
 // Rows of a unit are (token, query head) pairs of one KV head, so grouped heads
 // share every K/V tile.  For D <= 128 a unit has 256 rows in two streams of 128, for
-// D = 256 it has 128 rows in one.  Key tiles are 64 wide, and each stream has S in two
-// TMEM buffers, so Q K^T of the next tile runs while the softmax warps work on this
-// one: they never wait for a product (with 128-key tiles and one buffer the chain
-// Q K^T, softmax, P V of a stream took 3500 cycles, against 2048 of products of both).
-// S is taken from TMEM by one thread a row, P overwrites it there as one 16-bit term
-// (its rounding is the size of the output's own) and P V accumulates in f32.
+// D = 256 it has 128 rows in one.  S = Q K^T of a 64-key tile is taken from TMEM into
+// registers by one thread a row, which frees it at once: Q K^T of the next tile runs
+// while the softmax warps work on this one.  P goes to TMEM columns of its own, as one
+// 16-bit term (its rounding is the size of the output's own), and P V accumulates in
+// f32.  (With P over S in two buffers of S, Q K^T waited for the P V two tiles back:
+// 1820 cycles a tile against 1280 of products; with 128-key tiles and one buffer, 4200
+// against 2048.)
 //
-//   warp 0      schedule and TMA producer: Q of a unit, K and V tiles through rings
+//   warp 0      schedule and TMA producer: Q of a unit, K tiles through a ring
+//   warp 6      TMA producer of V tiles (one producer for both held K back until V's
+//               slot was free: Q K^T could not run ahead)
 //   warps 1, 2  issue Q K^T and P V of stream 0; warps 4, 5 of stream 1.  Four issuing
 //               threads: the tensor core's queue is short, so it idles while a thread
 //               that has just issued its products waits on barriers and commits (two
 //               threads for both streams: 2240 cycles a tile, of them 1280 of products)
-//   warp 3      V guard: before a V tile that not every row sees in full is used,
+//   warps 3, 7  V guard: before a V tile that not every row sees in full is used,
 //               rows past the last key are zeroed and elements that are not finite
 //               are taken out (0 x NaN would reach rows that do not see them); the
 //               rows that do see such an element get NaN in its column at the end
@@ -40,8 +43,13 @@ struct Cfg {
     static constexpr int TK = 1 << TKS;                 // keys per tile
     static constexpr int NSTR = D == 256 ? 1 : 2;       // row streams
     static constexpr int ROWS = 128 * NSTR;
-    static constexpr int SW = 4 * NSTR;                 // first softmax warp
-    static constexpr int THREADS = 256 * NSTR;
+    // TMEM, 512 columns: per stream NS buffers of S (64 columns), NP of P (32), and O
+    static constexpr int NS = D == 128 ? 1 : 2, NP = 2;
+    static constexpr int CS = 64 * NS + 32 * NP;        // S and P columns of a stream
+    static constexpr int CO = NSTR * CS;                // first column of O
+    static_assert(CO + NSTR * D <= 512, "TMEM");
+    static constexpr int SW = 8;                        // first softmax warp
+    static constexpr int THREADS = 32 * SW + 128 * NSTR;
     static constexpr int SLABS = D / 64;                // 64-column slabs of a tile
     static constexpr int SLAB = TK * 128;               // bytes of a K / V slab
     static constexpr int QSLAB = ROWS * 128;            // bytes of a Q slab
@@ -55,6 +63,7 @@ struct Cfg {
 };
 
 constexpr int kPieces = 4;
+constexpr int kUnitCost = 5;      // of the schedule: a unit's start and end take as long as 5 key tiles
 // The guard is at most kPieces + 2 pieces ahead of an epilogue (a piece is published
 // once every reader has fetched the one kPieces before it, and an epilogue runs
 // right after the next fetch), so a ring of 8 marks is never overrun.
@@ -64,13 +73,13 @@ constexpr float kSlack = 8.0f;
 
 struct Misc {
     uint64_t k_full[4], k_empty[4], v_full[4], v_ready[4], v_empty[4];
-    uint64_t q_full, q_empty, s_full[2][2], p_full[2][2], o_done[2][2], o_free[2];   // stream, S buffer
+    uint64_t q_full, q_empty, s_full[2][2], s_free[2][2], p_full[2][2], o_done[2][2], o_free[2];   // stream, S or P buffer
     uint64_t piece_full[kPieces], piece_empty[kPieces];
-    uint64_t drain[4];
+    uint64_t drain[4], guard;         // guard: both guard warps have looked at a masked tile
+    int found[2][2];                  // masked tile parity, guard warp
     SeqPiece piece[kPieces];
     SeqScratch sched;
     uint32_t tmem_base;
-    volatile int abort_flag;
     int poisoned[kPoison];            // piece n % kPoison: some row has a poisoned column
 };
 constexpr int kMiscBytes = 3000;
@@ -88,7 +97,11 @@ struct Args {
 };
 struct Maps {
     CUtensorMap q;        // {D, H, T}, box {64, g, tokens of a unit}: rows (token, head) as they stand in a unit
-    CUtensorMap k, v;     // paged: {D, page, Hk, pages}; packed: {D, T, Hk}; 64-column boxes, 128-byte swizzle
+    // {64, tokens, D / 64, Hk, pages} (packed: no last axis), 128-byte swizzle.  A box is
+    // a whole 64-key tile where a page holds one; of smaller pages V comes a page at a
+    // time and K a page and 64 columns at a time.  (A box costs about 0.15 us of the copy
+    // engine whatever its size: eight 8 KB boxes a tile held D = 256 at 3200 cycles a tile.)
+    CUtensorMap k, v;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -140,20 +153,30 @@ __device__ __forceinline__ uint32_t odd16(uint32_t w) {
     return BF16 ? (w & 0x7f807f80u) + 0x00800080u : (w & 0x7c007c00u) + 0x04000400u;
 }
 
-static __device__ __noinline__ bool give_up(Misc *m, int *status) {
-    m->abort_flag = 1;
-    atomicOr(status, kSeqTimeout);
-    return false;
+// Wait for a phase, about 2 s at most; false: given up.  Six instructions and no call:
+// the instruction cache holds the loops of all roles only while they are small (the
+// same kernel with 100 bytes more a wait took 1.25 times as long), and a call would
+// spill what the softmax warps hold.
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+        "mov.u32 n, 0;\n\t"
+        "L:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
+        "@p bra.uni D;\n\t"
+        "add.u32 n, n, 1;\n\t"
+        "setp.lt.u32 q, n, 2097152;\n\t"
+        "@q bra.uni L;\n\t"
+        "D:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity & 1u)
+        : "memory");
+    return ok != 0;
 }
-__device__ __forceinline__ bool wait_or_abort(Misc *m, uint64_t *bar, uint32_t parity, int *status) {
-    if (mbar_try_wait(bar, parity)) return true;
-#pragma unroll 1
-    for (uint32_t i = 0; i < (1u << 21); ++i) {         // about 2 s
-        if (mbar_try_wait_sleep(bar, parity, 1000)) return true;
-        if (m->abort_flag) return false;
-    }
-    return give_up(m, status);
-}
+// The same for a whole warp, one outcome.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_bar(bar, parity)) != 0; }
 
 // Registers of this warpgroup's threads from here on (the block's sum stays what
 // it was launched with).
@@ -191,12 +214,26 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, u
         "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
         : "memory");
 }
+__device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z, int w, int v) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v)
+        : "memory");
+}
+
+// Byte offset of (64-column slab, key row) of a V tile: `bk` rows a box, the slabs of a
+// box one behind the other.
+template <int D>
+__device__ __forceinline__ int v_offset(int bk, int slab, int row) {
+    return (row & ~(bk - 1)) * (Cfg<D>::SLABS * 128) + slab * bk * 128 + (row & (bk - 1)) * 128;
+}
 
 // One warp: mark the rows that see an element of this V tile that is not finite
 // (bit d of a row's marks), and take the element out.
 template <int D, bool BF16>
-__device__ __noinline__ void mark_odd(const SeqArgs &a, const SeqPiece &p, int k0, int live, unsigned char *v, uint32_t *poison,
-                                      bool clear) {
+__device__ __noinline__ void mark_odd(const SeqArgs &a, const SeqPiece &p, int k0, int live, int bk, unsigned char *v,
+                                      uint32_t *poison, bool clear) {
     using C = Cfg<D>;
     const int lane = threadIdx.x & 31;
     if (clear)
@@ -208,7 +245,7 @@ __device__ __noinline__ void mark_odd(const SeqArgs &a, const SeqPiece &p, int k
         for (int c = lane; c < D / 2; c += 32) {
             // column pair c of key row r, at its swizzled place
             const int s = c >> 5, ch = (c & 31) >> 2;
-            uint32_t *x = reinterpret_cast<uint32_t *>(v + s * C::SLAB + r * 128 + ((ch ^ (r & 7)) << 4)) + (c & 3);
+            uint32_t *x = reinterpret_cast<uint32_t *>(v + v_offset<D>(bk, s, r) + ((ch ^ (r & 7)) << 4)) + (c & 3);
             const uint32_t odd = odd16<BF16>(*x) & 0x80008000u;
             if (odd == 0u) continue;
             const uint32_t bits = ((odd >> 15) & 1u) << ((2 * c) & 31) | (odd >> 31) << ((2 * c + 1) & 31);
@@ -227,10 +264,20 @@ __device__ __noinline__ void mark_odd(const SeqArgs &a, const SeqPiece &p, int k
     __syncwarp();
 }
 
+// The larger magnitudes, NaN if either is one: a running check for values that are
+// not finite, one instruction a pair.
+template <bool BF16>
+__device__ __forceinline__ uint32_t max_abs(uint32_t acc, uint32_t w) {
+    uint32_t r;
+    if constexpr (BF16) asm("{\n\t.reg .b32 a;\n\tabs.bf16x2 a, %2;\n\tmax.NaN.bf16x2 %0, %1, a;\n\t}" : "=r"(r) : "r"(acc), "r"(w));
+    else asm("{\n\t.reg .b32 a;\n\tabs.f16x2 a, %2;\n\tmax.NaN.f16x2 %0, %1, a;\n\t}" : "=r"(r) : "r"(acc), "r"(w));
+    return r;
+}
+
 template <int D, bool PAGED, bool BF16>
 __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args ar, const __grid_constant__ Maps maps) {
     using C = Cfg<D>;
-    constexpr int TK = C::TK, TKS = C::TKS, NSTR = C::NSTR, NK = C::NK, NV = C::NV, ROWS = C::ROWS;
+    constexpr int TK = C::TK, TKS = C::TKS, NSTR = C::NSTR, NK = C::NK, NV = C::NV, NS = C::NS, NP = C::NP, ROWS = C::ROWS;
     extern __shared__ __align__(1024) unsigned char sm[];
     const SeqArgs &a = ar.a;
     if ((smem_u32(sm) & 1023u) != 0) {                  // swizzled tiles need it; the same in every CTA
@@ -239,20 +286,22 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
     }
     Misc *mi = reinterpret_cast<Misc *>(sm + C::OFF_MISC);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
-    // arrivals on a piece's empty slot: issuers, guard, softmax warps
-    constexpr int kReaders = 2 * NSTR + 1 + 4 * NSTR;
+    // arrivals on a piece's empty slot: issuers, guards, V producer, softmax warps
+    constexpr int kReaders = 2 * NSTR + 3 + 4 * NSTR;
     if (tid == 0) {
         for (int i = 0; i < NK; ++i) { mbar_init(&mi->k_full[i], 1); mbar_init(&mi->k_empty[i], NSTR); }
         for (int i = 0; i < NV; ++i) {
             mbar_init(&mi->v_full[i], 1);
-            mbar_init(&mi->v_ready[i], 1);
+            mbar_init(&mi->v_ready[i], 2);
             mbar_init(&mi->v_empty[i], NSTR);
         }
         mbar_init(&mi->q_full, 1);
+        mbar_init(&mi->guard, 2);
         mbar_init(&mi->q_empty, NSTR);
         for (int i = 0; i < 2; ++i) {
             for (int j = 0; j < 2; ++j) {
                 mbar_init(&mi->s_full[i][j], 1);
+                mbar_init(&mi->s_free[i][j], 4);
                 mbar_init(&mi->p_full[i][j], 4);
                 mbar_init(&mi->o_done[i][j], 1);
             }
@@ -261,7 +310,6 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
             mbar_init(&mi->drain[2 * i + 1], 1);
         }
         for (int i = 0; i < kPieces; ++i) { mbar_init(&mi->piece_full[i], 1); mbar_init(&mi->piece_empty[i], kReaders); }
-        mi->abort_flag = 0;
         for (int i = 0; i < kPoison; ++i) mi->poisoned[i] = 0;
         fence_mbar_init();
     }
@@ -275,22 +323,41 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
         tma_prefetch_desc(&maps.v);
     }
     pdl_wait();
-    const SeqRun run = seq_schedule<C::THREADS, TKS>(a, ar.tpt, cta, ar.G, &mi->sched);
+    const SeqRun run = seq_schedule<C::THREADS, TKS, kUnitCost>(a, ar.tpt, cta, ar.G, &mi->sched);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     pdl_launch_dependents();
     const uint32_t tmem = mi->tmem_base;
-    const uint32_t tm_o0 = tmem + 256;
+    const uint32_t tm_o0 = tmem + C::CO;
+
+    // Boxes of bk keys; of a part tile K's are 64 columns wide: lanes 0 .. k_boxes - 1 issue
+    // one each (V: lanes 0 .. per_slab - 1).
+    const int bk = PAGED ? min(TK, 1 << a.page_shift) : TK, per_slab = TK / bk;          // 1, 2 or 4 boxes
+    const int box = lane & (per_slab - 1), slab = bk == TK ? 0 : lane / per_slab, k_boxes = bk == TK ? 1 : per_slab * C::SLABS;
+    // page of this lane's box of key tile t (n_pages: out of range, read as zeros)
+    auto page_of = [&](const SeqPiece &p, int t) -> int {
+        if constexpr (!PAGED) return 0;
+        const int key = (t << TKS) + box * bk;
+        if (key >= p.kv) return a.n_pages;
+        const int g = __ldg(a.table + static_cast<long long>(p.b) * a.max_pages + (key >> a.page_shift));
+        if (g >= 0 && g < a.n_pages) return g;
+        if (lane < per_slab) atomicOr(a.status, kSeqBadPage);
+        return a.n_pages;
+    };
 
     // The next piece, in order; a reader's warp-wide copy.
     int piece_n = 0;
+    bool failed = false;                                // a wait of this warp gave up
     auto fetch = [&](SeqPiece *p) -> bool {
         const int i = piece_n % kPieces;
-        bool ok = wait_or_abort(mi, &mi->piece_full[i], static_cast<uint32_t>(piece_n / kPieces) & 1u, a.status);
-        ok = __all_sync(0xffffffffu, ok);
+        const bool ok = warp_wait(&mi->piece_full[i], piece_n / kPieces);
         ++piece_n;
-        if (!ok) { p->valid = 0; return false; }
+        if (!ok) {                                      // gave up
+            p->valid = 0;
+            failed = true;
+            return false;
+        }
         *p = mi->piece[i];
         __syncwarp();
         if (lane == 0) mbar_arrive(&mi->piece_empty[i]);
@@ -304,9 +371,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
     if constexpr (NSTR == 2) regs_down<88>();
     if (warp == 0) {
         // ------------------------------------------------- schedule, TMA producer
-        SeqWalk<TKS> walk;
+        SeqWalk<TKS, kUnitCost> walk;
         walk.init(a, ar.tpt, run, &mi->sched, cta);
-        int n = 0, kn = 0, vn = 0, qn = 0;              // pieces, K tiles, V tiles, Q tiles so far
+        int n = 0, kn = 0, qn = 0;                      // pieces, K tiles, Q tiles so far
         bool ok = true;
         if (lane == 0) ar.ws.rec[cta] = {0, 0, 0, 0};
 #pragma unroll 1
@@ -316,8 +383,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
             const bool more = walk.next(a, ar.tpt, run, &p);
             const int i = n % kPieces;
             if (n >= kPieces)
-                ok = __all_sync(0xffffffffu, wait_or_abort(mi, &mi->piece_empty[i],
-                                                           static_cast<uint32_t>(n / kPieces - 1) & 1u, a.status));
+                ok = warp_wait(&mi->piece_empty[i], n / kPieces - 1);
             if (!ok) break;
             if (lane == 0) {
                 mi->piece[i] = p;
@@ -327,49 +393,25 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
             }
             __syncwarp();
             if (!more) break;
-            // a tile = SLABS boxes per page (or per tile); lanes 0 .. boxes-1 issue one each
-            const int bk = PAGED ? min(TK, 1 << a.page_shift) : TK;       // keys per box
-            const int per_slab = TK / bk;
-            const int box = lane % per_slab, slab = lane / per_slab;       // per_slab: a power of two, at most 8
-            auto load = [&](const CUtensorMap *map, unsigned char *dst, uint64_t *bar, int page, int key) {
-                for (int s = slab; s < C::SLABS; s += 32 / per_slab) {
-                    unsigned char *d = dst + s * C::SLAB + box * bk * 128;
-                    if constexpr (PAGED) {
-                        tma_load_4d(d, map, bar, s * 64, key & ((1 << a.page_shift) - 1), p.kh, page);
-                    } else if (lane < C::SLABS) {
-                        tma_load_3d(d, map, bar, s * 64, p.q0 + key, p.kh);
-                    }
-                }
-            };
-            // page of this lane's box of tile t (n_pages: out of range, read as zeros)
-            auto page_of = [&](int t) -> int {
-                if constexpr (!PAGED) return 0;
-                const int key = (t << TKS) + box * bk;
-                if (key >= p.kv) return a.n_pages;
-                const int g = __ldg(a.table + static_cast<long long>(p.b) * a.max_pages + (key >> a.page_shift));
-                if (g >= 0 && g < a.n_pages) return g;
-                if (slab == 0) atomicOr(a.status, kSeqBadPage);
-                return a.n_pages;
-            };
-            int page = page_of(p.t0);
+            int page = page_of(p, p.t0);
 #pragma unroll 1
             for (int t = 0; t < p.nt; ++t) {
-                const int next = t + 1 < p.nt ? page_of(p.t0 + t + 1) : 0;
+                const int next = t + 1 < p.nt ? page_of(p, p.t0 + t + 1) : 0;
                 const int key = ((p.t0 + t) << TKS) + box * bk;
-                // K and V of a tile together: V of tile t is then on its way while Q K^T of
-                // tile t - 1 still holds its K stage
-                const int sk = kn % NK;
-                ok = wait_or_abort(mi, &mi->k_empty[sk], (static_cast<uint32_t>(kn / NK) & 1u) ^ 1u, a.status);
-                ok = __all_sync(0xffffffffu, ok);
+                const int st = kn % NK;
+                ok = warp_wait(&mi->k_empty[st], (static_cast<uint32_t>(kn / NK) & 1u) ^ 1u);
                 if (!ok) break;
-                if (lane == 0) mbar_arrive_expect_tx(&mi->k_full[sk], C::STAGE);
+                if (lane == 0) mbar_arrive_expect_tx(&mi->k_full[st], C::STAGE);
                 __syncwarp();
-                load(&maps.k, sm + C::OFF_K + sk * C::STAGE, &mi->k_full[sk], page, key);
+                if (lane < k_boxes) {
+                    unsigned char *d = sm + C::OFF_K + st * C::STAGE + slab * C::SLAB + box * bk * 128;
+                    if constexpr (PAGED) tma_load_5d(d, &maps.k, &mi->k_full[st], 0, key & ((1 << a.page_shift) - 1), slab, p.kh, page);
+                    else tma_load_4d(d, &maps.k, &mi->k_full[st], 0, p.q0 + key, 0, p.kh);
+                }
                 ++kn;
                 if (t == 0) {
                     // the unit's rows of Q, once the products of the piece before have read theirs
-                    if (n > 0) ok = wait_or_abort(mi, &mi->q_empty, static_cast<uint32_t>(n - 1) & 1u, a.status);
-                    ok = __all_sync(0xffffffffu, ok);
+                    if (n > 0) ok = warp_wait(&mi->q_empty, n - 1);
                     if (!ok) break;
                     if (lane == 0) {
                         mbar_arrive_expect_tx(&mi->q_full, C::SLABS * ar.tpt * a.g * 128);
@@ -379,39 +421,61 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                     }
                     __syncwarp();
                 }
-                const int sv = vn % NV;
-                ok = wait_or_abort(mi, &mi->v_empty[sv], (static_cast<uint32_t>(vn / NV) & 1u) ^ 1u, a.status);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                if (lane == 0) mbar_arrive_expect_tx(&mi->v_full[sv], C::STAGE);
-                __syncwarp();
-                load(&maps.v, sm + C::OFF_V + sv * C::STAGE, &mi->v_full[sv], page, key);
-                ++vn;
                 page = next;
             }
             if (!ok) break;
         }
-        // Drain: every copy issued has landed before the CTA's memory goes.
+        failed = !ok;
+        // every copy issued has landed before the CTA's memory goes
         if (lane == 0) {
             if (qn > 0 && !mbar_wait_sleep(&mi->q_full, static_cast<uint32_t>(qn - 1) & 1u, 1u << 21, 1000))
                 atomicOr(a.status, kSeqTimeout);
             for (int i = max(0, kn - NK); i < kn; ++i)
                 if (!mbar_wait_sleep(&mi->k_full[i % NK], static_cast<uint32_t>(i / NK) & 1u, 1u << 21, 1000))
                     atomicOr(a.status, kSeqTimeout);
+        }
+    } else if (warp == 6) {
+        // ------------------------------------------------------------- V producer
+        int vn = 0;
+        bool ok = true;
+        SeqPiece p;
+#pragma unroll 1
+        while (ok && fetch(&p)) {
+            int page = page_of(p, p.t0);
+#pragma unroll 1
+            for (int t = 0; t < p.nt; ++t) {
+                const int next = t + 1 < p.nt ? page_of(p, p.t0 + t + 1) : 0;
+                const int key = ((p.t0 + t) << TKS) + box * bk;
+                const int st = vn % NV;
+                ok = warp_wait(&mi->v_empty[st], (static_cast<uint32_t>(vn / NV) & 1u) ^ 1u);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(&mi->v_full[st], C::STAGE);
+                __syncwarp();
+                if (lane < per_slab) {
+                    unsigned char *d = sm + C::OFF_V + st * C::STAGE + box * bk * (C::SLABS * 128);
+                    if constexpr (PAGED) tma_load_5d(d, &maps.v, &mi->v_full[st], 0, key & ((1 << a.page_shift) - 1), 0, p.kh, page);
+                    else tma_load_4d(d, &maps.v, &mi->v_full[st], 0, p.q0 + key, 0, p.kh);
+                }
+                ++vn;
+                page = next;
+            }
+        }
+        failed |= !ok;
+        if (lane == 0)
             for (int i = max(0, vn - NV); i < vn; ++i)
                 if (!mbar_wait_sleep(&mi->v_full[i % NV], static_cast<uint32_t>(i / NV) & 1u, 1u << 21, 1000))
                     atomicOr(a.status, kSeqTimeout);
-        }
-    } else if (warp == 1 || warp == 2 || warp == 4 || warp == 5) {
+    } else if (warp == 1 || warp == 2 || (NSTR == 2 && (warp == 4 || warp == 5))) {
         // ------------------------------------------------------------ MMA issuers
         const int x = warp >> 2, w = warp - (x ? 4 : 1);   // stream; 0: Q K^T, 1: P V
         const uint32_t q_addr = smem_u32(sm + C::OFF_Q), k_addr = smem_u32(sm + C::OFF_K), v_addr = smem_u32(sm + C::OFF_V);
         constexpr uint32_t id_qk = idesc_f16(128, TK, BF16 ? 1 : 0, 0, 0);
         constexpr uint32_t id_pv = idesc_f16(128, D, BF16 ? 1 : 0, 0, 1);
         constexpr uint64_t kHiQK = (uint64_t(16 >> 4) << 16) | (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
-        constexpr uint64_t kHiV = (uint64_t(C::SLAB >> 4) << 16) | (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+        constexpr uint64_t kHiV = (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
         constexpr uint32_t qk_lo = static_cast<uint32_t>(kHiQK), qk_hi = static_cast<uint32_t>(kHiQK >> 32);
-        constexpr uint32_t v_lo = static_cast<uint32_t>(kHiV), v_hi = static_cast<uint32_t>(kHiV >> 32);
+        constexpr uint32_t v_hi = static_cast<uint32_t>(kHiV >> 32);
+        const uint32_t v_lo = static_cast<uint32_t>(bk * 128 >> 4) << 16;    // slabs bk rows apart
         // shared addresses in a descriptor's 16-byte units
         const uint32_t q16 = (q_addr >> 4) | qk_lo, k16 = (k_addr >> 4) | qk_lo, v16 = (v_addr >> 4) | v_lo;
         auto qk = [&](uint32_t q, uint32_t k, uint32_t s) {
@@ -424,15 +488,16 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
         };
         auto pv = [&](uint32_t p, uint32_t v, uint32_t o, uint32_t acc) {
 #pragma unroll
-            for (int kk = 0; kk < TK / 16; ++kk) mma_ts(o, p + 8 * kk, v + kk * (2048 >> 4), v_hi, id_pv, kk != 0 ? 1u : acc);
+            for (int kk = 0; kk < TK / 16; ++kk)
+                mma_ts(o, p + 8 * kk, v + (v_offset<D>(bk, 0, 16 * kk) >> 4), v_hi, id_pv, kk != 0 ? 1u : acc);
         };
         bool ok = true;
         SeqPiece p;
-        auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_or_abort(mi, bar, parity & 1u, a.status); };
-        // bn: tiles of the stream, in its two S buffers in turn; pn: its pieces; cn: tiles of
+        auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_bar(bar, parity); };
+        // bn: tiles of the stream, in its S or P buffers in turn; pn: its pieces; cn: tiles of
         // the CTA; n: its pieces
         int bn = 0, pn = 0, cn = 0, n = 0;
-        const uint32_t s0 = tmem + 128 * x, o = tm_o0 + 128 * x, q = q16 + x * (16384 >> 4);
+        const uint32_t s0 = tmem + C::CS * x, o = tm_o0 + D * x, q = q16 + x * (16384 >> 4);
 #pragma unroll 1
         while (ok && fetch(&p)) {
             if (lane == 0) {
@@ -441,14 +506,14 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                     ok = wait(&mi->q_full, n);
 #pragma unroll 1
                     for (int t = 0; t < p.nt && ok; ++t, ++cn) {
-                        const int st = cn % NK, sb = bn & 1;
+                        const int st = cn % NK, sb = bn % NS;
                         ok = wait(&mi->k_full[st], cn / NK);
                         if (!act) {                     // the other stream's alone: release it with that one
                             mbar_arrive(&mi->k_empty[st]);
                             continue;
                         }
-                        // S over P: the P V that read this buffer two tiles ago is done
-                        if (ok && bn >= 2) ok = wait(&mi->o_done[x][sb], (bn >> 1) - 1);
+                        // the softmax warps have taken the S that was here
+                        if (ok && bn >= NS) ok = wait(&mi->s_free[x][sb], bn / NS - 1);
                         if (!ok) break;
                         tc_fence_after();
                         qk(q, k16 + st * (C::STAGE >> 4), s0 + 64 * sb);
@@ -461,18 +526,18 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                 } else {
 #pragma unroll 1
                     for (int t = 0; t < p.nt && ok; ++t, ++cn) {
-                        const int st = cn % NV, sb = bn & 1;
+                        const int st = cn % NV, sb = bn % NP;
                         ok = wait(&mi->v_ready[st], cn / NV);
                         if (!act) {
                             mbar_arrive(&mi->v_empty[st]);
                             continue;
                         }
-                        if (ok) ok = wait(&mi->p_full[x][sb], bn >> 1);
+                        if (ok) ok = wait(&mi->p_full[x][sb], bn / NP);
                         // O is rewritten: the piece before has been read out
                         if (ok && t == 0 && pn > 0) ok = wait(&mi->o_free[x], pn - 1);
                         if (!ok) break;
                         tc_fence_after();
-                        pv(s0 + 64 * sb, v16 + st * (C::STAGE >> 4), o, t != 0);
+                        pv(s0 + 64 * NS + 32 * sb, v16 + st * (C::STAGE >> 4), o, t != 0);
                         mma_commit(&mi->o_done[x][sb]);
                         mma_commit(&mi->v_empty[st]);
                         ++bn;
@@ -483,69 +548,88 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
         }
+        failed |= !ok;
         if (lane == 0) {                                // every MMA issued has completed
             mma_commit(&mi->drain[2 * x + w]);
             if (!mbar_wait_sleep(&mi->drain[2 * x + w], 0, 1u << 21, 1000)) atomicOr(a.status, kSeqTimeout);
         }
         __syncwarp();
-    } else if (warp == 3) {
-        // ---------------------------------------------------------------- V guard
-        int vn = 0, n = 0;
+    } else if (warp == 3 || warp == 7) {
+        // --------------------------------------------------------------- V guards
+        // Two warps, every other 4 rows each; warp 3 does the marking.
+        const int part = warp >> 2;
+        int vn = 0, n = 0, gn = 0;                      // V tiles, pieces, masked tiles so far
         bool ok = true;
         SeqPiece p;
 #pragma unroll 1
         for (; ok && fetch(&p); ++n) {
             bool marked = false;
             uint32_t *poison = ar.poison + (static_cast<size_t>(cta) * kPoison + n % kPoison) * ROWS * (D / 32);
-            if (lane == 0) mi->poisoned[n % kPoison] = 0;
+            if (part == 0 && lane == 0) mi->poisoned[n % kPoison] = 0;
 #pragma unroll 1
             for (int t = 0; t < p.nt && ok; ++t, ++vn) {
                 const int st = vn % NV, k0 = (p.t0 + t) << TKS;
-                ok = __all_sync(0xffffffffu, wait_or_abort(mi, &mi->v_full[st], static_cast<uint32_t>(vn / NV) & 1u, a.status));
+                ok = warp_wait(&mi->v_full[st], vn / NV);
                 if (!ok) break;
                 if (is_masked(p, p.t0 + t)) {
                     unsigned char *v = sm + C::OFF_V + st * C::STAGE;
                     const int live = min(max(p.kv - k0, 0), TK);
                     // slab rows are 128 bytes; lane l takes chunk l % 8 of rows l / 8, l / 8 + 4, ...
                     // Rows that every row of the unit sees need no look: left of full_lo and
-                    // right of full_hi they are scanned, past the last key zeroed.  16 vectors in
-                    // flight: the one warp's latency is the scan's time.
+                    // right of full_hi they are scanned, past the last key zeroed.
                     uint32_t acc[4] = {};
-                    auto scan = [&](int r0, int r1) {              // slab-wise, r0 a multiple of 4
-                        for (int s = 0; s < C::SLABS; ++s)
+                    auto scan = [&](int r0, int r1) {              // r0 a multiple of 8
 #pragma unroll 1
-                            for (int r = r0 + (lane >> 3); r < r1; r += 64) {
-                                const uint4 *x = reinterpret_cast<const uint4 *>(v + s * C::SLAB + r * 128 + (lane & 7) * 16);
-                                uint4 y[16];
+                        for (int s = 0; s < C::SLABS; ++s) {
+                            uint4 y[8];
 #pragma unroll
-                                for (int u = 0; u < 16; ++u) y[u] = r + 4 * u < r1 ? x[u * 32] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                                for (int u = 0; u < 16; ++u) {
-                                    acc[0] |= odd16<BF16>(y[u].x);
-                                    acc[1] |= odd16<BF16>(y[u].y);
-                                    acc[2] |= odd16<BF16>(y[u].z);
-                                    acc[3] |= odd16<BF16>(y[u].w);
-                                }
+                            for (int u = 0; u < 8; ++u) {
+                                const int r = r0 + (lane >> 3) + 8 * u + 4 * part;
+                                y[u] = r < r1 ? *reinterpret_cast<const uint4 *>(v + v_offset<D>(bk, s, r) + (lane & 7) * 16)
+                                              : make_uint4(0, 0, 0, 0);
                             }
+#pragma unroll
+                            for (int u = 0; u < 8; ++u) {
+                                acc[0] = max_abs<BF16>(acc[0], y[u].x);
+                                acc[1] = max_abs<BF16>(acc[1], y[u].y);
+                                acc[2] = max_abs<BF16>(acc[2], y[u].z);
+                                acc[3] = max_abs<BF16>(acc[3], y[u].w);
+                            }
+                        }
                     };
-                    const int right = min(max(p.full_hi - k0, 0), live) & ~3, left = min(p.full_lo - k0, right);
+                    const int right = min(max(p.full_hi - k0, 0), live) & ~7, left = min(p.full_lo - k0, right);
                     if (left > 0) scan(0, left);
                     if (right < live) scan(right, live);
+#pragma unroll 1
                     for (int s = 0; s < C::SLABS; ++s)
-                        for (int r = live + (lane >> 3); r < TK; r += 4)
-                            *reinterpret_cast<uint4 *>(v + s * C::SLAB + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
-                    const bool found = ((acc[0] | acc[1] | acc[2] | acc[3]) & 0x80008000u) != 0;
-                    if (__any_sync(0xffffffffu, found)) {
-                        mark_odd<D, BF16>(a, p, k0, live, v, poison, !marked);
-                        marked = true;
-                        if (lane == 0) mi->poisoned[n % kPoison] = 1;
-                    }
+#pragma unroll 1
+                        for (int r = live + (lane >> 3) + 4 * part; r < TK; r += 8)
+                            *reinterpret_cast<uint4 *>(v + v_offset<D>(bk, s, r) + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    const bool found = ((odd16<BF16>(acc[0]) | odd16<BF16>(acc[1]) | odd16<BF16>(acc[2]) | odd16<BF16>(acc[3])) & 0x80008000u) != 0;
                     fence_proxy_async_smem();
+                    const bool any = __any_sync(0xffffffffu, found);
+                    if (lane == 0) {
+                        mi->found[gn & 1][part] = any;
+                        mbar_arrive(&mi->guard);
+                    }
+                    ok = warp_wait(&mi->guard, gn);
+                    if (!ok) break;
+                    const volatile int *f = mi->found[gn & 1];
+                    ++gn;
+                    if (f[0] | f[1]) {
+                        if (part == 0) {
+                            mark_odd<D, BF16>(a, p, k0, live, bk, v, poison, !marked);
+                            if (lane == 0) mi->poisoned[n % kPoison] = 1;
+                            fence_proxy_async_smem();
+                        }
+                        marked = true;
+                    }
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&mi->v_ready[st]);
             }
         }
+        failed |= !ok;
     }
     } else {
         // ---------------------------------------------------- softmax and epilogue
@@ -555,13 +639,13 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
         const int r = quarter * 32 + lane;              // row within the stream
         const int urow = 128 * s + r;                   // row within the unit
         const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-        const uint32_t tm_s = tmem + lane_off + 128 * s, tm_o = tm_o0 + lane_off + 128 * s;
+        const uint32_t tm_s = tmem + lane_off + C::CS * s, tm_o = tm_o0 + lane_off + D * s;
         const float scale2 = fmaxf(a.scale * kLog2e, FLT_MIN);   // above 0: a masked -inf stays -inf
         const int tok_row = static_cast<int>((static_cast<uint32_t>(urow) * ar.g_inv) >> 16);
         int tn = 0, vn = 0;                             // tiles of this stream, tiles of the CTA
         bool ok = true;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
-            ok = __all_sync(0xffffffffu, ok && wait_or_abort(mi, bar, parity & 1u, a.status));
+            ok = warp_wait(bar, parity) && ok;
         };
         SeqPiece p;
 #pragma unroll 1
@@ -572,64 +656,45 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                 const int i = p.i0 + tok_row;
                 uint32_t anc[kMaxTreeBitsNodes / 32];
                 if (a.parents && live) seq_ancestors(a.parents + p.q0, i, anc);
+                uint32_t v[TK];
+                // S of tile tn of the stream, on its way into v
+                auto take = [&](int n) {
+                    wait(&mi->s_full[s][n % NS], n / NS);
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < TK / 32; ++c)
+                        tmem_ld32(tm_s + 64 * (n % NS) + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&v[32 * c]));
+                };
+                take(tn);
 #pragma unroll 1
                 for (int t = 0; t < p.nt; ++t, ++tn) {
-                    const int sb = tn & 1;
-                    const uint32_t col = tm_s + 64 * sb;
-                    wait(&mi->s_full[s][sb], tn >> 1);
+                    const int pb = tn % NP;
+                    tmem_wait_ld();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&mi->s_free[s][tn % NS]);
                     if (!ok) break;
-                    tc_fence_after();
                     const bool masked = is_masked(p, p.t0 + t);
-                    // The row max is needed before the exponentials on a piece's first tile, and
-                    // on masked ones.  Else P is taken with the running max as it is and the
-                    // tile's own max beside the exponentials (other pipes); only where some
-                    // row's max rose by more than 2^8 is the tile done again.
-                    bool known = t == 0 || masked, again = false;
-                    float top = -INFINITY;
+                    if (__builtin_expect(masked, 0)) {
+                        uint32_t m[TK / 32];
+                        seq_visible<TK / 32>(a, p.prefix, live ? p.kv : 0, i, anc, (p.t0 + t) << TKS, m);
+#pragma unroll
+                        for (int e = 0; e < TK; ++e)
+                            if (!((m[e >> 5] >> (e & 31)) & 1u)) v[e] = 0xff800000u;
+                    }
+                    if (__builtin_expect(t == 0, 0)) {
+                        float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                        for (int e = 0; e < TK / 2; ++e) mx[e & 1] = max3(mx[e & 1], __uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+                        m_run = fmaxf(mx[0], mx[1]) * scale2;
+                    }
+                    // P with the running max as it is, the tile's own max taken beside the
+                    // exponentials (other pipes); only where some row's max rose by more than 2^8
+                    // do O and l follow, and P is taken again
                     uint32_t pk[TK / 2];
                     float l_tile;
 #pragma unroll 1
                     for (;;) {
-                        uint32_t v[TK];
-#pragma unroll
-                        for (int c = 0; c < TK / 32; ++c)
-                            tmem_ld32(col + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&v[32 * c]));
-                        tmem_wait_ld();
-                        if (masked) {
-                            uint32_t m[TK / 32];
-                            seq_visible<TK / 32>(a, p.prefix, live ? p.kv : 0, i, anc, (p.t0 + t) << TKS, m);
-#pragma unroll
-                            for (int e = 0; e < TK; ++e)
-                                if (!((m[e >> 5] >> (e & 31)) & 1u)) v[e] = 0xff800000u;
-                        }
-                        if (known) {
-                            if (!again) {
-#pragma unroll
-                                for (int e = 0; e < TK; e += 2) top = max3(top, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-                            }
-                            // O and l follow where the running max rises
-                            const float rmax = top * scale2;
-                            float alpha = 1.0f;
-                            if (rmax > m_run + kSlack) {
-                                alpha = ex2(m_run - rmax);          // 0 from -inf
-                                l_run *= alpha;
-                                m_run = rmax;
-                            }
-                            if (t > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
-                                // O must be at rest: the P V of the tile before is done
-                                wait(&mi->o_done[s][(tn - 1) & 1], (tn - 1) >> 1);
-                                tc_fence_after();
-#pragma unroll 1
-                                for (int c = 0; c < D; c += 16) {
-                                    uint32_t o[16];
-                                    tmem_ld16(tm_o + c, o);
-                                    tmem_wait_ld();
-#pragma unroll
-                                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                                    tmem_st16(tm_o + c, o);
-                                }
-                            }
-                        }
                         const float m_use = m_run == -INFINITY ? 0.0f : m_run;
                         const uint64_t sc = pack64(scale2, scale2), mm = pack64(-m_use, -m_use);
                         uint64_t sum[2] = {0, 0};
@@ -645,24 +710,44 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                         }
                         const uint64_t all = add2(sum[0], sum[1]);
                         l_tile = lo64(all) + hi64(all);
-                        if (known) break;
-                        top = fmaxf(mx[0], mx[1]);
-                        if (!__any_sync(0xffffffffu, top * scale2 > m_run + kSlack)) break;
-                        known = again = true;
+                        const float top = fmaxf(mx[0], mx[1]) * scale2;
+                        if (__builtin_expect(!__any_sync(0xffffffffu, top > m_run + kSlack), 1)) break;
+                        float alpha = 1.0f;
+                        if (top > m_run + kSlack) {
+                            alpha = ex2(m_run - top);   // 0 from -inf
+                            l_run *= alpha;
+                            m_run = top;
+                        }
+                        // O must be at rest: the P V of the tile before is done (t > 0 here: the
+                        // first tile's max is the running max)
+                        wait(&mi->o_done[s][(tn - 1) % NP], (tn - 1) / NP);
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(tm_o + c, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                            tmem_st16(tm_o + c, o);
+                        }
                     }
                     l_run += l_tile;
-                    tmem_st32(col, pk);
+                    // the P V that read this buffer NP tiles ago is done
+                    if (tn >= NP) wait(&mi->o_done[s][pb], tn / NP - 1);
                     // the guard's marks of this V tile are in before its P V can be issued
                     if (masked) wait(&mi->v_ready[(vn + t) % NV], (vn + t) / NV);
+                    if (t + 1 < p.nt) take(tn + 1);     // the next S comes while this P goes
+                    tmem_st32(tm_s + 64 * NS + 32 * pb, pk);
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&mi->p_full[s][sb]);
+                    if (lane == 0) mbar_arrive(&mi->p_full[s][pb]);
                 }
             }
             vn += p.nt;
             if (act && ok) {
-                wait(&mi->o_done[s][(tn - 1) & 1], (tn - 1) >> 1);
+                wait(&mi->o_done[s][(tn - 1) % NP], (tn - 1) / NP);
                 if (!ok) break;
                 tc_fence_after();
                 const bool odd = *static_cast<volatile int *>(&mi->poisoned[n % kPoison]) != 0;
@@ -671,6 +756,16 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                 const size_t slot = static_cast<size_t>(p.slot < 0 ? 0 : p.slot);
                 float4 *part = reinterpret_cast<float4 *>(ar.ws.o) + slot * (D / 4) * ROWS + urow;
                 unsigned char *stage = sm + C::OFF_OUT + (warp - C::SW) * 2048;
+                // rows 8 u + lane / 4 of the warp, 16 bytes at 8 (lane % 4) columns
+                uint16_t *dst[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int ur = 128 * s + 32 * quarter + 8 * u + (lane >> 2);
+                    const int tok = static_cast<int>((static_cast<uint32_t>(ur) * ar.g_inv) >> 16), h = p.kh * a.g + ur - tok * a.g;
+                    dst[u] = ur < p.rows ? static_cast<uint16_t *>(a.out) + static_cast<long long>(p.q0 + p.i0 + tok) * a.o_st +
+                                               h * a.o_sh + (lane & 3) * 8
+                                         : nullptr;
+                }
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     uint32_t o[32];
@@ -696,14 +791,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                         }
                         __syncwarp();
 #pragma unroll
-                        for (int u = 0; u < 32; u += 8) {
-                            const int row = u + (lane >> 2), ch = lane & 3, ur = 128 * s + 32 * quarter + row;
-                            const uint4 x = *reinterpret_cast<const uint4 *>(stage + row * 64 + ((ch ^ ((row >> 1) & 3)) << 4));
-                            const int tok = static_cast<int>((static_cast<uint32_t>(ur) * ar.g_inv) >> 16), h = p.kh * a.g + ur - tok * a.g;
-                            if (ur < p.rows)
-                                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) +
-                                                           static_cast<long long>(p.q0 + p.i0 + tok) * a.o_st + h * a.o_sh + c +
-                                                           ch * 8) = x;
+                        for (int u = 0; u < 4; ++u) {
+                            const int row = 8 * u + (lane >> 2);
+                            const uint4 x = *reinterpret_cast<const uint4 *>(stage + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4));
+                            if (dst[u]) *reinterpret_cast<uint4 *>(dst[u] + c) = x;
                         }
                     } else if (live) {
 #pragma unroll
@@ -720,7 +811,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                 if (lane == 0) mbar_arrive(&mi->o_free[s]);
             }
         }
+        failed |= !ok;
     }
+    if (failed && lane == 0) atomicOr(a.status, kSeqTimeout);
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
