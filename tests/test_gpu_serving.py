@@ -157,9 +157,15 @@ class Paged:
             outs.append(reference(self.q[self.cu[b]:self.cu[b + 1]], self.keys[b], self.values[b], see, self.scale))
         return torch.cat([o for o, _ in outs]), torch.cat([s for _, s in outs])
 
-    def check(self, got, window=0):
+    def check(self, got, window=0, only=None):
+        """All requests' rows, or those of the requests `only`."""
         ref, spread = self.expect(window)
-        check(got[:self.cu[-1]], ref, spread, self.dtype, max(self.lens))
+        for b in range(len(self.lens)) if only is not None else ():
+            s = slice(self.cu[b], self.cu[b + 1])
+            if b in only:
+                check(got[s], ref[s], spread[s], self.dtype, max(self.lens))
+        if only is None:
+            check(got[:self.cu[-1]], ref, spread, self.dtype, max(self.lens))
 
 
 # -------------------------------------------------------------------- prompts
@@ -184,6 +190,59 @@ def test_prompt(ta, lens, h, hk, d, dtype):
                     s = slice(cu[b], cu[b + 1])
                     ref, spread = reference(q[s], k[s], v[s], visible(n, n, window), d ** -0.5)
                     check(out[s], ref, spread, dt, n)
+
+
+@pytest.mark.parametrize("h,hk,d,window", [(8, 2, 128, 0), (8, 2, 128, 1500), (3, 1, 256, 0), (2, 2, 64, 700)])
+def test_long_prompt(ta, h, hk, d, window):
+    """More row tiles than a warp has lanes, units cut between CTAs."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(d)
+    lens = [4700, 0, 333]
+    q, k, v = (randn(g, sum(lens), n, d, dtype=torch.bfloat16, std=s) for n, s in ((h, 2.0), (hk, 1.0), (hk, 1.0)))
+    cu = offsets(lens)
+    out = ta.prompt_attention(q, k, v, i32(cu), scale=d ** -0.5, window=window)
+    for b, n in enumerate(lens):
+        if n:
+            s = slice(cu[b], cu[b + 1])
+            i = torch.arange(n)
+            see = (i[None] <= i[:, None]) & ((i[None] > i[:, None] - window) if window else True)
+            ref, spread = reference(q[s], k[s], v[s], see, d ** -0.5)
+            check(out[s], ref, spread, torch.bfloat16, n)
+
+
+def test_many_short_prompts(ta):
+    """More requests than a block has threads."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    rnd = random.Random(2)
+    lens = [rnd.choice([0, 1, 2, 3, 9]) for _ in range(1300)]
+    q, k, v = (randn(g, sum(lens), n, 64, dtype=torch.float16) for n in (4, 2, 2))
+    out = ta.prompt_attention(q, k, v, i32(offsets(lens)), scale=0.125)
+    want = ta.prompt_attention(q, k, v, i32(offsets(lens)), scale=0.125, kernel=1)
+    # each side within half a step of its own value, plus P's rounding on values up to 5
+    assert bool(((out - want).abs() <= 2.0 ** -10 * want.abs() + 5 * 2.0 ** -10).all())
+
+
+@pytest.mark.parametrize("kernel", [0, 1, 2, 3])
+def test_scales(ta, kernel):
+    """A scale of zero weighs every visible key alike; a negative one turns the order."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(12)
+    lens, h, hk, d = [90, 200], 4, 2, 128
+    q, k, v = (randn(g, sum(lens), n, d, dtype=torch.bfloat16) for n in (h, hk, hk))
+    cu = offsets(lens)
+    for scale in (0.0, -0.2, 1e-30, 0.7):
+        out = ta.prompt_attention(q, k, v, i32(cu), scale=scale, window=2 ** 31 - 1, kernel=kernel)
+        for b, n in enumerate(lens):
+            s = slice(cu[b], cu[b + 1])
+            ref, spread = reference(q[s], k[s], v[s], visible(n, n), scale)
+            # |scale| 0.7: sum |q k| scale is up to 8 times what check() allows for
+            check(out[s], ref, spread * (1 + 2.0 ** -8), torch.bfloat16, n)
+    c = Paged([300, 40], [1, 1], 8, 2, 128, 16, torch.bfloat16, seed=3)
+    c.scale = -0.1
+    c.check(c.run(ta, kernel=kernel))
+    c.scale = 0.0
+    c.check(c.run(ta, kernel=kernel))
 
 
 def test_prompt_strides_of_a_fused_projection(ta):
@@ -232,6 +291,19 @@ def test_decode(ta, h, hk, d, dtype, ps):
     for kernel in FAMILIES:
         for window in (0, 1, 100):
             c.check(c.run(ta, kernel=kernel, window=window), window)
+
+
+@pytest.mark.parametrize("h,hk,d,new,batch", [(4, 2, 64, 1, 700), (8, 2, 128, 2, 300), (2, 2, 128, 1, 2), (4, 1, 256, 20, 600)])
+def test_many_or_long_requests(ta, h, hk, d, new, batch):
+    """More requests than a block has threads; contexts cut into many pieces."""
+    rnd = random.Random(batch)
+    lens = [rnd.randint(new, 90) for _ in range(batch)] if batch > 2 else [30000, 9001]
+    c = Paged(lens, [new if batch == 2 or rnd.random() < 0.9 else 0 for _ in lens], h, hk, d, 16, torch.bfloat16, seed=batch)
+    got, want = c.run(ta), c.run(ta, kernel=1)
+    # both within P's and the output's rounding of one value (values up to 6)
+    assert bool(((got - want).abs() <= 2.0 ** -7 * want.abs() + 6 * 2.0 ** -8).all())
+    if batch == 2:
+        c.check(got)
 
 
 @pytest.mark.parametrize("h,hk,d,ps,dtype,new", [
@@ -360,8 +432,9 @@ def test_bad_pages_set_the_status(ta, new, kernel):
 @pytest.mark.parametrize("kernel", FAMILIES)
 @pytest.mark.parametrize("max_q", [4, 64])
 def test_contradicting_lengths_set_the_status(ta, max_q, kernel):
+    # (not the same bits as a call with sound lengths: where units are cut between CTAs, and so
+    # the rounding, follows from all lengths of a batch)
     c = Paged([200, 100, 150], [4, 4, 4], 8, 2, 128, 16, torch.bfloat16, seed=11)
-    clean = c.run(ta, kernel=kernel, max_q_len=max_q)
 
     def go(cu, lens):
         tmp = ta.paged_attention_workspace(c.q, c.k, c.table, max_q_len=max_q, kernel=kernel)
@@ -371,15 +444,18 @@ def test_contradicting_lengths_set_the_status(ta, max_q, kernel):
         return out, int(tmp.view(torch.int32)[0])
 
     out, st = go([0, 4, 8, 12], [200, -5, 150])
-    assert st == 4 and torch.equal(out[:4], clean[:4]) and torch.equal(out[8:], clean[8:])
-    assert bool((out[4:8] == 0).all())
+    assert st == 4 and bool((out[4:8] == 0).all())
+    c.check(out, only=(0, 2))
     out, st = go([0, 4, 2 ** 30, 12], [200, 100, 150])        # runs past the rows, then backwards
-    assert st & 4 and torch.equal(out[:4], clean[:4])
+    assert st & 4
+    c.check(out, only=(0,))
     out, st = go([-3, 4, 8, 12], [200, 100, 150])
-    assert st & 4 and torch.equal(out[4:], clean[4:])
+    assert st & 4
+    c.check(out, only=(1, 2))
     # more keys than a table row holds
     out, st = go([0, 4, 8, 12], [200, 2 ** 31 - 1, 150])
-    assert st & 4 and torch.equal(out[:4], clean[:4]) and torch.equal(out[8:], clean[8:])
+    assert st & 4
+    c.check(out, only=(0, 2))
 
 
 def test_rows_past_max_q_len_are_left(ta):

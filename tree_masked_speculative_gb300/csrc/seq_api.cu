@@ -75,13 +75,17 @@ ta_status check_stride(const char *op, const char *name, uint64_t s) {
     return TA_OK;
 }
 
+// Rows of a call and keys of a request: positions, and positions less a window, stay
+// within 32 bits.
+constexpr uint32_t kMostKeys = 1u << 30;
+
 ta_status check_heads(const char *op, uint32_t batch, uint32_t h, uint32_t hk, uint32_t d, uint32_t tokens, uint32_t kernel,
                       float scale) {
     if (batch == 0 || h == 0 || hk == 0) SEQ_FAIL(TA_ERR_INVALID_ARGUMENT, "%s: batch, n_heads and n_kv_heads must be > 0", op);
     if (h % hk != 0) SEQ_FAIL(TA_ERR_INVALID_ARGUMENT, "%s: n_heads (%u) must be divisible by n_kv_heads (%u)", op, h, hk);
     if (d != 64 && d != 128 && d != 256) SEQ_FAIL(TA_ERR_INVALID_ARGUMENT, "%s: head_dim must be 64, 128 or 256, got %u", op, d);
     if (h / hk > 128) SEQ_FAIL(TA_ERR_UNSUPPORTED, "%s: more than 128 query heads per KV head", op);
-    if (batch > 65535 || hk > 65535 || static_cast<uint64_t>(tokens) * h > static_cast<uint64_t>(INT_MAX))
+    if (batch > 65535 || hk > 65535 || tokens > kMostKeys || static_cast<uint64_t>(tokens) * h > static_cast<uint64_t>(INT_MAX))
         SEQ_FAIL(TA_ERR_UNSUPPORTED, "%s: sizes exceed the kernels' index range", op);
     if (kernel > TA_KERNEL_WARP_MMA) SEQ_FAIL(TA_ERR_INVALID_ARGUMENT, "%s: kernel must be 0 (auto), 1, 2 or 3, got %u", op, kernel);
     if (!std::isfinite(scale)) SEQ_FAIL(TA_ERR_INVALID_ARGUMENT, "%s: scale is not finite", op);
@@ -111,7 +115,7 @@ ta_status check_paged(const ta_paged_params *p) {
         SEQ_FAIL(TA_ERR_INVALID_ARGUMENT, "paged_attn: n_pages and max_pages must be > 0");
     if (p->window > static_cast<uint32_t>(INT_MAX) || p->max_q_len > static_cast<uint32_t>(INT_MAX) ||
         p->n_pages > static_cast<uint32_t>(INT_MAX) ||
-        static_cast<uint64_t>(p->max_pages) * p->page_size > static_cast<uint64_t>(INT_MAX) / 2)
+        static_cast<uint64_t>(p->max_pages) * p->page_size > kMostKeys)
         SEQ_FAIL(TA_ERR_UNSUPPORTED, "paged_attn: sizes exceed the kernels' index range");
     return TA_OK;
 }
@@ -398,7 +402,7 @@ TA_EXPORT ta_status paged_attn_fwd(const ta_paged_params *pp, const ta_buf *q, c
     a.D = static_cast<int>(p.head_dim);
     a.T = static_cast<int>(p.tokens);
     a.max_q = static_cast<int>(p.max_q_len);
-    a.window = static_cast<int>(p.window);
+    a.window = static_cast<int>(p.window < kMostKeys ? p.window : kMostKeys);     // no request has more keys
     a.page_shift = log2_of(p.page_size);
     a.n_pages = static_cast<int>(p.n_pages);
     a.max_pages = static_cast<int>(p.max_pages);
@@ -463,7 +467,7 @@ TA_EXPORT ta_status prompt_attn_fwd(const ta_prompt_params *pp, const ta_buf *q,
     a.g = a.H / a.Hk;
     a.D = static_cast<int>(p.head_dim);
     a.T = a.max_q = static_cast<int>(p.tokens);
-    a.window = static_cast<int>(p.window);
+    a.window = static_cast<int>(p.window < kMostKeys ? p.window : kMostKeys);     // no request has more keys
     a.bf16 = type == TA_BF16;
     a.q_st = static_cast<long long>(p.q_token_stride);
     a.q_sh = static_cast<long long>(p.q_head_stride);

@@ -6,7 +6,7 @@
 // least one, and UC tiles' worth of time before the first (its rows of Q, its
 // epilogue).  All units' work, one behind the other (request, then KV head, then row
 // tile), is cut into G equal runs (fewer where there is less), one per CTA: the batch
-// is balanced whatever its lengths are, a unit is cut only where a run ends, and a CTA
+// is balanced whatever its lengths are (LEAST: tiles a run has at least), a unit is cut only where a run ends, and a CTA
 // has at most two pieces of cut units (its first and its last), so 2 G partial
 // slots hold every cut piece.  (With UC = 0, of the time of a causal prompt of 4096
 // tokens a CTA worked 72 % on average: those with the short units ended last.)
@@ -82,7 +82,7 @@ struct SeqScratch {
 
 // This CTA's run [P0, P1) of the W tiles of work and where it starts (in *s, valid when
 // P0 < P1).  Block-collective.
-template <int NT, int TKS, int UC>
+template <int NT, int TKS, int UC, int LEAST>
 __device__ SeqRun seq_schedule(const SeqArgs &a, int tpt, int cta, int G, SeqScratch *s) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     SeqReq r;
@@ -124,7 +124,8 @@ __device__ SeqRun seq_schedule(const SeqArgs &a, int tpt, int cta, int G, SeqScr
         scan(tiles_of(b0 + tid), &t);
         run.W += t;
     }
-    run.G = static_cast<int>(min(static_cast<long long>(G), run.W));
+    run.G = static_cast<int>(min(static_cast<long long>(G), max(1ll, run.W / LEAST)));
+    if (run.W == 0) run.G = 0;
     if (run.W <= 0x7fffffffll) {
         const uint32_t g = max(run.G, 1), w = static_cast<uint32_t>(run.W), q = w / g;
         run.base = q;

@@ -48,6 +48,11 @@ struct Cfg {
     static constexpr int CS = 64 * NS + 32 * NP;        // S and P columns of a stream
     static constexpr int CO = NSTR * CS;                // first column of O
     static_assert(CO + NSTR * D <= 512, "TMEM");
+    // Who waits for a P buffer to be read: the issuer of Q K^T (S then means the buffer is
+    // free) or the softmax warps.  D = 64, whose softmax sets the pace: 200 against 220 us
+    // for a prompt of 8192 tokens, 16 heads; D = 256, whose products do: 230 against 208 us
+    // (4096 tokens, 24 / 4 heads); D = 128 the same.
+    static constexpr bool kQkWaitsP = D == 64;
     static constexpr int SW = 8;                        // first softmax warp
     static constexpr int THREADS = 32 * SW + 128 * NSTR;
     static constexpr int SLABS = D / 64;                // 64-column slabs of a tile
@@ -323,7 +328,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
         tma_prefetch_desc(&maps.v);
     }
     pdl_wait();
-    const SeqRun run = seq_schedule<C::THREADS, TKS, kUnitCost>(a, ar.tpt, cta, ar.G, &mi->sched);
+    const SeqRun run = seq_schedule<C::THREADS, TKS, kUnitCost, 1>(a, ar.tpt, cta, ar.G, &mi->sched);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -514,6 +519,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                         }
                         // the softmax warps have taken the S that was here
                         if (ok && bn >= NS) ok = wait(&mi->s_free[x][sb], bn / NS - 1);
+                        if (C::kQkWaitsP && ok && bn >= NP) ok = wait(&mi->o_done[x][bn % NP], bn / NP - 1);
                         if (!ok) break;
                         tc_fence_after();
                         qk(q, k16 + st * (C::STAGE >> 4), s0 + 64 * sb);
@@ -733,16 +739,16 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                         }
                     }
                     l_run += l_tile;
-                    // the P V that read this buffer NP tiles ago is done
-                    if (tn >= NP) wait(&mi->o_done[s][pb], tn / NP - 1);
+                    // the P V that read this buffer NP tiles ago is done (kQkWaitsP: S says so)
+                    if (!C::kQkWaitsP && tn >= NP) wait(&mi->o_done[s][pb], tn / NP - 1);
                     // the guard's marks of this V tile are in before its P V can be issued
                     if (masked) wait(&mi->v_ready[(vn + t) % NV], (vn + t) / NV);
-                    if (t + 1 < p.nt) take(tn + 1);     // the next S comes while this P goes
                     tmem_st32(tm_s + 64 * NS + 32 * pb, pk);
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&mi->p_full[s][pb]);
+                    if (t + 1 < p.nt) take(tn + 1);     // (before P's store it held P V back)
                 }
             }
             vn += p.nt;
