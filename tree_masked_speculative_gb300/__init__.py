@@ -466,8 +466,13 @@ _paged_entry = _Entry("paged_attn_fwd", "11If7Q", 9)
 _prompt_entry = _Entry("prompt_attn_fwd", "7If8Q", 6)
 
 
-def _as_stream(stream) -> torch.cuda.Stream:
-    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+def _as_stream(stream, dev: int) -> torch.cuda.Stream:
+    """`stream` (a torch stream or a handle) on the tensors' device."""
+    if not isinstance(stream, torch.cuda.Stream):
+        return torch.cuda.ExternalStream(int(stream), device=dev)
+    if stream.device.index != dev:
+        raise ValueError("stream is on %s, the tensors are on cuda:%d" % (stream.device, dev))
+    return stream
 
 
 def _device_of(t: torch.Tensor) -> int:
@@ -542,7 +547,7 @@ def _cache_pair(k_cache, v_cache, dev):
 
 def _elsewhere(fn, dev, stream, args, kw):
     """The call made with `stream`, or with the tensors' device, current."""
-    with torch.cuda.stream(_as_stream(stream)) if stream is not None else torch.cuda.device(dev):
+    with torch.cuda.stream(_as_stream(stream, dev)) if stream is not None else torch.cuda.device(dev):
         return fn(*args, **kw)
 
 
