@@ -514,7 +514,8 @@ size_t paged_attn_workspace_bytes(const ta_paged_params *p);
  * NaN makes the rows that see it NaN or infinite in its column.
  *   q, out      [tokens, n_heads, head_dim], the cache's type
  *   k_cache, v_cache   as above
- *   table       [batch, max_pages] i32; cells past a request's last page are not read
+ *   table       [batch, max_pages] i32; cells past a request's last page, and with a
+ *               window those of pages that no row of the request sees, may hold anything
  *   cu [batch + 1] i32, kv_lens [batch] i32
  *   parents     [tokens] i32 or absent; with parents window must be 0, and
  *               max_q_len > 256 is TA_ERR_UNSUPPORTED

@@ -430,6 +430,21 @@ def test_bad_pages_set_the_status(ta, new, kernel):
 
 
 @pytest.mark.parametrize("kernel", FAMILIES)
+@pytest.mark.parametrize("ps", [16, 32, 128])
+@pytest.mark.parametrize("new", [1, 3, 200])
+def test_pages_behind_the_window_may_be_gone(ta, new, ps, kernel):
+    """Cells of pages that lie before every row's window hold no page of the cache."""
+    c = Paged([900, 431, 5 + new], [new, max(new - 2, 1), new], 8, 2, 64, ps, torch.bfloat16, seed=17)
+    window = 70
+    for b, n in enumerate(c.lens):
+        c.table[b, :max(0, n - c.new[b] - window + 1) // ps] = -1
+    tmp = ta.paged_attention_workspace(c.q, c.k, c.table, max_q_len=new, kernel=kernel)
+    c.check(c.run(ta, window=window, tmp=tmp, kernel=kernel), window)
+    assert int(tmp.view(torch.int32)[0]) == 0
+
+
+
+@pytest.mark.parametrize("kernel", FAMILIES)
 @pytest.mark.parametrize("max_q", [4, 64])
 def test_contradicting_lengths_set_the_status(ta, max_q, kernel):
     # (not the same bits as a call with sound lengths: where units are cut between CTAs, and so

@@ -136,6 +136,7 @@ PAGED_BUFS = ["q", "k_cache", "v_cache", "table", "cu", "kv_lens", "parents", "t
     (dict(max_pages=1 << 27), None, None, 4, "index range"),
     (dict(window=1 << 31), None, None, 4, "index range"),
     (dict(tokens=2 ** 30), None, None, 4, "index range"),
+    (dict(n_heads=2, tokens=2 ** 23, max_q_len=2 ** 23, max_pages=2 ** 22, head_dim=64), None, None, 4, "tokens x keys"),
     (dict(kernel=4), None, None, 1, "kernel"),
     (dict(scale=float("nan")), None, None, 1, "scale"),
     (dict(scale=float("inf")), None, None, 1, "scale"),
@@ -181,6 +182,8 @@ PROMPT_BUFS = ["q", "k", "v", "cu", "tmp", "out"]
     (dict(n_heads=7), None, None, 1, "divisible"),
     (dict(head_dim=32), None, None, 1, "head_dim"),
     (dict(window=2 ** 32 - 1), None, None, 4, "index range"),
+    (dict(n_heads=2, tokens=2 ** 23, head_dim=64), None, None, 4, "tokens x keys"),
+    (dict(n_heads=128, n_kv_heads=1, tokens=2 ** 21), None, None, 4, "tokens x keys"),
     (dict(kernel=9), None, None, 1, "kernel"),
     (dict(v_token_stride=12), None, None, 1, "v_token_stride"),
     (dict(k_head_stride=1 << 39), None, None, 4, "k_head_stride"),
@@ -208,3 +211,27 @@ def test_python_refuses_host_tensors(ta):
         ta.prompt_attention(x, x, x, torch.tensor([0, 4], dtype=torch.int32), scale=1.0)
     with pytest.raises(ValueError, match="CUDA"):
         ta.paged_append(x, x, x[None], x[None], torch.zeros(4, dtype=torch.int64))
+
+
+def test_work_counted_within_32_bits_is_taken(ta):
+    # a window, another family and a smaller request leave the range alone: the next check speaks
+    for kw in (dict(window=4096), dict(kernel=1), dict(tokens=2 ** 22)):
+        p = ta.PromptParams(**{**PROMPT, **dict(n_heads=2, tokens=2 ** 23, head_dim=64), **kw})
+        st, msg = _call(ta, ta.lib.prompt_attn_fwd, p, [None] * 6)
+        assert st == 1 and "q dtype" in msg, msg
+
+
+def test_a_stream_of_another_device_is_refused(ta, monkeypatch):
+    class Stream:
+        def __init__(self, index):
+            self.device = torch.device("cuda", index)
+
+    made = []
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: made.append((handle, device)))
+    mine = Stream(1)
+    assert ta._as_stream(mine, 1) is mine
+    with pytest.raises(ValueError, match="stream is on cuda:0"):
+        ta._as_stream(Stream(0), 1)
+    ta._as_stream(0x1234, 1)
+    assert made == [(0x1234, 1)]

@@ -581,10 +581,6 @@ bool quant_tmp(const ta_quant_params *p, uint32_t nwg, uint64_t *bytes) {
 
 }  // namespace
 
-int device_sm_count() { return sm_count(); }
-
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() { return get_encoder() ? g_encode : nullptr; }
-
 void count_launch(int n) { g_launches.fetch_add((uint64_t)n, std::memory_order_relaxed); }
 
 void set_last_error(const char *fmt, ...) {

@@ -1,5 +1,8 @@
 // C ABI of the batched serving operators: argument checks (all before any
 // launch, overflow-checked), workspace sizes and kernel choice.
+#include <cudaTypedefs.h>
+
+#include <atomic>
 #include <climits>
 #include <cmath>
 
@@ -103,7 +106,45 @@ void cache_strides(uint64_t hk, uint64_t ps, uint64_t d, uint64_t *page, uint64_
     if (*page == 0) *page = hk * ps * d;
 }
 
+// SMs of the current device, asked once a device (0: none visible).
+int device_sm_count() {
+    static std::atomic<int> known[64];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) dev = -1;
+    else if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (dev < 0 || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// cuTensorMapEncodeTiled of the driver, looked up once; nullptr when it has none.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+        void *fn = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) == cudaSuccess &&
+                        found == cudaDriverEntryPointSuccess;
+        if (!ok) cudaGetLastError();
+        return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn) : nullptr;
+    }();
+    return encode;
+}
+
 constexpr uint64_t kStatusBytes = 256;
+
+int seq_family(uint32_t d, uint32_t kernel, uint64_t rows, float scale);
+
+// The tensor-core kernel counts the key tiles of a request and KV head in 32 bits
+// (`rows` tokens of it, `keys` a token sees on average; a part tile at either end).
+ta_status check_work(const char *op, uint32_t g, uint32_t d, uint64_t rows, uint64_t keys) {
+    const uint64_t tpt = static_cast<uint64_t>(seq_tc_rows(static_cast<int>(d))) / g;
+    if ((rows / tpt + 1) * ((keys + tpt) / kSeqTcTileKeys + 2 + kSeqTcUnitCost) > static_cast<uint64_t>(INT_MAX))
+        SEQ_FAIL(TA_ERR_UNSUPPORTED, "%s: tokens x keys of a request exceed the kernel's index range", op);
+    return TA_OK;
+}
 
 ta_status check_paged(const ta_paged_params *p) {
     if (p == nullptr) SEQ_FAIL(TA_ERR_INVALID_ARGUMENT, "paged_attn: params is NULL");
@@ -117,6 +158,10 @@ ta_status check_paged(const ta_paged_params *p) {
         p->n_pages > static_cast<uint32_t>(INT_MAX) ||
         static_cast<uint64_t>(p->max_pages) * p->page_size > kMostKeys)
         SEQ_FAIL(TA_ERR_UNSUPPORTED, "paged_attn: sizes exceed the kernels' index range");
+    const uint64_t g = p->n_heads / p->n_kv_heads, keys = static_cast<uint64_t>(p->max_pages) * p->page_size;
+    if (seq_family(p->head_dim, p->kernel, p->max_q_len * g, p->scale) == TA_KERNEL_TENSOR_CORES)
+        SEQ_TRY(check_work("paged_attn", static_cast<uint32_t>(g), p->head_dim, p->max_q_len < p->tokens ? p->max_q_len : p->tokens,
+                           p->window && p->window < keys ? p->window : keys));
     return TA_OK;
 }
 
@@ -125,6 +170,10 @@ ta_status check_prompt(const ta_prompt_params *p) {
     SEQ_TRY(check_heads("prompt_attn", p->batch, p->n_heads, p->n_kv_heads, p->head_dim, p->tokens, p->kernel, p->scale));
     if (p->window > static_cast<uint32_t>(INT_MAX))
         SEQ_FAIL(TA_ERR_UNSUPPORTED, "prompt_attn: sizes exceed the kernels' index range");
+    const uint64_t keys = p->tokens / 2;               // causal: half of them on average
+    if (seq_family(p->head_dim, p->kernel, 0, p->scale) == TA_KERNEL_TENSOR_CORES)
+        SEQ_TRY(check_work("prompt_attn", p->n_heads / p->n_kv_heads, p->head_dim, p->tokens,
+                           p->window && p->window < keys ? p->window : keys));
     return TA_OK;
 }
 

@@ -73,8 +73,9 @@ struct SeqTcPlan {
     void *ws;
     CUtensorMap q, k, v;
 };
-// Keys per key tile and rows per row tile of the tensor-core kernel.
-constexpr int kSeqTcTileKeys = 64;
+// Keys per key tile, tiles' worth of time of a unit's start and end, and rows per row
+// tile of the tensor-core kernel.
+constexpr int kSeqTcTileKeys = 64, kSeqTcUnitCost = 5;
 constexpr int seq_tc_rows(int d) { return d == 256 ? 128 : 256; }
 // Its workspace on a grid of G CTAs: status, records, (m, l) and O of 2 G partial
 // slots, and the marks of columns that are not finite (8 pieces a CTA).

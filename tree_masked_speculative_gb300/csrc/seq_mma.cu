@@ -141,7 +141,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D, RH>) seq_mma_kernel(co
             if (key >= key_end) return -1;
             const int page = __ldg(table + (key >> a.page_shift));
             if (page < 0 || page >= a.n_pages) {
-                if (lane == 0) atomicOr(a.status, kSeqBadPage);
+                // a page before every row's window may be gone
+                if (lane == 0 && !(a.window && key + 16 <= p.prefix - a.window + 1)) atomicOr(a.status, kSeqBadPage);
                 return -1;
             }
             return page * a.k_sp + (key & ((1 << a.page_shift) - 1)) * a.k_st + head;

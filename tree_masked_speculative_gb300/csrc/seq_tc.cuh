@@ -68,7 +68,7 @@ struct Cfg {
 };
 
 constexpr int kPieces = 4;
-constexpr int kUnitCost = 5;      // of the schedule: a unit's start and end take as long as 5 key tiles
+constexpr int kUnitCost = kSeqTcUnitCost;      // of the schedule: a unit's start and end take as long as 5 key tiles
 // The guard is at most kPieces + 2 pieces ahead of an epilogue (a piece is published
 // once every reader has fetched the one kPieces before it, and an epilogue runs
 // right after the next fetch), so a ring of 8 marks is never overrun.
@@ -347,7 +347,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
         if (key >= p.kv) return a.n_pages;
         const int g = __ldg(a.table + static_cast<long long>(p.b) * a.max_pages + (key >> a.page_shift));
         if (g >= 0 && g < a.n_pages) return g;
-        if (lane < per_slab) atomicOr(a.status, kSeqBadPage);
+        // a page before every row's window may be gone
+        if (lane < per_slab && !(a.window && key + bk <= p.prefix + p.i0 - a.window + 1)) atomicOr(a.status, kSeqBadPage);
         return a.n_pages;
     };
 

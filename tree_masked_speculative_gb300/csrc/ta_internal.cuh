@@ -2,7 +2,6 @@
 #pragma once
 
 #include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -421,12 +420,6 @@ int quant_mma16_ctas_per_sm_b8(int dim, int ng);
 constexpr int kFmaRowsPerCta = 16;
 
 void count_launch(int n = 1);
-
-// SMs of the current device (0: none visible).
-int device_sm_count();
-
-// cuTensorMapEncodeTiled of the driver, nullptr when it is not available.
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 // Set the calling thread's ta_last_error() message (printf format).
 void set_last_error(const char *fmt, ...);
