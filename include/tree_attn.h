@@ -56,7 +56,8 @@ typedef enum {
 typedef enum { TA_F32 = 0, TA_F16 = 1, TA_BF16 = 2, TA_U32 = 3, TA_I32 = 4, TA_I64 = 5 } ta_dtype;
 
 /*
- * Kernel family of a call (ta_tree_options.kernel, ta_quant_params.kernel).
+ * Kernel family of a call (ta_tree_options.kernel, ta_quant_params.kernel,
+ * ta_paged_params.kernel, ta_prompt_params.kernel).
  * TA_KERNEL_AUTO is the library's choice; the others force a family, for
  * tests and measurements.  The choice travels with the call: there is no
  * process-wide setting, so concurrent callers cannot affect one another.
@@ -65,7 +66,7 @@ typedef enum {
     TA_KERNEL_AUTO = 0,         /* tensor cores where the shape makes a dense contraction */
     TA_KERNEL_CUDA_CORES = 1,   /* always the CUDA-core kernel */
     TA_KERNEL_TENSOR_CORES = 2, /* the tensor-core kernel wherever its shape rules allow it */
-    TA_KERNEL_WARP_MMA = 3      /* quantized path only: the warp-MMA kernel wherever its
+    TA_KERNEL_WARP_MMA = 3      /* quantized and paged paths: the warp-MMA kernel wherever its
                                    shape rules allow it (the tree path rejects it) */
 } ta_kernel;
 
@@ -382,6 +383,12 @@ ta_status quant_sdpa_fwd_tree(const ta_quant_params *p, uint32_t q_l, const ta_b
  *     any page, head and token strides (elements, multiples of 8, the last
  *     axis contiguous), so a [n_pages, page_size, n_kv_heads, head_dim] cache is
  *     the same cache with other strides.  page_size: 16, 32, 64, 128 or 256.
+ *   - Rows of a call and keys of a request (its table row's cells) are at most
+ *     2^30, and a request has at most 2^31 tiles of 64 keys x 256 rows of work a KV
+ *     head; more is TA_ERR_UNSUPPORTED.
+ *   - The same call gives the same bits.  The attention cuts the batch's work evenly
+ *     over the GPU, so the last bits of a request's rows may change with the other
+ *     requests' lengths.
  *   - Device data that contradicts itself (a length beyond its table row, a
  *     page outside the cache, offsets that run backwards) never makes a kernel
  *     read or write outside its buffers; it sets bits of the call's status
@@ -477,8 +484,10 @@ ta_status paged_kv_append(const ta_append_params *p, const ta_buf *k_new, const 
  *                kernel; rows past it are left as they were and set a status bit)
  *   window       0, or the number of last positions a token sees, itself included
  *   page_size, n_pages, max_pages (cells per block-table row)
- *   kernel       ta_kernel
- *   scale        logit = (q . k) * scale
+ *   kernel       ta_kernel: automatic is the warp-MMA kernel up to max_q_len x (heads
+ *                per KV head) = 16 rows (8 for head_dim 256) and the tensor-core kernel
+ *                above; TA_KERNEL_WARP_MMA above that is the tensor-core kernel
+ *   scale        logit = (q . k) * scale; a negative one is served by the CUDA cores
  *   strides in elements, multiples of 8; 0 = contiguous
  */
 typedef struct {

@@ -3,7 +3,10 @@
 // head dimension 256), f16 / bf16.
 //
 // The work is reading K and V once, so HBM bounds it (4 D bytes a key and KV head;
-// 16 query rows are far below the tensor rate).  K and V go from global memory
+// 16 query rows are far below the tensor rate): 64 requests of 900 to 16384 keys, 32 / 8
+// heads of 128: 371 us, 6.4 TB/s (95 % of a plain copy's rate; the tcgen05 kernel, whose
+// 128-row tiles hold 4 rows of it, 567 us).  Three requests of 200 to 2100 keys take
+// 14 us, a chain of latencies: schedule, table, K and V, join, merge.  K and V go from global memory
 // straight into MMA fragments, without shared memory: Q K^T contracts over d in any
 // order, so a lane's 16-byte vector of K serves two m16n8k16 products as it is;
 // for P V a lane holds the same 8 columns of keys 2t, 2t + 1, 2t + 8, 2t + 9 and
