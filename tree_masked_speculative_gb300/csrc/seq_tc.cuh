@@ -183,6 +183,12 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
+// Has the phase completed.
+__device__ __forceinline__ bool poll_bar(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity & 1u) : "memory");
+    return ok != 0;
+}
 // The same for a whole warp, one outcome.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_bar(bar, parity)) != 0; }
 
@@ -654,8 +660,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
         const int tok_row = static_cast<int>((static_cast<uint32_t>(urow) * ar.g_inv) >> 16);
         int tn = 0, vn = 0;                             // tiles of this stream, tiles of the CTA
         bool ok = true;
+        // (the lanes' outcomes are joined once a tile: a vote at every wait took 443 us for a
+        // prompt of 8192 tokens against 423)
         auto wait = [&](uint64_t *bar, uint32_t parity) {
-            ok = warp_wait(bar, parity) && ok;
+            ok = wait_bar(bar, parity) && ok;
         };
         SeqPiece p;
 #pragma unroll 1
@@ -675,6 +683,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                     for (int c = 0; c < TK / 32; ++c)
                         tmem_ld32(tm_s + 64 * (n % NS) + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&v[32 * c]));
                 };
+                // tiles [plain0, plain0 + plains) are seen by every row and are not the first: one
+                // compare and branch a tile
+                const int plain0 = max(1, ((p.full_lo + TK - 1) >> TKS) - p.t0), plains = max(0, (p.full_hi >> TKS) - p.t0 - plain0);
                 take(tn);
 #pragma unroll 1
                 for (int t = 0; t < p.nt; ++t, ++tn) {
@@ -683,24 +694,33 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&mi->s_free[s][tn % NS]);
+                    ok = __all_sync(0xffffffffu, ok) != 0;
                     if (!ok) break;
-                    const bool masked = is_masked(p, p.t0 + t);
-                    if (__builtin_expect(masked, 0)) {
-                        uint32_t m[TK / 32];
-                        seq_visible<TK / 32>(a, p.prefix, live ? p.kv : 0, i, anc, (p.t0 + t) << TKS, m);
+                    bool masked = false;
+                    if (__builtin_expect(static_cast<unsigned>(t - plain0) >= static_cast<unsigned>(plains), 0)) {
+                        masked = is_masked(p, p.t0 + t);
+                        if (masked) {
+                            uint32_t m[TK / 32];
+                            seq_visible<TK / 32>(a, p.prefix, live ? p.kv : 0, i, anc, (p.t0 + t) << TKS, m);
 #pragma unroll
-                        for (int e = 0; e < TK; ++e)
-                            if (!((m[e >> 5] >> (e & 31)) & 1u)) v[e] = 0xff800000u;
-                    }
-                    if (__builtin_expect(t == 0, 0)) {
-                        float mx[2] = {-INFINITY, -INFINITY};
+                            for (int e = 0; e < TK; ++e)
+                                if (!((m[e >> 5] >> (e & 31)) & 1u)) v[e] = 0xff800000u;
+                        }
+                        if (t == 0) {
+                            float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                        for (int e = 0; e < TK / 2; ++e) mx[e & 1] = max3(mx[e & 1], __uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
-                        m_run = fmaxf(mx[0], mx[1]) * scale2;
+                            for (int e = 0; e < TK / 2; ++e)
+                                mx[e & 1] = max3(mx[e & 1], __uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+                            m_run = fmaxf(mx[0], mx[1]) * scale2;
+                        }
                     }
                     // P with the running max as it is, the tile's own max taken beside the
                     // exponentials (other pipes); only where some row's max rose by more than 2^8
                     // do O and l follow, and P is taken again
+                    // has the P V that read this P buffer NP tiles ago finished (kQkWaitsP: S says so):
+                    // asked here, where the answer arrives beside the exponentials (a wait in front of
+                    // P's store: 420 us for a prompt of 8192 tokens against 402)
+                    const bool o_done = C::kQkWaitsP || tn < NP || __all_sync(0xffffffffu, poll_bar(&mi->o_done[s][pb], tn / NP - 1));
                     uint32_t pk[TK / 2];
                     float l_tile;
 #pragma unroll 1
@@ -743,8 +763,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                         }
                     }
                     l_run += l_tile;
-                    // the P V that read this buffer NP tiles ago is done (kQkWaitsP: S says so)
-                    if (!C::kQkWaitsP && tn >= NP) wait(&mi->o_done[s][pb], tn / NP - 1);
+                    if (__builtin_expect(!o_done, 0)) wait(&mi->o_done[s][pb], tn / NP - 1);
                     // the guard's marks of this V tile are in before its P V can be issued
                     if (masked) wait(&mi->v_ready[(vn + t) % NV], (vn + t) / NV);
                     tmem_st32(tm_s + 64 * NS + 32 * pb, pk);
@@ -756,8 +775,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                 }
             }
             vn += p.nt;
+            ok = __all_sync(0xffffffffu, ok) != 0;
             if (act && ok) {
                 wait(&mi->o_done[s][(tn - 1) % NP], (tn - 1) / NP);
+                ok = __all_sync(0xffffffffu, ok) != 0;
                 if (!ok) break;
                 tc_fence_after();
                 const bool odd = *static_cast<volatile int *>(&mi->poisoned[n % kPoison]) != 0;
