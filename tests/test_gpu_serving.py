@@ -548,6 +548,50 @@ def test_repeats_streams_and_graphs(ta, new):
     assert torch.equal(graphs[0][2], want)
 
 
+@pytest.mark.parametrize("h,d", [(128, 64), (128, 256), (100, 128), (33, 256), (17, 64)])
+@pytest.mark.parametrize("kernel", [0, 2])
+def test_many_heads_of_one_kv_head(ta, h, d, kernel):
+    """Units of one or a few tokens, rows that do not divide by the heads."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(h)
+    lens = [1, 70, 0, 3, 131]
+    cu = offsets(lens)
+    q, k, v = (randn(g, cu[-1], n, d, dtype=torch.bfloat16, std=s) for n, s in ((h, 2.0), (1, 1.0), (1, 1.0)))
+    out = ta.prompt_attention(q, k, v, i32(cu), scale=d ** -0.5, kernel=kernel)
+    for b, n in enumerate(lens):
+        r = slice(cu[b], cu[b + 1])
+        if n:
+            check(out[r], *reference(q[r], k[r], v[r], visible(n, n), d ** -0.5), torch.bfloat16, n)
+    c = Paged([150, 64, 9], [1, 5, 9], h, 1, d, 32, torch.float16, seed=h, tree=True)
+    c.check(c.run(ta, kernel=kernel))
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_requests_that_share_pages(ta, new):
+    """A common prefix: both requests' tables name the same pages."""
+    c = Paged([320, 330], [new, new], 8, 2, 128, 32, torch.bfloat16, seed=18)
+    shared = 256 // 32
+    c.table[1, :shared] = c.table[0, :shared]
+    c.keys[1][:256], c.values[1][:256] = c.keys[0][:256], c.values[0][:256]
+    c.check(c.run(ta))
+
+
+@pytest.mark.parametrize("new", [1, 5, 90])
+def test_two_streams_at_once(ta, new):
+    cs = [Paged([2000, 77 + new, 300], [new] * 3, 8, 2, 128, 16, torch.bfloat16, seed=19 + i) for i in range(2)]
+    want = [c.run(ta) for c in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    tmps = [ta.paged_attention_workspace(c.q, c.k, c.table, max_q_len=new) for c in cs]
+    rows, lens = [i32(c.cu) for c in cs], [i32(c.lens) for c in cs]
+    torch.cuda.synchronize()
+    got = [[ta.paged_attention(c.q, c.k, c.v, c.table, rows[i], lens[i], scale=c.scale, max_q_len=new, tmp=tmps[i],
+                               stream=streams[i]) for i, c in enumerate(cs)] for _ in range(20)]
+    torch.cuda.synchronize()
+    for pair in got:
+        assert all(torch.equal(x, y) for x, y in zip(pair, want))
+    assert not any(int(tmp.view(torch.int32)[0]) for tmp in tmps)
+
+
 # ----------------------------------------------------------------- append
 @pytest.mark.parametrize("hk,d,ps,t,nhd", [(8, 128, 16, 1, False), (1, 64, 16, 77, True), (4, 256, 64, 500, False),
                                            (3, 128, 256, 1000, True)])

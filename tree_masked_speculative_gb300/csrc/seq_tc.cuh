@@ -27,7 +27,7 @@
 // (P <= 256 fits f16, the sum stays in f32), so O in TMEM is rarely rescaled.
 // Bound: one key tile of both streams is 1280 cycles of products at D = 128 (1024 at the
 // rate of wider products) and about as many issue slots of softmax; a prompt of 8192 tokens with 32 / 8
-// heads of 128 takes 443 us, 1240 TFLOP/s (66 % of the cuBLAS rate).
+// heads of 128 takes 402 us, 1369 TFLOP/s (73 % of the cuBLAS rate).
 // Every wait is bounded; a wait that gives up sets the status word, and the CTA
 // drains its copies and MMAs, frees TMEM and exits.
 #pragma once
@@ -52,7 +52,7 @@ struct Cfg {
     static constexpr int CO = NSTR * CS;                // first column of O
     static_assert(CO + NSTR * D <= 512, "TMEM");
     // Who waits for a P buffer to be read: the issuer of Q K^T (S then means the buffer is
-    // free) or the softmax warps.  D = 64, whose softmax sets the pace: 200 against 220 us
+    // free) or the softmax warps.  D = 64, whose softmax sets the pace: 189 against 206 us
     // for a prompt of 8192 tokens, 16 heads; D = 256, whose products do: 230 against 208 us
     // (4096 tokens, 24 / 4 heads); D = 128 the same.
     static constexpr bool kQkWaitsP = D == 64;
