@@ -764,3 +764,73 @@ def test_a_serving_run(ta, d, h, hk, ps, dtype):
             check(out[s], ref, spread, dt, keep[b] + new[b])
             if fresh:
                 check(other[s], ref, spread, dt, new[b])
+
+
+# ----------------------------------------------------- values that are not finite
+NAN_KEYS = [1, 17, 300]                      # one key; one alone in its block of 16; many blocks
+
+
+def nan_rows(clean, got, hit):
+    """Exactly the rows `hit` ([T, H] bool) are NaN, the others have the clean bits."""
+    hit = hit.cuda()
+    assert bool(torch.isfinite(clean).all())
+    assert bool(torch.isnan(got[hit]).all()), "a NaN logit was lost"
+    assert torch.equal(got[~hit], clean[~hit])
+
+
+@pytest.mark.parametrize("keys", NAN_KEYS)
+@pytest.mark.parametrize("new", [1, 3, 40])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("kernel", [0, 2, 3])
+def test_nan_logits_reach_the_rows_that_see_them(ta, kernel, d, new, keys):
+    """A NaN in a row's query, or in K of a key that it sees (the first, one in the middle, the last of
+    the prefix, the last of all), makes the whole row NaN."""
+    nan_case(ta, kernel, d, new, keys)
+
+
+def nan_case(ta, kernel, d, new, keys):
+    h, hk = 8, 2
+    c = Paged([keys + new - 1, 90 + new], [new, new], h, hk, d, 16, torch.bfloat16, seed=21)
+    for window in (0, 20):
+        clean = c.run(ta, kernel=kernel, window=window)
+        q = c.q.clone()
+        c.q[new - 1, 5, 3] = float("nan")
+        hit = torch.zeros(2 * new, h, dtype=torch.bool)
+        hit[new - 1, 5] = True
+        nan_rows(clean, c.run(ta, kernel=kernel, window=window), hit)
+        c.q = q
+        see = visible(new, c.lens[0], window)
+        for j in sorted({0, c.lens[0] // 2, keys - 1, c.lens[0] - 1}):
+            page, off = int(c.table[0, j // 16]), j % 16
+            was = c.k[page, 1, off, 2].clone()
+            c.k[page, 1, off, 2] = float("nan")
+            hit = torch.zeros(2 * new, h, dtype=torch.bool)
+            hit[:new, 4:] = see[:, j, None]
+            nan_rows(clean, c.run(ta, kernel=kernel, window=window), hit)
+            c.k[page, 1, off, 2] = was
+
+
+@pytest.mark.parametrize("lens", [[1, 5], [17, 3], [300, 40]])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_nan_logits_of_prompts(ta, d, lens):
+    nan_prompt(ta, 0, d, lens)
+
+
+def nan_prompt(ta, kernel, d, lens):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(22)
+    t, h, hk, cu = sum(lens), 4, 2, i32(offsets(lens))
+    q, k, v = (randn(g, t, n, d, dtype=torch.float16) for n in (h, hk, hk))
+    clean = ta.prompt_attention(q, k, v, cu, scale=0.1, kernel=kernel)
+    n = lens[0]
+    for j in sorted({0, n // 2, n - 1}):
+        for what in "qk":
+            q2, k2 = q.clone(), k.clone()
+            hit = torch.zeros(t, h, dtype=torch.bool)
+            if what == "q":
+                q2[j, 1, 0] = float("nan")
+                hit[j, 1] = True
+            else:
+                k2[j, 1, 7] = float("nan")
+                hit[j:n, 2:] = True
+            nan_rows(clean, ta.prompt_attention(q2, k2, v, cu, scale=0.1, kernel=kernel), hit)

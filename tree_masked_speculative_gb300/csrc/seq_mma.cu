@@ -338,11 +338,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D, RH>) seq_mma_kernel(co
                 w[k] = s_ml[k][row];
                 ms = fmaxf(ms, w[k].x);
             }
+            // a warp without a logit above -inf adds 0, or NaN where its logits were NaN
+            const float mu = ms == -INFINITY ? 0.0f : ms;
             float r[8] = {};
 #pragma unroll
             for (int k = 0; k < kWarps; ++k) {
-                if (w[k].x == -INFINITY) continue;
-                const float f = ex2(w[k].x - ms);
+                const float f = ex2(w[k].x - mu);
                 ls += f * w[k].y;
                 const float4 y = *reinterpret_cast<const float4 *>(s_o + (k * RR + row) * D + d);
                 const float4 z = *reinterpret_cast<const float4 *>(s_o + (k * RR + row) * D + d + 4);
