@@ -834,3 +834,16 @@ def nan_prompt(ta, kernel, d, lens):
                 k2[j, 1, 7] = float("nan")
                 hit[j:n, 2:] = True
             nan_rows(clean, ta.prompt_attention(q2, k2, v, cu, scale=0.1, kernel=kernel), hit)
+
+
+@pytest.mark.parametrize("keys", NAN_KEYS)
+@pytest.mark.parametrize("new", [1, 3, 40])
+@pytest.mark.parametrize("d", [64, 256])
+def test_nan_logits_on_the_cuda_cores(ta, d, new, keys):
+    """The same wherever the NaN stands among a row's keys, the first included."""
+    nan_case(ta, 1, d, new, keys)
+
+
+@pytest.mark.parametrize("lens", [[1, 5], [17, 3], [300, 40]])
+def test_nan_logits_of_prompts_on_the_cuda_cores(ta, lens):
+    nan_prompt(ta, 1, 128, lens)

@@ -67,8 +67,9 @@ __global__ void __launch_bounds__(kWarps * 32) seq_fma_kernel(const SeqArgs a) {
 #pragma unroll
         for (int e = 0; e < E; ++e) s = fmaf(qf[e], to_f32(k[e]), s);
         s = warp_sum(s);
-        const float mn = fmaxf(m, s);
-        const float c = mn == -INFINITY ? 1.0f : expf(m - mn), p = mn == -INFINITY ? 0.0f : expf(s - mn);
+        // relative to a finite max, so that a NaN logit is kept (fmaxf drops it) wherever it stands
+        const float mn = fmaxf(m, s), mu = mn == -INFINITY ? 0.0f : mn;
+        const float c = expf(m - mu), p = expf(s - mu);
         l = l * c + p;
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] = o[e] * c + p * to_f32(v[e]);
