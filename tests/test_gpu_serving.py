@@ -847,3 +847,26 @@ def test_nan_logits_on_the_cuda_cores(ta, d, new, keys):
 @pytest.mark.parametrize("lens", [[1, 5], [17, 3], [300, 40]])
 def test_nan_logits_of_prompts_on_the_cuda_cores(ta, lens):
     nan_prompt(ta, 1, 128, lens)
+
+
+# a contradiction that no row of q belongs to
+@pytest.mark.parametrize("kernel", FAMILIES)
+@pytest.mark.parametrize("max_q", [4, 64])
+@pytest.mark.parametrize("cu,lens", [([0, 4, 4, 12], [200, -5, 150]), ([0, 4, 4, 12], [200, 2 ** 30, 150]),
+                                     ([0, 8, 4, 12], [200, 100, 150])])
+def test_contradictions_without_rows_set_the_status(ta, cu, lens, max_q, kernel):
+    c = Paged([200, 100, 150], [4, 4, 4], 8, 2, 128, 16, torch.bfloat16, seed=11)
+    tmp = ta.paged_attention_workspace(c.q, c.k, c.table, max_q_len=max_q, kernel=kernel)
+    ta.paged_attention(c.q, c.k, c.v, c.table, i32(cu), i32(lens), scale=c.scale, max_q_len=max_q, tmp=tmp, kernel=kernel)
+    assert int(tmp.view(torch.int32)[0]) == 4
+
+
+def test_contradictions_of_more_requests_than_rows_set_the_status(ta):
+    """The last of 5000 requests, on a call of one row."""
+    c = Paged([20], [1], 1, 1, 64, 16, torch.bfloat16, seed=23)
+    table = c.table[:1].expand(5000, -1).contiguous()
+    for kernel in FAMILIES:
+        tmp = ta.paged_attention_workspace(c.q, c.k, table, max_q_len=1, kernel=kernel)
+        ta.paged_attention(c.q, c.k, c.v, table, i32([0] + [1] * 5000), i32([20] + [0] * 4998 + [-1]), scale=1.0, max_q_len=1,
+                           tmp=tmp, kernel=kernel)
+        assert int(tmp.view(torch.int32)[0]) == 4

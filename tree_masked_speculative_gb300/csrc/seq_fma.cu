@@ -14,6 +14,9 @@ __global__ void __launch_bounds__(kWarps * 32) seq_fma_kernel(const SeqArgs a) {
     constexpr int E = D / 32;                     // dimensions per lane: lane * E ..
     pdl_wait();
     const int lane = threadIdx.x & 31;
+    // every request is checked, those without rows too
+    for (long long b = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; b < a.B; b += static_cast<long long>(gridDim.x) * blockDim.x)
+        if (seq_request(a, static_cast<int>(b)).bad) atomicOr(a.status, kSeqBadLength);
     const long long row = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
     if (row >= static_cast<long long>(a.T) * a.H) return;
     const int t = static_cast<int>(row / a.H), h = static_cast<int>(row % a.H), kh = h / a.g;
@@ -24,7 +27,6 @@ __global__ void __launch_bounds__(kWarps * 32) seq_fma_kernel(const SeqArgs a) {
         if (__ldg(a.cu + mid) <= t) lo = mid; else hi = mid;
     }
     const SeqReq r = seq_request(a, lo);
-    if (r.bad && lane == 0) atomicOr(a.status, kSeqBadLength);
     const int i = t - r.q0;
     if (i < 0 || i >= r.qn) return;               // behind the last sequence: left as it was
 
