@@ -870,3 +870,37 @@ def test_contradictions_of_more_requests_than_rows_set_the_status(ta):
         ta.paged_attention(c.q, c.k, c.v, table, i32([0] + [1] * 5000), i32([20] + [0] * 4998 + [-1]), scale=1.0, max_q_len=1,
                            tmp=tmp, kernel=kernel)
         assert int(tmp.view(torch.int32)[0]) == 4
+
+
+# --------------------------------------------------------------- small weights
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("new,kernel", [(1, 0), (2, 1), (1, 2), (40, 0)])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_many_small_weights_beside_a_large_one(ta, d, new, kernel, dtype):
+    """One key takes almost all the weight, thousands have about 2^-25 of it each and the values
+    that count.  The tolerance of check() but for its last term: with P held 2^7 higher an f16
+    weight below the normal range is off by 2^-25 (half a subnormal step) 2^-7 = 2^-32."""
+    dt, n, batch, hk = DT[dtype], 6000, 32, 2
+    g = torch.Generator(device="cuda")
+    g.manual_seed(24)
+    ps = 64
+    pages = -(-n // ps)
+    k = torch.zeros(pages, hk, ps, d, dtype=dt, device="cuda")
+    v = torch.zeros(pages, hk, ps, d, dtype=dt, device="cuda")
+    # logits 8 k: 8 for key 0, 17.4 to 17.8 lower (2^-25.1 to 2^-25.7) for the others
+    k[..., 0] = (-1.175 - 0.05 * torch.rand(pages, hk, ps, generator=g, device="cuda")).to(dt)
+    v.copy_(torch.rand(v.shape, generator=g, device="cuda") * 32 + 32)
+    k[0, :, 0, 0], v[0, :, 0] = 1.0, 0.0
+    q = torch.zeros(batch * new, hk, d, dtype=dt, device="cuda")
+    q[..., 0] = 8.0
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").expand(batch, -1).contiguous()
+    out = ta.paged_attention(q, k, v, table, i32([new * b for b in range(batch + 1)]), i32([n] * batch), scale=1.0,
+                             max_q_len=new, kernel=kernel)
+    keys, values = (x.transpose(1, 2).reshape(-1, hk, d)[:n] for x in (k, v))
+    ref, spread = reference(q[:new], keys, values, visible(new, n), 1.0)
+    half = torch.finfo(dt).eps / 2
+    tol = half * ref.abs() + (half + 2.0 ** -12) * spread + (n * 2.0 ** -32 * 64 if dtype == "f16" else 0)
+    # the output's own subnormal steps (f16, below 2^-14)
+    tol = tol + 2.0 ** -25
+    err = (out.view(batch, new, hk, d).double() - ref).abs()
+    assert bool((err <= tol).all()), "off by %.3g, values around %.3g" % (err.max().item(), ref.mean().item())

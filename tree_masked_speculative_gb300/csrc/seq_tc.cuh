@@ -24,7 +24,7 @@
 //               rows that do see such an element get NaN in its column at the end
 //   4 warps per stream  softmax and epilogue, one row a thread
 // The running max moves only when a row's max exceeds it by more than 2^8
-// (P <= 256 fits f16, the sum stays in f32), so O in TMEM is rarely rescaled.
+// (P <= 2^15 fits f16, see kRaise; the sum stays in f32), so O in TMEM is rarely rescaled.
 // Bound: one key tile of both streams is 1280 cycles of products at D = 128 (1024 at the
 // rate of wider products) and about as many issue slots of softmax; a prompt of 8192 tokens with 32 / 8
 // heads of 128 takes 402 us, 1369 TFLOP/s (73 % of the cuBLAS rate).
@@ -78,6 +78,10 @@ constexpr int kUnitCost = kSeqTcUnitCost;      // of the schedule: a unit's star
 constexpr int kPoison = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;
+// P and l of f16 rows are held 2^7 higher (P <= 2^15): a weight is subnormal only below 2^-21 of
+// the running max's, and off by 2^-32 of it at most (at 2^0 weights up to 2^-25 were lost).
+template <bool BF16>
+constexpr float kRaise = BF16 ? 0.0f : 7.0f;
 
 struct Misc {
     uint64_t k_full[4], k_empty[4], v_full[4], v_ready[4], v_empty[4];
@@ -725,7 +729,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                     float l_tile;
 #pragma unroll 1
                     for (;;) {
-                        const float m_use = m_run == -INFINITY ? 0.0f : m_run;
+                        const float m_use = m_run == -INFINITY ? 0.0f : m_run - kRaise<BF16>;
                         const uint64_t sc = pack64(scale2, scale2), mm = pack64(-m_use, -m_use);
                         uint64_t sum[2] = {0, 0};
                         float mx[2] = {-INFINITY, -INFINITY};
