@@ -904,3 +904,21 @@ def test_many_small_weights_beside_a_large_one(ta, d, new, kernel, dtype):
     tol = tol + 2.0 ** -25
     err = (out.view(batch, new, hk, d).double() - ref).abs()
     assert bool((err <= tol).all()), "off by %.3g, values around %.3g" % (err.max().item(), ref.mean().item())
+
+
+# ------------------------------------------------------------------ streams, arguments
+def test_stream_handle_zero_is_the_default_stream(ta):
+    """0 is the handle of the default stream, not a request for a stream of its own."""
+    c = Paged([300, 40], [3, 3], 8, 2, 128, 16, torch.bfloat16, seed=25)
+    want = c.run(ta)
+    q, tmp, out = c.q, ta.paged_attention_workspace(c.q, c.k, c.table, max_q_len=3), torch.zeros_like(c.q)
+    cu, lens = i32(c.cu), i32(c.lens)
+    late, side = torch.zeros_like(q), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)                 # the default stream is about 10 ms behind
+    late.copy_(q)
+    with torch.cuda.stream(side):
+        ta.paged_attention(late, c.k, c.v, c.table, cu, lens, scale=c.scale, max_q_len=3, tmp=tmp, out=out, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    assert torch.cuda.default_stream().cuda_stream == 0

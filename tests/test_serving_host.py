@@ -235,3 +235,11 @@ def test_a_stream_of_another_device_is_refused(ta, monkeypatch):
         ta._as_stream(Stream(0), 1)
     ta._as_stream(0x1234, 1)
     assert made == [(0x1234, 1)]
+
+
+def test_stream_handles_of_the_default_stream(ta, monkeypatch):
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: ("default", device))
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: ("external", handle, device))
+    for handle in (0, 1):
+        assert ta._as_stream(handle, 1) == ("default", 1)
+    assert ta._as_stream(0x1230, 1) == ("external", 0x1230, 1)

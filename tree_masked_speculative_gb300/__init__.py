@@ -467,9 +467,12 @@ _prompt_entry = _Entry("prompt_attn_fwd", "7If8Q", 6)
 
 
 def _as_stream(stream, dev: int) -> torch.cuda.Stream:
-    """`stream` (a torch stream or a handle) on the tensors' device."""
+    """`stream` (a torch stream or a handle) on the tensors' device.  The handles 0
+    and cudaStreamLegacy (1) are the default stream's: torch would make a new stream
+    of a 0."""
     if not isinstance(stream, torch.cuda.Stream):
-        return torch.cuda.ExternalStream(int(stream), device=dev)
+        handle = int(stream)
+        return torch.cuda.default_stream(dev) if handle in (0, 1) else torch.cuda.ExternalStream(handle, device=dev)
     if stream.device.index != dev:
         raise ValueError("stream is on %s, the tensors are on cuda:%d" % (stream.device, dev))
     return stream
