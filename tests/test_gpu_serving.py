@@ -922,3 +922,11 @@ def test_stream_handle_zero_is_the_default_stream(ta):
     torch.cuda.synchronize()
     assert torch.equal(out, want)
     assert torch.cuda.default_stream().cuda_stream == 0
+
+
+def test_parents_of_no_token_are_refused(ta):
+    """An empty or too short `parents` is an error, not the causal rule."""
+    c = Paged([300, 40], [3, 3], 8, 2, 128, 16, torch.bfloat16, seed=26, tree=True)
+    for bad in (torch.empty(0, dtype=torch.int32, device="cuda"), c.flat_parents()[:5]):
+        with pytest.raises((ValueError, ta.TreeAttentionError), match="parents"):
+            c.run(ta, parents=bad)

@@ -668,6 +668,8 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         raise ValueError("q and the caches must have one head dimension")
     if block_table.dim() != 2 or cu_q.numel() != block_table.shape[0] + 1 or kv_lens.numel() != block_table.shape[0]:
         raise ValueError("block_table must be [batch, max_pages], cu_q [batch + 1] and kv_lens [batch]")
+    if parents is not None and parents.numel() < t:         # (an empty one would pass for none)
+        raise ValueError("parents must be [%d]" % t)
     batch, width = block_table.shape
     if tmp is None:
         tmp = _workspace(paged_attn_workspace_bytes(PagedParams(batch, h, hk, d, t, max_q_len, window, ps, n_pages, width,
