@@ -930,3 +930,17 @@ def test_parents_of_no_token_are_refused(ta):
     for bad in (torch.empty(0, dtype=torch.int32, device="cuda"), c.flat_parents()[:5]):
         with pytest.raises((ValueError, ta.TreeAttentionError), match="parents"):
             c.run(ta, parents=bad)
+
+
+def test_workspaces_of_windowed_calls(ta):
+    """A call whose work is in range only with its window has a workspace of that window."""
+    t = 2 ** 23
+    q = torch.empty(t, 2, 64, dtype=torch.float16, device="cuda")
+    with pytest.raises(ta.TreeAttentionError, match="tokens x keys"):
+        ta.prompt_attention_workspace(q, q, i32([0, t]))
+    assert ta.prompt_attention_workspace(q, q, i32([0, t]), window=4096).numel() > 64
+    k = torch.empty(4, 2, 256, 64, dtype=torch.float16, device="cuda")
+    table = torch.zeros(1, 2 ** 20, dtype=torch.int32, device="cuda")
+    with pytest.raises(ta.TreeAttentionError, match="tokens x keys"):
+        ta.paged_attention_workspace(q, k, table, max_q_len=t)
+    assert ta.paged_attention_workspace(q, k, table, max_q_len=t, window=4096).numel() > 64

@@ -620,20 +620,23 @@ def _workspace(nbytes: int, device) -> torch.Tensor:
 
 
 def paged_attention_workspace(q: torch.Tensor, k_cache: torch.Tensor, block_table: torch.Tensor, *,
-                              max_q_len: int, kernel: int = KERNEL_AUTO, scale: float = 1.0) -> torch.Tensor:
+                              max_q_len: int, kernel: int = KERNEL_AUTO, scale: float = 1.0,
+                              window: int = 0) -> torch.Tensor:
     """A tmp buffer for paged_attention calls of these shapes (its first 32-bit
-    word, zero here, is the status word; calls that overlap must not share it)."""
+    word, zero here, is the status word; calls that overlap must not share it).
+    The window changes no size, but a call may be in range only with it."""
     n_pages, hk, ps, d = k_cache.shape
-    p = PagedParams(block_table.shape[0], q.shape[1], hk, d, q.shape[0], max_q_len, 0, ps, n_pages,
+    p = PagedParams(block_table.shape[0], q.shape[1], hk, d, q.shape[0], max_q_len, window, ps, n_pages,
                     block_table.shape[1], kernel, scale)
     with torch.cuda.device(_device_of(q)):
         return _workspace(paged_attn_workspace_bytes(p), q.device)
 
 
 def prompt_attention_workspace(q: torch.Tensor, k: torch.Tensor, cu_seqlens: torch.Tensor, *,
-                               kernel: int = KERNEL_AUTO, scale: float = 1.0) -> torch.Tensor:
-    """A tmp buffer for prompt_attention calls of these shapes."""
-    p = PromptParams(cu_seqlens.numel() - 1, q.shape[1], k.shape[1], q.shape[2], q.shape[0], 0, kernel, scale)
+                               kernel: int = KERNEL_AUTO, scale: float = 1.0, window: int = 0) -> torch.Tensor:
+    """A tmp buffer for prompt_attention calls of these shapes (see
+    paged_attention_workspace)."""
+    p = PromptParams(cu_seqlens.numel() - 1, q.shape[1], k.shape[1], q.shape[2], q.shape[0], window, kernel, scale)
     with torch.cuda.device(_device_of(q)):
         return _workspace(prompt_attn_workspace_bytes(p), q.device)
 
