@@ -243,3 +243,16 @@ def test_stream_handles_of_the_default_stream(ta, monkeypatch):
     for handle in (0, 1):
         assert ta._as_stream(handle, 1) == ("default", 1)
     assert ta._as_stream(0x1230, 1) == ("external", 0x1230, 1)
+
+
+@pytest.mark.parametrize("kw,status,frag", [(dict(head_dim=80), 1, "head_dim"), (dict(batch=65536), 4, "index range"),
+                                            (dict(n_heads=258), 4, "128 query heads"), ({}, 5, "no CUDA device"),
+                                            (dict(tokens=0), 5, "no CUDA device")])
+def test_a_refused_workspace_names_the_status(ta, kw, status, frag):
+    if status == 5 and torch.cuda.is_available():
+        pytest.skip("a device is visible")
+    for p in (ta.PagedParams(**{**PAGED, **kw}), ta.PromptParams(**{**PROMPT, **kw})):
+        before = ta.ta_launch_count()
+        with pytest.raises(ta.TreeAttentionError, match=frag) as e:
+            ta._workspace(p, torch.device("cuda"))
+        assert e.value.status == status and ta.ta_launch_count() == before

@@ -32,7 +32,7 @@ __all__ = [
     "prompt_attention_workspace", "prompt_attn_workspace_bytes",
 ]
 
-TA_OK = 0
+TA_OK, TA_ERR_CUDA = 0, 5
 TA_F32, TA_F16, TA_BF16, TA_U32, TA_I32, TA_I64 = 0, 1, 2, 3, 4, 5
 KERNEL_AUTO, KERNEL_CUDA_CORES, KERNEL_TENSOR_CORES, KERNEL_WARP_MMA = 0, 1, 2, 3
 MASK_DENSE, MASK_CAUSAL, MASK_PARENTS = 0, 1, 2
@@ -611,9 +611,17 @@ def prompt_attn_workspace_bytes(p: PromptParams) -> int:
     return int(lib.prompt_attn_workspace_bytes(ctypes.byref(p)))
 
 
-def _workspace(nbytes: int, device) -> torch.Tensor:
+def _workspace(p, device) -> torch.Tensor:
+    """The tmp buffer of a call with parameters `p`, its status word zero."""
+    query, call, n_bufs = ((paged_attn_workspace_bytes, lib.paged_attn_fwd, 9) if isinstance(p, PagedParams) else
+                           (prompt_attn_workspace_bytes, lib.prompt_attn_fwd, 6))
+    nbytes = query(p)
     if nbytes >= 2 ** 63:
-        raise TreeAttentionError(1, ta_last_error())
+        why = ta_last_error()
+        # the call itself, without buffers, is refused by the same check and says with which status;
+        # parameters that it takes lack a device to size the workspace for
+        status = call(ctypes.byref(p), *[None] * n_bufs, None)
+        raise TreeAttentionError(status if status != TA_OK and ta_last_error() == why else TA_ERR_CUDA, why)
     ws = torch.empty((nbytes + 3) // 4, dtype=torch.float32, device=device)
     ws[:1].zero_()                                   # the status word
     return ws
@@ -629,7 +637,7 @@ def paged_attention_workspace(q: torch.Tensor, k_cache: torch.Tensor, block_tabl
     p = PagedParams(block_table.shape[0], q.shape[1], hk, d, q.shape[0], max_q_len, window, ps, n_pages,
                     block_table.shape[1], kernel, scale)
     with torch.cuda.device(_device_of(q)):
-        return _workspace(paged_attn_workspace_bytes(p), q.device)
+        return _workspace(p, q.device)
 
 
 def prompt_attention_workspace(q: torch.Tensor, k: torch.Tensor, cu_seqlens: torch.Tensor, *,
@@ -638,7 +646,7 @@ def prompt_attention_workspace(q: torch.Tensor, k: torch.Tensor, cu_seqlens: tor
     paged_attention_workspace)."""
     p = PromptParams(cu_seqlens.numel() - 1, q.shape[1], k.shape[1], q.shape[2], q.shape[0], window, kernel, scale)
     with torch.cuda.device(_device_of(q)):
-        return _workspace(prompt_attn_workspace_bytes(p), q.device)
+        return _workspace(p, q.device)
 
 
 def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
@@ -675,8 +683,7 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         raise ValueError("parents must be [%d]" % t)
     batch, width = block_table.shape
     if tmp is None:
-        tmp = _workspace(paged_attn_workspace_bytes(PagedParams(batch, h, hk, d, t, max_q_len, window, ps, n_pages, width,
-                                                                kernel, scale)), q.device)
+        tmp = _workspace(PagedParams(batch, h, hk, d, t, max_q_len, window, ps, n_pages, width, kernel, scale), q.device)
     _paged_entry(dev, batch, h, hk, d, t, max_q_len, window, ps, n_pages, width, kernel, scale, *qs, *os_, *cs, *qb, *kb,
                  *vb, *_flat(block_table, dev), *_flat(cu_q, dev), *_flat(kv_lens, dev), *_flat(parents, dev),
                  *_flat(tmp, dev), *ob)
@@ -708,7 +715,7 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
         raise ValueError("k and v must be [%d, Hk, %d]" % (t, d))
     batch, hk = cu_seqlens.numel() - 1, k.shape[1]
     if tmp is None:
-        tmp = _workspace(prompt_attn_workspace_bytes(PromptParams(max(batch, 0), h, hk, d, t, window, kernel, scale)), q.device)
+        tmp = _workspace(PromptParams(max(batch, 0), h, hk, d, t, window, kernel, scale), q.device)
     _prompt_entry(dev, batch, h, hk, d, t, window, kernel, scale, *qs, *os_, *ks, *vs, *qb, *kb, *vb,
                   *_flat(cu_seqlens, dev), *_flat(tmp, dev), *ob)
     return out
