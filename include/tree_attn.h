@@ -518,9 +518,11 @@ size_t paged_attn_workspace_bytes(const ta_paged_params *p);
  * tree_mask_build per request: parents[cu[b] + i] is the parent's index inside
  * the request's chunk; a chain ends at a value outside [0, current node)):
  * the prefix j < kv_lens[b] - q_len, the node's ancestors and itself.
- * A row that sees no key gives zeros.  K and V at positions a row does not see
+ * A row that sees no key gives zeros; so do the tokens before position 0 where
+ * kv_lens[b] < q_len, which is no error.  K and V at positions a row does not see
  * do not touch its result, whatever they hold.  A V value that is infinite or
- * NaN makes the rows that see it NaN or infinite in its column.
+ * NaN makes the rows that see it NaN or infinite in its column; a logit that is NaN
+ * (a NaN in the row's q, or in a key that it sees) makes the whole row NaN.
  *   q, out      [tokens, n_heads, head_dim], the cache's type
  *   k_cache, v_cache   as above
  *   table       [batch, max_pages] i32; cells past a request's last page, and with a

@@ -659,8 +659,12 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     K/V; kv_lens [B] counts all keys.  Token i of q_len sees the keys up to its own
     position kv_len - q_len + i (the last `window` of them), or, with `parents`
     (int32 [T], each request's draft tree by index inside its chunk), the prefix,
-    its ancestors and itself.  Returns out [T, H, D] in q's type; rows behind the
-    last request are not written."""
+    its ancestors and itself; tokens before position 0 (kv_len < q_len) see nothing
+    and give zeros.  Returns out [T, H, D] in q's type; rows behind the last request
+    are not written.  What only the GPU sees (a page outside the cache, a length out of
+    range, a wait that gave up) is ORed into the first 32-bit word of `tmp`, and the rows
+    concerned are then not valid: to learn of it, pass a `tmp` from
+    paged_attention_workspace.  Without one it goes unreported."""
     dev = _device_of(q)
     if stream is not None or dev != _this_device():
         return _elsewhere(paged_attention, dev, stream, (q, k_cache, v_cache, block_table, cu_q, kv_lens),
@@ -697,7 +701,9 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     k and v [T, Hk, D] (any token and head strides, as slices of one projection),
     cu_seqlens [B + 1] int32 on the device.  Row i of a prompt sees its rows up to
     i (the last `window` of them).  Returns out [T, H, D] in q's type; rows behind
-    the last prompt are not written."""
+    the last prompt are not written.  Errors that only the GPU sees are ORed into the
+    first 32-bit word of `tmp` (see paged_attention); without a `tmp` from
+    prompt_attention_workspace they go unreported."""
     dev = _device_of(q)
     if stream is not None or dev != _this_device():
         return _elsewhere(prompt_attention, dev, stream, (q, k, v, cu_seqlens),
