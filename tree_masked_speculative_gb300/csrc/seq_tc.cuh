@@ -168,7 +168,8 @@ __device__ __forceinline__ uint32_t odd16(uint32_t w) {
 // Wait for a phase, about 2 s at most; false: given up.  Six instructions and no call:
 // the instruction cache holds the loops of all roles only while they are small (the
 // same kernel with 100 bytes more a wait took 1.25 times as long), and a call would
-// spill what the softmax warps hold.
+// spill what the softmax warps hold.  The lanes of a warp may see a phase end at different
+// polls, so the branches are not uniform.
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -176,10 +177,10 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity) {
         "mov.u32 n, 0;\n\t"
         "L:\n\t"
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
-        "@p bra.uni D;\n\t"
+        "@p bra D;\n\t"
         "add.u32 n, n, 1;\n\t"
         "setp.lt.u32 q, n, 2097152;\n\t"
-        "@q bra.uni L;\n\t"
+        "@q bra L;\n\t"
         "D:\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
@@ -665,9 +666,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
         int tn = 0, vn = 0;                             // tiles of this stream, tiles of the CTA
         bool ok = true;
         // (the lanes' outcomes are joined once a tile: a vote at every wait took 443 us for a
-        // prompt of 8192 tokens against 423)
+        // prompt of 8192 tokens against 423; the warp itself is joined here, since the TMEM loads
+        // and stores behind a wait need all of it: 0.7 % of the same time)
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             ok = wait_bar(bar, parity) && ok;
+            __syncwarp();
         };
         SeqPiece p;
 #pragma unroll 1
