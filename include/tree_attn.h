@@ -629,6 +629,20 @@ ta_status ta_test_quant_sdpa_fwd_wait_limit(uint32_t first_wait_polls, const ta_
                                             const ta_buf *mask_bool, const ta_buf *mask_float,
                                             const ta_buf *tmp, const ta_buf *out, void *stream);
 
+/*
+ * Test hook, not for production use: paged_attn_fwd on the tensor-core kernel
+ * (p->kernel must resolve to it, else TA_ERR_UNSUPPORTED) with every wait bounded
+ * by `wait_polls` polls, of about 1 us each, instead of the normal 2^21.  0 lets a wait
+ * that does not find its phase completed by the first poll give up.  It exercises the
+ * failure path without any fault: a CTA ORs 1 into the status word, lets its copies and
+ * products end (waiting with the normal bound), frees its tensor memory and returns.  The output
+ * is then not valid.  Same buffers and checks as paged_attn_fwd.
+ */
+ta_status ta_test_paged_attn_fwd_wait_limit(uint32_t wait_polls, const ta_paged_params *p, const ta_buf *q,
+                                            const ta_buf *k_cache, const ta_buf *v_cache, const ta_buf *table,
+                                            const ta_buf *cu, const ta_buf *kv_lens, const ta_buf *parents,
+                                            const ta_buf *tmp, const ta_buf *out, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

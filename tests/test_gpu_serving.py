@@ -944,3 +944,30 @@ def test_workspaces_of_windowed_calls(ta):
     with pytest.raises(ta.TreeAttentionError, match="tokens x keys"):
         ta.paged_attention_workspace(q, k, table, max_q_len=t)
     assert ta.paged_attention_workspace(q, k, table, max_q_len=t, window=4096).numel() > 64
+
+
+# ------------------------------------------------------------- waits that give up
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_waits_that_give_up_set_the_status(ta, d, tree):
+    """Every wait bounded by a few polls: CTAs give up at different places, let their copies and
+    products end, say so in the status word and return; the next call on the same workspace is right."""
+    c = Paged([900, 60, 3000, 61], [60, 60, 33, 7], 8, 2, d, 16, torch.bfloat16, seed=27, tree=tree)
+    want = c.run(ta, kernel=2)
+    tmp = ta.paged_attention_workspace(c.q, c.k, c.table, max_q_len=60, kernel=2)
+    word = tmp.view(torch.int32)
+    cu, lens, parents = i32(c.cu), i32(c.lens), c.flat_parents()
+    p = ta.PagedParams(4, 8, 2, d, c.q.shape[0], 60, 0, 16, c.k.shape[0], c.table.shape[1], 2, c.scale)
+    for polls in (0, 0, 1, 2, 4, 8):
+        out = torch.zeros_like(c.q)
+        ta.ta_test_paged_attn_fwd_wait_limit(polls, p, c.q, c.k, c.v, c.table, cu, lens, parents, tmp, out)
+        torch.cuda.synchronize()
+        status = int(word[0])
+        assert status == 1 if polls == 0 else status in (0, 1)
+        assert status or torch.equal(out, want)
+        word[0] = 0
+        assert torch.equal(c.run(ta, kernel=2, tmp=tmp), want)
+        assert int(word[0]) == 0
+    with pytest.raises(ta.TreeAttentionError, match="tensor-core kernel only"):
+        p.kernel = 1
+        ta.ta_test_paged_attn_fwd_wait_limit(0, p, c.q, c.k, c.v, c.table, cu, lens, parents, tmp, out)

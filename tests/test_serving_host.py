@@ -256,3 +256,13 @@ def test_a_refused_workspace_names_the_status(ta, kw, status, frag):
         with pytest.raises(ta.TreeAttentionError, match=frag) as e:
             ta._workspace(p, torch.device("cuda"))
         assert e.value.status == status and ta.ta_launch_count() == before
+
+
+def test_the_wait_limit_hook_takes_the_tensor_core_kernel_alone(ta):
+    f16, i32 = _b(ta, ta.TA_F16), _b(ta, ta.TA_I32)
+    bufs = [ctypes.byref(b) for b in (f16, f16, f16, i32, i32, i32)] + [None, ctypes.byref(_b(ta, ta.TA_F32)), ctypes.byref(f16)]
+    for kernel in (0, 1, 3):                    # 16 rows a KV head: the warp-MMA kernel, or the CUDA cores
+        p, before = ta.PagedParams(**{**PAGED, "kernel": kernel}), ta.ta_launch_count()
+        assert ta.lib.ta_test_paged_attn_fwd_wait_limit(0, ctypes.byref(p), *bufs, None) == 4
+        assert "tensor-core kernel only" in ta.ta_last_error() and ta.ta_launch_count() == before
+    assert ta.lib.ta_test_paged_attn_fwd_wait_limit(0, None, *bufs, None) == 1

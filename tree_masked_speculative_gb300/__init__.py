@@ -29,7 +29,7 @@ __all__ = [
     "tree_mask_build", "TreeOptions", "KERNEL_AUTO", "KERNEL_CUDA_CORES", "KERNEL_TENSOR_CORES",
     "PlanParams", "AppendParams", "PagedParams", "PromptParams", "PagedStep", "paged_plan", "paged_append",
     "paged_attention", "paged_attention_workspace", "paged_attn_workspace_bytes", "prompt_attention",
-    "prompt_attention_workspace", "prompt_attn_workspace_bytes",
+    "prompt_attention_workspace", "prompt_attn_workspace_bytes", "ta_test_paged_attn_fwd_wait_limit",
 ]
 
 TA_OK, TA_ERR_CUDA = 0, 5
@@ -162,6 +162,8 @@ def _load() -> ctypes.CDLL:
     L.paged_attn_workspace_bytes.restype = ctypes.c_size_t
     L.paged_attn_fwd.argtypes = [ctypes.POINTER(PagedParams)] + [B] * 9 + [P]
     L.paged_attn_fwd.restype = ctypes.c_int
+    L.ta_test_paged_attn_fwd_wait_limit.argtypes = [u32, ctypes.POINTER(PagedParams)] + [B] * 9 + [P]
+    L.ta_test_paged_attn_fwd_wait_limit.restype = ctypes.c_int
     L.prompt_attn_workspace_bytes.argtypes = [ctypes.POINTER(PromptParams)]
     L.prompt_attn_workspace_bytes.restype = ctypes.c_size_t
     L.prompt_attn_fwd.argtypes = [ctypes.POINTER(PromptParams)] + [B] * 6 + [P]
@@ -692,6 +694,16 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
                  *vb, *_flat(block_table, dev), *_flat(cu_q, dev), *_flat(kv_lens, dev), *_flat(parents, dev),
                  *_flat(tmp, dev), *ob)
     return out
+
+
+def ta_test_paged_attn_fwd_wait_limit(wait_polls: int, p: PagedParams, q, k_cache, v_cache, block_table, cu_q, kv_lens,
+                                      parents, tmp, out, stream=None):
+    """Test hook: paged_attn_fwd (tensor-core kernel, contiguous tensors) whose waits
+    give up after `wait_polls` polls of about 1 us."""
+    i32 = TA_I32
+    _check(lib.ta_test_paged_attn_fwd_wait_limit(wait_polls, ctypes.byref(p), buf(q), buf(k_cache), buf(v_cache),
+                                                 buf(block_table, i32), buf(cu_q, i32), buf(kv_lens, i32),
+                                                 buf(parents, i32), buf(tmp), buf(out), _stream(stream)))
 
 
 def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, *, scale: float,

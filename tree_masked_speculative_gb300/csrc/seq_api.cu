@@ -236,7 +236,7 @@ bool kv_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap *m, const SeqA
     return encode_16bit(encode, m, a, ptr, paged ? 5 : 4, dims, str, box);
 }
 
-ta_status run_seq(const char *op, const SeqArgs &a, int family, void *ws, cudaStream_t s) {
+ta_status run_seq(const char *op, const SeqArgs &a, int family, void *ws, cudaStream_t s, uint32_t polls = kSeqWaitPolls) {
     cudaError_t e;
     if (family == TA_KERNEL_CUDA_CORES) {
         e = launch_seq_fma(a, s);
@@ -245,6 +245,7 @@ ta_status run_seq(const char *op, const SeqArgs &a, int family, void *ws, cudaSt
     } else {
         SeqTcPlan pl;
         pl.G = device_sm_count();
+        pl.polls = polls;
         pl.ws = ws;
         const auto encode = tensor_map_encoder();
         if (encode == nullptr) SEQ_FAIL(TA_ERR_CUDA, "%s: cuTensorMapEncodeTiled is not available", op);
@@ -395,11 +396,15 @@ TA_EXPORT size_t prompt_attn_workspace_bytes(const ta_prompt_params *p) {
     return ws ? ws : SIZE_MAX;
 }
 
-TA_EXPORT ta_status paged_attn_fwd(const ta_paged_params *pp, const ta_buf *q, const ta_buf *k_cache,
-                                   const ta_buf *v_cache, const ta_buf *table, const ta_buf *cu, const ta_buf *kv_lens,
-                                   const ta_buf *parents, const ta_buf *tmp, const ta_buf *out, void *stream) {
+// paged_attn_fwd; `polls` bounds the tensor-core kernel's waits (hook: the test entry point, which
+// takes that kernel alone).
+static ta_status paged_fwd(const ta_paged_params *pp, const ta_buf *q, const ta_buf *k_cache, const ta_buf *v_cache,
+                           const ta_buf *table, const ta_buf *cu, const ta_buf *kv_lens, const ta_buf *parents,
+                           const ta_buf *tmp, const ta_buf *out, void *stream, uint32_t polls, bool hook) {
     const char *op = "paged_attn";
     SEQ_TRY(check_paged(pp));
+    if (hook && paged_family(pp) != TA_KERNEL_TENSOR_CORES)
+        SEQ_FAIL(TA_ERR_UNSUPPORTED, "paged_attn: the wait-limit hook is for the tensor-core kernel only");
     ta_paged_params p = *pp;
     const bool tree = !is_absent(parents);
     if (tree && p.window != 0) SEQ_FAIL(TA_ERR_INVALID_ARGUMENT, "paged_attn: window must be 0 with parents");
@@ -465,7 +470,20 @@ TA_EXPORT ta_status paged_attn_fwd(const ta_paged_params *pp, const ta_buf *q, c
     a.k_sh = a.v_sh = static_cast<long long>(p.head_stride);
     a.scale = p.scale;
     if (ws == 0) SEQ_FAIL(TA_ERR_CUDA, "%s: no CUDA device", op);
-    return run_seq(op, a, paged_family(&p), tmp->ptr, static_cast<cudaStream_t>(stream));
+    return run_seq(op, a, paged_family(&p), tmp->ptr, static_cast<cudaStream_t>(stream), polls);
+}
+
+TA_EXPORT ta_status paged_attn_fwd(const ta_paged_params *p, const ta_buf *q, const ta_buf *k_cache,
+                                   const ta_buf *v_cache, const ta_buf *table, const ta_buf *cu, const ta_buf *kv_lens,
+                                   const ta_buf *parents, const ta_buf *tmp, const ta_buf *out, void *stream) {
+    return paged_fwd(p, q, k_cache, v_cache, table, cu, kv_lens, parents, tmp, out, stream, kSeqWaitPolls, false);
+}
+
+TA_EXPORT ta_status ta_test_paged_attn_fwd_wait_limit(uint32_t wait_polls, const ta_paged_params *p, const ta_buf *q,
+                                                      const ta_buf *k_cache, const ta_buf *v_cache, const ta_buf *table,
+                                                      const ta_buf *cu, const ta_buf *kv_lens, const ta_buf *parents,
+                                                      const ta_buf *tmp, const ta_buf *out, void *stream) {
+    return paged_fwd(p, q, k_cache, v_cache, table, cu, kv_lens, parents, tmp, out, stream, wait_polls, true);
 }
 
 TA_EXPORT ta_status prompt_attn_fwd(const ta_prompt_params *pp, const ta_buf *q, const ta_buf *k, const ta_buf *v,

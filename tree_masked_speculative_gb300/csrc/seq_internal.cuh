@@ -67,9 +67,12 @@ __device__ __forceinline__ SeqReq seq_request(const SeqArgs &a, int b) {
 
 cudaError_t launch_seq_fma(const SeqArgs &a, cudaStream_t s);
 
+// Polls (about 1 us each) after which a wait of the tensor-core kernel gives up.
+constexpr uint32_t kSeqWaitPolls = 1u << 21;
 // Tensor-core kernel: grid size, workspace and the tensor maps of K and V.
 struct SeqTcPlan {
     int G;
+    uint32_t polls;     // bound of its waits (kSeqWaitPolls but for a test)
     void *ws;
     CUtensorMap q, k, v;
 };

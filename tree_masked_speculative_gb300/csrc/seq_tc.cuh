@@ -105,6 +105,7 @@ struct Args {
     SeqWs ws;
     uint32_t *poison;     // [G][kPoison][ROWS][D / 32]
     int tpt, G;
+    uint32_t polls;       // of every wait, see wait_bar
     uint32_t g_inv;       // ceil(2^16 / g): row / g = row * g_inv >> 16, exact for rows < 256 and g <= 128
 };
 struct Maps {
@@ -165,12 +166,12 @@ __device__ __forceinline__ uint32_t odd16(uint32_t w) {
     return BF16 ? (w & 0x7f807f80u) + 0x00800080u : (w & 0x7c007c00u) + 0x04000400u;
 }
 
-// Wait for a phase, about 2 s at most; false: given up.  Six instructions and no call:
+// Wait for a phase, `polls` polls of about 1 us at most; false: given up.  Six instructions and no call:
 // the instruction cache holds the loops of all roles only while they are small (the
 // same kernel with 100 bytes more a wait took 1.25 times as long), and a call would
 // spill what the softmax warps hold.  The lanes of a warp may see a phase end at different
 // polls, so the branches are not uniform.
-__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity) {
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, uint32_t polls) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
@@ -179,12 +180,12 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity) {
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
         "@p bra D;\n\t"
         "add.u32 n, n, 1;\n\t"
-        "setp.lt.u32 q, n, 2097152;\n\t"
+        "setp.lt.u32 q, n, %3;\n\t"
         "@q bra L;\n\t"
         "D:\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity & 1u)
+        : "r"(smem_u32(bar)), "r"(parity & 1u), "r"(polls)
         : "memory");
     return ok != 0;
 }
@@ -194,9 +195,6 @@ __device__ __forceinline__ bool poll_bar(uint64_t *bar, uint32_t parity) {
     asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity & 1u) : "memory");
     return ok != 0;
 }
-// The same for a whole warp, one outcome.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_bar(bar, parity)) != 0; }
-
 // Registers of this warpgroup's threads from here on (the block's sum stays what
 // it was launched with).
 template <int N>
@@ -366,6 +364,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
         return a.n_pages;
     };
 
+    // A whole warp's wait, one outcome.
+    auto warp_wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_bar(bar, parity, ar.polls)) != 0; };
     // The next piece, in order; a reader's warp-wide copy.
     int piece_n = 0;
     bool failed = false;                                // a wait of this warp gave up
@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
         };
         bool ok = true;
         SeqPiece p;
-        auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_bar(bar, parity); };
+        auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_bar(bar, parity, ar.polls); };
         // bn: tiles of the stream, in its S or P buffers in turn; pn: its pieces; cn: tiles of
         // the CTA; n: its pieces
         int bn = 0, pn = 0, cn = 0, n = 0;
@@ -669,7 +669,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
         // prompt of 8192 tokens against 423; the warp itself is joined here, since the TMEM loads
         // and stores behind a wait need all of it: 0.7 % of the same time)
         auto wait = [&](uint64_t *bar, uint32_t parity) {
-            ok = wait_bar(bar, parity) && ok;
+            ok = wait_bar(bar, parity, ar.polls) && ok;
             __syncwarp();
         };
         SeqPiece p;
@@ -925,6 +925,7 @@ cudaError_t launch_dim(const SeqArgs &a, const SeqTcPlan &pl, cudaStream_t s) {
     Args ar;
     ar.a = a;
     ar.G = pl.G;
+    ar.polls = pl.polls;
     ar.tpt = Cfg<D>::ROWS / a.g;
     ar.g_inv = (65536u + a.g - 1) / a.g;
     char *ws = static_cast<char *>(pl.ws);
