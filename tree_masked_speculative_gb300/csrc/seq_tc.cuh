@@ -298,7 +298,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
     extern __shared__ __align__(1024) unsigned char sm[];
     const SeqArgs &a = ar.a;
     if ((smem_u32(sm) & 1023u) != 0) {                  // swizzled tiles need it; the same in every CTA
-        if (threadIdx.x == 0) atomicOr(a.status, kSeqTimeout);
+        pdl_wait();
+        if (threadIdx.x == 0) {
+            atomicOr(a.status, kSeqTimeout);
+            ar.ws.rec[blockIdx.x] = {0, 0, 0, 0};       // nothing for the merge to read
+        }
         return;
     }
     Misc *mi = reinterpret_cast<Misc *>(sm + C::OFF_MISC);
