@@ -485,8 +485,9 @@ ta_status paged_kv_append(const ta_append_params *p, const ta_buf *k_new, const 
  *   window       0, or the number of last positions a token sees, itself included
  *   page_size, n_pages, max_pages (cells per block-table row)
  *   kernel       ta_kernel: automatic is the warp-MMA kernel up to max_q_len x (heads
- *                per KV head) = 16 rows (8 for head_dim 256) and the tensor-core kernel
- *                above; TA_KERNEL_WARP_MMA above that is the tensor-core kernel
+ *                per KV head) = 16 rows (for head_dim 256 up to 8, with batch x n_kv_heads
+ *                <= 8) and the tensor-core kernel above; TA_KERNEL_WARP_MMA above 16 (8) rows
+ *                is the tensor-core kernel
  *   scale        logit = (q . k) * scale; a negative one is served by the CUDA cores
  *   strides in elements, multiples of 8; 0 = contiguous
  */

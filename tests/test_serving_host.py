@@ -266,3 +266,18 @@ def test_the_wait_limit_hook_takes_the_tensor_core_kernel_alone(ta):
         assert ta.lib.ta_test_paged_attn_fwd_wait_limit(0, ctypes.byref(p), *bufs, None) == 4
         assert "tensor-core kernel only" in ta.ta_last_error() and ta.ta_launch_count() == before
     assert ta.lib.ta_test_paged_attn_fwd_wait_limit(0, None, *bufs, None) == 1
+
+
+@pytest.mark.parametrize("d,rows,batch,hk,auto,asked", [
+    (64, 16, 4, 2, True, True), (64, 17, 4, 2, False, False), (128, 16, 300, 90, True, True), (128, 17, 4, 2, False, False),
+    (256, 8, 4, 2, True, True), (256, 1, 3, 3, False, True), (256, 9, 4, 2, False, False)])
+def test_the_kernel_choice(ta, d, rows, batch, hk, auto, asked):
+    """The warp-MMA kernel by itself and when asked for; else the tensor-core kernel (the one that
+    the hook takes: there the next check, of tmp, speaks)."""
+    f16, i32 = _b(ta, ta.TA_F16), _b(ta, ta.TA_I32)
+    bufs = [ctypes.byref(b) for b in (f16, f16, f16, i32, i32, i32)] + [None, None, ctypes.byref(f16)]
+    for kernel, mma in ((0, auto), (3, asked)):
+        p = ta.PagedParams(**{**PAGED, "head_dim": d, "n_heads": hk, "n_kv_heads": hk, "max_q_len": rows, "batch": batch,
+                              "kernel": kernel})
+        st = ta.lib.ta_test_paged_attn_fwd_wait_limit(0, ctypes.byref(p), *bufs, None)
+        assert (st, "tensor-core kernel only" in ta.ta_last_error()) == ((4, True) if mma else (1, False))

@@ -135,7 +135,8 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 
 constexpr uint64_t kStatusBytes = 256;
 
-int seq_family(uint32_t d, uint32_t kernel, uint64_t rows, float scale);
+int seq_family(uint32_t d, uint32_t kernel, uint64_t rows, uint64_t units, float scale);
+int paged_family(const ta_paged_params *p);
 
 // The tensor-core kernel counts the key tiles of a request and KV head in 32 bits
 // (`rows` tokens of it, `keys` a token sees on average; a part tile at either end).
@@ -159,7 +160,7 @@ ta_status check_paged(const ta_paged_params *p) {
         static_cast<uint64_t>(p->max_pages) * p->page_size > kMostKeys)
         SEQ_FAIL(TA_ERR_UNSUPPORTED, "paged_attn: sizes exceed the kernels' index range");
     const uint64_t g = p->n_heads / p->n_kv_heads, keys = static_cast<uint64_t>(p->max_pages) * p->page_size;
-    if (seq_family(p->head_dim, p->kernel, p->max_q_len * g, p->scale) == TA_KERNEL_TENSOR_CORES)
+    if (paged_family(p) == TA_KERNEL_TENSOR_CORES)
         SEQ_TRY(check_work("paged_attn", static_cast<uint32_t>(g), p->head_dim, p->max_q_len < p->tokens ? p->max_q_len : p->tokens,
                            p->window && p->window < keys ? p->window : keys));
     return TA_OK;
@@ -171,19 +172,21 @@ ta_status check_prompt(const ta_prompt_params *p) {
     if (p->window > static_cast<uint32_t>(INT_MAX))
         SEQ_FAIL(TA_ERR_UNSUPPORTED, "prompt_attn: sizes exceed the kernels' index range");
     const uint64_t keys = p->tokens / 2;               // causal: half of them on average
-    if (seq_family(p->head_dim, p->kernel, 0, p->scale) == TA_KERNEL_TENSOR_CORES)
+    if (seq_family(p->head_dim, p->kernel, 0, 0, p->scale) == TA_KERNEL_TENSOR_CORES)
         SEQ_TRY(check_work("prompt_attn", p->n_heads / p->n_kv_heads, p->head_dim, p->tokens,
                            p->window && p->window < keys ? p->window : keys));
     return TA_OK;
 }
 
 // Kernel family of a call (rows: most query rows of a request per KV head, 0 for
-// prompts).  Few rows over pages go to the warp-MMA kernel unless another family is
-// asked for; the tensor-core kernel takes the largest product for the largest
-// logit, so a negative scale goes to the CUDA cores, as it does for the warp-MMA one.
-int seq_family(uint32_t d, uint32_t kernel, uint64_t rows, float scale) {
+// prompts; units: requests x KV heads).  Few rows over pages go to the warp-MMA kernel,
+// where it is the faster one, unless another family is asked for; the tensor-core kernel
+// takes the largest product for the largest logit, so a negative scale goes to the CUDA
+// cores, as it does for the warp-MMA one.
+int seq_family(uint32_t d, uint32_t kernel, uint64_t rows, uint64_t units, float scale) {
     if (kernel == TA_KERNEL_CUDA_CORES || scale < 0.0f) return TA_KERNEL_CUDA_CORES;
-    if (kernel != TA_KERNEL_TENSOR_CORES && rows > 0 && seq_mma_takes(static_cast<int>(d), static_cast<long long>(rows)))
+    if (kernel != TA_KERNEL_TENSOR_CORES && rows > 0 && seq_mma_takes(static_cast<int>(d), static_cast<long long>(rows)) &&
+        (kernel == TA_KERNEL_WARP_MMA || seq_mma_best(static_cast<int>(d), static_cast<long long>(units))))
         return TA_KERNEL_WARP_MMA;
     return TA_KERNEL_TENSOR_CORES;
 }
@@ -197,13 +200,14 @@ uint64_t seq_workspace(uint32_t d, int family, uint64_t rows) {
                                         : seq_tc_workspace(static_cast<int>(d), sms);
 }
 int paged_family(const ta_paged_params *p) {
-    return seq_family(p->head_dim, p->kernel, static_cast<uint64_t>(p->max_q_len) * (p->n_heads / p->n_kv_heads), p->scale);
+    return seq_family(p->head_dim, p->kernel, static_cast<uint64_t>(p->max_q_len) * (p->n_heads / p->n_kv_heads),
+                      static_cast<uint64_t>(p->batch) * p->n_kv_heads, p->scale);
 }
 uint64_t paged_workspace(const ta_paged_params *p) {
     return seq_workspace(p->head_dim, paged_family(p), static_cast<uint64_t>(p->max_q_len) * (p->n_heads / p->n_kv_heads));
 }
 uint64_t prompt_workspace(const ta_prompt_params *p) {
-    return seq_workspace(p->head_dim, seq_family(p->head_dim, p->kernel, 0, p->scale), 0);
+    return seq_workspace(p->head_dim, seq_family(p->head_dim, p->kernel, 0, 0, p->scale), 0);
 }
 
 bool encode_16bit(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap *m, const SeqArgs &a, const void *ptr, int rank,
@@ -546,5 +550,5 @@ TA_EXPORT ta_status prompt_attn_fwd(const ta_prompt_params *pp, const ta_buf *q,
     a.v_sh = static_cast<long long>(p.v_head_stride);
     a.scale = p.scale;
     if (ws == 0) SEQ_FAIL(TA_ERR_CUDA, "%s: no CUDA device", op);
-    return run_seq(op, a, seq_family(p.head_dim, p.kernel, 0, p.scale), tmp->ptr, static_cast<cudaStream_t>(stream));
+    return run_seq(op, a, seq_family(p.head_dim, p.kernel, 0, 0, p.scale), tmp->ptr, static_cast<cudaStream_t>(stream));
 }

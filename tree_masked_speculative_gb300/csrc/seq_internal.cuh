@@ -90,9 +90,10 @@ cudaError_t launch_seq_tc64(const SeqArgs &a, const SeqTcPlan &pl, cudaStream_t 
 cudaError_t launch_seq_tc128(const SeqArgs &a, const SeqTcPlan &pl, cudaStream_t s);
 cudaError_t launch_seq_tc256(const SeqArgs &a, const SeqTcPlan &pl, cudaStream_t s);
 
-// Warp-MMA kernel for few rows per KV head (paged): which rows it takes, its
-// workspace and launch.
+// Warp-MMA kernel for few rows per KV head (paged): which rows it takes, with how many
+// (request, KV head) pairs it is the faster one, its workspace and launch.
 bool seq_mma_takes(int d, long long rows);
+bool seq_mma_best(int d, long long units);
 unsigned long long seq_mma_workspace(int d, int rows, int sms);
 cudaError_t launch_seq_mma(const SeqArgs &a, void *ws, int sms, cudaStream_t s);
 

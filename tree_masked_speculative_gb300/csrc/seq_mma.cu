@@ -3,9 +3,7 @@
 // head dimension 256), f16 / bf16.
 //
 // The work is reading K and V once, so HBM bounds it (4 D bytes a key and KV head;
-// 16 query rows are far below the tensor rate): 64 requests of 900 to 16384 keys, 32 / 8
-// heads of 128: 371 us, 6.4 TB/s (95 % of a plain copy's rate; the tcgen05 kernel, whose
-// 128-row tiles hold 4 rows of it, 567 us).  Three requests of 200 to 2100 keys take
+// 16 query rows are far below the tensor rate).  Three requests of 200 to 2100 keys take
 // 14 us, a chain of latencies: schedule, table, K and V, join, merge.  K and V go from global memory
 // straight into MMA fragments, without shared memory: Q K^T contracts over d in any
 // order, so a lane's 16-byte vector of K serves two m16n8k16 products as it is;
@@ -15,6 +13,22 @@
 // 12 warps an SM then cover HBM's latency.  No barrier inside the key loop; the four
 // warps' (max, sum, O) are joined in shared memory at the end of a unit's piece.
 // The batch is cut evenly over the CTAs by the schedule of seq_sched.cuh.
+//
+// Against the tcgen05 kernel, whose 128-row tiles hold these few rows (us, bf16, one token of 32
+// heads on 8 KV heads where nothing else is said, graphs replayed on inputs out of L2):
+//                                          D = 64       D = 128      D = 256
+//   64 requests of 900 to 16384 keys      189 / 296    373 / 374   1064 / 694
+//   32 of 4096 keys, 4 rows                53 /  80     96 / 101    270 / 177
+//   32 of 4096 keys, 8 rows                54 /  82     97 / 101    274 / 177
+//   32 of 4096 keys, 16 rows               59 /  82     99 / 102       -
+//   200 of 300 keys                        37 /  73     62 /  82    154 / 111
+//   1000 of 40 keys                        60 / 181     94 / 199    208 / 236
+//   one of 4000 keys                       17 /  36     19 /  39     32 /  41
+//   one of 4000 keys, 8 heads on one       14 /  52     18 /  52     25 /  54
+// At D = 256 an SM holds only 8 warps of it, with 255 registers and 720 bytes of spills a thread: 4.4
+// of 6.8 TB/s.  There it is chosen where (request, KV head) pairs are few, seq_mma_best().
+// (Spills of the other instances: 316 bytes at D = 64, 232 with 16 rows; 360 at D = 128, none
+// with 16 rows.)
 #include "seq_sched.cuh"
 
 namespace ta {
@@ -477,6 +491,9 @@ int ctas_per_sm(int d, int rows) {
 }  // namespace
 
 bool seq_mma_takes(int d, long long rows) { return rows <= (d == 256 ? 8 : 16); }
+// Few units are cut into many pieces, and latency counts: one request of 4000 keys on 8 KV heads
+// 32 us against 41, on one 25 against 54.  From 64 units on HBM does: 48 against 41 (2000 keys).
+bool seq_mma_best(int d, long long units) { return d <= 128 || units <= 8; }
 
 unsigned long long seq_mma_workspace(int d, int rows, int sms) {
     const unsigned long long G = static_cast<unsigned long long>(sms) * ctas_per_sm(d, rows);
