@@ -281,3 +281,14 @@ def test_the_kernel_choice(ta, d, rows, batch, hk, auto, asked):
                               "kernel": kernel})
         st = ta.lib.ta_test_paged_attn_fwd_wait_limit(0, ctypes.byref(p), *bufs, None)
         assert (st, "tensor-core kernel only" in ta.ta_last_error()) == ((4, True) if mma else (1, False))
+
+
+@pytest.mark.parametrize("at,value", [(0, -1), (0, 2 ** 32), (11, 1e300), (11, "x"), (12, -8)])
+def test_values_that_no_field_holds_are_refused(ta, at, value):
+    """A negative or too large size, a scale past f32: ValueError before the call."""
+    values = [1, 8, 2, 128, 4, 4, 0, 16, 9, 4, 0, 0.1] + [0] * 7 + [0, 0, 0, 0] * 9
+    values[at] = value
+    before = ta.ta_launch_count()
+    with pytest.raises(ValueError, match="out of range"):
+        ta._paged_entry(0, *values)
+    assert ta.ta_launch_count() == before

@@ -455,7 +455,7 @@ class _Entry:
             args = local.args = tuple(ctypes.c_void_p(base + o) for o in self.offsets)
         try:
             self.layout.pack_into(mem, 0, *values)
-        except struct.error as e:
+        except (struct.error, OverflowError) as e:      # (a float past f32 raises the latter)
             raise ValueError("argument out of range: %s" % e) from None
         status = self.fn(*args, _raw_stream(dev))
         if status != TA_OK:
