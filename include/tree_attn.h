@@ -383,6 +383,7 @@ ta_status quant_sdpa_fwd_tree(const ta_quant_params *p, uint32_t q_l, const ta_b
  *     any page, head and token strides (elements, multiples of 8, the last
  *     axis contiguous), so a [n_pages, page_size, n_kv_heads, head_dim] cache is
  *     the same cache with other strides.  page_size: 16, 32, 64, 128 or 256.
+ *   - batch and n_kv_heads are at most 65535, tokens x n_heads below 2^31.
  *   - Rows of a call and keys of a request (its table row's cells) are at most
  *     2^30, and a request has at most 2^31 tiles of 64 keys x 256 rows of work a KV
  *     head; more is TA_ERR_UNSUPPORTED.

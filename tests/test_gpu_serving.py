@@ -971,3 +971,28 @@ def test_waits_that_give_up_set_the_status(ta, d, tree):
     with pytest.raises(ta.TreeAttentionError, match="tensor-core kernel only"):
         p.kernel = 1
         ta.ta_test_paged_attn_fwd_wait_limit(0, p, c.q, c.k, c.v, c.table, cu, lens, parents, tmp, out)
+
+
+# ------------------------------------------------------------------ odd trees
+@pytest.mark.parametrize("kernel", FAMILIES)
+@pytest.mark.parametrize("new", [2, 4, 70])
+def test_trees_of_fewer_keys_than_tokens(ta, new, kernel):
+    """kv_len < q_len with parents: nodes before position 0 are no keys, and give zeros."""
+    c = Paged([200, 200], [new, new], 8, 2, 128, 16, torch.float16, seed=28, tree=True)
+    for short in sorted({0, 1, new - 1, new // 2}):
+        out = ta.paged_attention(c.q, c.k, c.v, c.table, i32(c.cu), i32([200, short]), scale=c.scale, max_q_len=new,
+                                 parents=c.flat_parents(), kernel=kernel)
+        see = visible(new, 200, 0, c.parents[1])[:, 200 - short:]
+        ref, spread = reference(c.q[new:], c.keys[1][:short], c.values[1][:short], see, c.scale)
+        check(out[new:], ref, spread, torch.float16, short + 1)
+        assert bool((out[new:][~see.any(1)] == 0).all())
+
+
+@pytest.mark.parametrize("kernel", FAMILIES)
+@pytest.mark.parametrize("new", [4, 70])
+def test_parents_outside_their_node_end_the_chain(ta, new, kernel):
+    """Itself, a later node, a value past every node or far below: each is the end of the chain."""
+    c = Paged([300, 90], [new, new], 8, 2, 64, 32, torch.bfloat16, seed=29, tree=True)
+    for odd in (lambda i: i, lambda i: i + 1, lambda i: 2 ** 31 - 1, lambda i: -2 ** 31, lambda i: new):
+        c.parents = [[odd(i) if i % 3 == 0 else i - 1 for i in range(new)] for _ in c.new]
+        c.check(c.run(ta, kernel=kernel))
