@@ -6,8 +6,9 @@
 // D = 256 it has 128 rows in one.  S = Q K^T of a 64-key tile is taken from TMEM into
 // registers by one thread a row, which frees it at once: Q K^T of the next tile runs
 // while the softmax warps work on this one.  P goes to TMEM columns of its own, as one
-// 16-bit term (its rounding is the size of the output's own), and P V accumulates in
-// f32.  (With P over S in two buffers of S, Q K^T waited for the P V two tiles back:
+// 16-bit term (off by half a step of a weight, as the 16-bit output is of its value: the error
+// against 64 bits is 1.1 to 1.4 times that of an f32 form rounded once; a second term would
+// double the P V products), and P V accumulates in f32.  (With P over S in two buffers of S, Q K^T waited for the P V two tiles back:
 // 1820 cycles a tile against 1280 of products; with 128-key tiles and one buffer, 4200
 // against 2048.)
 //
@@ -27,7 +28,7 @@
 // (P <= 2^15 fits f16, see kRaise; the sum stays in f32), so O in TMEM is rarely rescaled.
 // Bound: one key tile of both streams is 1280 cycles of products at D = 128 (1024 at the
 // rate of wider products) and about as many issue slots of softmax; a prompt of 8192 tokens with 32 / 8
-// heads of 128 takes 402 us, 1369 TFLOP/s (73 % of the cuBLAS rate).
+// heads of 128 takes 431 us on inputs out of L2, 1276 TFLOP/s (68 % of the cuBLAS rate).
 // Every wait is bounded; a wait that gives up sets the status word, and the CTA
 // drains its copies and MMAs, frees TMEM and exits.
 #pragma once
@@ -670,8 +671,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
         int tn = 0, vn = 0;                             // tiles of this stream, tiles of the CTA
         bool ok = true;
         // (the lanes' outcomes are joined once a tile: a vote at every wait took 443 us for a
-        // prompt of 8192 tokens against 423; the warp itself is joined here, since the TMEM loads
-        // and stores behind a wait need all of it: 0.7 % of the same time)
+        // prompt of 8192 tokens against 423, on one set of inputs; the warp itself is joined here,
+        // since the TMEM loads and stores behind a wait need all of it: 432 us against 427.  Polled
+        // by one lane: 480)
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             ok = wait_bar(bar, parity, ar.polls) && ok;
             __syncwarp();
@@ -730,7 +732,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                     // do O and l follow, and P is taken again
                     // has the P V that read this P buffer NP tiles ago finished (kQkWaitsP: S says so):
                     // asked here, where the answer arrives beside the exponentials (a wait in front of
-                    // P's store: 420 us for a prompt of 8192 tokens against 402)
+                    // P's store: 420 us for a prompt of 8192 tokens against 402, on one set of inputs)
                     const bool o_done = C::kQkWaitsP || tn < NP || __all_sync(0xffffffffu, poll_bar(&mi->o_done[s][pb], tn / NP - 1));
                     uint32_t pk[TK / 2];
                     float l_tile;
