@@ -996,3 +996,15 @@ def test_parents_outside_their_node_end_the_chain(ta, new, kernel):
     for odd in (lambda i: i, lambda i: i + 1, lambda i: 2 ** 31 - 1, lambda i: -2 ** 31, lambda i: new):
         c.parents = [[odd(i) if i % 3 == 0 else i - 1 for i in range(new)] for _ in c.new]
         c.check(c.run(ta, kernel=kernel))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("new", [1, 3, 40])
+def test_a_workspace_serves_other_batches(ta, d, new):
+    """The tmp of one request takes the calls of twenty, and the other way round."""
+    one, many = (Paged([90 + 7 * i for i in range(b)], [new] * b, 4, 2, d, 16, torch.bfloat16, seed=30 + b) for b in (1, 20))
+    tmps = [ta.paged_attention_workspace(c.q, c.k, c.table, max_q_len=new) for c in (one, many)]
+    for c in (one, many):
+        for tmp in tmps:
+            c.check(c.run(ta, tmp=tmp))
+            assert int(tmp.view(torch.int32)[0]) == 0

@@ -388,7 +388,14 @@ TA_EXPORT ta_status paged_kv_append(const ta_append_params *pp, const ta_buf *k_
 
 TA_EXPORT size_t paged_attn_workspace_bytes(const ta_paged_params *p) {
     if (check_paged(p) != TA_OK) return SIZE_MAX;
-    const uint64_t ws = paged_workspace(p);
+    uint64_t ws = paged_workspace(p);
+    if (ws && paged_family(p) == TA_KERNEL_WARP_MMA && p->kernel == TA_KERNEL_AUTO) {
+        // the same for every batch, also where a larger one takes the tensor-core kernel
+        ta_paged_params most = *p;
+        most.batch = 65535;
+        const uint64_t other = paged_workspace(&most);
+        ws = other > ws ? other : ws;
+    }
     if (ws == 0) set_last_error("paged_attn: no CUDA device to size the workspace for");
     return ws ? ws : SIZE_MAX;
 }
