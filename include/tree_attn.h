@@ -566,6 +566,141 @@ size_t prompt_attn_workspace_bytes(const ta_prompt_params *p);
 ta_status prompt_attn_fwd(const ta_prompt_params *p, const ta_buf *q, const ta_buf *k, const ta_buf *v,
                           const ta_buf *cu, const ta_buf *tmp, const ta_buf *out, void *stream);
 
+/*
+ * Rotation of the new tokens' queries and keys by their positions, and their K/V rows
+ * into 16-bit pages, in one launch.
+ *   tokens         rows T of q, k_new, v_new, slot_map and positions (0: nothing is launched)
+ *   n_heads        query heads (0: no q)
+ *   rotary_dim     R: the first R elements of a head are turned, a multiple of 16, at
+ *                  most head_dim
+ *   interleaved    0: element i is paired with i + R/2; 1: 2 i with 2 i + 1 (i < R/2)
+ *   max_positions  rows of the table
+ *   strides in elements, multiples of 8; 0 = contiguous
+ */
+typedef struct {
+    uint32_t tokens;
+    uint32_t n_heads;
+    uint32_t n_kv_heads;
+    uint32_t head_dim;   /* 64, 128 or 256 */
+    uint32_t page_size;
+    uint32_t n_pages;
+    uint32_t rotary_dim;
+    uint32_t interleaved;
+    uint32_t max_positions;
+    uint32_t reserved;   /* must be 0 */
+    uint64_t q_token_stride, q_head_stride, q_out_token_stride, q_out_head_stride;
+    uint64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+    uint64_t page_stride, head_stride, token_stride;
+} ta_rotary_append_params;
+
+/*
+ * Pair i (x1, x2) of a head of token t becomes (x1 c - x2 s, x2 c + x1 s) with
+ * c = table[positions[t]][i], s = table[positions[t]][R/2 + i]; computed in f32,
+ * rounded once.  Turned q rows go to q_out, turned k_new rows and v_new rows to cache
+ * slot slot_map[t] (see paged_kv_append; a slot outside the cache stores no K/V, its
+ * q is turned all the same).  A token whose position is outside [0, max_positions),
+ * such as the -1 of paged_plan_build, stores nothing: its q_out row stays as it was.
+ *   q, q_out   [tokens, n_heads, head_dim]; q_out may be q (with the same strides) and must
+ *              not overlap another buffer otherwise
+ *   k_new, v_new [tokens, n_kv_heads, head_dim]; k_cache, v_cache; one type, f16 or
+ *              bf16, 16-byte aligned
+ *   slot_map   [tokens] i64, positions [tokens] i32
+ *   table      [max_positions, R] f32, 16-byte aligned
+ */
+ta_status paged_rotary_append(const ta_rotary_append_params *p, const ta_buf *q, const ta_buf *k_new,
+                              const ta_buf *v_new, const ta_buf *slot_map, const ta_buf *positions,
+                              const ta_buf *table, const ta_buf *q_out, const ta_buf *k_cache,
+                              const ta_buf *v_cache, void *stream);
+
+/*
+ * 4-bit pages.  A group of `group_size` (32 or 64) neighbouring elements of a row is held as
+ * codes 0 .. 15 with a scale and a bias: element = scale * code + bias.
+ *   codes   [n_pages, n_kv_heads, page_size, head_dim / 8] 32-bit words (U32).  A row is
+ *           head_dim / 4 quads of 16 bits, each 4 neighbouring elements from the lowest
+ *           nibble on; quad g (0 .. 7) of block j of 32 elements is the row's quad
+ *           g * (head_dim / 32) + j.  (A warp then reads its part of a row for a matrix
+ *           instruction as one vector, each instruction within one group.)
+ *   affine  [n_pages, n_kv_heads, page_size, head_dim / group_size, 2] f16 or bf16: scale,
+ *           bias
+ * K and V have one set of strides: of codes in words, multiples of 4; of affine in elements,
+ * multiples of 8, or of 2 head_dim / group_size where that is less; 0 = contiguous.  Both are
+ * 16-byte aligned.
+ */
+typedef struct {
+    uint32_t tokens;
+    uint32_t n_heads;        /* query heads (0: no q) */
+    uint32_t n_kv_heads;
+    uint32_t head_dim;       /* 64, 128 or 256 */
+    uint32_t page_size;
+    uint32_t n_pages;
+    uint32_t group_size;     /* 32 or 64 */
+    uint32_t rotary_dim;     /* 0: nothing is turned; positions and table are not read */
+    uint32_t interleaved;
+    uint32_t max_positions;
+    uint64_t q_token_stride, q_head_stride, q_out_token_stride, q_out_head_stride;
+    uint64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+    uint64_t codes_page_stride, codes_head_stride, codes_token_stride;
+    uint64_t affine_page_stride, affine_head_stride, affine_token_stride;
+} ta_quant_append_params;
+
+/*
+ * As paged_rotary_append, into 4-bit pages: with x the group's elements (K's after the turn,
+ * not rounded), T the 16-bit type and all else exact,
+ *   scale = T(f32((max x - min x) / 15)), bias = T(f32(min x)),
+ *   code  = (x - bias) / scale rounded to nearest even, clamped to 0 .. 15; 0 where scale is 0.
+ * A group with an element that is not finite (a turned one: that f32 cannot hold), or whose bias T
+ * cannot hold, gets scale and bias NaN and codes 0: it reads as NaN.  (Turned elements below
+ * 2^-100 are those of f32.)  With rotary_dim 0, q must be absent.
+ */
+ta_status paged_quant_append(const ta_quant_append_params *p, const ta_buf *q, const ta_buf *k_new,
+                             const ta_buf *v_new, const ta_buf *slot_map, const ta_buf *positions,
+                             const ta_buf *table, const ta_buf *q_out, const ta_buf *k_codes,
+                             const ta_buf *k_affine, const ta_buf *v_codes, const ta_buf *v_affine,
+                             void *stream);
+
+/*
+ * Rows of 4-bit pages as 16-bit values (scale * code + bias in f32, rounded once): row t of k
+ * and v ([tokens, n_kv_heads, head_dim] with the k_ and v_ strides) from slot slot_map[t].  Slots
+ * may repeat; rows whose slot is outside the cache stay as they were.  n_heads and rotary_dim must
+ * be 0.
+ */
+ta_status paged_quant_read(const ta_quant_append_params *p, const ta_buf *slot_map, const ta_buf *k_codes,
+                           const ta_buf *k_affine, const ta_buf *v_codes, const ta_buf *v_affine,
+                           const ta_buf *k, const ta_buf *v, void *stream);
+
+/* As ta_paged_params, over 4-bit pages. */
+typedef struct {
+    uint32_t batch;
+    uint32_t n_heads;
+    uint32_t n_kv_heads;
+    uint32_t head_dim;
+    uint32_t tokens;
+    uint32_t max_q_len;
+    uint32_t window;
+    uint32_t page_size;
+    uint32_t n_pages;
+    uint32_t max_pages;
+    uint32_t group_size;
+    uint32_t kernel;
+    float scale;
+    uint32_t reserved;       /* must be 0 */
+    uint64_t q_token_stride, q_head_stride, out_token_stride, out_head_stride;
+    uint64_t codes_page_stride, codes_head_stride, codes_token_stride;
+    uint64_t affine_page_stride, affine_head_stride, affine_token_stride;
+} ta_paged_quant_params;
+
+/* Bytes the `tmp` buffer of paged_quant_attn_fwd must hold; SIZE_MAX on invalid parameters. */
+size_t paged_quant_attn_workspace_bytes(const ta_paged_quant_params *p);
+
+/*
+ * paged_attn_fwd over 4-bit pages: the same rows, masks, status bits and rules, with k_j and v_j
+ * the values that the pages stand for.  q and out are of the type of the scales.
+ */
+ta_status paged_quant_attn_fwd(const ta_paged_quant_params *p, const ta_buf *q, const ta_buf *k_codes,
+                               const ta_buf *k_affine, const ta_buf *v_codes, const ta_buf *v_affine,
+                               const ta_buf *table, const ta_buf *cu, const ta_buf *kv_lens,
+                               const ta_buf *parents, const ta_buf *tmp, const ta_buf *out, void *stream);
+
 /* ----------------------------------------------------------------- misc */
 
 /* Message for the calling thread's last non-TA_OK status ("" if none). */

@@ -30,6 +30,9 @@ __all__ = [
     "PlanParams", "AppendParams", "PagedParams", "PromptParams", "PagedStep", "paged_plan", "paged_append",
     "paged_attention", "paged_attention_workspace", "paged_attn_workspace_bytes", "prompt_attention",
     "prompt_attention_workspace", "prompt_attn_workspace_bytes", "ta_test_paged_attn_fwd_wait_limit",
+    "RotaryAppendParams", "QuantAppendParams", "PagedQuantParams", "PagedQuantCache", "paged_append_rotary",
+    "paged_quant_cache", "paged_quant_append", "paged_quant_read", "paged_quant_attention",
+    "paged_quant_attention_workspace", "paged_quant_attn_workspace_bytes", "rotary_table",
 ]
 
 TA_OK, TA_ERR_CUDA = 0, 5
@@ -100,6 +103,36 @@ class PromptParams(ctypes.Structure):
                                                 "v_token_stride", "v_head_stride")])
 
 
+class RotaryAppendParams(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_uint32) for n in ("tokens", "n_heads", "n_kv_heads", "head_dim", "page_size", "n_pages",
+                                                "rotary_dim", "interleaved", "max_positions", "reserved")] +
+                [(n, ctypes.c_uint64) for n in ("q_token_stride", "q_head_stride", "q_out_token_stride",
+                                                "q_out_head_stride", "k_token_stride", "k_head_stride",
+                                                "v_token_stride", "v_head_stride", "page_stride", "head_stride",
+                                                "token_stride")])
+
+
+class QuantAppendParams(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_uint32) for n in ("tokens", "n_heads", "n_kv_heads", "head_dim", "page_size", "n_pages",
+                                                "group_size", "rotary_dim", "interleaved", "max_positions")] +
+                [(n, ctypes.c_uint64) for n in ("q_token_stride", "q_head_stride", "q_out_token_stride",
+                                                "q_out_head_stride", "k_token_stride", "k_head_stride",
+                                                "v_token_stride", "v_head_stride", "codes_page_stride",
+                                                "codes_head_stride", "codes_token_stride", "affine_page_stride",
+                                                "affine_head_stride", "affine_token_stride")])
+
+
+class PagedQuantParams(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_uint32) for n in ("batch", "n_heads", "n_kv_heads", "head_dim", "tokens", "max_q_len",
+                                                "window", "page_size", "n_pages", "max_pages", "group_size",
+                                                "kernel")] +
+                [("scale", ctypes.c_float), ("reserved", ctypes.c_uint32)] +
+                [(n, ctypes.c_uint64) for n in ("q_token_stride", "q_head_stride", "out_token_stride",
+                                                "out_head_stride", "codes_page_stride", "codes_head_stride",
+                                                "codes_token_stride", "affine_page_stride", "affine_head_stride",
+                                                "affine_token_stride")])
+
+
 def library_path() -> str:
     return _build_mod.LIB
 
@@ -168,6 +201,16 @@ def _load() -> ctypes.CDLL:
     L.prompt_attn_workspace_bytes.restype = ctypes.c_size_t
     L.prompt_attn_fwd.argtypes = [ctypes.POINTER(PromptParams)] + [B] * 6 + [P]
     L.prompt_attn_fwd.restype = ctypes.c_int
+    L.paged_rotary_append.argtypes = [ctypes.POINTER(RotaryAppendParams)] + [B] * 9 + [P]
+    L.paged_rotary_append.restype = ctypes.c_int
+    L.paged_quant_append.argtypes = [ctypes.POINTER(QuantAppendParams)] + [B] * 11 + [P]
+    L.paged_quant_append.restype = ctypes.c_int
+    L.paged_quant_read.argtypes = [ctypes.POINTER(QuantAppendParams)] + [B] * 7 + [P]
+    L.paged_quant_read.restype = ctypes.c_int
+    L.paged_quant_attn_workspace_bytes.argtypes = [ctypes.POINTER(PagedQuantParams)]
+    L.paged_quant_attn_workspace_bytes.restype = ctypes.c_size_t
+    L.paged_quant_attn_fwd.argtypes = [ctypes.POINTER(PagedQuantParams)] + [B] * 11 + [P]
+    L.paged_quant_attn_fwd.restype = ctypes.c_int
     return L
 
 
@@ -466,6 +509,10 @@ _plan_entry = _Entry("paged_plan_build", "6I", 13)
 _append_entry = _Entry("paged_kv_append", "6I7Q", 5)
 _paged_entry = _Entry("paged_attn_fwd", "11If7Q", 9)
 _prompt_entry = _Entry("prompt_attn_fwd", "7If8Q", 6)
+_rotary_entry = _Entry("paged_rotary_append", "10I11Q", 9)
+_quant_append_entry = _Entry("paged_quant_append", "10I14Q", 11)
+_quant_read_entry = _Entry("paged_quant_read", "10I14Q", 7)
+_paged_quant_entry = _Entry("paged_quant_attn_fwd", "12IfI10Q", 11)
 
 
 def _as_stream(stream, dev: int) -> torch.cuda.Stream:
@@ -616,6 +663,8 @@ def prompt_attn_workspace_bytes(p: PromptParams) -> int:
 def _workspace(p, device) -> torch.Tensor:
     """The tmp buffer of a call with parameters `p`, its status word zero."""
     query, call, n_bufs = ((paged_attn_workspace_bytes, lib.paged_attn_fwd, 9) if isinstance(p, PagedParams) else
+                           (paged_quant_attn_workspace_bytes, lib.paged_quant_attn_fwd, 11)
+                           if isinstance(p, PagedQuantParams) else
                            (prompt_attn_workspace_bytes, lib.prompt_attn_fwd, 6))
     nbytes = query(p)
     if nbytes >= 2 ** 63:
@@ -736,4 +785,217 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
         tmp = _workspace(PromptParams(max(batch, 0), h, hk, d, t, window, kernel, scale), q.device)
     _prompt_entry(dev, batch, h, hk, d, t, window, kernel, scale, *qs, *os_, *ks, *vs, *qb, *kb, *vb,
                   *_flat(cu_seqlens, dev), *_flat(tmp, dev), *ob)
+    return out
+
+
+# ------------------------------------- rotated rows and 4-bit pages (serving)
+
+class PagedQuantCache(NamedTuple):
+    """A paged K/V cache in 4 bits: element = scale * code + bias of its group.  Codes
+    int32 [n_pages, Hk, page_size, D / 8] (the order of a row's codes: paged_quant_append
+    in include/tree_attn.h), affine float16 or bfloat16 [n_pages, Hk, page_size,
+    D / group_size, 2], (scale, bias) pairs.  Any page, head and token strides."""
+    k_codes: torch.Tensor
+    k_affine: torch.Tensor
+    v_codes: torch.Tensor
+    v_affine: torch.Tensor
+
+
+def paged_quant_cache(n_pages: int, n_kv_heads: int, page_size: int, head_dim: int, *, group_size: int = 64,
+                      dtype: torch.dtype = torch.bfloat16, device="cuda") -> PagedQuantCache:
+    """An empty (zero) 4-bit cache; `dtype` is the 16-bit type of its scales and of
+    the rows that go with it."""
+    shape = (n_pages, n_kv_heads, page_size)
+    if dtype not in (torch.float16, torch.bfloat16) or group_size not in (32, 64) or head_dim % group_size:
+        raise ValueError("dtype must be float16 or bfloat16, group_size 32 or 64, a divisor of head_dim")
+    return PagedQuantCache(*[torch.zeros(*shape, *last, dtype=t, device=device) for t, last in
+                             ((torch.int32, (head_dim // 8,)), (dtype, (head_dim // group_size, 2))) * 2])
+
+
+def rotary_table(positions: int, rotary_dim: int, *, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """The table [positions, rotary_dim] f32 of paged_append_rotary and paged_quant_append:
+    cosines, then sines, of position * base^(-2 i / rotary_dim); angles in 64 bits."""
+    turn = base ** (-torch.arange(0, rotary_dim, 2, dtype=torch.float64, device=device) / rotary_dim)
+    angle = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * turn
+    return torch.cat([angle.cos(), angle.sin()], -1).float()
+
+
+def _new_rows(q, k_new, v_new, slot_map, positions, rotary, q_out, hk, d, dev):
+    """Checks and fields of the rows that both appends take: sizes, strides, ta_bufs
+    (q, k_new, v_new, slot_map, positions, rotary, q_out) and the q_out to return."""
+    kn, ks = _strided(k_new, dev, 3, "k_new")
+    vn, vs = _strided(v_new, dev, 3, "v_new")
+    t = k_new.shape[0]
+    if k_new.shape != v_new.shape or tuple(k_new.shape[1:]) != (hk, d):
+        raise ValueError("k_new and v_new must be [T, %d, %d]" % (hk, d))
+    if slot_map.dim() != 1 or slot_map.shape[0] < t:
+        raise ValueError("slot_map must be [T]")
+    h, qb, qs, ob, os_ = 0, _ABSENT, (0, 0), _ABSENT, (0, 0)
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != t or q.shape[2] != d or q.shape[1] == 0:
+            raise ValueError("q must be [%d, H, %d]" % (t, d))
+        h = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        elif q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+        qb, qs = _strided(q, dev, 3, "q")
+        ob, os_ = _strided(q_out, dev, 3, "q_out")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    pb, tb, r, most = _ABSENT, _ABSENT, 0, 0
+    if rotary is not None:
+        if positions is None or positions.dim() != 1 or positions.shape[0] < t:
+            raise ValueError("positions must be [T]")
+        if rotary.dim() != 2 or rotary.shape[1] == 0:
+            raise ValueError("rotary must be [positions, rotary_dim]")
+        most, r = rotary.shape
+        pb, tb = _flat(positions, dev), _flat(rotary, dev)
+    elif positions is not None or q is not None:
+        raise ValueError("positions and q need a rotary table")
+    return t, h, r, most, (*qs, *os_, *ks, *vs), (*qb, *kn, *vn, *_flat(slot_map, dev), *pb, *tb, *ob), q_out
+
+
+def paged_append_rotary(q: Optional[torch.Tensor], k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tensor,
+                        v_cache: torch.Tensor, slot_map: torch.Tensor, positions: torch.Tensor,
+                        rotary: torch.Tensor, *, interleaved: bool = False, q_out: Optional[torch.Tensor] = None,
+                        stream=None) -> Optional[torch.Tensor]:
+    """paged_append with the position rotation on the way: q [T, H, D] and k_new [T, Hk, D]
+    turned by positions [T] (int32), the turned keys and v_new written to the slots
+    slot_map [T] of the caches.  rotary [positions, R] f32 holds cosines, then sines
+    (rotary_table); the first R elements of a head are turned, element i with i + R / 2,
+    or, `interleaved`, 2 i with 2 i + 1.  Returns the turned q (in q_out, which may be q;
+    None without q).  A token whose position is outside the table stores nothing and its
+    q_out row stays as it was."""
+    dev = _device_of(k_cache)
+    if stream is not None or dev != _this_device():
+        return _elsewhere(paged_append_rotary, dev, stream,
+                          (q, k_new, v_new, k_cache, v_cache, slot_map, positions, rotary),
+                          dict(interleaved=interleaved, q_out=q_out))
+    if rotary is None:
+        raise ValueError("rotary must be [positions, rotary_dim]")
+    kb, vb, cs = _cache_pair(k_cache, v_cache, dev)
+    n_pages, hk, ps, d = k_cache.shape
+    t, h, r, most, strides, bufs, q_out = _new_rows(q, k_new, v_new, slot_map, positions, rotary, q_out, hk, d, dev)
+    _rotary_entry(dev, t, h, hk, d, ps, n_pages, r, bool(interleaved), most, 0, *strides, *cs, *bufs, *kb, *vb)
+    return q_out
+
+
+def _quant_cache(cache, dev):
+    """A PagedQuantCache as (n_pages, Hk, page_size, D, group_size, strides, ta_bufs)."""
+    kc, ka, vc, va = cache
+    if kc.dtype != torch.int32 or vc.dtype != torch.int32:
+        raise ValueError("codes must be int32")
+    if kc.shape != vc.shape or ka.shape != va.shape:
+        raise ValueError("K and V must have one shape")
+    if kc.dim() != 4 or ka.dim() != 5 or kc.shape[:3] != ka.shape[:3] or ka.shape[4] != 2 or ka.shape[3] == 0:
+        raise ValueError("a cache is codes [n_pages, Hk, page_size, D / 8], affine [n_pages, Hk, page_size, D / group, 2]")
+    d = 8 * kc.shape[3]
+    if d % ka.shape[3]:
+        raise ValueError("D / 8 words and D / group pairs a row do not go together")
+    bufs, strides = [], []
+    for k, v, what, code in ((kc, vc, "codes", TA_U32), (ka, va, "affine", None)):
+        if what == "affine":                     # a row's pairs stand one behind the other
+            if any(x.stride(4) != 1 or (x.shape[3] > 1 and x.stride(3) != 2) for x in (k, v)) and k.numel():
+                raise ValueError("a row's (scale, bias) pairs must be contiguous")
+            k, v = (x.flatten(3) if x.numel() else x.reshape(*x.shape[:3], -1) for x in (k, v))
+        kb, vb, s = _cache_pair(k, v, dev)
+        for b in (kb, vb):
+            bufs.append(b if code is None else (b[0], b[1], code, 0))
+        strides.append(s)
+    (kcb, vcb, kab, vab) = bufs
+    return (*kc.shape[:3], d, d // ka.shape[3], (*strides[0], *strides[1]), (*kcb, *kab, *vcb, *vab))
+
+
+def paged_quant_append(k_new: torch.Tensor, v_new: torch.Tensor, cache: PagedQuantCache, slot_map: torch.Tensor, *,
+                       q: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                       rotary: Optional[torch.Tensor] = None, interleaved: bool = False,
+                       q_out: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """Write the rows k_new, v_new [T, Hk, D] to the slots slot_map [T] of a 4-bit cache, each
+    group of elements as round((x - min) / scale) with scale = (max - min) / 15.  With
+    `rotary` and `positions`, keys and q are turned on the way as in paged_append_rotary
+    (the keys unrounded); returns the turned q.  A group with an element that is not
+    finite reads as NaN."""
+    dev = _device_of(cache[0])
+    if stream is not None or dev != _this_device():
+        return _elsewhere(paged_quant_append, dev, stream, (k_new, v_new, cache, slot_map),
+                          dict(q=q, positions=positions, rotary=rotary, interleaved=interleaved, q_out=q_out))
+    n_pages, hk, ps, d, group, cs, cb = _quant_cache(cache, dev)
+    t, h, r, most, strides, bufs, q_out = _new_rows(q, k_new, v_new, slot_map, positions, rotary, q_out, hk, d, dev)
+    _quant_append_entry(dev, t, h, hk, d, ps, n_pages, group, r, bool(interleaved), most, *strides, *cs, *bufs, *cb)
+    return q_out
+
+
+def paged_quant_read(cache: PagedQuantCache, slot_map: torch.Tensor, *, out=None, stream=None):
+    """The rows of slots slot_map [T] (int64) of a 4-bit cache as 16-bit (k, v), each
+    [T, Hk, D] in the type of its scales (`out`: the two tensors to write into).  Rows whose
+    slot is outside the cache are not written (zero without an `out`)."""
+    dev = _device_of(cache[0])
+    if stream is not None or dev != _this_device():
+        return _elsewhere(paged_quant_read, dev, stream, (cache, slot_map), dict(out=out))
+    n_pages, hk, ps, d, group, cs, cb = _quant_cache(cache, dev)
+    if slot_map.dim() != 1:
+        raise ValueError("slot_map must be [T]")
+    t = slot_map.shape[0]
+    if out is None:
+        out = tuple(torch.zeros(t, hk, d, dtype=cache[1].dtype, device=cache[1].device) for _ in range(2))
+    k, v = out
+    if tuple(k.shape) != (t, hk, d) or k.shape != v.shape:
+        raise ValueError("out must be two tensors [%d, %d, %d]" % (t, hk, d))
+    kb, ks = _strided(k, dev, 3, "k")
+    vb, vs = _strided(v, dev, 3, "v")
+    _quant_read_entry(dev, t, 0, hk, d, ps, n_pages, group, 0, 0, 0, 0, 0, 0, 0, *ks, *vs, *cs, *_flat(slot_map, dev), *cb,
+                      *kb, *vb)
+    return k, v
+
+
+def paged_quant_attn_workspace_bytes(p: PagedQuantParams) -> int:
+    return int(lib.paged_quant_attn_workspace_bytes(ctypes.byref(p)))
+
+
+def paged_quant_attention_workspace(q: torch.Tensor, cache: PagedQuantCache, block_table: torch.Tensor, *,
+                                    max_q_len: int, kernel: int = KERNEL_AUTO, scale: float = 1.0,
+                                    window: int = 0) -> torch.Tensor:
+    """A tmp buffer for paged_quant_attention calls of these shapes (see
+    paged_attention_workspace)."""
+    n_pages, hk, ps, words = cache[0].shape
+    p = PagedQuantParams(block_table.shape[0], q.shape[1], hk, 8 * words, q.shape[0], max_q_len, window, ps, n_pages,
+                         block_table.shape[1], 8 * words // max(1, cache[1].shape[3]), kernel, scale)
+    with torch.cuda.device(_device_of(q)):
+        return _workspace(p, q.device)
+
+
+def paged_quant_attention(q: torch.Tensor, cache: PagedQuantCache, block_table: torch.Tensor, cu_q: torch.Tensor,
+                          kv_lens: torch.Tensor, *, scale: float, max_q_len: int, window: int = 0,
+                          parents: Optional[torch.Tensor] = None, tmp: Optional[torch.Tensor] = None,
+                          out: Optional[torch.Tensor] = None, kernel: int = KERNEL_AUTO, stream=None) -> torch.Tensor:
+    """paged_attention over a 4-bit cache: the same arguments, masks, `tmp` (from
+    paged_quant_attention_workspace) and status bits, with keys and values
+    scale * code + bias.  q and out have the type of the cache's scales."""
+    dev = _device_of(q)
+    if stream is not None or dev != _this_device():
+        return _elsewhere(paged_quant_attention, dev, stream, (q, cache, block_table, cu_q, kv_lens),
+                          dict(scale=scale, max_q_len=max_q_len, window=window, parents=parents, tmp=tmp, out=out,
+                               kernel=kernel))
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    qb, qs = _strided(q, dev, 3, "q")
+    ob, os_ = _strided(out, dev, 3, "out")
+    n_pages, hk, ps, dk, group, cs, cb = _quant_cache(cache, dev)
+    t, h, d = q.shape
+    if d != dk:
+        raise ValueError("q and the cache must have one head dimension")
+    if block_table.dim() != 2 or cu_q.numel() != block_table.shape[0] + 1 or kv_lens.numel() != block_table.shape[0]:
+        raise ValueError("block_table must be [batch, max_pages], cu_q [batch + 1] and kv_lens [batch]")
+    if parents is not None and parents.numel() < t:         # (an empty one would pass for none)
+        raise ValueError("parents must be [%d]" % t)
+    batch, width = block_table.shape
+    if tmp is None:
+        tmp = _workspace(PagedQuantParams(batch, h, hk, d, t, max_q_len, window, ps, n_pages, width, group, kernel,
+                                          scale), q.device)
+    _paged_quant_entry(dev, batch, h, hk, d, t, max_q_len, window, ps, n_pages, width, group, kernel, scale, 0, *qs, *os_,
+                       *cs, *qb, *cb, *_flat(block_table, dev), *_flat(cu_q, dev), *_flat(kv_lens, dev),
+                       *_flat(parents, dev), *_flat(tmp, dev), *ob)
     return out

@@ -1,0 +1,63 @@
+// 4-bit pages and the rotation of new rows: internal declarations (not installed).
+//
+// A row of a KV head is D / 8 words: 16-bit quads (4 neighbouring elements, lowest nibble
+// first), quad g of 32-element block j at place g * (D / 32) + j.  Scale and bias of a group
+// stand side by side, so that one load brings both.
+#pragma once
+
+#include "seq_internal.cuh"
+
+namespace ta {
+
+struct QuantCache {
+    uint32_t *kc, *vc;                // codes
+    void *ka, *va;                    // scale, bias pairs
+    long long c_sp, c_sh, c_st;       // strides of the codes, words
+    long long a_sp, a_sh, a_st;       // strides of the affine, pairs (32 bits)
+};
+
+// New rows: q turned to q_out, k_new turned and v_new to the cache.  Row strides in 16-byte
+// vectors.
+struct RotaryArgs {
+    const void *q, *k_new, *v_new;
+    void *q_out;
+    const int64_t *slot;
+    const int32_t *pos;               // nullptr: nothing is turned
+    const float *table;               // [max_pos][R]: cos, sin
+    int T, H, Hk, D, R, max_pos, interleaved;
+    int page_shift, n_pages, bf16;
+    long long q_st, q_sh, qo_st, qo_sh, k_st, k_sh, v_st, v_sh;
+};
+struct RotaryAppendArgs {
+    RotaryArgs r;
+    void *k, *v;
+    long long c_sp, c_sh, c_st;       // of the 16-bit cache, vectors
+};
+cudaError_t launch_rotary_append(const RotaryAppendArgs &a, cudaStream_t s);
+
+struct QuantAppendArgs {
+    RotaryArgs r;
+    QuantCache c;
+    int group;
+};
+cudaError_t launch_quant_append(const QuantAppendArgs &a, cudaStream_t s);
+
+struct QuantReadArgs {
+    QuantCache c;
+    const int64_t *slot;
+    void *k, *v;
+    int T, Hk, D, group, page_shift, n_pages, bf16;
+    long long k_st, k_sh, v_st, v_sh;   // elements
+};
+cudaError_t launch_quant_read(const QuantReadArgs &a, cudaStream_t s);
+
+// Attention of ragged rows over 4-bit pages: SeqArgs (whose k, v and their strides are not used)
+// and the cache.
+struct SeqQuantArgs {
+    SeqArgs s;
+    QuantCache c;
+    int group;
+};
+cudaError_t launch_seq_quant_fma(const SeqQuantArgs &a, cudaStream_t s);
+
+}  // namespace ta
