@@ -60,4 +60,13 @@ struct SeqQuantArgs {
 };
 cudaError_t launch_seq_quant_fma(const SeqQuantArgs &a, cudaStream_t s);
 
+// Warp-MMA kernel for few rows per KV head: up to 16 rows; its workspace and launch.
+constexpr int kQuantMmaRows = 16;
+unsigned long long seq_quant_mma_workspace64(int rows, int sms);
+unsigned long long seq_quant_mma_workspace128(int rows, int sms);
+unsigned long long seq_quant_mma_workspace256(int rows, int sms);
+cudaError_t launch_seq_quant_mma64(const SeqQuantArgs &a, void *ws, int sms, cudaStream_t s);
+cudaError_t launch_seq_quant_mma128(const SeqQuantArgs &a, void *ws, int sms, cudaStream_t s);
+cudaError_t launch_seq_quant_mma256(const SeqQuantArgs &a, void *ws, int sms, cudaStream_t s);
+
 }  // namespace ta

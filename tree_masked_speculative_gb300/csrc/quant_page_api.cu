@@ -143,8 +143,30 @@ ta_status new_rows(const char *op, P *p, const ta_buf *q, const ta_buf *k_new, c
     return TA_OK;
 }
 
+uint64_t quant_rows(const ta_paged_quant_params *p) { return static_cast<uint64_t>(p->max_q_len) * (p->n_heads / p->n_kv_heads); }
+
+// Kernel family of a call.  A negative scale goes to the CUDA cores (the running max is that of the
+// products).
+int quant_family(const ta_paged_quant_params *p) {
+    if (p->kernel == TA_KERNEL_CUDA_CORES || p->scale < 0.0f) return TA_KERNEL_CUDA_CORES;
+    return quant_rows(p) <= kQuantMmaRows ? TA_KERNEL_WARP_MMA : TA_KERNEL_CUDA_CORES;
+}
+
 // Workspace of a call; 0 when no device is visible to size the grid for.
-uint64_t quant_workspace(const ta_paged_quant_params *) { return kStatusBytes; }
+uint64_t quant_workspace(const ta_paged_quant_params *p) {
+    if (quant_family(p) == TA_KERNEL_CUDA_CORES) return kStatusBytes;
+    const int sms = device_sm_count(), rows = static_cast<int>(quant_rows(p));
+    if (sms <= 0) return 0;
+    return p->head_dim == 64 ? seq_quant_mma_workspace64(rows, sms)
+                             : p->head_dim == 128 ? seq_quant_mma_workspace128(rows, sms) : seq_quant_mma_workspace256(rows, sms);
+}
+
+cudaError_t run_quant(const SeqQuantArgs &a, int family, void *ws, cudaStream_t s) {
+    if (family == TA_KERNEL_CUDA_CORES) return launch_seq_quant_fma(a, s);
+    const int sms = device_sm_count();
+    return a.s.D == 64 ? launch_seq_quant_mma64(a, ws, sms, s)
+                       : a.s.D == 128 ? launch_seq_quant_mma128(a, ws, sms, s) : launch_seq_quant_mma256(a, ws, sms, s);
+}
 
 ta_status check_quant_attn(const ta_paged_quant_params *p) {
     const char *op = "paged_quant_attn";
@@ -338,7 +360,7 @@ TA_EXPORT ta_status paged_quant_attn_fwd(const ta_paged_quant_params *pp, const 
     s.scale = p.scale;
     a.group = static_cast<int>(p.group_size);
     if (ws == 0) SEQ_FAIL(TA_ERR_CUDA, "%s: no CUDA device", op);
-    const cudaError_t e = launch_seq_quant_fma(a, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = run_quant(a, quant_family(&p), tmp->ptr, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) SEQ_FAIL(TA_ERR_CUDA, "%s: launch: %s", op, cudaGetErrorString(e));
     return TA_OK;
 }

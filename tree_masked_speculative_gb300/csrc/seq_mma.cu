@@ -29,7 +29,7 @@
 // of 6.8 TB/s.  There it is chosen where (request, KV head) pairs are few, seq_mma_best().
 // (Spills of the other instances: 316 bytes at D = 64, 232 with 16 rows; 360 at D = 128, none
 // with 16 rows.)
-#include "seq_sched.cuh"
+#include "seq_merge.cuh"
 
 namespace ta {
 namespace {
@@ -56,19 +56,6 @@ struct MmaArgs {
     int G;
 };
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-// K and V are read once: past L1.
-__device__ __forceinline__ uint4 load_once(const void *p) {
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.L2::128B.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
 template <bool BF16>
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     if constexpr (BF16)
@@ -79,16 +66,6 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
         asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
-    if constexpr (BF16) {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t *>(&v);
-    } else {
-        const __half2 v = __floats2half2_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t *>(&v);
-    }
 }
 // Bits 15 and 31: is the low / high value infinite or NaN.
 template <bool BF16>
@@ -402,73 +379,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D, RH>) seq_mma_kernel(co
     }
 }
 
-// out = sum_p O_p 2^(m_p - m*) / sum_p l_p 2^(m_p - m*) over the pieces of the cut unit
-// that starts in CTA blockIdx.x.  A few units are cut into many pieces when the
-// batch is small, so a block's threads share the pieces as well as the columns
-// (one thread a column through all of 22 pieces took 14 us).
-constexpr int kMergeThreads = 256;
-template <int D, bool BF16>
-__global__ void __launch_bounds__(kMergeThreads) seq_mma_merge_kernel(const MmaArgs ar) {
-    const SeqArgs &a = ar.a;
-    __shared__ float s_m[16], s_inv[16];
-    __shared__ float4 s_part[kMergeThreads];
-    pdl_wait();
-    const int c = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const SeqRec rec = ar.rec[c];
-    if (rec.parts == 0) return;
-    auto slot = [&](int p) { return static_cast<size_t>(p == 0 ? 2 * c + 1 : 2 * (c + p)); };
-    for (int row = warp; row < rec.rows; row += kMergeThreads / 32) {
-        float m = -INFINITY, l = 0.0f;
-#pragma unroll 2
-        for (int p = lane; p < rec.parts; p += 32) {
-            const float2 w = ar.ml[slot(p) * 16 + row];
-            const float mn = fmaxf(m, w.x), mu = mn == -INFINITY ? 0.0f : mn;
-            l = l * ex2(m - mu) + w.y * ex2(w.x - mu);
-            m = mn;
-        }
-        const float mr = warp_max(m), mu = mr == -INFINITY ? 0.0f : mr;
-        l = warp_sum(l * ex2(m - mu));
-        if (lane == 0) {
-            s_m[row] = mu;
-            s_inv[row] = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-        }
-    }
-    __syncthreads();
-    // items: 4 columns of a row; `share` threads take the pieces of one item in turn
-    const int items = rec.rows * (D / 4);
-    int share = 1;
-    while (2 * share * items <= kMergeThreads) share *= 2;
-    const int per = kMergeThreads / share;              // items at a time
-    for (int i0 = 0; i0 < items; i0 += per) {
-        const int k = tid / per, i = i0 + tid - k * per;
-        float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        const int row = i / (D / 4), d = (i - row * (D / 4)) * 4;
-        if (i < items) {
-            const float mu = s_m[row];
-#pragma unroll 4
-            for (int p = k; p < rec.parts; p += share) {
-                const float f = ex2(ar.ml[slot(p) * 16 + row].x - mu);
-                const float4 y = *reinterpret_cast<const float4 *>(ar.o + (slot(p) * 16 + row) * D + d);
-                r.x += f * y.x; r.y += f * y.y; r.z += f * y.z; r.w += f * y.w;
-            }
-        }
-        s_part[tid] = r;
-        __syncthreads();
-        if (k == 0 && i < items) {
-            for (int j = 1; j < share; ++j) {
-                const float4 y = s_part[tid + j * per];
-                r.x += y.x; r.y += y.y; r.z += y.z; r.w += y.w;
-            }
-            const float inv = s_inv[row];
-            const int tk = row / a.g;
-            uint16_t *out = static_cast<uint16_t *>(a.out) + static_cast<long long>(rec.token + tk) * a.o_st +
-                            static_cast<long long>(rec.kh * a.g + row - tk * a.g) * a.o_sh + d;
-            *reinterpret_cast<uint2 *>(out) = make_uint2(pack16<BF16>(r.x * inv, r.y * inv), pack16<BF16>(r.z * inv, r.w * inv));
-        }
-        __syncthreads();
-    }
-}
-
 template <int D, int RH, bool BF16>
 cudaError_t launch(const MmaArgs &ar, cudaStream_t s) {
     auto kern = seq_mma_kernel<D, RH, BF16>;
@@ -476,7 +386,7 @@ cudaError_t launch(const MmaArgs &ar, cudaStream_t s) {
     cudaError_t e = launch_pdl(kern, dim3(ar.G), dim3(kThreads), smem, s, ar);
     count_launch();
     if (e != cudaSuccess) return e;
-    e = launch_pdl(seq_mma_merge_kernel<D, BF16>, dim3(ar.G), dim3(kMergeThreads), 0, s, ar);
+    e = launch_pdl(seq_mma_merge_kernel<D, 16, BF16>, dim3(ar.G), dim3(kMergeThreads), 0, s, ar.a, ar.rec, ar.ml, ar.o);
     count_launch();
     return e;
 }

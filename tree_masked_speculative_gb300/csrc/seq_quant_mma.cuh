@@ -1,0 +1,547 @@
+// Attention of few query rows per KV head over 4-bit pages with warp-level MMAs: single tokens
+// and small drafts, max_q_len * (heads per KV head) <= 16 rows.
+//
+// The work is reading codes, scales and biases once, D + 8 D / G bytes a key and KV head; HBM
+// bounds it, and next to it the instructions that widen the codes.  So codes are not
+// turned into values: a nibble masked out of its word is the f16 subnormal c 2^-24 (or 16 c 2^-24,
+// without a shift), which a matrix instruction takes as it is, and scales and biases are applied to
+// sums.  With q' a row of Q times a power of two in f16, per group of G elements
+//   q . k = 2^24 / 2^e  sum_g s_g (q'_g . c_g 2^-24) + sum_g b_g (sum of q in g)
+//   sum_key P v = sum_key (P s_g) c + sum_key P b_g     (the second one number a row and group)
+// The products are keys (16) x rows (8) x elements, and elements (16) x rows (8) x keys: keys and
+// elements, not the few rows, fill the long side.  P s_g goes from the first product's layout to the
+// second's by an 8 x 8 transpose (movmatrix), in f16, held within its range by a power of two per
+// row and group that, like the running max, moves only when a block needs it.
+// A lane's words: for K the quads 2 t and 2 t + 1 of every 32-element block of keys g and
+// g + 8, for V quad g of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9 - one vector a key and
+// product, straight from global memory.  A warp takes every fourth block of 16 keys of its CTA's
+// run with the next block's words in flight; the batch is cut evenly over the CTAs by the schedule of
+// seq_sched.cuh.
+#pragma once
+
+#include "quant_page.cuh"
+#include "seq_merge.cuh"
+
+namespace ta {
+namespace {
+
+constexpr int kQmWarps = 4, kQmThreads = kQmWarps * 32;
+constexpr int kQmTks = 6;                           // schedule granularity: 64 keys, 16 a warp
+constexpr int kQmLeast = 3;                         // tiles of a CTA's run at least
+constexpr float kQmLog2e = 1.4426950408889634f;
+// The running max moves when a row's max exceeds it by more than 2^8; P and l are held 2^7 higher
+// (P <= 2^15): a weight is subnormal only below 2^-21 of the running max's.
+constexpr float kQmSlack = 8.0f, kQmRaise = 7.0f;
+
+struct QmArgs {
+    SeqQuantArgs q;
+    SeqRec *rec;      // [G]
+    float2 *ml;       // [2 G][8 NR]
+    float *o;         // [2 G][8 NR][D]
+    int G;
+};
+
+__device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+// N words (1, 2, 4 or 8) that are read once.
+template <int N>
+__device__ __forceinline__ void load_words(const uint32_t *p, uint32_t *w) {
+    if constexpr (N == 1) {
+        asm volatile("ld.global.L1::no_allocate.L2::128B.u32 %0, [%1];" : "=r"(w[0]) : "l"(p));
+    } else if constexpr (N == 2) {
+        asm volatile("ld.global.L1::no_allocate.L2::128B.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const uint4 x = load_once(p + i);
+            w[i] = x.x; w[i + 1] = x.y; w[i + 2] = x.z; w[i + 3] = x.w;
+        }
+    }
+}
+// Scale and bias of a pair.
+template <bool BF16>
+__device__ __forceinline__ float scale_of(uint32_t sb) {
+    if constexpr (BF16) return __uint_as_float(sb << 16);
+    else return __half2float(__ushort_as_half(static_cast<unsigned short>(sb & 0xffffu)));
+}
+template <bool BF16>
+__device__ __forceinline__ float bias_of(uint32_t sb) {
+    if constexpr (BF16) return __uint_as_float(sb & 0xffff0000u);
+    else return __half2float(__ushort_as_half(static_cast<unsigned short>(sb >> 16)));
+}
+
+// NR: tiles of 8 query rows.
+template <int D, int NR>
+constexpr int kQmCtas = D == 256 ? 2 : NR == 2 ? (D == 64 ? 4 : 3) : (D == 64 ? 5 : 4);
+// Q's fragments in shared memory where registers are short.
+template <int D, int NR>
+constexpr bool kQmSharedQ = D * NR > 128;
+template <int D, int NR>
+constexpr size_t kQmSmem = sizeof(float) * kQmWarps * 8 * NR * (D + 4) + (kQmSharedQ<D, NR> ? NR * (D / 32) * 512 : 0);
+
+template <int D, int G, int NR, bool BF16>
+__global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_kernel(const QmArgs ar) {
+    const SeqArgs &a = ar.q.s;
+    const QuantCache &cc = ar.q.c;
+    constexpr int RR = 8 * NR, NB = D / 32, NG = D / G, BPG = G / 32, VW = NB / 2, OS = D + 4;
+    constexpr bool SQ = kQmSharedQ<D, NR>;
+    __shared__ SeqScratch sched;
+    __shared__ float2 s_ml[kQmWarps][RR];
+    extern __shared__ __align__(16) float s_o[];        // [kQmWarps][RR][OS], then Q's fragments
+    uint4 *s_q = reinterpret_cast<uint4 *>(s_o + kQmWarps * RR * OS);   // [NR][NB][32]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3, cta = blockIdx.x;
+    pdl_wait();
+    const SeqRun run = seq_schedule<kQmThreads, kQmTks, 0, kQmLeast>(a, a.max_q, cta, ar.G, &sched);
+    pdl_launch_dependents();
+    if (tid == 0) ar.rec[cta] = {0, 0, 0, 0};
+    const float scale2 = fmaxf(a.scale * kQmLog2e, FLT_MIN);   // above 0: a masked -inf stays -inf
+    SeqWalk<kQmTks, 0> walk;
+    walk.init(a, a.max_q, run, &sched, cta);
+    SeqPiece p;
+    while (walk.next(a, a.max_q, run, &p)) {
+        // Q fragments: of block j the elements 32 j + 8 t + {0, 4 | 1, 5 | 2, 6 | 3, 7}, the second and
+        // fourth pair over 16 (their codes come as 16 c), times 2^e: the row's largest in [2^13, 2^14)
+        uint4 qb[SQ ? 1 : NR][SQ ? 1 : NB];
+        float fr[NR][2], qs[NR][NG][2];
+#pragma unroll
+        for (int x = 0; x < NR; ++x) {
+            const int row = g + 8 * x, tok = row / a.g;
+            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + static_cast<long long>(p.q0 + tok) * a.q_st +
+                                                               static_cast<long long>(p.kh * a.g + row - tok * a.g) * a.q_sh) + t;
+            uint4 raw[NB];
+            float big = 0.0f;
+#pragma unroll
+            for (int j = 0; j < NB; ++j) raw[j] = row < p.rows ? src[4 * j] : make_uint4(0, 0, 0, 0);
+            auto widen = [](uint32_t w, float *f) {
+                f[0] = scale_of<BF16>(w);
+                f[1] = bias_of<BF16>(w);
+            };
+            float sum[NG];
+#pragma unroll
+            for (int n = 0; n < NG; ++n) sum[n] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                float f[8];
+                widen(raw[j].x, f); widen(raw[j].y, f + 2); widen(raw[j].z, f + 4); widen(raw[j].w, f + 6);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(f[e]));
+                sum[j / BPG] += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+            }
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+            // exponents as they stand in the bits: 2^(13 - floor(log2 big))
+            const int up = min(267 - static_cast<int>(__float_as_uint(big) >> 23), 250);
+            const float mul = __uint_as_float(static_cast<uint32_t>(up) << 23), mul16 = mul * 0.0625f;
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                float f[8];
+                widen(raw[j].x, f); widen(raw[j].y, f + 2); widen(raw[j].z, f + 4); widen(raw[j].w, f + 6);
+                const uint4 y = make_uint4(pack16<false>(f[0] * mul, f[4] * mul), pack16<false>(f[1] * mul16, f[5] * mul16),
+                                           pack16<false>(f[2] * mul, f[6] * mul), pack16<false>(f[3] * mul16, f[7] * mul16));
+                if constexpr (SQ) {
+                    if (warp == (j & 3)) s_q[(x * NB + j) * 32 + lane] = y;
+                } else {
+                    qb[x][j] = y;
+                }
+            }
+            // 2^24 / 2^e of row g, and its sums: to the lanes that hold the rows 2 t and 2 t + 1 of a product
+            const float back = __uint_as_float(static_cast<uint32_t>(254 - up) << 23) * 0x1p24f * scale2;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) fr[x][e] = __shfl_sync(0xffffffffu, back, 8 * t + 4 * e);
+#pragma unroll
+            for (int n = 0; n < NG; ++n) {
+                float y = sum[n];
+                y += __shfl_xor_sync(0xffffffffu, y, 1);
+                y += __shfl_xor_sync(0xffffffffu, y, 2);
+                y *= scale2;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) qs[x][n][e] = __shfl_sync(0xffffffffu, y, 8 * t + 4 * e);
+            }
+        }
+        if constexpr (SQ) __syncthreads();
+        // Of rows 2 t + e of tile x: running max, sum, sums of P b (each lane its keys'), power of two of P s
+        float o[NR][NB][2][4], m[NR][2], l[NR][2], ab[NR][NG][2], sc[NR][NG][2];
+#pragma unroll
+        for (int x = 0; x < NR; ++x)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                m[x][e] = -INFINITY;
+                l[x][e] = 0.0f;
+#pragma unroll
+                for (int n = 0; n < NG; ++n) {
+                    ab[x][n][e] = 0.0f;
+                    sc[x][n][e] = 0x1p100f;             // too large for any scale: the first block sets it
+                }
+#pragma unroll
+                for (int j = 0; j < NB; ++j)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) o[x][j][h][e] = o[x][j][h][2 + e] = 0.0f;
+            }
+        const int key_end = min(p.kv, (p.t0 + p.nt) << kQmTks);
+        const int32_t *table = a.table + static_cast<long long>(p.b) * a.max_pages;
+        // page of the 16-key block at `key`, -1: none
+        auto page_of = [&](int key) -> int {
+            if (key >= key_end) return -1;
+            const int page = __ldg(table + (key >> a.page_shift));
+            if (page >= 0 && page < a.n_pages) return page;
+            // a page before every row's window may be gone
+            if (lane == 0 && !(a.window && key + 16 <= p.prefix - a.window + 1)) atomicOr(a.status, kSeqBadPage);
+            return -1;
+        };
+        uint32_t kw[2][NB], ka[2][NG], vw[4][VW], va[2][NG];
+        auto load_k = [&](int page, int key) {
+            const int in = key & ((1 << a.page_shift) - 1);
+            const long long co = page * cc.c_sp + p.kh * cc.c_sh, ao = page * cc.a_sp + p.kh * cc.a_sh;
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const int kk = 8 * n + g;
+                if (page >= 0 && key + kk < p.kv) {
+                    load_words<NB>(cc.kc + co + (in + kk) * cc.c_st + t * NB, kw[n]);
+                    load_words<NG>(static_cast<const uint32_t *>(cc.ka) + ao + (in + kk) * cc.a_st, ka[n]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < NB; ++i) kw[n][i] = 0u;
+#pragma unroll
+                    for (int i = 0; i < NG; ++i) ka[n][i] = 0u;
+                }
+            }
+        };
+        auto load_v = [&](int page, int key) {
+            const int in = key & ((1 << a.page_shift) - 1);
+            const long long co = page * cc.c_sp + p.kh * cc.c_sh, ao = page * cc.a_sp + p.kh * cc.a_sh;
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const int kk = 2 * t + (n & 1) + 8 * (n >> 1);
+                if (page >= 0 && key + kk < p.kv) {
+                    load_words<VW>(cc.vc + co + (in + kk) * cc.c_st + g * VW, vw[n]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < VW; ++i) vw[n][i] = 0u;
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const int kk = 8 * n + g;
+                if (page >= 0 && key + kk < p.kv) {
+                    load_words<NG>(static_cast<const uint32_t *>(cc.va) + ao + (in + kk) * cc.a_st, va[n]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < NG; ++i) va[n][i] = 0u;
+                }
+            }
+        };
+        int key = (p.t0 << kQmTks) + 16 * warp;
+        int page = page_of(key), next = page_of(key + 16 * kQmWarps);
+        load_k(page, key);
+        load_v(page, key);
+#pragma unroll 1
+        for (; key < key_end; key += 16 * kQmWarps) {
+            // logits in log2 units: s[x][2 n + e] of key g + 8 n, row 2 t + e of tile x
+            float s[NR][4], u[NR][4];
+#pragma unroll
+            for (int x = 0; x < NR; ++x)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[x][i] = u[x][i] = 0.0f;
+#pragma unroll
+            for (int n = 0; n < NG; ++n) {
+                float acc[NR][4];
+#pragma unroll
+                for (int x = 0; x < NR; ++x) acc[x][0] = acc[x][1] = acc[x][2] = acc[x][3] = 0.0f;
+#pragma unroll
+                for (int j = n * BPG; j < (n + 1) * BPG; ++j) {
+                    const uint32_t sel = j & 1 ? 0x7632u : 0x5410u;
+                    const uint32_t w0 = __byte_perm(kw[0][j / 2], kw[0][NB / 2 + j / 2], sel), w1 = __byte_perm(kw[1][j / 2], kw[1][NB / 2 + j / 2], sel);
+                    const uint32_t h0 = w0 >> 8, h1 = w1 >> 8;
+#pragma unroll
+                    for (int x = 0; x < NR; ++x) {
+                        uint4 b;
+                        if constexpr (SQ) b = s_q[(x * NB + j) * 32 + lane];
+                        else b = qb[x][j];
+                        mma16(acc[x], w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u, b.x, b.y);
+                        mma16(acc[x], h0 & 0x000f000fu, h1 & 0x000f000fu, h0 & 0x00f000f0u, h1 & 0x00f000f0u, b.z, b.w);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float sk = scale_of<BF16>(ka[i][n]), bk = bias_of<BF16>(ka[i][n]);
+#pragma unroll
+                    for (int x = 0; x < NR; ++x)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            s[x][2 * i + e] = fmaf(sk, acc[x][2 * i + e], s[x][2 * i + e]);
+                            u[x][2 * i + e] = fmaf(bk, qs[x][n][e], u[x][2 * i + e]);
+                        }
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < NR; ++x)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[x][i] = fmaf(s[x][i], fr[x][i & 1], u[x][i]);
+            const int after = page_of(key + 32 * kQmWarps);
+            load_k(next, key + 16 * kQmWarps);
+            // bit 2 n + e: is key g + 8 n seen by row 2 t + e
+            const bool masked = key < p.full_lo || key + 16 > p.full_hi;
+            uint32_t see[NR];
+#pragma unroll
+            for (int x = 0; x < NR; ++x) see[x] = 15u;
+            if (masked) {
+#pragma unroll
+                for (int x = 0; x < NR; ++x) {
+                    see[x] = 0u;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int row = 8 * x + 2 * t + e, tok = row / a.g;
+                        const bool live = row < p.rows;
+                        uint32_t anc[kMaxTreeBitsNodes / 32] = {}, w[1];
+                        if (a.parents && live) seq_ancestors(a.parents + p.q0, tok, anc);
+                        seq_visible<1>(a, p.prefix, live ? p.kv : 0, tok, anc, key, w);
+                        see[x] |= ((w[0] >> g) & 1u) << e | ((w[0] >> (g + 8)) & 1u) << (2 + e);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (!((see[x] >> i) & 1u)) s[x][i] = -INFINITY;
+                }
+            }
+            bool rise = false;
+#pragma unroll
+            for (int x = 0; x < NR; ++x)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) rise |= fmaxf(s[x][e], s[x][2 + e]) > m[x][e] + kQmSlack;
+            if (__any_sync(0xffffffffu, rise)) {
+#pragma unroll
+                for (int x = 0; x < NR; ++x)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float mx = fmaxf(s[x][e], s[x][2 + e]);
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                        if (mx > m[x][e] + kQmSlack) {
+                            const float f = ex2(m[x][e] - mx);      // 0 from -inf
+                            m[x][e] = mx;
+                            l[x][e] *= f;
+#pragma unroll
+                            for (int n = 0; n < NG; ++n) ab[x][n][e] *= f;
+#pragma unroll
+                            for (int j = 0; j < NB; ++j)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    o[x][j][h][e] *= f;
+                                    o[x][j][h][2 + e] *= f;
+                                }
+                        }
+                    }
+            }
+            float pr[NR][4];
+#pragma unroll
+            for (int x = 0; x < NR; ++x)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float mu = m[x][e] == -INFINITY ? 0.0f : m[x][e] - kQmRaise;
+                    pr[x][e] = ex2(s[x][e] - mu);
+                    pr[x][2 + e] = ex2(s[x][2 + e] - mu);
+                    l[x][e] += pr[x][e] + pr[x][2 + e];
+                }
+            // P s and the sums of P b; where a row does not see a key its scale and bias do not count
+            float ps[NR][NG][4];
+            bool over = false;
+            if (!masked) {
+#pragma unroll
+                for (int x = 0; x < NR; ++x)
+#pragma unroll
+                    for (int n = 0; n < NG; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t sb = va[i >> 1][n];
+                            ps[x][n][i] = pr[x][i] * sc[x][n][i & 1] * scale_of<BF16>(sb);
+                            ab[x][n][i & 1] = fmaf(pr[x][i], bias_of<BF16>(sb), ab[x][n][i & 1]);
+                            over |= fabsf(ps[x][n][i]) > 40000.0f;
+                        }
+            } else {
+#pragma unroll
+                for (int x = 0; x < NR; ++x)
+#pragma unroll
+                    for (int n = 0; n < NG; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t sb = (see[x] >> i) & 1u ? va[i >> 1][n] : 0u;
+                            ps[x][n][i] = pr[x][i] * sc[x][n][i & 1] * scale_of<BF16>(sb);
+                            ab[x][n][i & 1] = fmaf(pr[x][i], bias_of<BF16>(sb), ab[x][n][i & 1]);
+                            over |= fabsf(ps[x][n][i]) > 40000.0f;
+                        }
+            }
+            if (__any_sync(0xffffffffu, over)) {
+                // a row and group whose P s leaves f16's range: its power of two so that the largest finite scale
+                // it sees here becomes 1/8 to 1/4
+#pragma unroll
+                for (int x = 0; x < NR; ++x)
+#pragma unroll
+                    for (int n = 0; n < NG; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float s0 = (see[x] >> e) & 1u ? fabsf(scale_of<BF16>(va[0][n])) : 0.0f;
+                            const float s1 = (see[x] >> (2 + e)) & 1u ? fabsf(scale_of<BF16>(va[1][n])) : 0.0f;
+                            float top = fmaxf(s0 <= FLT_MAX ? s0 : 0.0f, s1 <= FLT_MAX ? s1 : 0.0f);
+                            float hit = fmaxf(fabsf(ps[x][n][e]), fabsf(ps[x][n][2 + e]));
+#pragma unroll
+                            for (int k = 4; k < 32; k <<= 1) {
+                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+                                hit = fmaxf(hit, __shfl_xor_sync(0xffffffffu, hit, k));
+                            }
+                            if (hit > 40000.0f && top > 0.0f) {
+                                const float to = __uint_as_float(static_cast<uint32_t>(max(251 - static_cast<int>(__float_as_uint(top) >> 23), 1)) << 23);
+                                if (to < sc[x][n][e]) {
+                                    const float f = to / sc[x][n][e];
+                                    sc[x][n][e] = to;
+#pragma unroll
+                                    for (int j = n * BPG; j < (n + 1) * BPG; ++j)
+#pragma unroll
+                                        for (int h = 0; h < 2; ++h) {
+                                            o[x][j][h][e] *= f;
+                                            o[x][j][h][2 + e] *= f;
+                                        }
+                                }
+                                ps[x][n][e] = (see[x] >> e) & 1u ? pr[x][e] * sc[x][n][e] * scale_of<BF16>(va[0][n]) : 0.0f;
+                                ps[x][n][2 + e] = (see[x] >> (2 + e)) & 1u ? pr[x][2 + e] * sc[x][n][e] * scale_of<BF16>(va[1][n]) : 0.0f;
+                            }
+                        }
+            }
+            uint32_t pb[NR][NG][2];
+#pragma unroll
+            for (int x = 0; x < NR; ++x)
+#pragma unroll
+                for (int n = 0; n < NG; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) pb[x][n][i] = transpose8(pack16<false>(ps[x][n][2 * i], ps[x][n][2 * i + 1]));
+            // O += V^T (P s): elements 32 j + 4 g + 2 h (+ 1) of 16 rows of the product, 8 query rows
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                const uint32_t sel = j & 1 ? 0x7632u : 0x5410u;
+                const uint32_t w0 = __byte_perm(vw[0][j / 2], vw[1][j / 2], sel), w1 = __byte_perm(vw[2][j / 2], vw[3][j / 2], sel);
+                const uint32_t h0 = w0 >> 8, h1 = w1 >> 8;
+#pragma unroll
+                for (int x = 0; x < NR; ++x) {
+                    mma16(o[x][j][0], w0 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x000f000fu, w1 & 0x00f000f0u, pb[x][j / BPG][0], pb[x][j / BPG][1]);
+                    mma16(o[x][j][1], h0 & 0x000f000fu, h0 & 0x00f000f0u, h1 & 0x000f000fu, h1 & 0x00f000f0u, pb[x][j / BPG][0], pb[x][j / BPG][1]);
+                }
+            }
+            load_v(next, key + 16 * kQmWarps);
+            next = after;
+        }
+        if (tid == 0 && p.rest > 0) ar.rec[cta] = seq_record(run, cta, p);
+        // ---- join the four warps
+#pragma unroll
+        for (int x = 0; x < NR; ++x)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int row = 8 * x + 2 * t + e;
+                float y = l[x][e];
+#pragma unroll
+                for (int k = 4; k < 32; k <<= 1) y += __shfl_xor_sync(0xffffffffu, y, k);
+                if (g == 0) s_ml[warp][row] = make_float2(m[x][e], y);
+                float *dst = s_o + (warp * RR + row) * OS + 4 * g;
+#pragma unroll
+                for (int n = 0; n < NG; ++n) {
+                    float b = ab[x][n][e];
+#pragma unroll
+                    for (int k = 4; k < 32; k <<= 1) b += __shfl_xor_sync(0xffffffffu, b, k);
+                    const float f = 0x1p24f / sc[x][n][e], f16 = f * 0.0625f;
+#pragma unroll
+                    for (int j = n * BPG; j < (n + 1) * BPG; ++j)
+                        *reinterpret_cast<float4 *>(dst + 32 * j) =
+                            make_float4(fmaf(o[x][j][0][e], f, b), fmaf(o[x][j][0][2 + e], f16, b), fmaf(o[x][j][1][e], f, b), fmaf(o[x][j][1][2 + e], f16, b));
+                }
+            }
+        __syncthreads();
+        for (int i = tid; i < p.rows * (D / 8); i += kQmThreads) {
+            const int row = i / (D / 8), d = (i - row * (D / 8)) * 8;
+            float2 w[kQmWarps];
+            float ms = -INFINITY, ls = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kQmWarps; ++k) {
+                w[k] = s_ml[k][row];
+                ms = fmaxf(ms, w[k].x);
+            }
+            // a warp without a logit above -inf adds 0, or NaN where its logits were NaN
+            const float mu = ms == -INFINITY ? 0.0f : ms;
+            float r[8] = {};
+#pragma unroll
+            for (int k = 0; k < kQmWarps; ++k) {
+                const float f = ex2(w[k].x - mu);
+                ls += f * w[k].y;
+                const float4 y = *reinterpret_cast<const float4 *>(s_o + (k * RR + row) * OS + d);
+                const float4 z = *reinterpret_cast<const float4 *>(s_o + (k * RR + row) * OS + d + 4);
+                r[0] += f * y.x; r[1] += f * y.y; r[2] += f * y.z; r[3] += f * y.w;
+                r[4] += f * z.x; r[5] += f * z.y; r[6] += f * z.z; r[7] += f * z.w;
+            }
+            if (p.slot < 0) {
+                const float inv = ls > 0.0f ? 1.0f / ls : (ls == 0.0f ? 0.0f : ls);
+                const int tk = row / a.g;
+                uint16_t *out = static_cast<uint16_t *>(a.out) + static_cast<long long>(p.q0 + tk) * a.o_st +
+                                static_cast<long long>(p.kh * a.g + row - tk * a.g) * a.o_sh + d;
+                uint4 y;
+                y.x = pack16<BF16>(r[0] * inv, r[1] * inv);
+                y.y = pack16<BF16>(r[2] * inv, r[3] * inv);
+                y.z = pack16<BF16>(r[4] * inv, r[5] * inv);
+                y.w = pack16<BF16>(r[6] * inv, r[7] * inv);
+                *reinterpret_cast<uint4 *>(out) = y;
+            } else {
+                float *dst = ar.o + (static_cast<size_t>(p.slot) * RR + row) * D + d;
+                *reinterpret_cast<float4 *>(dst) = make_float4(r[0], r[1], r[2], r[3]);
+                *reinterpret_cast<float4 *>(dst + 4) = make_float4(r[4], r[5], r[6], r[7]);
+                if (d == 0) ar.ml[static_cast<size_t>(p.slot) * RR + row] = make_float2(ms, ls);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+template <int D, int G, int NR, bool BF16>
+cudaError_t qm_launch(const SeqQuantArgs &a, void *ws, int sms, cudaStream_t s) {
+    constexpr int RR = 8 * NR;
+    QmArgs ar;
+    ar.q = a;
+    ar.G = sms * kQmCtas<D, NR>;
+    char *w = static_cast<char *>(ws);
+    ar.rec = reinterpret_cast<SeqRec *>(w + 256);
+    w += 256 + (ar.G * sizeof(SeqRec) + 255) / 256 * 256;
+    ar.ml = reinterpret_cast<float2 *>(w);
+    ar.o = reinterpret_cast<float *>(w + sizeof(float2) * 2 * ar.G * RR);
+    auto kern = seq_quant_mma_kernel<D, G, NR, BF16>;
+    static unsigned long long done = 0;
+    cudaError_t e = set_smem_limit_once(kern, kQmSmem<D, NR>, &done);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(kern, dim3(ar.G), dim3(kQmThreads), kQmSmem<D, NR>, s, ar);
+    count_launch();
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(seq_mma_merge_kernel<D, RR, BF16>, dim3(ar.G), dim3(kMergeThreads), 0, s, a.s, ar.rec, ar.ml, ar.o);
+    count_launch();
+    return e;
+}
+
+template <int D, int G>
+cudaError_t qm_launch_group(const SeqQuantArgs &a, void *ws, int sms, cudaStream_t s) {
+    const bool two = a.s.max_q * a.s.g > 8;
+    if (a.s.bf16) return two ? qm_launch<D, G, 2, true>(a, ws, sms, s) : qm_launch<D, G, 1, true>(a, ws, sms, s);
+    return two ? qm_launch<D, G, 2, false>(a, ws, sms, s) : qm_launch<D, G, 1, false>(a, ws, sms, s);
+}
+template <int D>
+cudaError_t qm_launch_dim(const SeqQuantArgs &a, void *ws, int sms, cudaStream_t s) {
+    return a.group == 32 ? qm_launch_group<D, 32>(a, ws, sms, s) : qm_launch_group<D, 64>(a, ws, sms, s);
+}
+template <int D>
+unsigned long long qm_workspace(int rows, int sms) {
+    const unsigned long long G = static_cast<unsigned long long>(sms) * (rows > 8 ? kQmCtas<D, 2> : kQmCtas<D, 1>), cap = rows > 8 ? 16 : 8;
+    return 256 + (G * sizeof(SeqRec) + 255) / 256 * 256 + 2 * G * cap * (sizeof(float2) + sizeof(float) * D);
+}
+
+}  // namespace
+}  // namespace ta

@@ -1,0 +1,7 @@
+// Warp-MMA attention over 4-bit pages, head dimension 64.
+#include "seq_quant_mma.cuh"
+
+namespace ta {
+cudaError_t launch_seq_quant_mma64(const SeqQuantArgs &a, void *ws, int sms, cudaStream_t s) { return qm_launch_dim<64>(a, ws, sms, s); }
+unsigned long long seq_quant_mma_workspace64(int rows, int sms) { return qm_workspace<64>(rows, sms); }
+}  // namespace ta
