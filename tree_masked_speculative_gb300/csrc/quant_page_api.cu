@@ -145,27 +145,44 @@ ta_status new_rows(const char *op, P *p, const ta_buf *q, const ta_buf *k_new, c
 
 uint64_t quant_rows(const ta_paged_quant_params *p) { return static_cast<uint64_t>(p->max_q_len) * (p->n_heads / p->n_kv_heads); }
 
-// Kernel family of a call.  A negative scale goes to the CUDA cores (the running max is that of the
-// products).
+// Kernel family of a call: few rows go to the warp-MMA kernel unless the tensor-core kernel is asked for.  Both
+// take the largest product for the largest logit, so a negative scale goes to the CUDA cores.
 int quant_family(const ta_paged_quant_params *p) {
     if (p->kernel == TA_KERNEL_CUDA_CORES || p->scale < 0.0f) return TA_KERNEL_CUDA_CORES;
-    return quant_rows(p) <= kQuantMmaRows ? TA_KERNEL_WARP_MMA : TA_KERNEL_CUDA_CORES;
+    return p->kernel != TA_KERNEL_TENSOR_CORES && quant_rows(p) <= kQuantMmaRows ? TA_KERNEL_WARP_MMA : TA_KERNEL_TENSOR_CORES;
 }
 
 // Workspace of a call; 0 when no device is visible to size the grid for.
 uint64_t quant_workspace(const ta_paged_quant_params *p) {
-    if (quant_family(p) == TA_KERNEL_CUDA_CORES) return kStatusBytes;
-    const int sms = device_sm_count(), rows = static_cast<int>(quant_rows(p));
+    const int family = quant_family(p), rows = static_cast<int>(quant_rows(p));
+    if (family == TA_KERNEL_CUDA_CORES) return kStatusBytes;
+    const int sms = device_sm_count();
     if (sms <= 0) return 0;
+    if (family == TA_KERNEL_TENSOR_CORES) return seq_tc_workspace(static_cast<int>(p->head_dim), sms);
     return p->head_dim == 64 ? seq_quant_mma_workspace64(rows, sms)
                              : p->head_dim == 128 ? seq_quant_mma_workspace128(rows, sms) : seq_quant_mma_workspace256(rows, sms);
 }
 
-cudaError_t run_quant(const SeqQuantArgs &a, int family, void *ws, cudaStream_t s) {
-    if (family == TA_KERNEL_CUDA_CORES) return launch_seq_quant_fma(a, s);
+ta_status run_quant(const char *op, const SeqQuantArgs &a, int family, void *ws, cudaStream_t s, uint32_t polls) {
     const int sms = device_sm_count();
-    return a.s.D == 64 ? launch_seq_quant_mma64(a, ws, sms, s)
-                       : a.s.D == 128 ? launch_seq_quant_mma128(a, ws, sms, s) : launch_seq_quant_mma256(a, ws, sms, s);
+    cudaError_t e;
+    if (family == TA_KERNEL_CUDA_CORES) {
+        e = launch_seq_quant_fma(a, s);
+    } else if (family == TA_KERNEL_WARP_MMA) {
+        e = a.s.D == 64 ? launch_seq_quant_mma64(a, ws, sms, s)
+                        : a.s.D == 128 ? launch_seq_quant_mma128(a, ws, sms, s) : launch_seq_quant_mma256(a, ws, sms, s);
+    } else {
+        SeqTcPlan pl = {};
+        pl.G = sms;
+        pl.polls = polls;
+        pl.ws = ws;
+        const auto encode = tensor_map_encoder();
+        if (encode == nullptr) SEQ_FAIL(TA_ERR_CUDA, "%s: cuTensorMapEncodeTiled is not available", op);
+        if (!q_map(encode, &pl.q, a.s)) SEQ_FAIL(TA_ERR_CUDA, "%s: TMA descriptor encoding failed", op);
+        e = a.s.D == 64 ? launch_seq_quant_tc64(a, pl, s) : a.s.D == 128 ? launch_seq_quant_tc128(a, pl, s) : launch_seq_quant_tc256(a, pl, s);
+    }
+    if (e != cudaSuccess) SEQ_FAIL(TA_ERR_CUDA, "%s: launch: %s", op, cudaGetErrorString(e));
+    return TA_OK;
 }
 
 ta_status check_quant_attn(const ta_paged_quant_params *p) {
@@ -182,6 +199,10 @@ ta_status check_quant_attn(const ta_paged_quant_params *p) {
     if (p->window > static_cast<uint32_t>(INT_MAX) || p->max_q_len > static_cast<uint32_t>(INT_MAX) ||
         p->n_pages > static_cast<uint32_t>(INT_MAX) || static_cast<uint64_t>(p->max_pages) * p->page_size > kMostKeys)
         SEQ_FAIL(TA_ERR_UNSUPPORTED, "%s: sizes exceed the kernels' index range", op);
+    const uint64_t keys = static_cast<uint64_t>(p->max_pages) * p->page_size;
+    if (quant_family(p) == TA_KERNEL_TENSOR_CORES)
+        SEQ_TRY(check_work(op, p->n_heads / p->n_kv_heads, p->head_dim, p->max_q_len < p->tokens ? p->max_q_len : p->tokens,
+                           p->window && p->window < keys ? p->window : keys));
     return TA_OK;
 }
 
@@ -360,7 +381,5 @@ TA_EXPORT ta_status paged_quant_attn_fwd(const ta_paged_quant_params *pp, const 
     s.scale = p.scale;
     a.group = static_cast<int>(p.group_size);
     if (ws == 0) SEQ_FAIL(TA_ERR_CUDA, "%s: no CUDA device", op);
-    const cudaError_t e = run_quant(a, quant_family(&p), tmp->ptr, static_cast<cudaStream_t>(stream));
-    if (e != cudaSuccess) SEQ_FAIL(TA_ERR_CUDA, "%s: launch: %s", op, cudaGetErrorString(e));
-    return TA_OK;
+    return run_quant(op, a, quant_family(&p), tmp->ptr, static_cast<cudaStream_t>(stream), kSeqWaitPolls);
 }

@@ -73,22 +73,6 @@ uint64_t prompt_workspace(const ta_prompt_params *p) {
     return seq_workspace(p->head_dim, seq_family(p->head_dim, p->kernel, 0, 0, p->scale), 0);
 }
 
-bool encode_16bit(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap *m, const SeqArgs &a, const void *ptr, int rank,
-                  const cuuint64_t *dims, const cuuint64_t *str, const cuuint32_t *box) {
-    const cuuint32_t es[5] = {1, 1, 1, 1, 1};
-    return encode(m, a.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
-                  const_cast<void *>(ptr), dims, str, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Tensor map of Q: {D, H, T}, a unit's tokens x the g heads of a KV head at once.
-bool q_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap *m, const SeqArgs &a) {
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.D), static_cast<cuuint64_t>(a.H), static_cast<cuuint64_t>(a.T)};
-    const cuuint64_t str[2] = {static_cast<cuuint64_t>(a.q_sh) * 2, static_cast<cuuint64_t>(a.q_st) * 2};
-    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(a.g), static_cast<cuuint32_t>(seq_tc_rows(a.D) / a.g)};
-    return encode_16bit(encode, m, a, a.q, 3, dims, str, box);
-}
-
 // Tensor map of K or V: {64, page_size, D / 64, Hk, n_pages} (paged) or {64, T, D / 64, Hk};
 // a box holds `slabs` 64-column slabs.
 bool kv_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap *m, const SeqArgs &a, const void *ptr, long long st,

@@ -33,6 +33,7 @@
 // drains its copies and MMAs, frees TMEM and exits.
 #pragma once
 
+#include "quant_page.cuh"
 #include "seq_sched.cuh"
 #include "sm100_ptx.cuh"
 
@@ -71,6 +72,9 @@ struct Cfg {
     static constexpr int OFF_MISC = OFF_OUT + NSTR * 8192;
 };
 
+// Where K and V come from: packed rows, 16-bit pages, 4-bit pages.
+enum Source { kPacked, kPages, kQuant };
+
 constexpr int kPieces = 4;
 constexpr int kUnitCost = kSeqTcUnitCost;      // of the schedule: a unit's start and end take as long as 5 key tiles
 // The guard is at most kPieces + 2 pieces ahead of an epilogue (a piece is published
@@ -108,6 +112,7 @@ struct Args {
     int tpt, G;
     uint32_t polls;       // of every wait, see wait_bar
     uint32_t g_inv;       // ceil(2^16 / g): row / g = row * g_inv >> 16, exact for rows < 256 and g <= 128
+    QuantCache qc;        // 4-bit pages
 };
 struct Maps {
     CUtensorMap q;        // {D, H, T}, box {64, g, tokens of a unit}: rows (token, head) as they stand in a unit
@@ -292,9 +297,112 @@ __device__ __forceinline__ uint32_t max_abs(uint32_t acc, uint32_t w) {
     return r;
 }
 
-template <int D, bool PAGED, bool BF16>
+// ---- 4-bit pages: a tile is widened to 16-bit values on its way into shared memory, by two warps for K
+// (0 and 3) and two for V (6 and 7, which also do the guards' work).
+// A unit is a key's quads 2 t and 2 t + 1 of every 32-element block (D / 32 words in a row of
+// memory): 8 neighbouring elements of each block.  A warp has 32 keys of a tile, a lane 4 units: t = lane % 4 of
+// keys 8 i + qrow(lane).  Eight lanes that store together cover all banks: rows r and r + 4.
+__device__ __forceinline__ int qrow(int lane) { return (lane >> 3) + ((lane >> 2) & 1) * 4; }
+
+template <int N>
+__device__ __forceinline__ void load_words(const uint32_t *p, uint32_t (&w)[N]) {
+    if constexpr (N == 1) {
+        asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(w[0]) : "l"(p));
+    } else if constexpr (N == 2) {
+        asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+            asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3]) : "l"(p + i));
+    }
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t hfma(uint32_t x, uint32_t y, uint32_t z) {
+    uint32_t r;
+    if constexpr (BF16) asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(y), "r"(z));
+    else asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(y), "r"(z));
+    return r;
+}
+// scale * code + bias of 8 codes (word x: quad in the low half, the next quad in the high half) as 16-bit pairs of
+// elements n and n + 4, each rounded once.  A code under the exponent of a power of two is that power plus the code
+// (f16: 1024 + c or 1024 + 16 c; bf16: 128 + c); taking the power off again is exact.
+template <bool BF16>
+__device__ __forceinline__ void widen(uint32_t x, uint32_t s2, uint32_t b2, uint32_t (&v)[4]) {
+    if constexpr (BF16) {
+        constexpr uint32_t one = 0x3f803f80u, off = 0xc300c300u;                   // 1, -128
+#pragma unroll
+        for (int n = 0; n < 4; ++n) v[n] = hfma<true>(hfma<true>(((x >> (4 * n)) & 0x000f000fu) | 0x43004300u, one, off), s2, b2);
+    } else {
+        constexpr uint32_t one = 0x3c003c00u, off = 0xe400e400u, part = 0x2c002c00u, off16 = 0xd400d400u;   // 1, -1024, 1/16, -64
+        const uint32_t y = x >> 8;
+        v[0] = hfma<false>(hfma<false>((x & 0x000f000fu) | 0x64006400u, one, off), s2, b2);
+        v[1] = hfma<false>(hfma<false>((x & 0x00f000f0u) | 0x64006400u, part, off16), s2, b2);
+        v[2] = hfma<false>(hfma<false>((y & 0x000f000fu) | 0x64006400u, one, off), s2, b2);
+        v[3] = hfma<false>(hfma<false>((y & 0x00f000f0u) | 0x64006400u, part, off16), s2, b2);
+    }
+}
+
+// One warp's half of the tiles of K or V.
+template <int D, int G, bool BF16, bool IS_K>
+struct QuantFeed {
+    static constexpr int NB = D / 32, NG = D / G, UN = 4;
+    uint32_t w[UN][NB], sb[UN][NG];
+    int page[2];          // of the lane's next tile: keys 0 .. 15 and 16 .. 31 of the warp's half
+
+    __device__ __forceinline__ void pages(const SeqArgs &a, const SeqPiece &p, int k0) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const int key = k0 + 16 * b;
+            page[b] = -1;
+            if (key >= p.kv) continue;
+            const int g = __ldg(a.table + static_cast<long long>(p.b) * a.max_pages + (key >> a.page_shift));
+            if (g >= 0 && g < a.n_pages) page[b] = g;
+            // a page before every row's window may be gone
+            else if ((threadIdx.x & 31) == 0 && !(a.window && key + 16 <= p.prefix + p.i0 - a.window + 1)) atomicOr(a.status, kSeqBadPage);
+        }
+    }
+    __device__ __forceinline__ void load(const SeqArgs &a, const QuantCache &c, const SeqPiece &p, int k0, int i) {
+        const int lane = threadIdx.x & 31, key = k0 + 8 * i + qrow(lane), pg = page[i >> 1];
+        if (pg >= 0 && key < p.kv) {
+            const int in = key & ((1 << a.page_shift) - 1);
+            load_words<NB>((IS_K ? c.kc : c.vc) + pg * c.c_sp + p.kh * c.c_sh + in * c.c_st + (lane & 3) * NB, w[i]);
+            load_words<NG>(static_cast<const uint32_t *>(IS_K ? c.ka : c.va) + pg * c.a_sp + p.kh * c.a_sh + in * c.a_st, sb[i]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < NB; ++j) w[i][j] = 0u;
+#pragma unroll
+            for (int n = 0; n < NG; ++n) sb[i][n] = 0u;
+        }
+    }
+    // Unit i into its row of a tile (64-column slabs of 64 rows, 128-byte swizzle).  K's elements are put in
+    // order; V's stay as 0, 4, 1, 5, 2, 6, 3, 7 of every eight, the epilogue's names for O's columns.
+    __device__ __forceinline__ void store(unsigned char *tile, int half, int i, bool look, uint32_t (&acc)[4]) {
+        const int lane = threadIdx.x & 31, t = lane & 3, row = 32 * half + 8 * i + qrow(lane);
+        unsigned char *dst = tile + row * 128;
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+            const uint32_t x = __byte_perm(w[i][j / 2], w[i][NB / 2 + j / 2], j & 1 ? 0x7632 : 0x5410);
+            const uint32_t s2 = __byte_perm(sb[i][j * 32 / G], 0u, 0x1010), b2 = __byte_perm(sb[i][j * 32 / G], 0u, 0x3232);
+            uint32_t v[4];
+            widen<BF16>(x, s2, b2, v);
+            uint4 y;
+            if constexpr (IS_K)
+                y = make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410), __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
+            else
+                y = make_uint4(v[0], v[1], v[2], v[3]);
+            if (!IS_K && look) {
+#pragma unroll
+                for (int n = 0; n < 4; ++n) acc[n] = max_abs<BF16>(acc[n], v[n]);
+            }
+            *reinterpret_cast<uint4 *>(dst + (j / 2) * Cfg<D>::SLAB + ((((j & 1) * 4 + t) ^ (row & 7)) << 4)) = y;
+        }
+    }
+};
+
+template <int D, int SRC, bool BF16, int G = 32>
 __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args ar, const __grid_constant__ Maps maps) {
     using C = Cfg<D>;
+    constexpr bool PAGED = SRC == kPages, QUANT = SRC == kQuant;
     constexpr int TK = C::TK, TKS = C::TKS, NSTR = C::NSTR, NK = C::NK, NV = C::NV, NS = C::NS, NP = C::NP, ROWS = C::ROWS;
     extern __shared__ __align__(1024) unsigned char sm[];
     const SeqArgs &a = ar.a;
@@ -311,7 +419,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
     // arrivals on a piece's empty slot: issuers, guards, V producer, softmax warps
     constexpr int kReaders = 2 * NSTR + 3 + 4 * NSTR;
     if (tid == 0) {
-        for (int i = 0; i < NK; ++i) { mbar_init(&mi->k_full[i], 1); mbar_init(&mi->k_empty[i], NSTR); }
+        for (int i = 0; i < NK; ++i) { mbar_init(&mi->k_full[i], QUANT ? 2 : 1); mbar_init(&mi->k_empty[i], NSTR); }
         for (int i = 0; i < NV; ++i) {
             mbar_init(&mi->v_full[i], 1);
             mbar_init(&mi->v_ready[i], 2);
@@ -341,8 +449,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
     }
     if (warp == 0 && lane == 0) {
         tma_prefetch_desc(&maps.q);
-        tma_prefetch_desc(&maps.k);
-        tma_prefetch_desc(&maps.v);
+        if constexpr (!QUANT) {
+            tma_prefetch_desc(&maps.k);
+            tma_prefetch_desc(&maps.v);
+        }
     }
     pdl_wait();
     const SeqRun run = seq_schedule<C::THREADS, TKS, kUnitCost, 1>(a, ar.tpt, cta, ar.G, &mi->sched);
@@ -391,6 +501,37 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
     // Does some row of the piece not see all of key tile t.
     auto is_masked = [&](const SeqPiece &p, int t) { return (t << TKS) < p.full_lo || ((t + 1) << TKS) > p.full_hi; };
 
+    // 4-bit pages: one warp's half of a piece's K tiles; `after_first` runs behind the first.
+    auto feed_k = [&](int half, const SeqPiece &p, int *kn, bool *ok, auto &&after_first) {
+        if constexpr (QUANT) {
+            QuantFeed<D, G, BF16, true> f;
+            const int k0 = (p.t0 << TKS) + 32 * half;
+            uint32_t none[4];
+            f.pages(a, p, k0);
+#pragma unroll
+            for (int i = 0; i < f.UN; ++i) f.load(a, ar.qc, p, k0, i);
+            if (p.nt > 1) f.pages(a, p, k0 + TK);
+#pragma unroll 1
+            for (int t = 0; t < p.nt; ++t) {
+                const int st = *kn % NK;
+                *ok = warp_wait(&mi->k_empty[st], (static_cast<uint32_t>(*kn / NK) & 1u) ^ 1u);
+                if (!*ok) return;
+#pragma unroll
+                for (int i = 0; i < f.UN; ++i) {
+                    f.store(sm + C::OFF_K + st * C::STAGE, half, i, false, none);
+                    if (t + 1 < p.nt) f.load(a, ar.qc, p, k0 + (t + 1) * TK, i);
+                }
+                if (t + 2 < p.nt) f.pages(a, p, k0 + (t + 2) * TK);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&mi->k_full[st]);
+                ++*kn;
+                if (t == 0) after_first();
+                if (!*ok) return;
+            }
+        }
+    };
+
     // D <= 128: 4 x 128 registers a thread at launch = 2 x 88 + 2 x 168.
     if (warp < C::SW) {
     if constexpr (NSTR == 2) regs_down<88>();
@@ -418,6 +559,24 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
             }
             __syncwarp();
             if (!more) break;
+            auto load_q = [&] {
+                // the unit's rows of Q, once the products of the piece before have read theirs
+                if (n > 0) ok = warp_wait(&mi->q_empty, n - 1);
+                if (!ok) return;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&mi->q_full, C::SLABS * ar.tpt * a.g * 128);
+                    for (int x = 0; x < C::SLABS; ++x)
+                        tma_load_3d(sm + C::OFF_Q + x * C::QSLAB, &maps.q, &mi->q_full, x * 64, p.kh * a.g, p.q0 + p.i0);
+                    ++qn;
+                }
+                __syncwarp();
+            };
+            if constexpr (QUANT) {
+                if (n == 0) load_q();
+                feed_k(0, p, &kn, &ok, [&] { if (n > 0) load_q(); });
+                if (!ok) break;
+                continue;
+            }
             int page = page_of(p, p.t0);
 #pragma unroll 1
             for (int t = 0; t < p.nt; ++t) {
@@ -435,16 +594,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                 }
                 ++kn;
                 if (t == 0) {
-                    // the unit's rows of Q, once the products of the piece before have read theirs
-                    if (n > 0) ok = warp_wait(&mi->q_empty, n - 1);
+                    load_q();
                     if (!ok) break;
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(&mi->q_full, C::SLABS * ar.tpt * a.g * 128);
-                        for (int x = 0; x < C::SLABS; ++x)
-                            tma_load_3d(sm + C::OFF_Q + x * C::QSLAB, &maps.q, &mi->q_full, x * 64, p.kh * a.g, p.q0 + p.i0);
-                        ++qn;
-                    }
-                    __syncwarp();
                 }
                 page = next;
             }
@@ -455,9 +606,77 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
         if (lane == 0) {
             if (qn > 0 && !mbar_wait_sleep(&mi->q_full, static_cast<uint32_t>(qn - 1) & 1u, 1u << 21, 1000))
                 atomicOr(a.status, kSeqTimeout);
-            for (int i = max(0, kn - NK); i < kn; ++i)
+            for (int i = QUANT ? kn : max(0, kn - NK); i < kn; ++i)
                 if (!mbar_wait_sleep(&mi->k_full[i % NK], static_cast<uint32_t>(i / NK) & 1u, 1u << 21, 1000))
                     atomicOr(a.status, kSeqTimeout);
+        }
+    } else if (QUANT && warp == 3) {
+        // -------------------------------------------------- 4-bit pages: second half of K
+        int kn = 0;
+        bool ok = true;
+        SeqPiece p;
+#pragma unroll 1
+        while (ok && fetch(&p)) feed_k(1, p, &kn, &ok, [] {});
+        failed |= !ok;
+    } else if (QUANT && (warp == 6 || warp == 7)) {
+        // ------------------------------------------- 4-bit pages: V, guarded as it is widened
+        if constexpr (QUANT) {
+            const int half = warp - 6;
+            int vn = 0, n = 0, gn = 0;                  // V tiles, pieces, masked tiles so far
+            bool ok = true;
+            SeqPiece p;
+#pragma unroll 1
+            for (; ok && fetch(&p); ++n) {
+                bool marked = false;
+                uint32_t *poison = ar.poison + (static_cast<size_t>(cta) * kPoison + n % kPoison) * ROWS * (D / 32);
+                if (half == 0 && lane == 0) mi->poisoned[n % kPoison] = 0;
+                QuantFeed<D, G, BF16, false> f;
+                const int first = (p.t0 << TKS) + 32 * half;
+                f.pages(a, p, first);
+#pragma unroll
+                for (int i = 0; i < f.UN; ++i) f.load(a, ar.qc, p, first, i);
+                if (p.nt > 1) f.pages(a, p, first + TK);
+#pragma unroll 1
+                for (int t = 0; t < p.nt; ++t, ++vn) {
+                    const int st = vn % NV, k0 = (p.t0 + t) << TKS;
+                    unsigned char *v = sm + C::OFF_V + st * C::STAGE;
+                    const bool look = is_masked(p, p.t0 + t);
+                    uint32_t acc[4] = {};
+                    ok = warp_wait(&mi->v_empty[st], (static_cast<uint32_t>(vn / NV) & 1u) ^ 1u);
+                    if (!ok) break;
+#pragma unroll
+                    for (int i = 0; i < f.UN; ++i) {
+                        f.store(v, half, i, look, acc);
+                        if (t + 1 < p.nt) f.load(a, ar.qc, p, first + (t + 1) * TK, i);
+                    }
+                    if (t + 2 < p.nt) f.pages(a, p, first + (t + 2) * TK);
+                    fence_proxy_async_smem();
+                    if (look) {
+                        // an element that is not finite must not reach rows that do not see it (0 x NaN)
+                        const bool found = ((odd16<BF16>(acc[0]) | odd16<BF16>(acc[1]) | odd16<BF16>(acc[2]) | odd16<BF16>(acc[3])) & 0x80008000u) != 0;
+                        const bool any = __any_sync(0xffffffffu, found);
+                        if (lane == 0) {
+                            mi->found[gn & 1][half] = any;
+                            mbar_arrive(&mi->guard);
+                        }
+                        ok = warp_wait(&mi->guard, gn);
+                        if (!ok) break;
+                        const volatile int *fd = mi->found[gn & 1];
+                        ++gn;
+                        if (fd[0] | fd[1]) {
+                            if (half == 0) {
+                                mark_odd<D, BF16>(a, p, k0, min(max(p.kv - k0, 0), TK), TK, v, poison, !marked);
+                                if (lane == 0) mi->poisoned[n % kPoison] = 1;
+                                fence_proxy_async_smem();
+                            }
+                            marked = true;
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&mi->v_ready[st]);
+                }
+            }
+            failed |= !ok;
         }
     } else if (warp == 6) {
         // ------------------------------------------------------------- V producer
@@ -797,6 +1016,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                 const bool odd = *static_cast<volatile int *>(&mi->poisoned[n % kPoison]) != 0;
                 const uint32_t *poison = ar.poison + ((static_cast<size_t>(cta) * kPoison + n % kPoison) * ROWS + urow) * (D / 32);
                 const float inv = l_run > 0.0f ? 1.0f / l_run : (l_run == 0.0f ? 0.0f : l_run);
+                // column of element e of a vector of O's columns (4-bit pages: V's order of every eight)
+                auto at = [](int e) { return QUANT ? (e & ~7) + ((e & 3) << 1) + ((e >> 2) & 1) : e; };
                 const size_t slot = static_cast<size_t>(p.slot < 0 ? 0 : p.slot);
                 float4 *part = reinterpret_cast<float4 *>(ar.ws.o) + slot * (D / 4) * ROWS + urow;
                 unsigned char *stage = sm + C::OFF_OUT + (warp - C::SW) * 2048;
@@ -827,10 +1048,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
 #pragma unroll
                         for (int e = 0; e < 32; e += 8) {
                             uint4 x;
-                            x.x = pack16<BF16>(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
-                            x.y = pack16<BF16>(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-                            x.z = pack16<BF16>(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
-                            x.w = pack16<BF16>(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
+                            x.x = pack16<BF16>(__uint_as_float(o[at(e)]) * inv, __uint_as_float(o[at(e + 1)]) * inv);
+                            x.y = pack16<BF16>(__uint_as_float(o[at(e + 2)]) * inv, __uint_as_float(o[at(e + 3)]) * inv);
+                            x.z = pack16<BF16>(__uint_as_float(o[at(e + 4)]) * inv, __uint_as_float(o[at(e + 5)]) * inv);
+                            x.w = pack16<BF16>(__uint_as_float(o[at(e + 6)]) * inv, __uint_as_float(o[at(e + 7)]) * inv);
                             *reinterpret_cast<uint4 *>(stage + lane * 64 + (((e / 8) ^ ((lane >> 1) & 3)) << 4)) = x;
                         }
                         __syncwarp();
@@ -844,8 +1065,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
                             part[static_cast<size_t>((c + e) / 4) * ROWS] =
-                                make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
-                                            __uint_as_float(o[e + 3]));
+                                make_float4(__uint_as_float(o[at(e)]), __uint_as_float(o[at(e + 1)]), __uint_as_float(o[at(e + 2)]),
+                                            __uint_as_float(o[at(e + 3)]));
                     }
                     __syncwarp();
                 }
@@ -912,9 +1133,9 @@ __global__ void __launch_bounds__(Cfg<D>::ROWS) seq_merge_kernel(const SeqArgs a
     }
 }
 
-template <int D, bool PAGED, bool BF16>
+template <int D, int SRC, bool BF16, int G = 32>
 cudaError_t launch(const Args &ar, const Maps &maps, cudaStream_t s) {
-    auto kern = seq_tc_kernel<D, PAGED, BF16>;
+    auto kern = seq_tc_kernel<D, SRC, BF16, G>;
     static unsigned long long done = 0;
     cudaError_t e = set_smem_limit_once(kern, kSmem<D>, &done);
     if (e != cudaSuccess) return e;
@@ -927,29 +1148,46 @@ cudaError_t launch(const Args &ar, const Maps &maps, cudaStream_t s) {
 }
 
 template <int D>
-cudaError_t launch_dim(const SeqArgs &a, const SeqTcPlan &pl, cudaStream_t s) {
-    Args ar;
-    ar.a = a;
-    ar.G = pl.G;
-    ar.polls = pl.polls;
-    ar.tpt = Cfg<D>::ROWS / a.g;
-    ar.g_inv = (65536u + a.g - 1) / a.g;
+void fill_args(const SeqArgs &a, const SeqTcPlan &pl, Args *ar) {
+    ar->a = a;
+    ar->G = pl.G;
+    ar->polls = pl.polls;
+    ar->tpt = Cfg<D>::ROWS / a.g;
+    ar->g_inv = (65536u + a.g - 1) / a.g;
     char *ws = static_cast<char *>(pl.ws);
-    ar.ws.rec = reinterpret_cast<SeqRec *>(ws + 256);
+    ar->ws.rec = reinterpret_cast<SeqRec *>(ws + 256);
     const size_t slots = 2 * static_cast<size_t>(pl.G), rows = Cfg<D>::ROWS;
     size_t off = 256 + (pl.G * sizeof(SeqRec) + 255) / 256 * 256;
-    ar.ws.ml = reinterpret_cast<float2 *>(ws + off);
+    ar->ws.ml = reinterpret_cast<float2 *>(ws + off);
     off += slots * rows * sizeof(float2);
-    ar.ws.o = reinterpret_cast<float *>(ws + off);
+    ar->ws.o = reinterpret_cast<float *>(ws + off);
     off += slots * rows * D * sizeof(float);
-    ar.poison = reinterpret_cast<uint32_t *>(ws + off);
+    ar->poison = reinterpret_cast<uint32_t *>(ws + off);
+}
+
+template <int D>
+cudaError_t launch_dim(const SeqArgs &a, const SeqTcPlan &pl, cudaStream_t s) {
+    Args ar = {};
+    fill_args<D>(a, pl, &ar);
     Maps maps;
     maps.q = pl.q;
     maps.k = pl.k;
     maps.v = pl.v;
     if (a.kv_lens)
-        return a.bf16 ? launch<D, true, true>(ar, maps, s) : launch<D, true, false>(ar, maps, s);
-    return a.bf16 ? launch<D, false, true>(ar, maps, s) : launch<D, false, false>(ar, maps, s);
+        return a.bf16 ? launch<D, kPages, true>(ar, maps, s) : launch<D, kPages, false>(ar, maps, s);
+    return a.bf16 ? launch<D, kPacked, true>(ar, maps, s) : launch<D, kPacked, false>(ar, maps, s);
+}
+
+// 4-bit pages (pl.k and pl.v are not used).
+template <int D>
+cudaError_t launch_quant_dim(const SeqQuantArgs &a, const SeqTcPlan &pl, cudaStream_t s) {
+    Args ar = {};
+    fill_args<D>(a.s, pl, &ar);
+    ar.qc = a.c;
+    Maps maps = {};
+    maps.q = pl.q;
+    if (a.s.bf16) return a.group == 32 ? launch<D, kQuant, true, 32>(ar, maps, s) : launch<D, kQuant, true, 64>(ar, maps, s);
+    return a.group == 32 ? launch<D, kQuant, false, 32>(ar, maps, s) : launch<D, kQuant, false, 64>(ar, maps, s);
 }
 
 }  // namespace seqtc
