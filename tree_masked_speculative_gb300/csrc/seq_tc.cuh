@@ -33,6 +33,8 @@
 // drains its copies and MMAs, frees TMEM and exits.
 #pragma once
 
+#include <type_traits>
+
 #include "quant_page.cuh"
 #include "seq_sched.cuh"
 #include "sm100_ptx.cuh"
@@ -297,25 +299,55 @@ __device__ __forceinline__ uint32_t max_abs(uint32_t acc, uint32_t w) {
     return r;
 }
 
-// ---- 4-bit pages: a tile is widened to 16-bit values on its way into shared memory, by two warps for K
-// (0 and 3) and two for V (6 and 7, which also do the guards' work).
-// A unit is a key's quads 2 t and 2 t + 1 of every 32-element block (D / 32 words in a row of
-// memory): 8 neighbouring elements of each block.  A warp has 32 keys of a tile, a lane 4 units: t = lane % 4 of
-// keys 8 i + qrow(lane).  Eight lanes that store together cover all banks: rows r and r + 4.
-__device__ __forceinline__ int qrow(int lane) { return (lane >> 3) + ((lane >> 2) & 1) * 4; }
+// ---- 4-bit pages.  Warp 0 brings codes (TMA) and scales and biases (cp.async) of K and V tiles through one ring
+// of raw stages, K two tiles ahead of V; the widening warps (3, 6, 7; for D = 256 also 4 and 5) turn each into a
+// tile of 16-bit values, and guard V's as they go.  One rolled loop serves K and V and holds little code: with
+// K's and V's loops unrolled in two places the instruction cache missed and a key tile took 7300 cycles.
+template <int D, int G>
+struct QuantCfg : Cfg<D> {
+    using B = Cfg<D>;
+    static constexpr int NG = D / G, NDQ = D == 256 ? 5 : 3;           // groups of a row, widening warps
+    static constexpr int NK = D == 128 ? 3 : B::NK, NV = D == 128 ? 3 : B::NV;
+    static constexpr int NR = D == 256 ? 2 : 8;                        // raw stages
+    static constexpr int AFFINE = B::TK * (D / 2), RAW = AFFINE + B::TK * NG * 4;
+    static constexpr int OFF_K = B::OFF_K, OFF_V = OFF_K + NK * B::STAGE;
+    static constexpr int OFF_OUT = OFF_V + NV * B::STAGE, OFF_RAW = OFF_OUT + B::NSTR * 8192;
+    static constexpr int OFF_MISC = OFF_RAW + NR * RAW;
+    static constexpr int kLead = 2;                                    // K tiles ahead of V's
+};
+template <int D, int G>
+constexpr int kQuantSmem = QuantCfg<D, G>::OFF_MISC + kMiscBytes + 400;
+static_assert(kQuantSmem<64, 32> <= 232448 && kQuantSmem<128, 32> <= 232448 && kQuantSmem<256, 32> <= 232448, "shared memory budget");
+struct RawInfo {
+    int kind;             // 0: K, 1: V, 2: no more
+    int first, look, k0;  // V: first tile of its piece, some row does not see all of it, its first key
+};
+struct QuantMisc {
+    uint64_t full[8], empty[8];
+    RawInfo info[8];
+    int found[2][5];
+};
+static_assert(sizeof(QuantMisc) <= 400, "barrier area");
 
+__device__ __forceinline__ void tma_load_raw(void *dst, const CUtensorMap *map, uint64_t *bar, int token, int kh, int page) {
+    tma_load_4d(dst, map, bar, 0, token, kh, page);
+}
+// N 4-byte words to shared memory, zeros where `live` is false.
 template <int N>
-__device__ __forceinline__ void load_words(const uint32_t *p, uint32_t (&w)[N]) {
-    if constexpr (N == 1) {
-        asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(w[0]) : "l"(p));
-    } else if constexpr (N == 2) {
-        asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
-    } else {
+__device__ __forceinline__ void copy_words(uint32_t dst, const uint32_t *src, bool live) {
+    if constexpr (N >= 4) {
 #pragma unroll
         for (int i = 0; i < N; i += 4)
-            asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3]) : "l"(p + i));
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 4 * i), "l"(src + i), "r"(live ? 16 : 0) : "memory");
+    } else {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(4 * N), "r"(live ? 4 * N : 0) : "memory");
     }
 }
+// The barrier gets this thread's arrival once its copies so far are done.
+__device__ __forceinline__ void arrive_after_copies(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
 template <bool BF16>
 __device__ __forceinline__ uint32_t hfma(uint32_t x, uint32_t y, uint32_t z) {
     uint32_t r;
@@ -323,7 +355,7 @@ __device__ __forceinline__ uint32_t hfma(uint32_t x, uint32_t y, uint32_t z) {
     else asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(y), "r"(z));
     return r;
 }
-// scale * code + bias of 8 codes (word x: quad in the low half, the next quad in the high half) as 16-bit pairs of
+// scale * code + bias of 8 codes (word x: a quad in the low half, the next in the high half) as 16-bit pairs of
 // elements n and n + 4, each rounded once.  A code under the exponent of a power of two is that power plus the code
 // (f16: 1024 + c or 1024 + 16 c; bf16: 128 + c); taking the power off again is exact.
 template <bool BF16>
@@ -341,68 +373,54 @@ __device__ __forceinline__ void widen(uint32_t x, uint32_t s2, uint32_t b2, uint
         v[3] = hfma<false>(hfma<false>((y & 0x00f000f0u) | 0x64006400u, part, off16), s2, b2);
     }
 }
-
-// One warp's half of the tiles of K or V.
-template <int D, int G, bool BF16, bool IS_K>
-struct QuantFeed {
-    static constexpr int NB = D / 32, NG = D / G, UN = 4;
-    uint32_t w[UN][NB], sb[UN][NG];
-    int page[2];          // of the lane's next tile: keys 0 .. 15 and 16 .. 31 of the warp's half
-
-    __device__ __forceinline__ void pages(const SeqArgs &a, const SeqPiece &p, int k0) {
+template <int N>
+__device__ __forceinline__ void shared_words(const unsigned char *p, uint32_t (&w)[N]) {
+    if constexpr (N == 1) {
+        w[0] = *reinterpret_cast<const uint32_t *>(p);
+    } else if constexpr (N == 2) {
+        const uint2 x = *reinterpret_cast<const uint2 *>(p);
+        w[0] = x.x; w[1] = x.y;
+    } else {
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const int key = k0 + 16 * b;
-            page[b] = -1;
-            if (key >= p.kv) continue;
-            const int g = __ldg(a.table + static_cast<long long>(p.b) * a.max_pages + (key >> a.page_shift));
-            if (g >= 0 && g < a.n_pages) page[b] = g;
-            // a page before every row's window may be gone
-            else if ((threadIdx.x & 31) == 0 && !(a.window && key + 16 <= p.prefix + p.i0 - a.window + 1)) atomicOr(a.status, kSeqBadPage);
+        for (int i = 0; i < N; i += 4) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(p + 4 * i);
+            w[i] = x.x; w[i + 1] = x.y; w[i + 2] = x.z; w[i + 3] = x.w;
         }
     }
-    __device__ __forceinline__ void load(const SeqArgs &a, const QuantCache &c, const SeqPiece &p, int k0, int i) {
-        const int lane = threadIdx.x & 31, key = k0 + 8 * i + qrow(lane), pg = page[i >> 1];
-        if (pg >= 0 && key < p.kv) {
-            const int in = key & ((1 << a.page_shift) - 1);
-            load_words<NB>((IS_K ? c.kc : c.vc) + pg * c.c_sp + p.kh * c.c_sh + in * c.c_st + (lane & 3) * NB, w[i]);
-            load_words<NG>(static_cast<const uint32_t *>(IS_K ? c.ka : c.va) + pg * c.a_sp + p.kh * c.a_sh + in * c.a_st, sb[i]);
-        } else {
+}
+// 32 units of a tile, one a lane: a key's quads 2 t and 2 t + 1 of every 32-element block (D / 32 words in a row of
+// memory), 8 neighbouring elements of each block, to 64-column slabs of 64 rows with the 128-byte swizzle.  Eight
+// lanes that work together take rows r and r ^ 5: their loads and their stores cover all banks once.  acc: the largest
+// magnitudes, where `look`.
+template <int D, int G, bool BF16>
+__device__ __forceinline__ void widen_units(const unsigned char *raw, unsigned char *tile, int it, bool look, uint32_t (&acc)[4]) {
+    using C = QuantCfg<D, G>;
+    constexpr int NB = D / 32, NG = D / G;
+    const int lane = threadIdx.x & 31, t = lane & 3, r = (lane >> 3) ^ ((lane & 4) ? 5 : 0), row = 8 * it + r;
+    uint32_t w[NB], sb[NG];
+    shared_words<NB>(raw + row * (D / 2) + t * (NB * 4), w);
+    shared_words<NG>(raw + C::AFFINE + row * (NG * 4), sb);
+    unsigned char *dst = tile + row * 128;
 #pragma unroll
-            for (int j = 0; j < NB; ++j) w[i][j] = 0u;
+    for (int j = 0; j < NB; ++j) {
+        const uint32_t x = __byte_perm(w[j / 2], w[NB / 2 + j / 2], j & 1 ? 0x7632 : 0x5410);
+        const uint32_t s2 = __byte_perm(sb[j * 32 / G], 0u, 0x1010), b2 = __byte_perm(sb[j * 32 / G], 0u, 0x3232);
+        uint32_t v[4];
+        widen<BF16>(x, s2, b2, v);
+        if (look) {
 #pragma unroll
-            for (int n = 0; n < NG; ++n) sb[i][n] = 0u;
+            for (int n = 0; n < 4; ++n) acc[n] = max_abs<BF16>(acc[n], v[n]);
         }
+        *reinterpret_cast<uint4 *>(dst + (j / 2) * C::SLAB + ((((j & 1) * 4 + t) ^ (r & 7)) << 4)) =
+            make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410), __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
     }
-    // Unit i into its row of a tile (64-column slabs of 64 rows, 128-byte swizzle).  K's elements are put in
-    // order; V's stay as 0, 4, 1, 5, 2, 6, 3, 7 of every eight, the epilogue's names for O's columns.
-    __device__ __forceinline__ void store(unsigned char *tile, int half, int i, bool look, uint32_t (&acc)[4]) {
-        const int lane = threadIdx.x & 31, t = lane & 3, row = 32 * half + 8 * i + qrow(lane);
-        unsigned char *dst = tile + row * 128;
-#pragma unroll
-        for (int j = 0; j < NB; ++j) {
-            const uint32_t x = __byte_perm(w[i][j / 2], w[i][NB / 2 + j / 2], j & 1 ? 0x7632 : 0x5410);
-            const uint32_t s2 = __byte_perm(sb[i][j * 32 / G], 0u, 0x1010), b2 = __byte_perm(sb[i][j * 32 / G], 0u, 0x3232);
-            uint32_t v[4];
-            widen<BF16>(x, s2, b2, v);
-            uint4 y;
-            if constexpr (IS_K)
-                y = make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410), __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
-            else
-                y = make_uint4(v[0], v[1], v[2], v[3]);
-            if (!IS_K && look) {
-#pragma unroll
-                for (int n = 0; n < 4; ++n) acc[n] = max_abs<BF16>(acc[n], v[n]);
-            }
-            *reinterpret_cast<uint4 *>(dst + (j / 2) * Cfg<D>::SLAB + ((((j & 1) * 4 + t) ^ (row & 7)) << 4)) = y;
-        }
-    }
-};
+}
 
 template <int D, int SRC, bool BF16, int G = 32>
 __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args ar, const __grid_constant__ Maps maps) {
-    using C = Cfg<D>;
     constexpr bool PAGED = SRC == kPages, QUANT = SRC == kQuant;
+    using QC = QuantCfg<D, G>;
+    using C = std::conditional_t<QUANT, QC, Cfg<D>>;
     constexpr int TK = C::TK, TKS = C::TKS, NSTR = C::NSTR, NK = C::NK, NV = C::NV, NS = C::NS, NP = C::NP, ROWS = C::ROWS;
     extern __shared__ __align__(1024) unsigned char sm[];
     const SeqArgs &a = ar.a;
@@ -415,18 +433,21 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
         return;
     }
     Misc *mi = reinterpret_cast<Misc *>(sm + C::OFF_MISC);
+    QuantMisc *qm = reinterpret_cast<QuantMisc *>(sm + C::OFF_MISC + kMiscBytes);     // 4-bit pages only
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
-    // arrivals on a piece's empty slot: issuers, guards, V producer, softmax warps
-    constexpr int kReaders = 2 * NSTR + 3 + 4 * NSTR;
+    // arrivals on a piece's empty slot: issuers, guards (or widening warps), V producer, softmax warps
+    constexpr int kReaders = 2 * NSTR + (QUANT ? QC::NDQ : 2) + 1 + 4 * NSTR;
     if (tid == 0) {
-        for (int i = 0; i < NK; ++i) { mbar_init(&mi->k_full[i], QUANT ? 2 : 1); mbar_init(&mi->k_empty[i], NSTR); }
+        for (int i = 0; i < NK; ++i) { mbar_init(&mi->k_full[i], QUANT ? QC::NDQ : 1); mbar_init(&mi->k_empty[i], NSTR); }
         for (int i = 0; i < NV; ++i) {
             mbar_init(&mi->v_full[i], 1);
-            mbar_init(&mi->v_ready[i], 2);
+            mbar_init(&mi->v_ready[i], QUANT ? QC::NDQ : 2);
             mbar_init(&mi->v_empty[i], NSTR);
         }
         mbar_init(&mi->q_full, 1);
-        mbar_init(&mi->guard, 2);
+        mbar_init(&mi->guard, QUANT ? QC::NDQ : 2);
+        if constexpr (QUANT)
+            for (int i = 0; i < QC::NR; ++i) { mbar_init(&qm->full[i], 33); mbar_init(&qm->empty[i], QC::NDQ); }
         mbar_init(&mi->q_empty, NSTR);
         for (int i = 0; i < 2; ++i) {
             for (int j = 0; j < 2; ++j) {
@@ -449,10 +470,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
     }
     if (warp == 0 && lane == 0) {
         tma_prefetch_desc(&maps.q);
-        if constexpr (!QUANT) {
-            tma_prefetch_desc(&maps.k);
-            tma_prefetch_desc(&maps.v);
-        }
+        tma_prefetch_desc(&maps.k);
+        tma_prefetch_desc(&maps.v);
     }
     pdl_wait();
     const SeqRun run = seq_schedule<C::THREADS, TKS, kUnitCost, 1>(a, ar.tpt, cta, ar.G, &mi->sched);
@@ -465,6 +484,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
 
     // Boxes of bk keys; of a part tile K's are 64 columns wide: lanes 0 .. k_boxes - 1 issue
     // one each (V: lanes 0 .. per_slab - 1).
+    // (4-bit pages: boxes of raw rows; their tiles are whole.)
     const int bk = PAGED ? min(TK, 1 << a.page_shift) : TK, per_slab = TK / bk;          // 1, 2 or 4 boxes
     const int box = lane & (per_slab - 1), slab = bk == TK ? 0 : lane / per_slab, k_boxes = bk == TK ? 1 : per_slab * C::SLABS;
     // page of this lane's box of key tile t (n_pages: out of range, read as zeros)
@@ -501,37 +521,6 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
     // Does some row of the piece not see all of key tile t.
     auto is_masked = [&](const SeqPiece &p, int t) { return (t << TKS) < p.full_lo || ((t + 1) << TKS) > p.full_hi; };
 
-    // 4-bit pages: one warp's half of a piece's K tiles; `after_first` runs behind the first.
-    auto feed_k = [&](int half, const SeqPiece &p, int *kn, bool *ok, auto &&after_first) {
-        if constexpr (QUANT) {
-            QuantFeed<D, G, BF16, true> f;
-            const int k0 = (p.t0 << TKS) + 32 * half;
-            uint32_t none[4];
-            f.pages(a, p, k0);
-#pragma unroll
-            for (int i = 0; i < f.UN; ++i) f.load(a, ar.qc, p, k0, i);
-            if (p.nt > 1) f.pages(a, p, k0 + TK);
-#pragma unroll 1
-            for (int t = 0; t < p.nt; ++t) {
-                const int st = *kn % NK;
-                *ok = warp_wait(&mi->k_empty[st], (static_cast<uint32_t>(*kn / NK) & 1u) ^ 1u);
-                if (!*ok) return;
-#pragma unroll
-                for (int i = 0; i < f.UN; ++i) {
-                    f.store(sm + C::OFF_K + st * C::STAGE, half, i, false, none);
-                    if (t + 1 < p.nt) f.load(a, ar.qc, p, k0 + (t + 1) * TK, i);
-                }
-                if (t + 2 < p.nt) f.pages(a, p, k0 + (t + 2) * TK);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&mi->k_full[st]);
-                ++*kn;
-                if (t == 0) after_first();
-                if (!*ok) return;
-            }
-        }
-    };
-
     // D <= 128: 4 x 128 registers a thread at launch = 2 x 88 + 2 x 168.
     if (warp < C::SW) {
     if constexpr (NSTR == 2) regs_down<88>();
@@ -541,6 +530,63 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
         walk.init(a, ar.tpt, run, &mi->sched, cta);
         int n = 0, kn = 0, qn = 0;                      // pieces, K tiles, Q tiles so far
         bool ok = true;
+        // 4-bit pages: raw jobs so far, K tiles that V is behind; V's piece and how far it is
+        int jn = 0, lead = 0, vt = 0;
+        SeqPiece kp, vp;
+        vp.nt = 0;
+        int kpage[2], vpage[2];                         // pages of this lane's keys (lane, lane + 32) of K's and V's next tile
+        auto raw_pages = [&](const SeqPiece &p, int t, int (&page)[2]) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int key = (t << TKS) + 32 * i + lane;
+                page[i] = a.n_pages;                    // out of range: zeros
+                if (key >= p.kv) continue;
+                const int g = __ldg(a.table + static_cast<long long>(p.b) * a.max_pages + (key >> a.page_shift));
+                if (g >= 0 && g < a.n_pages) page[i] = g;
+                // a page before every row's window may be gone
+                else if (!(a.window && key < p.prefix + p.i0 - a.window + 1)) atomicOr(a.status, kSeqBadPage);
+            }
+        };
+        // codes, scales and biases of tile t of K or V into the next raw stage
+        auto raw_job = [&](int kind, const SeqPiece &p, int t, bool more, int first, int (&page)[2]) -> bool {
+            const int st = jn % QC::NR;
+            if (!warp_wait(&qm->empty[st], (static_cast<uint32_t>(jn / QC::NR) & 1u) ^ 1u)) return false;
+            unsigned char *raw = sm + QC::OFF_RAW + st * QC::RAW;
+            uint64_t *bar = &qm->full[st];
+            const int qk = min(TK, 1 << a.page_shift), boxes = TK / qk, key = t << TKS;     // keys a box
+            if (lane == 0) {
+                qm->info[st] = {kind, first, is_masked(p, t), key};
+                mbar_arrive_expect_tx(bar, QC::AFFINE);
+            }
+            __syncwarp();
+            // the page of box x is that of key qk x: lane (qk x) % 32 holds it
+            const int at = lane * qk, pg = __shfl_sync(0xffffffffu, page[0], at & 31), pg1 = __shfl_sync(0xffffffffu, page[1], at & 31);
+            if (lane < boxes)
+                tma_load_raw(raw + at * (D / 2), kind ? &maps.v : &maps.k, bar, (key + at) & ((1 << a.page_shift) - 1), p.kh, at < 32 ? pg : pg1);
+            const uint32_t *src = static_cast<const uint32_t *>(kind ? ar.qc.va : ar.qc.ka) + p.kh * ar.qc.a_sh;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int k = 32 * i + lane, in = (key + k) & ((1 << a.page_shift) - 1);
+                const bool live = page[i] < a.n_pages;
+                copy_words<QC::NG>(smem_u32(raw) + QC::AFFINE + k * (QC::NG * 4), live ? src + page[i] * ar.qc.a_sp + in * ar.qc.a_st : src, live);
+            }
+            arrive_after_copies(bar);
+            ++jn;
+            if (more) raw_pages(p, t + 1, page);
+            return true;
+        };
+        auto raw_v = [&]() -> bool {
+            const bool first = vt == vp.nt;
+            if (first) {
+                if (!fetch(&vp)) return false;
+                vt = 0;
+                raw_pages(vp, vp.t0, vpage);
+            }
+            if (!raw_job(1, vp, vp.t0 + vt, vt + 1 < vp.nt, first, vpage)) return false;
+            ++vt;
+            --lead;
+            return true;
+        };
         if (lane == 0) ar.ws.rec[cta] = {0, 0, 0, 0};
 #pragma unroll 1
         for (;; ++n) {
@@ -573,7 +619,14 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
             };
             if constexpr (QUANT) {
                 if (n == 0) load_q();
-                feed_k(0, p, &kn, &ok, [&] { if (n > 0) load_q(); });
+                kp = p;
+                raw_pages(kp, kp.t0, kpage);
+#pragma unroll 1
+                for (int t = 0; t < kp.nt && ok; ++t) {
+                    ok = raw_job(0, kp, kp.t0 + t, t + 1 < kp.nt, 0, kpage);
+                    if (ok && t == 0 && n > 0) load_q();
+                    if (ok && ++lead > QC::kLead) ok = raw_v();
+                }
                 if (!ok) break;
                 continue;
             }
@@ -601,7 +654,25 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
             }
             if (!ok) break;
         }
-        failed = !ok;
+        if constexpr (QUANT) {
+            while (ok && lead > 0) ok = raw_v();
+            if (ok) ok = warp_wait(&qm->empty[jn % QC::NR], (static_cast<uint32_t>(jn / QC::NR) & 1u) ^ 1u);
+            if (ok) {                                   // the end, for the widening warps
+                uint64_t *bar = &qm->full[jn % QC::NR];
+                if (lane == 0) {
+                    qm->info[jn % QC::NR].kind = 2;
+                    mbar_arrive(bar);
+                }
+                __syncwarp();
+                mbar_arrive(bar);
+                ++jn;
+            }
+            if (lane == 0)
+                for (int i = max(0, jn - QC::NR); i < jn; ++i)
+                    if (!mbar_wait_sleep(&qm->full[i % QC::NR], static_cast<uint32_t>(i / QC::NR) & 1u, 1u << 21, 1000))
+                        atomicOr(a.status, kSeqTimeout);
+        }
+        failed |= !ok;
         // every copy issued has landed before the CTA's memory goes
         if (lane == 0) {
             if (qn > 0 && !mbar_wait_sleep(&mi->q_full, static_cast<uint32_t>(qn - 1) & 1u, 1u << 21, 1000))
@@ -610,71 +681,70 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                 if (!mbar_wait_sleep(&mi->k_full[i % NK], static_cast<uint32_t>(i / NK) & 1u, 1u << 21, 1000))
                     atomicOr(a.status, kSeqTimeout);
         }
-    } else if (QUANT && warp == 3) {
-        // -------------------------------------------------- 4-bit pages: second half of K
-        int kn = 0;
-        bool ok = true;
-        SeqPiece p;
-#pragma unroll 1
-        while (ok && fetch(&p)) feed_k(1, p, &kn, &ok, [] {});
-        failed |= !ok;
-    } else if (QUANT && (warp == 6 || warp == 7)) {
-        // ------------------------------------------- 4-bit pages: V, guarded as it is widened
+    } else if (QUANT && (warp == 3 || warp >= 6 || (NSTR == 1 && warp >= 4))) {
+        // -------------------------------------------------- 4-bit pages: widening, V guarded
         if constexpr (QUANT) {
-            const int half = warp - 6;
-            int vn = 0, n = 0, gn = 0;                  // V tiles, pieces, masked tiles so far
-            bool ok = true;
+            const int me = NSTR == 1 ? warp - 3 : warp == 3 ? 0 : warp - 5;
+            int jn = 0, kn = 0, vn = 0, n = -1, gn = 0, it = me;   // jobs, K and V tiles, V's piece, masked tiles
+            bool ok = true, marked = false;
             SeqPiece p;
+            uint32_t *poison = nullptr;
 #pragma unroll 1
-            for (; ok && fetch(&p); ++n) {
-                bool marked = false;
-                uint32_t *poison = ar.poison + (static_cast<size_t>(cta) * kPoison + n % kPoison) * ROWS * (D / 32);
-                if (half == 0 && lane == 0) mi->poisoned[n % kPoison] = 0;
-                QuantFeed<D, G, BF16, false> f;
-                const int first = (p.t0 << TKS) + 32 * half;
-                f.pages(a, p, first);
-#pragma unroll
-                for (int i = 0; i < f.UN; ++i) f.load(a, ar.qc, p, first, i);
-                if (p.nt > 1) f.pages(a, p, first + TK);
-#pragma unroll 1
-                for (int t = 0; t < p.nt; ++t, ++vn) {
-                    const int st = vn % NV, k0 = (p.t0 + t) << TKS;
-                    unsigned char *v = sm + C::OFF_V + st * C::STAGE;
-                    const bool look = is_masked(p, p.t0 + t);
-                    uint32_t acc[4] = {};
-                    ok = warp_wait(&mi->v_empty[st], (static_cast<uint32_t>(vn / NV) & 1u) ^ 1u);
+            for (; ok; ++jn) {
+                const int rs = jn % QC::NR;
+                ok = warp_wait(&qm->full[rs], jn / QC::NR);
+                if (!ok) break;
+                const RawInfo info = qm->info[rs];
+                if (info.kind == 2) break;
+                if (info.first) {
+                    ok = fetch(&p);
                     if (!ok) break;
-#pragma unroll
-                    for (int i = 0; i < f.UN; ++i) {
-                        f.store(v, half, i, look, acc);
-                        if (t + 1 < p.nt) f.load(a, ar.qc, p, first + (t + 1) * TK, i);
-                    }
-                    if (t + 2 < p.nt) f.pages(a, p, first + (t + 2) * TK);
-                    fence_proxy_async_smem();
-                    if (look) {
-                        // an element that is not finite must not reach rows that do not see it (0 x NaN)
-                        const bool found = ((odd16<BF16>(acc[0]) | odd16<BF16>(acc[1]) | odd16<BF16>(acc[2]) | odd16<BF16>(acc[3])) & 0x80008000u) != 0;
-                        const bool any = __any_sync(0xffffffffu, found);
-                        if (lane == 0) {
-                            mi->found[gn & 1][half] = any;
-                            mbar_arrive(&mi->guard);
-                        }
-                        ok = warp_wait(&mi->guard, gn);
-                        if (!ok) break;
-                        const volatile int *fd = mi->found[gn & 1];
-                        ++gn;
-                        if (fd[0] | fd[1]) {
-                            if (half == 0) {
-                                mark_odd<D, BF16>(a, p, k0, min(max(p.kv - k0, 0), TK), TK, v, poison, !marked);
-                                if (lane == 0) mi->poisoned[n % kPoison] = 1;
-                                fence_proxy_async_smem();
-                            }
-                            marked = true;
-                        }
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&mi->v_ready[st]);
+                    ++n;
+                    marked = false;
+                    poison = ar.poison + (static_cast<size_t>(cta) * kPoison + n % kPoison) * ROWS * (D / 32);
+                    if (me == 0 && lane == 0) mi->poisoned[n % kPoison] = 0;
                 }
+                const bool is_v = info.kind == 1;
+                const int st = is_v ? vn % NV : kn % NK, round = is_v ? vn / NV : kn / NK;
+                ok = warp_wait(is_v ? &mi->v_empty[st] : &mi->k_empty[st], (static_cast<uint32_t>(round) & 1u) ^ 1u);
+                if (!ok) break;
+                unsigned char *tile = sm + (is_v ? C::OFF_V : C::OFF_K) + st * C::STAGE;
+                const bool look = is_v && info.look;
+                uint32_t acc[4] = {};
+#pragma unroll 1
+                for (; it < 8; it += QC::NDQ) widen_units<D, G, BF16>(sm + QC::OFF_RAW + rs * QC::RAW, tile, it, look, acc);
+                it -= 8;                                // the warps' shares are even over the jobs
+                fence_proxy_async_smem();
+                if (look) {
+                    // an element that is not finite must not reach rows that do not see it (0 x NaN)
+                    const bool found = ((odd16<BF16>(acc[0]) | odd16<BF16>(acc[1]) | odd16<BF16>(acc[2]) | odd16<BF16>(acc[3])) & 0x80008000u) != 0;
+                    const bool any = __any_sync(0xffffffffu, found);
+                    if (lane == 0) {
+                        qm->found[gn & 1][me] = any;
+                        mbar_arrive(&mi->guard);
+                    }
+                    ok = warp_wait(&mi->guard, gn);
+                    if (!ok) break;
+                    const volatile int *f = qm->found[gn & 1];
+                    ++gn;
+                    int all = 0;
+#pragma unroll
+                    for (int i = 0; i < QC::NDQ; ++i) all |= f[i];
+                    if (all) {
+                        if (me == 0) {
+                            mark_odd<D, BF16>(a, p, info.k0, min(max(p.kv - info.k0, 0), TK), TK, tile, poison, !marked);
+                            if (lane == 0) mi->poisoned[n % kPoison] = 1;
+                            fence_proxy_async_smem();
+                        }
+                        marked = true;
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(is_v ? &mi->v_ready[st] : &mi->k_full[st]);
+                    mbar_arrive(&qm->empty[rs]);
+                }
+                if (is_v) ++vn; else ++kn;
             }
             failed |= !ok;
         }
@@ -1016,8 +1086,6 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                 const bool odd = *static_cast<volatile int *>(&mi->poisoned[n % kPoison]) != 0;
                 const uint32_t *poison = ar.poison + ((static_cast<size_t>(cta) * kPoison + n % kPoison) * ROWS + urow) * (D / 32);
                 const float inv = l_run > 0.0f ? 1.0f / l_run : (l_run == 0.0f ? 0.0f : l_run);
-                // column of element e of a vector of O's columns (4-bit pages: V's order of every eight)
-                auto at = [](int e) { return QUANT ? (e & ~7) + ((e & 3) << 1) + ((e >> 2) & 1) : e; };
                 const size_t slot = static_cast<size_t>(p.slot < 0 ? 0 : p.slot);
                 float4 *part = reinterpret_cast<float4 *>(ar.ws.o) + slot * (D / 4) * ROWS + urow;
                 unsigned char *stage = sm + C::OFF_OUT + (warp - C::SW) * 2048;
@@ -1048,10 +1116,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
 #pragma unroll
                         for (int e = 0; e < 32; e += 8) {
                             uint4 x;
-                            x.x = pack16<BF16>(__uint_as_float(o[at(e)]) * inv, __uint_as_float(o[at(e + 1)]) * inv);
-                            x.y = pack16<BF16>(__uint_as_float(o[at(e + 2)]) * inv, __uint_as_float(o[at(e + 3)]) * inv);
-                            x.z = pack16<BF16>(__uint_as_float(o[at(e + 4)]) * inv, __uint_as_float(o[at(e + 5)]) * inv);
-                            x.w = pack16<BF16>(__uint_as_float(o[at(e + 6)]) * inv, __uint_as_float(o[at(e + 7)]) * inv);
+                            x.x = pack16<BF16>(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+                            x.y = pack16<BF16>(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+                            x.z = pack16<BF16>(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
+                            x.w = pack16<BF16>(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
                             *reinterpret_cast<uint4 *>(stage + lane * 64 + (((e / 8) ^ ((lane >> 1) & 3)) << 4)) = x;
                         }
                         __syncwarp();
@@ -1065,8 +1133,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
                             part[static_cast<size_t>((c + e) / 4) * ROWS] =
-                                make_float4(__uint_as_float(o[at(e)]), __uint_as_float(o[at(e + 1)]), __uint_as_float(o[at(e + 2)]),
-                                            __uint_as_float(o[at(e + 3)]));
+                                make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
+                                            __uint_as_float(o[e + 3]));
                     }
                     __syncwarp();
                 }
@@ -1137,9 +1205,10 @@ template <int D, int SRC, bool BF16, int G = 32>
 cudaError_t launch(const Args &ar, const Maps &maps, cudaStream_t s) {
     auto kern = seq_tc_kernel<D, SRC, BF16, G>;
     static unsigned long long done = 0;
-    cudaError_t e = set_smem_limit_once(kern, kSmem<D>, &done);
+    constexpr int smem = SRC == kQuant ? kQuantSmem<D, G> : kSmem<D>;
+    cudaError_t e = set_smem_limit_once(kern, smem, &done);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(kern, dim3(ar.G), dim3(Cfg<D>::THREADS), kSmem<D>, s, ar, maps);
+    e = launch_pdl(kern, dim3(ar.G), dim3(Cfg<D>::THREADS), smem, s, ar, maps);
     count_launch();
     if (e != cudaSuccess) return e;
     e = launch_pdl(seq_merge_kernel<D, BF16>, dim3(ar.G, D / 16), dim3(Cfg<D>::ROWS), 0, s, ar.a, ar.ws);
@@ -1178,14 +1247,16 @@ cudaError_t launch_dim(const SeqArgs &a, const SeqTcPlan &pl, cudaStream_t s) {
     return a.bf16 ? launch<D, kPacked, true>(ar, maps, s) : launch<D, kPacked, false>(ar, maps, s);
 }
 
-// 4-bit pages (pl.k and pl.v are not used).
+// 4-bit pages: pl.k and pl.v are maps of the codes.
 template <int D>
 cudaError_t launch_quant_dim(const SeqQuantArgs &a, const SeqTcPlan &pl, cudaStream_t s) {
     Args ar = {};
     fill_args<D>(a.s, pl, &ar);
     ar.qc = a.c;
-    Maps maps = {};
+    Maps maps;
     maps.q = pl.q;
+    maps.k = pl.k;
+    maps.v = pl.v;
     if (a.s.bf16) return a.group == 32 ? launch<D, kQuant, true, 32>(ar, maps, s) : launch<D, kQuant, true, 64>(ar, maps, s);
     return a.group == 32 ? launch<D, kQuant, false, 32>(ar, maps, s) : launch<D, kQuant, false, 64>(ar, maps, s);
 }
