@@ -257,7 +257,7 @@ __device__ __forceinline__ int v_offset(int bk, int slab, int row) {
 // One warp: mark the rows that see an element of this V tile that is not finite
 // (bit d of a row's marks), and take the element out.
 template <int D, bool BF16>
-__device__ __noinline__ void mark_odd(const SeqArgs &a, const SeqPiece &p, int k0, int live, int bk, unsigned char *v,
+__device__ __noinline__ void mark_odd(const SeqArgs &a, const SeqPiece &p, int k0, int r0, int live, int bk, unsigned char *v,
                                       uint32_t *poison, bool clear) {
     using C = Cfg<D>;
     const int lane = threadIdx.x & 31;
@@ -265,7 +265,7 @@ __device__ __noinline__ void mark_odd(const SeqArgs &a, const SeqPiece &p, int k
         for (int i = lane; i < C::ROWS * (D / 32); i += 32) poison[i] = 0u;
     __syncwarp();
 #pragma unroll 1
-    for (int r = 0; r < live; ++r)
+    for (int r = r0; r < live; ++r)
 #pragma unroll 1
         for (int c = lane; c < D / 2; c += 32) {
             // column pair c of key row r, at its swizzled place
@@ -299,36 +299,43 @@ __device__ __forceinline__ uint32_t max_abs(uint32_t acc, uint32_t w) {
     return r;
 }
 
-// ---- 4-bit pages.  Warp 0 brings codes (TMA) and scales and biases (cp.async) of K and V tiles through one ring
-// of raw stages, K two tiles ahead of V; the widening warps (3, 6, 7; for D = 256 also 4 and 5) turn each into a
-// tile of 16-bit values, and guard V's as they go.  One rolled loop serves K and V and holds little code: with
-// K's and V's loops unrolled in two places the instruction cache missed and a key tile took 7300 cycles.
+// ---- 4-bit pages.  Warp 0 brings codes (TMA) and scales and biases (cp.async) of K and V tiles to raw stages, K
+// two tiles ahead of V's; widening warps turn them into tiles of 16-bit values and guard V's as they go.  For D <= 128
+// warps 3, 6 and 7 take every third tile of K and of V whole, K and V in turn; for D = 256 warps 3 and 4 take
+// a half each of every K tile, 6 and 7 of every V tile.  A stage and a slot of the rings belong to the same warps
+// always (3 of each, or all of them), who so see each of a barrier's phases: a wait tells phases apart by parity alone.
+// (A third of every tile each, all waiting for the same barriers: 524 us for the chunks of twelve requests.)  One
+// rolled loop serves K and V and holds little code: with loops of their own, unrolled, the instruction cache missed
+// and they took 1046 us.
 template <int D, int G>
 struct QuantCfg : Cfg<D> {
     using B = Cfg<D>;
-    static constexpr int NG = D / G, NDQ = D == 256 ? 5 : 3;           // groups of a row, widening warps
-    static constexpr int NK = D == 128 ? 3 : B::NK, NV = D == 128 ? 3 : B::NV;
-    static constexpr int NR = D == 256 ? 2 : 8;                        // raw stages
+    static constexpr int NG = D / G;
+    static constexpr int PARTS = D == 256 ? 2 : 1;                     // warps that share a tile
+    static constexpr int NK = D == 256 ? 2 : 3, NV = NK;
+    static constexpr int NR = D == 256 ? 1 : 3;                        // raw stages of K, and of V
+    static_assert(PARTS == 2 || (NK == 3 && NR == 3), "a slot and a stage belong to one warp");
     static constexpr int AFFINE = B::TK * (D / 2), RAW = AFFINE + B::TK * NG * 4;
     static constexpr int OFF_K = B::OFF_K, OFF_V = OFF_K + NK * B::STAGE;
     static constexpr int OFF_OUT = OFF_V + NV * B::STAGE, OFF_RAW = OFF_OUT + B::NSTR * 8192;
-    static constexpr int OFF_MISC = OFF_RAW + NR * RAW;
+    static constexpr int OFF_MISC = OFF_RAW + 2 * NR * RAW;
     static constexpr int kLead = 2;                                    // K tiles ahead of V's
 };
-template <int D, int G>
-constexpr int kQuantSmem = QuantCfg<D, G>::OFF_MISC + kMiscBytes + 400;
-static_assert(kQuantSmem<64, 32> <= 232448 && kQuantSmem<128, 32> <= 232448 && kQuantSmem<256, 32> <= 232448, "shared memory budget");
 struct RawInfo {
-    int kind;             // 0: K, 1: V, 2: no more
-    int first, look, k0;  // V: first tile of its piece, some row does not see all of it, its first key
+    int end;              // no more tiles
+    int look, n, k0;      // V: some row does not see all of it; its piece's number, its first key
+    SeqPiece p;           // V, where look
 };
 struct QuantMisc {
-    uint64_t full[8], empty[8];
-    RawInfo info[8];
-    int found[2][5];
+    uint64_t full[6], empty[6];   // of K's raw stages, then V's
+    RawInfo info[6];
 };
-static_assert(sizeof(QuantMisc) <= 400, "barrier area");
+constexpr int kQuantMiscBytes = 800;
+static_assert(sizeof(QuantMisc) <= kQuantMiscBytes, "barrier area");
 
+template <int D, int G>
+constexpr int kQuantSmem = QuantCfg<D, G>::OFF_MISC + kMiscBytes + kQuantMiscBytes;
+static_assert(kQuantSmem<64, 32> <= 232448 && kQuantSmem<128, 32> <= 232448 && kQuantSmem<256, 32> <= 232448, "shared memory budget");
 __device__ __forceinline__ void tma_load_raw(void *dst, const CUtensorMap *map, uint64_t *bar, int token, int kh, int page) {
     tma_load_4d(dst, map, bar, 0, token, kh, page);
 }
@@ -388,32 +395,56 @@ __device__ __forceinline__ void shared_words(const unsigned char *p, uint32_t (&
         }
     }
 }
-// 32 units of a tile, one a lane: a key's quads 2 t and 2 t + 1 of every 32-element block (D / 32 words in a row of
-// memory), 8 neighbouring elements of each block, to 64-column slabs of 64 rows with the 128-byte swizzle.  Eight
-// lanes that work together take rows r and r ^ 5: their loads and their stores cover all banks once.  acc: the largest
-// magnitudes, where `look`.
-template <int D, int G, bool BF16>
-__device__ __forceinline__ void widen_units(const unsigned char *raw, unsigned char *tile, int it, bool look, uint32_t (&acc)[4]) {
+// 32 U units of a tile, U a lane: a unit is a key's quads 2 t and 2 t + 1 of every 32-element block (D / 32 words in a
+// row of memory), 8 neighbouring elements of each block, to 64-column slabs of 64 rows with the 128-byte swizzle.  Eight
+// lanes that work together take rows r and r ^ 5: their loads and their stores cover all banks once.  K's elements
+// are put in order, V's stay as 0, 4, 1, 5, 2, 6, 3, 7 of every eight (the epilogue names O's columns so).
+// acc: the largest magnitudes, where `look`.
+template <int D, int G, bool BF16, int U>
+__device__ __forceinline__ void widen_units(const unsigned char *raw, unsigned char *tile, int it, bool order, bool look, uint32_t (&acc)[4]) {
     using C = QuantCfg<D, G>;
     constexpr int NB = D / 32, NG = D / G;
     const int lane = threadIdx.x & 31, t = lane & 3, r = (lane >> 3) ^ ((lane & 4) ? 5 : 0), row = 8 * it + r;
-    uint32_t w[NB], sb[NG];
-    shared_words<NB>(raw + row * (D / 2) + t * (NB * 4), w);
-    shared_words<NG>(raw + C::AFFINE + row * (NG * 4), sb);
-    unsigned char *dst = tile + row * 128;
+    uint32_t w[U][NB], sb[U][NG];
 #pragma unroll
-    for (int j = 0; j < NB; ++j) {
-        const uint32_t x = __byte_perm(w[j / 2], w[NB / 2 + j / 2], j & 1 ? 0x7632 : 0x5410);
-        const uint32_t s2 = __byte_perm(sb[j * 32 / G], 0u, 0x1010), b2 = __byte_perm(sb[j * 32 / G], 0u, 0x3232);
-        uint32_t v[4];
-        widen<BF16>(x, s2, b2, v);
-        if (look) {
-#pragma unroll
-            for (int n = 0; n < 4; ++n) acc[n] = max_abs<BF16>(acc[n], v[n]);
-        }
-        *reinterpret_cast<uint4 *>(dst + (j / 2) * C::SLAB + ((((j & 1) * 4 + t) ^ (r & 7)) << 4)) =
-            make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410), __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
+    for (int u = 0; u < U; ++u) {
+        shared_words<NB>(raw + (row + 8 * u) * (D / 2) + t * (NB * 4), w[u]);
+        shared_words<NG>(raw + C::AFFINE + (row + 8 * u) * (NG * 4), sb[u]);
     }
+    unsigned char *dst = tile + row * 128 + ((t ^ r) << 4);
+    const int odd = (r & 4) ? -64 : 64;                 // from an even block's place to the odd one's
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j0 = 0; j0 < NB; j0 += 4) {
+            constexpr int NJ = NB < 4 ? NB : 4;
+            uint32_t v[NJ][4];
+#pragma unroll
+            for (int jj = 0; jj < NJ; ++jj) {
+                const int j = j0 + jj;
+                const uint32_t x = __byte_perm(w[u][j / 2], w[u][NB / 2 + j / 2], j & 1 ? 0x7632 : 0x5410);
+                widen<BF16>(x, __byte_perm(sb[u][j * 32 / G], 0u, 0x1010), __byte_perm(sb[u][j * 32 / G], 0u, 0x3232), v[jj]);
+            }
+            if (look) {
+#pragma unroll
+                for (int jj = 0; jj < NJ; ++jj)
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) acc[n] = max_abs<BF16>(acc[n], v[jj][n]);
+            }
+            if (order) {
+#pragma unroll
+                for (int jj = 0; jj < NJ; ++jj) {
+                    const uint32_t a = v[jj][0], b = v[jj][1], c = v[jj][2], d = v[jj][3];
+                    v[jj][0] = __byte_perm(a, b, 0x5410);
+                    v[jj][1] = __byte_perm(c, d, 0x5410);
+                    v[jj][2] = __byte_perm(a, b, 0x7632);
+                    v[jj][3] = __byte_perm(c, d, 0x7632);
+                }
+            }
+#pragma unroll
+            for (int jj = 0; jj < NJ; ++jj)
+                *reinterpret_cast<uint4 *>(dst + 1024 * u + ((j0 + jj) / 2) * C::SLAB + (jj & 1 ? odd : 0)) = make_uint4(v[jj][0], v[jj][1], v[jj][2], v[jj][3]);
+        }
 }
 
 template <int D, int SRC, bool BF16, int G = 32>
@@ -435,19 +466,19 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
     Misc *mi = reinterpret_cast<Misc *>(sm + C::OFF_MISC);
     QuantMisc *qm = reinterpret_cast<QuantMisc *>(sm + C::OFF_MISC + kMiscBytes);     // 4-bit pages only
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
-    // arrivals on a piece's empty slot: issuers, guards (or widening warps), V producer, softmax warps
-    constexpr int kReaders = 2 * NSTR + (QUANT ? QC::NDQ : 2) + 1 + 4 * NSTR;
+    // arrivals on a piece's empty slot: issuers, guards, V producer, softmax warps
+    constexpr int kReaders = 2 * NSTR + (QUANT ? 0 : 2) + 1 + 4 * NSTR;
     if (tid == 0) {
-        for (int i = 0; i < NK; ++i) { mbar_init(&mi->k_full[i], QUANT ? QC::NDQ : 1); mbar_init(&mi->k_empty[i], NSTR); }
+        for (int i = 0; i < NK; ++i) { mbar_init(&mi->k_full[i], QUANT ? QC::PARTS : 1); mbar_init(&mi->k_empty[i], NSTR); }
         for (int i = 0; i < NV; ++i) {
             mbar_init(&mi->v_full[i], 1);
-            mbar_init(&mi->v_ready[i], QUANT ? QC::NDQ : 2);
+            mbar_init(&mi->v_ready[i], QUANT ? QC::PARTS : 2);
             mbar_init(&mi->v_empty[i], NSTR);
         }
         mbar_init(&mi->q_full, 1);
-        mbar_init(&mi->guard, QUANT ? QC::NDQ : 2);
+        mbar_init(&mi->guard, 2);
         if constexpr (QUANT)
-            for (int i = 0; i < QC::NR; ++i) { mbar_init(&qm->full[i], 33); mbar_init(&qm->empty[i], QC::NDQ); }
+            for (int i = 0; i < 2 * QC::NR; ++i) { mbar_init(&qm->full[i], 33); mbar_init(&qm->empty[i], QC::PARTS); }
         mbar_init(&mi->q_empty, NSTR);
         for (int i = 0; i < 2; ++i) {
             for (int j = 0; j < 2; ++j) {
@@ -530,8 +561,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
         walk.init(a, ar.tpt, run, &mi->sched, cta);
         int n = 0, kn = 0, qn = 0;                      // pieces, K tiles, Q tiles so far
         bool ok = true;
-        // 4-bit pages: raw jobs so far, K tiles that V is behind; V's piece and how far it is
-        int jn = 0, lead = 0, vt = 0;
+        // 4-bit pages: K tiles that V is behind; V's tiles so far, its piece, how far that is, its number
+        int lead = 0, vn = 0, vt = 0, vpn = -1;
         SeqPiece kp, vp;
         vp.nt = 0;
         int kpage[2], vpage[2];                         // pages of this lane's keys (lane, lane + 32) of K's and V's next tile
@@ -548,14 +579,19 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
             }
         };
         // codes, scales and biases of tile t of K or V into the next raw stage
-        auto raw_job = [&](int kind, const SeqPiece &p, int t, bool more, int first, int (&page)[2]) -> bool {
-            const int st = jn % QC::NR;
+        auto raw_job = [&](int kind, const SeqPiece &p, int t, bool more, int (&page)[2]) -> bool {
+            const int jn = kind ? vn : kn, st = kind * QC::NR + jn % QC::NR;
             if (!warp_wait(&qm->empty[st], (static_cast<uint32_t>(jn / QC::NR) & 1u) ^ 1u)) return false;
             unsigned char *raw = sm + QC::OFF_RAW + st * QC::RAW;
             uint64_t *bar = &qm->full[st];
             const int qk = min(TK, 1 << a.page_shift), boxes = TK / qk, key = t << TKS;     // keys a box
             if (lane == 0) {
-                qm->info[st] = {kind, first, is_masked(p, t), key};
+                RawInfo &info = qm->info[st];
+                info.end = 0;
+                info.look = kind && is_masked(p, t);
+                info.n = vpn;
+                info.k0 = key;
+                if (info.look) info.p = p;
                 mbar_arrive_expect_tx(bar, QC::AFFINE);
             }
             __syncwarp();
@@ -571,18 +607,18 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                 copy_words<QC::NG>(smem_u32(raw) + QC::AFFINE + k * (QC::NG * 4), live ? src + page[i] * ar.qc.a_sp + in * ar.qc.a_st : src, live);
             }
             arrive_after_copies(bar);
-            ++jn;
+            ++(kind ? vn : kn);
             if (more) raw_pages(p, t + 1, page);
             return true;
         };
         auto raw_v = [&]() -> bool {
-            const bool first = vt == vp.nt;
-            if (first) {
+            if (vt == vp.nt) {
                 if (!fetch(&vp)) return false;
                 vt = 0;
+                ++vpn;
                 raw_pages(vp, vp.t0, vpage);
             }
-            if (!raw_job(1, vp, vp.t0 + vt, vt + 1 < vp.nt, first, vpage)) return false;
+            if (!raw_job(1, vp, vp.t0 + vt, vt + 1 < vp.nt, vpage)) return false;
             ++vt;
             --lead;
             return true;
@@ -597,6 +633,16 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
             if (n >= kPieces)
                 ok = warp_wait(&mi->piece_empty[i], n / kPieces - 1);
             if (!ok) break;
+            if constexpr (QUANT) {
+                // no marks of the piece's columns yet; the piece that had their place has been written out
+                uint32_t *poison = ar.poison + (static_cast<size_t>(cta) * kPoison + n % kPoison) * ROWS * (D / 32);
+                if (lane == 0) mi->poisoned[n % kPoison] = 0;
+                if (more && (((p.t0 + p.nt) << TKS) > p.full_hi || (p.t0 << TKS) < p.full_lo)) {   // some tile is looked at
+                    for (int x = lane; x < p.rows * (D / 32); x += 32) poison[x] = 0u;
+                    __threadfence();
+                }
+                __syncwarp();
+            }
             if (lane == 0) {
                 mi->piece[i] = p;
                 mbar_arrive(&mi->piece_full[i]);
@@ -623,7 +669,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                 raw_pages(kp, kp.t0, kpage);
 #pragma unroll 1
                 for (int t = 0; t < kp.nt && ok; ++t) {
-                    ok = raw_job(0, kp, kp.t0 + t, t + 1 < kp.nt, 0, kpage);
+                    ok = raw_job(0, kp, kp.t0 + t, t + 1 < kp.nt, kpage);
                     if (ok && t == 0 && n > 0) load_q();
                     if (ok && ++lead > QC::kLead) ok = raw_v();
                 }
@@ -656,21 +702,27 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
         }
         if constexpr (QUANT) {
             while (ok && lead > 0) ok = raw_v();
-            if (ok) ok = warp_wait(&qm->empty[jn % QC::NR], (static_cast<uint32_t>(jn / QC::NR) & 1u) ^ 1u);
-            if (ok) {                                   // the end, for the widening warps
-                uint64_t *bar = &qm->full[jn % QC::NR];
+            // the end, at each stage of K (D = 256: of K and of V)
+#pragma unroll 1
+            for (int i = 0; ok && i < (QC::PARTS == 2 ? 2 : QC::NR); ++i) {
+                const int kind = QC::PARTS == 2 ? i : 0, jn = kind ? vn : kn, st = kind * QC::NR + jn % QC::NR;
+                ok = warp_wait(&qm->empty[st], (static_cast<uint32_t>(jn / QC::NR) & 1u) ^ 1u);
+                if (!ok) break;
                 if (lane == 0) {
-                    qm->info[jn % QC::NR].kind = 2;
-                    mbar_arrive(bar);
+                    qm->info[st].end = 1;
+                    mbar_arrive(&qm->full[st]);
                 }
                 __syncwarp();
-                mbar_arrive(bar);
-                ++jn;
+                mbar_arrive(&qm->full[st]);
+                ++(kind ? vn : kn);
             }
             if (lane == 0)
-                for (int i = max(0, jn - QC::NR); i < jn; ++i)
-                    if (!mbar_wait_sleep(&qm->full[i % QC::NR], static_cast<uint32_t>(i / QC::NR) & 1u, 1u << 21, 1000))
+                for (int i = 0; i < 2 * QC::NR; ++i) {
+                    // the stage's last job
+                    const int c = i < QC::NR ? kn : vn, jn = c - 1 - ((c - 1 - i % QC::NR) % QC::NR + QC::NR) % QC::NR;
+                    if (jn >= 0 && !mbar_wait_sleep(&qm->full[i], static_cast<uint32_t>(jn / QC::NR) & 1u, 1u << 21, 1000))
                         atomicOr(a.status, kSeqTimeout);
+                }
         }
         failed |= !ok;
         // every copy issued has landed before the CTA's memory goes
@@ -681,70 +733,52 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                 if (!mbar_wait_sleep(&mi->k_full[i % NK], static_cast<uint32_t>(i / NK) & 1u, 1u << 21, 1000))
                     atomicOr(a.status, kSeqTimeout);
         }
-    } else if (QUANT && (warp == 3 || warp >= 6 || (NSTR == 1 && warp >= 4))) {
+    } else if (QUANT && (warp == 3 || warp >= 6 || (NSTR == 1 && warp == 4))) {
         // -------------------------------------------------- 4-bit pages: widening, V guarded
         if constexpr (QUANT) {
-            const int me = NSTR == 1 ? warp - 3 : warp == 3 ? 0 : warp - 5;
-            int jn = 0, kn = 0, vn = 0, n = -1, gn = 0, it = me;   // jobs, K and V tiles, V's piece, masked tiles
-            bool ok = true, marked = false;
-            SeqPiece p;
-            uint32_t *poison = nullptr;
+            constexpr int PARTS = QC::PARTS, ITS = 8 / PARTS, U = D == 256 ? 1 : 2;
+            const int part = PARTS == 2 ? (warp == 4 || warp == 7) : 0;
+            int kind = PARTS == 2 && warp >= 6;         // 0: K, 1: V
+            int j = PARTS == 2 ? 0 : warp == 3 ? 0 : warp - 5;   // tile
+            bool ok = true;
 #pragma unroll 1
-            for (; ok; ++jn) {
-                const int rs = jn % QC::NR;
-                ok = warp_wait(&qm->full[rs], jn / QC::NR);
+            for (;;) {
+                const int rs = kind * QC::NR + j % QC::NR, st = j % NK;
+                ok = warp_wait(&qm->full[rs], j / QC::NR);
                 if (!ok) break;
-                const RawInfo info = qm->info[rs];
-                if (info.kind == 2) break;
-                if (info.first) {
-                    ok = fetch(&p);
-                    if (!ok) break;
-                    ++n;
-                    marked = false;
-                    poison = ar.poison + (static_cast<size_t>(cta) * kPoison + n % kPoison) * ROWS * (D / 32);
-                    if (me == 0 && lane == 0) mi->poisoned[n % kPoison] = 0;
-                }
-                const bool is_v = info.kind == 1;
-                const int st = is_v ? vn % NV : kn % NK, round = is_v ? vn / NV : kn / NK;
-                ok = warp_wait(is_v ? &mi->v_empty[st] : &mi->k_empty[st], (static_cast<uint32_t>(round) & 1u) ^ 1u);
+                const RawInfo &info = qm->info[rs];
+                if (info.end) break;
+                const bool look = kind && info.look;
+                ok = warp_wait(kind ? &mi->v_empty[st] : &mi->k_empty[st], (static_cast<uint32_t>(j / NK) & 1u) ^ 1u);
                 if (!ok) break;
-                unsigned char *tile = sm + (is_v ? C::OFF_V : C::OFF_K) + st * C::STAGE;
-                const bool look = is_v && info.look;
+                unsigned char *tile = sm + (kind ? C::OFF_V : C::OFF_K) + st * C::STAGE;
                 uint32_t acc[4] = {};
 #pragma unroll 1
-                for (; it < 8; it += QC::NDQ) widen_units<D, G, BF16>(sm + QC::OFF_RAW + rs * QC::RAW, tile, it, look, acc);
-                it -= 8;                                // the warps' shares are even over the jobs
-                fence_proxy_async_smem();
+                for (int it = ITS * part; it < ITS * (part + 1); it += U)
+                    widen_units<D, G, BF16, U>(sm + QC::OFF_RAW + rs * QC::RAW, tile, it, kind == 0, look, acc);
                 if (look) {
-                    // an element that is not finite must not reach rows that do not see it (0 x NaN)
+                    // an element that is not finite must not reach rows that do not see it (0 x NaN): it is taken out,
+                    // and the rows that see it are marked
                     const bool found = ((odd16<BF16>(acc[0]) | odd16<BF16>(acc[1]) | odd16<BF16>(acc[2]) | odd16<BF16>(acc[3])) & 0x80008000u) != 0;
-                    const bool any = __any_sync(0xffffffffu, found);
-                    if (lane == 0) {
-                        qm->found[gn & 1][me] = any;
-                        mbar_arrive(&mi->guard);
-                    }
-                    ok = warp_wait(&mi->guard, gn);
-                    if (!ok) break;
-                    const volatile int *f = qm->found[gn & 1];
-                    ++gn;
-                    int all = 0;
-#pragma unroll
-                    for (int i = 0; i < QC::NDQ; ++i) all |= f[i];
-                    if (all) {
-                        if (me == 0) {
-                            mark_odd<D, BF16>(a, p, info.k0, min(max(p.kv - info.k0, 0), TK), TK, tile, poison, !marked);
-                            if (lane == 0) mi->poisoned[n % kPoison] = 1;
-                            fence_proxy_async_smem();
-                        }
-                        marked = true;
+                    if (__any_sync(0xffffffffu, found)) {
+                        const int n = info.n % kPoison, r0 = 8 * ITS * part;
+                        mark_odd<D, BF16>(a, info.p, info.k0, r0, min(max(info.p.kv - info.k0, 0), r0 + 8 * ITS), TK, tile,
+                                          ar.poison + (static_cast<size_t>(cta) * kPoison + n) * ROWS * (D / 32), false);
+                        if (lane == 0) mi->poisoned[n] = 1;
                     }
                 }
+                fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(is_v ? &mi->v_ready[st] : &mi->k_full[st]);
+                    mbar_arrive(kind ? &mi->v_ready[st] : &mi->k_full[st]);
                     mbar_arrive(&qm->empty[rs]);
                 }
-                if (is_v) ++vn; else ++kn;
+                if (PARTS == 2) {
+                    ++j;
+                } else {
+                    j += 3 * kind;
+                    kind ^= 1;
+                }
             }
             failed |= !ok;
         }
@@ -933,7 +967,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                     ++gn;
                     if (f[0] | f[1]) {
                         if (part == 0) {
-                            mark_odd<D, BF16>(a, p, k0, live, bk, v, poison, !marked);
+                            mark_odd<D, BF16>(a, p, k0, 0, live, bk, v, poison, !marked);
                             if (lane == 0) mi->poisoned[n % kPoison] = 1;
                             fence_proxy_async_smem();
                         }
@@ -1086,6 +1120,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                 const bool odd = *static_cast<volatile int *>(&mi->poisoned[n % kPoison]) != 0;
                 const uint32_t *poison = ar.poison + ((static_cast<size_t>(cta) * kPoison + n % kPoison) * ROWS + urow) * (D / 32);
                 const float inv = l_run > 0.0f ? 1.0f / l_run : (l_run == 0.0f ? 0.0f : l_run);
+                // column of element e of a run of O's columns (4-bit pages: V's order of every eight)
+                auto at = [](int e) { return QUANT ? (e & ~7) + ((e & 3) << 1) + ((e >> 2) & 1) : e; };
                 const size_t slot = static_cast<size_t>(p.slot < 0 ? 0 : p.slot);
                 float4 *part = reinterpret_cast<float4 *>(ar.ws.o) + slot * (D / 4) * ROWS + urow;
                 unsigned char *stage = sm + C::OFF_OUT + (warp - C::SW) * 2048;
@@ -1116,10 +1152,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
 #pragma unroll
                         for (int e = 0; e < 32; e += 8) {
                             uint4 x;
-                            x.x = pack16<BF16>(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
-                            x.y = pack16<BF16>(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-                            x.z = pack16<BF16>(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
-                            x.w = pack16<BF16>(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
+                            x.x = pack16<BF16>(__uint_as_float(o[at(e)]) * inv, __uint_as_float(o[at(e + 1)]) * inv);
+                            x.y = pack16<BF16>(__uint_as_float(o[at(e + 2)]) * inv, __uint_as_float(o[at(e + 3)]) * inv);
+                            x.z = pack16<BF16>(__uint_as_float(o[at(e + 4)]) * inv, __uint_as_float(o[at(e + 5)]) * inv);
+                            x.w = pack16<BF16>(__uint_as_float(o[at(e + 6)]) * inv, __uint_as_float(o[at(e + 7)]) * inv);
                             *reinterpret_cast<uint4 *>(stage + lane * 64 + (((e / 8) ^ ((lane >> 1) & 3)) << 4)) = x;
                         }
                         __syncwarp();
@@ -1133,8 +1169,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
                             part[static_cast<size_t>((c + e) / 4) * ROWS] =
-                                make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
-                                            __uint_as_float(o[e + 3]));
+                                make_float4(__uint_as_float(o[at(e)]), __uint_as_float(o[at(e + 1)]), __uint_as_float(o[at(e + 2)]),
+                                            __uint_as_float(o[at(e + 3)]));
                     }
                     __syncwarp();
                 }
