@@ -202,6 +202,8 @@ class QuantPaged:
     def run(self, ta, **kw):
         a = dict(scale=self.scale, max_q_len=max(1, max(self.new)), parents=self.flat_parents())
         a.update(kw)
+        if a.get("out") is None:                # a row that is not written shows
+            a["out"] = torch.full_like(self.q, 77.0)
         return ta.paged_quant_attention(self.q, self.cache, self.table, i32(self.cu), i32(self.lens), **a)
 
     def check(self, got, window=0, only=None):

@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
         mbar_init(&mi->q_full, 1);
         mbar_init(&mi->guard, 2);
         if constexpr (QUANT)
-            for (int i = 0; i < 2 * QC::NR; ++i) { mbar_init(&qm->full[i], 33); mbar_init(&qm->empty[i], QC::PARTS); }
+            for (int i = 0; i < 2 * QC::NR; ++i) { mbar_init(&qm->full[i], 17); mbar_init(&qm->empty[i], QC::PARTS); }
         mbar_init(&mi->q_empty, NSTR);
         for (int i = 0; i < 2; ++i) {
             for (int j = 0; j < 2; ++j) {
@@ -561,66 +561,86 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
         walk.init(a, ar.tpt, run, &mi->sched, cta);
         int n = 0, kn = 0, qn = 0;                      // pieces, K tiles, Q tiles so far
         bool ok = true;
-        // 4-bit pages: K tiles that V is behind; V's tiles so far, its piece, how far that is, its number
+        // 4-bit pages: lanes 0 .. 15 bring K's tiles, lanes 16 .. 31 V's, four keys each, in one pass (one after the
+        // other took this warp 2400 cycles a tile, and everybody waited).  lead: K tiles that V is behind; V's tiles so
+        // far, its piece, how far that is, its number
+        const bool mine_v = lane >= 16;
         int lead = 0, vn = 0, vt = 0, vpn = -1;
-        SeqPiece kp, vp;
+        SeqPiece vp;
         vp.nt = 0;
-        int kpage[2], vpage[2];                         // pages of this lane's keys (lane, lane + 32) of K's and V's next tile
-        auto raw_pages = [&](const SeqPiece &p, int t, int (&page)[2]) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int key = (t << TKS) + 32 * i + lane;
-                page[i] = a.n_pages;                    // out of range: zeros
-                if (key >= p.kv) continue;
-                const int g = __ldg(a.table + static_cast<long long>(p.b) * a.max_pages + (key >> a.page_shift));
-                if (g >= 0 && g < a.n_pages) page[i] = g;
-                // a page before every row's window may be gone
-                else if (!(a.window && key < p.prefix + p.i0 - a.window + 1)) atomicOr(a.status, kSeqBadPage);
-            }
+        // of this lane's piece: table row, keys, first key not behind every row's window, KV head, affine; its next
+        // four keys and their page (n_pages: out of range, zeros)
+        const int32_t *row = a.table;
+        int r_kv = 0, r_lo = 0, r_kh = 0, r_key = 0, r_page = 0;
+        const uint32_t *r_src = static_cast<const uint32_t *>(mine_v ? ar.qc.va : ar.qc.ka);
+        auto raw_page = [&] {
+            r_page = a.n_pages;
+            if (r_key >= r_kv) return;
+            const int g = __ldg(row + (r_key >> a.page_shift));
+            if (g >= 0 && g < a.n_pages) r_page = g;
+            else if (r_key + 4 > r_lo) atomicOr(a.status, kSeqBadPage);     // (a page behind the window may be gone)
         };
-        // codes, scales and biases of tile t of K or V into the next raw stage
-        auto raw_job = [&](int kind, const SeqPiece &p, int t, bool more, int (&page)[2]) -> bool {
-            const int jn = kind ? vn : kn, st = kind * QC::NR + jn % QC::NR;
-            if (!warp_wait(&qm->empty[st], (static_cast<uint32_t>(jn / QC::NR) & 1u) ^ 1u)) return false;
-            unsigned char *raw = sm + QC::OFF_RAW + st * QC::RAW;
+        auto raw_piece = [&](const SeqPiece &p, bool v) {
+            if (mine_v != v) return;
+            row = a.table + static_cast<long long>(p.b) * a.max_pages;
+            r_kv = p.kv;
+            r_lo = a.window ? p.prefix + p.i0 - a.window + 1 : INT_MIN;
+            r_kh = p.kh;
+            r_key = (p.t0 << TKS) + 4 * (lane & 15);
+            raw_page();
+        };
+        // the next tile of K (where k_on; k_more: its piece has another) and of V (v_on)
+        auto raw_step = [&](bool k_on, bool k_more, bool v_on) -> bool {
+            bool v_more = false;
+            if (v_on) {
+                if (vt == vp.nt) {
+                    if (!fetch(&vp)) return false;
+                    vt = 0;
+                    ++vpn;
+                    raw_piece(vp, true);
+                }
+                v_more = vt + 1 < vp.nt;
+            }
+            const bool on = mine_v ? v_on : k_on;
+            const int jn = mine_v ? vn : kn, st = (mine_v ? QC::NR : 0) + jn % QC::NR;
             uint64_t *bar = &qm->full[st];
-            const int qk = min(TK, 1 << a.page_shift), boxes = TK / qk, key = t << TKS;     // keys a box
-            if (lane == 0) {
+            bool got = true;
+            if (on) got = wait_bar(&qm->empty[st], (static_cast<uint32_t>(jn / QC::NR) & 1u) ^ 1u, ar.polls);
+            if (!__all_sync(0xffffffffu, got)) return false;
+            if (on && (lane & 15) == 0) {
                 RawInfo &info = qm->info[st];
                 info.end = 0;
-                info.look = kind && is_masked(p, t);
-                info.n = vpn;
-                info.k0 = key;
-                if (info.look) info.p = p;
+                if (mine_v) {
+                    info.look = is_masked(vp, vp.t0 + vt);
+                    info.n = vpn;
+                    info.k0 = r_key;
+                    if (info.look) info.p = vp;
+                }
                 mbar_arrive_expect_tx(bar, QC::AFFINE);
             }
             __syncwarp();
-            // the page of box x is that of key qk x: lane (qk x) % 32 holds it
-            const int at = lane * qk, pg = __shfl_sync(0xffffffffu, page[0], at & 31), pg1 = __shfl_sync(0xffffffffu, page[1], at & 31);
-            if (lane < boxes)
-                tma_load_raw(raw + at * (D / 2), kind ? &maps.v : &maps.k, bar, (key + at) & ((1 << a.page_shift) - 1), p.kh, at < 32 ? pg : pg1);
-            const uint32_t *src = static_cast<const uint32_t *>(kind ? ar.qc.va : ar.qc.ka) + p.kh * ar.qc.a_sh;
+            if (on) {
+                unsigned char *raw = sm + QC::OFF_RAW + st * QC::RAW;
+                const int qk = min(TK, 1 << a.page_shift), at = 4 * (lane & 15), in = r_key & ((1 << a.page_shift) - 1);
+                if ((at & (qk - 1)) == 0) {             // one map an instruction
+                    if (mine_v) tma_load_raw(raw + at * (D / 2), &maps.v, bar, in, r_kh, r_page);
+                    else tma_load_raw(raw + at * (D / 2), &maps.k, bar, in, r_kh, r_page);
+                }
+                const bool live = r_page < a.n_pages;
+                const uint32_t *src = live ? r_src + r_kh * ar.qc.a_sh + r_page * ar.qc.a_sp + in * ar.qc.a_st : r_src;
+                const uint32_t dst = smem_u32(raw) + QC::AFFINE + at * (QC::NG * 4);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int k = 32 * i + lane, in = (key + k) & ((1 << a.page_shift) - 1);
-                const bool live = page[i] < a.n_pages;
-                copy_words<QC::NG>(smem_u32(raw) + QC::AFFINE + k * (QC::NG * 4), live ? src + page[i] * ar.qc.a_sp + in * ar.qc.a_st : src, live);
+                for (int i = 0; i < 4; ++i) {
+                    const bool l = live && r_key + i < r_kv;
+                    copy_words<QC::NG>(dst + i * (QC::NG * 4), l ? src + i * ar.qc.a_st : r_src, l);
+                }
+                arrive_after_copies(bar);
+                r_key += TK;
+                if (mine_v ? v_more : k_more) raw_page();
             }
-            arrive_after_copies(bar);
-            ++(kind ? vn : kn);
-            if (more) raw_pages(p, t + 1, page);
-            return true;
-        };
-        auto raw_v = [&]() -> bool {
-            if (vt == vp.nt) {
-                if (!fetch(&vp)) return false;
-                vt = 0;
-                ++vpn;
-                raw_pages(vp, vp.t0, vpage);
-            }
-            if (!raw_job(1, vp, vp.t0 + vt, vt + 1 < vp.nt, vpage)) return false;
-            ++vt;
-            --lead;
+            __syncwarp();
+            if (k_on) { ++kn; ++lead; }
+            if (v_on) { ++vn; ++vt; --lead; }
             return true;
         };
         if (lane == 0) ar.ws.rec[cta] = {0, 0, 0, 0};
@@ -665,13 +685,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
             };
             if constexpr (QUANT) {
                 if (n == 0) load_q();
-                kp = p;
-                raw_pages(kp, kp.t0, kpage);
+                raw_piece(p, false);
 #pragma unroll 1
-                for (int t = 0; t < kp.nt && ok; ++t) {
-                    ok = raw_job(0, kp, kp.t0 + t, t + 1 < kp.nt, kpage);
+                for (int t = 0; t < p.nt && ok; ++t) {
+                    ok = raw_step(true, t + 1 < p.nt, lead >= QC::kLead);
                     if (ok && t == 0 && n > 0) load_q();
-                    if (ok && ++lead > QC::kLead) ok = raw_v();
                 }
                 if (!ok) break;
                 continue;
@@ -701,7 +719,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
             if (!ok) break;
         }
         if constexpr (QUANT) {
-            while (ok && lead > 0) ok = raw_v();
+            while (ok && lead > 0) ok = raw_step(false, false, true);
             // the end, at each stage of K (D = 256: of K and of V)
 #pragma unroll 1
             for (int i = 0; ok && i < (QC::PARTS == 2 ? 2 : QC::NR); ++i) {
@@ -713,7 +731,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                     mbar_arrive(&qm->full[st]);
                 }
                 __syncwarp();
-                mbar_arrive(&qm->full[st]);
+                if (lane < 16) mbar_arrive(&qm->full[st]);
                 ++(kind ? vn : kn);
             }
             if (lane == 0)
