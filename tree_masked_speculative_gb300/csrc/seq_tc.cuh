@@ -399,9 +399,10 @@ __device__ __forceinline__ void shared_words(const unsigned char *p, uint32_t (&
 // row of memory), 8 neighbouring elements of each block, to 64-column slabs of 64 rows with the 128-byte swizzle.  Eight
 // lanes that work together take rows r and r ^ 5: their loads and their stores cover all banks once.  K's elements
 // are put in order, V's stay as 0, 4, 1, 5, 2, 6, 3, 7 of every eight (the epilogue names O's columns so).
-// acc: the largest magnitudes, where `look`.
+// acc: the largest magnitudes, where `look`.  `done`: a barrier to arrive on once the raw words are in registers.
 template <int D, int G, bool BF16, int U>
-__device__ __forceinline__ void widen_units(const unsigned char *raw, unsigned char *tile, int it, bool order, bool look, uint32_t (&acc)[4]) {
+__device__ __forceinline__ void widen_units(const unsigned char *raw, unsigned char *tile, int it, bool order, bool look, uint32_t (&acc)[4],
+                                            uint64_t *done) {
     using C = QuantCfg<D, G>;
     constexpr int NB = D / 32, NG = D / G;
     const int lane = threadIdx.x & 31, t = lane & 3, r = (lane >> 3) ^ ((lane & 4) ? 5 : 0), row = 8 * it + r;
@@ -410,6 +411,10 @@ __device__ __forceinline__ void widen_units(const unsigned char *raw, unsigned c
     for (int u = 0; u < U; ++u) {
         shared_words<NB>(raw + (row + 8 * u) * (D / 2) + t * (NB * 4), w[u]);
         shared_words<NG>(raw + C::AFFINE + (row + 8 * u) * (NG * 4), sb[u]);
+    }
+    if (done) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(done);
     }
     unsigned char *dst = tile + row * 128 + ((t ^ r) << 4);
     const int odd = (r & 4) ? -64 : 64;                 // from an even block's place to the odd one's
@@ -555,7 +560,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
     // D <= 128: 4 x 128 registers a thread at launch = 2 x 88 + 2 x 168.
     if (warp < C::SW) {
     if constexpr (NSTR == 2) regs_down<88>();
-    if (warp == 0) {
+    // 4-bit pages: the same roles, one widening warp a quarter of the SM (warps w and w + 4 share its issue slots and ALUs;
+    // as warps 3, 6 and 7 two of them shared one)
+    const int role = !QUANT ? warp : ((NSTR == 2 ? 0x54217630 : 0x75214630) >> (4 * warp)) & 7;
+    if (role == 0) {
         // ------------------------------------------------- schedule, TMA producer
         SeqWalk<TKS, kUnitCost> walk;
         walk.init(a, ar.tpt, run, &mi->sched, cta);
@@ -569,17 +577,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
         SeqPiece vp;
         vp.nt = 0;
         // of this lane's piece: table row, keys, first key not behind every row's window, KV head, affine; its next
-        // four keys and their page (n_pages: out of range, zeros)
+        // four keys and the cells of their page and of that of the four a tile on
         const int32_t *row = a.table;
-        int r_kv = 0, r_lo = 0, r_kh = 0, r_key = 0, r_page = 0;
+        int r_kv = 0, r_lo = 0, r_kh = 0, r_key = 0, r_cell[2] = {};
         const uint32_t *r_src = static_cast<const uint32_t *>(mine_v ? ar.qc.va : ar.qc.ka);
-        auto raw_page = [&] {
-            r_page = a.n_pages;
-            if (r_key >= r_kv) return;
-            const int g = __ldg(row + (r_key >> a.page_shift));
-            if (g >= 0 && g < a.n_pages) r_page = g;
-            else if (r_key + 4 > r_lo) atomicOr(a.status, kSeqBadPage);     // (a page behind the window may be gone)
-        };
+        auto raw_cell = [&](int key) { return key < r_kv ? __ldg(row + (key >> a.page_shift)) : 0; };
         auto raw_piece = [&](const SeqPiece &p, bool v) {
             if (mine_v != v) return;
             row = a.table + static_cast<long long>(p.b) * a.max_pages;
@@ -587,19 +589,16 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
             r_lo = a.window ? p.prefix + p.i0 - a.window + 1 : INT_MIN;
             r_kh = p.kh;
             r_key = (p.t0 << TKS) + 4 * (lane & 15);
-            raw_page();
+            r_cell[0] = raw_cell(r_key);
+            r_cell[1] = raw_cell(r_key + TK);
         };
-        // the next tile of K (where k_on; k_more: its piece has another) and of V (v_on)
-        auto raw_step = [&](bool k_on, bool k_more, bool v_on) -> bool {
-            bool v_more = false;
-            if (v_on) {
-                if (vt == vp.nt) {
-                    if (!fetch(&vp)) return false;
-                    vt = 0;
-                    ++vpn;
-                    raw_piece(vp, true);
-                }
-                v_more = vt + 1 < vp.nt;
+        // the next tile of K (where k_on) and of V (v_on)
+        auto raw_step = [&](bool k_on, bool v_on) -> bool {
+            if (v_on && vt == vp.nt) {
+                if (!fetch(&vp)) return false;
+                vt = 0;
+                ++vpn;
+                raw_piece(vp, true);
             }
             const bool on = mine_v ? v_on : k_on;
             const int jn = mine_v ? vn : kn, st = (mine_v ? QC::NR : 0) + jn % QC::NR;
@@ -622,12 +621,15 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
             if (on) {
                 unsigned char *raw = sm + QC::OFF_RAW + st * QC::RAW;
                 const int qk = min(TK, 1 << a.page_shift), at = 4 * (lane & 15), in = r_key & ((1 << a.page_shift) - 1);
+                // n_pages: out of range, zeros
+                const bool live = r_key < r_kv && r_cell[0] >= 0 && r_cell[0] < a.n_pages;
+                const int page = live ? r_cell[0] : a.n_pages;
+                if (!live && r_key < r_kv && r_key + 4 > r_lo) atomicOr(a.status, kSeqBadPage);   // (behind the window it may be gone)
                 if ((at & (qk - 1)) == 0) {             // one map an instruction
-                    if (mine_v) tma_load_raw(raw + at * (D / 2), &maps.v, bar, in, r_kh, r_page);
-                    else tma_load_raw(raw + at * (D / 2), &maps.k, bar, in, r_kh, r_page);
+                    if (mine_v) tma_load_raw(raw + at * (D / 2), &maps.v, bar, in, r_kh, page);
+                    else tma_load_raw(raw + at * (D / 2), &maps.k, bar, in, r_kh, page);
                 }
-                const bool live = r_page < a.n_pages;
-                const uint32_t *src = live ? r_src + r_kh * ar.qc.a_sh + r_page * ar.qc.a_sp + in * ar.qc.a_st : r_src;
+                const uint32_t *src = live ? r_src + r_kh * ar.qc.a_sh + page * ar.qc.a_sp + in * ar.qc.a_st : r_src;
                 const uint32_t dst = smem_u32(raw) + QC::AFFINE + at * (QC::NG * 4);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -636,7 +638,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                 }
                 arrive_after_copies(bar);
                 r_key += TK;
-                if (mine_v ? v_more : k_more) raw_page();
+                r_cell[0] = r_cell[1];
+                r_cell[1] = raw_cell(r_key + TK);       // (past the piece's last tile it is not used)
             }
             __syncwarp();
             if (k_on) { ++kn; ++lead; }
@@ -688,7 +691,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                 raw_piece(p, false);
 #pragma unroll 1
                 for (int t = 0; t < p.nt && ok; ++t) {
-                    ok = raw_step(true, t + 1 < p.nt, lead >= QC::kLead);
+                    ok = raw_step(true, lead >= QC::kLead);
                     if (ok && t == 0 && n > 0) load_q();
                 }
                 if (!ok) break;
@@ -719,7 +722,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
             if (!ok) break;
         }
         if constexpr (QUANT) {
-            while (ok && lead > 0) ok = raw_step(false, false, true);
+            while (ok && lead > 0) ok = raw_step(false, true);
             // the end, at each stage of K (D = 256: of K and of V)
 #pragma unroll 1
             for (int i = 0; ok && i < (QC::PARTS == 2 ? 2 : QC::NR); ++i) {
@@ -751,13 +754,13 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                 if (!mbar_wait_sleep(&mi->k_full[i % NK], static_cast<uint32_t>(i / NK) & 1u, 1u << 21, 1000))
                     atomicOr(a.status, kSeqTimeout);
         }
-    } else if (QUANT && (warp == 3 || warp >= 6 || (NSTR == 1 && warp == 4))) {
+    } else if (QUANT && (role == 3 || role >= 6 || (NSTR == 1 && role == 4))) {
         // -------------------------------------------------- 4-bit pages: widening, V guarded
         if constexpr (QUANT) {
-            constexpr int PARTS = QC::PARTS, ITS = 8 / PARTS, U = D == 256 ? 1 : 2;
-            const int part = PARTS == 2 ? (warp == 4 || warp == 7) : 0;
-            int kind = PARTS == 2 && warp >= 6;         // 0: K, 1: V
-            int j = PARTS == 2 ? 0 : warp == 3 ? 0 : warp - 5;   // tile
+            constexpr int PARTS = QC::PARTS, ITS = 8 / PARTS, U = 2;
+            const int part = PARTS == 2 ? (role == 4 || role == 7) : 0;
+            int kind = PARTS == 2 && role >= 6;         // 0: K, 1: V
+            int j = PARTS == 2 || role == 3 ? 0 : role - 5;   // tile
             bool ok = true;
 #pragma unroll 1
             for (;;) {
@@ -773,7 +776,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                 uint32_t acc[4] = {};
 #pragma unroll 1
                 for (int it = ITS * part; it < ITS * (part + 1); it += U)
-                    widen_units<D, G, BF16, U>(sm + QC::OFF_RAW + rs * QC::RAW, tile, it, kind == 0, look, acc);
+                    widen_units<D, G, BF16, U>(sm + QC::OFF_RAW + rs * QC::RAW, tile, it, kind == 0, look, acc,
+                                               it + U == ITS * (part + 1) && !look ? &qm->empty[rs] : nullptr);
                 if (look) {
                     // an element that is not finite must not reach rows that do not see it (0 x NaN): it is taken out,
                     // and the rows that see it are marked
@@ -789,7 +793,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(kind ? &mi->v_ready[st] : &mi->k_full[st]);
-                    mbar_arrive(&qm->empty[rs]);
+                    if (look) mbar_arrive(&qm->empty[rs]);    // (not before the marks: they want the piece)
                 }
                 if (PARTS == 2) {
                     ++j;
@@ -800,7 +804,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
             }
             failed |= !ok;
         }
-    } else if (warp == 6) {
+    } else if (role == 6) {
         // ------------------------------------------------------------- V producer
         int vn = 0;
         bool ok = true;
@@ -831,9 +835,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
             for (int i = max(0, vn - NV); i < vn; ++i)
                 if (!mbar_wait_sleep(&mi->v_full[i % NV], static_cast<uint32_t>(i / NV) & 1u, 1u << 21, 1000))
                     atomicOr(a.status, kSeqTimeout);
-    } else if (warp == 1 || warp == 2 || (NSTR == 2 && (warp == 4 || warp == 5))) {
+    } else if (role == 1 || role == 2 || (NSTR == 2 && (role == 4 || role == 5))) {
         // ------------------------------------------------------------ MMA issuers
-        const int x = warp >> 2, w = warp - (x ? 4 : 1);   // stream; 0: Q K^T, 1: P V
+        const int x = role >> 2, w = role - (x ? 4 : 1);   // stream; 0: Q K^T, 1: P V
         const uint32_t q_addr = smem_u32(sm + C::OFF_Q), k_addr = smem_u32(sm + C::OFF_K), v_addr = smem_u32(sm + C::OFF_V);
         constexpr uint32_t id_qk = idesc_f16(128, TK, BF16 ? 1 : 0, 0, 0);
         constexpr uint32_t id_pv = idesc_f16(128, D, BF16 ? 1 : 0, 0, 1);
@@ -921,7 +925,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
             if (!mbar_wait_sleep(&mi->drain[2 * x + w], 0, 1u << 21, 1000)) atomicOr(a.status, kSeqTimeout);
         }
         __syncwarp();
-    } else if (warp == 3 || warp == 7) {
+    } else if (role == 3 || role == 7) {
         // --------------------------------------------------------------- V guards
         // Two warps, every other 4 rows each; warp 3 does the marking.
         const int part = warp >> 2;
