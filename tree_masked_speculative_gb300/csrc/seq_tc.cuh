@@ -301,20 +301,24 @@ __device__ __forceinline__ uint32_t max_abs(uint32_t acc, uint32_t w) {
 
 // ---- 4-bit pages.  Warp 0 brings codes (TMA) and scales and biases (cp.async) of K and V tiles to raw stages, K
 // two tiles ahead of V's; widening warps turn them into tiles of 16-bit values and guard V's as they go.  For D <= 128
-// warps 3, 6 and 7 take every third tile of K and of V whole, K and V in turn; for D = 256 warps 3 and 4 take
-// a half each of every K tile, 6 and 7 of every V tile.  A stage and a slot of the rings belong to the same warps
-// always (3 of each, or all of them), who so see each of a barrier's phases: a wait tells phases apart by parity alone.
-// (A third of every tile each, all waiting for the same barriers: 524 us for the chunks of twelve requests.)  One
-// rolled loop serves K and V and holds little code: with loops of their own, unrolled, the instruction cache missed
-// and they took 1046 us.
+// three warps take every third K tile each, three others every third V tile; for D = 256 four share every K
+// tile, four every V tile.  A stage and a slot of the rings belong to the same warps always, who so see each of a
+// barrier's phases: a wait tells phases apart by parity alone.  The chunks of twelve requests took 524 us with a third
+// of every tile by each of three warps, all waiting for the same barriers, 391 us with K and V in turn by three warps, one a tile.
+// One rolled loop serves K and V and holds little code: with loops of their own, unrolled, the instruction cache
+// missed and they took 1046 us.
 template <int D, int G>
 struct QuantCfg : Cfg<D> {
     using B = Cfg<D>;
     static constexpr int NG = D / G;
-    static constexpr int PARTS = D == 256 ? 2 : 1;                     // warps that share a tile
+    static constexpr int PARTS = D == 256 ? 4 : 1;                     // warps that share a tile
     static constexpr int NK = D == 256 ? 2 : 3, NV = NK;
     static constexpr int NR = D == 256 ? 1 : 3;                        // raw stages of K, and of V
-    static_assert(PARTS == 2 || (NK == 3 && NR == 3), "a slot and a stage belong to one warp");
+    static_assert(PARTS == 4 || (NK == 3 && NR == 3), "a slot and a stage belong to one warp");
+    static constexpr int THREADS = B::THREADS + 128;                   // V's widening warps behind the softmax warps
+    // registers a thread: (4 or 5) x (128 or 96) at launch
+    static constexpr int DOWN = D == 256 ? 112 : 72, UP = D == 256 ? 168 : 128;
+    static_assert(D == 256 ? 3 * DOWN + UP <= 4 * 128 : 3 * DOWN + 2 * UP <= 5 * 96, "registers");
     static constexpr int AFFINE = B::TK * (D / 2), RAW = AFFINE + B::TK * NG * 4;
     static constexpr int OFF_K = B::OFF_K, OFF_V = OFF_K + NK * B::STAGE;
     static constexpr int OFF_OUT = OFF_V + NV * B::STAGE, OFF_RAW = OFF_OUT + B::NSTR * 8192;
@@ -452,11 +456,14 @@ __device__ __forceinline__ void widen_units(const unsigned char *raw, unsigned c
         }
 }
 
+template <int D, int SRC, int G>
+using CfgOf = std::conditional_t<SRC == kQuant, QuantCfg<D, G>, Cfg<D>>;
+
 template <int D, int SRC, bool BF16, int G = 32>
-__global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args ar, const __grid_constant__ Maps maps) {
+__global__ void __launch_bounds__((CfgOf<D, SRC, G>::THREADS), 1) seq_tc_kernel(const Args ar, const __grid_constant__ Maps maps) {
     constexpr bool PAGED = SRC == kPages, QUANT = SRC == kQuant;
     using QC = QuantCfg<D, G>;
-    using C = std::conditional_t<QUANT, QC, Cfg<D>>;
+    using C = CfgOf<D, SRC, G>;
     constexpr int TK = C::TK, TKS = C::TKS, NSTR = C::NSTR, NK = C::NK, NV = C::NV, NS = C::NS, NP = C::NP, ROWS = C::ROWS;
     extern __shared__ __align__(1024) unsigned char sm[];
     const SeqArgs &a = ar.a;
@@ -558,11 +565,14 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
     auto is_masked = [&](const SeqPiece &p, int t) { return (t << TKS) < p.full_lo || ((t + 1) << TKS) > p.full_hi; };
 
     // D <= 128: 4 x 128 registers a thread at launch = 2 x 88 + 2 x 168.
-    if (warp < C::SW) {
-    if constexpr (NSTR == 2) regs_down<88>();
-    // 4-bit pages: the same roles, one widening warp a quarter of the SM (warps w and w + 4 share its issue slots and ALUs;
-    // as warps 3, 6 and 7 two of them shared one)
-    const int role = !QUANT ? warp : ((NSTR == 2 ? 0x54217630 : 0x75214630) >> (4 * warp)) & 7;
+    constexpr int kBehind = C::SW + 4 * NSTR;           // the first warp behind the softmax warps
+    if (warp < C::SW || warp >= kBehind) {
+    if constexpr (QUANT) regs_down<QC::DOWN>();
+    else if constexpr (NSTR == 2) regs_down<88>();
+    // 4-bit pages: warps 1, 2, 3 (D = 256: and 7) widen K, those behind the softmax warps V; the issuers are warps 4 and up.
+    // Warps w and w + 4 share a quarter of the SM, its issue slots and ALUs.
+    const int role = !QUANT ? warp : warp >= kBehind ? (NSTR == 2 && warp == kBehind + 3 ? 8 : 6)
+                                                     : ((NSTR == 2 ? 0x54213330 : 0x38213330) >> (4 * warp)) & 15;
     if (role == 0) {
         // ------------------------------------------------- schedule, TMA producer
         SeqWalk<TKS, kUnitCost> walk;
@@ -723,10 +733,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
         }
         if constexpr (QUANT) {
             while (ok && lead > 0) ok = raw_step(false, true);
-            // the end, at each stage of K (D = 256: of K and of V)
+            // the end, at each stage
 #pragma unroll 1
-            for (int i = 0; ok && i < (QC::PARTS == 2 ? 2 : QC::NR); ++i) {
-                const int kind = QC::PARTS == 2 ? i : 0, jn = kind ? vn : kn, st = kind * QC::NR + jn % QC::NR;
+            for (int i = 0; ok && i < 2 * QC::NR; ++i) {
+                const int kind = i >= QC::NR, jn = kind ? vn : kn, st = kind * QC::NR + jn % QC::NR;
                 ok = warp_wait(&qm->empty[st], (static_cast<uint32_t>(jn / QC::NR) & 1u) ^ 1u);
                 if (!ok) break;
                 if (lane == 0) {
@@ -754,13 +764,13 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                 if (!mbar_wait_sleep(&mi->k_full[i % NK], static_cast<uint32_t>(i / NK) & 1u, 1u << 21, 1000))
                     atomicOr(a.status, kSeqTimeout);
         }
-    } else if (QUANT && (role == 3 || role >= 6 || (NSTR == 1 && role == 4))) {
+    } else if (QUANT && (role == 3 || role == 6)) {
         // -------------------------------------------------- 4-bit pages: widening, V guarded
         if constexpr (QUANT) {
             constexpr int PARTS = QC::PARTS, ITS = 8 / PARTS, U = 2;
-            const int part = PARTS == 2 ? (role == 4 || role == 7) : 0;
-            int kind = PARTS == 2 && role >= 6;         // 0: K, 1: V
-            int j = PARTS == 2 || role == 3 ? 0 : role - 5;   // tile
+            const int kind = role == 6, me = kind ? warp - kBehind : warp == 7 ? 3 : warp - 1;   // kind 0: K, 1: V
+            const int part = PARTS == 1 ? 0 : me;
+            int j = PARTS == 1 ? me : 0;                // tile
             bool ok = true;
 #pragma unroll 1
             for (;;) {
@@ -795,12 +805,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
                     mbar_arrive(kind ? &mi->v_ready[st] : &mi->k_full[st]);
                     if (look) mbar_arrive(&qm->empty[rs]);    // (not before the marks: they want the piece)
                 }
-                if (PARTS == 2) {
-                    ++j;
-                } else {
-                    j += 3 * kind;
-                    kind ^= 1;
-                }
+                j += PARTS == 1 ? 3 : 1;
             }
             failed |= !ok;
         }
@@ -1004,7 +1009,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) seq_tc_kernel(const Args a
     }
     } else {
         // ---------------------------------------------------- softmax and epilogue
-        if constexpr (NSTR == 2) regs_up<168>();
+        if constexpr (QUANT) regs_up<QC::UP>();
+        else if constexpr (NSTR == 2) regs_up<168>();
         const int s = (warp - C::SW) >> 2;
         const int quarter = warp & 3;
         const int r = quarter * 32 + lane;              // row within the stream
@@ -1266,7 +1272,7 @@ cudaError_t launch(const Args &ar, const Maps &maps, cudaStream_t s) {
     constexpr int smem = SRC == kQuant ? kQuantSmem<D, G> : kSmem<D>;
     cudaError_t e = set_smem_limit_once(kern, smem, &done);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(kern, dim3(ar.G), dim3(Cfg<D>::THREADS), smem, s, ar, maps);
+    e = launch_pdl(kern, dim3(ar.G), dim3(CfgOf<D, SRC, G>::THREADS), smem, s, ar, maps);
     count_launch();
     if (e != cudaSuccess) return e;
     e = launch_pdl(seq_merge_kernel<D, BF16>, dim3(ar.G, D / 16), dim3(Cfg<D>::ROWS), 0, s, ar.a, ar.ws);
