@@ -69,7 +69,7 @@ cudaError_t launch_seq_quant_mma64(const SeqQuantArgs &a, void *ws, int sms, cud
 cudaError_t launch_seq_quant_mma128(const SeqQuantArgs &a, void *ws, int sms, cudaStream_t s);
 cudaError_t launch_seq_quant_mma256(const SeqQuantArgs &a, void *ws, int sms, cudaStream_t s);
 
-// Tensor-core kernel; the plan's maps of K and V are those of their codes.
+// Tensor-core kernel (the plan's maps of K and V are not used).
 cudaError_t launch_seq_quant_tc64(const SeqQuantArgs &a, const SeqTcPlan &pl, cudaStream_t s);
 cudaError_t launch_seq_quant_tc128(const SeqQuantArgs &a, const SeqTcPlan &pl, cudaStream_t s);
 cudaError_t launch_seq_quant_tc256(const SeqQuantArgs &a, const SeqTcPlan &pl, cudaStream_t s);

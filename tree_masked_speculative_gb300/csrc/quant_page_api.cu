@@ -163,17 +163,6 @@ uint64_t quant_workspace(const ta_paged_quant_params *p) {
                              : p->head_dim == 128 ? seq_quant_mma_workspace128(rows, sms) : seq_quant_mma_workspace256(rows, sms);
 }
 
-// Tensor map of K's or V's codes: {D / 8 words, page_size, Hk, n_pages}, boxes of a key tile's rows in a page.
-bool codes_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap *m, const SeqQuantArgs &a, const uint32_t *ptr) {
-    const cuuint64_t ps = cuuint64_t(1) << a.s.page_shift;
-    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.s.D / 8), ps, static_cast<cuuint64_t>(a.s.Hk), static_cast<cuuint64_t>(a.s.n_pages)};
-    const cuuint64_t str[3] = {static_cast<cuuint64_t>(a.c.c_st) * 4, static_cast<cuuint64_t>(a.c.c_sh) * 4, static_cast<cuuint64_t>(a.c.c_sp) * 4};
-    const cuuint32_t box[4] = {static_cast<cuuint32_t>(a.s.D / 8), ps < kSeqTcTileKeys ? static_cast<cuuint32_t>(ps) : kSeqTcTileKeys, 1, 1};
-    const cuuint32_t es[4] = {1, 1, 1, 1};
-    return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, const_cast<uint32_t *>(ptr), dims, str, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 ta_status run_quant(const char *op, const SeqQuantArgs &a, int family, void *ws, cudaStream_t s, uint32_t polls) {
     const int sms = device_sm_count();
     cudaError_t e;
@@ -189,8 +178,7 @@ ta_status run_quant(const char *op, const SeqQuantArgs &a, int family, void *ws,
         pl.ws = ws;
         const auto encode = tensor_map_encoder();
         if (encode == nullptr) SEQ_FAIL(TA_ERR_CUDA, "%s: cuTensorMapEncodeTiled is not available", op);
-        if (!q_map(encode, &pl.q, a.s) || !codes_map(encode, &pl.k, a, a.c.kc) || !codes_map(encode, &pl.v, a, a.c.vc))
-            SEQ_FAIL(TA_ERR_CUDA, "%s: TMA descriptor encoding failed", op);
+        if (!q_map(encode, &pl.q, a.s)) SEQ_FAIL(TA_ERR_CUDA, "%s: TMA descriptor encoding failed", op);
         e = a.s.D == 64 ? launch_seq_quant_tc64(a, pl, s) : a.s.D == 128 ? launch_seq_quant_tc128(a, pl, s) : launch_seq_quant_tc256(a, pl, s);
     }
     if (e != cudaSuccess) SEQ_FAIL(TA_ERR_CUDA, "%s: launch: %s", op, cudaGetErrorString(e));

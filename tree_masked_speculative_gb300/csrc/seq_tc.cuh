@@ -299,50 +299,40 @@ __device__ __forceinline__ uint32_t max_abs(uint32_t acc, uint32_t w) {
     return r;
 }
 
-// ---- 4-bit pages.  Warp 0 brings codes (TMA) and scales and biases (cp.async) of K and V tiles to raw stages, K
-// two tiles ahead of V's; widening warps turn them into tiles of 16-bit values and guard V's as they go.  For D <= 128
-// three warps take every third K tile each, three others every third V tile; for D = 256 four share every K
-// tile, four every V tile.  A stage and a slot of the rings belong to the same warps always, who so see each of a
-// barrier's phases: a wait tells phases apart by parity alone.  The chunks of twelve requests took 524 us with a third
-// of every tile by each of three warps, all waiting for the same barriers, 391 us with K and V in turn by three warps, one a tile.
-// One rolled loop serves K and V and holds little code: with loops of their own, unrolled, the instruction cache
-// missed and they took 1046 us.
+// ---- 4-bit pages.  Widening warps bring codes, scales and biases of their keys to shared memory (cp.async, one
+// tile of theirs ahead, 16 keys at a time), turn them into tiles of 16-bit values and guard V's as they go.  For
+// D <= 128 three warps take every third K tile each, three others every third V tile; for D = 256 four share
+// every K tile, four every V tile, 16 keys each.  A slot of the rings belongs to the same warps always, who so see
+// each of a barrier's phases: a wait tells phases apart by parity alone.
+// Chunks of twelve requests (us): 524 with a third of every tile by each of three warps, 391 with tiles in turn, 344 with six
+// warps, all fed by warp 0 (TMA), which needed 2100 cycles a tile.  One rolled loop serves K and V and holds little code: with
+// loops of their own, unrolled, the instruction cache missed and they took 1046.
 template <int D, int G>
 struct QuantCfg : Cfg<D> {
     using B = Cfg<D>;
     static constexpr int NG = D / G;
     static constexpr int PARTS = D == 256 ? 4 : 1;                     // warps that share a tile
+    static constexpr int WARPS = D == 256 ? 4 : 3;                     // widening warps of K, and of V
+    static constexpr int STEP = PARTS == 1 ? WARPS : 1;                // from a warp's tile to its next
+    static constexpr int ROUNDS = 4 / PARTS;                           // 16 keys each
     static constexpr int NK = D == 256 ? 2 : 3, NV = NK;
-    static constexpr int NR = D == 256 ? 1 : 3;                        // raw stages of K, and of V
-    static_assert(PARTS == 4 || (NK == 3 && NR == 3), "a slot and a stage belong to one warp");
+    static_assert(PARTS == WARPS || NK == WARPS, "a slot belongs to one warp");
     static constexpr int THREADS = B::THREADS + 128;                   // V's widening warps behind the softmax warps
     // registers a thread: (4 or 5) x (128 or 96) at launch
     static constexpr int DOWN = D == 256 ? 112 : 72, UP = D == 256 ? 168 : 128;
     static_assert(D == 256 ? 3 * DOWN + UP <= 4 * 128 : 3 * DOWN + 2 * UP <= 5 * 96, "registers");
-    static constexpr int AFFINE = B::TK * (D / 2), RAW = AFFINE + B::TK * NG * 4;
+    static constexpr int CODES = 16 * (D / 2), RAW = CODES + 16 * NG * 4;   // a round's bytes
     static constexpr int OFF_K = B::OFF_K, OFF_V = OFF_K + NK * B::STAGE;
     static constexpr int OFF_OUT = OFF_V + NV * B::STAGE, OFF_RAW = OFF_OUT + B::NSTR * 8192;
-    static constexpr int OFF_MISC = OFF_RAW + 2 * NR * RAW;
-    static constexpr int kLead = 2;                                    // K tiles ahead of V's
-};
-struct RawInfo {
-    int end;              // no more tiles
-    int look, n, k0;      // V: some row does not see all of it; its piece's number, its first key
-    SeqPiece p;           // V, where look
+    static constexpr int OFF_MISC = OFF_RAW + 2 * WARPS * ROUNDS * RAW;
 };
 struct QuantMisc {
-    uint64_t full[6], empty[6];   // of K's raw stages, then V's
-    RawInfo info[6];
+    SeqPiece own[8][2];   // of each widening warp: the pieces of its tile and of its next
 };
-constexpr int kQuantMiscBytes = 800;
-static_assert(sizeof(QuantMisc) <= kQuantMiscBytes, "barrier area");
-
 template <int D, int G>
-constexpr int kQuantSmem = QuantCfg<D, G>::OFF_MISC + kMiscBytes + kQuantMiscBytes;
+constexpr int kQuantSmem = QuantCfg<D, G>::OFF_MISC + kMiscBytes + static_cast<int>(sizeof(QuantMisc));
 static_assert(kQuantSmem<64, 32> <= 232448 && kQuantSmem<128, 32> <= 232448 && kQuantSmem<256, 32> <= 232448, "shared memory budget");
-__device__ __forceinline__ void tma_load_raw(void *dst, const CUtensorMap *map, uint64_t *bar, int token, int kh, int page) {
-    tma_load_4d(dst, map, bar, 0, token, kh, page);
-}
+
 // N 4-byte words to shared memory, zeros where `live` is false.
 template <int N>
 __device__ __forceinline__ void copy_words(uint32_t dst, const uint32_t *src, bool live) {
@@ -353,10 +343,6 @@ __device__ __forceinline__ void copy_words(uint32_t dst, const uint32_t *src, bo
     } else {
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(4 * N), "r"(live ? 4 * N : 0) : "memory");
     }
-}
-// The barrier gets this thread's arrival once its copies so far are done.
-__device__ __forceinline__ void arrive_after_copies(uint64_t *bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 template <bool BF16>
@@ -399,28 +385,25 @@ __device__ __forceinline__ void shared_words(const unsigned char *p, uint32_t (&
         }
     }
 }
-// 32 U units of a tile, U a lane: a unit is a key's quads 2 t and 2 t + 1 of every 32-element block (D / 32 words in a
+// A round: 16 keys, two units a lane.  A unit is a key's quads 2 t and 2 t + 1 of every 32-element block (D / 32 words in a
 // row of memory), 8 neighbouring elements of each block, to 64-column slabs of 64 rows with the 128-byte swizzle.  Eight
-// lanes that work together take rows r and r ^ 5: their loads and their stores cover all banks once.  K's elements
-// are put in order, V's stay as 0, 4, 1, 5, 2, 6, 3, 7 of every eight (the epilogue names O's columns so).
-// acc: the largest magnitudes, where `look`.  `done`: a barrier to arrive on once the raw words are in registers.
-template <int D, int G, bool BF16, int U>
-__device__ __forceinline__ void widen_units(const unsigned char *raw, unsigned char *tile, int it, bool order, bool look, uint32_t (&acc)[4],
-                                            uint64_t *done) {
+// lanes that work together take rows r and r ^ 5: their stores cover all banks once.  K's elements are put in order,
+// V's stay as 0, 4, 1, 5, 2, 6, 3, 7 of every eight (the epilogue names O's columns so).  `behind` runs once the raw words are
+// in registers.  acc: the largest magnitudes, where `look`.
+template <int D, int G, bool BF16, typename Behind>
+__device__ __forceinline__ void widen_round(const unsigned char *raw, unsigned char *tile, bool order, bool look, uint32_t (&acc)[4], Behind &&behind) {
     using C = QuantCfg<D, G>;
-    constexpr int NB = D / 32, NG = D / G;
-    const int lane = threadIdx.x & 31, t = lane & 3, r = (lane >> 3) ^ ((lane & 4) ? 5 : 0), row = 8 * it + r;
+    constexpr int NB = D / 32, NG = D / G, U = 2;
+    const int lane = threadIdx.x & 31, t = lane & 3, r = (lane >> 3) ^ ((lane & 4) ? 5 : 0);
     uint32_t w[U][NB], sb[U][NG];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        shared_words<NB>(raw + (row + 8 * u) * (D / 2) + t * (NB * 4), w[u]);
-        shared_words<NG>(raw + C::AFFINE + (row + 8 * u) * (NG * 4), sb[u]);
+        shared_words<NB>(raw + (r + 8 * u) * (D / 2) + t * (NB * 4), w[u]);
+        shared_words<NG>(raw + C::CODES + (r + 8 * u) * (NG * 4), sb[u]);
     }
-    if (done) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(done);
-    }
-    unsigned char *dst = tile + row * 128 + ((t ^ r) << 4);
+    __syncwarp();
+    behind();
+    unsigned char *dst = tile + r * 128 + ((t ^ r) << 4);
     const int odd = (r & 4) ? -64 : 64;                 // from an even block's place to the odd one's
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -478,8 +461,8 @@ __global__ void __launch_bounds__((CfgOf<D, SRC, G>::THREADS), 1) seq_tc_kernel(
     Misc *mi = reinterpret_cast<Misc *>(sm + C::OFF_MISC);
     QuantMisc *qm = reinterpret_cast<QuantMisc *>(sm + C::OFF_MISC + kMiscBytes);     // 4-bit pages only
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
-    // arrivals on a piece's empty slot: issuers, guards, V producer, softmax warps
-    constexpr int kReaders = 2 * NSTR + (QUANT ? 0 : 2) + 1 + 4 * NSTR;
+    // arrivals on a piece's empty slot: issuers, guards and V producer (or widening warps and Q's producer), softmax warps
+    constexpr int kReaders = 2 * NSTR + (QUANT ? 2 * QC::WARPS + 1 : 3) + 4 * NSTR;
     if (tid == 0) {
         for (int i = 0; i < NK; ++i) { mbar_init(&mi->k_full[i], QUANT ? QC::PARTS : 1); mbar_init(&mi->k_empty[i], NSTR); }
         for (int i = 0; i < NV; ++i) {
@@ -489,8 +472,6 @@ __global__ void __launch_bounds__((CfgOf<D, SRC, G>::THREADS), 1) seq_tc_kernel(
         }
         mbar_init(&mi->q_full, 1);
         mbar_init(&mi->guard, 2);
-        if constexpr (QUANT)
-            for (int i = 0; i < 2 * QC::NR; ++i) { mbar_init(&qm->full[i], 17); mbar_init(&qm->empty[i], QC::PARTS); }
         mbar_init(&mi->q_empty, NSTR);
         for (int i = 0; i < 2; ++i) {
             for (int j = 0; j < 2; ++j) {
@@ -513,8 +494,10 @@ __global__ void __launch_bounds__((CfgOf<D, SRC, G>::THREADS), 1) seq_tc_kernel(
     }
     if (warp == 0 && lane == 0) {
         tma_prefetch_desc(&maps.q);
-        tma_prefetch_desc(&maps.k);
-        tma_prefetch_desc(&maps.v);
+        if constexpr (!QUANT) {
+            tma_prefetch_desc(&maps.k);
+            tma_prefetch_desc(&maps.v);
+        }
     }
     pdl_wait();
     const SeqRun run = seq_schedule<C::THREADS, TKS, kUnitCost, 1>(a, ar.tpt, cta, ar.G, &mi->sched);
@@ -527,7 +510,6 @@ __global__ void __launch_bounds__((CfgOf<D, SRC, G>::THREADS), 1) seq_tc_kernel(
 
     // Boxes of bk keys; of a part tile K's are 64 columns wide: lanes 0 .. k_boxes - 1 issue
     // one each (V: lanes 0 .. per_slab - 1).
-    // (4-bit pages: boxes of raw rows; their tiles are whole.)
     const int bk = PAGED ? min(TK, 1 << a.page_shift) : TK, per_slab = TK / bk;          // 1, 2 or 4 boxes
     const int box = lane & (per_slab - 1), slab = bk == TK ? 0 : lane / per_slab, k_boxes = bk == TK ? 1 : per_slab * C::SLABS;
     // page of this lane's box of key tile t (n_pages: out of range, read as zeros)
@@ -569,8 +551,8 @@ __global__ void __launch_bounds__((CfgOf<D, SRC, G>::THREADS), 1) seq_tc_kernel(
     if (warp < C::SW || warp >= kBehind) {
     if constexpr (QUANT) regs_down<QC::DOWN>();
     else if constexpr (NSTR == 2) regs_down<88>();
-    // 4-bit pages: warps 1, 2, 3 (D = 256: and 7) widen K, those behind the softmax warps V; the issuers are warps 4 and up.
-    // Warps w and w + 4 share a quarter of the SM, its issue slots and ALUs.
+    // 4-bit pages: warps 1, 2, 3 (D = 256: and 7) widen K, those behind the softmax warps V; warps 4 and up issue products, the
+    // last one (D = 256: warp 6; role 8) brings Q.  Warps w and w + 4 share a quarter of the SM, its issue slots and ALUs.
     const int role = !QUANT ? warp : warp >= kBehind ? (NSTR == 2 && warp == kBehind + 3 ? 8 : 6)
                                                      : ((NSTR == 2 ? 0x54213330 : 0x38213330) >> (4 * warp)) & 15;
     if (role == 0) {
@@ -579,83 +561,6 @@ __global__ void __launch_bounds__((CfgOf<D, SRC, G>::THREADS), 1) seq_tc_kernel(
         walk.init(a, ar.tpt, run, &mi->sched, cta);
         int n = 0, kn = 0, qn = 0;                      // pieces, K tiles, Q tiles so far
         bool ok = true;
-        // 4-bit pages: lanes 0 .. 15 bring K's tiles, lanes 16 .. 31 V's, four keys each, in one pass (one after the
-        // other took this warp 2400 cycles a tile, and everybody waited).  lead: K tiles that V is behind; V's tiles so
-        // far, its piece, how far that is, its number
-        const bool mine_v = lane >= 16;
-        int lead = 0, vn = 0, vt = 0, vpn = -1;
-        SeqPiece vp;
-        vp.nt = 0;
-        // of this lane's piece: table row, keys, first key not behind every row's window, KV head, affine; its next
-        // four keys and the cells of their page and of that of the four a tile on
-        const int32_t *row = a.table;
-        int r_kv = 0, r_lo = 0, r_kh = 0, r_key = 0, r_cell[2] = {};
-        const uint32_t *r_src = static_cast<const uint32_t *>(mine_v ? ar.qc.va : ar.qc.ka);
-        auto raw_cell = [&](int key) { return key < r_kv ? __ldg(row + (key >> a.page_shift)) : 0; };
-        auto raw_piece = [&](const SeqPiece &p, bool v) {
-            if (mine_v != v) return;
-            row = a.table + static_cast<long long>(p.b) * a.max_pages;
-            r_kv = p.kv;
-            r_lo = a.window ? p.prefix + p.i0 - a.window + 1 : INT_MIN;
-            r_kh = p.kh;
-            r_key = (p.t0 << TKS) + 4 * (lane & 15);
-            r_cell[0] = raw_cell(r_key);
-            r_cell[1] = raw_cell(r_key + TK);
-        };
-        // the next tile of K (where k_on) and of V (v_on)
-        auto raw_step = [&](bool k_on, bool v_on) -> bool {
-            if (v_on && vt == vp.nt) {
-                if (!fetch(&vp)) return false;
-                vt = 0;
-                ++vpn;
-                raw_piece(vp, true);
-            }
-            const bool on = mine_v ? v_on : k_on;
-            const int jn = mine_v ? vn : kn, st = (mine_v ? QC::NR : 0) + jn % QC::NR;
-            uint64_t *bar = &qm->full[st];
-            bool got = true;
-            if (on) got = wait_bar(&qm->empty[st], (static_cast<uint32_t>(jn / QC::NR) & 1u) ^ 1u, ar.polls);
-            if (!__all_sync(0xffffffffu, got)) return false;
-            if (on && (lane & 15) == 0) {
-                RawInfo &info = qm->info[st];
-                info.end = 0;
-                if (mine_v) {
-                    info.look = is_masked(vp, vp.t0 + vt);
-                    info.n = vpn;
-                    info.k0 = r_key;
-                    if (info.look) info.p = vp;
-                }
-                mbar_arrive_expect_tx(bar, QC::AFFINE);
-            }
-            __syncwarp();
-            if (on) {
-                unsigned char *raw = sm + QC::OFF_RAW + st * QC::RAW;
-                const int qk = min(TK, 1 << a.page_shift), at = 4 * (lane & 15), in = r_key & ((1 << a.page_shift) - 1);
-                // n_pages: out of range, zeros
-                const bool live = r_key < r_kv && r_cell[0] >= 0 && r_cell[0] < a.n_pages;
-                const int page = live ? r_cell[0] : a.n_pages;
-                if (!live && r_key < r_kv && r_key + 4 > r_lo) atomicOr(a.status, kSeqBadPage);   // (behind the window it may be gone)
-                if ((at & (qk - 1)) == 0) {             // one map an instruction
-                    if (mine_v) tma_load_raw(raw + at * (D / 2), &maps.v, bar, in, r_kh, page);
-                    else tma_load_raw(raw + at * (D / 2), &maps.k, bar, in, r_kh, page);
-                }
-                const uint32_t *src = live ? r_src + r_kh * ar.qc.a_sh + page * ar.qc.a_sp + in * ar.qc.a_st : r_src;
-                const uint32_t dst = smem_u32(raw) + QC::AFFINE + at * (QC::NG * 4);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bool l = live && r_key + i < r_kv;
-                    copy_words<QC::NG>(dst + i * (QC::NG * 4), l ? src + i * ar.qc.a_st : r_src, l);
-                }
-                arrive_after_copies(bar);
-                r_key += TK;
-                r_cell[0] = r_cell[1];
-                r_cell[1] = raw_cell(r_key + TK);       // (past the piece's last tile it is not used)
-            }
-            __syncwarp();
-            if (k_on) { ++kn; ++lead; }
-            if (v_on) { ++vn; ++vt; --lead; }
-            return true;
-        };
         if (lane == 0) ar.ws.rec[cta] = {0, 0, 0, 0};
 #pragma unroll 1
         for (;; ++n) {
@@ -696,17 +601,7 @@ __global__ void __launch_bounds__((CfgOf<D, SRC, G>::THREADS), 1) seq_tc_kernel(
                 }
                 __syncwarp();
             };
-            if constexpr (QUANT) {
-                if (n == 0) load_q();
-                raw_piece(p, false);
-#pragma unroll 1
-                for (int t = 0; t < p.nt && ok; ++t) {
-                    ok = raw_step(true, lead >= QC::kLead);
-                    if (ok && t == 0 && n > 0) load_q();
-                }
-                if (!ok) break;
-                continue;
-            }
+            if constexpr (QUANT) continue;              // (that is all; other warps bring Q, K and V)
             int page = page_of(p, p.t0);
 #pragma unroll 1
             for (int t = 0; t < p.nt; ++t) {
@@ -731,30 +626,6 @@ __global__ void __launch_bounds__((CfgOf<D, SRC, G>::THREADS), 1) seq_tc_kernel(
             }
             if (!ok) break;
         }
-        if constexpr (QUANT) {
-            while (ok && lead > 0) ok = raw_step(false, true);
-            // the end, at each stage
-#pragma unroll 1
-            for (int i = 0; ok && i < 2 * QC::NR; ++i) {
-                const int kind = i >= QC::NR, jn = kind ? vn : kn, st = kind * QC::NR + jn % QC::NR;
-                ok = warp_wait(&qm->empty[st], (static_cast<uint32_t>(jn / QC::NR) & 1u) ^ 1u);
-                if (!ok) break;
-                if (lane == 0) {
-                    qm->info[st].end = 1;
-                    mbar_arrive(&qm->full[st]);
-                }
-                __syncwarp();
-                if (lane < 16) mbar_arrive(&qm->full[st]);
-                ++(kind ? vn : kn);
-            }
-            if (lane == 0)
-                for (int i = 0; i < 2 * QC::NR; ++i) {
-                    // the stage's last job
-                    const int c = i < QC::NR ? kn : vn, jn = c - 1 - ((c - 1 - i % QC::NR) % QC::NR + QC::NR) % QC::NR;
-                    if (jn >= 0 && !mbar_wait_sleep(&qm->full[i], static_cast<uint32_t>(jn / QC::NR) & 1u, 1u << 21, 1000))
-                        atomicOr(a.status, kSeqTimeout);
-                }
-        }
         failed |= !ok;
         // every copy issued has landed before the CTA's memory goes
         if (lane == 0) {
@@ -764,49 +635,130 @@ __global__ void __launch_bounds__((CfgOf<D, SRC, G>::THREADS), 1) seq_tc_kernel(
                 if (!mbar_wait_sleep(&mi->k_full[i % NK], static_cast<uint32_t>(i / NK) & 1u, 1u << 21, 1000))
                     atomicOr(a.status, kSeqTimeout);
         }
+    } else if (QUANT && role == 8) {
+        // ------------------------------------------------------- 4-bit pages: Q producer
+        // (of its own: pieces have to be published ahead of Q's place coming free, since the widening warps look up to three
+        // tiles ahead for their copies)
+        int qn = 0;
+        bool ok = true;
+        SeqPiece p;
+#pragma unroll 1
+        while (ok && fetch(&p)) {
+            if (qn > 0) ok = warp_wait(&mi->q_empty, qn - 1);
+            if (!ok) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&mi->q_full, C::SLABS * ar.tpt * a.g * 128);
+                for (int x = 0; x < C::SLABS; ++x)
+                    tma_load_3d(sm + C::OFF_Q + x * C::QSLAB, &maps.q, &mi->q_full, x * 64, p.kh * a.g, p.q0 + p.i0);
+            }
+            __syncwarp();
+            ++qn;
+        }
+        failed |= !ok;
+        if (lane == 0 && qn > 0 && !mbar_wait_sleep(&mi->q_full, static_cast<uint32_t>(qn - 1) & 1u, 1u << 21, 1000)) atomicOr(a.status, kSeqTimeout);
     } else if (QUANT && (role == 3 || role == 6)) {
         // -------------------------------------------------- 4-bit pages: widening, V guarded
         if constexpr (QUANT) {
-            constexpr int PARTS = QC::PARTS, ITS = 8 / PARTS, U = 2;
             const int kind = role == 6, me = kind ? warp - kBehind : warp == 7 ? 3 : warp - 1;   // kind 0: K, 1: V
-            const int part = PARTS == 1 ? 0 : me;
-            int j = PARTS == 1 ? me : 0;                // tile
-            bool ok = true;
+            const int part = QC::PARTS == 1 ? 0 : me, wi = kind * QC::WARPS + me;
+            SeqPiece *own = qm->own[wi];
+            unsigned char *raw = sm + QC::OFF_RAW + wi * QC::ROUNDS * QC::RAW;
+            // this lane's vector of the first row it copies, and its row of scales and biases, in a page's first token of its head
+            constexpr int CPR = D / 32, CROWS = 32 / CPR;          // 16-byte vectors of a row of codes, rows a warp copies at once
+            const uint32_t *codes = kind ? ar.qc.vc : ar.qc.kc, *affine = static_cast<const uint32_t *>(kind ? ar.qc.va : ar.qc.ka);
+            // the warp's next tile: tile t of piece n (in own[slot]), its first key of this warp, and what its copies need;
+            // lane r holds the cell of the page of round r
+            int n = -1, slot = 0, t = QC::PARTS == 1 ? me : 0, nt = 0, t0 = 0, key = 0, kv = 0, lo = 0, cell = 0;
+            const int32_t *cells = a.table;
+            bool more = true, ok = true;
+            auto advance = [&] {
+                while (t >= nt) {
+                    t -= nt;
+                    const int i = piece_n % kPieces;
+                    ok = warp_wait(&mi->piece_full[i], piece_n / kPieces) && ok;
+                    ++piece_n;
+                    more = ok && mi->piece[i].valid;
+                    if (!ok) return;
+                    if (lane < static_cast<int>(sizeof(SeqPiece) / 4)) reinterpret_cast<uint32_t *>(&own[slot])[lane] = reinterpret_cast<const uint32_t *>(&mi->piece[i])[lane];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&mi->piece_empty[i]);
+                    if (!more) return;
+                    const SeqPiece &p = own[slot];
+                    ++n;
+                    nt = p.nt;
+                    t0 = p.t0;
+                    kv = p.kv;
+                    lo = a.window ? p.prefix + p.i0 - a.window + 1 : INT_MIN;
+                    cells = a.table + static_cast<long long>(p.b) * a.max_pages;
+                    codes = (kind ? ar.qc.vc : ar.qc.kc) + p.kh * ar.qc.c_sh + lane / CPR * ar.qc.c_st + lane % CPR * 4;
+                    affine = static_cast<const uint32_t *>(kind ? ar.qc.va : ar.qc.ka) + p.kh * ar.qc.a_sh + (lane & 15) * ar.qc.a_st;
+                }
+                key = ((t0 + t) << TKS) + 16 * part;
+                cell = lane < QC::ROUNDS && key + 16 * lane < kv ? __ldg(cells + ((key + 16 * lane) >> a.page_shift)) : 0;
+            };
+            // copies of round r of the next tile, as one group (an empty one where there is none)
+            auto issue = [&](int r) {
+                if (more) {
+                    const int k = key + 16 * r, in = k & ((1 << a.page_shift) - 1);
+                    int page = __shfl_sync(0xffffffffu, cell, r);
+                    const bool live = k < kv && static_cast<unsigned>(page) < static_cast<unsigned>(a.n_pages);
+                    if (!live) {
+                        if (k < kv && k + 16 > lo && lane == 0) atomicOr(a.status, kSeqBadPage);   // (behind the window it may be gone)
+                        page = 0;
+                    }
+                    // keys that do not exist have scale and bias 0: what their codes are does not matter
+                    const uint32_t dst = smem_u32(raw + r * QC::RAW);
+                    const uint32_t *src = codes + (page * ar.qc.c_sp + in * ar.qc.c_st);
+#pragma unroll
+                    for (int i = 0; i < CPR / 2; ++i)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + lane * 16 + i * 512), "l"(src + i * CROWS * ar.qc.c_st) : "memory");
+                    if (lane < 16)
+                        copy_words<QC::NG>(dst + QC::CODES + lane * (QC::NG * 4), affine + (page * ar.qc.a_sp + in * ar.qc.a_st), live && k + lane < kv);
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            };
+            advance();
+            for (int r = 0; r < QC::ROUNDS; ++r) issue(r);
 #pragma unroll 1
-            for (;;) {
-                const int rs = kind * QC::NR + j % QC::NR, st = j % NK;
-                ok = warp_wait(&qm->full[rs], j / QC::NR);
+            for (int j = QC::PARTS == 1 ? me : 0; more && ok; j += QC::STEP) {   // tile
+                const SeqPiece &p = own[slot];
+                const int k0 = (t0 + t) << TKS, poison_n = n % kPoison;
+                const bool look = kind && is_masked(p, t0 + t);
+                const int st = j % NK;
+                // the next tile, whose copies follow this one's reads
+                slot ^= 1;
+                t += QC::STEP;
+                if (t < nt && lane < static_cast<int>(sizeof(SeqPiece) / 4))   // (of the same piece)
+                    reinterpret_cast<uint32_t *>(&own[slot])[lane] = reinterpret_cast<const uint32_t *>(&p)[lane];
+                __syncwarp();
+                advance();
+                ok = ok && warp_wait(kind ? &mi->v_empty[st] : &mi->k_empty[st], (static_cast<uint32_t>(j / NK) & 1u) ^ 1u);
                 if (!ok) break;
-                const RawInfo &info = qm->info[rs];
-                if (info.end) break;
-                const bool look = kind && info.look;
-                ok = warp_wait(kind ? &mi->v_empty[st] : &mi->k_empty[st], (static_cast<uint32_t>(j / NK) & 1u) ^ 1u);
-                if (!ok) break;
-                unsigned char *tile = sm + (kind ? C::OFF_V : C::OFF_K) + st * C::STAGE;
+                unsigned char *tile = sm + (kind ? C::OFF_V : C::OFF_K) + st * C::STAGE + part * 2048;
                 uint32_t acc[4] = {};
 #pragma unroll 1
-                for (int it = ITS * part; it < ITS * (part + 1); it += U)
-                    widen_units<D, G, BF16, U>(sm + QC::OFF_RAW + rs * QC::RAW, tile, it, kind == 0, look, acc,
-                                               it + U == ITS * (part + 1) && !look ? &qm->empty[rs] : nullptr);
+                for (int r = 0; r < QC::ROUNDS; ++r) {
+                    asm volatile("cp.async.wait_group %0;" ::"n"(QC::ROUNDS - 1) : "memory");
+                    __syncwarp();
+                    widen_round<D, G, BF16>(raw + r * QC::RAW, tile + r * 2048, kind == 0, look, acc, [&] { issue(r); });
+                }
                 if (look) {
                     // an element that is not finite must not reach rows that do not see it (0 x NaN): it is taken out,
                     // and the rows that see it are marked
                     const bool found = ((odd16<BF16>(acc[0]) | odd16<BF16>(acc[1]) | odd16<BF16>(acc[2]) | odd16<BF16>(acc[3])) & 0x80008000u) != 0;
                     if (__any_sync(0xffffffffu, found)) {
-                        const int n = info.n % kPoison, r0 = 8 * ITS * part;
-                        mark_odd<D, BF16>(a, info.p, info.k0, r0, min(max(info.p.kv - info.k0, 0), r0 + 8 * ITS), TK, tile,
-                                          ar.poison + (static_cast<size_t>(cta) * kPoison + n) * ROWS * (D / 32), false);
-                        if (lane == 0) mi->poisoned[n] = 1;
+                        const int r0 = 16 * part;
+                        mark_odd<D, BF16>(a, p, k0, r0, min(max(p.kv - k0, 0), r0 + 16 * QC::ROUNDS), TK, sm + C::OFF_V + st * C::STAGE,
+                                          ar.poison + (static_cast<size_t>(cta) * kPoison + poison_n) * ROWS * (D / 32), false);
+                        if (lane == 0) mi->poisoned[poison_n] = 1;
                     }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(kind ? &mi->v_ready[st] : &mi->k_full[st]);
-                    if (look) mbar_arrive(&qm->empty[rs]);    // (not before the marks: they want the piece)
-                }
-                j += PARTS == 1 ? 3 : 1;
+                if (lane == 0) mbar_arrive(kind ? &mi->v_ready[st] : &mi->k_full[st]);
             }
+            // every copy has landed before the CTA's memory goes
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
             failed |= !ok;
         }
     } else if (role == 6) {
@@ -1311,16 +1263,14 @@ cudaError_t launch_dim(const SeqArgs &a, const SeqTcPlan &pl, cudaStream_t s) {
     return a.bf16 ? launch<D, kPacked, true>(ar, maps, s) : launch<D, kPacked, false>(ar, maps, s);
 }
 
-// 4-bit pages: pl.k and pl.v are maps of the codes.
+// 4-bit pages (pl.k and pl.v are not used).
 template <int D>
 cudaError_t launch_quant_dim(const SeqQuantArgs &a, const SeqTcPlan &pl, cudaStream_t s) {
     Args ar = {};
     fill_args<D>(a.s, pl, &ar);
     ar.qc = a.c;
-    Maps maps;
+    Maps maps = {};
     maps.q = pl.q;
-    maps.k = pl.k;
-    maps.v = pl.v;
     if (a.s.bf16) return a.group == 32 ? launch<D, kQuant, true, 32>(ar, maps, s) : launch<D, kQuant, true, 64>(ar, maps, s);
     return a.group == 32 ? launch<D, kQuant, false, 32>(ar, maps, s) : launch<D, kQuant, false, 64>(ar, maps, s);
 }
