@@ -352,23 +352,26 @@ __device__ __forceinline__ uint32_t hfma(uint32_t x, uint32_t y, uint32_t z) {
     else asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(y), "r"(z));
     return r;
 }
-// scale * code + bias of 8 codes (word x: a quad in the low half, the next in the high half) as 16-bit pairs of
-// elements n and n + 4, each rounded once.  A code under the exponent of a power of two is that power plus the code
-// (f16: 1024 + c or 1024 + 16 c; bf16: 128 + c); taking the power off again is exact.
-template <bool BF16>
-__device__ __forceinline__ void widen(uint32_t x, uint32_t s2, uint32_t b2, uint32_t (&v)[4]) {
-    if constexpr (BF16) {
-        constexpr uint32_t one = 0x3f803f80u, off = 0xc300c300u;                   // 1, -128
+// scale * code + bias of the 8 codes of a block's half H in two quads' words, as 16-bit pairs in order, each rounded
+// once.  A code under the exponent of a power of two is that power plus the code; taking the power off again is
+// exact.  f16: a byte in both halves, its low nibble under 1024 (a step of 1), its high one under 64 (1/16).  bf16, whose
+// seven bits hold one nibble in place: the high half from the word shifted by a nibble, both under 128.
+template <bool BF16, int H>
+__device__ __forceinline__ uint4 widen8(uint32_t a, uint32_t a4, uint32_t b, uint32_t b4, uint32_t s2, uint32_t b2) {
+    uint32_t v[4];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) v[n] = hfma<true>(hfma<true>(((x >> (4 * n)) & 0x000f000fu) | 0x43004300u, one, off), s2, b2);
-    } else {
-        constexpr uint32_t one = 0x3c003c00u, off = 0xe400e400u, part = 0x2c002c00u, off16 = 0xd400d400u;   // 1, -1024, 1/16, -64
-        const uint32_t y = x >> 8;
-        v[0] = hfma<false>(hfma<false>((x & 0x000f000fu) | 0x64006400u, one, off), s2, b2);
-        v[1] = hfma<false>(hfma<false>((x & 0x00f000f0u) | 0x64006400u, part, off16), s2, b2);
-        v[2] = hfma<false>(hfma<false>((y & 0x000f000fu) | 0x64006400u, one, off), s2, b2);
-        v[3] = hfma<false>(hfma<false>((y & 0x00f000f0u) | 0x64006400u, part, off16), s2, b2);
+    for (int n = 0; n < 4; ++n) {
+        const int k = 2 * H + (n & 1);
+        const uint32_t w = n < 2 ? a : b, w4 = n < 2 ? a4 : b4;
+        if constexpr (BF16) {
+            const uint32_t x = (__byte_perm(w, w4, 0x4400 + 0x1111 * k) & 0x000f000fu) | 0x43004300u;
+            v[n] = hfma<true>(hfma<true>(x, 0x3f803f80u, 0xc300c300u), s2, b2);
+        } else {
+            const uint32_t x = (__byte_perm(w, w, 0x1111 * k) & 0x00f0000fu) | 0x54006400u;
+            v[n] = hfma<false>(hfma<false>(x, 0x3c003c00u, 0xd400e400u), s2, b2);
+        }
     }
+    return make_uint4(v[0], v[1], v[2], v[3]);
 }
 template <int N>
 __device__ __forceinline__ void shared_words(const unsigned char *p, uint32_t (&w)[N]) {
@@ -385,58 +388,59 @@ __device__ __forceinline__ void shared_words(const unsigned char *p, uint32_t (&
         }
     }
 }
+// Where lane's part of a 16-key round begins: row r (+ 8), the 16-byte vector of its elements 8 t .. 8 t + 7 of an even
+// block (the odd block's is 64 bytes on or back: 128-byte swizzle).  Eight lanes that work together take rows r and
+// r ^ 5: their stores cover all banks once.
+struct RoundLane {
+    int row, at, odd;
+};
+__device__ __forceinline__ RoundLane round_lane() {
+    const int lane = threadIdx.x & 31, r = (lane >> 3) ^ ((lane & 4) ? 5 : 0);
+    return {r, r * 128 + (((lane & 3) ^ r) << 4), (r & 4) ? -64 : 64};
+}
 // A round: 16 keys, two units a lane.  A unit is a key's quads 2 t and 2 t + 1 of every 32-element block (D / 32 words in a
-// row of memory), 8 neighbouring elements of each block, to 64-column slabs of 64 rows with the 128-byte swizzle.  Eight
-// lanes that work together take rows r and r ^ 5: their stores cover all banks once.  K's elements are put in order,
-// V's stay as 0, 4, 1, 5, 2, 6, 3, 7 of every eight (the epilogue names O's columns so).  `behind` runs once the raw words are
-// in registers.  acc: the largest magnitudes, where `look`.
+// row of memory), 8 neighbouring elements of each block, to 64-column slabs of 64 rows with the 128-byte swizzle.
+// `behind` runs once the raw words are in registers.
 template <int D, int G, bool BF16, typename Behind>
-__device__ __forceinline__ void widen_round(const unsigned char *raw, unsigned char *tile, bool order, bool look, uint32_t (&acc)[4], Behind &&behind) {
+__device__ __forceinline__ void widen_round(const unsigned char *raw, unsigned char *tile, Behind &&behind) {
     using C = QuantCfg<D, G>;
     constexpr int NB = D / 32, NG = D / G, U = 2;
-    const int lane = threadIdx.x & 31, t = lane & 3, r = (lane >> 3) ^ ((lane & 4) ? 5 : 0);
+    const RoundLane me = round_lane();
+    const int t = threadIdx.x & 3;
     uint32_t w[U][NB], sb[U][NG];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        shared_words<NB>(raw + (r + 8 * u) * (D / 2) + t * (NB * 4), w[u]);
-        shared_words<NG>(raw + C::CODES + (r + 8 * u) * (NG * 4), sb[u]);
+        shared_words<NB>(raw + (me.row + 8 * u) * (D / 2) + t * (NB * 4), w[u]);
+        shared_words<NG>(raw + C::CODES + (me.row + 8 * u) * (NG * 4), sb[u]);
     }
     __syncwarp();
     behind();
-    unsigned char *dst = tile + r * 128 + ((t ^ r) << 4);
-    const int odd = (r & 4) ? -64 : 64;                 // from an even block's place to the odd one's
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int j0 = 0; j0 < NB; j0 += 4) {
-            constexpr int NJ = NB < 4 ? NB : 4;
-            uint32_t v[NJ][4];
-#pragma unroll
-            for (int jj = 0; jj < NJ; ++jj) {
-                const int j = j0 + jj;
-                const uint32_t x = __byte_perm(w[u][j / 2], w[u][NB / 2 + j / 2], j & 1 ? 0x7632 : 0x5410);
-                widen<BF16>(x, __byte_perm(sb[u][j * 32 / G], 0u, 0x1010), __byte_perm(sb[u][j * 32 / G], 0u, 0x3232), v[jj]);
-            }
-            if (look) {
-#pragma unroll
-                for (int jj = 0; jj < NJ; ++jj)
-#pragma unroll
-                    for (int n = 0; n < 4; ++n) acc[n] = max_abs<BF16>(acc[n], v[jj][n]);
-            }
-            if (order) {
-#pragma unroll
-                for (int jj = 0; jj < NJ; ++jj) {
-                    const uint32_t a = v[jj][0], b = v[jj][1], c = v[jj][2], d = v[jj][3];
-                    v[jj][0] = __byte_perm(a, b, 0x5410);
-                    v[jj][1] = __byte_perm(c, d, 0x5410);
-                    v[jj][2] = __byte_perm(a, b, 0x7632);
-                    v[jj][3] = __byte_perm(c, d, 0x7632);
-                }
-            }
-#pragma unroll
-            for (int jj = 0; jj < NJ; ++jj)
-                *reinterpret_cast<uint4 *>(dst + 1024 * u + ((j0 + jj) / 2) * C::SLAB + (jj & 1 ? odd : 0)) = make_uint4(v[jj][0], v[jj][1], v[jj][2], v[jj][3]);
+        for (int i = 0; i < NB / 2; ++i) {              // blocks 2 i and 2 i + 1: one slab
+            const uint32_t a = w[u][i], b = w[u][NB / 2 + i], a4 = BF16 ? a >> 4 : 0u, b4 = BF16 ? b >> 4 : 0u;
+            unsigned char *dst = tile + me.at + 1024 * u + i * C::SLAB;
+            const uint32_t g0 = sb[u][64 * i / G], g1 = sb[u][(64 * i + 32) / G];
+            *reinterpret_cast<uint4 *>(dst) = widen8<BF16, 0>(a, a4, b, b4, __byte_perm(g0, 0u, 0x1010), __byte_perm(g0, 0u, 0x3232));
+            *reinterpret_cast<uint4 *>(dst + me.odd) = widen8<BF16, 1>(a, a4, b, b4, __byte_perm(g1, 0u, 0x1010), __byte_perm(g1, 0u, 0x3232));
         }
+}
+// Is some element of what this lane wrote in `rounds` rounds not finite.
+template <int D, bool BF16>
+__device__ __forceinline__ bool round_odd(const unsigned char *tile, int rounds) {
+    const RoundLane me = round_lane();
+    uint32_t acc = 0u;
+#pragma unroll 1
+    for (int i = 0; i < 2 * rounds; ++i)
+#pragma unroll 1
+        for (int s = 0; s < D / 64; ++s) {
+            const unsigned char *p = tile + me.at + 1024 * i + s * Cfg<D>::SLAB;
+            const uint4 x = *reinterpret_cast<const uint4 *>(p), y = *reinterpret_cast<const uint4 *>(p + me.odd);
+            acc = max_abs<BF16>(max_abs<BF16>(max_abs<BF16>(max_abs<BF16>(acc, x.x), x.y), x.z), x.w);
+            acc = max_abs<BF16>(max_abs<BF16>(max_abs<BF16>(max_abs<BF16>(acc, y.x), y.y), y.z), y.w);
+        }
+    return (odd16<BF16>(acc) & 0x80008000u) != 0;
 }
 
 template <int D, int SRC, int G>
@@ -735,18 +739,16 @@ __global__ void __launch_bounds__((CfgOf<D, SRC, G>::THREADS), 1) seq_tc_kernel(
                 ok = ok && warp_wait(kind ? &mi->v_empty[st] : &mi->k_empty[st], (static_cast<uint32_t>(j / NK) & 1u) ^ 1u);
                 if (!ok) break;
                 unsigned char *tile = sm + (kind ? C::OFF_V : C::OFF_K) + st * C::STAGE + part * 2048;
-                uint32_t acc[4] = {};
 #pragma unroll 1
                 for (int r = 0; r < QC::ROUNDS; ++r) {
                     asm volatile("cp.async.wait_group %0;" ::"n"(QC::ROUNDS - 1) : "memory");
                     __syncwarp();
-                    widen_round<D, G, BF16>(raw + r * QC::RAW, tile + r * 2048, kind == 0, look, acc, [&] { issue(r); });
+                    widen_round<D, G, BF16>(raw + r * QC::RAW, tile + r * 2048, [&] { issue(r); });
                 }
                 if (look) {
                     // an element that is not finite must not reach rows that do not see it (0 x NaN): it is taken out,
                     // and the rows that see it are marked
-                    const bool found = ((odd16<BF16>(acc[0]) | odd16<BF16>(acc[1]) | odd16<BF16>(acc[2]) | odd16<BF16>(acc[3])) & 0x80008000u) != 0;
-                    if (__any_sync(0xffffffffu, found)) {
+                    if (__any_sync(0xffffffffu, round_odd<D, BF16>(tile, QC::ROUNDS))) {
                         const int r0 = 16 * part;
                         mark_odd<D, BF16>(a, p, k0, r0, min(max(p.kv - k0, 0), r0 + 16 * QC::ROUNDS), TK, sm + C::OFF_V + st * C::STAGE,
                                           ar.poison + (static_cast<size_t>(cta) * kPoison + poison_n) * ROWS * (D / 32), false);
@@ -1100,8 +1102,6 @@ __global__ void __launch_bounds__((CfgOf<D, SRC, G>::THREADS), 1) seq_tc_kernel(
                 const bool odd = *static_cast<volatile int *>(&mi->poisoned[n % kPoison]) != 0;
                 const uint32_t *poison = ar.poison + ((static_cast<size_t>(cta) * kPoison + n % kPoison) * ROWS + urow) * (D / 32);
                 const float inv = l_run > 0.0f ? 1.0f / l_run : (l_run == 0.0f ? 0.0f : l_run);
-                // column of element e of a run of O's columns (4-bit pages: V's order of every eight)
-                auto at = [](int e) { return QUANT ? (e & ~7) + ((e & 3) << 1) + ((e >> 2) & 1) : e; };
                 const size_t slot = static_cast<size_t>(p.slot < 0 ? 0 : p.slot);
                 float4 *part = reinterpret_cast<float4 *>(ar.ws.o) + slot * (D / 4) * ROWS + urow;
                 unsigned char *stage = sm + C::OFF_OUT + (warp - C::SW) * 2048;
@@ -1132,10 +1132,10 @@ __global__ void __launch_bounds__((CfgOf<D, SRC, G>::THREADS), 1) seq_tc_kernel(
 #pragma unroll
                         for (int e = 0; e < 32; e += 8) {
                             uint4 x;
-                            x.x = pack16<BF16>(__uint_as_float(o[at(e)]) * inv, __uint_as_float(o[at(e + 1)]) * inv);
-                            x.y = pack16<BF16>(__uint_as_float(o[at(e + 2)]) * inv, __uint_as_float(o[at(e + 3)]) * inv);
-                            x.z = pack16<BF16>(__uint_as_float(o[at(e + 4)]) * inv, __uint_as_float(o[at(e + 5)]) * inv);
-                            x.w = pack16<BF16>(__uint_as_float(o[at(e + 6)]) * inv, __uint_as_float(o[at(e + 7)]) * inv);
+                            x.x = pack16<BF16>(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+                            x.y = pack16<BF16>(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+                            x.z = pack16<BF16>(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
+                            x.w = pack16<BF16>(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
                             *reinterpret_cast<uint4 *>(stage + lane * 64 + (((e / 8) ^ ((lane >> 1) & 3)) << 4)) = x;
                         }
                         __syncwarp();
@@ -1149,8 +1149,8 @@ __global__ void __launch_bounds__((CfgOf<D, SRC, G>::THREADS), 1) seq_tc_kernel(
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
                             part[static_cast<size_t>((c + e) / 4) * ROWS] =
-                                make_float4(__uint_as_float(o[at(e)]), __uint_as_float(o[at(e + 1)]), __uint_as_float(o[at(e + 2)]),
-                                            __uint_as_float(o[at(e + 3)]));
+                                make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
+                                            __uint_as_float(o[e + 3]));
                     }
                     __syncwarp();
                 }
