@@ -51,6 +51,28 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
+// Two f32 at a time: the two query rows that a lane holds of a key.
+__device__ __forceinline__ uint64_t two(float x, float y) {
+    return static_cast<uint64_t>(__float_as_uint(x)) | (static_cast<uint64_t>(__float_as_uint(y)) << 32);
+}
+__device__ __forceinline__ float first(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x)); }
+__device__ __forceinline__ float second(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x >> 32)); }
+__device__ __forceinline__ uint64_t fma_two(uint64_t x, uint64_t y, uint64_t z) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul_two(uint64_t x, uint64_t y) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+// The larger of three, of the magnitudes where a NaN does not count.
+__device__ __forceinline__ float max_abs3(float x, float y, float z) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(fabsf(y)), "f"(fabsf(z)));
+    return r;
+}
 // N words (1, 2, 4 or 8) that are read once.
 template <int N>
 __device__ __forceinline__ void load_words(const uint32_t *p, uint32_t *w) {
@@ -110,7 +132,7 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
         // Q fragments: of block j the elements 32 j + 8 t + {0, 4 | 1, 5 | 2, 6 | 3, 7}, the second and
         // fourth pair over 16 (their codes come as 16 c), times 2^e: the row's largest in [2^13, 2^14)
         uint4 qb[SQ ? 1 : NR][SQ ? 1 : NB];
-        float fr[NR][2], qs[NR][NG][2];
+        uint64_t fr[NR], qs[NR][NG];
 #pragma unroll
         for (int x = 0; x < NR; ++x) {
             const int row = g + 8 * x, tok = row / a.g;
@@ -154,31 +176,32 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
             }
             // 2^24 / 2^e of row g, and its sums: to the lanes that hold the rows 2 t and 2 t + 1 of a product
             const float back = __uint_as_float(static_cast<uint32_t>(254 - up) << 23) * 0x1p24f * scale2;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) fr[x][e] = __shfl_sync(0xffffffffu, back, 8 * t + 4 * e);
+            fr[x] = two(__shfl_sync(0xffffffffu, back, 8 * t), __shfl_sync(0xffffffffu, back, 8 * t + 4));
 #pragma unroll
             for (int n = 0; n < NG; ++n) {
                 float y = sum[n];
                 y += __shfl_xor_sync(0xffffffffu, y, 1);
                 y += __shfl_xor_sync(0xffffffffu, y, 2);
                 y *= scale2;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) qs[x][n][e] = __shfl_sync(0xffffffffu, y, 8 * t + 4 * e);
+                qs[x][n] = two(__shfl_sync(0xffffffffu, y, 8 * t), __shfl_sync(0xffffffffu, y, 8 * t + 4));
             }
         }
         if constexpr (SQ) __syncthreads();
         // Of rows 2 t + e of tile x: running max, sum, sums of P b (each lane its keys'), power of two of P s
-        float o[NR][NB][2][4], m[NR][2], l[NR][2], ab[NR][NG][2], sc[NR][NG][2];
+        // (mu: the running max less the raise, 0 where there is none; up: what moves it)
+        float o[NR][NB][2][4], mu[NR][2], up[NR][2], l[NR][2];
+        uint64_t ab[NR][NG], sc[NR][NG];
 #pragma unroll
         for (int x = 0; x < NR; ++x)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                m[x][e] = -INFINITY;
+                mu[x][e] = 0.0f;
+                up[x][e] = -INFINITY;
                 l[x][e] = 0.0f;
 #pragma unroll
                 for (int n = 0; n < NG; ++n) {
-                    ab[x][n][e] = 0.0f;
-                    sc[x][n][e] = 0x1p100f;             // too large for any scale: the first block sets it
+                    ab[x][n] = 0;
+                    sc[x][n] = two(0x1p100f, 0x1p100f); // too large for any scale: the first block sets it
                 }
 #pragma unroll
                 for (int j = 0; j < NB; ++j)
@@ -187,56 +210,38 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
             }
         const int key_end = min(p.kv, (p.t0 + p.nt) << kQmTks);
         const int32_t *table = a.table + static_cast<long long>(p.b) * a.max_pages;
-        // page of the 16-key block at `key`, -1: none
+        // page of the 16-key block at `key` (0 where there is none: nothing of it is seen, or the rows are not valid)
         auto page_of = [&](int key) -> int {
-            if (key >= key_end) return -1;
+            if (key >= key_end) return 0;
             const int page = __ldg(table + (key >> a.page_shift));
-            if (page >= 0 && page < a.n_pages) return page;
+            if (static_cast<unsigned>(page) < static_cast<unsigned>(a.n_pages)) return page;
             // a page before every row's window may be gone
             if (lane == 0 && !(a.window && key + 16 <= p.prefix - a.window + 1)) atomicOr(a.status, kSeqBadPage);
-            return -1;
+            return 0;
         };
+        // The whole block is in its page, so keys past the last one are read too, and masked like the others that
+        // a row does not see.
         uint32_t kw[2][NB], ka[2][NG], vw[4][VW], va[2][NG];
+        const uint32_t *k_lane = cc.kc + p.kh * cc.c_sh + g * cc.c_st + t * NB, *v_lane = cc.vc + p.kh * cc.c_sh + 2 * t * cc.c_st + g * VW;
+        const uint32_t *ka_lane = static_cast<const uint32_t *>(cc.ka) + p.kh * cc.a_sh + g * cc.a_st;
+        const uint32_t *va_lane = static_cast<const uint32_t *>(cc.va) + p.kh * cc.a_sh + g * cc.a_st;
         auto load_k = [&](int page, int key) {
             const int in = key & ((1 << a.page_shift) - 1);
-            const long long co = page * cc.c_sp + p.kh * cc.c_sh, ao = page * cc.a_sp + p.kh * cc.a_sh;
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const int kk = 8 * n + g;
-                if (page >= 0 && key + kk < p.kv) {
-                    load_words<NB>(cc.kc + co + (in + kk) * cc.c_st + t * NB, kw[n]);
-                    load_words<NG>(static_cast<const uint32_t *>(cc.ka) + ao + (in + kk) * cc.a_st, ka[n]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < NB; ++i) kw[n][i] = 0u;
-#pragma unroll
-                    for (int i = 0; i < NG; ++i) ka[n][i] = 0u;
-                }
-            }
+            const uint32_t *c = k_lane + (page * cc.c_sp + in * cc.c_st), *f = ka_lane + (page * cc.a_sp + in * cc.a_st);
+            load_words<NB>(c, kw[0]);
+            load_words<NB>(c + 8 * cc.c_st, kw[1]);
+            load_words<NG>(f, ka[0]);
+            load_words<NG>(f + 8 * cc.a_st, ka[1]);
         };
         auto load_v = [&](int page, int key) {
             const int in = key & ((1 << a.page_shift) - 1);
-            const long long co = page * cc.c_sp + p.kh * cc.c_sh, ao = page * cc.a_sp + p.kh * cc.a_sh;
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                const int kk = 2 * t + (n & 1) + 8 * (n >> 1);
-                if (page >= 0 && key + kk < p.kv) {
-                    load_words<VW>(cc.vc + co + (in + kk) * cc.c_st + g * VW, vw[n]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < VW; ++i) vw[n][i] = 0u;
-                }
-            }
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const int kk = 8 * n + g;
-                if (page >= 0 && key + kk < p.kv) {
-                    load_words<NG>(static_cast<const uint32_t *>(cc.va) + ao + (in + kk) * cc.a_st, va[n]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < NG; ++i) va[n][i] = 0u;
-                }
-            }
+            const uint32_t *c = v_lane + (page * cc.c_sp + in * cc.c_st), *f = va_lane + (page * cc.a_sp + in * cc.a_st);
+            load_words<VW>(c, vw[0]);
+            load_words<VW>(c + cc.c_st, vw[1]);
+            load_words<VW>(c + 8 * cc.c_st, vw[2]);
+            load_words<VW>(c + 9 * cc.c_st, vw[3]);
+            load_words<NG>(f, va[0]);
+            load_words<NG>(f + 8 * cc.a_st, va[1]);
         };
         int key = (p.t0 << kQmTks) + 16 * warp;
         int page = page_of(key), next = page_of(key + 16 * kQmWarps);
@@ -245,11 +250,9 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
 #pragma unroll 1
         for (; key < key_end; key += 16 * kQmWarps) {
             // logits in log2 units: s[x][2 n + e] of key g + 8 n, row 2 t + e of tile x
-            float s[NR][4], u[NR][4];
+            uint64_t s2[NR][2], u2[NR][2];
 #pragma unroll
-            for (int x = 0; x < NR; ++x)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) s[x][i] = u[x][i] = 0.0f;
+            for (int x = 0; x < NR; ++x) s2[x][0] = s2[x][1] = u2[x][0] = u2[x][1] = 0;
 #pragma unroll
             for (int n = 0; n < NG; ++n) {
                 float acc[NR][4];
@@ -273,18 +276,21 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
                 for (int i = 0; i < 2; ++i) {
                     const float sk = scale_of<BF16>(ka[i][n]), bk = bias_of<BF16>(ka[i][n]);
 #pragma unroll
-                    for (int x = 0; x < NR; ++x)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            s[x][2 * i + e] = fmaf(sk, acc[x][2 * i + e], s[x][2 * i + e]);
-                            u[x][2 * i + e] = fmaf(bk, qs[x][n][e], u[x][2 * i + e]);
-                        }
+                    for (int x = 0; x < NR; ++x) {
+                        s2[x][i] = fma_two(two(sk, sk), two(acc[x][2 * i], acc[x][2 * i + 1]), s2[x][i]);
+                        u2[x][i] = fma_two(two(bk, bk), qs[x][n], u2[x][i]);
+                    }
                 }
             }
+            float s[NR][4];
 #pragma unroll
             for (int x = 0; x < NR; ++x)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s[x][i] = fmaf(s[x][i], fr[x][i & 1], u[x][i]);
+                for (int i = 0; i < 2; ++i) {
+                    const uint64_t y = fma_two(s2[x][i], fr[x], u2[x][i]);
+                    s[x][2 * i] = first(y);
+                    s[x][2 * i + 1] = second(y);
+                }
             const int after = page_of(key + 32 * kQmWarps);
             load_k(next, key + 16 * kQmWarps);
             // bit 2 n + e: is key g + 8 n seen by row 2 t + e
@@ -314,7 +320,7 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
 #pragma unroll
             for (int x = 0; x < NR; ++x)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) rise |= fmaxf(s[x][e], s[x][2 + e]) > m[x][e] + kQmSlack;
+                for (int e = 0; e < 2; ++e) rise |= fmaxf(s[x][e], s[x][2 + e]) > up[x][e];
             if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
                 for (int x = 0; x < NR; ++x)
@@ -324,12 +330,13 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                        if (mx > m[x][e] + kQmSlack) {
-                            const float f = ex2(m[x][e] - mx);      // 0 from -inf
-                            m[x][e] = mx;
+                        if (mx > up[x][e]) {
+                            const float f = up[x][e] == -INFINITY ? 0.0f : ex2(mu[x][e] + kQmRaise - mx);
+                            mu[x][e] = mx - kQmRaise;
+                            up[x][e] = mx + kQmSlack;
                             l[x][e] *= f;
 #pragma unroll
-                            for (int n = 0; n < NG; ++n) ab[x][n][e] *= f;
+                            for (int n = 0; n < NG; ++n) ab[x][n] = mul_two(ab[x][n], e ? two(1.0f, f) : two(f, 1.0f));
 #pragma unroll
                             for (int j = 0; j < NB; ++j)
 #pragma unroll
@@ -340,45 +347,47 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
                         }
                     }
             }
-            float pr[NR][4];
+            uint64_t pr[NR][2];
 #pragma unroll
-            for (int x = 0; x < NR; ++x)
+            for (int x = 0; x < NR; ++x) {
+                float y[4];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float mu = m[x][e] == -INFINITY ? 0.0f : m[x][e] - kQmRaise;
-                    pr[x][e] = ex2(s[x][e] - mu);
-                    pr[x][2 + e] = ex2(s[x][2 + e] - mu);
-                    l[x][e] += pr[x][e] + pr[x][2 + e];
-                }
+                for (int i = 0; i < 4; ++i) y[i] = ex2(s[x][i] - mu[x][i & 1]);
+                l[x][0] += y[0] + y[2];
+                l[x][1] += y[1] + y[3];
+                pr[x][0] = two(y[0], y[1]);
+                pr[x][1] = two(y[2], y[3]);
+            }
             // P s and the sums of P b; where a row does not see a key its scale and bias do not count
-            float ps[NR][NG][4];
-            bool over = false;
+            uint64_t ps[NR][NG][2];
+            float most = 0.0f;
             if (!masked) {
 #pragma unroll
-                for (int x = 0; x < NR; ++x)
+                for (int n = 0; n < NG; ++n)
 #pragma unroll
-                    for (int n = 0; n < NG; ++n)
+                    for (int i = 0; i < 2; ++i) {
+                        const float sv = scale_of<BF16>(va[i][n]), bv = bias_of<BF16>(va[i][n]);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t sb = va[i >> 1][n];
-                            ps[x][n][i] = pr[x][i] * sc[x][n][i & 1] * scale_of<BF16>(sb);
-                            ab[x][n][i & 1] = fmaf(pr[x][i], bias_of<BF16>(sb), ab[x][n][i & 1]);
-                            over |= fabsf(ps[x][n][i]) > 40000.0f;
+                        for (int x = 0; x < NR; ++x) {
+                            ps[x][n][i] = mul_two(mul_two(pr[x][i], sc[x][n]), two(sv, sv));
+                            ab[x][n] = fma_two(pr[x][i], two(bv, bv), ab[x][n]);
+                            most = max_abs3(most, first(ps[x][n][i]), second(ps[x][n][i]));
                         }
+                    }
             } else {
 #pragma unroll
-                for (int x = 0; x < NR; ++x)
+                for (int n = 0; n < NG; ++n)
 #pragma unroll
-                    for (int n = 0; n < NG; ++n)
+                    for (int i = 0; i < 2; ++i)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t sb = (see[x] >> i) & 1u ? va[i >> 1][n] : 0u;
-                            ps[x][n][i] = pr[x][i] * sc[x][n][i & 1] * scale_of<BF16>(sb);
-                            ab[x][n][i & 1] = fmaf(pr[x][i], bias_of<BF16>(sb), ab[x][n][i & 1]);
-                            over |= fabsf(ps[x][n][i]) > 40000.0f;
+                        for (int x = 0; x < NR; ++x) {
+                            const uint32_t w0 = (see[x] >> (2 * i)) & 1u ? va[i][n] : 0u, w1 = (see[x] >> (2 * i + 1)) & 1u ? va[i][n] : 0u;
+                            ps[x][n][i] = mul_two(mul_two(pr[x][i], sc[x][n]), two(scale_of<BF16>(w0), scale_of<BF16>(w1)));
+                            ab[x][n] = fma_two(pr[x][i], two(bias_of<BF16>(w0), bias_of<BF16>(w1)), ab[x][n]);
+                            most = max_abs3(most, first(ps[x][n][i]), second(ps[x][n][i]));
                         }
             }
-            if (__any_sync(0xffffffffu, over)) {
+            if (__any_sync(0xffffffffu, most > 40000.0f)) {
                 // a row and group whose P s leaves f16's range: its power of two so that the largest finite scale
                 // it sees here becomes 1/8 to 1/4
 #pragma unroll
@@ -387,10 +396,11 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
                     for (int n = 0; n < NG; ++n)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const float s0 = (see[x] >> e) & 1u ? fabsf(scale_of<BF16>(va[0][n])) : 0.0f;
-                            const float s1 = (see[x] >> (2 + e)) & 1u ? fabsf(scale_of<BF16>(va[1][n])) : 0.0f;
-                            float top = fmaxf(s0 <= FLT_MAX ? s0 : 0.0f, s1 <= FLT_MAX ? s1 : 0.0f);
-                            float hit = fmaxf(fabsf(ps[x][n][e]), fabsf(ps[x][n][2 + e]));
+                            auto part = [&](uint64_t y) { return e ? second(y) : first(y); };
+                            const float v0 = (see[x] >> e) & 1u ? scale_of<BF16>(va[0][n]) : 0.0f;
+                            const float v1 = (see[x] >> (2 + e)) & 1u ? scale_of<BF16>(va[1][n]) : 0.0f;
+                            float top = fmaxf(fabsf(v0) <= FLT_MAX ? fabsf(v0) : 0.0f, fabsf(v1) <= FLT_MAX ? fabsf(v1) : 0.0f);
+                            float hit = fmaxf(fabsf(part(ps[x][n][0])), fabsf(part(ps[x][n][1])));
 #pragma unroll
                             for (int k = 4; k < 32; k <<= 1) {
                                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
@@ -398,9 +408,9 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
                             }
                             if (hit > 40000.0f && top > 0.0f) {
                                 const float to = __uint_as_float(static_cast<uint32_t>(max(251 - static_cast<int>(__float_as_uint(top) >> 23), 1)) << 23);
-                                if (to < sc[x][n][e]) {
-                                    const float f = to / sc[x][n][e];
-                                    sc[x][n][e] = to;
+                                const float was = part(sc[x][n]), now = fminf(to, was), f = now / was;
+                                if (now < was) {
+                                    sc[x][n] = e ? two(first(sc[x][n]), now) : two(now, second(sc[x][n]));
 #pragma unroll
                                     for (int j = n * BPG; j < (n + 1) * BPG; ++j)
 #pragma unroll
@@ -409,8 +419,9 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
                                             o[x][j][h][2 + e] *= f;
                                         }
                                 }
-                                ps[x][n][e] = (see[x] >> e) & 1u ? pr[x][e] * sc[x][n][e] * scale_of<BF16>(va[0][n]) : 0.0f;
-                                ps[x][n][2 + e] = (see[x] >> (2 + e)) & 1u ? pr[x][2 + e] * sc[x][n][e] * scale_of<BF16>(va[1][n]) : 0.0f;
+                                const float y0 = part(pr[x][0]) * now * v0, y1 = part(pr[x][1]) * now * v1;
+                                ps[x][n][0] = e ? two(first(ps[x][n][0]), y0) : two(y0, second(ps[x][n][0]));
+                                ps[x][n][1] = e ? two(first(ps[x][n][1]), y1) : two(y1, second(ps[x][n][1]));
                             }
                         }
             }
@@ -420,7 +431,7 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
 #pragma unroll
                 for (int n = 0; n < NG; ++n)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) pb[x][n][i] = transpose8(pack16<false>(ps[x][n][2 * i], ps[x][n][2 * i + 1]));
+                    for (int i = 0; i < 2; ++i) pb[x][n][i] = transpose8(pack16<false>(first(ps[x][n][i]), second(ps[x][n][i])));
             // O += V^T (P s): elements 32 j + 4 g + 2 h (+ 1) of 16 rows of the product, 8 query rows
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
@@ -446,14 +457,14 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
                 float y = l[x][e];
 #pragma unroll
                 for (int k = 4; k < 32; k <<= 1) y += __shfl_xor_sync(0xffffffffu, y, k);
-                if (g == 0) s_ml[warp][row] = make_float2(m[x][e], y);
+                if (g == 0) s_ml[warp][row] = make_float2(up[x][e] - kQmSlack, y);
                 float *dst = s_o + (warp * RR + row) * OS + 4 * g;
 #pragma unroll
                 for (int n = 0; n < NG; ++n) {
-                    float b = ab[x][n][e];
+                    float b = e ? second(ab[x][n]) : first(ab[x][n]);
 #pragma unroll
                     for (int k = 4; k < 32; k <<= 1) b += __shfl_xor_sync(0xffffffffu, b, k);
-                    const float f = 0x1p24f / sc[x][n][e], f16 = f * 0.0625f;
+                    const float f = 0x1p24f / (e ? second(sc[x][n]) : first(sc[x][n])), f16 = f * 0.0625f;
 #pragma unroll
                     for (int j = n * BPG; j < (n + 1) * BPG; ++j)
                         *reinterpret_cast<float4 *>(dst + 32 * j) =
