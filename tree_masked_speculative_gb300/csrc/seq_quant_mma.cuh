@@ -14,9 +14,9 @@
 // row and group that, like the running max, moves only when a block needs it.
 // A lane's words: for K the quads 2 t and 2 t + 1 of every 32-element block of keys g and
 // g + 8, for V quad g of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9 - one vector a key and
-// product, straight from global memory.  A warp takes every fourth block of 16 keys of its CTA's
-// run with the next block's words in flight; the batch is cut evenly over the CTAs by the schedule of
-// seq_sched.cuh.
+// product.  A warp takes every fourth block of 16 keys of its CTA's run, copied to shared memory three
+// blocks ahead (cp.async; no barrier inside the key loop); the batch is cut evenly over the CTAs by the
+// schedule of seq_sched.cuh.
 #pragma once
 
 #include "quant_page.cuh"
@@ -73,19 +73,31 @@ __device__ __forceinline__ float max_abs3(float x, float y, float z) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(fabsf(y)), "f"(fabsf(z)));
     return r;
 }
-// N words (1, 2, 4 or 8) that are read once.
+// N words (1, 2, 4 or 8) of shared memory.
 template <int N>
-__device__ __forceinline__ void load_words(const uint32_t *p, uint32_t *w) {
+__device__ __forceinline__ void load_words(const unsigned char *p, uint32_t *w) {
     if constexpr (N == 1) {
-        asm volatile("ld.global.L1::no_allocate.L2::128B.u32 %0, [%1];" : "=r"(w[0]) : "l"(p));
+        w[0] = *reinterpret_cast<const uint32_t *>(p);
     } else if constexpr (N == 2) {
-        asm volatile("ld.global.L1::no_allocate.L2::128B.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+        const uint2 x = *reinterpret_cast<const uint2 *>(p);
+        w[0] = x.x; w[1] = x.y;
     } else {
 #pragma unroll
         for (int i = 0; i < N; i += 4) {
-            const uint4 x = load_once(p + i);
+            const uint4 x = *reinterpret_cast<const uint4 *>(p + 4 * i);
             w[i] = x.x; w[i + 1] = x.y; w[i + 2] = x.z; w[i + 3] = x.w;
         }
+    }
+}
+// N words to shared memory, past L1 where the instruction takes 16 bytes.
+template <int N>
+__device__ __forceinline__ void copy_words(uint32_t dst, const uint32_t *src) {
+    if constexpr (N >= 4) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+            asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst + 4 * i), "l"(src + i) : "memory");
+    } else {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(4 * N) : "memory");
     }
 }
 // Scale and bias of a pair.
@@ -106,8 +118,15 @@ constexpr int kQmCtas = D == 256 ? 2 : NR == 2 ? (D == 64 ? 4 : 3) : (D == 64 ? 
 // Q's fragments in shared memory where registers are short.
 template <int D, int NR>
 constexpr bool kQmSharedQ = D * NR > 128;
-template <int D, int NR>
-constexpr size_t kQmSmem = sizeof(float) * kQmWarps * 8 * NR * (D + 4) + (kQmSharedQ<D, NR> ? NR * (D / 32) * 512 : 0);
+// Blocks of 16 keys that a warp has on their way or in work, each [K codes][V codes][K affine][V affine].
+constexpr int kQmStages = 4;
+template <int D, int G>
+constexpr int kQmStage = 16 * D + 2 * 16 * (D / G) * 4;
+// A warp's stages; its rows of O at the end of a piece stand in their place.
+template <int D, int G, int NR>
+constexpr int kQmWarpBytes = kQmStages * kQmStage<D, G> > 8 * NR * (D + 4) * 4 ? kQmStages * kQmStage<D, G> : 8 * NR * (D + 4) * 4;
+template <int D, int G, int NR>
+constexpr size_t kQmSmem = kQmWarps * kQmWarpBytes<D, G, NR> + (kQmSharedQ<D, NR> ? NR * (D / 32) * 512 : 0);
 
 template <int D, int G, int NR, bool BF16>
 __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_kernel(const QmArgs ar) {
@@ -117,8 +136,10 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
     constexpr bool SQ = kQmSharedQ<D, NR>;
     __shared__ SeqScratch sched;
     __shared__ float2 s_ml[kQmWarps][RR];
-    extern __shared__ __align__(16) float s_o[];        // [kQmWarps][RR][OS], then Q's fragments
-    uint4 *s_q = reinterpret_cast<uint4 *>(s_o + kQmWarps * RR * OS);   // [NR][NB][32]
+    extern __shared__ __align__(128) unsigned char s_mem[];   // the warps' stages (or rows of O: [RR][OS]), then Q's fragments
+    constexpr int WB = kQmWarpBytes<D, G, NR>, STG = kQmStage<D, G>;
+    uint4 *s_q = reinterpret_cast<uint4 *>(s_mem + kQmWarps * WB);      // [NR][NB][32]
+    auto s_o = [&](int w) { return reinterpret_cast<float *>(s_mem + w * WB); };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3, cta = blockIdx.x;
     pdl_wait();
     const SeqRun run = seq_schedule<kQmThreads, kQmTks, 0, kQmLeast>(a, a.max_q, cta, ar.G, &sched);
@@ -219,37 +240,58 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
             if (lane == 0 && !(a.window && key + 16 <= p.prefix - a.window + 1)) atomicOr(a.status, kSeqBadPage);
             return 0;
         };
-        // The whole block is in its page, so keys past the last one are read too, and masked like the others that
-        // a row does not see.
-        uint32_t kw[2][NB], ka[2][NG], vw[4][VW], va[2][NG];
-        const uint32_t *k_lane = cc.kc + p.kh * cc.c_sh + g * cc.c_st + t * NB, *v_lane = cc.vc + p.kh * cc.c_sh + 2 * t * cc.c_st + g * VW;
-        const uint32_t *ka_lane = static_cast<const uint32_t *>(cc.ka) + p.kh * cc.a_sh + g * cc.a_st;
-        const uint32_t *va_lane = static_cast<const uint32_t *>(cc.va) + p.kh * cc.a_sh + g * cc.a_st;
-        auto load_k = [&](int page, int key) {
-            const int in = key & ((1 << a.page_shift) - 1);
-            const uint32_t *c = k_lane + (page * cc.c_sp + in * cc.c_st), *f = ka_lane + (page * cc.a_sp + in * cc.a_st);
-            load_words<NB>(c, kw[0]);
-            load_words<NB>(c + 8 * cc.c_st, kw[1]);
-            load_words<NG>(f, ka[0]);
-            load_words<NG>(f + 8 * cc.a_st, ka[1]);
+        // Copies of a block: K's and V's rows of codes, a 16-byte vector a lane and instruction, then rows of scales and
+        // biases, K's by lanes 0 .. 15, V's by the others.  The whole block is in its page, so keys past the last
+        // one come too, and are masked like the others that a row does not see.  V's vectors stand swizzled, so that the
+        // reads below, of rows 2 t, find all banks.
+        constexpr int CPR = D / 32, ROWS = 32 / CPR;                        // vectors of a row, rows of an instruction
+        constexpr int OV = 8 * D, OA = 16 * D;                              // of V's codes, of the affine in a stage
+        auto swizzled = [](int row, int off) { return off ^ ((D == 64 ? (row >> 2) & 1 : (row >> 1) & 3) << 5); };
+        unsigned char *mine = s_mem + warp * WB;
+        const int c_row = lane / CPR;
+        const uint32_t *k_lane = cc.kc + p.kh * cc.c_sh + c_row * cc.c_st + lane % CPR * 4;
+        const uint32_t *a_lane = static_cast<const uint32_t *>(lane < 16 ? cc.ka : cc.va) + p.kh * cc.a_sh + (lane & 15) * cc.a_st;
+        const long long v_off = cc.vc - cc.kc;
+        auto copy_block = [&](int key, int page, int st) {
+            if (key < key_end) {
+                const int in = key & ((1 << a.page_shift) - 1);
+                const uint32_t *c = k_lane + (page * cc.c_sp + in * cc.c_st);
+                const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(mine + st * STG));
+#pragma unroll
+                for (int i = 0; i < CPR / 2; ++i) {
+                    const uint32_t *ci = c + i * ROWS * cc.c_st;
+                    copy_words<4>(dst + lane * 16 + 512 * i, ci);
+                    copy_words<4>(dst + OV + swizzled(c_row + i * ROWS, lane * 16 + 512 * i), ci + v_off);
+                }
+                copy_words<NG>(dst + OA + lane * (NG * 4), a_lane + (page * cc.a_sp + in * cc.a_st));
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        auto load_v = [&](int page, int key) {
-            const int in = key & ((1 << a.page_shift) - 1);
-            const uint32_t *c = v_lane + (page * cc.c_sp + in * cc.c_st), *f = va_lane + (page * cc.a_sp + in * cc.a_st);
-            load_words<VW>(c, vw[0]);
-            load_words<VW>(c + cc.c_st, vw[1]);
-            load_words<VW>(c + 8 * cc.c_st, vw[2]);
-            load_words<VW>(c + 9 * cc.c_st, vw[3]);
-            load_words<NG>(f, va[0]);
-            load_words<NG>(f + 8 * cc.a_st, va[1]);
-        };
-        int key = (p.t0 << kQmTks) + 16 * warp;
-        int page = page_of(key), next = page_of(key + 16 * kQmWarps);
-        load_k(page, key);
-        load_v(page, key);
+        int key = (p.t0 << kQmTks) + 16 * warp, ahead = key, st = 0;
+        int page = page_of(key);
+#pragma unroll 1
+        for (int i = 0; i < kQmStages - 1; ++i) {
+            const int cell = page_of(ahead + 16 * kQmWarps);
+            copy_block(ahead, page, i);
+            ahead += 16 * kQmWarps;
+            page = cell;
+        }
 #pragma unroll 1
         for (; key < key_end; key += 16 * kQmWarps) {
             // logits in log2 units: s[x][2 n + e] of key g + 8 n, row 2 t + e of tile x
+            asm volatile("cp.async.wait_group %0;" ::"n"(kQmStages - 2) : "memory");
+            __syncwarp();
+            copy_block(ahead, page, (st + kQmStages - 1) % kQmStages);     // where the block before was
+            ahead += 16 * kQmWarps;
+            page = page_of(ahead);
+            const unsigned char *blk = mine + st * STG;
+            st = (st + 1) % kQmStages;
+            uint32_t kw[2][NB], ka[2][NG], vw[4][VW], va[2][NG];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                load_words<NB>(blk + (8 * n + g) * (D / 2) + t * (NB * 4), kw[n]);
+                load_words<NG>(blk + OA + (8 * n + g) * (NG * 4), ka[n]);
+            }
             uint64_t s2[NR][2], u2[NR][2];
 #pragma unroll
             for (int x = 0; x < NR; ++x) s2[x][0] = s2[x][1] = u2[x][0] = u2[x][1] = 0;
@@ -291,8 +333,13 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
                     s[x][2 * i] = first(y);
                     s[x][2 * i + 1] = second(y);
                 }
-            const int after = page_of(key + 32 * kQmWarps);
-            load_k(next, key + 16 * kQmWarps);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const int row = 2 * t + (n & 1) + 8 * (n >> 1);
+                load_words<VW>(blk + OV + swizzled(row, row * (D / 2) + g * (VW * 4)), vw[n]);
+            }
+#pragma unroll
+            for (int n = 0; n < 2; ++n) load_words<NG>(blk + OA + (16 + 8 * n + g) * (NG * 4), va[n]);
             // bit 2 n + e: is key g + 8 n seen by row 2 t + e
             const bool masked = key < p.full_lo || key + 16 > p.full_hi;
             uint32_t see[NR];
@@ -444,9 +491,9 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
                     mma16(o[x][j][1], h0 & 0x000f000fu, h0 & 0x00f000f0u, h1 & 0x000f000fu, h1 & 0x00f000f0u, pb[x][j / BPG][0], pb[x][j / BPG][1]);
                 }
             }
-            load_v(next, key + 16 * kQmWarps);
-            next = after;
         }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncwarp();                                   // O's rows stand where the stages were
         if (tid == 0 && p.rest > 0) ar.rec[cta] = seq_record(run, cta, p);
         // ---- join the four warps
 #pragma unroll
@@ -458,7 +505,7 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
 #pragma unroll
                 for (int k = 4; k < 32; k <<= 1) y += __shfl_xor_sync(0xffffffffu, y, k);
                 if (g == 0) s_ml[warp][row] = make_float2(up[x][e] - kQmSlack, y);
-                float *dst = s_o + (warp * RR + row) * OS + 4 * g;
+                float *dst = s_o(warp) + row * OS + 4 * g;
 #pragma unroll
                 for (int n = 0; n < NG; ++n) {
                     float b = e ? second(ab[x][n]) : first(ab[x][n]);
@@ -488,8 +535,8 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
             for (int k = 0; k < kQmWarps; ++k) {
                 const float f = ex2(w[k].x - mu);
                 ls += f * w[k].y;
-                const float4 y = *reinterpret_cast<const float4 *>(s_o + (k * RR + row) * OS + d);
-                const float4 z = *reinterpret_cast<const float4 *>(s_o + (k * RR + row) * OS + d + 4);
+                const float4 y = *reinterpret_cast<const float4 *>(s_o(k) + row * OS + d);
+                const float4 z = *reinterpret_cast<const float4 *>(s_o(k) + row * OS + d + 4);
                 r[0] += f * y.x; r[1] += f * y.y; r[2] += f * y.z; r[3] += f * y.w;
                 r[4] += f * z.x; r[5] += f * z.y; r[6] += f * z.z; r[7] += f * z.w;
             }
@@ -528,9 +575,9 @@ cudaError_t qm_launch(const SeqQuantArgs &a, void *ws, int sms, cudaStream_t s) 
     ar.o = reinterpret_cast<float *>(w + sizeof(float2) * 2 * ar.G * RR);
     auto kern = seq_quant_mma_kernel<D, G, NR, BF16>;
     static unsigned long long done = 0;
-    cudaError_t e = set_smem_limit_once(kern, kQmSmem<D, NR>, &done);
+    cudaError_t e = set_smem_limit_once(kern, kQmSmem<D, G, NR>, &done);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(kern, dim3(ar.G), dim3(kQmThreads), kQmSmem<D, NR>, s, ar);
+    e = launch_pdl(kern, dim3(ar.G), dim3(kQmThreads), kQmSmem<D, G, NR>, s, ar);
     count_launch();
     if (e != cudaSuccess) return e;
     e = launch_pdl(seq_mma_merge_kernel<D, RR, BF16>, dim3(ar.G), dim3(kMergeThreads), 0, s, a.s, ar.rec, ar.ml, ar.o);
