@@ -623,8 +623,8 @@ ta_status paged_rotary_append(const ta_rotary_append_params *p, const ta_buf *q,
  *   affine  [n_pages, n_kv_heads, page_size, head_dim / group_size, 2] f16 or bf16: scale,
  *           bias
  * K and V have one set of strides: of codes in words, multiples of 4; of affine in elements,
- * multiples of 8, or of 2 head_dim / group_size where that is less; 0 = contiguous.  Both are
- * 16-byte aligned.
+ * multiples of 8, or of 2 head_dim / group_size where that is less; below 2^30; 0 = contiguous.
+ * Both are 16-byte aligned.
  */
 typedef struct {
     uint32_t tokens;

@@ -110,8 +110,8 @@ PAGES = [
     (dict(group_size=128), None, None, 1, "group_size"),
     (dict(codes_token_stride=18), None, None, 1, "codes"),
     (dict(affine_token_stride=6), None, None, 1, "affine"),
-    (dict(affine_page_stride=1 << 38), None, None, 4, "stride"),
-    (dict(n_pages=2 ** 31 - 1, codes_page_stride=2 ** 37), None, None, 3, "overflow"),
+    (dict(affine_page_stride=1 << 30), None, None, 4, "stride"),
+
     ({}, "k_codes", dict(code="TA_I32"), 1, "k_codes dtype"),
     ({}, "v_codes", dict(nbytes=5 * 16 * 2 * 64 - 1), 2, "v_codes"),
     ({}, "v_codes", dict(ptr=0x10004), 1, "aligned"),

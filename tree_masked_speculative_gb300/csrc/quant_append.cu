@@ -151,11 +151,11 @@ __global__ void __launch_bounds__(kRotThreads) quant_append_kernel(const QuantAp
     }
     const bool live = slot >= 0 && slot < static_cast<long long>(a.n_pages) << a.page_shift;
     const int h0 = static_cast<int>(hb) * HB, heads = live ? min(HB, a.Hk - h0) : 0;
-    const long long page = live ? slot >> a.page_shift : 0, in = live ? slot & ((1ll << a.page_shift) - 1) : 0;
+    const uint32_t page = live ? static_cast<uint32_t>(slot >> a.page_shift) : 0u, in = live ? static_cast<uint32_t>(slot) & ((1u << a.page_shift) - 1) : 0u;
     // where the lane's word goes: quads g and g + 1 of block i / 4, two blocks' quads a word
     const unsigned j = i >> 2, nb = static_cast<unsigned>(a.D) >> 5, g = 2 * (i & 3) + (j & 1);
-    uint32_t *codes = (is_v ? ar.c.vc : ar.c.kc) + page * ar.c.c_sp + in * ar.c.c_st + h0 * ar.c.c_sh + (g * nb + (j & ~1u)) / 2;
-    uint32_t *affine = static_cast<uint32_t *>(is_v ? ar.c.va : ar.c.ka) + page * ar.c.a_sp + in * ar.c.a_st + h0 * ar.c.a_sh + i / GL;
+    uint32_t *codes = at_bytes(at_bytes(at_bytes((is_v ? ar.c.vc : ar.c.kc) + (g * nb + (j & ~1u)) / 2, page, ar.c.c_sp), in, ar.c.c_st), h0, ar.c.c_sh);
+    uint32_t *affine = at_bytes(at_bytes(at_bytes(static_cast<uint32_t *>(is_v ? ar.c.va : ar.c.ka) + i / GL, page, ar.c.a_sp), in, ar.c.a_st), h0, ar.c.a_sh);
     const long long sh = is_v ? a.v_sh : a.k_sh;
     const uint4 *src = static_cast<const uint4 *>(is_v ? a.v_new : a.k_new) + (live ? t * (is_v ? a.v_st : a.k_st) + h0 * sh : 0);
     const unsigned half = static_cast<unsigned>(a.R) >> 4;          // vectors of half of the turned part
@@ -218,8 +218,8 @@ __global__ void __launch_bounds__(kRotThreads) quant_append_kernel(const QuantAp
         const uint32_t got = __shfl_xor_sync(0xffffffffu, send, 4);
         const uint32_t word = j & 1 ? got | (cd & 0xffff0000u) : (cd & 0xffffu) | got << 16;
         if (h < heads) {
-            codes[h * ar.c.c_sh] = word;
-            if (i % GL == 0) affine[h * ar.c.a_sh] = af;
+            *at_bytes(codes, h, ar.c.c_sh) = word;
+            if (i % GL == 0) *at_bytes(affine, h, ar.c.a_sh) = af;
         }
     }
 }
@@ -236,9 +236,9 @@ __global__ void __launch_bounds__(kRotThreads) quant_read_kernel(const QuantRead
         const bool is_v = h2 & 1;
         const long long slot = a.slot[t];
         if (slot < 0 || slot >= static_cast<long long>(a.n_pages) << a.page_shift) continue;
-        const long long page = slot >> a.page_shift, in = slot & ((1ll << a.page_shift) - 1);
-        const uint32_t c = __ldg((is_v ? a.c.vc : a.c.kc) + page * a.c.c_sp + h * a.c.c_sh + in * a.c.c_st + w);
-        const uint32_t *af = static_cast<const uint32_t *>(is_v ? a.c.va : a.c.ka) + page * a.c.a_sp + h * a.c.a_sh + in * a.c.a_st;
+        const uint32_t page = static_cast<uint32_t>(slot >> a.page_shift), in = static_cast<uint32_t>(slot) & ((1u << a.page_shift) - 1);
+        const uint32_t c = __ldg(at_bytes(at_bytes(at_bytes((is_v ? a.c.vc : a.c.kc) + w, page, a.c.c_sp), h, a.c.c_sh), in, a.c.c_st));
+        const uint32_t *af = at_bytes(at_bytes(at_bytes(static_cast<const uint32_t *>(is_v ? a.c.va : a.c.ka), page, a.c.a_sp), h, a.c.a_sh), in, a.c.a_st);
         uint16_t *out = static_cast<uint16_t *>(is_v ? a.v : a.k) + t * (is_v ? a.v_st : a.k_st) + h * (is_v ? a.v_sh : a.k_sh);
         const unsigned g = 2 * w / nb, j = 2 * w % nb;
 #pragma unroll

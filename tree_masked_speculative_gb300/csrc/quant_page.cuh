@@ -12,9 +12,15 @@ namespace ta {
 struct QuantCache {
     uint32_t *kc, *vc;                // codes
     void *ka, *va;                    // scale, bias pairs
-    long long c_sp, c_sh, c_st;       // strides of the codes, words
-    long long a_sp, a_sh, a_st;       // strides of the affine, pairs (32 bits)
+    // strides in bytes, of the codes and of the affine: below 2^32, so that an offset is one 32 x 32 -> 64 bit product
+    uint32_t c_sp, c_sh, c_st;
+    uint32_t a_sp, a_sh, a_st;
 };
+// base + i * stride
+template <typename T>
+__device__ __forceinline__ T *at_bytes(T *base, uint32_t i, uint32_t stride) {
+    return reinterpret_cast<T *>(reinterpret_cast<uintptr_t>(base) + static_cast<uint64_t>(i) * stride);
+}
 
 // New rows: q turned to q_out, k_new turned and v_new to the cache.  Row strides in 16-byte
 // vectors.

@@ -41,7 +41,7 @@ ta_status page_strides(const char *op, uint64_t hk, uint64_t ps, uint64_t d, uin
     if (s->ap % av || s->ah % av || s->at % av)
         SEQ_FAIL(TA_ERR_INVALID_ARGUMENT, "%s: strides of the affine must be multiples of %llu elements", op, static_cast<unsigned long long>(av));
     for (const uint64_t x : {s->cp, s->ch, s->ct, s->ap, s->ah, s->at})
-        if (x >= (uint64_t(1) << 38)) SEQ_FAIL(TA_ERR_UNSUPPORTED, "%s: a cache stride exceeds 2^38 elements", op);
+        if (x >= (uint64_t(1) << 30)) SEQ_FAIL(TA_ERR_UNSUPPORTED, "%s: a cache stride exceeds 2^30 elements", op);
     return TA_OK;
 }
 // Buffers of 4-bit pages.
@@ -60,12 +60,12 @@ ta_status page_buffers(const char *op, const PageStrides &s, uint64_t n_pages, u
     c->vc = static_cast<uint32_t *>(vc->ptr);
     c->ka = ka->ptr;
     c->va = va->ptr;
-    c->c_sp = static_cast<long long>(s.cp);
-    c->c_sh = static_cast<long long>(s.ch);
-    c->c_st = static_cast<long long>(s.ct);
-    c->a_sp = static_cast<long long>(s.ap / 2);
-    c->a_sh = static_cast<long long>(s.ah / 2);
-    c->a_st = static_cast<long long>(s.at / 2);
+    c->c_sp = static_cast<uint32_t>(4 * s.cp);
+    c->c_sh = static_cast<uint32_t>(4 * s.ch);
+    c->c_st = static_cast<uint32_t>(4 * s.ct);
+    c->a_sp = static_cast<uint32_t>(2 * s.ap);
+    c->a_sh = static_cast<uint32_t>(2 * s.ah);
+    c->a_st = static_cast<uint32_t>(2 * s.at);
     return TA_OK;
 }
 

@@ -71,9 +71,10 @@ __global__ void __launch_bounds__(kWarps * 32) seq_quant_fma_kernel(const SeqQua
             continue;
         }
         const int in = key & ((1 << a.page_shift) - 1);
-        const long long co = page * ar.c.c_sp + kh * ar.c.c_sh + in * ar.c.c_st, ao = page * ar.c.a_sp + kh * ar.c.a_sh + in * ar.c.a_st;
-        const uint32_t kw = lane_codes<E>(ar.c.kc + co, lane), vw = lane_codes<E>(ar.c.vc + co, lane);
-        const T *ka = static_cast<const T *>(ar.c.ka) + 2 * ao, *va = static_cast<const T *>(ar.c.va) + 2 * ao;
+        auto codes = [&](const uint32_t *c) { return lane_codes<E>(at_bytes(at_bytes(at_bytes(c, page, ar.c.c_sp), kh, ar.c.c_sh), in, ar.c.c_st), lane); };
+        auto affine = [&](const void *f) { return at_bytes(at_bytes(at_bytes(static_cast<const T *>(f), page, ar.c.a_sp), kh, ar.c.a_sh), in, ar.c.a_st); };
+        const uint32_t kw = codes(ar.c.kc), vw = codes(ar.c.vc);
+        const T *ka = affine(ar.c.ka), *va = affine(ar.c.va);
         float s = 0.0f, v[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) {

@@ -114,7 +114,7 @@ __device__ __forceinline__ float bias_of(uint32_t sb) {
 
 // NR: tiles of 8 query rows.
 template <int D, int NR>
-constexpr int kQmCtas = D == 256 ? 2 : NR == 2 ? (D == 64 ? 4 : 3) : (D == 64 ? 5 : 4);
+constexpr int kQmCtas = D == 256 ? 2 : NR == 2 ? (D == 64 ? 4 : 3) : (D == 64 ? 5 : 3);
 // Q's fragments in shared memory where registers are short.
 template <int D, int NR>
 constexpr bool kQmSharedQ = D * NR > 128;
@@ -150,8 +150,10 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
     walk.init(a, a.max_q, run, &sched, cta);
     SeqPiece p;
     while (walk.next(a, a.max_q, run, &p)) {
-        // Q fragments: of block j the elements 32 j + 8 t + {0, 4 | 1, 5 | 2, 6 | 3, 7}, the second and
-        // fourth pair over 16 (their codes come as 16 c), times 2^e: the row's largest in [2^13, 2^14)
+        // Q fragments of each two products: with G = 32 of block j the elements 32 j + 8 t + {0, 4 | 1, 5 | 2, 6 | 3, 7};
+        // with G = 64, whose two blocks' quads are the halves of a word as it is, of blocks j0 and j0 + 1 (j0 = j less its lowest
+        // bit b) the elements 8 t + 4 b + {0 | 1 | 2 | 3} of both.  The second and fourth pair are over 16 (their codes come
+        // as 16 c), all times 2^e: the row's largest in [2^13, 2^14)
         uint4 qb[SQ ? 1 : NR][SQ ? 1 : NB];
         uint64_t fr[NR], qs[NR][NG];
 #pragma unroll
@@ -186,7 +188,13 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
                 float f[8];
-                widen(raw[j].x, f); widen(raw[j].y, f + 2); widen(raw[j].z, f + 4); widen(raw[j].w, f + 6);
+                if constexpr (G == 32) {
+                    widen(raw[j].x, f); widen(raw[j].y, f + 2); widen(raw[j].z, f + 4); widen(raw[j].w, f + 6);
+                } else {
+                    const uint4 r0 = raw[j & ~1], r1 = raw[j | 1];
+                    widen(j & 1 ? r0.z : r0.x, f); widen(j & 1 ? r0.w : r0.y, f + 2);
+                    widen(j & 1 ? r1.z : r1.x, f + 4); widen(j & 1 ? r1.w : r1.y, f + 6);
+                }
                 const uint4 y = make_uint4(pack16<false>(f[0] * mul, f[4] * mul), pack16<false>(f[1] * mul16, f[5] * mul16),
                                            pack16<false>(f[2] * mul, f[6] * mul), pack16<false>(f[3] * mul16, f[7] * mul16));
                 if constexpr (SQ) {
@@ -249,21 +257,21 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
         auto swizzled = [](int row, int off) { return off ^ ((D == 64 ? (row >> 2) & 1 : (row >> 1) & 3) << 5); };
         unsigned char *mine = s_mem + warp * WB;
         const int c_row = lane / CPR;
-        const uint32_t *k_lane = cc.kc + p.kh * cc.c_sh + c_row * cc.c_st + lane % CPR * 4;
-        const uint32_t *a_lane = static_cast<const uint32_t *>(lane < 16 ? cc.ka : cc.va) + p.kh * cc.a_sh + (lane & 15) * cc.a_st;
+        const uint32_t *k_lane = at_bytes(at_bytes(cc.kc + lane % CPR * 4, p.kh, cc.c_sh), c_row, cc.c_st);
+        const uint32_t *a_lane = at_bytes(at_bytes(static_cast<const uint32_t *>(lane < 16 ? cc.ka : cc.va), p.kh, cc.a_sh), lane & 15, cc.a_st);
         const long long v_off = cc.vc - cc.kc;
         auto copy_block = [&](int key, int page, int st) {
             if (key < key_end) {
                 const int in = key & ((1 << a.page_shift) - 1);
-                const uint32_t *c = k_lane + (page * cc.c_sp + in * cc.c_st);
+                const uint32_t *c = at_bytes(at_bytes(k_lane, page, cc.c_sp), in, cc.c_st);
                 const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(mine + st * STG));
 #pragma unroll
                 for (int i = 0; i < CPR / 2; ++i) {
-                    const uint32_t *ci = c + i * ROWS * cc.c_st;
+                    const uint32_t *ci = at_bytes(c, i * ROWS, cc.c_st);
                     copy_words<4>(dst + lane * 16 + 512 * i, ci);
                     copy_words<4>(dst + OV + swizzled(c_row + i * ROWS, lane * 16 + 512 * i), ci + v_off);
                 }
-                copy_words<NG>(dst + OA + lane * (NG * 4), a_lane + (page * cc.a_sp + in * cc.a_st));
+                copy_words<NG>(dst + OA + lane * (NG * 4), at_bytes(at_bytes(a_lane, page, cc.a_sp), in, cc.a_st));
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
@@ -303,7 +311,9 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
 #pragma unroll
                 for (int j = n * BPG; j < (n + 1) * BPG; ++j) {
                     const uint32_t sel = j & 1 ? 0x7632u : 0x5410u;
-                    const uint32_t w0 = __byte_perm(kw[0][j / 2], kw[0][NB / 2 + j / 2], sel), w1 = __byte_perm(kw[1][j / 2], kw[1][NB / 2 + j / 2], sel);
+                    const int i0 = j / 2 + (j & 1 ? NB / 2 : 0);
+                    const uint32_t w0 = G == 64 ? kw[0][i0] : __byte_perm(kw[0][j / 2], kw[0][NB / 2 + j / 2], sel);
+                    const uint32_t w1 = G == 64 ? kw[1][i0] : __byte_perm(kw[1][j / 2], kw[1][NB / 2 + j / 2], sel);
                     const uint32_t h0 = w0 >> 8, h1 = w1 >> 8;
 #pragma unroll
                     for (int x = 0; x < NR; ++x) {

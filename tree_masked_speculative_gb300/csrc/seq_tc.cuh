@@ -694,8 +694,8 @@ __global__ void __launch_bounds__((CfgOf<D, SRC, G>::THREADS), 1) seq_tc_kernel(
                     kv = p.kv;
                     lo = a.window ? p.prefix + p.i0 - a.window + 1 : INT_MIN;
                     cells = a.table + static_cast<long long>(p.b) * a.max_pages;
-                    codes = (kind ? ar.qc.vc : ar.qc.kc) + p.kh * ar.qc.c_sh + lane / CPR * ar.qc.c_st + lane % CPR * 4;
-                    affine = static_cast<const uint32_t *>(kind ? ar.qc.va : ar.qc.ka) + p.kh * ar.qc.a_sh + (lane & 15) * ar.qc.a_st;
+                    codes = at_bytes(at_bytes((kind ? ar.qc.vc : ar.qc.kc) + lane % CPR * 4, p.kh, ar.qc.c_sh), lane / CPR, ar.qc.c_st);
+                    affine = at_bytes(at_bytes(static_cast<const uint32_t *>(kind ? ar.qc.va : ar.qc.ka), p.kh, ar.qc.a_sh), lane & 15, ar.qc.a_st);
                 }
                 key = ((t0 + t) << TKS) + 16 * part;
                 cell = lane < QC::ROUNDS && key + 16 * lane < kv ? __ldg(cells + ((key + 16 * lane) >> a.page_shift)) : 0;
@@ -712,12 +712,12 @@ __global__ void __launch_bounds__((CfgOf<D, SRC, G>::THREADS), 1) seq_tc_kernel(
                     }
                     // keys that do not exist have scale and bias 0: what their codes are does not matter
                     const uint32_t dst = smem_u32(raw + r * QC::RAW);
-                    const uint32_t *src = codes + (page * ar.qc.c_sp + in * ar.qc.c_st);
+                    const uint32_t *src = at_bytes(at_bytes(codes, page, ar.qc.c_sp), in, ar.qc.c_st);
 #pragma unroll
                     for (int i = 0; i < CPR / 2; ++i)
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + lane * 16 + i * 512), "l"(src + i * CROWS * ar.qc.c_st) : "memory");
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + lane * 16 + i * 512), "l"(at_bytes(src, i * CROWS, ar.qc.c_st)) : "memory");
                     if (lane < 16)
-                        copy_words<QC::NG>(dst + QC::CODES + lane * (QC::NG * 4), affine + (page * ar.qc.a_sp + in * ar.qc.a_st), live && k + lane < kv);
+                        copy_words<QC::NG>(dst + QC::CODES + lane * (QC::NG * 4), at_bytes(at_bytes(affine, page, ar.qc.a_sp), in, ar.qc.a_st), live && k + lane < kv);
                 }
                 asm volatile("cp.async.commit_group;" ::: "memory");
             };
