@@ -884,27 +884,38 @@ def paged_append_rotary(q: Optional[torch.Tensor], k_new: torch.Tensor, v_new: t
 def _quant_cache(cache, dev):
     """A PagedQuantCache as (n_pages, Hk, page_size, D, group_size, strides, ta_bufs)."""
     kc, ka, vc, va = cache
+    cs, fs = kc.shape, ka.shape
     if kc.dtype != torch.int32 or vc.dtype != torch.int32:
         raise ValueError("codes must be int32")
-    if kc.shape != vc.shape or ka.shape != va.shape:
+    if cs != vc.shape or fs != va.shape:
         raise ValueError("K and V must have one shape")
-    if kc.dim() != 4 or ka.dim() != 5 or kc.shape[:3] != ka.shape[:3] or ka.shape[4] != 2 or ka.shape[3] == 0:
+    if len(cs) != 4 or len(fs) != 5 or cs[:3] != fs[:3] or fs[4] != 2 or fs[3] == 0:
         raise ValueError("a cache is codes [n_pages, Hk, page_size, D / 8], affine [n_pages, Hk, page_size, D / group, 2]")
-    d = 8 * kc.shape[3]
-    if d % ka.shape[3]:
+    n_pages, hk, ps, words = cs
+    groups = fs[3]
+    if 8 * words % groups:
         raise ValueError("D / 8 words and D / group pairs a row do not go together")
-    bufs, strides = [], []
-    for k, v, what, code in ((kc, vc, "codes", TA_U32), (ka, va, "affine", None)):
-        if what == "affine":                     # a row's pairs stand one behind the other
-            if any(x.stride(4) != 1 or (x.shape[3] > 1 and x.stride(3) != 2) for x in (k, v)) and k.numel():
-                raise ValueError("a row's (scale, bias) pairs must be contiguous")
-            k, v = (x.flatten(3) if x.numel() else x.reshape(*x.shape[:3], -1) for x in (k, v))
-        kb, vb, s = _cache_pair(k, v, dev)
-        for b in (kb, vb):
-            bufs.append(b if code is None else (b[0], b[1], code, 0))
-        strides.append(s)
-    (kcb, vcb, kab, vab) = bufs
-    return (*kc.shape[:3], d, d // ka.shape[3], (*strides[0], *strides[1]), (*kcb, *kab, *vcb, *vab))
+    if kc.is_contiguous() and vc.is_contiguous() and ka.is_contiguous() and va.is_contiguous():
+        if not kc.get_device() == vc.get_device() == ka.get_device() == va.get_device() == dev:
+            raise ValueError("all tensors must be on cuda:%d" % dev)
+        code = _SERVE_CODE.get(ka.dtype), _SERVE_CODE.get(va.dtype)
+        if None in code:
+            raise ValueError("unsupported dtype %s" % ka.dtype)
+        rows = n_pages * hk * ps
+        nc, na = 4 * rows * words, ka.element_size() * rows * groups * 2
+        return (n_pages, hk, ps, 8 * words, 8 * words // groups, _NO_STRIDES,
+                (kc.data_ptr(), nc, TA_U32, 0, ka.data_ptr(), na, code[0], 0, vc.data_ptr(), nc, TA_U32, 0, va.data_ptr(), na,
+                 code[1], 0))
+    # a row's pairs stand one behind the other
+    if any(x.stride(4) != 1 or (groups > 1 and x.stride(3) != 2) for x in (ka, va)) and ka.numel():
+        raise ValueError("a row's (scale, bias) pairs must be contiguous")
+    kcb, vcb, c_str = _cache_pair(kc, vc, dev)
+    kab, vab, f_str = _cache_pair(*(x.flatten(3) if x.numel() else x.reshape(*fs[:3], -1) for x in (ka, va)), dev)
+    return (n_pages, hk, ps, 8 * words, 8 * words // groups, (*c_str, *f_str),
+            (kcb[0], kcb[1], TA_U32, 0, *kab, vcb[0], vcb[1], TA_U32, 0, *vab))
+
+
+_NO_STRIDES = (0,) * 6                           # contiguous
 
 
 def paged_quant_append(k_new: torch.Tensor, v_new: torch.Tensor, cache: PagedQuantCache, slot_map: torch.Tensor, *,

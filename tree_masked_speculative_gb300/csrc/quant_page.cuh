@@ -66,8 +66,8 @@ struct SeqQuantArgs {
 };
 cudaError_t launch_seq_quant_fma(const SeqQuantArgs &a, cudaStream_t s);
 
-// Warp-MMA kernel for few rows per KV head: up to 16 rows; its workspace and launch.
-constexpr int kQuantMmaRows = 16;
+// Warp-MMA kernel for few rows per KV head; its workspace and launch.
+constexpr int quant_mma_rows(int d) { return d == 256 ? 8 : 16; }
 unsigned long long seq_quant_mma_workspace64(int rows, int sms);
 unsigned long long seq_quant_mma_workspace128(int rows, int sms);
 unsigned long long seq_quant_mma_workspace256(int rows, int sms);

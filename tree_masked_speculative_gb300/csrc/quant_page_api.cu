@@ -149,7 +149,7 @@ uint64_t quant_rows(const ta_paged_quant_params *p) { return static_cast<uint64_
 // take the largest product for the largest logit, so a negative scale goes to the CUDA cores.
 int quant_family(const ta_paged_quant_params *p) {
     if (p->kernel == TA_KERNEL_CUDA_CORES || p->scale < 0.0f) return TA_KERNEL_CUDA_CORES;
-    return p->kernel != TA_KERNEL_TENSOR_CORES && quant_rows(p) <= kQuantMmaRows ? TA_KERNEL_WARP_MMA : TA_KERNEL_TENSOR_CORES;
+    return p->kernel != TA_KERNEL_TENSOR_CORES && quant_rows(p) <= static_cast<uint64_t>(quant_mma_rows(static_cast<int>(p->head_dim))) ? TA_KERNEL_WARP_MMA : TA_KERNEL_TENSOR_CORES;
 }
 
 // Workspace of a call; 0 when no device is visible to size the grid for.

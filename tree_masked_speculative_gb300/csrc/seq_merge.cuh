@@ -35,8 +35,9 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 // batch is small, so a block's threads share the pieces as well as the columns
 // (one thread a column through all of 22 pieces took 14 us).
 constexpr int kMergeThreads = 256;
-// CAP: rows of a partial slot.
-template <int D, int CAP, bool BF16>
+// CAP: rows of a partial slot.  COLS: columns a block takes (blockIdx.y), fewer than D where a few units of many pieces
+// would leave the work to a few blocks.
+template <int D, int CAP, bool BF16, int COLS = D>
 __global__ void __launch_bounds__(kMergeThreads) seq_mma_merge_kernel(const SeqArgs a, const SeqRec *recs, const float2 *ml, const float *o) {
     __shared__ float s_m[CAP], s_inv[CAP];
     __shared__ float4 s_part[kMergeThreads];
@@ -63,14 +64,14 @@ __global__ void __launch_bounds__(kMergeThreads) seq_mma_merge_kernel(const SeqA
     }
     __syncthreads();
     // items: 4 columns of a row; `share` threads take the pieces of one item in turn
-    const int items = rec.rows * (D / 4);
+    const int items = rec.rows * (COLS / 4);
     int share = 1;
     while (2 * share * items <= kMergeThreads) share *= 2;
     const int per = kMergeThreads / share;              // items at a time
     for (int i0 = 0; i0 < items; i0 += per) {
         const int k = tid / per, i = i0 + tid - k * per;
         float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        const int row = i / (D / 4), d = (i - row * (D / 4)) * 4;
+        const int row = i / (COLS / 4), d = blockIdx.y * COLS + (i - row * (COLS / 4)) * 4;
         if (i < items) {
             const float mu = s_m[row];
 #pragma unroll 4

@@ -115,25 +115,21 @@ __device__ __forceinline__ float bias_of(uint32_t sb) {
 // NR: tiles of 8 query rows.
 template <int D, int NR>
 constexpr int kQmCtas = D == 256 ? 2 : NR == 2 ? (D == 64 ? 4 : 3) : (D == 64 ? 5 : 3);
-// Q's fragments in shared memory where registers are short.
-template <int D, int NR>
-constexpr bool kQmSharedQ = D * NR > 128;
 // Blocks of 16 keys that a warp has on their way or in work, each [K codes][V codes][K affine][V affine].
-constexpr int kQmStages = 4;
+constexpr int kQmStages = 3;
 template <int D, int G>
 constexpr int kQmStage = 16 * D + 2 * 16 * (D / G) * 4;
 // A warp's stages; its rows of O at the end of a piece stand in their place.
 template <int D, int G, int NR>
 constexpr int kQmWarpBytes = kQmStages * kQmStage<D, G> > 8 * NR * (D + 4) * 4 ? kQmStages * kQmStage<D, G> : 8 * NR * (D + 4) * 4;
 template <int D, int G, int NR>
-constexpr size_t kQmSmem = kQmWarps * kQmWarpBytes<D, G, NR> + (kQmSharedQ<D, NR> ? NR * (D / 32) * 512 : 0);
+constexpr size_t kQmSmem = kQmWarps * kQmWarpBytes<D, G, NR> + NR * (D / 32) * 512;
 
 template <int D, int G, int NR, bool BF16>
 __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_kernel(const QmArgs ar) {
     const SeqArgs &a = ar.q.s;
     const QuantCache &cc = ar.q.c;
     constexpr int RR = 8 * NR, NB = D / 32, NG = D / G, BPG = G / 32, VW = NB / 2, OS = D + 4;
-    constexpr bool SQ = kQmSharedQ<D, NR>;
     __shared__ SeqScratch sched;
     __shared__ float2 s_ml[kQmWarps][RR];
     extern __shared__ __align__(128) unsigned char s_mem[];   // the warps' stages (or rows of O: [RR][OS]), then Q's fragments
@@ -154,7 +150,6 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
         // with G = 64, whose two blocks' quads are the halves of a word as it is, of blocks j0 and j0 + 1 (j0 = j less its lowest
         // bit b) the elements 8 t + 4 b + {0 | 1 | 2 | 3} of both.  The second and fourth pair are over 16 (their codes come
         // as 16 c), all times 2^e: the row's largest in [2^13, 2^14)
-        uint4 qb[SQ ? 1 : NR][SQ ? 1 : NB];
         uint64_t fr[NR], qs[NR][NG];
 #pragma unroll
         for (int x = 0; x < NR; ++x) {
@@ -197,11 +192,7 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
                 }
                 const uint4 y = make_uint4(pack16<false>(f[0] * mul, f[4] * mul), pack16<false>(f[1] * mul16, f[5] * mul16),
                                            pack16<false>(f[2] * mul, f[6] * mul), pack16<false>(f[3] * mul16, f[7] * mul16));
-                if constexpr (SQ) {
-                    if (warp == (j & 3)) s_q[(x * NB + j) * 32 + lane] = y;
-                } else {
-                    qb[x][j] = y;
-                }
+                if (warp == (j & 3)) s_q[(x * NB + j) * 32 + lane] = y;
             }
             // 2^24 / 2^e of row g, and its sums: to the lanes that hold the rows 2 t and 2 t + 1 of a product
             const float back = __uint_as_float(static_cast<uint32_t>(254 - up) << 23) * 0x1p24f * scale2;
@@ -215,7 +206,7 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
                 qs[x][n] = two(__shfl_sync(0xffffffffu, y, 8 * t), __shfl_sync(0xffffffffu, y, 8 * t + 4));
             }
         }
-        if constexpr (SQ) __syncthreads();
+        __syncthreads();
         // Of rows 2 t + e of tile x: running max, sum, sums of P b (each lane its keys'), power of two of P s
         // (mu: the running max less the raise, 0 where there is none; up: what moves it)
         float o[NR][NB][2][4], mu[NR][2], up[NR][2], l[NR][2];
@@ -317,9 +308,7 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
                     const uint32_t h0 = w0 >> 8, h1 = w1 >> 8;
 #pragma unroll
                     for (int x = 0; x < NR; ++x) {
-                        uint4 b;
-                        if constexpr (SQ) b = s_q[(x * NB + j) * 32 + lane];
-                        else b = qb[x][j];
+                        const uint4 b = s_q[(x * NB + j) * 32 + lane];
                         mma16(acc[x], w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u, b.x, b.y);
                         mma16(acc[x], h0 & 0x000f000fu, h1 & 0x000f000fu, h0 & 0x00f000f0u, h1 & 0x00f000f0u, b.z, b.w);
                     }
@@ -590,16 +579,17 @@ cudaError_t qm_launch(const SeqQuantArgs &a, void *ws, int sms, cudaStream_t s) 
     e = launch_pdl(kern, dim3(ar.G), dim3(kQmThreads), kQmSmem<D, G, NR>, s, ar);
     count_launch();
     if (e != cudaSuccess) return e;
-    e = launch_pdl(seq_mma_merge_kernel<D, RR, BF16>, dim3(ar.G), dim3(kMergeThreads), 0, s, a.s, ar.rec, ar.ml, ar.o);
+    e = launch_pdl(seq_mma_merge_kernel<D, RR, BF16, 32>, dim3(ar.G, D / 32), dim3(kMergeThreads), 0, s, a.s, ar.rec, ar.ml, ar.o);
     count_launch();
     return e;
 }
 
 template <int D, int G>
 cudaError_t qm_launch_group(const SeqQuantArgs &a, void *ws, int sms, cudaStream_t s) {
-    const bool two = a.s.max_q * a.s.g > 8;
-    if (a.s.bf16) return two ? qm_launch<D, G, 2, true>(a, ws, sms, s) : qm_launch<D, G, 1, true>(a, ws, sms, s);
-    return two ? qm_launch<D, G, 2, false>(a, ws, sms, s) : qm_launch<D, G, 1, false>(a, ws, sms, s);
+    const int rows = a.s.max_q * a.s.g;
+    if constexpr (D <= 128)
+        if (rows > 8) return a.s.bf16 ? qm_launch<D, G, 2, true>(a, ws, sms, s) : qm_launch<D, G, 2, false>(a, ws, sms, s);
+    return a.s.bf16 ? qm_launch<D, G, 1, true>(a, ws, sms, s) : qm_launch<D, G, 1, false>(a, ws, sms, s);
 }
 template <int D>
 cudaError_t qm_launch_dim(const SeqQuantArgs &a, void *ws, int sms, cudaStream_t s) {
@@ -607,7 +597,8 @@ cudaError_t qm_launch_dim(const SeqQuantArgs &a, void *ws, int sms, cudaStream_t
 }
 template <int D>
 unsigned long long qm_workspace(int rows, int sms) {
-    const unsigned long long G = static_cast<unsigned long long>(sms) * (rows > 8 ? kQmCtas<D, 2> : kQmCtas<D, 1>), cap = rows > 8 ? 16 : 8;
+    const int nr = D <= 128 && rows > 8 ? 2 : 1;
+    const unsigned long long G = static_cast<unsigned long long>(sms) * (nr == 2 ? kQmCtas<D, 2> : kQmCtas<D, 1>), cap = 8 * nr;
     return 256 + (G * sizeof(SeqRec) + 255) / 256 * 256 + 2 * G * cap * (sizeof(float2) + sizeof(float) * D);
 }
 

@@ -333,15 +333,19 @@ template <int D, int G>
 constexpr int kQuantSmem = QuantCfg<D, G>::OFF_MISC + kMiscBytes + static_cast<int>(sizeof(QuantMisc));
 static_assert(kQuantSmem<64, 32> <= 232448 && kQuantSmem<128, 32> <= 232448 && kQuantSmem<256, 32> <= 232448, "shared memory budget");
 
-// N 4-byte words to shared memory, zeros where `live` is false.
+// Copies without a branch, so that they are scheduled among the widening: 16 bytes; N 4-byte words by the threads that
+// `take` part, zeros where `live` is false.
+__device__ __forceinline__ void copy_vector(uint32_t dst, const uint32_t *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 template <int N>
-__device__ __forceinline__ void copy_words(uint32_t dst, const uint32_t *src, bool live) {
+__device__ __forceinline__ void copy_words(uint32_t dst, const uint32_t *src, bool take, bool live) {
     if constexpr (N >= 4) {
 #pragma unroll
         for (int i = 0; i < N; i += 4)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 4 * i), "l"(src + i), "r"(live ? 16 : 0) : "memory");
+            asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %3, 0;\n\t@p cp.async.cg.shared.global [%0], [%1], 16, %2;\n\t}" ::"r"(dst + 4 * i), "l"(src + i), "r"(live ? 16 : 0), "r"(static_cast<int>(take)) : "memory");
     } else {
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(4 * N), "r"(live ? 4 * N : 0) : "memory");
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %4, 0;\n\t@p cp.async.ca.shared.global [%0], [%1], %2, %3;\n\t}" ::"r"(dst), "l"(src), "n"(4 * N), "r"(live ? 4 * N : 0), "r"(static_cast<int>(take)) : "memory");
     }
 }
 
@@ -416,9 +420,9 @@ __device__ __forceinline__ void widen_round(const unsigned char *raw, unsigned c
     __syncwarp();
     behind();
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int i = 0; i < NB / 2; ++i)                    // blocks 2 i and 2 i + 1: one slab
 #pragma unroll
-        for (int i = 0; i < NB / 2; ++i) {              // blocks 2 i and 2 i + 1: one slab
+        for (int u = 0; u < U; ++u) {
             const uint32_t a = w[u][i], b = w[u][NB / 2 + i], a4 = BF16 ? a >> 4 : 0u, b4 = BF16 ? b >> 4 : 0u;
             unsigned char *dst = tile + me.at + 1024 * u + i * C::SLAB;
             const uint32_t g0 = sb[u][64 * i / G], g1 = sb[u][(64 * i + 32) / G];
@@ -672,7 +676,7 @@ __global__ void __launch_bounds__((CfgOf<D, SRC, G>::THREADS), 1) seq_tc_kernel(
             const uint32_t *codes = kind ? ar.qc.vc : ar.qc.kc, *affine = static_cast<const uint32_t *>(kind ? ar.qc.va : ar.qc.ka);
             // the warp's next tile: tile t of piece n (in own[slot]), its first key of this warp, and what its copies need;
             // lane r holds the cell of the page of round r
-            int n = -1, slot = 0, t = QC::PARTS == 1 ? me : 0, nt = 0, t0 = 0, key = 0, kv = 0, lo = 0, cell = 0;
+            int n = -1, slot = 0, t = QC::PARTS == 1 ? me : 0, nt = 0, t0 = 0, key = 0, kv = 0, lo = 0, cell = -1;
             const int32_t *cells = a.table;
             bool more = true, ok = true;
             auto advance = [&] {
@@ -686,7 +690,10 @@ __global__ void __launch_bounds__((CfgOf<D, SRC, G>::THREADS), 1) seq_tc_kernel(
                     if (lane < static_cast<int>(sizeof(SeqPiece) / 4)) reinterpret_cast<uint32_t *>(&own[slot])[lane] = reinterpret_cast<const uint32_t *>(&mi->piece[i])[lane];
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&mi->piece_empty[i]);
-                    if (!more) return;
+                    if (!more) {
+                        cell = -1;
+                        return;
+                    }
                     const SeqPiece &p = own[slot];
                     ++n;
                     nt = p.nt;
@@ -698,27 +705,28 @@ __global__ void __launch_bounds__((CfgOf<D, SRC, G>::THREADS), 1) seq_tc_kernel(
                     affine = at_bytes(at_bytes(static_cast<const uint32_t *>(kind ? ar.qc.va : ar.qc.ka), p.kh, ar.qc.a_sh), lane & 15, ar.qc.a_st);
                 }
                 key = ((t0 + t) << TKS) + 16 * part;
-                cell = lane < QC::ROUNDS && key + 16 * lane < kv ? __ldg(cells + ((key + 16 * lane) >> a.page_shift)) : 0;
-            };
-            // copies of round r of the next tile, as one group (an empty one where there is none)
-            auto issue = [&](int r) {
-                if (more) {
-                    const int k = key + 16 * r, in = k & ((1 << a.page_shift) - 1);
-                    int page = __shfl_sync(0xffffffffu, cell, r);
-                    const bool live = k < kv && static_cast<unsigned>(page) < static_cast<unsigned>(a.n_pages);
-                    if (!live) {
-                        if (k < kv && k + 16 > lo && lane == 0) atomicOr(a.status, kSeqBadPage);   // (behind the window it may be gone)
-                        page = 0;
+                // (-1: no page)
+                cell = -1;
+                const int k = key + 16 * lane;
+                if (lane < QC::ROUNDS && k < kv) {
+                    cell = __ldg(cells + (k >> a.page_shift));
+                    if (static_cast<unsigned>(cell) >= static_cast<unsigned>(a.n_pages)) {
+                        if (k + 16 > lo) atomicOr(a.status, kSeqBadPage);       // (behind the window it may be gone)
+                        cell = -1;
                     }
-                    // keys that do not exist have scale and bias 0: what their codes are does not matter
-                    const uint32_t dst = smem_u32(raw + r * QC::RAW);
-                    const uint32_t *src = at_bytes(at_bytes(codes, page, ar.qc.c_sp), in, ar.qc.c_st);
-#pragma unroll
-                    for (int i = 0; i < CPR / 2; ++i)
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + lane * 16 + i * 512), "l"(at_bytes(src, i * CROWS, ar.qc.c_st)) : "memory");
-                    if (lane < 16)
-                        copy_words<QC::NG>(dst + QC::CODES + lane * (QC::NG * 4), at_bytes(at_bytes(affine, page, ar.qc.a_sp), in, ar.qc.a_st), live && k + lane < kv);
                 }
+            };
+            // copies of round r of the next tile, as one group (behind the last one, of what is in the first page).  Keys that
+            // do not exist have scale and bias 0: what their codes are does not matter
+            auto issue = [&](int r) {
+                const int k = key + 16 * r, in = k & ((1 << a.page_shift) - 1);
+                const int page = __shfl_sync(0xffffffffu, cell, r);
+                const uint32_t dst = smem_u32(raw + r * QC::RAW);
+                const uint32_t *src = at_bytes(at_bytes(codes, max(page, 0), ar.qc.c_sp), in, ar.qc.c_st);
+#pragma unroll
+                for (int i = 0; i < CPR / 2; ++i) copy_vector(dst + lane * 16 + i * 512, at_bytes(src, i * CROWS, ar.qc.c_st));
+                copy_words<QC::NG>(dst + QC::CODES + (lane & 15) * (QC::NG * 4), at_bytes(at_bytes(affine, max(page, 0), ar.qc.a_sp), in, ar.qc.a_st),
+                                   lane < 16, page >= 0 && k + lane < kv);
                 asm volatile("cp.async.commit_group;" ::: "memory");
             };
             advance();
