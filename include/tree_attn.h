@@ -661,8 +661,7 @@ ta_status paged_quant_append(const ta_quant_append_params *p, const ta_buf *q, c
 /*
  * Rows of 4-bit pages as 16-bit values (scale * code + bias in f32, rounded once): row t of k
  * and v ([tokens, n_kv_heads, head_dim] with the k_ and v_ strides) from slot slot_map[t].  Slots
- * may repeat; rows whose slot is outside the cache stay as they were.  n_heads and rotary_dim must
- * be 0.
+ * may repeat; rows whose slot is outside the cache are 0.  n_heads and rotary_dim must be 0.
  */
 ta_status paged_quant_read(const ta_quant_append_params *p, const ta_buf *slot_map, const ta_buf *k_codes,
                            const ta_buf *k_affine, const ta_buf *v_codes, const ta_buf *v_affine,

@@ -940,7 +940,7 @@ def paged_quant_append(k_new: torch.Tensor, v_new: torch.Tensor, cache: PagedQua
 def paged_quant_read(cache: PagedQuantCache, slot_map: torch.Tensor, *, out=None, stream=None):
     """The rows of slots slot_map [T] (int64) of a 4-bit cache as 16-bit (k, v), each
     [T, Hk, D] in the type of its scales (`out`: the two tensors to write into).  Rows whose
-    slot is outside the cache are not written (zero without an `out`)."""
+    slot is outside the cache are 0."""
     dev = _device_of(cache[0])
     if stream is not None or dev != _this_device():
         return _elsewhere(paged_quant_read, dev, stream, (cache, slot_map), dict(out=out))
@@ -949,7 +949,7 @@ def paged_quant_read(cache: PagedQuantCache, slot_map: torch.Tensor, *, out=None
         raise ValueError("slot_map must be [T]")
     t = slot_map.shape[0]
     if out is None:
-        out = tuple(torch.zeros(t, hk, d, dtype=cache[1].dtype, device=cache[1].device) for _ in range(2))
+        out = tuple(torch.empty(t, hk, d, dtype=cache[1].dtype, device=cache[1].device) for _ in range(2))
     k, v = out
     if tuple(k.shape) != (t, hk, d) or k.shape != v.shape:
         raise ValueError("out must be two tensors [%d, %d, %d]" % (t, hk, d))

@@ -32,15 +32,40 @@ __device__ __forceinline__ float round16(float x) {
     else return __half2float(__float2half_rn(x));
 }
 
+// Two f32 at a time.
+__device__ __forceinline__ uint64_t two(float x, float y) {
+    return static_cast<uint64_t>(__float_as_uint(x)) | (static_cast<uint64_t>(__float_as_uint(y)) << 32);
+}
+__device__ __forceinline__ float first(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x)); }
+__device__ __forceinline__ float second(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x >> 32)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+// x - y
+__device__ __forceinline__ uint64_t sub2(uint64_t x, uint64_t y) { return fma2(y, two(-1.0f, -1.0f), x); }
+
 // x c + y s as hi + lo: hi the nearest f32, lo what is left (relative error about 2^-47).
-__device__ __forceinline__ void turn_exact(float x, float c, float y, float s, float *hi, float *lo) {
-    const float p = __fmul_rn(x, c), pe = __fmaf_rn(x, c, -p);
-    const float q = __fmul_rn(y, s), qe = __fmaf_rn(y, s, -q);
-    const float z = __fadd_rn(p, q), b = __fadd_rn(z, -p);
-    const float e = __fadd_rn(__fadd_rn(p, -__fadd_rn(z, -b)), __fadd_rn(q, -b));
-    const float l = __fadd_rn(e, __fadd_rn(pe, qe));
-    *hi = __fadd_rn(z, l);
-    *lo = __fadd_rn(l, -__fadd_rn(*hi, -z));
+__device__ __forceinline__ void turn_exact(uint64_t x, uint64_t c, uint64_t y, uint64_t s, uint64_t *hi, uint64_t *lo) {
+    const uint64_t minus = two(-1.0f, -1.0f);
+    const uint64_t p = mul2(x, c), pe = fma2(mul2(x, minus), c, p);        // pe, qe: the products' errors, negated
+    const uint64_t q = mul2(y, s), qe = fma2(mul2(y, minus), s, q);
+    const uint64_t z = add2(p, q), b = sub2(z, p);
+    const uint64_t e = add2(sub2(p, sub2(z, b)), sub2(q, b));
+    const uint64_t l = sub2(e, add2(pe, qe));
+    *hi = add2(z, l);
+    *lo = sub2(l, sub2(*hi, z));
 }
 
 // A quotient next to k + 1/2: which of k and k + 1 is nearer to (hi + lo - bias) / scale.
@@ -65,31 +90,33 @@ __device__ __noinline__ float near_border(float hi, float lo, float bias, float 
 // Codes of a lane's 8 elements (4 bits each, lowest first) and their group's scale and bias as
 // 16-bit halves of *affine.  The GL lanes of a group call it together, the warp's others too.
 template <bool BF16, int GL, bool EXACT>
-__device__ __forceinline__ uint32_t quantise(const float (&hi)[8], const float (&lo)[8], uint32_t *affine) {
-    float mx = hi[0], mn = hi[0];
+__device__ __forceinline__ uint32_t quantise(const uint64_t (&hi)[4], const uint64_t (&lo)[4], uint32_t *affine) {
+    float mx = first(hi[0]), mn = mx;
 #pragma unroll
-    for (int e = 1; e < 8; ++e) {
-        mx = max_nan(mx, hi[e]);
-        mn = min_nan(mn, hi[e]);
+    for (int e = 0; e < 4; ++e) {
+        mx = max_nan(mx, max_nan(first(hi[e]), second(hi[e])));
+        mn = min_nan(mn, min_nan(first(hi[e]), second(hi[e])));
     }
 #pragma unroll
     for (int o = 1; o < GL; o <<= 1) {
         mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
         mn = min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, o));
     }
-    const float range = __fadd_rn(mx, -mn), r = __fmul_rn(range, 1.0f / 15.0f);
-    uint32_t sb = bits16<BF16>(r);
+    const float range = __fadd_rn(mx, -mn), r = __fmul_rn(range, 1.0f / 15.0f), big = fmaxf(fabsf(mx), fabsf(mn));
     // does a relative error of 2^-20 move the 16-bit scale (r is off by 2^-22, and by what is left of the
     // extremes, at most 2^-24 of each)
-    const bool unsure = bits16<BF16>(r * (1.0f - 0x1p-20f)) != bits16<BF16>(r * (1.0f + 0x1p-20f)) || !(range <= FLT_MAX) ||
-                        (EXACT && fmaxf(fabsf(mx), fabsf(mn)) > 4.0f * range);
+    const uint32_t both = narrow2<BF16>(r * (1.0f - 0x1p-20f), r * (1.0f + 0x1p-20f));
+    uint32_t sb = both & 0xffffu;
+    const bool unsure = sb != both >> 16 || !(range <= FLT_MAX) || (EXACT && big > 4.0f * range);
     if (__any_sync(0xffffffffu, unsure)) {
         float lx = -INFINITY, ln = INFINITY;            // what is left of the largest and the least
         if constexpr (EXACT) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if (hi[e] == mx) lx = fmaxf(lx, lo[e]);
-                if (hi[e] == mn) ln = fminf(ln, lo[e]);
+            for (int e = 0; e < 4; ++e) {
+                if (first(hi[e]) == mx) lx = fmaxf(lx, first(lo[e]));
+                if (second(hi[e]) == mx) lx = fmaxf(lx, second(lo[e]));
+                if (first(hi[e]) == mn) ln = fminf(ln, first(lo[e]));
+                if (second(hi[e]) == mn) ln = fminf(ln, second(lo[e]));
             }
 #pragma unroll
             for (int o = 1; o < GL; o <<= 1) {
@@ -102,27 +129,50 @@ __device__ __forceinline__ uint32_t quantise(const float (&hi)[8], const float (
         if (unsure)
             sb = bits16<BF16>(static_cast<float>(((static_cast<double>(mx) + lx) - (static_cast<double>(mn) + ln)) / 15.0));
     }
-    const float bias = round16<BF16>(mn), scale = BF16 ? __uint_as_float(sb << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(sb)));
+    const uint32_t bb = bits16<BF16>(mn);
+    const float bias = BF16 ? __uint_as_float(bb << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(bb)));
+    const float scale = BF16 ? __uint_as_float(sb << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(sb)));
     // (a NaN fails every comparison)
-    if (!(fabsf(mx) <= FLT_MAX && fabsf(mn) <= FLT_MAX && fabsf(bias) <= FLT_MAX && scale <= FLT_MAX)) {
-        *affine = 0x7fff7fffu;                          // NaN in either type
-        return 0u;
-    }
-    *affine = sb | bits16<BF16>(mn) << 16;
-    const float inv = scale > 0.0f ? __frcp_rn(scale) : 0.0f;
-    // v below is off by 2^-23 |v| from three roundings, and by lo / scale
-    float thr = 0.5f - 1e-5f;
-    if constexpr (EXACT) thr -= fmaxf(fabsf(mx), fabsf(mn)) * 0x1p-23f * inv;
-    if (scale < 0x1p-100f || !(range <= FLT_MAX)) thr = -1.0f;   // the reciprocal or a difference may be out of range
-    uint32_t codes = 0u;
+    const bool bad = !(fabsf(mx) <= FLT_MAX && fabsf(mn) <= FLT_MAX && fabsf(bias) <= FLT_MAX && scale <= FLT_MAX);
+    *affine = bad ? 0x7fff7fffu : sb | bb << 16;        // (NaN in either type)
+    const float inv = scale > 0.0f && !bad ? __frcp_rn(scale) : 0.0f;
+    // The quotients as x / scale - bias / scale, clamped, rounded by adding 1.5 2^23, packed by exact products.  They are
+    // off by 2^-22 of the larger term and by lo / scale at most; where one is next to a border between two
+    // codes, the 8 of them are looked at one by one.
+    const float shift = -bias * inv;
+    const uint64_t iv = two(inv, inv), sh = two(shift, shift), magic = two(12582912.0f, 12582912.0f), less = two(-12582912.0f, -12582912.0f);
+    float dev = 0.0f, quad[2];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float v = __fmul_rn(__fadd_rn(hi[e], -bias), inv);
-        float n = __fadd_rn(__fadd_rn(v, 12582912.0f), -12582912.0f);   // 1.5 2^23: rounds to nearest even
-        if (!(fabsf(v - n) <= thr)) n = scale > 0.0f ? near_border(hi[e], EXACT ? lo[e] : 0.0f, bias, scale, v, thr) : 0.0f;
-        codes |= static_cast<uint32_t>(fminf(fmaxf(n, 0.0f), 15.0f)) << (4 * e);
+    for (int w = 0; w < 2; ++w) {
+        float n[4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const uint64_t v = fma2(hi[2 * w + e], iv, sh);
+            const uint64_t c = two(fminf(fmaxf(first(v), 0.0f), 15.0f), fminf(fmaxf(second(v), 0.0f), 15.0f));
+            const uint64_t k = add2(add2(c, magic), less), d = sub2(c, k);
+            asm("max.f32 %0, %0, %1, %2;" : "+f"(dev) : "f"(fabsf(first(d))), "f"(fabsf(second(d))));
+            n[2 * e] = first(k);
+            n[2 * e + 1] = second(k);
+        }
+        quad[w] = fmaf(fmaf(fmaf(n[3], 16.0f, n[2]), 16.0f, n[1]), 16.0f, n[0]);
     }
-    return codes;
+    uint32_t codes = static_cast<uint32_t>(quad[0]) | static_cast<uint32_t>(quad[1]) << 16;
+    float thr = 0.5f - 4e-6f - big * inv * 0x1p-21f;
+    if (scale < 0x1p-100f || !(range <= FLT_MAX)) thr = -1.0f;   // the reciprocal or a difference may be out of range
+    if (!(dev <= thr)) {
+        codes = 0u;
+        if (scale > 0.0f && !bad) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float h = e & 1 ? second(hi[e >> 1]) : first(hi[e >> 1]), l = !EXACT ? 0.0f : e & 1 ? second(lo[e >> 1]) : first(lo[e >> 1]);
+                const float v = __fmul_rn(__fadd_rn(h, -bias), inv);
+                float k = rintf(v);
+                if (!(fabsf(v - k) <= thr)) k = near_border(h, l, bias, scale, v, thr);
+                codes |= static_cast<uint32_t>(fminf(fmaxf(k, 0.0f), 15.0f)) << (4 * e);
+            }
+        }
+    }
+    return bad ? 0u : codes;
 }
 
 // Blocks [0, nq) turn queries, [nq, nq + nk) take keys, the others values.
@@ -137,7 +187,7 @@ __global__ void __launch_bounds__(kRotThreads) quant_append_kernel(const QuantAp
     const bool is_v = blockIdx.x >= nq + nk;
     const long long x = static_cast<long long>(blockIdx.x - (is_v ? nq + nk : nq)) * kRotThreads + threadIdx.x;
     const unsigned cols = static_cast<unsigned>(a.D) >> 3, blocks = (static_cast<unsigned>(a.Hk) + HB - 1) / HB;
-    const long long t = x / (cols * blocks);
+    const long long t = item_token(x, cols * blocks);
     const unsigned r = static_cast<unsigned>(x - t * (cols * blocks)), hb = r / cols, i = r - hb * cols;
     // all lanes stay for the shuffles; a row's lanes agree
     const float *row = nullptr;
@@ -160,8 +210,8 @@ __global__ void __launch_bounds__(kRotThreads) quant_append_kernel(const QuantAp
     const uint4 *src = static_cast<const uint4 *>(is_v ? a.v_new : a.k_new) + (live ? t * (is_v ? a.v_st : a.k_st) + h0 * sh : 0);
     const unsigned half = static_cast<unsigned>(a.R) >> 4;          // vectors of half of the turned part
     const bool turned = !is_v && a.pos && i < 2 * half;
-    const bool second = !a.interleaved && i >= half;
-    const unsigned other = a.interleaved ? i : second ? i - half : i + half;
+    const bool second_half = !a.interleaved && i >= half;
+    const unsigned other = a.interleaved ? i : second_half ? i - half : i + half;
     uint4 u[HB], w[HB];
 #pragma unroll
     for (int h = 0; h < HB; ++h) {
@@ -171,45 +221,53 @@ __global__ void __launch_bounds__(kRotThreads) quant_append_kernel(const QuantAp
             if (turned && !a.interleaved) w[h] = src[h * sh + other];
         }
     }
-    float cs[8], sn[8];
+    uint64_t cs[4], sn[4];
     if (turned && live) {
         if (a.interleaved) {                            // 4 pairs
             const float4 c = __ldg(reinterpret_cast<const float4 *>(row) + i), s = __ldg(reinterpret_cast<const float4 *>(row + (a.R >> 1)) + i);
             const float c4[4] = {c.x, c.y, c.z, c.w}, s4[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                cs[e] = c4[e >> 1];
-                sn[e] = e & 1 ? s4[e >> 1] : -s4[e >> 1];
+            for (int e = 0; e < 4; ++e) {
+                cs[e] = two(c4[e], c4[e]);
+                sn[e] = two(-s4[e], s4[e]);
             }
         } else {
-            const unsigned c = second ? i - half : i;
-            load8(row + 8 * c, cs);
-            load8(row + (a.R >> 1) + 8 * c, sn);
+            const unsigned c = second_half ? i - half : i;
+            float c8[8], s8[8];
+            load8(row + 8 * c, c8);
+            load8(row + (a.R >> 1) + 8 * c, s8);
+            const float sign = second_half ? 1.0f : -1.0f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sn[e] = second ? sn[e] : -sn[e];
+            for (int e = 0; e < 4; ++e) {
+                cs[e] = two(c8[2 * e], c8[2 * e + 1]);
+                sn[e] = two(sign * s8[2 * e], sign * s8[2 * e + 1]);
+            }
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            cs[e] = 1.0f;
-            sn[e] = 0.0f;
+        for (int e = 0; e < 4; ++e) {
+            cs[e] = two(1.0f, 1.0f);
+            sn[e] = 0;
         }
     }
 #pragma unroll
     for (int h = 0; h < HB; ++h) {
-        float x8[8], y8[8], lo[8] = {};
+        float x8[8], y8[8];
+        uint64_t hi[4], lo[4] = {};
         widen8<BF16>(u[h], x8);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) hi[e] = two(x8[2 * e], x8[2 * e + 1]);
         uint32_t af, cd;
         if (is_v || !a.pos) {                           // uniform over the block
-            cd = quantise<BF16, GL, false>(x8, lo, &af);
+            cd = quantise<BF16, GL, false>(hi, lo, &af);
         } else {
             widen8<BF16>(w[h], y8);
-            float hi[8];
+            if (turned) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float y = a.interleaved ? x8[e ^ 1] : y8[e];
-                if (turned) turn_exact(x8[e], cs[e], y, sn[e], &hi[e], &lo[e]);
-                else hi[e] = x8[e];
+                for (int e = 0; e < 4; ++e) {
+                    const uint64_t y = a.interleaved ? two(x8[2 * e + 1], x8[2 * e]) : two(y8[2 * e], y8[2 * e + 1]);
+                    turn_exact(hi[e], cs[e], y, sn[e], &hi[e], &lo[e]);
+                }
             }
             cd = quantise<BF16, GL, true>(hi, lo, &af);
         }
@@ -231,16 +289,19 @@ __global__ void __launch_bounds__(kRotThreads) quant_read_kernel(const QuantRead
     const unsigned words = static_cast<unsigned>(a.D) >> 3, per = 2 * words * a.Hk, nb = static_cast<unsigned>(a.D) >> 5;
     const long long n = static_cast<long long>(a.T) * per;
     for (long long x = static_cast<long long>(blockIdx.x) * kRotThreads + threadIdx.x; x < n; x += static_cast<long long>(gridDim.x) * kRotThreads) {
-        const long long t = x / per;
+        const long long t = item_token(x, per);
         const unsigned r = static_cast<unsigned>(x - t * per), h2 = r / words, w = r - h2 * words, h = h2 >> 1;
         const bool is_v = h2 & 1;
         const long long slot = a.slot[t];
-        if (slot < 0 || slot >= static_cast<long long>(a.n_pages) << a.page_shift) continue;
+        uint16_t *out = static_cast<uint16_t *>(is_v ? a.v : a.k) + t * (is_v ? a.v_st : a.k_st) + h * (is_v ? a.v_sh : a.k_sh);
+        const unsigned g = 2 * w / nb, j = 2 * w % nb;
+        if (slot < 0 || slot >= static_cast<long long>(a.n_pages) << a.page_shift) {
+            for (unsigned q = 0; q < 2; ++q) *reinterpret_cast<uint2 *>(out + 32 * (j + q) + 4 * g) = make_uint2(0, 0);
+            continue;
+        }
         const uint32_t page = static_cast<uint32_t>(slot >> a.page_shift), in = static_cast<uint32_t>(slot) & ((1u << a.page_shift) - 1);
         const uint32_t c = __ldg(at_bytes(at_bytes(at_bytes((is_v ? a.c.vc : a.c.kc) + w, page, a.c.c_sp), h, a.c.c_sh), in, a.c.c_st));
         const uint32_t *af = at_bytes(at_bytes(at_bytes(static_cast<const uint32_t *>(is_v ? a.c.va : a.c.ka), page, a.c.a_sp), h, a.c.a_sh), in, a.c.a_st);
-        uint16_t *out = static_cast<uint16_t *>(is_v ? a.v : a.k) + t * (is_v ? a.v_st : a.k_st) + h * (is_v ? a.v_sh : a.k_sh);
-        const unsigned g = 2 * w / nb, j = 2 * w % nb;
 #pragma unroll
         for (unsigned q = 0; q < 2; ++q) {
             const unsigned d = 32 * (j + q) + 4 * g;

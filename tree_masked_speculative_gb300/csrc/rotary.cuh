@@ -40,6 +40,11 @@ __device__ __forceinline__ void load8(const float *p, float (&f)[8]) {
     f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
 }
 
+// x / per; most calls are small enough for a 32-bit quotient (a 64-bit one takes about a hundred instructions).
+__device__ __forceinline__ long long item_token(long long x, unsigned per) {
+    return x <= 0xffffffffll ? static_cast<long long>(static_cast<uint32_t>(x) / per) : x / per;
+}
+
 // Where row t goes: its table row (nullptr: position outside the table).
 __device__ __forceinline__ const float *rot_row(const RotaryArgs &a, int t) {
     const int p = __ldg(a.pos + t);
@@ -111,7 +116,7 @@ __device__ __forceinline__ void turn_rows(const RotaryArgs &a, const float *row,
 template <bool BF16, int HB>
 __device__ __forceinline__ void turn_queries(const RotaryArgs &a, long long x) {
     const unsigned cols = static_cast<unsigned>(a.D) >> 4, blocks = (static_cast<unsigned>(a.H) + HB - 1) / HB;
-    const long long t = x / (cols * blocks);
+    const long long t = item_token(x, cols * blocks);
     if (t >= a.T) return;
     const unsigned r = static_cast<unsigned>(x - t * (cols * blocks)), hb = r / cols, c = r - hb * cols;
     const float *row = rot_row(a, static_cast<int>(t));

@@ -22,7 +22,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_append_kernel(const Rotary
     const bool is_v = blockIdx.x >= nq + nk;
     const long long x = static_cast<long long>(blockIdx.x - (is_v ? nq + nk : nq)) * kRotThreads + threadIdx.x;
     const unsigned cols = static_cast<unsigned>(a.D) >> 4, blocks = (static_cast<unsigned>(a.Hk) + HB - 1) / HB;
-    const long long t = x / (cols * blocks);
+    const long long t = item_token(x, cols * blocks);
     if (t >= a.T) return;
     const unsigned r = static_cast<unsigned>(x - t * (cols * blocks)), hb = r / cols, c = r - hb * cols;
     const float *row = rot_row(a, static_cast<int>(t));
