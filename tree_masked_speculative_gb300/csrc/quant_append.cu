@@ -177,7 +177,7 @@ __device__ __forceinline__ uint32_t quantise(const uint64_t (&hi)[4], const uint
 
 // Blocks [0, nq) turn queries, [nq, nq + nk) take keys, the others values.
 template <bool BF16, int HB, int GL>
-__global__ void __launch_bounds__(kRotThreads) quant_append_kernel(const QuantAppendArgs ar, unsigned nq, unsigned nk) {
+__global__ void __launch_bounds__(kRotThreads, 3) quant_append_kernel(const QuantAppendArgs ar, unsigned nq, unsigned nk) {
     pdl_wait();
     const RotaryArgs &a = ar.r;
     if (blockIdx.x < nq) {
