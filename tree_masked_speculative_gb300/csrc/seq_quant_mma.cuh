@@ -115,13 +115,17 @@ __device__ __forceinline__ float bias_of(uint32_t sb) {
 // NR: tiles of 8 query rows.
 template <int D, int NR>
 constexpr int kQmCtas = D == 256 ? 2 : NR == 2 ? (D == 64 ? 4 : 3) : (D == 64 ? 5 : 3);
-// Blocks of 16 keys that a warp has on their way or in work, each [K codes][V codes][K affine][V affine].
+// Blocks of 16 keys that a warp takes at a time: two where registers allow, for work that does not wait for one another.
+template <int D, int NR>
+constexpr int kQmBlocks = D * NR <= 128 ? 2 : 1;
+// Sets of blocks that a warp has on their way or in work, each block [K codes][V codes][K affine][V affine].
 constexpr int kQmStages = 3;
 template <int D, int G>
 constexpr int kQmStage = 16 * D + 2 * 16 * (D / G) * 4;
 // A warp's stages; its rows of O at the end of a piece stand in their place.
 template <int D, int G, int NR>
-constexpr int kQmWarpBytes = kQmStages * kQmStage<D, G> > 8 * NR * (D + 4) * 4 ? kQmStages * kQmStage<D, G> : 8 * NR * (D + 4) * 4;
+constexpr int kQmWarpBytes = kQmStages * kQmBlocks<D, NR> * kQmStage<D, G> > 8 * NR * (D + 4) * 4 ? kQmStages * kQmBlocks<D, NR> * kQmStage<D, G>
+                                                                                               : 8 * NR * (D + 4) * 4;
 template <int D, int G, int NR>
 constexpr size_t kQmSmem = kQmWarps * kQmWarpBytes<D, G, NR> + NR * (D / 32) * 512;
 
@@ -132,8 +136,9 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
     constexpr int RR = 8 * NR, NB = D / 32, NG = D / G, BPG = G / 32, VW = NB / 2, OS = D + 4;
     __shared__ SeqScratch sched;
     __shared__ float2 s_ml[kQmWarps][RR];
+    __shared__ __align__(8) float s_qs[NR * NG][8];
     extern __shared__ __align__(128) unsigned char s_mem[];   // the warps' stages (or rows of O: [RR][OS]), then Q's fragments
-    constexpr int WB = kQmWarpBytes<D, G, NR>, STG = kQmStage<D, G>;
+    constexpr int WB = kQmWarpBytes<D, G, NR>, STG = kQmStage<D, G>, BL = kQmBlocks<D, NR>, STEP = 16 * kQmWarps;
     uint4 *s_q = reinterpret_cast<uint4 *>(s_mem + kQmWarps * WB);      // [NR][NB][32]
     auto s_o = [&](int w) { return reinterpret_cast<float *>(s_mem + w * WB); };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3, cta = blockIdx.x;
@@ -150,7 +155,7 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
         // with G = 64, whose two blocks' quads are the halves of a word as it is, of blocks j0 and j0 + 1 (j0 = j less its lowest
         // bit b) the elements 8 t + 4 b + {0 | 1 | 2 | 3} of both.  The second and fourth pair are over 16 (their codes come
         // as 16 c), all times 2^e: the row's largest in [2^13, 2^14)
-        uint64_t fr[NR], qs[NR][NG];
+        uint64_t fr[NR];
 #pragma unroll
         for (int x = 0; x < NR; ++x) {
             const int row = g + 8 * x, tok = row / a.g;
@@ -203,19 +208,18 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
                 y += __shfl_xor_sync(0xffffffffu, y, 1);
                 y += __shfl_xor_sync(0xffffffffu, y, 2);
                 y *= scale2;
-                qs[x][n] = two(__shfl_sync(0xffffffffu, y, 8 * t), __shfl_sync(0xffffffffu, y, 8 * t + 4));
+                if (t == 0 && warp == 0) s_qs[x * NG + n][g] = y;
             }
         }
         __syncthreads();
         // Of rows 2 t + e of tile x: running max, sum, sums of P b (each lane its keys'), power of two of P s
         // (mu: the running max less the raise, 0 where there is none; up: what moves it)
-        float o[NR][NB][2][4], mu[NR][2], up[NR][2], l[NR][2];
+        float o[NR][NB][2][4], up[NR][2], l[NR][2];
         uint64_t ab[NR][NG], sc[NR][NG];
 #pragma unroll
         for (int x = 0; x < NR; ++x)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                mu[x][e] = 0.0f;
                 up[x][e] = -INFINITY;
                 l[x][e] = 0.0f;
 #pragma unroll
@@ -251,46 +255,57 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
         const uint32_t *k_lane = at_bytes(at_bytes(cc.kc + lane % CPR * 4, p.kh, cc.c_sh), c_row, cc.c_st);
         const uint32_t *a_lane = at_bytes(at_bytes(static_cast<const uint32_t *>(lane < 16 ? cc.ka : cc.va), p.kh, cc.a_sh), lane & 15, cc.a_st);
         const long long v_off = cc.vc - cc.kc;
-        auto copy_block = [&](int key, int page, int st) {
-            if (key < key_end) {
-                const int in = key & ((1 << a.page_shift) - 1);
-                const uint32_t *c = at_bytes(at_bytes(k_lane, page, cc.c_sp), in, cc.c_st);
-                const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(mine + st * STG));
+        // (as one group) of the blocks at `key` and, where BL = 2, 64 keys on
+        auto copy_blocks = [&](int key, const int (&page)[BL], int st) {
 #pragma unroll
-                for (int i = 0; i < CPR / 2; ++i) {
-                    const uint32_t *ci = at_bytes(c, i * ROWS, cc.c_st);
-                    copy_words<4>(dst + lane * 16 + 512 * i, ci);
-                    copy_words<4>(dst + OV + swizzled(c_row + i * ROWS, lane * 16 + 512 * i), ci + v_off);
+            for (int b = 0; b < BL; ++b)
+                if (key + b * STEP < key_end) {
+                    const int in = (key + b * STEP) & ((1 << a.page_shift) - 1);
+                    const uint32_t *c = at_bytes(at_bytes(k_lane, page[b], cc.c_sp), in, cc.c_st);
+                    const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(mine + (st * BL + b) * STG));
+#pragma unroll
+                    for (int i = 0; i < CPR / 2; ++i) {
+                        const uint32_t *ci = at_bytes(c, i * ROWS, cc.c_st);
+                        copy_words<4>(dst + lane * 16 + 512 * i, ci);
+                        copy_words<4>(dst + OV + swizzled(c_row + i * ROWS, lane * 16 + 512 * i), ci + v_off);
+                    }
+                    copy_words<NG>(dst + OA + lane * (NG * 4), at_bytes(at_bytes(a_lane, page[b], cc.a_sp), in, cc.a_st));
                 }
-                copy_words<NG>(dst + OA + lane * (NG * 4), at_bytes(at_bytes(a_lane, page, cc.a_sp), in, cc.a_st));
-            }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        int key = (p.t0 << kQmTks) + 16 * warp, ahead = key, st = 0;
-        int page = page_of(key);
+        int key = (p.t0 << kQmTks) + 16 * warp, ahead = key, st = 0, page[BL];
+#pragma unroll
+        for (int b = 0; b < BL; ++b) page[b] = page_of(key + b * STEP);
 #pragma unroll 1
         for (int i = 0; i < kQmStages - 1; ++i) {
-            const int cell = page_of(ahead + 16 * kQmWarps);
-            copy_block(ahead, page, i);
-            ahead += 16 * kQmWarps;
-            page = cell;
+            int cell[BL];
+#pragma unroll
+            for (int b = 0; b < BL; ++b) cell[b] = page_of(ahead + (BL + b) * STEP);
+            copy_blocks(ahead, page, i);
+            ahead += BL * STEP;
+#pragma unroll
+            for (int b = 0; b < BL; ++b) page[b] = cell[b];
         }
 #pragma unroll 1
-        for (; key < key_end; key += 16 * kQmWarps) {
-            // logits in log2 units: s[x][2 n + e] of key g + 8 n, row 2 t + e of tile x
+        for (; key < key_end; key += BL * STEP) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kQmStages - 2) : "memory");
             __syncwarp();
-            copy_block(ahead, page, (st + kQmStages - 1) % kQmStages);     // where the block before was
-            ahead += 16 * kQmWarps;
-            page = page_of(ahead);
-            const unsigned char *blk = mine + st * STG;
-            st = (st + 1) % kQmStages;
-            uint32_t kw[2][NB], ka[2][NG], vw[4][VW], va[2][NG];
+            copy_blocks(ahead, page, (st + kQmStages - 1) % kQmStages);    // where the blocks before were
+            ahead += BL * STEP;
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                load_words<NB>(blk + (8 * n + g) * (D / 2) + t * (NB * 4), kw[n]);
-                load_words<NG>(blk + OA + (8 * n + g) * (NG * 4), ka[n]);
-            }
+            for (int b = 0; b < BL; ++b) page[b] = page_of(ahead + b * STEP);
+            const unsigned char *blk = mine + st * BL * STG;
+            st = (st + 1) % kQmStages;
+            // logits in log2 units: s[b][x][2 n + e] of key g + 8 n of block b, row 2 t + e of tile x
+            float s[BL][NR][4];
+#pragma unroll
+            for (int b = 0; b < BL; ++b) {
+                uint32_t kw[2][NB], ka[2][NG];
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    load_words<NB>(blk + b * STG + (8 * n + g) * (D / 2) + t * (NB * 4), kw[n]);
+                    load_words<NG>(blk + b * STG + OA + (8 * n + g) * (NG * 4), ka[n]);
+                }
             uint64_t s2[NR][2], u2[NR][2];
 #pragma unroll
             for (int x = 0; x < NR; ++x) s2[x][0] = s2[x][1] = u2[x][0] = u2[x][1] = 0;
@@ -319,66 +334,72 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
 #pragma unroll
                     for (int x = 0; x < NR; ++x) {
                         s2[x][i] = fma_two(two(sk, sk), two(acc[x][2 * i], acc[x][2 * i + 1]), s2[x][i]);
-                        u2[x][i] = fma_two(two(bk, bk), qs[x][n], u2[x][i]);
+                        u2[x][i] = fma_two(two(bk, bk), *reinterpret_cast<const uint64_t *>(&s_qs[x * NG + n][2 * t]), u2[x][i]);
                     }
                 }
             }
-            float s[NR][4];
 #pragma unroll
             for (int x = 0; x < NR; ++x)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const uint64_t y = fma_two(s2[x][i], fr[x], u2[x][i]);
-                    s[x][2 * i] = first(y);
-                    s[x][2 * i + 1] = second(y);
+                    s[b][x][2 * i] = first(y);
+                    s[b][x][2 * i + 1] = second(y);
                 }
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                const int row = 2 * t + (n & 1) + 8 * (n >> 1);
-                load_words<VW>(blk + OV + swizzled(row, row * (D / 2) + g * (VW * 4)), vw[n]);
             }
+            // bit 2 n + e: is key g + 8 n of block b seen by row 2 t + e
+            const int last = key + (BL - 1) * STEP;
+            const bool masked = key < p.full_lo || last + 16 > p.full_hi || last >= key_end;
+            uint32_t see[BL][NR];
 #pragma unroll
-            for (int n = 0; n < 2; ++n) load_words<NG>(blk + OA + (16 + 8 * n + g) * (NG * 4), va[n]);
-            // bit 2 n + e: is key g + 8 n seen by row 2 t + e
-            const bool masked = key < p.full_lo || key + 16 > p.full_hi;
-            uint32_t see[NR];
+            for (int b = 0; b < BL; ++b)
 #pragma unroll
-            for (int x = 0; x < NR; ++x) see[x] = 15u;
+                for (int x = 0; x < NR; ++x) see[b][x] = 15u;
             if (masked) {
 #pragma unroll
                 for (int x = 0; x < NR; ++x) {
-                    see[x] = 0u;
+#pragma unroll
+                    for (int b = 0; b < BL; ++b) see[b][x] = 0u;
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int row = 8 * x + 2 * t + e, tok = row / a.g;
                         const bool live = row < p.rows;
                         uint32_t anc[kMaxTreeBitsNodes / 32] = {}, w[1];
                         if (a.parents && live) seq_ancestors(a.parents + p.q0, tok, anc);
-                        seq_visible<1>(a, p.prefix, live ? p.kv : 0, tok, anc, key, w);
-                        see[x] |= ((w[0] >> g) & 1u) << e | ((w[0] >> (g + 8)) & 1u) << (2 + e);
+#pragma unroll
+                        for (int b = 0; b < BL; ++b) {
+                            seq_visible<1>(a, p.prefix, live && key + b * STEP < key_end ? p.kv : 0, tok, anc, key + b * STEP, w);
+                            see[b][x] |= ((w[0] >> g) & 1u) << e | ((w[0] >> (g + 8)) & 1u) << (2 + e);
+                        }
                     }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (!((see[x] >> i) & 1u)) s[x][i] = -INFINITY;
+                    for (int b = 0; b < BL; ++b)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (!((see[b][x] >> i) & 1u)) s[b][x][i] = -INFINITY;
                 }
             }
             bool rise = false;
 #pragma unroll
             for (int x = 0; x < NR; ++x)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) rise |= fmaxf(s[x][e], s[x][2 + e]) > up[x][e];
+                for (int e = 0; e < 2; ++e) {
+                    float mx = fmaxf(s[0][x][e], s[0][x][2 + e]);
+                    if (BL == 2) mx = fmaxf(mx, fmaxf(s[BL - 1][x][e], s[BL - 1][x][2 + e]));
+                    rise |= mx > up[x][e];
+                }
             if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
                 for (int x = 0; x < NR; ++x)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float mx = fmaxf(s[x][e], s[x][2 + e]);
+                        float mx = fmaxf(s[0][x][e], s[0][x][2 + e]);
+                        if (BL == 2) mx = fmaxf(mx, fmaxf(s[BL - 1][x][e], s[BL - 1][x][2 + e]));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
                         if (mx > up[x][e]) {
-                            const float f = up[x][e] == -INFINITY ? 0.0f : ex2(mu[x][e] + kQmRaise - mx);
-                            mu[x][e] = mx - kQmRaise;
+                            const float f = up[x][e] == -INFINITY ? 0.0f : ex2(up[x][e] - kQmSlack - mx);
                             up[x][e] = mx + kQmSlack;
                             l[x][e] *= f;
 #pragma unroll
@@ -393,45 +414,60 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
                         }
                     }
             }
-            uint64_t pr[NR][2];
+            uint64_t pr[BL][NR][2];
 #pragma unroll
             for (int x = 0; x < NR; ++x) {
-                float y[4];
+                float mu[2];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) y[i] = ex2(s[x][i] - mu[x][i & 1]);
-                l[x][0] += y[0] + y[2];
-                l[x][1] += y[1] + y[3];
-                pr[x][0] = two(y[0], y[1]);
-                pr[x][1] = two(y[2], y[3]);
+                for (int e = 0; e < 2; ++e) mu[e] = up[x][e] == -INFINITY ? 0.0f : up[x][e] - (kQmSlack + kQmRaise);
+#pragma unroll
+                for (int b = 0; b < BL; ++b) {
+                    float y[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) y[i] = ex2(s[b][x][i] - mu[i & 1]);
+                    l[x][0] += y[0] + y[2];
+                    l[x][1] += y[1] + y[3];
+                    pr[b][x][0] = two(y[0], y[1]);
+                    pr[b][x][1] = two(y[2], y[3]);
+                }
             }
+            uint32_t va[BL][2][NG];
+#pragma unroll
+            for (int b = 0; b < BL; ++b)
+#pragma unroll
+                for (int n = 0; n < 2; ++n) load_words<NG>(blk + b * STG + OA + (16 + 8 * n + g) * (NG * 4), va[b][n]);
             // P s and the sums of P b; where a row does not see a key its scale and bias do not count
-            uint64_t ps[NR][NG][2];
+            uint64_t ps[BL][NR][NG][2];
             float most = 0.0f;
             if (!masked) {
 #pragma unroll
-                for (int n = 0; n < NG; ++n)
+                for (int b = 0; b < BL; ++b)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float sv = scale_of<BF16>(va[i][n]), bv = bias_of<BF16>(va[i][n]);
+                    for (int n = 0; n < NG; ++n)
 #pragma unroll
-                        for (int x = 0; x < NR; ++x) {
-                            ps[x][n][i] = mul_two(mul_two(pr[x][i], sc[x][n]), two(sv, sv));
-                            ab[x][n] = fma_two(pr[x][i], two(bv, bv), ab[x][n]);
-                            most = max_abs3(most, first(ps[x][n][i]), second(ps[x][n][i]));
+                        for (int i = 0; i < 2; ++i) {
+                            const float sv = scale_of<BF16>(va[b][i][n]), bv = bias_of<BF16>(va[b][i][n]);
+#pragma unroll
+                            for (int x = 0; x < NR; ++x) {
+                                ps[b][x][n][i] = mul_two(mul_two(pr[b][x][i], sc[x][n]), two(sv, sv));
+                                ab[x][n] = fma_two(pr[b][x][i], two(bv, bv), ab[x][n]);
+                                most = max_abs3(most, first(ps[b][x][n][i]), second(ps[b][x][n][i]));
+                            }
                         }
-                    }
             } else {
 #pragma unroll
-                for (int n = 0; n < NG; ++n)
+                for (int b = 0; b < BL; ++b)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
+                    for (int n = 0; n < NG; ++n)
 #pragma unroll
-                        for (int x = 0; x < NR; ++x) {
-                            const uint32_t w0 = (see[x] >> (2 * i)) & 1u ? va[i][n] : 0u, w1 = (see[x] >> (2 * i + 1)) & 1u ? va[i][n] : 0u;
-                            ps[x][n][i] = mul_two(mul_two(pr[x][i], sc[x][n]), two(scale_of<BF16>(w0), scale_of<BF16>(w1)));
-                            ab[x][n] = fma_two(pr[x][i], two(bias_of<BF16>(w0), bias_of<BF16>(w1)), ab[x][n]);
-                            most = max_abs3(most, first(ps[x][n][i]), second(ps[x][n][i]));
-                        }
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int x = 0; x < NR; ++x) {
+                                const uint32_t w0 = (see[b][x] >> (2 * i)) & 1u ? va[b][i][n] : 0u, w1 = (see[b][x] >> (2 * i + 1)) & 1u ? va[b][i][n] : 0u;
+                                ps[b][x][n][i] = mul_two(mul_two(pr[b][x][i], sc[x][n]), two(scale_of<BF16>(w0), scale_of<BF16>(w1)));
+                                ab[x][n] = fma_two(pr[b][x][i], two(bias_of<BF16>(w0), bias_of<BF16>(w1)), ab[x][n]);
+                                most = max_abs3(most, first(ps[b][x][n][i]), second(ps[b][x][n][i]));
+                            }
             }
             if (__any_sync(0xffffffffu, most > 40000.0f)) {
                 // a row and group whose P s leaves f16's range: its power of two so that the largest finite scale
@@ -443,10 +479,15 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             auto part = [&](uint64_t y) { return e ? second(y) : first(y); };
-                            const float v0 = (see[x] >> e) & 1u ? scale_of<BF16>(va[0][n]) : 0.0f;
-                            const float v1 = (see[x] >> (2 + e)) & 1u ? scale_of<BF16>(va[1][n]) : 0.0f;
-                            float top = fmaxf(fabsf(v0) <= FLT_MAX ? fabsf(v0) : 0.0f, fabsf(v1) <= FLT_MAX ? fabsf(v1) : 0.0f);
-                            float hit = fmaxf(fabsf(part(ps[x][n][0])), fabsf(part(ps[x][n][1])));
+                            float v[BL][2], top = 0.0f, hit = 0.0f;
+#pragma unroll
+                            for (int b = 0; b < BL; ++b)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    v[b][i] = (see[b][x] >> (2 * i + e)) & 1u ? scale_of<BF16>(va[b][i][n]) : 0.0f;
+                                    top = fmaxf(top, fabsf(v[b][i]) <= FLT_MAX ? fabsf(v[b][i]) : 0.0f);
+                                    hit = fmaxf(hit, fabsf(part(ps[b][x][n][i])));
+                                }
 #pragma unroll
                             for (int k = 4; k < 32; k <<= 1) {
                                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
@@ -465,29 +506,41 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
                                             o[x][j][h][2 + e] *= f;
                                         }
                                 }
-                                const float y0 = part(pr[x][0]) * now * v0, y1 = part(pr[x][1]) * now * v1;
-                                ps[x][n][0] = e ? two(first(ps[x][n][0]), y0) : two(y0, second(ps[x][n][0]));
-                                ps[x][n][1] = e ? two(first(ps[x][n][1]), y1) : two(y1, second(ps[x][n][1]));
+#pragma unroll
+                                for (int b = 0; b < BL; ++b)
+#pragma unroll
+                                    for (int i = 0; i < 2; ++i) {
+                                        const float y = part(pr[b][x][i]) * now * v[b][i];
+                                        ps[b][x][n][i] = e ? two(first(ps[b][x][n][i]), y) : two(y, second(ps[b][x][n][i]));
+                                    }
                             }
                         }
             }
-            uint32_t pb[NR][NG][2];
-#pragma unroll
-            for (int x = 0; x < NR; ++x)
-#pragma unroll
-                for (int n = 0; n < NG; ++n)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) pb[x][n][i] = transpose8(pack16<false>(first(ps[x][n][i]), second(ps[x][n][i])));
             // O += V^T (P s): elements 32 j + 4 g + 2 h (+ 1) of 16 rows of the product, 8 query rows
 #pragma unroll
-            for (int j = 0; j < NB; ++j) {
-                const uint32_t sel = j & 1 ? 0x7632u : 0x5410u;
-                const uint32_t w0 = __byte_perm(vw[0][j / 2], vw[1][j / 2], sel), w1 = __byte_perm(vw[2][j / 2], vw[3][j / 2], sel);
-                const uint32_t h0 = w0 >> 8, h1 = w1 >> 8;
+            for (int b = 0; b < BL; ++b) {
+                uint32_t pb[NR][NG][2], vw[4][VW];
 #pragma unroll
-                for (int x = 0; x < NR; ++x) {
-                    mma16(o[x][j][0], w0 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x000f000fu, w1 & 0x00f000f0u, pb[x][j / BPG][0], pb[x][j / BPG][1]);
-                    mma16(o[x][j][1], h0 & 0x000f000fu, h0 & 0x00f000f0u, h1 & 0x000f000fu, h1 & 0x00f000f0u, pb[x][j / BPG][0], pb[x][j / BPG][1]);
+                for (int n = 0; n < 4; ++n) {
+                    const int row = 2 * t + (n & 1) + 8 * (n >> 1);
+                    load_words<VW>(blk + b * STG + OV + swizzled(row, row * (D / 2) + g * (VW * 4)), vw[n]);
+                }
+#pragma unroll
+                for (int x = 0; x < NR; ++x)
+#pragma unroll
+                    for (int n = 0; n < NG; ++n)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) pb[x][n][i] = transpose8(pack16<false>(first(ps[b][x][n][i]), second(ps[b][x][n][i])));
+#pragma unroll
+                for (int j = 0; j < NB; ++j) {
+                    const uint32_t sel = j & 1 ? 0x7632u : 0x5410u;
+                    const uint32_t w0 = __byte_perm(vw[0][j / 2], vw[1][j / 2], sel), w1 = __byte_perm(vw[2][j / 2], vw[3][j / 2], sel);
+                    const uint32_t h0 = w0 >> 8, h1 = w1 >> 8;
+#pragma unroll
+                    for (int x = 0; x < NR; ++x) {
+                        mma16(o[x][j][0], w0 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x000f000fu, w1 & 0x00f000f0u, pb[x][j / BPG][0], pb[x][j / BPG][1]);
+                        mma16(o[x][j][1], h0 & 0x000f000fu, h0 & 0x00f000f0u, h1 & 0x000f000fu, h1 & 0x00f000f0u, pb[x][j / BPG][0], pb[x][j / BPG][1]);
+                    }
                 }
             }
         }
