@@ -28,6 +28,9 @@ namespace {
 constexpr int kQmWarps = 4, kQmThreads = kQmWarps * 32;
 constexpr int kQmTks = 6;                           // schedule granularity: 64 keys, 16 a warp
 constexpr int kQmLeast = 3;                         // tiles of a CTA's run at least
+// A unit's start and end (Q, the first copies, the join) in tiles' worth of time.  0, 4, 6, 8 and 12: 156, 154, 152, 153 and
+// 154 us for 64 requests of 900 to 16384 keys, 99, 88, 88, 88 and 88 us for 96 of up to 2000 keys with 16 KV heads.
+constexpr int kQmUnitCost = 6;
 constexpr float kQmLog2e = 1.4426950408889634f;
 // The running max moves when a row's max exceeds it by more than 2^8; P and l are held 2^7 higher
 // (P <= 2^15): a weight is subnormal only below 2^-21 of the running max's.
@@ -143,11 +146,11 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
     auto s_o = [&](int w) { return reinterpret_cast<float *>(s_mem + w * WB); };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3, cta = blockIdx.x;
     pdl_wait();
-    const SeqRun run = seq_schedule<kQmThreads, kQmTks, 0, kQmLeast>(a, a.max_q, cta, ar.G, &sched);
+    const SeqRun run = seq_schedule<kQmThreads, kQmTks, kQmUnitCost, kQmLeast>(a, a.max_q, cta, ar.G, &sched);
     pdl_launch_dependents();
     if (tid == 0) ar.rec[cta] = {0, 0, 0, 0};
     const float scale2 = fmaxf(a.scale * kQmLog2e, FLT_MIN);   // above 0: a masked -inf stays -inf
-    SeqWalk<kQmTks, 0> walk;
+    SeqWalk<kQmTks, kQmUnitCost> walk;
     walk.init(a, a.max_q, run, &sched, cta);
     SeqPiece p;
     while (walk.next(a, a.max_q, run, &p)) {
