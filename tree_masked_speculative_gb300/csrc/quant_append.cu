@@ -8,7 +8,10 @@
 // taken again in 64 bits.
 //
 // It reads 4 D and writes D + 8 D / G bytes a KV head and token (HBM); a lane takes 8
-// neighbouring elements of up to HB heads, a group's 4 or 8 lanes reduce by shuffles.
+// neighbouring elements of up to HB heads, a group's 4 or 8 lanes reduce by shuffles.  Latency of
+// the loads and the instructions of exact codes bound it (half of the issue slots, half of HBM).
+// Measured: 16381 tokens, 32 / 8 heads of 128, f16, groups of 32: append 90 us (40 of K and V alone, not
+// turned), read 34 us, which together have 454 MB to move (68 us); 48 tokens: 2.8 and 1.7 us.
 #include "rotary.cuh"
 
 namespace ta {
@@ -175,7 +178,8 @@ __device__ __forceinline__ uint32_t quantise(const uint64_t (&hi)[4], const uint
     return bad ? 0u : codes;
 }
 
-// Blocks [0, nq) turn queries, [nq, nq + nk) take keys, the others values.
+// Blocks [0, nq) turn queries, [nq, nq + nk) take keys, the others values.  Three blocks an SM (90 us for the tokens above)
+// leave more registers than four (105) and more warps than two (104); HB = 4 heads a thread: 1 and 2 took 135, 8 took 161.
 template <bool BF16, int HB, int GL>
 __global__ void __launch_bounds__(kRotThreads, 3) quant_append_kernel(const QuantAppendArgs ar, unsigned nq, unsigned nk) {
     pdl_wait();

@@ -66,7 +66,20 @@ struct SeqQuantArgs {
 };
 cudaError_t launch_seq_quant_fma(const SeqQuantArgs &a, cudaStream_t s);
 
-// Warp-MMA kernel for few rows per KV head; its workspace and launch.
+// Warp-MMA kernel for few rows (max_q_len * heads per KV head); its workspace and launch.  More rows would be
+// products it has no registers for, or keys widened twice.  Replayed graphs, us, warp MMA / tcgen05 (bf16, 32 / 8
+// heads; D = 256 with half the requests):
+//                                      4 rows       8 rows      16 rows     32 rows (warp MMA with four row tiles)
+//   64 of 900 to 16384 keys, D 128 G 64  159 / 483  161 / 484   252 / 484   483 / 484
+//                            D 128 G 32  191 / 478  192 / 479   326 / 479  1027 / 480
+//                            D  64 G 32  127 / 379  127 / 381   187 / 381   358 / 382
+//                            D 256 G 64   89 / 180   91 / 180   149 / 179
+//                            D 256 G 32  109 / 185  111 / 185   307 / 185
+//   16 of 300 to 9000 keys,  D 128 G 64   28 / 69    29 / 69     46 / 70     95 / 70
+//   1 of 4000 keys,          D 128 G 64   11 / 29    12 / 29     17 / 29     28 / 30
+//   200 of 300 keys,         D 128 G 64   39 / 98    41 / 98     68 / 99    153 / 102
+//                            D 256 G 32   38 / 38    40 / 39     98 / 38
+// (D = 256 with 16 rows: 41 / 38 for 8 of 300 to 9000 keys, 22 / 41 for one of 4000.)
 constexpr int quant_mma_rows(int d) { return d == 256 ? 8 : 16; }
 unsigned long long seq_quant_mma_workspace64(int rows, int sms);
 unsigned long long seq_quant_mma_workspace128(int rows, int sms);

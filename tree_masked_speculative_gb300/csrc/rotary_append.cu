@@ -5,6 +5,8 @@
 // It moves 4 D bytes a query head and 8 D a KV head and token, so HBM bounds it; a thread takes
 // the two vectors of a column that belong together, of up to HB heads, so that a cosine and sine
 // (4 bytes each against 2 of an element) are loaded once for them and 2 HB loads are in flight.
+// Measured: 16381 tokens, 24 / 4 heads of 256, half of each turned (545 MB): 80 us, 6.8 TB/s; 64 tokens, 32 / 8 heads of
+// 128: 2.2 us.
 #include "rotary.cuh"
 
 namespace ta {
@@ -64,7 +66,7 @@ cudaError_t launch(const RotaryAppendArgs &a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_rotary_append(const RotaryAppendArgs &a, cudaStream_t s) {
-    // one head a thread while that leaves the GPU's thread slots unfilled
+    // one head a thread while that leaves the GPU's thread slots unfilled (more loads of the table, but all of them at once)
     const bool few = static_cast<long long>(a.r.T) * (a.r.H + 2 * a.r.Hk) * (a.r.D / 16) <= 152ll * 2048;
     if (a.r.bf16) return few ? launch<true, 1>(a, s) : launch<true, 4>(a, s);
     return few ? launch<false, 1>(a, s) : launch<false, 4>(a, s);

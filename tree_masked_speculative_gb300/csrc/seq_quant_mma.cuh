@@ -14,9 +14,16 @@
 // row and group that, like the running max, moves only when a block needs it.
 // A lane's words: for K the quads 2 t and 2 t + 1 of every 32-element block of keys g and
 // g + 8, for V quad g of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9 - one vector a key and
-// product.  A warp takes every fourth block of 16 keys of its CTA's run, copied to shared memory three
-// blocks ahead (cp.async; no barrier inside the key loop); the batch is cut evenly over the CTAs by the
-// schedule of seq_sched.cuh.
+// product.  A warp takes every fourth block of 16 keys of its CTA's run, one or two blocks at a time, copied to
+// shared memory two such sets ahead (cp.async; no barrier inside the key loop); the batch is cut evenly over the
+// CTAs by the schedule of seq_sched.cuh.
+// Measured: one token of 64 requests of 900 to 16384 keys, 32 / 8 heads of 128, groups of 64 (668 MB): 152 us, 4.4
+// TB/s; a key costs as at 6 TB/s, the rest is about 14 us of start, first copies, join and merge and CTAs that end
+// unevenly.  131001 keys of 4 heads of 256, groups of 32 (168 MB): 50 us; 96 requests with a window of
+// 2000 keys, 16 / 16 heads of 64, groups of 32 (216 MB): 87 us, 2.5 TB/s, half of the products' rows empty.
+// The same 64 requests took 253 us with codes straight from global memory into registers and a row an instruction, 198 with two
+// rows an instruction, 179 through shared memory, 167 with 32-bit strides, 160 with copies without branches, 156 with two blocks
+// at a time, 152 with the unit cost below.
 #pragma once
 
 #include "quant_page.cuh"
@@ -115,7 +122,8 @@ __device__ __forceinline__ float bias_of(uint32_t sb) {
     else return __half2float(__ushort_as_half(static_cast<unsigned short>(sb >> 16)));
 }
 
-// NR: tiles of 8 query rows.
+// NR: tiles of 8 query rows.  CTAs an SM: as many as leave few registers in memory.  (Spilled are 72 to 416 bytes a thread with
+// D = 128 and NR = 2 and up to 440 with D = 64, none with D = 256.)
 template <int D, int NR>
 constexpr int kQmCtas = D == 256 ? 2 : NR == 2 ? (D == 64 ? 4 : 3) : (D == 64 ? 5 : 3);
 // Blocks of 16 keys that a warp takes at a time: two where registers allow, for work that does not wait for one another.

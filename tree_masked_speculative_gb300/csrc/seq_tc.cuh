@@ -304,9 +304,13 @@ __device__ __forceinline__ uint32_t max_abs(uint32_t acc, uint32_t w) {
 // D <= 128 three warps take every third K tile each, three others every third V tile; for D = 256 four share
 // every K tile, four every V tile, 16 keys each.  A slot of the rings belongs to the same warps always, who so see
 // each of a barrier's phases: a wait tells phases apart by parity alone.
-// Chunks of twelve requests (us): 524 with a third of every tile by each of three warps, 391 with tiles in turn, 344 with six
-// warps, all fed by warp 0 (TMA), which needed 2100 cycles a tile.  One rolled loop serves K and V and holds little code: with
-// loops of their own, unrolled, the instruction cache missed and they took 1046.
+// Chunks of twelve requests (1 to 512 tokens over up to 8192 keys, 32 / 8 heads of 128; us): 524 with a third of every tile
+// by each of three warps, 391 with tiles in turn, 344 with six warps, all fed by warp 0 (TMA), which needed 2100 cycles a tile,
+// 314 (908 TFLOP/s) with copies of their own.  One rolled loop serves K and V and holds little code: with loops of their own,
+// unrolled, the instruction cache missed and they took 1046.  Two chunks of 1000 to 2047 tokens, window 1500, 24 / 4 heads
+// of 256: 190; trees of 32 nodes of eight requests, the same heads: 51.  Issue slots and shared memory, which the
+// widening shares with the softmax and the products' operands, bound it: over 16-bit pages, where TMA brings the tiles, the same
+// chunks take 243.
 template <int D, int G>
 struct QuantCfg : Cfg<D> {
     using B = Cfg<D>;
