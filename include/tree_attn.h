@@ -370,8 +370,10 @@ ta_status quant_sdpa_fwd_tree(const ta_quant_params *p, uint32_t q_l, const ta_b
  * (pages, tables and slots from the requests' lengths), paged_kv_append (the
  * new tokens' K/V rows into their pages, per layer) and paged_attn_fwd (the new
  * tokens' attention over the pages, per layer); prompt_attn_fwd is the attention
- * of whole prompts before anything of them is cached.  The pages of the
- * sources have no counterpart of these calls.
+ * of whole prompts before anything of them is cached.  paged_rotary_append takes the
+ * place of paged_kv_append where keys and queries are turned by their positions;
+ * paged_quant_append and paged_quant_attn_fwd are the two on a cache of 4-bit pages.
+ * The pages of the sources have no counterpart of these calls.
  *
  * Common to them:
  *   - Rows are packed: the new tokens of request b are rows cu[b] .. cu[b+1]-1
@@ -694,6 +696,10 @@ size_t paged_quant_attn_workspace_bytes(const ta_paged_quant_params *p);
 /*
  * paged_attn_fwd over 4-bit pages: the same rows, masks, status bits and rules, with k_j and v_j
  * the values that the pages stand for.  q and out are of the type of the scales.
+ * Kernels: up to 16 rows (max_q_len * n_heads / n_kv_heads; 8 with head_dim 256) warp-level MMAs,
+ * which take the codes as they are; more rows, or TA_KERNEL_TENSOR_CORES, the tcgen05 kernel, for
+ * which each element is rounded to the 16-bit type (one beyond the type's range is infinite there, as it
+ * is for paged_quant_read); TA_KERNEL_CUDA_CORES or a negative scale the CUDA cores.
  */
 ta_status paged_quant_attn_fwd(const ta_paged_quant_params *p, const ta_buf *q, const ta_buf *k_codes,
                                const ta_buf *k_affine, const ta_buf *v_codes, const ta_buf *v_affine,
@@ -778,6 +784,13 @@ ta_status ta_test_paged_attn_fwd_wait_limit(uint32_t wait_polls, const ta_paged_
                                             const ta_buf *k_cache, const ta_buf *v_cache, const ta_buf *table,
                                             const ta_buf *cu, const ta_buf *kv_lens, const ta_buf *parents,
                                             const ta_buf *tmp, const ta_buf *out, void *stream);
+
+/* The same for paged_quant_attn_fwd. */
+ta_status ta_test_paged_quant_attn_fwd_wait_limit(uint32_t wait_polls, const ta_paged_quant_params *p, const ta_buf *q,
+                                                  const ta_buf *k_codes, const ta_buf *k_affine, const ta_buf *v_codes,
+                                                  const ta_buf *v_affine, const ta_buf *table, const ta_buf *cu,
+                                                  const ta_buf *kv_lens, const ta_buf *parents, const ta_buf *tmp,
+                                                  const ta_buf *out, void *stream);
 
 #ifdef __cplusplus
 }

@@ -545,3 +545,164 @@ def test_a_serving_run(ta, d, h, hk, ps, group, dtype, inter):
             if new[b]:
                 ref, tol = reference(qr[s], rows[b], vals[b], mags[b], visible(new[b], have[b]), d ** -0.5, torch.finfo(dt).eps / 2)
                 check(out[s], ref, tol)
+
+
+# ------------------------------------------------------------------ calls as others make them
+@pytest.mark.parametrize("kernel", FAMILIES)
+@pytest.mark.parametrize("h,d", [(24, 64), (56, 128), (128, 128), (5, 256), (128, 256)])
+def test_many_heads_of_one_kv_head(ta, h, d, kernel):
+    """Units of one or a few tokens, rows that do not divide by the heads."""
+    c = QuantPaged(ta, [150, 64, 9], [1, 5, 9], h, 1, d, 32, 32, torch.float16, seed=h, tree=True)
+    c.check(c.run(ta, kernel=kernel))
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_requests_that_share_pages(ta, new):
+    """A common prefix: both requests' tables name the same pages."""
+    c = QuantPaged(ta, [320, 330], [new, new], 8, 2, 128, 32, 64, torch.bfloat16, seed=18)
+    c.table[1, :8] = c.table[0, :8]
+    for rows in (c.keys, c.vals, c.mags):
+        rows[1][:256] = rows[0][:256]
+    c.check(c.run(ta))
+
+
+@pytest.mark.parametrize("new", [1, 5, 90])
+def test_two_streams_at_once(ta, new):
+    cs = [QuantPaged(ta, [2000, 77 + new, 300], [new] * 3, 8, 2, 128, 16, 64, torch.bfloat16, seed=19 + i) for i in range(2)]
+    want = [c.run(ta, out=torch.zeros_like(c.q)) for c in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    tmps = [ta.paged_quant_attention_workspace(c.q, c.cache, c.table, max_q_len=new) for c in cs]
+    rows, lens = [i32(c.cu) for c in cs], [i32(c.lens) for c in cs]
+    got = [[torch.zeros_like(c.q) for c in cs] for _ in range(20)]
+    torch.cuda.synchronize()
+    for pair in got:
+        for i, c in enumerate(cs):
+            ta.paged_quant_attention(c.q, c.cache, c.table, rows[i], lens[i], scale=c.scale, max_q_len=new, tmp=tmps[i],
+                                     out=pair[i], stream=streams[i])
+    torch.cuda.synchronize()
+    for pair in got:
+        assert all(torch.equal(x, y) for x, y in zip(pair, want))
+    assert not any(int(tmp.view(torch.int32)[0]) for tmp in tmps)
+
+
+@pytest.mark.parametrize("kernel", FAMILIES)
+@pytest.mark.parametrize("new", [4, 70])
+def test_parents_outside_their_node_end_the_chain(ta, new, kernel):
+    """Itself, a later node, a value past every node or far below: each is the end of the chain."""
+    c = QuantPaged(ta, [300, 90], [new, new], 8, 2, 64, 32, 32, torch.bfloat16, seed=29, tree=True)
+    for odd in (lambda i: i, lambda i: i + 1, lambda i: 2 ** 31 - 1, lambda i: -2 ** 31, lambda i: new):
+        c.parents = [[odd(i) if i % 3 == 0 else i - 1 for i in range(new)] for _ in c.new]
+        c.check(c.run(ta, kernel=kernel))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("new", [1, 3, 40])
+def test_a_workspace_serves_other_batches(ta, d, new):
+    """The tmp of one request takes the calls of twenty, and the other way round."""
+    one, many = (QuantPaged(ta, [90 + 7 * i for i in range(b)], [new] * b, 4, 2, d, 16, 64, torch.bfloat16, seed=30 + b)
+                 for b in (1, 20))
+    tmps = [ta.paged_quant_attention_workspace(c.q, c.cache, c.table, max_q_len=new) for c in (one, many)]
+    for c in (one, many):
+        for tmp in tmps:
+            c.check(c.run(ta, tmp=tmp))
+            assert int(tmp.view(torch.int32)[0]) == 0
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_two_graphs_on_one_workspace(ta, new):
+    """Replayed one after the other, in either order, with the workspace filled in between but for its status."""
+    cs = [QuantPaged(ta, [2000, 77 + new], [new] * 2, 8, 2, 128, 16, 32, torch.float16, seed=50 + i) for i in range(2)]
+    want = [c.run(ta, out=torch.zeros_like(c.q)) for c in cs]
+    tmp = ta.paged_quant_attention_workspace(cs[0].q, cs[0].cache, cs[0].table, max_q_len=new)
+    rows, lens, outs, graphs = [i32(c.cu) for c in cs], [i32(c.lens) for c in cs], [torch.zeros_like(c.q) for c in cs], []
+    for i, c in enumerate(cs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            ta.paged_quant_attention(c.q, c.cache, c.table, rows[i], lens[i], scale=c.scale, max_q_len=new, tmp=tmp, out=outs[i])
+    for order in ((0, 1), (1, 0), (0, 0), (1, 1)):
+        for o in outs:
+            o.zero_()
+        tmp[64:].fill_(float("nan"))
+        for i in order:
+            graphs[i].replay()
+        for i in set(order):
+            assert torch.equal(outs[i], want[i])
+    assert int(tmp.view(torch.int32)[0]) == 0
+
+
+def test_appends_and_reads_in_graphs_and_on_streams(ta):
+    """Captured and replayed with other rows, slots and positions; on another stream than the current one."""
+    g, t, h, hk, d, ps = gen(77), 37, 8, 2, 128, 16
+    rotary = ta.rotary_table(500, d)
+    q, k, v = (randn(g, t, n, d, dtype=torch.bfloat16) for n in (h, hk, hk))
+    slot, pos = slots_of(g, t, 6 * ps), torch.randint(-1, 510, (t,), generator=g, device="cuda", dtype=torch.int32)
+
+    def fresh():
+        return ([torch.zeros(6, hk, ps, d, dtype=torch.bfloat16, device="cuda") for _ in "kv"],
+                ta.paged_quant_cache(6, hk, ps, d, group_size=32), [torch.zeros_like(q) for _ in range(2)],
+                [torch.zeros_like(k) for _ in range(2)])
+
+    def run(state, **kw):
+        pages, cache, qs, kv = state
+        ta.paged_append_rotary(q, k, v, *pages, slot, pos, rotary, q_out=qs[0], **kw)
+        ta.paged_quant_append(k, v, cache, slot, q=q, positions=pos, rotary=rotary, q_out=qs[1], **kw)
+        ta.paged_quant_read(cache, slot, out=tuple(kv), **kw)
+        return [*pages, *cache, *qs, *kv]
+
+    want, state = run(fresh()), fresh()
+    side, stream = fresh(), torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    got = run(side, stream=stream)
+    torch.cuda.current_stream().wait_stream(stream)
+    assert all(same(x, y) for x, y in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run(state)
+    graph.replay()
+    assert all(same(x, y) for x, y in zip(got, want))
+    for x, y in ((q, randn(g, *q.shape, dtype=q.dtype)), (k, randn(g, *k.shape, dtype=k.dtype)), (slot, slots_of(g, t, 6 * ps)),
+                 (pos, pos.flip(0))):
+        x.copy_(y)
+    for x in got:
+        x.zero_()
+    want = run(fresh())
+    graph.replay()
+    assert all(same(x, y) for x, y in zip(got, want))
+
+
+def test_slots_read_again(ta):
+    """A slot named by several rows of one read, in any order."""
+    g, hk, d, ps = gen(5), 3, 64, 16
+    cache = ta.paged_quant_cache(4, hk, ps, d, group_size=64, dtype=torch.float16)
+    k, v = (randn(g, 4 * ps, hk, d, dtype=torch.float16) for _ in "kv")
+    ta.paged_quant_append(k, v, cache, torch.arange(4 * ps, device="cuda"))
+    whole = ta.paged_quant_read(cache, torch.arange(4 * ps, device="cuda"))
+    pick = torch.randint(0, 4 * ps, (1000,), generator=g, device="cuda")
+    for x, y in zip(ta.paged_quant_read(cache, pick), whole):
+        assert torch.equal(x, y[pick])
+
+
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("d,group", [(64, 32), (128, 64), (256, 32)])
+def test_waits_that_give_up_set_the_status(ta, d, group, tree):
+    """Every wait bounded by a few polls: CTAs give up at different places, let their copies and
+    products end, say so in the status word and return; the next call on the same workspace is right."""
+    c = QuantPaged(ta, [900, 60, 3000, 61], [60, 60, 33, 7], 8, 2, d, 16, group, torch.bfloat16, seed=27, tree=tree)
+    want = c.run(ta, kernel=2)
+    tmp = ta.paged_quant_attention_workspace(c.q, c.cache, c.table, max_q_len=60, kernel=2)
+    word = tmp.view(torch.int32)
+    cu, lens, parents = i32(c.cu), i32(c.lens), c.flat_parents()
+    p = ta.PagedQuantParams(4, 8, 2, d, c.q.shape[0], 60, 0, 16, c.cache[0].shape[0], c.table.shape[1], group, 2, c.scale)
+    for polls in (0, 0, 1, 2, 4, 8):
+        out = torch.full_like(c.q, 77.0)
+        ta.ta_test_paged_quant_attn_fwd_wait_limit(polls, p, c.q, c.cache, c.table, cu, lens, parents, tmp, out)
+        torch.cuda.synchronize()
+        status = int(word[0])
+        assert status == 1 if polls == 0 else status in (0, 1)
+        assert status or torch.equal(out, want)
+        word[0] = 0
+        assert torch.equal(c.run(ta, kernel=2, tmp=tmp), want)
+        assert int(word[0]) == 0
+    with pytest.raises(ta.TreeAttentionError, match="tensor-core kernel only"):
+        p.kernel = 1
+        ta.ta_test_paged_quant_attn_fwd_wait_limit(0, p, c.q, c.cache, c.table, cu, lens, parents, tmp, out)

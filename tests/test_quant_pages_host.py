@@ -252,3 +252,17 @@ def test_rotary_table_angles(ta):
     for p, i in ((0, 0), (1, 3), (99999, 0), (100000, 15), (54321, 7)):
         a = p * 10000.0 ** (-2 * i / 32)
         assert abs(t[p, i] - math.cos(a)) < 1e-7 and abs(t[p, 16 + i] - math.sin(a)) < 1e-7
+
+
+@pytest.mark.parametrize("h,hk,d,new,kernel,scale,tensor_cores", [
+    (32, 8, 128, 4, 0, 0.1, False), (32, 8, 128, 5, 0, 0.1, True), (17, 1, 64, 1, 0, 0.1, True), (16, 1, 64, 1, 0, 0.0, False),
+    (8, 1, 256, 1, 0, 0.1, False), (9, 1, 256, 1, 0, 0.1, True), (32, 8, 128, 1, 2, 0.1, True), (32, 8, 128, 5, 3, 0.1, True),
+    (32, 8, 128, 5, 1, 0.1, False), (32, 8, 128, 5, 2, -0.1, False)])
+def test_kernel_choice(ta, h, hk, d, new, kernel, scale, tensor_cores):
+    """Up to 16 rows a KV head (8 with head_dim 256) stay off the tensor-core kernel, as a negative scale does."""
+    p = ta.PagedQuantParams(**{**ATTEND, "tokens": 0, "n_heads": h, "n_kv_heads": hk, "head_dim": d, "max_q_len": new,
+                               "kernel": kernel, "scale": scale})
+    fn = lambda *a: ta.lib.ta_test_paged_quant_attn_fwd_wait_limit(1, *a)
+    st, msg = _call(ta, fn, p, [None] * 11)
+    assert st == (0 if tensor_cores else 4)
+    assert tensor_cores or "tensor-core kernel only" in msg

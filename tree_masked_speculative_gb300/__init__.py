@@ -30,6 +30,7 @@ __all__ = [
     "PlanParams", "AppendParams", "PagedParams", "PromptParams", "PagedStep", "paged_plan", "paged_append",
     "paged_attention", "paged_attention_workspace", "paged_attn_workspace_bytes", "prompt_attention",
     "prompt_attention_workspace", "prompt_attn_workspace_bytes", "ta_test_paged_attn_fwd_wait_limit",
+    "ta_test_paged_quant_attn_fwd_wait_limit",
     "RotaryAppendParams", "QuantAppendParams", "PagedQuantParams", "PagedQuantCache", "paged_append_rotary",
     "paged_quant_cache", "paged_quant_append", "paged_quant_read", "paged_quant_attention",
     "paged_quant_attention_workspace", "paged_quant_attn_workspace_bytes", "rotary_table",
@@ -197,6 +198,8 @@ def _load() -> ctypes.CDLL:
     L.paged_attn_fwd.restype = ctypes.c_int
     L.ta_test_paged_attn_fwd_wait_limit.argtypes = [u32, ctypes.POINTER(PagedParams)] + [B] * 9 + [P]
     L.ta_test_paged_attn_fwd_wait_limit.restype = ctypes.c_int
+    L.ta_test_paged_quant_attn_fwd_wait_limit.argtypes = [u32, ctypes.POINTER(PagedQuantParams)] + [B] * 11 + [P]
+    L.ta_test_paged_quant_attn_fwd_wait_limit.restype = ctypes.c_int
     L.prompt_attn_workspace_bytes.argtypes = [ctypes.POINTER(PromptParams)]
     L.prompt_attn_workspace_bytes.restype = ctypes.c_size_t
     L.prompt_attn_fwd.argtypes = [ctypes.POINTER(PromptParams)] + [B] * 6 + [P]
@@ -1010,3 +1013,15 @@ def paged_quant_attention(q: torch.Tensor, cache: PagedQuantCache, block_table: 
                        *cs, *qb, *cb, *_flat(block_table, dev), *_flat(cu_q, dev), *_flat(kv_lens, dev),
                        *_flat(parents, dev), *_flat(tmp, dev), *ob)
     return out
+
+
+def ta_test_paged_quant_attn_fwd_wait_limit(wait_polls: int, p: PagedQuantParams, q, cache: PagedQuantCache, block_table,
+                                            cu_q, kv_lens, parents, tmp, out, stream=None):
+    """Test hook: paged_quant_attn_fwd (tensor-core kernel, contiguous tensors) whose waits
+    give up after `wait_polls` polls of about 1 us."""
+    i32 = TA_I32
+    kc, ka, vc, va = cache
+    _check(lib.ta_test_paged_quant_attn_fwd_wait_limit(wait_polls, ctypes.byref(p), buf(q), buf(kc, TA_U32), buf(ka),
+                                                       buf(vc, TA_U32), buf(va), buf(block_table, i32), buf(cu_q, i32),
+                                                       buf(kv_lens, i32), buf(parents, i32), buf(tmp), buf(out),
+                                                       _stream(stream)))

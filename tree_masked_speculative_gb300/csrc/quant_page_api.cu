@@ -145,8 +145,8 @@ ta_status new_rows(const char *op, P *p, const ta_buf *q, const ta_buf *k_new, c
 
 uint64_t quant_rows(const ta_paged_quant_params *p) { return static_cast<uint64_t>(p->max_q_len) * (p->n_heads / p->n_kv_heads); }
 
-// Kernel family of a call: few rows go to the warp-MMA kernel unless the tensor-core kernel is asked for.  Both
-// take the largest product for the largest logit, so a negative scale goes to the CUDA cores.
+// Kernel family of a call: few rows go to the warp-MMA kernel (measured at quant_mma_rows) unless the tensor-core kernel is
+// asked for.  Both take the largest product for the largest logit, so a negative scale goes to the CUDA cores.
 int quant_family(const ta_paged_quant_params *p) {
     if (p->kernel == TA_KERNEL_CUDA_CORES || p->scale < 0.0f) return TA_KERNEL_CUDA_CORES;
     return p->kernel != TA_KERNEL_TENSOR_CORES && quant_rows(p) <= static_cast<uint64_t>(quant_mma_rows(static_cast<int>(p->head_dim))) ? TA_KERNEL_WARP_MMA : TA_KERNEL_TENSOR_CORES;
@@ -319,11 +319,14 @@ TA_EXPORT size_t paged_quant_attn_workspace_bytes(const ta_paged_quant_params *p
     return ws ? ws : SIZE_MAX;
 }
 
-TA_EXPORT ta_status paged_quant_attn_fwd(const ta_paged_quant_params *pp, const ta_buf *q, const ta_buf *k_codes, const ta_buf *k_affine,
-                                         const ta_buf *v_codes, const ta_buf *v_affine, const ta_buf *table, const ta_buf *cu,
-                                         const ta_buf *kv_lens, const ta_buf *parents, const ta_buf *tmp, const ta_buf *out, void *stream) {
+static ta_status quant_attn_fwd(const ta_paged_quant_params *pp, const ta_buf *q, const ta_buf *k_codes, const ta_buf *k_affine,
+                                const ta_buf *v_codes, const ta_buf *v_affine, const ta_buf *table, const ta_buf *cu,
+                                const ta_buf *kv_lens, const ta_buf *parents, const ta_buf *tmp, const ta_buf *out, void *stream,
+                                uint32_t polls, bool hook) {
     const char *op = "paged_quant_attn";
     SEQ_TRY(check_quant_attn(pp));
+    if (hook && quant_family(pp) != TA_KERNEL_TENSOR_CORES)
+        SEQ_FAIL(TA_ERR_UNSUPPORTED, "%s: the wait-limit hook is for the tensor-core kernel only", op);
     ta_paged_quant_params p = *pp;
     const bool tree = !is_absent(parents);
     if (tree && p.window != 0) SEQ_FAIL(TA_ERR_INVALID_ARGUMENT, "%s: window must be 0 with parents", op);
@@ -381,5 +384,19 @@ TA_EXPORT ta_status paged_quant_attn_fwd(const ta_paged_quant_params *pp, const 
     s.scale = p.scale;
     a.group = static_cast<int>(p.group_size);
     if (ws == 0) SEQ_FAIL(TA_ERR_CUDA, "%s: no CUDA device", op);
-    return run_quant(op, a, quant_family(&p), tmp->ptr, static_cast<cudaStream_t>(stream), kSeqWaitPolls);
+    return run_quant(op, a, quant_family(&p), tmp->ptr, static_cast<cudaStream_t>(stream), polls);
+}
+
+TA_EXPORT ta_status paged_quant_attn_fwd(const ta_paged_quant_params *p, const ta_buf *q, const ta_buf *k_codes, const ta_buf *k_affine,
+                                         const ta_buf *v_codes, const ta_buf *v_affine, const ta_buf *table, const ta_buf *cu,
+                                         const ta_buf *kv_lens, const ta_buf *parents, const ta_buf *tmp, const ta_buf *out, void *stream) {
+    return quant_attn_fwd(p, q, k_codes, k_affine, v_codes, v_affine, table, cu, kv_lens, parents, tmp, out, stream, kSeqWaitPolls, false);
+}
+
+TA_EXPORT ta_status ta_test_paged_quant_attn_fwd_wait_limit(uint32_t wait_polls, const ta_paged_quant_params *p, const ta_buf *q,
+                                                            const ta_buf *k_codes, const ta_buf *k_affine, const ta_buf *v_codes,
+                                                            const ta_buf *v_affine, const ta_buf *table, const ta_buf *cu,
+                                                            const ta_buf *kv_lens, const ta_buf *parents, const ta_buf *tmp,
+                                                            const ta_buf *out, void *stream) {
+    return quant_attn_fwd(p, q, k_codes, k_affine, v_codes, v_affine, table, cu, kv_lens, parents, tmp, out, stream, wait_polls, true);
 }
