@@ -1,0 +1,125 @@
+"""Attention over 4-bit pages at the ends of its range (scales, queries and weights that differ by many orders of
+magnitude, keys and pages that are not there): every kernel family against 64 bits."""
+import math
+
+import pytest
+import torch
+
+from quant_pages import check, i32, pack, visible
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f16": torch.float16, "bf16": torch.bfloat16}
+FAMILIES = [1, 0, 2, 3]
+
+
+@pytest.fixture(scope="module")
+def ta():
+    import tree_masked_speculative_gb300 as m
+    return m
+
+
+def shared_pages(ta, logits, v_scale, v_codes, v_bias, ps, group, dtype, batch, new, h):
+    """A cache that `batch` requests share, one KV head, with logits given exactly (a key's K scale is 0 and its bias one
+    number for all elements; queries are one number a head, so no key is rounded): keys with the given logits [n] (for a head whose
+    queries are 1; every other head has queries of 1/2) and V scales and biases [n], codes [n, D].
+    Returns attend(kernel), the output [new, h, D] in 64 bits and its tolerance."""
+    n, d = v_codes.shape
+    pages = -(-n // ps)
+    cache = ta.paged_quant_cache(pages, 1, ps, d, group_size=group, dtype=dtype)
+    slot = torch.arange(n, device="cuda")
+    ka = torch.zeros(n, 1, d // group, 2, device="cuda")
+    ka[..., 1] = logits[:, None, None]
+    va = torch.stack([v_scale, v_bias], -1)[:, None, None].expand(n, 1, d // group, 2)
+    cache.k_affine[slot // ps, :, slot % ps] = ka.to(dtype)
+    cache.v_affine[slot // ps, :, slot % ps] = va.to(dtype)
+    cache.v_codes[slot // ps, :, slot % ps] = pack(v_codes)[:, None]
+    cache.k_codes.random_(-2 ** 31, 2 ** 31 - 1)
+    assert torch.equal(ka.to(dtype).float(), ka)
+    table = torch.arange(pages, device="cuda", dtype=torch.int32).repeat(batch, 1)
+    q = torch.ones(batch * new, h, d, dtype=dtype, device="cuda")
+    q[:, 1::2] = 0.5
+    cu, lens = torch.arange(batch + 1, device="cuda", dtype=torch.int32) * new, i32([n] * batch)
+
+    def attend(kernel, **kw):
+        return ta.paged_quant_attention(q, cache, table, cu, lens, scale=1.0 / d, max_q_len=new, kernel=kernel, **kw)
+
+    half = torch.finfo(dtype).eps / 2
+    s, b = (va[:, 0, 0].to(dtype).double()[:, i] for i in (0, 1))
+    val = s[:, None] * v_codes + b[:, None]
+    mag = (s[:, None] * v_codes).abs() + b[:, None].abs()
+    ref = torch.zeros(new, h, d, dtype=torch.float64, device="cuda")
+    tol = torch.zeros_like(ref)
+    see = visible(new, n).cuda()
+    for i in range(h):
+        t = logits.double() * (0.5 if i % 2 else 1.0)
+        w = torch.softmax(torch.where(see, t, -math.inf), -1)
+        ref[:, i] = w @ val
+        # half |ref|           the output
+        # 2 half W, 2^-12 W    weights and values to 16 bits; f32 work (see quant_pages.reference; the keys are exact)
+        # 15 sum_k min(2^-30 max_j w_j s_j, 2^-20 s_k)
+        #                      P s as f16, off by 2^-25 at most: of the largest of a row and group, 2^5 at least,
+        #                      that is 2^-30; of a weight (the largest 2^7 at least) 2^-20, as scales below 2^-12
+        #                      there are not taken in f16; a code is 15 at most
+        # 2^-32 sum_k |v_k|    (f16) weights below the normal range
+        top = (w * s.abs()).amax(-1, keepdim=True)
+        lost = 15 * torch.minimum(2.0 ** -30 * top, 2.0 ** -20 * s.abs()).sum(-1, keepdim=True)
+        tol[:, i] = half * ref[:, i].abs() + (2 * half + 2.0 ** -12) * (w @ mag) + lost + 1e-30
+        if dtype == torch.float16:
+            tol[:, i] += 2.0 ** -32 * mag.sum(0) + 2.0 ** -25       # (and half a subnormal step of the output)
+    return attend, ref, tol
+
+
+# base scale, scale of the odd keys, their logit, which keys those are (the warp-MMA kernel's warps take every fourth
+# 16 keys each: all of these are in the same warp as the key of the largest weight, 2000)
+ODD_KEYS = [
+    ("f16", 0.3, 4000.0, -41.5, [17]),                   # next to no weight, before the key of the largest weight
+    ("f16", 2.0 ** -12, 2.0 ** 12, -20.0, [17, 5010]),
+    ("bf16", 1.0, 2.0 ** 28, -41.5, [17]),
+    ("bf16", 1.0, 2.0 ** 40, -55.0, [17]),
+    ("bf16", 1.0, 2.0 ** 40, -55.0, [4051, 8976]),       # behind it
+    ("bf16", 1.0, 2.0 ** 40, -55.0, list(range(300))),   # the running max rises far above them
+    ("bf16", 1.0, 2.0 ** 30, -2.75, [17]),               # weight 1/16: elements of code 0 still see the others
+    ("f16", 2.0 ** -10, 2.0 ** 11, -2.75, [17, 4051]),
+    ("bf16", 2.0 ** -100, 2.0 ** 20, -2.75, [300]),
+]
+
+
+@pytest.mark.parametrize("d,group", [(64, 32), (128, 32), (128, 64), (256, 64)])
+@pytest.mark.parametrize("odd", range(len(ODD_KEYS)))
+@pytest.mark.parametrize("new", [1, 4])
+def test_keys_of_odd_scales(ta, new, odd, d, group):
+    """A few keys whose V scale is many orders above the others', of little weight or of some: what the others
+    add up to stays."""
+    name, base, far, t, keys = ODD_KEYS[odd]
+    g = torch.Generator(device="cuda")
+    g.manual_seed(odd)
+    n = 9000
+    logits = torch.full((n,), -11.0, device="cuda")
+    logits[:300] -= 30
+    logits[2000] = 0.0
+    scale = torch.full((n,), base, device="cuda")
+    logits[keys], scale[keys] = t, far
+    codes = torch.randint(0, 16, (n, d), generator=g, device="cuda")
+    bias = torch.randn(n, generator=g, device="cuda") * base * 4
+    bias[keys] = 0.0
+    attend, ref, tol = shared_pages(ta, logits, scale, codes, bias, 64, group, DT[name], 456, new, 4)
+    for kernel in FAMILIES:
+        got = attend(kernel).view(456, new, 4, d)
+        check(got, ref, tol)
+
+
+@pytest.mark.parametrize("d,group", [(64, 64), (128, 32), (256, 32)])
+def test_scales_of_zero_beside_others(ta, d, group):
+    """Groups of one value (scale 0) among groups of all sizes."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(d)
+    n = 3000
+    logits = torch.randint(-40, 1, (n,), generator=g, device="cuda") * 0.25
+    scale = 2.0 ** torch.randint(-30, 3, (n,), generator=g, device="cuda").float()
+    scale[torch.rand(n, generator=g, device="cuda") < 0.3] = 0.0
+    codes = torch.randint(0, 16, (n, d), generator=g, device="cuda")
+    bias = torch.randn(n, generator=g, device="cuda") * 0.1
+    attend, ref, tol = shared_pages(ta, logits, scale, codes, bias, 32, group, torch.bfloat16, 30, 2, 4)
+    for kernel in FAMILIES:
+        check(attend(kernel).view(30, 2, 4, d), ref, tol)

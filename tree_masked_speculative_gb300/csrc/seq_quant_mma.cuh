@@ -11,7 +11,7 @@
 // The products are keys (16) x rows (8) x elements, and elements (16) x rows (8) x keys: keys and
 // elements, not the few rows, fill the long side.  P s_g goes from the first product's layout to the
 // second's by an 8 x 8 transpose (movmatrix), in f16, held within its range by a power of two per
-// row and group that, like the running max, moves only when a block needs it.
+// row and group that, like the running max, moves only when a block needs it (kQmTop).
 // A lane's words: for K the quads 2 t and 2 t + 1 of every 32-element block of keys g and
 // g + 8, for V quad g of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9 - one vector a key and
 // product.  A warp takes every fourth block of 16 keys of its CTA's run, one or two blocks at a time, copied to
@@ -40,8 +40,16 @@ constexpr int kQmLeast = 3;                         // tiles of a CTA's run at l
 constexpr int kQmUnitCost = 6;
 constexpr float kQmLog2e = 1.4426950408889634f;
 // The running max moves when a row's max exceeds it by more than 2^8; P and l are held 2^7 higher
-// (P <= 2^15): a weight is subnormal only below 2^-21 of the running max's.
+// (P <= 2^15).
 constexpr float kQmSlack = 8.0f, kQmRaise = 7.0f;
+// P s as f16.  The power of two of a row and group, 2^110 at most, starts as that; a block whose largest P s leaves f16's
+// range sets it so that this one becomes 2^5 to 2^6 (later ones may be 2^8 larger before the running max moves), and where the
+// running max moves it rises by what the older products lose.  So the largest of all products so far is 2^5 at least, as it
+// counts now, and what f16 loses of another one is 2^-30 of that.  Elements whose code is 0 in that key
+// would see the loss: blocks with a scale below 2^-12 under the power of two (2^-10 or less of the one that counts) at a
+// weight that is not far below all others (P > 2^-20) are taken in f32, a key at a time.
+constexpr int kQmTop = 110;
+constexpr float kQmFloor = 0x1p-12f, kQmFaint = 0x1p-20f;
 
 struct QmArgs {
     SeqQuantArgs q;
@@ -81,6 +89,12 @@ __device__ __forceinline__ uint64_t mul_two(uint64_t x, uint64_t y) {
 __device__ __forceinline__ float max_abs3(float x, float y, float z) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(fabsf(y)), "f"(fabsf(z)));
+    return r;
+}
+__device__ __forceinline__ float part(uint64_t x, int e) { return e ? second(x) : first(x); }
+__device__ __forceinline__ float min_abs3(float x, float y, float z) {
+    float r;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(fabsf(y)), "f"(fabsf(z)));
     return r;
 }
 // N words (1, 2, 4 or 8) of shared memory.
@@ -227,6 +241,7 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
         // (mu: the running max less the raise, 0 where there is none; up: what moves it)
         float o[NR][NB][2][4], up[NR][2], l[NR][2];
         uint64_t ab[NR][NG], sc[NR][NG];
+        const float top = __uint_as_float(static_cast<uint32_t>(127 + kQmTop) << 23);
 #pragma unroll
         for (int x = 0; x < NR; ++x)
 #pragma unroll
@@ -236,7 +251,7 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
 #pragma unroll
                 for (int n = 0; n < NG; ++n) {
                     ab[x][n] = 0;
-                    sc[x][n] = two(0x1p100f, 0x1p100f); // too large for any scale: the first block sets it
+                    sc[x][n] = two(top, top);   // too large for most scales: the first block sets it
                 }
 #pragma unroll
                 for (int j = 0; j < NB; ++j)
@@ -262,6 +277,8 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
         constexpr int OV = 8 * D, OA = 16 * D;                              // of V's codes, of the affine in a stage
         auto swizzled = [](int row, int off) { return off ^ ((D == 64 ? (row >> 2) & 1 : (row >> 1) & 3) << 5); };
         unsigned char *mine = s_mem + warp * WB;
+        constexpr int FG = NG >= 4 ? 2 : 1;                                 // groups that share a floor
+        float floors[NG / FG] = {};                                         // 0: nothing is below
         const int c_row = lane / CPR;
         const uint32_t *k_lane = at_bytes(at_bytes(cc.kc + lane % CPR * 4, p.kh, cc.c_sh), c_row, cc.c_st);
         const uint32_t *a_lane = at_bytes(at_bytes(static_cast<const uint32_t *>(lane < 16 ? cc.ka : cc.va), p.kh, cc.a_sh), lane & 15, cc.a_st);
@@ -410,18 +427,26 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
                         if (mx > up[x][e]) {
-                            const float f = up[x][e] == -INFINITY ? 0.0f : ex2(up[x][e] - kQmSlack - mx);
+                            const bool none = up[x][e] == -INFINITY;
+                            const float down = mx - (up[x][e] - kQmSlack), f = none ? 0.0f : ex2(-down);
                             up[x][e] = mx + kQmSlack;
                             l[x][e] *= f;
 #pragma unroll
-                            for (int n = 0; n < NG; ++n) ab[x][n] = mul_two(ab[x][n], e ? two(1.0f, f) : two(f, 1.0f));
+                            for (int n = 0; n < NG; ++n) {
+                                ab[x][n] = mul_two(ab[x][n], e ? two(1.0f, f) : two(f, 1.0f));
+                                // what O holds of the scales keeps its size as far as its power of two can take the factor
+                                const uint32_t was = __float_as_uint(part(sc[x][n], e));
+                                const float raise = none ? 0.0f : fminf(floorf(down), static_cast<float>(127 + kQmTop - static_cast<int>(was >> 23)));
+                                const float fo = none ? 0.0f : ex2(raise - down), now = __uint_as_float(was + (static_cast<uint32_t>(raise) << 23));
+                                sc[x][n] = e ? two(first(sc[x][n]), now) : two(now, second(sc[x][n]));
 #pragma unroll
-                            for (int j = 0; j < NB; ++j)
+                                for (int j = n * BPG; j < (n + 1) * BPG; ++j)
 #pragma unroll
-                                for (int h = 0; h < 2; ++h) {
-                                    o[x][j][h][e] *= f;
-                                    o[x][j][h][2 + e] *= f;
-                                }
+                                    for (int h = 0; h < 2; ++h) {
+                                        o[x][j][h][e] *= fo;
+                                        o[x][j][h][2 + e] *= fo;
+                                    }
+                            }
                         }
                     }
             }
@@ -480,52 +505,107 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
                                 most = max_abs3(most, first(ps[b][x][n][i]), second(ps[b][x][n][i]));
                             }
             }
-            if (__any_sync(0xffffffffu, most > 40000.0f)) {
-                // a row and group whose P s leaves f16's range: its power of two so that the largest finite scale
-                // it sees here becomes 1/8 to 1/4
+            // is a scale of this lane's keys below its groups' floor (or 0)
+            bool low = false;
+#pragma unroll
+            for (int f = 0; f < NG / FG; ++f) {
+                float y = floors[f];
+#pragma unroll
+                for (int n = f * FG; n < (f + 1) * FG; ++n)
+#pragma unroll
+                    for (int b = 0; b < BL; ++b) y = min_abs3(y, scale_of<BF16>(va[b][0][n]), scale_of<BF16>(va[b][1][n]));
+                low |= y < floors[f];
+            }
+            bool spread = false;                        // some scale is too far below the ones that count
+            if (__any_sync(0xffffffffu, most > 40000.0f || low)) {
 #pragma unroll
                 for (int x = 0; x < NR; ++x)
 #pragma unroll
                     for (int n = 0; n < NG; ++n)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            auto part = [&](uint64_t y) { return e ? second(y) : first(y); };
-                            float v[BL][2], top = 0.0f, hit = 0.0f;
+                            float v[BL][2], hit = 0.0f; // hit: the largest P s, 2^-16 of it
 #pragma unroll
                             for (int b = 0; b < BL; ++b)
 #pragma unroll
                                 for (int i = 0; i < 2; ++i) {
                                     v[b][i] = (see[b][x] >> (2 * i + e)) & 1u ? scale_of<BF16>(va[b][i][n]) : 0.0f;
-                                    top = fmaxf(top, fabsf(v[b][i]) <= FLT_MAX ? fabsf(v[b][i]) : 0.0f);
-                                    hit = fmaxf(hit, fabsf(part(ps[b][x][n][i])));
+                                    hit = fmaxf(hit, fabsf(v[b][i]) <= FLT_MAX ? part(pr[b][x][i], e) * (fabsf(v[b][i]) * 0x1p-16f) : 0.0f);
                                 }
 #pragma unroll
-                            for (int k = 4; k < 32; k <<= 1) {
-                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-                                hit = fmaxf(hit, __shfl_xor_sync(0xffffffffu, hit, k));
-                            }
-                            if (hit > 40000.0f && top > 0.0f) {
-                                const float to = __uint_as_float(static_cast<uint32_t>(max(251 - static_cast<int>(__float_as_uint(top) >> 23), 1)) << 23);
-                                const float was = part(sc[x][n]), now = fminf(to, was), f = now / was;
-                                if (now < was) {
-                                    sc[x][n] = e ? two(first(sc[x][n]), now) : two(now, second(sc[x][n]));
+                            for (int k = 4; k < 32; k <<= 1) hit = fmaxf(hit, __shfl_xor_sync(0xffffffffu, hit, k));
+                            float now = part(sc[x][n], e);
+                            if (hit * now > 40000.0f * 0x1p-16f) {
+                                // out of f16's range: the power of two that brings it to 2^5 .. 2^6
+                                const float was = now, f0 = __uint_as_float(static_cast<uint32_t>(max(243 - static_cast<int>(__float_as_uint(hit) >> 23), 1)) << 23);
+                                now = fminf(f0, was);
+                                const float f = now / was;
+                                sc[x][n] = e ? two(first(sc[x][n]), now) : two(now, second(sc[x][n]));
 #pragma unroll
-                                    for (int j = n * BPG; j < (n + 1) * BPG; ++j)
+                                for (int j = n * BPG; j < (n + 1) * BPG; ++j)
 #pragma unroll
-                                        for (int h = 0; h < 2; ++h) {
-                                            o[x][j][h][e] *= f;
-                                            o[x][j][h][2 + e] *= f;
-                                        }
-                                }
+                                    for (int h = 0; h < 2; ++h) {
+                                        o[x][j][h][e] *= f;
+                                        o[x][j][h][2 + e] *= f;
+                                    }
 #pragma unroll
                                 for (int b = 0; b < BL; ++b)
 #pragma unroll
                                     for (int i = 0; i < 2; ++i) {
-                                        const float y = part(pr[b][x][i]) * now * v[b][i];
+                                        const float y = part(pr[b][x][i], e) * now * v[b][i];
                                         ps[b][x][n][i] = e ? two(first(ps[b][x][n][i]), y) : two(y, second(ps[b][x][n][i]));
                                     }
                             }
+#pragma unroll
+                            for (int b = 0; b < BL; ++b)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    const float y = fabsf(v[b][i]) * now;
+                                    spread |= y > 0.0f && y < kQmFloor && part(pr[b][x][i], e) > kQmFaint;
+                                }
                         }
+                spread = __any_sync(0xffffffffu, spread);
+                // the floors as scales, of the rows and groups that count them the highest
+#pragma unroll
+                for (int f = 0; f < NG / FG; ++f) {
+                    float y = INFINITY;
+#pragma unroll
+                    for (int x = 0; x < NR; ++x)
+#pragma unroll
+                        for (int n = f * FG; n < (f + 1) * FG; ++n) y = min_abs3(y, first(sc[x][n]), second(sc[x][n]));
+                    floors[f] = kQmFloor / y;
+                }
+            }
+            if (spread) {
+                // in f32, a key at a time: O's places of the products below
+#pragma unroll
+                for (int b = 0; b < BL; ++b)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll 1
+                        for (int r = 0; r < 8; ++r) {
+                            const int row = r + 8 * i;
+                            uint32_t w[VW];
+                            load_words<VW>(blk + b * STG + OV + swizzled(row, row * (D / 2) + g * (VW * 4)), w);
+#pragma unroll
+                            for (int x = 0; x < NR; ++x)
+#pragma unroll
+                                for (int n = 0; n < NG; ++n) {
+                                    const uint64_t y = mul_two(__shfl_sync(0xffffffffu, ps[b][x][n][i], 4 * r + t), two(0x1p-24f, 0x1p-24f));
+#pragma unroll
+                                    for (int j = n * BPG; j < (n + 1) * BPG; ++j)
+#pragma unroll
+                                        for (int h = 0; h < 2; ++h) {
+                                            const uint32_t c = w[j / 2] >> (16 * (j & 1) + 8 * h);
+                                            const float c0 = static_cast<float>(c & 15u), c1 = static_cast<float>(c & 240u);
+                                            o[x][j][h][0] = fmaf(first(y), c0, o[x][j][h][0]);
+                                            o[x][j][h][1] = fmaf(second(y), c0, o[x][j][h][1]);
+                                            o[x][j][h][2] = fmaf(first(y), c1, o[x][j][h][2]);
+                                            o[x][j][h][3] = fmaf(second(y), c1, o[x][j][h][3]);
+                                        }
+                                }
+                        }
+                continue;
             }
             // O += V^T (P s): elements 32 j + 4 g + 2 h (+ 1) of 16 rows of the product, 8 query rows
 #pragma unroll
