@@ -699,7 +699,8 @@ size_t paged_quant_attn_workspace_bytes(const ta_paged_quant_params *p);
  * Kernels: up to 16 rows (max_q_len * n_heads / n_kv_heads; 8 with head_dim 256) warp-level MMAs,
  * which take the codes as they are; more rows, or TA_KERNEL_TENSOR_CORES, the tcgen05 kernel, for
  * which each element is rounded to the 16-bit type (one beyond the type's range is infinite there, as it
- * is for paged_quant_read); TA_KERNEL_CUDA_CORES or a negative scale the CUDA cores.
+ * is for paged_quant_read) and logits, scale included, must stay below 2^28; TA_KERNEL_CUDA_CORES or a negative
+ * scale the CUDA cores.  The other two families take whatever q and k make whose products f32 holds.
  */
 ta_status paged_quant_attn_fwd(const ta_paged_quant_params *p, const ta_buf *q, const ta_buf *k_codes,
                                const ta_buf *k_affine, const ta_buf *v_codes, const ta_buf *v_affine,

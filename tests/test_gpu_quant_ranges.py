@@ -5,7 +5,7 @@ import math
 import pytest
 import torch
 
-from quant_pages import check, i32, pack, visible
+from quant_pages import QuantPaged, check, i32, pack, visible
 
 pytestmark = pytest.mark.gpu
 
@@ -123,3 +123,50 @@ def test_scales_of_zero_beside_others(ta, d, group):
     attend, ref, tol = shared_pages(ta, logits, scale, codes, bias, 32, group, torch.bfloat16, 30, 2, 4)
     for kernel in FAMILIES:
         check(attend(kernel).view(30, 2, 4, d), ref, tol)
+
+
+@pytest.mark.parametrize("new,d,group", [(1, 128, 64), (4, 64, 32), (2, 256, 32)])
+@pytest.mark.parametrize("power", [18, 60, 110, 117, 118])
+def test_queries_near_the_largest(ta, power, new, d, group):
+    """bf16 queries whose products with the keys f32 still holds: the row is the value of its best key, whose
+    logit is 2^9 above the others' at least.  (The tensor-core kernel takes logits up to 2^28.)"""
+    families = FAMILIES if power < 20 else [1, 0, 3]
+    g = torch.Generator(device="cuda")
+    g.manual_seed(power)
+    n = 70
+    codes = torch.randint(0, 16, (n, d), generator=g, device="cuda")
+    c = QuantPaged(ta, [n], [new], 4, 1, d, 16, group, torch.bfloat16, seed=power)
+    order = torch.randperm(n, generator=g, device="cuda")
+    pages = c.table[0, :-(-n // 16)].long()
+    at = torch.arange(n, device="cuda")
+    page, inside = pages[at // 16], at % 16
+    t = (order.float() / 128).to(torch.bfloat16)                 # distinct, below 1
+    c.cache.k_affine[page, 0, inside] = torch.stack([torch.zeros_like(t), t], -1)[:, None]
+    for many in (True, False):
+        c.q.zero_()
+        if many:                                                 # d of them: sums up to 2^(power + 8)
+            c.q.fill_(2.0 ** power)
+        else:                                                    # one, up to the type's largest power
+            for r in range(new):
+                for h in range(4):
+                    c.q[r, h, (37 * r + 19 * h) % d] = 2.0 ** (power + 8)
+        for kernel in families:
+            got = c.run(ta, kernel=kernel, scale=1.0 / 8)
+            for r in range(new):
+                best = int(order[:n - new + 1 + r].argmax())
+                ref = c.vals[0][best, 0].double().expand(4, d)
+                mag = c.mags[0][best, 0]
+                # the value to 16 bits, the output, the weight (1 exactly, times a scale)
+                check(got[r], ref, (2.0 ** -8 * 3 + 2.0 ** -12) * mag.expand(4, d))
+    # the same with codes: one element of the query, and a key whose code there is the largest
+    e = (5 * power) % d
+    kc = torch.randint(0, 15, (n, d), generator=g, device="cuda")
+    top = int(torch.randint(0, n - new + 1, (1,), generator=g, device="cuda"))
+    kc[top, e] = 15
+    c.cache.k_codes[page, 0, inside] = pack(kc)
+    c.cache.k_affine[page, 0, inside] = torch.tensor([0.125, 0.0], dtype=torch.bfloat16, device="cuda").expand(n, d // group, 2)
+    c.q.zero_()
+    c.q[:, :, e] = 2.0 ** (power + 6)
+    ref, mag = c.vals[0][top, 0].double().expand(new, 4, d), c.mags[0][top, 0]
+    for kernel in families:
+        check(c.run(ta, kernel=kernel, scale=1.0 / 8), ref, (2.0 ** -8 * 3 + 2.0 ** -12) * mag)

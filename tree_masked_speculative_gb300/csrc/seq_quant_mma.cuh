@@ -162,6 +162,7 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
     __shared__ SeqScratch sched;
     __shared__ float2 s_ml[kQmWarps][RR];
     __shared__ __align__(8) float s_qs[NR * NG][8];
+    __shared__ float s_far[RR];
     extern __shared__ __align__(128) unsigned char s_mem[];   // the warps' stages (or rows of O: [RR][OS]), then Q's fragments
     constexpr int WB = kQmWarpBytes<D, G, NR>, STG = kQmStage<D, G>, BL = kQmBlocks<D, NR>, STEP = 16 * kQmWarps;
     uint4 *s_q = reinterpret_cast<uint4 *>(s_mem + kQmWarps * WB);      // [NR][NB][32]
@@ -180,7 +181,10 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
         // with G = 64, whose two blocks' quads are the halves of a word as it is, of blocks j0 and j0 + 1 (j0 = j less its lowest
         // bit b) the elements 8 t + 4 b + {0 | 1 | 2 | 3} of both.  The second and fourth pair are over 16 (their codes come
         // as 16 c), all times 2^e: the row's largest in [2^13, 2^14)
+        // Rows of very large queries are worked on as 2^-32 of them, so that no factor or sum leaves f32's range before
+        // the logit does (f16 holds none; s_far: 2^32 for such a row, 1 for another)
         uint64_t fr[NR];
+        bool far = false;
 #pragma unroll
         for (int x = 0; x < NR; ++x) {
             const int row = g + 8 * x, tok = row / a.g;
@@ -203,10 +207,15 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
                 widen(raw[j].x, f); widen(raw[j].y, f + 2); widen(raw[j].z, f + 4); widen(raw[j].w, f + 6);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(f[e]));
-                sum[j / BPG] += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum[j / BPG] = fmaf(f[e], 0x1p-7f, sum[j / BPG]);   // (2^-7 of it: below 2^128)
             }
             big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
             big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+            const bool is_far = BF16 && !(big * fmaxf(scale2, 1.0f) < 0x1p90f);
+            const float less = is_far ? 0x1p-32f : 1.0f;
+            far |= __any_sync(0xffffffffu, is_far) != 0;
+            if (BF16 && t == 0 && warp == 0) s_far[8 * x + g] = is_far ? 0x1p32f : 1.0f;
             // exponents as they stand in the bits: 2^(13 - floor(log2 big))
             const int up = min(267 - static_cast<int>(__float_as_uint(big) >> 23), 250);
             const float mul = __uint_as_float(static_cast<uint32_t>(up) << 23), mul16 = mul * 0.0625f;
@@ -225,11 +234,11 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
                 if (warp == (j & 3)) s_q[(x * NB + j) * 32 + lane] = y;
             }
             // 2^24 / 2^e of row g, and its sums: to the lanes that hold the rows 2 t and 2 t + 1 of a product
-            const float back = __uint_as_float(static_cast<uint32_t>(254 - up) << 23) * 0x1p24f * scale2;
+            const float back = __uint_as_float(static_cast<uint32_t>(254 - up) << 23) * less * 0x1p24f * scale2;
             fr[x] = two(__shfl_sync(0xffffffffu, back, 8 * t), __shfl_sync(0xffffffffu, back, 8 * t + 4));
 #pragma unroll
             for (int n = 0; n < NG; ++n) {
-                float y = sum[n];
+                float y = sum[n] * (less * 0x1p7f);
                 y += __shfl_xor_sync(0xffffffffu, y, 1);
                 y += __shfl_xor_sync(0xffffffffu, y, 2);
                 y *= scale2;
@@ -374,6 +383,14 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
                     s[b][x][2 * i] = first(y);
                     s[b][x][2 * i + 1] = second(y);
                 }
+            }
+            if (BF16 && __builtin_expect(far, 0)) {
+#pragma unroll
+                for (int x = 0; x < NR; ++x)
+#pragma unroll
+                    for (int b = 0; b < BL; ++b)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) s[b][x][i] *= s_far[8 * x + 2 * t + (i & 1)];
             }
             // bit 2 n + e: is key g + 8 n of block b seen by row 2 t + e
             const int last = key + (BL - 1) * STEP;
