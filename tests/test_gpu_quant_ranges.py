@@ -5,7 +5,7 @@ import math
 import pytest
 import torch
 
-from quant_pages import QuantPaged, check, i32, pack, visible
+from quant_pages import QuantPaged, check, i32, pack, values, visible
 
 pytestmark = pytest.mark.gpu
 
@@ -170,3 +170,24 @@ def test_queries_near_the_largest(ta, power, new, d, group):
     ref, mag = c.vals[0][top, 0].double().expand(new, 4, d), c.mags[0][top, 0]
     for kernel in families:
         check(c.run(ta, kernel=kernel, scale=1.0 / 8), ref, (2.0 ** -8 * 3 + 2.0 ** -12) * mag)
+
+
+# powers of two on queries and K scales: of most groups, and of the last one
+@pytest.mark.parametrize("name,q_most,k_most,q_last,k_last", [
+    ("bf16", 0, 0, -34, 34), ("bf16", 0, 0, -60, 59), ("f16", 12, -12, -14, 13)])
+@pytest.mark.parametrize("new,h,hk,d,group", [(1, 8, 2, 128, 64), (1, 4, 4, 64, 32), (4, 4, 1, 128, 32), (1, 6, 1, 256, 32),
+                                              (20, 4, 2, 128, 64)])
+def test_groups_of_small_queries_on_large_keys(ta, new, h, hk, d, group, name, q_most, k_most, q_last, k_last):
+    """A group's queries are many orders below the others', its keys as many above: both parts of a logit count."""
+    dt = DT[name]
+    c = QuantPaged(ta, [300, 45], [new, new], h, hk, d, 16, group, dt, seed=-q_last)
+    q, k = (torch.full((d,), 2.0 ** x, dtype=torch.float64, device="cuda") for x in (q_most, k_most))
+    q[-group:], k[-group:] = 2.0 ** q_last, 2.0 ** k_last
+    c.q = (c.q.double() * q).to(dt)
+    c.cache.k_affine.copy_((c.cache.k_affine.double() * k[::group, None]).to(dt))
+    for b, n in enumerate(c.lens):
+        pages = c.table[b, :-(-n // 16)].long()
+        w, a = (c.cache[i][pages].transpose(1, 2).flatten(0, 1)[:n] for i in (0, 1))
+        c.keys[b] = values(w, a)[0]
+    for kernel in FAMILIES:
+        c.check(c.run(ta, kernel=kernel))

@@ -5,8 +5,8 @@
 // bounds it, and next to it the instructions that widen the codes.  So codes are not
 // turned into values: a nibble masked out of its word is the f16 subnormal c 2^-24 (or 16 c 2^-24,
 // without a shift), which a matrix instruction takes as it is, and scales and biases are applied to
-// sums.  With q' a row of Q times a power of two in f16, per group of G elements
-//   q . k = 2^24 / 2^e  sum_g s_g (q'_g . c_g 2^-24) + sum_g b_g (sum of q in g)
+// sums.  With q' a row's group of G elements of Q times a power of two 2^e in f16
+//   q . k = sum_g s_g 2^24 / 2^e_g (q'_g . c_g 2^-24) + sum_g b_g (sum of q in g)
 //   sum_key P v = sum_key (P s_g) c + sum_key P b_g     (the second one number a row and group)
 // The products are keys (16) x rows (8) x elements, and elements (16) x rows (8) x keys: keys and
 // elements, not the few rows, fill the long side.  P s_g goes from the first product's layout to the
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
     constexpr int RR = 8 * NR, NB = D / 32, NG = D / G, BPG = G / 32, VW = NB / 2, OS = D + 4;
     __shared__ SeqScratch sched;
     __shared__ float2 s_ml[kQmWarps][RR];
-    __shared__ __align__(8) float s_qs[NR * NG][8];
+    __shared__ __align__(16) float s_qf[NR * NG][4][4];       // of rows 2 t and 2 t + 1: sums of Q in a group, factors of its products
     __shared__ float s_far[RR];
     extern __shared__ __align__(128) unsigned char s_mem[];   // the warps' stages (or rows of O: [RR][OS]), then Q's fragments
     constexpr int WB = kQmWarpBytes<D, G, NR>, STG = kQmStage<D, G>, BL = kQmBlocks<D, NR>, STEP = 16 * kQmWarps;
@@ -180,10 +180,9 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
         // Q fragments of each two products: with G = 32 of block j the elements 32 j + 8 t + {0, 4 | 1, 5 | 2, 6 | 3, 7};
         // with G = 64, whose two blocks' quads are the halves of a word as it is, of blocks j0 and j0 + 1 (j0 = j less its lowest
         // bit b) the elements 8 t + 4 b + {0 | 1 | 2 | 3} of both.  The second and fourth pair are over 16 (their codes come
-        // as 16 c), all times 2^e: the row's largest in [2^13, 2^14)
+        // as 16 c), all times 2^e: the largest of a row and group in [2^13, 2^14)
         // Rows of very large queries are worked on as 2^-32 of them, so that no factor or sum leaves f32's range before
         // the logit does (f16 holds none; s_far: 2^32 for such a row, 1 for another)
-        uint64_t fr[NR];
         bool far = false;
 #pragma unroll
         for (int x = 0; x < NR; ++x) {
@@ -198,27 +197,30 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
                 f[0] = scale_of<BF16>(w);
                 f[1] = bias_of<BF16>(w);
             };
-            float sum[NG];
+            float sum[NG], most[NG];
 #pragma unroll
-            for (int n = 0; n < NG; ++n) sum[n] = 0.0f;
+            for (int n = 0; n < NG; ++n) sum[n] = most[n] = 0.0f;
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
                 float f[8];
                 widen(raw[j].x, f); widen(raw[j].y, f + 2); widen(raw[j].z, f + 4); widen(raw[j].w, f + 6);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(f[e]));
+                for (int e = 0; e < 8; ++e) most[j / BPG] = fmaxf(most[j / BPG], fabsf(f[e]));
 #pragma unroll
                 for (int e = 0; e < 8; ++e) sum[j / BPG] = fmaf(f[e], 0x1p-7f, sum[j / BPG]);   // (2^-7 of it: below 2^128)
             }
-            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+#pragma unroll
+            for (int n = 0; n < NG; ++n) {
+                most[n] = fmaxf(most[n], __shfl_xor_sync(0xffffffffu, most[n], 1));
+                most[n] = fmaxf(most[n], __shfl_xor_sync(0xffffffffu, most[n], 2));
+                big = fmaxf(big, most[n]);
+            }
             const bool is_far = BF16 && !(big * fmaxf(scale2, 1.0f) < 0x1p90f);
             const float less = is_far ? 0x1p-32f : 1.0f;
             far |= __any_sync(0xffffffffu, is_far) != 0;
             if (BF16 && t == 0 && warp == 0) s_far[8 * x + g] = is_far ? 0x1p32f : 1.0f;
-            // exponents as they stand in the bits: 2^(13 - floor(log2 big))
-            const int up = min(267 - static_cast<int>(__float_as_uint(big) >> 23), 250);
-            const float mul = __uint_as_float(static_cast<uint32_t>(up) << 23), mul16 = mul * 0.0625f;
+            // exponents as they stand in the bits: 2^(13 - floor(log2 most))
+            auto up = [&](int n) { return min(267 - static_cast<int>(__float_as_uint(most[n]) >> 23), 250); };
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
                 float f[8];
@@ -229,20 +231,21 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
                     widen(j & 1 ? r0.z : r0.x, f); widen(j & 1 ? r0.w : r0.y, f + 2);
                     widen(j & 1 ? r1.z : r1.x, f + 4); widen(j & 1 ? r1.w : r1.y, f + 6);
                 }
+                const float mul = __uint_as_float(static_cast<uint32_t>(up(j / BPG)) << 23), mul16 = mul * 0.0625f;
                 const uint4 y = make_uint4(pack16<false>(f[0] * mul, f[4] * mul), pack16<false>(f[1] * mul16, f[5] * mul16),
                                            pack16<false>(f[2] * mul, f[6] * mul), pack16<false>(f[3] * mul16, f[7] * mul16));
                 if (warp == (j & 3)) s_q[(x * NB + j) * 32 + lane] = y;
             }
-            // 2^24 / 2^e of row g, and its sums: to the lanes that hold the rows 2 t and 2 t + 1 of a product
-            const float back = __uint_as_float(static_cast<uint32_t>(254 - up) << 23) * less * 0x1p24f * scale2;
-            fr[x] = two(__shfl_sync(0xffffffffu, back, 8 * t), __shfl_sync(0xffffffffu, back, 8 * t + 4));
+            // the sums of row g, and 2^24 / 2^e: to the lanes that hold the rows 2 t and 2 t + 1 of a product
 #pragma unroll
             for (int n = 0; n < NG; ++n) {
                 float y = sum[n] * (less * 0x1p7f);
                 y += __shfl_xor_sync(0xffffffffu, y, 1);
                 y += __shfl_xor_sync(0xffffffffu, y, 2);
-                y *= scale2;
-                if (t == 0 && warp == 0) s_qs[x * NG + n][g] = y;
+                if (t == 0 && warp == 0) {
+                    s_qf[x * NG + n][g >> 1][g & 1] = y * scale2;
+                    s_qf[x * NG + n][g >> 1][2 + (g & 1)] = __uint_as_float(static_cast<uint32_t>(254 - up(n)) << 23) * less * 0x1p24f * scale2;
+                }
             }
         }
         __syncthreads();
@@ -343,9 +346,9 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
                     load_words<NB>(blk + b * STG + (8 * n + g) * (D / 2) + t * (NB * 4), kw[n]);
                     load_words<NG>(blk + b * STG + OA + (8 * n + g) * (NG * 4), ka[n]);
                 }
-            uint64_t s2[NR][2], u2[NR][2];
+            uint64_t s2[NR][2];
 #pragma unroll
-            for (int x = 0; x < NR; ++x) s2[x][0] = s2[x][1] = u2[x][0] = u2[x][1] = 0;
+            for (int x = 0; x < NR; ++x) s2[x][0] = s2[x][1] = 0;
 #pragma unroll
             for (int n = 0; n < NG; ++n) {
                 float acc[NR][4];
@@ -366,12 +369,13 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float sk = scale_of<BF16>(ka[i][n]), bk = bias_of<BF16>(ka[i][n]);
+                for (int x = 0; x < NR; ++x) {
+                    const float4 qf = *reinterpret_cast<const float4 *>(s_qf[x * NG + n][t]);
 #pragma unroll
-                    for (int x = 0; x < NR; ++x) {
-                        s2[x][i] = fma_two(two(sk, sk), two(acc[x][2 * i], acc[x][2 * i + 1]), s2[x][i]);
-                        u2[x][i] = fma_two(two(bk, bk), *reinterpret_cast<const uint64_t *>(&s_qs[x * NG + n][2 * t]), u2[x][i]);
+                    for (int i = 0; i < 2; ++i) {
+                        const float sk = scale_of<BF16>(ka[i][n]), bk = bias_of<BF16>(ka[i][n]);
+                        s2[x][i] = fma_two(two(sk, sk), mul_two(two(acc[x][2 * i], acc[x][2 * i + 1]), two(qf.z, qf.w)), s2[x][i]);
+                        s2[x][i] = fma_two(two(bk, bk), two(qf.x, qf.y), s2[x][i]);
                     }
                 }
             }
@@ -379,9 +383,8 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
             for (int x = 0; x < NR; ++x)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const uint64_t y = fma_two(s2[x][i], fr[x], u2[x][i]);
-                    s[b][x][2 * i] = first(y);
-                    s[b][x][2 * i + 1] = second(y);
+                    s[b][x][2 * i] = first(s2[x][i]);
+                    s[b][x][2 * i + 1] = second(s2[x][i]);
                 }
             }
             if (BF16 && __builtin_expect(far, 0)) {
