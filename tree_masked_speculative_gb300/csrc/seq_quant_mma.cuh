@@ -26,6 +26,8 @@
 // at a time, 152 with the unit cost below.
 #pragma once
 
+#include <type_traits>
+
 #include "quant_page.cuh"
 #include "seq_merge.cuh"
 
@@ -180,10 +182,12 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
         // Q fragments of each two products: with G = 32 of block j the elements 32 j + 8 t + {0, 4 | 1, 5 | 2, 6 | 3, 7};
         // with G = 64, whose two blocks' quads are the halves of a word as it is, of blocks j0 and j0 + 1 (j0 = j less its lowest
         // bit b) the elements 8 t + 4 b + {0 | 1 | 2 | 3} of both.  The second and fourth pair are over 16 (their codes come
-        // as 16 c), all times 2^e: the largest of a row and group in [2^13, 2^14)
-        // Rows of very large queries are worked on as 2^-32 of them, so that no factor or sum leaves f32's range before
-        // the logit does (f16 holds none; s_far: 2^32 for such a row, 1 for another)
-        bool far = false;
+        // as 16 c), all times 2^e: the row's largest in [2^13, 2^14); each group's where a group's largest is below 2^-10 of that
+        // (what f16 loses of it could count beside keys of large scales).  Rows of very large queries are worked on as 2^-32 of
+        // them, so that no factor or sum leaves f32's range before the logit does (s_far: 2^32 for such a row, 1 for another).
+        // Both are for the careful loop.
+        uint64_t fr[NR];
+        bool careful = false;
 #pragma unroll
         for (int x = 0; x < NR; ++x) {
             const int row = g + 8 * x, tok = row / a.g;
@@ -206,8 +210,7 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
                 widen(raw[j].x, f); widen(raw[j].y, f + 2); widen(raw[j].z, f + 4); widen(raw[j].w, f + 6);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) most[j / BPG] = fmaxf(most[j / BPG], fabsf(f[e]));
-#pragma unroll
-                for (int e = 0; e < 8; ++e) sum[j / BPG] = fmaf(f[e], 0x1p-7f, sum[j / BPG]);   // (2^-7 of it: below 2^128)
+                sum[j / BPG] += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
             }
 #pragma unroll
             for (int n = 0; n < NG; ++n) {
@@ -217,10 +220,25 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
             }
             const bool is_far = BF16 && !(big * fmaxf(scale2, 1.0f) < 0x1p90f);
             const float less = is_far ? 0x1p-32f : 1.0f;
-            far |= __any_sync(0xffffffffu, is_far) != 0;
-            if (BF16 && t == 0 && warp == 0) s_far[8 * x + g] = is_far ? 0x1p32f : 1.0f;
-            // exponents as they stand in the bits: 2^(13 - floor(log2 most))
-            auto up = [&](int n) { return min(267 - static_cast<int>(__float_as_uint(most[n]) >> 23), 250); };
+            bool apart = false;
+#pragma unroll
+            for (int n = 0; n < NG; ++n) apart |= most[n] > 0.0f && most[n] < big * 0x1p-10f;
+            careful |= __any_sync(0xffffffffu, is_far || apart) != 0;
+            if (t == 0 && warp == 0) s_far[8 * x + g] = is_far ? 0x1p32f : 1.0f;
+            if (BF16 && is_far) {                       // the sums again
+#pragma unroll
+                for (int n = 0; n < NG; ++n) sum[n] = 0.0f;
+#pragma unroll
+                for (int j = 0; j < NB; ++j) {
+                    float f[8];
+                    widen(raw[j].x, f); widen(raw[j].y, f + 2); widen(raw[j].z, f + 4); widen(raw[j].w, f + 6);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) sum[j / BPG] = fmaf(f[e], less, sum[j / BPG]);
+                }
+            }
+            // exponents as they stand in the bits: 2^(13 - floor(log2 of the largest))
+            auto up = [&](int n) { return min(267 - static_cast<int>(__float_as_uint(apart ? most[n] : big) >> 23), 250); };
+            auto back = [&](int n) { return __uint_as_float(static_cast<uint32_t>(254 - up(n)) << 23) * less * 0x1p24f * scale2; };
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
                 float f[8];
@@ -236,15 +254,16 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
                                            pack16<false>(f[2] * mul, f[6] * mul), pack16<false>(f[3] * mul16, f[7] * mul16));
                 if (warp == (j & 3)) s_q[(x * NB + j) * 32 + lane] = y;
             }
-            // the sums of row g, and 2^24 / 2^e: to the lanes that hold the rows 2 t and 2 t + 1 of a product
+            // 2^24 / 2^e of row g, and its sums: to the lanes that hold the rows 2 t and 2 t + 1 of a product
+            fr[x] = two(__shfl_sync(0xffffffffu, back(0), 8 * t), __shfl_sync(0xffffffffu, back(0), 8 * t + 4));
 #pragma unroll
             for (int n = 0; n < NG; ++n) {
-                float y = sum[n] * (less * 0x1p7f);
+                float y = sum[n];
                 y += __shfl_xor_sync(0xffffffffu, y, 1);
                 y += __shfl_xor_sync(0xffffffffu, y, 2);
                 if (t == 0 && warp == 0) {
                     s_qf[x * NG + n][g >> 1][g & 1] = y * scale2;
-                    s_qf[x * NG + n][g >> 1][2 + (g & 1)] = __uint_as_float(static_cast<uint32_t>(254 - up(n)) << 23) * less * 0x1p24f * scale2;
+                    s_qf[x * NG + n][g >> 1][2 + (g & 1)] = back(n);
                 }
             }
         }
@@ -254,22 +273,6 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
         float o[NR][NB][2][4], up[NR][2], l[NR][2];
         uint64_t ab[NR][NG], sc[NR][NG];
         const float top = __uint_as_float(static_cast<uint32_t>(127 + kQmTop) << 23);
-#pragma unroll
-        for (int x = 0; x < NR; ++x)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                up[x][e] = -INFINITY;
-                l[x][e] = 0.0f;
-#pragma unroll
-                for (int n = 0; n < NG; ++n) {
-                    ab[x][n] = 0;
-                    sc[x][n] = two(top, top);   // too large for most scales: the first block sets it
-                }
-#pragma unroll
-                for (int j = 0; j < NB; ++j)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) o[x][j][h][e] = o[x][j][h][2 + e] = 0.0f;
-            }
         const int key_end = min(p.kv, (p.t0 + p.nt) << kQmTks);
         const int32_t *table = a.table + static_cast<long long>(p.b) * a.max_pages;
         // page of the 16-key block at `key` (0 where there is none: nothing of it is seen, or the rows are not valid)
@@ -290,7 +293,6 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
         auto swizzled = [](int row, int off) { return off ^ ((D == 64 ? (row >> 2) & 1 : (row >> 1) & 3) << 5); };
         unsigned char *mine = s_mem + warp * WB;
         constexpr int FG = NG >= 4 ? 2 : 1;                                 // groups that share a floor
-        float floors[NG / FG] = {};                                         // 0: nothing is below
         const int c_row = lane / CPR;
         const uint32_t *k_lane = at_bytes(at_bytes(cc.kc + lane % CPR * 4, p.kh, cc.c_sh), c_row, cc.c_st);
         const uint32_t *a_lane = at_bytes(at_bytes(static_cast<const uint32_t *>(lane < 16 ? cc.ka : cc.va), p.kh, cc.a_sh), lane & 15, cc.a_st);
@@ -313,6 +315,28 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
                 }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
+        // All keys of this warp.  CAREFUL: factors of each row and group, the lift of very large queries, keys whose V scale is
+        // far below others' in f32; without it, false where such a key is met.
+        auto all_keys = [&](auto is_careful) -> bool {
+        constexpr bool CAREFUL = decltype(is_careful)::value;
+#pragma unroll
+        for (int x = 0; x < NR; ++x)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                up[x][e] = -INFINITY;
+                l[x][e] = 0.0f;
+#pragma unroll
+                for (int n = 0; n < NG; ++n) {
+                    ab[x][n] = 0;
+                    sc[x][n] = two(top, top);   // too large for most scales: the first block sets it
+                }
+#pragma unroll
+                for (int j = 0; j < NB; ++j)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) o[x][j][h][e] = o[x][j][h][2 + e] = 0.0f;
+            }
+        float floors[NG / FG] = {};                                         // 0: nothing is below
+        auto lift = [&](int x, int e) { return CAREFUL ? s_far[8 * x + 2 * t + e] : 1.0f; };
         int key = (p.t0 << kQmTks) + 16 * warp, ahead = key, st = 0, page[BL];
 #pragma unroll
         for (int b = 0; b < BL; ++b) page[b] = page_of(key + b * STEP);
@@ -336,7 +360,7 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
             for (int b = 0; b < BL; ++b) page[b] = page_of(ahead + b * STEP);
             const unsigned char *blk = mine + st * BL * STG;
             st = (st + 1) % kQmStages;
-            // logits in log2 units: s[b][x][2 n + e] of key g + 8 n of block b, row 2 t + e of tile x
+            // logits in log2 units, before the lift: s[b][x][2 n + e] of key g + 8 n of block b, row 2 t + e of tile x
             float s[BL][NR][4];
 #pragma unroll
             for (int b = 0; b < BL; ++b) {
@@ -346,9 +370,9 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
                     load_words<NB>(blk + b * STG + (8 * n + g) * (D / 2) + t * (NB * 4), kw[n]);
                     load_words<NG>(blk + b * STG + OA + (8 * n + g) * (NG * 4), ka[n]);
                 }
-            uint64_t s2[NR][2];
+            uint64_t s2[NR][2], u2[NR][2];
 #pragma unroll
-            for (int x = 0; x < NR; ++x) s2[x][0] = s2[x][1] = 0;
+            for (int x = 0; x < NR; ++x) s2[x][0] = s2[x][1] = u2[x][0] = u2[x][1] = 0;
 #pragma unroll
             for (int n = 0; n < NG; ++n) {
                 float acc[NR][4];
@@ -369,13 +393,14 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
                     }
                 }
 #pragma unroll
-                for (int x = 0; x < NR; ++x) {
-                    const float4 qf = *reinterpret_cast<const float4 *>(s_qf[x * NG + n][t]);
+                for (int i = 0; i < 2; ++i) {
+                    const float sk = scale_of<BF16>(ka[i][n]), bk = bias_of<BF16>(ka[i][n]);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float sk = scale_of<BF16>(ka[i][n]), bk = bias_of<BF16>(ka[i][n]);
-                        s2[x][i] = fma_two(two(sk, sk), mul_two(two(acc[x][2 * i], acc[x][2 * i + 1]), two(qf.z, qf.w)), s2[x][i]);
-                        s2[x][i] = fma_two(two(bk, bk), two(qf.x, qf.y), s2[x][i]);
+                    for (int x = 0; x < NR; ++x) {
+                        const uint64_t *qf = reinterpret_cast<const uint64_t *>(s_qf[x * NG + n][t]);
+                        const uint64_t y = two(acc[x][2 * i], acc[x][2 * i + 1]);
+                        s2[x][i] = fma_two(two(sk, sk), CAREFUL ? mul_two(y, qf[1]) : y, s2[x][i]);
+                        u2[x][i] = fma_two(two(bk, bk), qf[0], u2[x][i]);
                     }
                 }
             }
@@ -383,17 +408,10 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
             for (int x = 0; x < NR; ++x)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    s[b][x][2 * i] = first(s2[x][i]);
-                    s[b][x][2 * i + 1] = second(s2[x][i]);
+                    const uint64_t y = fma_two(s2[x][i], CAREFUL ? two(1.0f, 1.0f) : fr[x], u2[x][i]);
+                    s[b][x][2 * i] = first(y);
+                    s[b][x][2 * i + 1] = second(y);
                 }
-            }
-            if (BF16 && __builtin_expect(far, 0)) {
-#pragma unroll
-                for (int x = 0; x < NR; ++x)
-#pragma unroll
-                    for (int b = 0; b < BL; ++b)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) s[b][x][i] *= s_far[8 * x + 2 * t + (i & 1)];
             }
             // bit 2 n + e: is key g + 8 n of block b seen by row 2 t + e
             const int last = key + (BL - 1) * STEP;
@@ -434,7 +452,7 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
                 for (int e = 0; e < 2; ++e) {
                     float mx = fmaxf(s[0][x][e], s[0][x][2 + e]);
                     if (BL == 2) mx = fmaxf(mx, fmaxf(s[BL - 1][x][e], s[BL - 1][x][2 + e]));
-                    rise |= mx > up[x][e];
+                    rise |= mx * lift(x, e) > up[x][e];
                 }
             if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
@@ -445,28 +463,29 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
                         if (BL == 2) mx = fmaxf(mx, fmaxf(s[BL - 1][x][e], s[BL - 1][x][2 + e]));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16)) * lift(x, e);
                         if (mx > up[x][e]) {
-                            const bool none = up[x][e] == -INFINITY;
-                            const float down = mx - (up[x][e] - kQmSlack), f = none ? 0.0f : ex2(-down);
-                            up[x][e] = mx + kQmSlack;
-                            l[x][e] *= f;
+                            if (up[x][e] != -INFINITY) {
+                                const float down = mx - (up[x][e] - kQmSlack), f = ex2(-down);
+                                l[x][e] *= f;
 #pragma unroll
-                            for (int n = 0; n < NG; ++n) {
-                                ab[x][n] = mul_two(ab[x][n], e ? two(1.0f, f) : two(f, 1.0f));
-                                // what O holds of the scales keeps its size as far as its power of two can take the factor
-                                const uint32_t was = __float_as_uint(part(sc[x][n], e));
-                                const float raise = none ? 0.0f : fminf(floorf(down), static_cast<float>(127 + kQmTop - static_cast<int>(was >> 23)));
-                                const float fo = none ? 0.0f : ex2(raise - down), now = __uint_as_float(was + (static_cast<uint32_t>(raise) << 23));
-                                sc[x][n] = e ? two(first(sc[x][n]), now) : two(now, second(sc[x][n]));
+                                for (int n = 0; n < NG; ++n) {
+                                    ab[x][n] = mul_two(ab[x][n], e ? two(1.0f, f) : two(f, 1.0f));
+                                    // what O holds of the scales keeps its size as far as its power of two can take the factor
+                                    const uint32_t was = __float_as_uint(part(sc[x][n], e));
+                                    const float raise = fminf(floorf(down), static_cast<float>(127 + kQmTop - static_cast<int>(was >> 23)));
+                                    const float fo = ex2(raise - down), now = __uint_as_float(was + (static_cast<uint32_t>(raise) << 23));
+                                    sc[x][n] = e ? two(first(sc[x][n]), now) : two(now, second(sc[x][n]));
 #pragma unroll
-                                for (int j = n * BPG; j < (n + 1) * BPG; ++j)
+                                    for (int j = n * BPG; j < (n + 1) * BPG; ++j)
 #pragma unroll
-                                    for (int h = 0; h < 2; ++h) {
-                                        o[x][j][h][e] *= fo;
-                                        o[x][j][h][2 + e] *= fo;
-                                    }
+                                        for (int h = 0; h < 2; ++h) {
+                                            o[x][j][h][e] *= fo;
+                                            o[x][j][h][2 + e] *= fo;
+                                        }
+                                }
                             }
+                            up[x][e] = mx + kQmSlack;
                         }
                     }
             }
@@ -480,7 +499,7 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
                 for (int b = 0; b < BL; ++b) {
                     float y[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) y[i] = ex2(s[b][x][i] - mu[i & 1]);
+                    for (int i = 0; i < 4; ++i) y[i] = ex2(CAREFUL ? fmaf(s[b][x][i], lift(x, i & 1), -mu[i & 1]) : s[b][x][i] - mu[i & 1]);
                     l[x][0] += y[0] + y[2];
                     l[x][1] += y[1] + y[3];
                     pr[b][x][0] = two(y[0], y[1]);
@@ -596,6 +615,8 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
                     floors[f] = kQmFloor / y;
                 }
             }
+            if (!CAREFUL && spread) return false;
+            if constexpr (CAREFUL)
             if (spread) {
                 // in f32, a key at a time: O's places of the products below
 #pragma unroll
@@ -654,6 +675,13 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
                     }
                 }
             }
+        }
+        return true;
+        };
+        if (careful || !all_keys(std::false_type{})) {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            __syncwarp();
+            all_keys(std::true_type{});
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncwarp();                                   // O's rows stand where the stages were
