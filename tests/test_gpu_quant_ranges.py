@@ -191,3 +191,16 @@ def test_groups_of_small_queries_on_large_keys(ta, new, h, hk, d, group, name, q
         c.keys[b] = values(w, a)[0]
     for kernel in FAMILIES:
         c.check(c.run(ta, kernel=kernel))
+
+
+@pytest.mark.parametrize("power", [90, 101, 108])
+@pytest.mark.parametrize("new,d,group", [(1, 128, 64), (3, 64, 32), (1, 256, 32), (30, 128, 32)])
+def test_values_of_large_scales(ta, new, d, group, power):
+    """V scales and biases of 2^power and more: a row's weighted sums are within f32."""
+    c = QuantPaged(ta, [200, 33], [new, new], 4, 2, d, 16, group, torch.bfloat16, seed=power)
+    c.cache.v_affine.copy_((c.cache.v_affine.double() * 2.0 ** power).to(c.dtype))
+    for x in (c.vals, c.mags):
+        for b in range(2):
+            x[b] = x[b] * 2.0 ** power
+    for kernel in FAMILIES:
+        c.check(c.run(ta, kernel=kernel))

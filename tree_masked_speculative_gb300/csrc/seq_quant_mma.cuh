@@ -702,11 +702,14 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
                     float b = e ? second(ab[x][n]) : first(ab[x][n]);
 #pragma unroll
                     for (int k = 4; k < 32; k <<= 1) b += __shfl_xor_sync(0xffffffffu, b, k);
-                    const float f = 0x1p24f / (e ? second(sc[x][n]) : first(sc[x][n])), f16 = f * 0.0625f;
+                    // (2^24 on O, not on f: that would be infinite for scales from 2^101 on)
+                    const float f = 1.0f / part(sc[x][n], e), f16 = f * 0.0625f;
+                    auto whole = [](float y) { return y * 0x1p24f; };
 #pragma unroll
                     for (int j = n * BPG; j < (n + 1) * BPG; ++j)
                         *reinterpret_cast<float4 *>(dst + 32 * j) =
-                            make_float4(fmaf(o[x][j][0][e], f, b), fmaf(o[x][j][0][2 + e], f16, b), fmaf(o[x][j][1][e], f, b), fmaf(o[x][j][1][2 + e], f16, b));
+                            make_float4(fmaf(whole(o[x][j][0][e]), f, b), fmaf(whole(o[x][j][0][2 + e]), f16, b),
+                                        fmaf(whole(o[x][j][1][e]), f, b), fmaf(whole(o[x][j][1][2 + e]), f16, b));
                 }
             }
         __syncthreads();
