@@ -204,3 +204,24 @@ def test_values_of_large_scales(ta, new, d, group, power):
             x[b] = x[b] * 2.0 ** power
     for kernel in FAMILIES:
         c.check(c.run(ta, kernel=kernel))
+
+
+@pytest.mark.parametrize("kernel", FAMILIES)
+@pytest.mark.parametrize("new,d,group", [(1, 128, 64), (3, 64, 64), (1, 256, 32), (4, 128, 32), (40, 128, 32)])
+def test_bad_pages_do_not_read_others(ta, new, d, group, kernel):
+    """A table cell outside the cache: the row is not valid, but it holds nothing of any page either."""
+    c = QuantPaged(ta, [200, 60], [new, new], 4, 2, d, 16, group, torch.bfloat16, seed=6)
+    tmp = ta.paged_quant_attention_workspace(c.q, c.cache, c.table, max_q_len=new, kernel=kernel)
+    mine = set(c.table[0, :13].tolist())
+    c.table[0, 2] = -1
+    c.table[0, 7] = c.cache[0].shape[0]
+    got = []
+    for fill in (1.0, 2.0, math.nan):
+        for page in range(c.cache[0].shape[0]):                  # every page that is not the request's
+            if page not in mine:
+                c.cache.k_affine[page] = fill
+                c.cache.v_affine[page] = fill
+        got.append(c.run(ta, kernel=kernel, tmp=tmp)[c.cu[0]:c.cu[1]])
+        assert int(tmp[:1].view(torch.int32)) == 2
+        tmp[:1].zero_()
+    assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])

@@ -115,15 +115,18 @@ __device__ __forceinline__ void load_words(const unsigned char *p, uint32_t *w) 
         }
     }
 }
-// N words to shared memory, past L1 where the instruction takes 16 bytes.
+// 16 bytes to shared memory, past L1; N words, or as many zeros, past L1 where the instruction takes 16 bytes.
+__device__ __forceinline__ void copy_vector(uint32_t dst, const uint32_t *src) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 template <int N>
-__device__ __forceinline__ void copy_words(uint32_t dst, const uint32_t *src) {
+__device__ __forceinline__ void copy_words(uint32_t dst, const uint32_t *src, bool live) {
     if constexpr (N >= 4) {
 #pragma unroll
         for (int i = 0; i < N; i += 4)
-            asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst + 4 * i), "l"(src + i) : "memory");
+            asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst + 4 * i), "l"(src + i), "r"(live ? 16 : 0) : "memory");
     } else {
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(4 * N) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(4 * N), "r"(live ? 4 * N : 0) : "memory");
     }
 }
 // Scale and bias of a pair.
@@ -275,14 +278,15 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
         const float top = __uint_as_float(static_cast<uint32_t>(127 + kQmTop) << 23);
         const int key_end = min(p.kv, (p.t0 + p.nt) << kQmTks);
         const int32_t *table = a.table + static_cast<long long>(p.b) * a.max_pages;
-        // page of the 16-key block at `key` (0 where there is none: nothing of it is seen, or the rows are not valid)
+        // page of the 16-key block at `key` (0 behind the last key; -1 where there is none: its scales and biases are 0, so that
+        // what its codes are does not matter)
         auto page_of = [&](int key) -> int {
             if (key >= key_end) return 0;
             const int page = __ldg(table + (key >> a.page_shift));
             if (static_cast<unsigned>(page) < static_cast<unsigned>(a.n_pages)) return page;
             // a page before every row's window may be gone
             if (lane == 0 && !(a.window && key + 16 <= p.prefix - a.window + 1)) atomicOr(a.status, kSeqBadPage);
-            return 0;
+            return -1;
         };
         // Copies of a block: K's and V's rows of codes, a 16-byte vector a lane and instruction, then rows of scales and
         // biases, K's by lanes 0 .. 15, V's by the others.  The whole block is in its page, so keys past the last
@@ -303,15 +307,16 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
             for (int b = 0; b < BL; ++b)
                 if (key + b * STEP < key_end) {
                     const int in = (key + b * STEP) & ((1 << a.page_shift) - 1);
-                    const uint32_t *c = at_bytes(at_bytes(k_lane, page[b], cc.c_sp), in, cc.c_st);
+                    const int from = max(page[b], 0);
+                    const uint32_t *c = at_bytes(at_bytes(k_lane, from, cc.c_sp), in, cc.c_st);
                     const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(mine + (st * BL + b) * STG));
 #pragma unroll
                     for (int i = 0; i < CPR / 2; ++i) {
                         const uint32_t *ci = at_bytes(c, i * ROWS, cc.c_st);
-                        copy_words<4>(dst + lane * 16 + 512 * i, ci);
-                        copy_words<4>(dst + OV + swizzled(c_row + i * ROWS, lane * 16 + 512 * i), ci + v_off);
+                        copy_vector(dst + lane * 16 + 512 * i, ci);
+                        copy_vector(dst + OV + swizzled(c_row + i * ROWS, lane * 16 + 512 * i), ci + v_off);
                     }
-                    copy_words<NG>(dst + OA + lane * (NG * 4), at_bytes(at_bytes(a_lane, page[b], cc.a_sp), in, cc.a_st));
+                    copy_words<NG>(dst + OA + lane * (NG * 4), at_bytes(at_bytes(a_lane, from, cc.a_sp), in, cc.a_st), page[b] >= 0);
                 }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
