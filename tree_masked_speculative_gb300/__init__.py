@@ -818,6 +818,12 @@ def paged_quant_cache(n_pages: int, n_kv_heads: int, page_size: int, head_dim: i
 def rotary_table(positions: int, rotary_dim: int, *, base: float = 10000.0, device="cuda") -> torch.Tensor:
     """The table [positions, rotary_dim] f32 of paged_append_rotary and paged_quant_append:
     cosines, then sines, of position * base^(-2 i / rotary_dim); angles in 64 bits."""
+    if rotary_dim <= 0 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be even and > 0, got %d" % rotary_dim)
+    if positions < 0:
+        raise ValueError("positions must be >= 0, got %d" % positions)
+    if not 0.0 < base < float("inf"):
+        raise ValueError("base must be finite and > 0, got %r" % base)
     turn = base ** (-torch.arange(0, rotary_dim, 2, dtype=torch.float64, device=device) / rotary_dim)
     angle = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * turn
     return torch.cat([angle.cos(), angle.sin()], -1).float()
