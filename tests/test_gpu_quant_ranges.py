@@ -5,7 +5,7 @@ import math
 import pytest
 import torch
 
-from quant_pages import QuantPaged, check, i32, pack, values, visible
+from quant_pages import QuantPaged, check, i32, pack, quantised, turned, values, visible
 
 pytestmark = pytest.mark.gpu
 
@@ -225,3 +225,54 @@ def test_bad_pages_do_not_read_others(ta, new, d, group, kernel):
         assert int(tmp[:1].view(torch.int32)) == 2
         tmp[:1].zero_()
     assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
+
+
+@pytest.mark.parametrize("kernel", FAMILIES)
+@pytest.mark.parametrize("fill", [math.nan, math.inf, 1000.0])
+@pytest.mark.parametrize("new,d", [(1, 128), (3, 64), (6, 256), (40, 128)])
+def test_keys_outside_every_row_do_not_matter(ta, new, d, fill, kernel):
+    """Scales, biases and codes behind the last key and before the window, changed between two calls."""
+    c = QuantPaged(ta, [200 + new, 64, new + 3], [new, 0, new], 4, 2, d, 16, 32, torch.bfloat16, seed=3)
+    for window in (0, 50):
+        want = c.run(ta, kernel=kernel, window=window)
+        c.check(want, window)
+        keep = [x.clone() for x in c.cache]
+        for b, n in enumerate(c.lens):
+            first = max(0, n - c.new[b] - window + 1) if window else 0
+            for j in [*range(first), *range(n, -(-n // 16) * 16)]:
+                page = int(c.table[b, j // 16])
+                for x in (c.cache.k_affine, c.cache.v_affine):
+                    x[page, :, j % 16] = fill
+                for x in (c.cache.k_codes, c.cache.v_codes):
+                    x[page, :, j % 16] = -1
+        assert torch.equal(c.run(ta, kernel=kernel, window=window), want)
+        for x, y in zip(c.cache, keep):
+            x.copy_(y)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("group", [32, 64])
+def test_turns_that_cancel(ta, group, inter, dtype):
+    """Pairs whose two products nearly or wholly take each other away, tables of sizes other than 1: codes, scales and
+    biases are still those of exact arithmetic."""
+    g, dt = torch.Generator(device="cuda"), DT[dtype]
+    g.manual_seed(group)
+    t, hk, d, ps, n_pos = 6000, 2, 128, 64, 512
+    angle = math.pi / 4 + torch.randint(-3, 4, (n_pos, d // 2), generator=g, device="cuda") * 2.0 ** -torch.randint(
+        10, 25, (n_pos, d // 2), generator=g, device="cuda").double()
+    size = torch.tensor([1.0, 1.37, 2.0 ** -9, 700.0], dtype=torch.float64, device="cuda")[torch.arange(n_pos, device="cuda") % 4, None]
+    table = torch.cat([angle.cos() * size, angle.sin() * size], -1).float()
+    x = torch.randn(t, hk, d // 2, generator=g, device="cuda").to(dt)
+    ulp = torch.randint(-1, 2, x.shape, generator=g, device="cuda").to(torch.int16)
+    y = (x.view(torch.int16) + ulp).view(dt)                     # x, or a step off
+    y = torch.where(torch.rand(x.shape, generator=g, device="cuda") < 0.1, torch.randn(x.shape, generator=g, device="cuda").to(dt) * 0.01, y)
+    k = torch.stack([x, y], -1).flatten(-2) if inter else torch.cat([x, y], -1)
+    k = k.contiguous()
+    pos = torch.randint(0, n_pos, (t,), generator=g, device="cuda").to(torch.int32)
+    slot = torch.arange(t, device="cuda")
+    cache = ta.paged_quant_cache(-(-t // ps), hk, ps, d, group_size=group, dtype=dt)
+    ta.paged_quant_append(k, k, cache, slot, positions=pos, rotary=table, interleaved=inter)
+    codes, affine = quantised(turned(k.double(), table[pos.long()], d, inter), group, dt)
+    assert torch.equal(cache.k_affine[slot // ps, :, slot % ps], affine)
+    assert torch.equal(cache.k_codes[slot // ps, :, slot % ps], pack(codes))
