@@ -45,13 +45,14 @@ constexpr float kQmLog2e = 1.4426950408889634f;
 // (P <= 2^15).
 constexpr float kQmSlack = 8.0f, kQmRaise = 7.0f;
 // P s as f16.  The power of two of a row and group, 2^110 at most, starts as that; a block whose largest P s leaves f16's
-// range sets it so that this one becomes 2^5 to 2^6 (later ones may be 2^8 larger before the running max moves), and where the
-// running max moves it rises by what the older products lose.  So the largest of all products so far is 2^5 at least, as it
-// counts now, and what f16 loses of another one is 2^-30 of that.  Elements whose code is 0 in that key
-// would see the loss: blocks with a scale below 2^-12 under the power of two (2^-10 or less of the one that counts) at a
-// weight that is not far below all others (P > 2^-20) are taken in f32, a key at a time.
+// range sets it so that this one becomes a quarter of the row's largest weight P, for which 2^7 is taken where it is less here
+// (a weight may grow to 2^15 before the running max moves); where the running max moves it rises by what
+// the older products lose.  So the largest of all products so far is 2^5 at least, as it counts now, and what f16 loses of
+// another one is 2^-30 of that.  Elements whose code is 0 in that key would see the loss: blocks with a scale below 2^-12
+// under the power of two (2^-10 or less of the one that counts) at a weight that is not far below all others (P > 2^-20) are
+// taken in f32, a key at a time.
 constexpr int kQmTop = 110;
-constexpr float kQmFloor = 0x1p-12f, kQmFaint = 0x1p-20f;
+constexpr float kQmFloor = 0x1p-12f, kQmFaint = 0x1p-20f, kQmPeak = 0x1p7f;
 
 struct QmArgs {
     SeqQuantArgs q;
@@ -565,9 +566,14 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
 #pragma unroll
                 for (int x = 0; x < NR; ++x)
 #pragma unroll
-                    for (int n = 0; n < NG; ++n)
+                    for (int e = 0; e < 2; ++e) {
+                        float peak = kQmPeak;           // the row's largest weight here, if above the least one of a largest
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
+                        for (int b = 0; b < BL; ++b) peak = fmaxf(peak, fmaxf(part(pr[b][x][0], e), part(pr[b][x][1], e)));
+#pragma unroll
+                        for (int k = 4; k < 32; k <<= 1) peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, k));
+#pragma unroll
+                        for (int n = 0; n < NG; ++n) {
                             float v[BL][2], hit = 0.0f; // hit: the largest P s, 2^-16 of it
 #pragma unroll
                             for (int b = 0; b < BL; ++b)
@@ -580,9 +586,10 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
                             for (int k = 4; k < 32; k <<= 1) hit = fmaxf(hit, __shfl_xor_sync(0xffffffffu, hit, k));
                             float now = part(sc[x][n], e);
                             if (hit * now > 40000.0f * 0x1p-16f) {
-                                // out of f16's range: the power of two that brings it to 2^5 .. 2^6
-                                const float was = now, f0 = __uint_as_float(static_cast<uint32_t>(max(243 - static_cast<int>(__float_as_uint(hit) >> 23), 1)) << 23);
-                                now = fminf(f0, was);
+                                // out of f16's range: the power of two that brings it to a quarter of the peak
+                                const float was = now;
+                                const int to = 109 + static_cast<int>(__float_as_uint(peak) >> 23) - static_cast<int>(__float_as_uint(hit) >> 23);
+                                now = fminf(__uint_as_float(static_cast<uint32_t>(max(to, 1)) << 23), was);
                                 const float f = now / was;
                                 sc[x][n] = e ? two(first(sc[x][n]), now) : two(now, second(sc[x][n]));
 #pragma unroll
@@ -608,6 +615,7 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
                                     spread |= y > 0.0f && y < kQmFloor && part(pr[b][x][i], e) > kQmFaint;
                                 }
                         }
+                    }
                 spread = __any_sync(0xffffffffu, spread);
                 // the floors as scales, of the rows and groups that count them the highest
 #pragma unroll
