@@ -698,9 +698,11 @@ size_t paged_quant_attn_workspace_bytes(const ta_paged_quant_params *p);
  * the values that the pages stand for.  q and out are of the type of the scales.
  * Kernels: up to 16 rows (max_q_len * n_heads / n_kv_heads; 8 with head_dim 256) warp-level MMAs,
  * which take the codes as they are; more rows, or TA_KERNEL_TENSOR_CORES, the tcgen05 kernel, for
- * which each element is rounded to the 16-bit type (one beyond the type's range is infinite there, as it
+ * which each element and weight is rounded to the 16-bit type, so that a row of a larger call is less exact than
+ * the same row of a small one, most of all in bf16 (an element beyond the type's range is infinite there, as it
  * is for paged_quant_read) and logits, scale included, must stay below 2^28; TA_KERNEL_CUDA_CORES or a negative
- * scale the CUDA cores.  The other two families take whatever q and k make whose products f32 holds.
+ * scale the CUDA cores (f32 all through, and about a hundred times slower).  The other two families take whatever q and k
+ * make whose products f32 holds.  A key whose table cell names no page counts as a key of zeros or not at all.
  */
 ta_status paged_quant_attn_fwd(const ta_paged_quant_params *p, const ta_buf *q, const ta_buf *k_codes,
                                const ta_buf *k_affine, const ta_buf *v_codes, const ta_buf *v_affine,

@@ -8,10 +8,11 @@
 // taken again in 64 bits.
 //
 // It reads 4 D and writes D + 8 D / G bytes a KV head and token (HBM); a lane takes 8
-// neighbouring elements of up to HB heads, a group's 4 or 8 lanes reduce by shuffles.  Latency of
-// the loads and the instructions of exact codes bound it (half of the issue slots, half of HBM).
-// Measured: 16381 tokens, 32 / 8 heads of 128, f16, groups of 32: append 90 us (40 of K and V alone, not
-// turned), read 34 us, which together have 454 MB to move (68 us); 48 tokens: 2.8 and 1.7 us.
+// neighbouring elements of up to HB heads, a group's 4 or 8 lanes reduce by shuffles.  Blocks run in order, so queries (HBM
+// bounds them) and keys and values (latency of the loads and the instructions of exact codes) take their times one behind the
+// other: half of the issue slots and half of HBM on average.  With four heads a thread 72 bytes are spilled and 140 read back.
+// Measured: 16381 tokens, 32 / 8 heads of 128, f16, groups of 32: append 90 us (K and V alone 52 turned, 40 as they are, 50 in
+// bf16), read 34 us, which together have 454 MB to move (68 us); 48 tokens: 3.0 and 1.7 us.
 #include "rotary.cuh"
 
 namespace ta {
@@ -59,7 +60,9 @@ __device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
 // x - y
 __device__ __forceinline__ uint64_t sub2(uint64_t x, uint64_t y) { return fma2(y, two(-1.0f, -1.0f), x); }
 
-// x c + y s as hi + lo: hi the nearest f32, lo what is left (relative error about 2^-47).
+// x c + y s as hi + lo: hi the nearest f32, lo what is left (off by about 2^-48 of the larger product; where the two cancel
+// so that this counts, nothing is off: products of a 16-bit and a 32-bit float of like size have 35 bits, and the errors'
+// sums fit f32).
 __device__ __forceinline__ void turn_exact(uint64_t x, uint64_t c, uint64_t y, uint64_t s, uint64_t *hi, uint64_t *lo) {
     const uint64_t minus = two(-1.0f, -1.0f);
     const uint64_t p = mul2(x, c), pe = fma2(mul2(x, minus), c, p);        // pe, qe: the products' errors, negated
@@ -286,7 +289,8 @@ __global__ void __launch_bounds__(kRotThreads, 3) quant_append_kernel(const Quan
     }
 }
 
-// A thread: one word (8 codes) of K or V of a row.
+// A thread: one word (8 codes) of K or V of a row.  Its index divisions by sizes that are known only at run time and its
+// 8-byte stores keep it at 2.6 times the time of its bytes.
 template <bool BF16>
 __global__ void __launch_bounds__(kRotThreads) quant_read_kernel(const QuantReadArgs a) {
     pdl_wait();

@@ -69,17 +69,19 @@ cudaError_t launch_seq_quant_fma(const SeqQuantArgs &a, cudaStream_t s);
 // Warp-MMA kernel for few rows (max_q_len * heads per KV head); its workspace and launch.  More rows would be
 // products it has no registers for, or keys widened twice.  Replayed graphs, us, warp MMA / tcgen05 (bf16, 32 / 8
 // heads; D = 256 with half the requests):
-//                                      4 rows       8 rows      16 rows     32 rows (warp MMA with four row tiles)
-//   64 of 900 to 16384 keys, D 128 G 64  159 / 483  161 / 484   252 / 484   483 / 484
-//                            D 128 G 32  191 / 478  192 / 479   326 / 479  1027 / 480
-//                            D  64 G 32  127 / 379  127 / 381   187 / 381   358 / 382
-//                            D 256 G 64   89 / 180   91 / 180   149 / 179
-//                            D 256 G 32  109 / 185  111 / 185   307 / 185
-//   16 of 300 to 9000 keys,  D 128 G 64   28 / 69    29 / 69     46 / 70     95 / 70
-//   1 of 4000 keys,          D 128 G 64   11 / 29    12 / 29     17 / 29     28 / 30
-//   200 of 300 keys,         D 128 G 64   39 / 98    41 / 98     68 / 99    153 / 102
-//                            D 256 G 32   38 / 38    40 / 39     98 / 38
-// (D = 256 with 16 rows: 41 / 38 for 8 of 300 to 9000 keys, 22 / 41 for one of 4000.)
+//                                      4 rows       8 rows      16 rows     32 rows
+//   64 of 900 to 16384 keys, D 128 G 64  162 / 539  164 / 537   262 / 537   - / 542
+//                            D 128 G 32  196 / 527  198 / 525   326 / 530   - / 527
+//                            D  64 G 32  126 / 419  126 / 421   189 / 419   - / 421
+//                            D 256 G 64  158 / 322  159 / 328    -  / 327   - / 329
+//                            D 256 G 32  187 / 329  192 / 332    -  / 333   - / 332
+//   16 of 300 to 9000 keys,  D 128 G 64   32 / 86    33 / 87     49 / 89    - / 89
+//   1 of 4000 keys,          D 128 G 64   12 / 28    14 / 28     18 / 28    - / 29
+//   200 of 300 keys,         D 128 G 64   48 / 99    49 / 100    70 / 100   - / 104
+//                            D 256 G 32   96 / 117  105 / 118    -  / 117   - / 120
+// An earlier state of the kernel had four row tiles (32 rows: 483 / 484 for the first line, 1027 / 480 for the second, 358 /
+// 382 for the third, 95 / 70 for 16 requests) and two at D = 256 (16 rows, half as many KV heads: 149 / 179 with groups of
+// 64, 307 / 185 with groups of 32, 98 / 38 for 200 of 300 keys, but 22 / 41 for one request of 4000): neither is compiled.
 constexpr int quant_mma_rows(int d) { return d == 256 ? 8 : 16; }
 unsigned long long seq_quant_mma_workspace64(int rows, int sms);
 unsigned long long seq_quant_mma_workspace128(int rows, int sms);

@@ -17,13 +17,15 @@
 // product.  A warp takes every fourth block of 16 keys of its CTA's run, one or two blocks at a time, copied to
 // shared memory two such sets ahead (cp.async; no barrier inside the key loop); the batch is cut evenly over the
 // CTAs by the schedule of seq_sched.cuh.
-// Measured: one token of 64 requests of 900 to 16384 keys, 32 / 8 heads of 128, groups of 64 (668 MB): 152 us, 4.4
-// TB/s; a key costs as at 6 TB/s, the rest is about 14 us of start, first copies, join and merge and CTAs that end
-// unevenly.  131001 keys of 4 heads of 256, groups of 32 (168 MB): 50 us; 96 requests with a window of
-// 2000 keys, 16 / 16 heads of 64, groups of 32 (216 MB): 87 us, 2.5 TB/s, half of the products' rows empty.
+// Measured: one token of 64 requests of 900 to 16384 keys, 32 / 8 heads of 128, groups of 64 (668 MB): 155 us, 4.3
+// TB/s.  Batches of 16 to 128 requests of 8192 keys (45 to 270 us) lie on a line of 4.7 TB/s and 14 us of start, first
+// copies, join and merge.  131001 keys of 4 heads of 256, groups of 32 (168 MB): 52 us; 96 requests with a window of
+// 2000 keys, 16 / 16 heads of 64, groups of 32 (216 MB): 89 us, 2.4 TB/s, half of the products' rows empty.
 // The same 64 requests took 253 us with codes straight from global memory into registers and a row an instruction, 198 with two
 // rows an instruction, 179 through shared memory, 167 with 32-bit strides, 160 with copies without branches, 156 with two blocks
-// at a time, 152 with the unit cost below.
+// at a time, 152 with the unit cost below, 155 since scales and queries of all sizes keep their weights (kQmTop, the careful
+// loop).  The careful loop: 167 where it is for queries alone, 190 with 1 % of V's scales 0 (each asks for a second look), 700
+// where every block holds scales 2^10 and more apart.
 #pragma once
 
 #include <type_traits>
@@ -37,8 +39,8 @@ namespace {
 constexpr int kQmWarps = 4, kQmThreads = kQmWarps * 32;
 constexpr int kQmTks = 6;                           // schedule granularity: 64 keys, 16 a warp
 constexpr int kQmLeast = 3;                         // tiles of a CTA's run at least
-// A unit's start and end (Q, the first copies, the join) in tiles' worth of time.  0, 4, 6, 8 and 12: 156, 154, 152, 153 and
-// 154 us for 64 requests of 900 to 16384 keys, 99, 88, 88, 88 and 88 us for 96 of up to 2000 keys with 16 KV heads.
+// A unit's start and end (Q, the first copies, the join) in tiles' worth of time.  0, 4, 6, 8 and 12: 160, 155, 155, 155 and
+// 157 us for 64 requests of 900 to 16384 keys, 103, 89, 89, 89 and 89 us for 96 of up to 2000 keys with 16 KV heads.
 constexpr int kQmUnitCost = 6;
 constexpr float kQmLog2e = 1.4426950408889634f;
 // The running max moves when a row's max exceeds it by more than 2^8; P and l are held 2^7 higher
@@ -142,8 +144,9 @@ __device__ __forceinline__ float bias_of(uint32_t sb) {
     else return __half2float(__ushort_as_half(static_cast<unsigned short>(sb >> 16)));
 }
 
-// NR: tiles of 8 query rows.  CTAs an SM: as many as leave few registers in memory.  (Spilled are 72 to 416 bytes a thread with
-// D = 128 and NR = 2 and up to 440 with D = 64, none with D = 256.)
+// NR: tiles of 8 query rows.  CTAs an SM: as many as leave few registers in memory.  (Spilled, bytes a thread: D = 64 28 to 52
+// with groups of 64 and 230 with groups of 32, with two row tiles 144 and 644; D = 128 none, with two row tiles 84 and 508;
+// D = 256 none.)
 template <int D, int NR>
 constexpr int kQmCtas = D == 256 ? 2 : NR == 2 ? (D == 64 ? 4 : 3) : (D == 64 ? 5 : 3);
 // Blocks of 16 keys that a warp takes at a time: two where registers allow, for work that does not wait for one another.
@@ -178,7 +181,7 @@ __global__ void __launch_bounds__(kQmThreads, (kQmCtas<D, NR>)) seq_quant_mma_ke
     const SeqRun run = seq_schedule<kQmThreads, kQmTks, kQmUnitCost, kQmLeast>(a, a.max_q, cta, ar.G, &sched);
     pdl_launch_dependents();
     if (tid == 0) ar.rec[cta] = {0, 0, 0, 0};
-    const float scale2 = fmaxf(a.scale * kQmLog2e, FLT_MIN);   // above 0: a masked -inf stays -inf
+    const float scale2 = fmaxf(a.scale * kQmLog2e, FLT_MIN);   // (a scale of 0 weighs all keys alike, infinite products too)
     SeqWalk<kQmTks, kQmUnitCost> walk;
     walk.init(a, a.max_q, run, &sched, cta);
     SeqPiece p;
