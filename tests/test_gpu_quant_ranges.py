@@ -250,6 +250,52 @@ def test_keys_outside_every_row_do_not_matter(ta, new, d, fill, kernel):
             x.copy_(y)
 
 
+@pytest.mark.parametrize("new,h,hk,d,group", [(1, 8, 2, 128, 64), (4, 4, 4, 64, 32), (3, 8, 2, 128, 32), (2, 4, 1, 256, 32), (30, 4, 2, 128, 64)])
+@pytest.mark.parametrize("far_q", [False, True])
+def test_wide_scales_under_every_mask(ta, far_q, new, h, hk, d, group):
+    """V scales over 2^16 from key to key, a few of them 0, some rows with a group of queries far below the others: causal,
+    windowed and tree rows, pages behind the window gone, NaN in a query, the same call twice and on ordinary data after it."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(d + new)
+    for tree in (False, True):
+        c = QuantPaged(ta, [500, new, 77, 260], [new, new, 0, new], h, hk, d, 16, group, torch.bfloat16, seed=d, tree=tree)
+        ordinary = [c.run(ta, kernel=k) for k in FAMILIES]
+        keep = [x.clone() for x in c.cache]
+        size = torch.randint(-16, 1, c.cache.v_affine.shape[:-1], generator=g, device="cuda")
+        scale = c.cache.v_affine[..., 0].double() * 2.0 ** size
+        scale[torch.rand(scale.shape, generator=g, device="cuda") < 0.05] = 0.0
+        c.cache.v_affine[..., 0] = scale.to(c.dtype)
+        q = c.q.clone()
+        if far_q:
+            c.q[::2, :, :32] *= 2.0 ** -20
+        for b, n in enumerate(c.lens):
+            pages = c.table[b, :-(-n // 16)].long()
+            w, a = (c.cache[i][pages].transpose(1, 2).flatten(0, 1)[:n] for i in (2, 3))
+            c.vals[b], c.mags[b] = values(w, a)
+        for kernel in FAMILIES:
+            for window in (0,) if tree else (0, 1, 50):
+                got = c.run(ta, kernel=kernel, window=window)
+                c.check(got, window)
+                assert torch.equal(c.run(ta, kernel=kernel, window=window), got)
+                if window:
+                    table = c.table.clone()
+                    for b, n in enumerate(c.lens):
+                        c.table[b, :max(0, n - new - window + 1) // 16] = -1
+                    assert torch.equal(c.run(ta, kernel=kernel, window=window), got)
+                    c.table = table
+            got, was = c.run(ta, kernel=kernel), float(c.q[0, 1, 5])
+            c.q[0, 1, 5] = math.nan
+            bad = c.run(ta, kernel=kernel)
+            assert bool(torch.isnan(bad[0, 1]).all())
+            bad[0, 1] = got[0, 1]
+            assert torch.equal(bad, got)
+            c.q[0, 1, 5] = was
+        c.q = q
+        for x, y in zip(c.cache, keep):
+            x.copy_(y)
+        assert all(torch.equal(c.run(ta, kernel=k), want) for k, want in zip(FAMILIES, ordinary))
+
+
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("inter", [False, True])
 @pytest.mark.parametrize("group", [32, 64])
