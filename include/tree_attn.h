@@ -389,6 +389,8 @@ ta_status quant_sdpa_fwd_tree(const ta_quant_params *p, uint32_t q_l, const ta_b
  *   - Rows of a call and keys of a request (its table row's cells) are at most
  *     2^30, and a request has at most 2^31 tiles of 64 keys x 256 rows of work a KV
  *     head; more is TA_ERR_UNSUPPORTED.
+ *   - The tcgen05 kernels of the attention take logits, scale included, up to 2^24 in
+ *     magnitude (f32 has no fraction bits left there); rows beyond are not valid.
  *   - The same call gives the same bits.  The attention cuts the batch's work evenly
  *     over the GPU, so the last bits of a request's rows may change with the other
  *     requests' lengths.
@@ -700,7 +702,7 @@ size_t paged_quant_attn_workspace_bytes(const ta_paged_quant_params *p);
  * which take the codes as they are; more rows, or TA_KERNEL_TENSOR_CORES, the tcgen05 kernel, for
  * which each element and weight is rounded to the 16-bit type, so that a row of a larger call is less exact than
  * the same row of a small one, most of all in bf16 (an element beyond the type's range is infinite there, as it
- * is for paged_quant_read) and logits, scale included, must stay below 2^28; TA_KERNEL_CUDA_CORES or a negative
+ * is for paged_quant_read) and logits, scale included, must stay below 2^24; TA_KERNEL_CUDA_CORES or a negative
  * scale the CUDA cores (f32 all through, and about a hundred times slower).  The other two families take whatever q and k
  * make whose products f32 holds.  A key whose table cell names no page counts as a key of zeros or not at all.
  */

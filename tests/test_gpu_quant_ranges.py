@@ -129,7 +129,7 @@ def test_scales_of_zero_beside_others(ta, d, group):
 @pytest.mark.parametrize("power", [18, 60, 110, 117, 118])
 def test_queries_near_the_largest(ta, power, new, d, group):
     """bf16 queries whose products with the keys f32 still holds: the row is the value of its best key, whose
-    logit is 2^9 above the others' at least.  (The tensor-core kernel takes logits up to 2^28.)"""
+    logit is 2^9 above the others' at least.  (The tensor-core kernel takes logits up to 2^24.)"""
     families = FAMILIES if power < 20 else [1, 0, 3]
     g = torch.Generator(device="cuda")
     g.manual_seed(power)
