@@ -307,7 +307,10 @@ __device__ __forceinline__ uint32_t max_abs(uint32_t acc, uint32_t w) {
 // Chunks of twelve requests (1 to 512 tokens over up to 8192 keys, 32 / 8 heads of 128; us): 524 with a third of every tile
 // by each of three warps, 391 with tiles in turn, 344 with six warps, all fed by warp 0 (TMA), which needed 2100 cycles a tile,
 // 314 (908 TFLOP/s) with copies of their own.  One rolled loop serves K and V and holds little code: with loops of their own,
-// unrolled, the instruction cache missed and they took 1046.  Two chunks of 1000 to 2047 tokens, window 1500, 24 / 4 heads
+// unrolled, the instruction cache missed and they took 1046.  An element is rounded once, to the type of Q and out: a
+// product takes one type for both operands, and a second term would double products and tiles.  Errors against 64 bits are 1.1
+// to 1.2 times those of an f32 form rounded once on long contexts and up to 1.55 times on a few dozen keys, where K's rounding counts
+// most (emulated: without it 1.4 times).  Two chunks of 1000 to 2047 tokens, window 1500, 24 / 4 heads
 // of 256: 190; trees of 32 nodes of eight requests, the same heads: 51.  Issue slots and shared memory, which the
 // widening shares with the softmax and the products' operands, bound it: over 16-bit pages, where TMA brings the tiles, the same
 // chunks take 243.
