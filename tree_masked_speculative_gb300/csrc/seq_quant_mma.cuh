@@ -24,8 +24,8 @@
 // The same 64 requests took 253 us with codes straight from global memory into registers and a row an instruction, 198 with two
 // rows an instruction, 179 through shared memory, 167 with 32-bit strides, 160 with copies without branches, 156 with two blocks
 // at a time, 152 with the unit cost below, 155 since scales and queries of all sizes keep their weights (kQmTop, the careful
-// loop).  The careful loop: 167 where it is for queries alone, 190 with 1 % of V's scales 0 (each asks for a second look), 700
-// where every block holds scales 2^10 and more apart.
+// loop).  Of a like batch that takes 162 us: 167 in the careful loop for the queries alone, 188 with 1 % of V's scales 0 (each
+// asks for a second look), 700 where every block holds scales 2^10 and more apart.
 #pragma once
 
 #include <type_traits>
